@@ -43,6 +43,34 @@ class _Camera(ctypes.Structure):
     _fields_ = [("v", ctypes.c_float * CAMERA_FIELDS)]
 
 
+class _GroupNorm(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("samples", ctypes.c_int32), ("channels", ctypes.c_int32),
+                ("groups", ctypes.c_int32), ("positions", ctypes.c_int64), ("activation", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+MAX_AXES = 4
+
+
+class _Rotary(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("tokens", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("axes", ctypes.c_int32), ("sections", ctypes.c_int32 * MAX_AXES),
+                ("positions_int", ctypes.c_int32), ("positions_batch_stride", ctypes.c_int64)]
+
+
+class _Attention(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("q_len", ctypes.c_int32),
+                ("kv_len", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("scale", ctypes.c_float), ("kv_lengths", ctypes.c_void_p),
+                ("key_mask", ctypes.c_void_p)]
+
+
 class _BinStats(ctypes.Structure):
     _fields_ = [("num_pairs", ctypes.c_uint32), ("emitting", ctypes.c_uint32),
                 ("radix_passes", ctypes.c_int32), ("depth_pass_mask", ctypes.c_uint32),
@@ -86,6 +114,18 @@ def _load():
     lib.gsr_exp_neg.restype = ctypes.c_int
     lib.gsr_peak_kernel.argtypes = [P, ctypes.c_int, i32, P, ctypes.POINTER(ctypes.c_uint64), P]
     lib.gsr_peak_kernel.restype = ctypes.c_int
+    norm, rotary, attention, heads = (ctypes.POINTER(t) for t in (_GroupNorm, _Rotary, _Attention, _Heads))
+    lib.gsr_group_norm_forward.argtypes = [P, norm] + [P] * 7
+    lib.gsr_group_norm_forward.restype = ctypes.c_int
+    lib.gsr_group_norm_backward.argtypes = [P, norm] + [P] * 10
+    lib.gsr_group_norm_backward.restype = ctypes.c_int
+    for name in ("gsr_rotary_forward", "gsr_rotary_backward"):
+        getattr(lib, name).argtypes = [P, rotary, heads, P, P, heads, P]
+        getattr(lib, name).restype = ctypes.c_int
+    lib.gsr_cross_attention_forward.argtypes = [P, attention] + [heads] * 4 + [P, P]
+    lib.gsr_cross_attention_forward.restype = ctypes.c_int
+    lib.gsr_cross_attention_backward.argtypes = [P, attention] + [heads] * 4 + [P] + [heads] * 4 + [P]
+    lib.gsr_cross_attention_backward.restype = ctypes.c_int
     return lib
 
 
@@ -352,3 +392,240 @@ def project_backward(ctx: Context, gauss: torch.Tensor, camera, dl_dsplat: torch
                                         ctypes.c_void_p(dl_dsplat.data_ptr()),
                                         ctypes.c_void_p(dl_dgauss.data_ptr()), _stream_ptr(stream, dev)))
     return dl_dgauss
+
+
+# -- the operators of an image-to-Gaussians decoder ---------------------------
+
+DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2}
+
+
+def _dtype(t: torch.Tensor, name, among):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in among:
+        raise ValueError(f"{name} must be one of {', '.join(map(str, among))}, got {t.dtype}")
+    return t.dtype
+
+
+def _heads(t: torch.Tensor, name, dtype, shape, device) -> _Heads:
+    """A [batch, tokens, heads, head_dim] tensor, any strides but a contiguous last dimension."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return _Heads(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}, got {t.device}")
+
+
+def _ptr(t):
+    return ctypes.c_void_p(None if t is None else t.data_ptr())
+
+
+def _new(shape, dtype, device, stream):
+    """An output of this call, allocated for the stream that writes it; the
+    caller's stream, which will read it, is recorded on it as well."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _norm_desc(x, groups, eps, activation):
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {activation!r}")
+    if x.dim() < 2:
+        raise ValueError(f"x must have shape [samples, ..., channels], got {tuple(x.shape)}")
+    positions = 1
+    for extent in x.shape[1:-1]:
+        positions *= extent
+    return _GroupNorm(DTYPES[x.dtype], x.shape[0], x.shape[-1], int(groups), positions, ACTIVATIONS[activation],
+                      float(eps))
+
+
+def group_norm_forward(ctx: Context, x: torch.Tensor, groups: int, weight=None, bias=None, eps: float = 1e-5,
+                       activation: str = "silu", out=None, mean=None, rstd=None, stream=None):
+    """act(group norm(x) * weight + bias) over channels-last x [samples, ..., channels]
+    (f32, bf16 or f16; weight and bias [channels] f32 or None).  `activation` is
+    "none", "silu" or "gelu".  Returns (out, mean, rstd), the last two
+    [samples, groups] f32 for the backward.  out may be x."""
+    dtype = _dtype(x, "x", DTYPES)
+    _need(x, "x", dtype)
+    desc, dev, c = _norm_desc(x, groups, eps, activation), x.device, x.shape[-1]
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _need(t, name, torch.float32, (c,))
+    stats = (x.shape[0], int(groups))
+    if out is None:
+        out = _new(x.shape, dtype, dev, stream)
+    if mean is None:
+        mean = _new(stats, torch.float32, dev, stream)
+    if rstd is None:
+        rstd = _new(stats, torch.float32, dev, stream)
+    _need(out, "out", dtype, x.shape)
+    _need(mean, "mean", torch.float32, stats)
+    _need(rstd, "rstd", torch.float32, stats)
+    _same_device(dev, weight=weight, bias=bias, out=out, mean=mean, rstd=rstd)
+    ctx._check(lib.gsr_group_norm_forward(ctx._h, ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(out),
+                                          _ptr(mean), _ptr(rstd), _stream_ptr(stream, dev)))
+    return out, mean, rstd
+
+
+def group_norm_backward(ctx: Context, dl_dout: torch.Tensor, x: torch.Tensor, groups: int, weight, bias,
+                        mean: torch.Tensor, rstd: torch.Tensor, activation: str = "silu", dl_dx=None,
+                        dl_dweight=None, dl_dbias=None, stream=None):
+    """Returns (dL/dx as x, dL/dweight [channels] f32, dL/dbias [channels] f32) for
+    dL/dout, with the forward's x, weight, bias, mean and rstd.  dl_dx may be dl_dout."""
+    dtype = _dtype(x, "x", DTYPES)
+    _need(x, "x", dtype)
+    _need(dl_dout, "dl_dout", dtype, x.shape)
+    desc, dev, c = _norm_desc(x, groups, 1.0, activation), x.device, x.shape[-1]
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _need(t, name, torch.float32, (c,))
+    stats = (x.shape[0], int(groups))
+    _need(mean, "mean", torch.float32, stats)
+    _need(rstd, "rstd", torch.float32, stats)
+    if dl_dx is None:
+        dl_dx = _new(x.shape, dtype, dev, stream)
+    if dl_dweight is None:
+        dl_dweight = _new((c,), torch.float32, dev, stream)
+    if dl_dbias is None:
+        dl_dbias = _new((c,), torch.float32, dev, stream)
+    _need(dl_dx, "dl_dx", dtype, x.shape)
+    _need(dl_dweight, "dl_dweight", torch.float32, (c,))
+    _need(dl_dbias, "dl_dbias", torch.float32, (c,))
+    _same_device(dev, dl_dout=dl_dout, weight=weight, bias=bias, mean=mean, rstd=rstd, dl_dx=dl_dx,
+                 dl_dweight=dl_dweight, dl_dbias=dl_dbias)
+    ctx._check(lib.gsr_group_norm_backward(ctx._h, ctypes.byref(desc), _ptr(dl_dout), _ptr(x), _ptr(weight),
+                                           _ptr(bias), _ptr(mean), _ptr(rstd), _ptr(dl_dx), _ptr(dl_dweight),
+                                           _ptr(dl_dbias), _stream_ptr(stream, dev)))
+    return dl_dx, dl_dweight, dl_dbias
+
+
+def rotary_frequencies(sections, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """The usual frequencies of rotary_forward, one progression per axis: pair j of
+    a section of s pairs turns by base^(-j / s) per unit of its axis' position."""
+    parts = [base ** (-torch.arange(int(s), dtype=torch.float64) / max(int(s), 1)) for s in sections]
+    return torch.cat(parts).float().to(device)
+
+
+def _rotary(call, name, ctx, x, positions, frequencies, sections, interleaved, out, out_name, stream):
+    dtype = _dtype(x, name, DTYPES)
+    if x.dim() != 4:
+        raise ValueError(f"{name} must have shape [batch, tokens, heads, head_dim], got {tuple(x.shape)}")
+    dev, (batch, tokens, heads, dim) = x.device, x.shape
+    sections = [int(s) for s in sections]
+    if not 1 <= len(sections) <= MAX_AXES:
+        raise ValueError(f"sections must hold 1 to {MAX_AXES} numbers of pairs, got {len(sections)}")
+    _need(frequencies, "frequencies", torch.float32, (sum(sections),))
+    _dtype(positions, "positions", (torch.int32, torch.float32))
+    shapes = ((tokens, len(sections)), (batch, tokens, len(sections)))
+    if tuple(positions.shape) not in shapes:
+        raise ValueError(f"positions must have shape {shapes[0]} or {shapes[1]}, got {tuple(positions.shape)}")
+    _need(positions, "positions", positions.dtype)
+    _same_device(dev, positions=positions, frequencies=frequencies)
+    src = _heads(x, name, dtype, x.shape, dev)
+    if out is None:
+        out = _new(x.shape, dtype, dev, stream)
+    dst = _heads(out, out_name, dtype, x.shape, dev)
+    desc = _Rotary(DTYPES[dtype], batch, tokens, heads, dim, int(bool(interleaved)), len(sections),
+                   (ctypes.c_int32 * MAX_AXES)(*sections), int(positions.dtype == torch.int32),
+                   tokens * len(sections) if positions.dim() == 3 else 0)
+    ctx._check(call(ctx._h, ctypes.byref(desc), ctypes.byref(src), _ptr(positions), _ptr(frequencies),
+                    ctypes.byref(dst), _stream_ptr(stream, dev)))
+    return out
+
+
+def rotary_forward(ctx: Context, x: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor, sections,
+                   interleaved: bool = False, out=None, stream=None) -> torch.Tensor:
+    """Turns the pairs of x [batch, tokens, heads, head_dim] (f32, bf16 or f16; any
+    strides with a contiguous last dimension) by positions [tokens, axes] or
+    [batch, tokens, axes] (f32 or int32) times frequencies [sum(sections)] f32;
+    sections[a] pairs turn by axis a.  Pairs are dimensions (i, i + sum(sections)),
+    or (2i, 2i + 1) when interleaved.  out may be x."""
+    return _rotary(lib.gsr_rotary_forward, "x", ctx, x, positions, frequencies, sections, interleaved, out, "out",
+                   stream)
+
+
+def rotary_backward(ctx: Context, dl_dout: torch.Tensor, positions: torch.Tensor, frequencies: torch.Tensor,
+                    sections, interleaved: bool = False, dl_dx=None, stream=None) -> torch.Tensor:
+    """dL/dx of rotary_forward for dL/dout.  dl_dx may be dl_dout."""
+    return _rotary(lib.gsr_rotary_backward, "dl_dout", ctx, dl_dout, positions, frequencies, sections, interleaved,
+                   dl_dx, "dl_dx", stream)
+
+
+def _attention_desc(q, k, v, kv_lengths, key_mask, scale):
+    dtype = _dtype(q, "q", (torch.bfloat16, torch.float16))
+    if q.dim() != 4 or not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("q, k and v must have shape [batch, tokens, heads, head_dim]")
+    batch, q_len, q_heads, dim = q.shape
+    kv_len, kv_heads = k.shape[1], k.shape[2]
+    dev = q.device
+    if kv_lengths is not None:
+        _need(kv_lengths, "kv_lengths", torch.int32, (batch,))
+    if key_mask is not None:
+        _dtype(key_mask, "key_mask", (torch.bool, torch.uint8))
+        _need(key_mask, "key_mask", key_mask.dtype, (batch, kv_len))
+    _same_device(dev, kv_lengths=kv_lengths, key_mask=key_mask)
+    desc = _Attention(DTYPES[dtype], batch, q_len, kv_len, q_heads, kv_heads, dim,
+                      float(dim ** -0.5 if scale is None else scale), _ptr(kv_lengths), _ptr(key_mask))
+    keys = (batch, kv_len, kv_heads, dim)
+    return desc, dtype, dev, keys, [_heads(q, "q", dtype, q.shape, dev), _heads(k, "k", dtype, keys, dev),
+                                    _heads(v, "v", dtype, keys, dev)]
+
+
+def cross_attention_forward(ctx: Context, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_lengths=None,
+                            key_mask=None, scale=None, out=None, lse=None, stream=None):
+    """Attention of q [batch, q_len, q_heads, head_dim] to k, v [batch, kv_len,
+    kv_heads, head_dim] (bf16 or f16; views with a contiguous last dimension).
+    Keys at or behind kv_lengths [batch] int32, or whose key_mask [batch, kv_len]
+    (bool or uint8) is 0, take no part; a row without any gives 0 and lse -inf.
+    `scale` defaults to head_dim ** -0.5.  Returns (out as q, lse [batch, q_heads,
+    q_len] f32)."""
+    desc, dtype, dev, _, (hq, hk, hv) = _attention_desc(q, k, v, kv_lengths, key_mask, scale)
+    rows = (q.shape[0], q.shape[2], q.shape[1])
+    if out is None:
+        out = _new(q.shape, dtype, dev, stream)
+    if lse is None:
+        lse = _new(rows, torch.float32, dev, stream)
+    ho = _heads(out, "out", dtype, q.shape, dev)
+    _need(lse, "lse", torch.float32, rows)
+    _same_device(dev, lse=lse)
+    ctx._check(lib.gsr_cross_attention_forward(ctx._h, ctypes.byref(desc), *map(ctypes.byref, (hq, hk, hv, ho)),
+                                               _ptr(lse), _stream_ptr(stream, dev)))
+    return out, lse
+
+
+def cross_attention_backward(ctx: Context, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                             lse: torch.Tensor, dl_dout: torch.Tensor, kv_lengths=None, key_mask=None, scale=None,
+                             dl_dq=None, dl_dk=None, dl_dv=None, stream=None):
+    """Returns (dL/dq, dL/dk, dL/dv) for dL/dout, with the forward's arguments, out
+    and lse.  Keys that took no part get zeros."""
+    desc, dtype, dev, keys, (hq, hk, hv) = _attention_desc(q, k, v, kv_lengths, key_mask, scale)
+    _need(lse, "lse", torch.float32, (q.shape[0], q.shape[2], q.shape[1]))
+    _same_device(dev, lse=lse)
+    if dl_dq is None:
+        dl_dq = _new(q.shape, dtype, dev, stream)
+    if dl_dk is None:
+        dl_dk = _new(keys, dtype, dev, stream)
+    if dl_dv is None:
+        dl_dv = _new(keys, dtype, dev, stream)
+    ho, hd = _heads(out, "out", dtype, q.shape, dev), _heads(dl_dout, "dl_dout", dtype, q.shape, dev)
+    gq = _heads(dl_dq, "dl_dq", dtype, q.shape, dev)
+    gk, gv = _heads(dl_dk, "dl_dk", dtype, keys, dev), _heads(dl_dv, "dl_dv", dtype, keys, dev)
+    ctx._check(lib.gsr_cross_attention_backward(
+        ctx._h, ctypes.byref(desc), *map(ctypes.byref, (hq, hk, hv, ho)), _ptr(lse),
+        *map(ctypes.byref, (hd, gq, gk, gv)), _stream_ptr(stream, dev)))
+    return dl_dq, dl_dk, dl_dv

@@ -124,6 +124,8 @@ void gsr_destroy(gsr_ctx *ctx)
         cudaFree(ctx->bnd);
         cudaFree(ctx->bwd_items);
         cudaFree(ctx->fwd_items);
+        cudaFree(ctx->work);
+        if (ctx->work_event) cudaEventDestroy(ctx->work_event);
         if (ctx->host_total) cudaFreeHost(ctx->host_total);
     }
     delete ctx;
@@ -361,6 +363,229 @@ int gsr_project_backward(gsr_ctx *ctx, const gsr_gaussian3d *gauss, int32_t n, c
     if (n == 0) return GSR_OK;
     return gsr::project_backward(ctx, reinterpret_cast<const float *>(gauss), n, *camera, dl_dsplat, dl_dgauss,
                                  (cudaStream_t)stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+size_t element_size(int dtype) { return dtype == GSR_F32 ? 4 : 2; }
+
+bool known_dtype(int dtype) { return dtype == GSR_F32 || dtype == GSR_BF16 || dtype == GSR_F16; }
+
+int check_group_norm(gsr_ctx *ctx, const gsr_group_norm *d, const void *x, const float *weight, const float *bias,
+                     const void *y, const float *mean, const float *rstd)
+{
+    if (!d) return fail(ctx, GSR_ERR_INVALID_ARG, "desc is NULL");
+    if (!known_dtype(d->dtype)) return fail(ctx, GSR_ERR_INVALID_ARG, "unknown dtype");
+    if (d->activation != GSR_ACT_NONE && d->activation != GSR_ACT_SILU && d->activation != GSR_ACT_GELU)
+        return fail(ctx, GSR_ERR_INVALID_ARG, "unknown activation");
+    if (d->samples < 0 || d->positions < 0) return fail(ctx, GSR_ERR_INVALID_ARG, "a size is negative");
+    if (d->channels < 1 || d->channels > GSR_MAX_CHANNELS)
+        return fail(ctx, GSR_ERR_INVALID_ARG, "channels outside [1, GSR_MAX_CHANNELS]");
+    if (d->groups < 1 || d->channels % d->groups != 0)
+        return fail(ctx, GSR_ERR_INVALID_ARG, "groups must divide channels");
+    if (d->positions > ((int64_t)1 << 40) / d->channels || d->samples > (1 << 20))
+        return fail(ctx, GSR_ERR_INVALID_ARG, "samples or positions too large");
+    if (!std::isfinite(d->eps) || !(d->eps > 0.0f))
+        return fail(ctx, GSR_ERR_INVALID_ARG, "eps must be finite and > 0");
+    if (d->samples == 0 || d->positions == 0) return GSR_OK;
+    if (!x || !y || !mean || !rstd) return fail(ctx, GSR_ERR_INVALID_ARG, "an array is NULL");
+    const size_t size = element_size(d->dtype);
+    if (!aligned(x, size) || !aligned(y, size) || !aligned(weight, 4) || !aligned(bias, 4) || !aligned(mean, 4) ||
+        !aligned(rstd, 4))
+        return fail(ctx, GSR_ERR_INVALID_ARG, "an array is not aligned to its element");
+    return GSR_OK;
+}
+
+// Sizes and strides of one [batch, tokens, heads, head_dim] array.
+int check_heads(gsr_ctx *ctx, const gsr_heads *t, const char *name, int64_t batch, int64_t tokens, int64_t heads,
+                size_t align, int64_t stride_unit, bool output)
+{
+    const std::string who(name);
+    if (!t) return fail(ctx, GSR_ERR_INVALID_ARG, who + " is NULL");
+    if (batch == 0 || tokens == 0 || heads == 0) return GSR_OK;
+    if (!t->data) return fail(ctx, GSR_ERR_INVALID_ARG, who + ".data is NULL");
+    if (!aligned(t->data, align))
+        return fail(ctx, GSR_ERR_INVALID_ARG, who + " must be " + std::to_string(align) + "-byte aligned");
+    const struct { int64_t extent, stride; const char *what; bool shared; } dims[3] = {
+        {batch, t->batch_stride, "batch", true}, {tokens, t->token_stride, "token", false},
+        {heads, t->head_stride, "head", true}};
+    for (const auto &dim : dims) {
+        if (dim.extent <= 1) continue;
+        if (dim.stride < 0 || dim.stride > ((int64_t)1 << 38) || dim.stride % stride_unit != 0)
+            return fail(ctx, GSR_ERR_INVALID_ARG, who + ": the " + dim.what + " stride must be a multiple of " +
+                                                      std::to_string(stride_unit) + " in [0, 2^38]");
+        if (dim.stride == 0 && (output || !dim.shared))
+            return fail(ctx, GSR_ERR_INVALID_ARG, who + ": the " + dim.what + " stride must not be 0");
+    }
+    return GSR_OK;
+}
+
+int check_rotary(gsr_ctx *ctx, const gsr_rotary *d, const gsr_heads *x, const void *positions,
+                 const float *frequencies, const gsr_heads *out)
+{
+    if (!d) return fail(ctx, GSR_ERR_INVALID_ARG, "desc is NULL");
+    if (!known_dtype(d->dtype)) return fail(ctx, GSR_ERR_INVALID_ARG, "unknown dtype");
+    if (d->batch < 0 || d->tokens < 0) return fail(ctx, GSR_ERR_INVALID_ARG, "a size is negative");
+    if ((int64_t)d->batch * d->tokens > GSR_MAX_TOKENS)
+        return fail(ctx, GSR_ERR_INVALID_ARG, "batch * tokens above GSR_MAX_TOKENS");
+    if (d->heads < 1 || d->heads > GSR_MAX_HEADS)
+        return fail(ctx, GSR_ERR_INVALID_ARG, "heads outside [1, GSR_MAX_HEADS]");
+    if (d->head_dim < 1 || d->head_dim > GSR_MAX_HEAD_DIM)
+        return fail(ctx, GSR_ERR_INVALID_ARG, "head_dim outside [1, GSR_MAX_HEAD_DIM]");
+    if (d->axes < 1 || d->axes > GSR_MAX_AXES) return fail(ctx, GSR_ERR_INVALID_ARG, "axes outside [1, GSR_MAX_AXES]");
+    int64_t pairs = 0;
+    for (int a = 0; a < d->axes; ++a) {
+        if (d->sections[a] < 0) return fail(ctx, GSR_ERR_INVALID_ARG, "a section is negative");
+        pairs += d->sections[a];
+    }
+    if (2 * pairs > d->head_dim) return fail(ctx, GSR_ERR_INVALID_ARG, "the sections hold more pairs than head_dim");
+    if (d->positions_batch_stride < 0 || d->positions_batch_stride > ((int64_t)1 << 38))
+        return fail(ctx, GSR_ERR_INVALID_ARG, "positions_batch_stride outside [0, 2^38]");
+    const size_t size = element_size(d->dtype);
+    if (int rc = check_heads(ctx, x, "x", d->batch, d->tokens, d->heads, size, 1, false)) return rc;
+    if (int rc = check_heads(ctx, out, "out", d->batch, d->tokens, d->heads, size, 1, true)) return rc;
+    if (d->batch > 0 && d->tokens > 0 && pairs > 0) {
+        if (!positions || !frequencies) return fail(ctx, GSR_ERR_INVALID_ARG, "positions or frequencies is NULL");
+        if (!aligned(positions, 4) || !aligned(frequencies, 4))
+            return fail(ctx, GSR_ERR_INVALID_ARG, "positions and frequencies must be 4-byte aligned");
+    }
+    return GSR_OK;
+}
+
+int check_attention(gsr_ctx *ctx, const gsr_attention *d)
+{
+    if (!d) return fail(ctx, GSR_ERR_INVALID_ARG, "desc is NULL");
+    if (d->dtype != GSR_BF16 && d->dtype != GSR_F16)
+        return fail(ctx, GSR_ERR_INVALID_ARG, "attention takes GSR_BF16 or GSR_F16");
+    if (d->batch < 0 || d->q_len < 0 || d->kv_len < 0) return fail(ctx, GSR_ERR_INVALID_ARG, "a size is negative");
+    if (d->kv_heads < 1 || d->q_heads < 1 || d->q_heads > GSR_MAX_HEADS || d->q_heads % d->kv_heads != 0)
+        return fail(ctx, GSR_ERR_INVALID_ARG, "q_heads must be a multiple of kv_heads, in [1, GSR_MAX_HEADS]");
+    if (d->head_dim < 8 || d->head_dim > GSR_ATTENTION_MAX_HEAD_DIM || d->head_dim % 8 != 0)
+        return fail(ctx, GSR_ERR_INVALID_ARG,
+                    "head_dim must be a multiple of 8 in [8, GSR_ATTENTION_MAX_HEAD_DIM]");
+    if (!std::isfinite(d->scale) || !(d->scale > 0.0f))
+        return fail(ctx, GSR_ERR_INVALID_ARG, "scale must be finite and > 0");
+    if (d->batch > (1 << 16) || d->q_len > (1 << 24) || d->kv_len > (1 << 24))
+        return fail(ctx, GSR_ERR_INVALID_ARG, "batch above 2^16 or a length above 2^24");
+    if (!aligned(d->kv_lengths, 4)) return fail(ctx, GSR_ERR_INVALID_ARG, "kv_lengths must be 4-byte aligned");
+    return GSR_OK;
+}
+
+int check_query(gsr_ctx *ctx, const gsr_attention *d, const gsr_heads *t, const char *name, bool output)
+{
+    return check_heads(ctx, t, name, d->batch, d->q_len, d->q_heads, 16, 8, output);
+}
+
+int check_key(gsr_ctx *ctx, const gsr_attention *d, const gsr_heads *t, const char *name, bool output)
+{
+    return check_heads(ctx, t, name, d->batch, d->kv_len, d->kv_heads, 16, 8, output);
+}
+
+}  // namespace
+
+extern "C" {
+
+int gsr_group_norm_forward(gsr_ctx *ctx, const gsr_group_norm *desc, const void *x, const float *weight,
+                           const float *bias, void *out, float *mean, float *rstd, void *stream)
+{
+    gsr::Range range("gsr_group_norm_forward");
+    if (!ctx) return GSR_ERR_INVALID_ARG;
+    ctx->err.clear();
+    if (int rc = check_group_norm(ctx, desc, x, weight, bias, out, mean, rstd)) return rc;
+    DeviceGuard g(ctx->device);
+    if (!g.ok) return fail(ctx, GSR_ERR_CUDA, "cannot select the context's device");
+    if (desc->samples == 0 || desc->positions == 0) return GSR_OK;
+    return gsr::group_norm_forward(ctx, *desc, x, weight, bias, out, mean, rstd, (cudaStream_t)stream);
+}
+
+int gsr_group_norm_backward(gsr_ctx *ctx, const gsr_group_norm *desc, const void *dl_dout, const void *x,
+                            const float *weight, const float *bias, const float *mean, const float *rstd,
+                            void *dl_dx, float *dl_dweight, float *dl_dbias, void *stream)
+{
+    gsr::Range range("gsr_group_norm_backward");
+    if (!ctx) return GSR_ERR_INVALID_ARG;
+    ctx->err.clear();
+    if (int rc = check_group_norm(ctx, desc, x, weight, bias, dl_dx, mean, rstd)) return rc;
+    if (desc->samples > 0 && desc->positions > 0 && !dl_dout)
+        return fail(ctx, GSR_ERR_INVALID_ARG, "dl_dout is NULL");
+    if (!aligned(dl_dout, element_size(desc->dtype)) || !aligned(dl_dweight, 4) || !aligned(dl_dbias, 4))
+        return fail(ctx, GSR_ERR_INVALID_ARG, "an array is not aligned to its element");
+    DeviceGuard g(ctx->device);
+    if (!g.ok) return fail(ctx, GSR_ERR_CUDA, "cannot select the context's device");
+    return gsr::group_norm_backward(ctx, *desc, dl_dout, x, weight, bias, mean, rstd, dl_dx, dl_dweight, dl_dbias,
+                                    (cudaStream_t)stream);
+}
+
+int gsr_rotary_forward(gsr_ctx *ctx, const gsr_rotary *desc, const gsr_heads *x, const void *positions,
+                       const float *frequencies, const gsr_heads *out, void *stream)
+{
+    gsr::Range range("gsr_rotary_forward");
+    if (!ctx) return GSR_ERR_INVALID_ARG;
+    ctx->err.clear();
+    if (int rc = check_rotary(ctx, desc, x, positions, frequencies, out)) return rc;
+    DeviceGuard g(ctx->device);
+    if (!g.ok) return fail(ctx, GSR_ERR_CUDA, "cannot select the context's device");
+    if (desc->batch == 0 || desc->tokens == 0) return GSR_OK;
+    return gsr::rotary(ctx, *desc, *x, positions, frequencies, *out, 1.0f, (cudaStream_t)stream);
+}
+
+int gsr_rotary_backward(gsr_ctx *ctx, const gsr_rotary *desc, const gsr_heads *dl_dout, const void *positions,
+                        const float *frequencies, const gsr_heads *dl_dx, void *stream)
+{
+    gsr::Range range("gsr_rotary_backward");
+    if (!ctx) return GSR_ERR_INVALID_ARG;
+    ctx->err.clear();
+    if (int rc = check_rotary(ctx, desc, dl_dout, positions, frequencies, dl_dx)) return rc;
+    DeviceGuard g(ctx->device);
+    if (!g.ok) return fail(ctx, GSR_ERR_CUDA, "cannot select the context's device");
+    if (desc->batch == 0 || desc->tokens == 0) return GSR_OK;
+    return gsr::rotary(ctx, *desc, *dl_dout, positions, frequencies, *dl_dx, -1.0f, (cudaStream_t)stream);
+}
+
+int gsr_cross_attention_forward(gsr_ctx *ctx, const gsr_attention *desc, const gsr_heads *q, const gsr_heads *k,
+                                const gsr_heads *v, const gsr_heads *out, float *lse, void *stream)
+{
+    gsr::Range range("gsr_cross_attention_forward");
+    if (!ctx) return GSR_ERR_INVALID_ARG;
+    ctx->err.clear();
+    if (int rc = check_attention(ctx, desc)) return rc;
+    if (int rc = check_query(ctx, desc, q, "q", false)) return rc;
+    if (int rc = check_key(ctx, desc, k, "k", false)) return rc;
+    if (int rc = check_key(ctx, desc, v, "v", false)) return rc;
+    if (int rc = check_query(ctx, desc, out, "out", true)) return rc;
+    if (desc->batch == 0 || desc->q_len == 0) return GSR_OK;
+    if (!lse || !aligned(lse, 4)) return fail(ctx, GSR_ERR_INVALID_ARG, "lse is NULL or misaligned");
+    DeviceGuard g(ctx->device);
+    if (!g.ok) return fail(ctx, GSR_ERR_CUDA, "cannot select the context's device");
+    return gsr::cross_attention_forward(ctx, *desc, *q, *k, *v, *out, lse, (cudaStream_t)stream);
+}
+
+int gsr_cross_attention_backward(gsr_ctx *ctx, const gsr_attention *desc, const gsr_heads *q, const gsr_heads *k,
+                                 const gsr_heads *v, const gsr_heads *out, const float *lse,
+                                 const gsr_heads *dl_dout, const gsr_heads *dl_dq, const gsr_heads *dl_dk,
+                                 const gsr_heads *dl_dv, void *stream)
+{
+    gsr::Range range("gsr_cross_attention_backward");
+    if (!ctx) return GSR_ERR_INVALID_ARG;
+    ctx->err.clear();
+    if (int rc = check_attention(ctx, desc)) return rc;
+    if (int rc = check_query(ctx, desc, q, "q", false)) return rc;
+    if (int rc = check_key(ctx, desc, k, "k", false)) return rc;
+    if (int rc = check_key(ctx, desc, v, "v", false)) return rc;
+    if (int rc = check_query(ctx, desc, out, "out", false)) return rc;
+    if (int rc = check_query(ctx, desc, dl_dout, "dl_dout", false)) return rc;
+    if (int rc = check_query(ctx, desc, dl_dq, "dl_dq", true)) return rc;
+    if (int rc = check_key(ctx, desc, dl_dk, "dl_dk", true)) return rc;
+    if (int rc = check_key(ctx, desc, dl_dv, "dl_dv", true)) return rc;
+    if (desc->batch == 0 || (desc->q_len == 0 && desc->kv_len == 0)) return GSR_OK;
+    if (desc->q_len > 0 && (!lse || !aligned(lse, 4)))
+        return fail(ctx, GSR_ERR_INVALID_ARG, "lse is NULL or misaligned");
+    DeviceGuard g(ctx->device);
+    if (!g.ok) return fail(ctx, GSR_ERR_CUDA, "cannot select the context's device");
+    return gsr::cross_attention_backward(ctx, *desc, *q, *k, *v, *out, lse, *dl_dout, *dl_dq, *dl_dk, *dl_dv,
+                                         (cudaStream_t)stream);
 }
 
 }  // extern "C"

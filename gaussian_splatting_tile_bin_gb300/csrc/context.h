@@ -72,6 +72,14 @@ struct gsr_ctx {
     uint64_t fwd_pairs_bound = 0;
     uint64_t bin_calls = 0;                     // gsr_bin_splats calls made
 
+    // Workspace of the decoder's operators (decoder.cu): scratch of one call at a
+    // time, ordered between streams by an event.
+    size_t cap_work = 0;
+    unsigned char *work = nullptr;
+    cudaStream_t work_stream = nullptr;         // stream of the last call that used it
+    cudaEvent_t work_event = nullptr;           // recorded after that call
+    bool work_pending = false;                  // work_event holds a record
+
     // Last binning, for gsr_get_bin_stats and gsr_num_pairs.
     cudaStream_t last_stream = nullptr;
     bool last_sync_free = false;                // its counts stayed on the device

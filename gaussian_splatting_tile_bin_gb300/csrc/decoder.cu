@@ -1,0 +1,52 @@
+// decoder.cu -- the workspace of the decoder's operators: scratch memory that
+// one call at a time uses, grown like the rest of the context's arena.
+#include "decoder.cuh"
+
+namespace gsr {
+
+int workspace(gsr_ctx *ctx, size_t bytes, cudaStream_t stream, void **out)
+{
+    *out = nullptr;
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (int rc = cuda_check(ctx, cudaStreamIsCapturing(stream, &capture), "workspace stream")) return rc;
+    if (bytes > ctx->cap_work) {
+        if (capture != cudaStreamCaptureStatusNone)
+            return fail(ctx, GSR_ERR_CUDA, "the workspace must grow during a capture: make one such call before it");
+        // Queued work of an earlier call may still use the old buffer.
+        if (int rc = cuda_check(ctx, cudaDeviceSynchronize(), "workspace growth")) return rc;
+        cudaFree(ctx->work);
+        ctx->work = nullptr;
+        ctx->cap_work = 0;
+        const size_t grown = round_up(bytes, (size_t)1 << 20);
+        void *p = nullptr;
+        if (device_alloc(ctx, &p, grown) != cudaSuccess) {
+            cudaGetLastError();
+            return fail(ctx, GSR_ERR_OOM, "cannot grow the workspace to " + std::to_string(grown) + " bytes");
+        }
+        ctx->work = (unsigned char *)p;
+        ctx->cap_work = grown;
+        ctx->work_pending = false;
+    }
+    // A captured call is ordered by its graph; events of the live streams stay out of it.
+    if (capture == cudaStreamCaptureStatusNone && ctx->work_pending && ctx->work_stream != stream)
+        if (int rc = cuda_check(ctx, cudaStreamWaitEvent(stream, ctx->work_event, 0), "workspace order")) return rc;
+    *out = ctx->work;
+    return GSR_OK;
+}
+
+int workspace_done(gsr_ctx *ctx, cudaStream_t stream)
+{
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (int rc = cuda_check(ctx, cudaStreamIsCapturing(stream, &capture), "workspace stream")) return rc;
+    if (capture != cudaStreamCaptureStatusNone) return GSR_OK;
+    if (!ctx->work_event)
+        if (int rc = cuda_check(ctx, cudaEventCreateWithFlags(&ctx->work_event, cudaEventDisableTiming),
+                                "workspace event"))
+            return rc;
+    if (int rc = cuda_check(ctx, cudaEventRecord(ctx->work_event, stream), "workspace event")) return rc;
+    ctx->work_stream = stream;
+    ctx->work_pending = true;
+    return GSR_OK;
+}
+
+}  // namespace gsr

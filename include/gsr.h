@@ -383,6 +383,161 @@ int gsr_exp_neg(gsr_ctx *ctx, const float *s, float *out, int32_t n, void *strea
 enum { GSR_PEAK_FFMA = 0, GSR_PEAK_EX2 = 1 };
 int gsr_peak_kernel(gsr_ctx *ctx, int kind, int32_t iters, float *sink, uint64_t *lane_ops, void *stream);
 
+/* ---- The operators of an image-to-Gaussians decoder ------------------------
+ *
+ * A network that predicts the Gaussians of gsr_project_forward from images has
+ * in front of it: feature maps of the input views (group norm with an
+ * activation, channels last), positions of patch tokens and Gaussian tokens
+ * (rotary positions with several axes), and Gaussian tokens that attend to the
+ * tokens of all views (cross attention to states of another length).  The calls
+ * below follow the conventions at the top of this file; a call that needs
+ * scratch memory takes it from a workspace of the context's arena, which grows
+ * (synchronising the device) and never shrinks.  Calls on one context from
+ * several streams are ordered on that workspace by an event.  A call made while
+ * its stream is being captured cannot grow the workspace (GSR_ERR_CUDA): make
+ * one such call before the capture, and order a graph's replays with the
+ * context's other calls.  Inputs and outputs must not overlap unless a call
+ * says so. */
+
+/* Element types of the decoder's arrays. */
+enum { GSR_F32 = 0, GSR_BF16 = 1, GSR_F16 = 2 };
+
+/* Activations of gsr_group_norm_*: z, z sigmoid(z), z Phi(z) with the normal
+ * distribution's Phi (the erf form). */
+enum { GSR_ACT_NONE = 0, GSR_ACT_SILU = 1, GSR_ACT_GELU = 2 };
+
+/* Group norm with an activation over channels-last features:
+ *   mean, var over the positions and the channels / groups channels of a group,
+ *   z = (x - mean) / sqrt(var + eps) * weight[c] + bias[c],  out = act(z).
+ *
+ *   dtype   type of x and out (GSR_F32, GSR_BF16, GSR_F16)
+ *   x       device, [samples, positions, channels]
+ *   weight, bias   device, [channels] float; each may be NULL (1 and 0)
+ *   out     device, as x; may be x itself
+ *   mean, rstd     device, [samples, groups] float, written (for the backward)
+ * All arrays aligned to their element.  Arrays of x aligned to 16 bytes with
+ * channels a multiple of 16 bytes take a vectorised path.  Statistics are taken
+ * in float as means and centred squares, merged in a fixed order: the same bits
+ * on every run.  positions = 0 writes nothing.
+ * Errors: GSR_ERR_INVALID_ARG (null or misaligned arrays; a negative size;
+ * groups < 1 or not dividing channels; channels > GSR_MAX_CHANNELS; eps not
+ * finite or <= 0; unknown dtype or activation), GSR_ERR_OOM, GSR_ERR_CUDA. */
+#define GSR_MAX_CHANNELS 4096
+typedef struct gsr_group_norm {
+    int32_t dtype;
+    int32_t samples, channels, groups;
+    int64_t positions;
+    int32_t activation;
+    float eps;
+} gsr_group_norm;
+int gsr_group_norm_forward(gsr_ctx *ctx, const gsr_group_norm *desc, const void *x, const float *weight,
+                           const float *bias, void *out, float *mean, float *rstd, void *stream);
+
+/* Backward of gsr_group_norm_forward: with xh = (x - mean) rstd, dz = dL/dout
+ * act'(z) and M elements in a group,
+ *   dL/dbias = sum dz,  dL/dweight = sum dz xh  (over samples and positions)
+ *   dL/dx = rstd (weight dz - sum(weight dz) / M - xh sum(weight dz xh) / M).
+ *   mean, rstd   the forward's, for the same x
+ *   dl_dx        device, as x; may be dl_dout itself
+ *   dl_dweight, dl_dbias   device, [channels] float, overwritten; each may be NULL
+ * The same bits on every run.  Errors: as the forward. */
+int gsr_group_norm_backward(gsr_ctx *ctx, const gsr_group_norm *desc, const void *dl_dout, const void *x,
+                            const float *weight, const float *bias, const float *mean, const float *rstd,
+                            void *dl_dx, float *dl_dweight, float *dl_dbias, void *stream);
+
+/* An array [batch, tokens, heads, head_dim] whose last dimension is contiguous.
+ * Strides are in elements.  A stride of 0 over the batch or the heads shares one
+ * array (inputs only). */
+typedef struct gsr_heads {
+    void *data;
+    int64_t batch_stride, token_stride, head_stride;
+} gsr_heads;
+
+/* Rotary positions with several axes.  The 2 * sum(sections) first dimensions of
+ * every head form pairs; pair i belongs to the axis a whose section holds it and
+ * turns by theta = positions[token][a] * frequencies[i]:
+ *   (u, v) -> (u cos theta - v sin theta, u sin theta + v cos theta).
+ * The remaining dimensions are copied.
+ *
+ *   dtype        type of x and out (GSR_F32, GSR_BF16, GSR_F16)
+ *   interleaved  0: pair i is dimensions (i, i + sum(sections)); 1: (2i, 2i + 1)
+ *   axes, sections   1 to GSR_MAX_AXES axes and their numbers of pairs (>= 0)
+ *   positions    device, [tokens, axes] per batch item, float or int32
+ *                (positions_int), batch items positions_batch_stride elements
+ *                apart (0: shared)
+ *   frequencies  device, [sum(sections)] float
+ *   x, out       out may be x itself (same data and strides)
+ * The angle's product is kept to twice float's length before its sine and
+ * cosine, so long positions lose nothing.
+ * Errors: GSR_ERR_INVALID_ARG (null or misaligned arrays; negative sizes;
+ * sizes above GSR_MAX_TOKENS, GSR_MAX_HEADS, GSR_MAX_HEAD_DIM; pairs beyond
+ * head_dim; out with a stride of 0 over more than one item), GSR_ERR_CUDA. */
+#define GSR_MAX_AXES 4
+#define GSR_MAX_TOKENS (1 << 28)   /* batch * tokens */
+#define GSR_MAX_HEADS 1024
+#define GSR_MAX_HEAD_DIM 1024
+typedef struct gsr_rotary {
+    int32_t dtype;
+    int32_t batch, tokens, heads, head_dim;
+    int32_t interleaved;
+    int32_t axes;
+    int32_t sections[GSR_MAX_AXES];
+    int32_t positions_int;
+    int64_t positions_batch_stride;
+} gsr_rotary;
+int gsr_rotary_forward(gsr_ctx *ctx, const gsr_rotary *desc, const gsr_heads *x, const void *positions,
+                       const float *frequencies, const gsr_heads *out, void *stream);
+
+/* Backward of gsr_rotary_forward: the rotation by -theta of dL/dout (positions
+ * and frequencies get no gradient).  dl_dx may be dl_dout itself. */
+int gsr_rotary_backward(gsr_ctx *ctx, const gsr_rotary *desc, const gsr_heads *dl_dout, const void *positions,
+                        const float *frequencies, const gsr_heads *dl_dx, void *stream);
+
+/* Cross attention of q_len query tokens to kv_len states of an encoder:
+ *   s = scale q . k over the valid keys,  lse = log sum exp s,
+ *   out = sum exp(s - lse) v.
+ * Key j of batch item b is valid when j < kv_lengths[b] and key_mask[b][j] != 0.
+ * A row without a valid key gives out = 0, lse = -inf and no gradient.  What an
+ * invalid key's k and v hold (infinities and NaN too) reaches no result.  Query
+ * head h attends to key head h / (q_heads / kv_heads).
+ *
+ *   dtype       GSR_BF16 or GSR_F16, of q, k, v and out; products are summed and
+ *               the softmax taken in float, its probabilities rounded to dtype
+ *               for the product with v
+ *   kv_lengths  device, [batch] int32 or NULL (all kv_len); values outside
+ *               [0, kv_len] are clamped
+ *   key_mask    device, [batch * kv_len] bytes or NULL
+ *   q, out      [batch, q_len, q_heads, head_dim]
+ *   k, v        [batch, kv_len, kv_heads, head_dim]
+ *   lse         device, [batch, q_heads, q_len] float, written (for the backward)
+ * head_dim is a multiple of 8, at most GSR_ATTENTION_MAX_HEAD_DIM; arrays are
+ * 16-byte aligned and their strides multiples of 8 elements.
+ * Errors: GSR_ERR_INVALID_ARG (the above, negative sizes, q_heads not a multiple
+ * of kv_heads, scale not finite or <= 0), GSR_ERR_OOM, GSR_ERR_CUDA. */
+#define GSR_ATTENTION_MAX_HEAD_DIM 128
+typedef struct gsr_attention {
+    int32_t dtype;
+    int32_t batch, q_len, kv_len, q_heads, kv_heads, head_dim;
+    float scale;
+    const int32_t *kv_lengths;
+    const uint8_t *key_mask;
+} gsr_attention;
+int gsr_cross_attention_forward(gsr_ctx *ctx, const gsr_attention *desc, const gsr_heads *q, const gsr_heads *k,
+                                const gsr_heads *v, const gsr_heads *out, float *lse, void *stream);
+
+/* Backward of gsr_cross_attention_forward: with p = exp(s - lse), dp = dL/dout v
+ * and delta = dL/dout . out,
+ *   dL/dv = sum p dL/dout,  ds = p (dp - delta),
+ *   dL/dq = scale sum ds k,  dL/dk = scale sum ds q
+ * (dL/dk and dL/dv summed over the query heads that share a key head; p and ds
+ * are rounded to dtype for their products).  out and lse are the forward's.  The
+ * gradients are overwritten, zero at invalid keys, and the same bits on every
+ * run.  Errors: as the forward. */
+int gsr_cross_attention_backward(gsr_ctx *ctx, const gsr_attention *desc, const gsr_heads *q, const gsr_heads *k,
+                                 const gsr_heads *v, const gsr_heads *out, const float *lse,
+                                 const gsr_heads *dl_dout, const gsr_heads *dl_dq, const gsr_heads *dl_dk,
+                                 const gsr_heads *dl_dv, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

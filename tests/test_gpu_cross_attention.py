@@ -1,0 +1,249 @@
+"""Cross attention to states of another length against its 64-bit form."""
+import math
+
+import pytest
+import torch
+
+import decoder_reference as ref
+
+pytestmark = pytest.mark.gpu
+BF16, F16 = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module")
+def gsr():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import gaussian_splatting_tile_bin_gb300 as g
+    return g
+
+
+@pytest.fixture(scope="module")
+def ctx(gsr):
+    c = gsr.Context(0)
+    yield c
+    c.close()
+
+
+def _inputs(b, lq, lk, hq, hk, d, dtype, seed, size=1.0):
+    g = torch.Generator().manual_seed(seed)
+    q, dout = (torch.randn(b, lq, hq, d, generator=g).to(dtype) for _ in range(2))
+    k, v = (torch.randn(b, lk, hk, d, generator=g).to(dtype) for _ in range(2))
+    return q * size, k, v, dout
+
+
+def _valid(b, lk, lengths, mask):
+    valid = torch.ones(b, lk, dtype=torch.bool)
+    if lengths is not None:
+        valid &= torch.arange(lk) < lengths[:, None]
+    if mask is not None:
+        valid &= mask.bool()
+    return valid
+
+
+def _compare(gsr, ctx, q, k, v, dout, lengths=None, mask=None, scale=None, backward=True, poison=True):
+    valid = _valid(k.shape[0], k.shape[1], lengths, mask)
+    want = ref.attention(q.double(), k.double(), v.double(), valid, scale or q.shape[3] ** -0.5, q.dtype,
+                         dout.double() if backward else None)
+    kd, vd = k.cuda(), v.cuda()
+    if poison:   # what an invalid key holds must reach nothing
+        kd[~valid.cuda()] = float("nan")
+        vd[~valid.cuda()] = float("inf")
+    opts = dict(kv_lengths=None if lengths is None else lengths.cuda(), key_mask=None if mask is None else mask.cuda(),
+                scale=scale)
+    out, lse = gsr.cross_attention_forward(ctx, q.cuda(), kd, vd, **opts)
+    ref.check(lse, want["lse"], "lse")
+    ref.check(out, want["out"], "out")
+    if backward:
+        grads = gsr.cross_attention_backward(ctx, q.cuda(), kd, vd, out, lse, dout.cuda(), **opts)
+        for name, got in zip(("dq", "dk", "dv"), grads):
+            ref.check(got, want[name], name)
+    return want
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d", [8, 32, 64, 72, 96, 128])
+@pytest.mark.parametrize("lq,lk", [(1, 1), (1, 300), (5, 77), (16, 256), (129, 127), (300, 130)])
+def test_parity(gsr, ctx, dtype, d, lq, lk):
+    _compare(gsr, ctx, *_inputs(2, lq, lk, 4, 2, d, dtype, lq + lk + d))
+
+
+@pytest.mark.parametrize("hq,hk", [(1, 1), (3, 1), (8, 2), (6, 3), (20, 1)])
+@pytest.mark.parametrize("lq", [1, 3, 40])
+def test_head_groups(gsr, ctx, hq, hk, lq):
+    _compare(gsr, ctx, *_inputs(1, lq, 140, hq, hk, 64, BF16, hq + hk + lq))
+
+
+@pytest.mark.parametrize("lq", [1, 2, 15, 16, 17, 64, 127, 128, 129, 255, 256, 257, 400])
+@pytest.mark.parametrize("lk", [63, 64, 65, 128, 129, 257])
+def test_lengths_around_the_tiles(gsr, ctx, lq, lk):
+    _compare(gsr, ctx, *_inputs(1, lq, lk, 2, 1, 64, F16, lq * lk))
+
+
+@pytest.mark.parametrize("lq", [1, 7, 50, 300])
+@pytest.mark.parametrize("d", [64, 128])
+def test_lengths_of_the_items(gsr, ctx, lq, d):
+    """Item lengths of zero, one, a tile's edges and all keys; values outside are clamped."""
+    args = _inputs(8, lq, 260, 2, 2, d, BF16, lq)
+    lengths = torch.tensor([0, 1, 127, 128, 129, 256, 260, 259], dtype=torch.int32)
+    want = _compare(gsr, ctx, *args, lengths=lengths)
+    assert (want["out"][0][0] == 0).all()
+    q, k, v, _ = args
+    wild = torch.tensor([-5, 1, 127, 128, 129, 256, 1 << 30, 259], dtype=torch.int32).cuda()
+    out, lse = gsr.cross_attention_forward(ctx, q.cuda(), k.cuda(), v.cuda(), kv_lengths=wild)
+    same, lse2 = gsr.cross_attention_forward(ctx, q.cuda(), k.cuda(), v.cuda(), kv_lengths=lengths.cuda())
+    assert torch.equal(out, same) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("lq", [1, 4, 140])
+@pytest.mark.parametrize("kind", [torch.bool, torch.uint8])
+def test_masks(gsr, ctx, lq, kind):
+    """Scattered masks, one that leaves nothing, one key, whole tiles out, with and without lengths."""
+    args = _inputs(5, lq, 515, 4, 2, 64, BF16, lq)
+    mask = torch.rand(5, 515, generator=torch.Generator().manual_seed(1)) < 0.5
+    mask[1] = False
+    mask[2] = False
+    mask[2, 300] = True
+    mask[3, 64:400] = False
+    mask[4] = True
+    stored = mask.to(kind) if kind == torch.bool else mask.to(kind) * 7
+    _compare(gsr, ctx, *args, mask=stored)
+    _compare(gsr, ctx, *args, mask=stored, lengths=torch.tensor([500, 515, 300, 65, 0], dtype=torch.int32))
+
+
+@pytest.mark.parametrize("lq,lk", [(1, 20000), (3, 9001), (33, 6000), (700, 2100), (2100, 77)])
+def test_long(gsr, ctx, lq, lk):
+    _compare(gsr, ctx, *_inputs(1, lq, lk, 2, 1, 128, BF16, lk), lengths=torch.tensor([lk - 3], dtype=torch.int32))
+
+
+def test_large_scores(gsr, ctx):
+    """Scores of several hundred: one key takes a row, and the running maximum moves late."""
+    q, k, v, dout = _inputs(1, 200, 400, 2, 2, 64, F16, 3, size=30.0)
+    k = (k * torch.linspace(0.2, 3.0, 400)[None, :, None, None]).to(F16)
+    _compare(gsr, ctx, q, k, v, dout)
+    for lq in (1, 200):
+        _compare(gsr, ctx, q[:, :lq], k.flip(1), v, dout[:, :lq], scale=0.5)
+
+
+def test_strides(gsr, ctx):
+    """Heads before tokens, packed projections, shared items and heads, gradients written into views."""
+    g = torch.Generator().manual_seed(9)
+    for lq in (2, 150):
+        q = torch.randn(2, 4, lq, 64, generator=g).to(BF16).cuda().transpose(1, 2)
+        kv = torch.randn(2, 300, 2, 2, 64, generator=g).to(BF16).cuda()
+        dout = torch.randn(2, 4, lq, 64, generator=g).to(BF16).cuda().transpose(1, 2)
+        k, v = kv[:, :, 0], kv[:, :, 1]
+        shared = torch.randn(1, 300, 1, 64, generator=g).to(BF16).cuda().expand(2, 300, 2, 64)
+        for kk, vv in ((k, v), (shared, v), (k[:1].expand_as(k), shared)):
+            dense = [t.contiguous() for t in (q, kk, vv, dout)]
+            out, lse = gsr.cross_attention_forward(ctx, *dense[:3])
+            want = gsr.cross_attention_backward(ctx, *dense[:3], out, lse, dense[3])
+            room = torch.zeros(2, 4, lq, 64, dtype=BF16, device="cuda").transpose(1, 2)
+            got, lse2 = gsr.cross_attention_forward(ctx, q, kk, vv, out=room)
+            assert torch.equal(got, out) and torch.equal(lse, lse2)
+            grad = torch.full_like(kv, 7.0)
+            dq = torch.zeros(2, 4, lq, 64, dtype=BF16, device="cuda").transpose(1, 2)
+            gsr.cross_attention_backward(ctx, q, kk, vv, got, lse2, dout, dl_dq=dq, dl_dk=grad[:, :, 0],
+                                         dl_dv=grad[:, :, 1])
+            assert torch.equal(dq, want[0]) and torch.equal(grad[:, :, 0], want[1])
+            assert torch.equal(grad[:, :, 1], want[2])
+
+
+def test_same_bits_on_every_run(gsr, ctx):
+    for lq, lk in ((1, 5000), (300, 900)):
+        q, k, v, dout = (t.cuda() for t in _inputs(2, lq, lk, 8, 2, 128, BF16, 5))
+        runs = []
+        for _ in range(3):
+            out, lse = gsr.cross_attention_forward(ctx, q, k, v)
+            runs.append((out, lse) + gsr.cross_attention_backward(ctx, q, k, v, out, lse, dout))
+        for run in runs[1:]:
+            assert all(torch.equal(a, b) for a, b in zip(run, runs[0]))
+
+
+def test_gradient_against_differences(gsr, ctx):
+    q, k, v, dout = _inputs(1, 40, 150, 4, 2, 32, F16, 6)
+    lengths = torch.tensor([141], dtype=torch.int32)
+    valid = _valid(1, 150, lengths, None)
+    out, lse = gsr.cross_attention_forward(ctx, q.cuda(), k.cuda(), v.cuda(), kv_lengths=lengths.cuda())
+    grads = gsr.cross_attention_backward(ctx, q.cuda(), k.cuda(), v.cuda(), out, lse, dout.cuda(),
+                                         kv_lengths=lengths.cuda())
+    args = [q.double(), k.double(), v.double()]
+    bounds = ref.attention(*args, valid, 32 ** -0.5, F16, dout.double())
+    h = 1e-5
+    for i, name in enumerate(("dq", "dk", "dv")):
+        d = torch.randn(args[i].shape, dtype=torch.float64, generator=torch.Generator().manual_seed(i))
+        ends = []
+        for sign in (1, -1):
+            moved = list(args)
+            moved[i] = args[i] + sign * h * d
+            ends.append((ref.attention(*moved, valid, 32 ** -0.5, F16)["out"][0] * dout.double()).sum())
+        slope = (ends[0] - ends[1]) / (2 * h)
+        got = (grads[i].cpu().double() * d).sum()
+        assert abs(slope - got) <= (bounds[name][1] * d.abs()).sum() + 1e-6
+
+
+def test_empty(gsr, ctx):
+    q, k, v, dout = (t.cuda() for t in _inputs(2, 5, 7, 2, 1, 64, BF16, 7))
+    none = k[:, :0]
+    out, lse = gsr.cross_attention_forward(ctx, q, none, none)
+    assert (out == 0).all() and (lse == -math.inf).all()
+    dq, dk, dv = gsr.cross_attention_backward(ctx, q, none, none, out, lse, dout)
+    assert (dq == 0).all() and dk.numel() == 0
+    out, lse = gsr.cross_attention_forward(ctx, q[:, :0], k, v)
+    assert out.numel() == 0
+    dq, dk, dv = gsr.cross_attention_backward(ctx, q[:, :0], k, v, out, lse, dout[:, :0])
+    assert (dk == 0).all() and (dv == 0).all()
+    out, lse = gsr.cross_attention_forward(ctx, q[:0], k[:0], v[:0])
+    assert out.numel() == 0 and lse.numel() == 0
+
+
+def test_other_stream_and_graph(gsr, ctx):
+    q, k, v, dout = (t.cuda() for t in _inputs(2, 200, 700, 4, 2, 64, F16, 8))
+    mask = (torch.rand(2, 700) < 0.7).cuda()
+
+    def step():
+        out, lse = gsr.cross_attention_forward(ctx, q, k, v, key_mask=mask)
+        one, lse1 = gsr.cross_attention_forward(ctx, q[:, :1], k, v, key_mask=mask)
+        return (out, lse, one, lse1) + gsr.cross_attention_backward(ctx, q, k, v, out, lse, dout, key_mask=mask)
+
+    want = step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out, lse = gsr.cross_attention_forward(ctx, q, k, v, key_mask=mask, stream=side)
+    again = step()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0]) and all(torch.equal(a, b) for a, b in zip(again, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_refusals(gsr, ctx):
+    q, k, v, dout = (t.cuda() for t in _inputs(2, 5, 7, 2, 1, 64, BF16, 7))
+    f = gsr.cross_attention_forward
+    for call in (lambda: f(ctx, q[..., :60], k[..., :60], v[..., :60]),                    # head_dim
+                 lambda: f(ctx, *(torch.zeros(1, 2, 1, 136, dtype=BF16, device="cuda"),) * 3),
+                 lambda: f(ctx, torch.zeros(2, 5, 3, 64, dtype=BF16, device="cuda"), *(k.expand(2, 7, 2, 64),) * 2),
+                 lambda: f(ctx, q, k, v, scale=0.0), lambda: f(ctx, q, k, v, scale=-1.0),
+                 lambda: f(ctx, q, k, v, scale=float("nan")),
+                 lambda: f(ctx, q, k[:, :1].expand_as(k), v),                              # tokens that share memory
+                 lambda: f(ctx, torch.zeros(2, 5, 2, 68, dtype=BF16, device="cuda")[..., 4:], k, v),  # alignment
+                 lambda: f(ctx, torch.zeros(2, 5, 2, 68, dtype=BF16, device="cuda")[..., :64], k, v),  # strides
+                 lambda: f(ctx, q, k, v, out=q[:1].expand_as(q))):
+        with pytest.raises(gsr.GsrError) as e:
+            call()
+        assert e.value.code == 1
+    for call in (lambda: f(ctx, q.float(), k.float(), v.float()), lambda: f(ctx, q, k.half(), v),
+                 lambda: f(ctx, q, k, v[:, :6]), lambda: f(ctx, q[0], k, v), lambda: f(ctx, q.cpu(), k, v),
+                 lambda: f(ctx, q.transpose(2, 3), k, v),
+                 lambda: f(ctx, q, k, v, kv_lengths=torch.ones(2, dtype=torch.int64, device="cuda")),
+                 lambda: f(ctx, q, k, v, kv_lengths=torch.ones(3, dtype=torch.int32, device="cuda")),
+                 lambda: f(ctx, q, k, v, key_mask=torch.ones(2, 6, dtype=torch.bool, device="cuda")),
+                 lambda: f(ctx, q, k, v, key_mask=torch.ones(2, 7, device="cuda")),
+                 lambda: f(ctx, q, k, v, lse=torch.ones(2, 2, 4, device="cuda"))):
+        with pytest.raises(ValueError):
+            call()
