@@ -125,6 +125,7 @@ void gsr_destroy(gsr_ctx *ctx)
         cudaFree(ctx->bwd_items);
         cudaFree(ctx->fwd_items);
         cudaFree(ctx->work);
+        if (ctx->status_host) cudaFreeHost(ctx->status_host);
         if (ctx->work_event) cudaEventDestroy(ctx->work_event);
         if (ctx->host_total) cudaFreeHost(ctx->host_total);
     }
@@ -469,6 +470,9 @@ int check_attention(gsr_ctx *ctx, const gsr_attention *d)
         return fail(ctx, GSR_ERR_INVALID_ARG, "scale must be finite and > 0");
     if (d->batch > (1 << 16) || d->q_len > (1 << 24) || d->kv_len > (1 << 24))
         return fail(ctx, GSR_ERR_INVALID_ARG, "batch above 2^16 or a length above 2^24");
+    constexpr int64_t kMost = 0x7fffffff;
+    if ((int64_t)d->batch * d->q_len > kMost / d->q_heads || (int64_t)d->batch * d->kv_len > kMost / d->kv_heads)
+        return fail(ctx, GSR_ERR_INVALID_ARG, "batch * heads * length above 2^31 - 1");
     if (!aligned(d->kv_lengths, 4)) return fail(ctx, GSR_ERR_INVALID_ARG, "kv_lengths must be 4-byte aligned");
     return GSR_OK;
 }

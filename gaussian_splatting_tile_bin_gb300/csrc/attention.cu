@@ -52,57 +52,11 @@ __device__ __forceinline__ float warp_sum(float x)
     return x;
 }
 
-__device__ __forceinline__ float warp_max(float x)
-{
-    for (int d = 16; d > 0; d /= 2) x = fmaxf(x, __shfl_xor_sync(~0u, x, d));
-    return x;
-}
-
 template <typename T>
 __device__ __forceinline__ void stage(float *to, const T *from, int dim, int lane)
 {
     for (int c = lane; c < dim; c += 32) to[c] = to_float(from[c]);
     __syncwarp();
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) k_attention_rows(const AttentionArgs a)
-{
-    grid_dependency_begin();
-    __shared__ float s_q[kWarps][kMaxDim];
-    const gsr_attention &d = a.d;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int64_t r = (int64_t)blockIdx.x * kWarps + warp;
-    if (r >= (int64_t)d.batch * d.q_heads * d.q_len) return;
-    const int64_t i = r % d.q_len, h = r / d.q_len % d.q_heads, b = r / d.q_len / d.q_heads;
-    const int64_t hk = h / (d.q_heads / d.kv_heads);
-    stage(s_q[warp], row_of<T>(a.q, b, i, h), d.head_dim, lane);
-    float m = -INFINITY, l = 0.0f, o[kPerLane] = {};
-    for (int j0 = 0; j0 < d.kv_len; j0 += 32) {
-        const int j = j0 + lane;
-        const bool ok = valid_key(d, b, j);
-        const unsigned live = __ballot_sync(~0u, ok);
-        if (!live) continue;
-        const float s = ok ? d.scale * dot(s_q[warp], row_of<T>(a.k, b, j, hk), d.head_dim) : -INFINITY;
-        const float top = fmaxf(m, warp_max(s));
-        const float base = top == -INFINITY ? 0.0f : top;
-        const float p = expf(s - base), keep = expf(m - base);
-        l = l * keep + warp_sum(p);
-        for (int e = 0; e < kPerLane; ++e) o[e] *= keep;
-        for (int n = 0; n < 32; ++n) {
-            if (!(live >> n & 1)) continue;
-            const float pn = __shfl_sync(~0u, p, n);
-            const T *v = row_of<T>(a.v, b, j0 + n, hk);
-            for (int e = 0; e < kPerLane; ++e)
-                if (lane + 32 * e < d.head_dim) o[e] = fmaf(pn, to_float(v[lane + 32 * e]), o[e]);
-        }
-        m = top;
-    }
-    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-    T *out = row_of<T>(a.out, b, i, h);
-    for (int e = 0; e < kPerLane; ++e)
-        if (lane + 32 * e < d.head_dim) out[lane + 32 * e] = from_float<T>(o[e] * inv);
-    if (lane == 0) a.lse[r] = m + logf(l);
 }
 
 template <typename T>
@@ -193,23 +147,6 @@ __global__ void __launch_bounds__(kWarps * 32) k_attention_grad_keys(const Atten
 dim3 warp_grid(int64_t rows) { return dim3((unsigned)((rows + kWarps - 1) / kWarps)); }
 
 }  // namespace
-
-int cross_attention_forward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr_heads &k,
-                            const gsr_heads &v, const gsr_heads &out, float *lse, cudaStream_t stream)
-{
-    AttentionArgs a = {};
-    a.d = d;
-    a.q = q;
-    a.k = k;
-    a.v = v;
-    a.out = out;
-    a.lse = lse;
-    const dim3 grid = warp_grid((int64_t)d.batch * d.q_heads * d.q_len);
-    const cudaError_t e = d.dtype == GSR_BF16
-                              ? launch_kernel(ctx, k_attention_rows<__nv_bfloat16>, grid, kWarps * 32, stream, a)
-                              : launch_kernel(ctx, k_attention_rows<__half>, grid, kWarps * 32, stream, a);
-    return cuda_check(ctx, e, "cross attention forward");
-}
 
 int cross_attention_backward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr_heads &k,
                              const gsr_heads &v, const gsr_heads &out, const float *lse, const gsr_heads &dout,

@@ -1,0 +1,483 @@
+// attention_forward.cu -- cross attention to an encoder's states of another
+// length, forward.
+//
+//   s = scale q . k,  o = sum exp(s - m) v / l,  l = sum exp(s - m),  lse = m + log l
+//
+// One pass over the keys with the running maximum m and sum l of each row.  A
+// block holds two tiles of 128 query rows, each with its own 128 threads (one
+// row a thread) and its own score and output accumulators in tensor memory.  One
+// thread issues the products: scores S = Q K^T (operands in shared memory) and
+// outputs O += P V with P in tensor memory, where it replaces the scores it came
+// from.  While one tile's threads take the exponentials, the tensor cores work
+// for the other tile, so both pipes stay busy.  K and V tiles arrive by bulk
+// tensor copies through a ring of stages.
+//
+// The output is rescaled only when a row's maximum grows by more than 2^8: until
+// then P exceeds 1 by at most that factor, which 16-bit P and float sums hold
+// without loss.  P is rounded to the storage type (the tensor cores take 16-bit
+// operands at the full rate); l sums the unrounded values in float.
+#include <math.h>
+
+#include "attention.cuh"
+
+namespace gsr {
+namespace {
+
+constexpr int kRowTile = 128;
+constexpr int kForwardThreads = 384;   // two row groups of 128; four warps of which one copies and one issues
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct ForwardArgs {
+    CUtensorMap q, k, v;
+    Schedule work;
+    void *out;
+    int64_t out_item, out_token, out_head;
+    float *lse;
+    float *partial;        // [2 blocks][256][dim] of cut tiles
+    float *partial_lse;    // [2 blocks][256]
+    uint32_t *status;
+    int q_len, q_heads, group, dim, row_tiles;
+    int q_item, q_head, k_item, k_head, v_item, v_head;   // 0: one array for all items / heads
+    float scale_log2;
+};
+
+template <int HD>
+struct ForwardShape {
+    static constexpr int kBlocks = HD / 64;
+    static constexpr int kTileBytes = kBlocks * kBlockBytes;
+    static constexpr int kStages = HD == 128 ? 5 : 8;
+    static constexpr int kBarriers = 2 + 2 * kStages + 6;
+    static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + kBarriers * 8 + 16;
+    static constexpr int kOut = 256;   // tensor memory column of the outputs
+    static constexpr int kColumns = 512;
+};
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const __grid_constant__ ForwardArgs a)
+{
+    grid_dependency_begin();
+    using S = ForwardShape<HD>;
+    extern __shared__ unsigned char s_raw[];
+    const uint32_t raw = smem_address(s_raw);
+    const uint32_t base = (raw + 1023) & ~1023u;
+    const uint32_t s_q = base, s_kv = base + 2 * S::kTileBytes, bars = s_kv + S::kStages * S::kTileBytes;
+    const uint32_t b_q = bars, b_q_free = bars + 8, b_kv = bars + 16, b_kv_free = b_kv + 8 * S::kStages;
+    const uint32_t b_s = b_kv_free + 8 * S::kStages, b_p = b_s + 16, b_o = b_p + 16, tail = b_o + 16;
+    uint32_t *s_words = (uint32_t *)(s_raw + (tail - raw));   // tensor memory base, abort flag
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const WaitGuard guard = {s_words + 1, a.status};
+
+    if (threadIdx.x == 0) {
+        s_words[1] = 0;
+        barrier_init(b_q, 1);
+        barrier_init(b_q_free, 1);
+        for (int i = 0; i < S::kStages; ++i) {
+            barrier_init(b_kv + 8 * i, 1);
+            barrier_init(b_kv_free + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            barrier_init(b_s + 8 * i, 1);
+            barrier_init(b_p + 8 * i, 4);
+            barrier_init(b_o + 8 * i, 1);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async();
+    }
+    if (warp == 9) tmem_alloc(tail, S::kColumns);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = s_words[0];
+
+    const int64_t line = QueryWalk::line(a.work);
+    const int blocks = busy_blocks(line, gridDim.x), block = min((int)blockIdx.x, blocks);
+    QueryWalk walk(a.work, share_begin(line, block, blocks),
+                   block < blocks ? share_begin(line, block + 1, blocks) : line);
+    Segment g;
+    const int row_tiles = a.row_tiles;   // of 256 rows, per head
+
+    if (warp >= 8) {
+    give_registers();
+    if (warp == 8) {
+        // ---- copies: Q of a segment, then K and V of every step ----
+        if (elect_one()) {
+            prefetch_map(&a.q);
+            prefetch_map(&a.k);
+            prefetch_map(&a.v);
+            uint32_t kv = 0, seg = 0;
+            while (walk.next(g)) {
+                if (g.length == 0) continue;
+                const int head = g.tile / row_tiles, row0 = (g.tile - head * row_tiles) * 2 * kRowTile;
+                const int tiles = a.q_len - row0 > kRowTile ? 2 : 1;
+                const int key_head = head / a.group;
+                if (seg > 0) barrier_wait(b_q_free, (seg - 1) & 1, guard);
+                barrier_expect(b_q, tiles * S::kTileBytes);
+                for (int t = 0; t < tiles; ++t)
+                    for (int c = 0; c < S::kBlocks; ++c)
+                        copy_box(s_q + t * S::kTileBytes + c * kBlockBytes, &a.q, b_q, c * 64, row0 + t * kRowTile,
+                                 head * a.q_head, g.item * a.q_item);
+                for (int i = g.begin; i < g.end; ++i)
+                    for (int half = 0; half < 2; ++half, ++kv) {
+                        const uint32_t stage = kv % S::kStages, round = kv / S::kStages;
+                        if (round > 0) barrier_wait(b_kv_free + 8 * stage, (round - 1) & 1, guard);
+                        const uint32_t bar = b_kv + 8 * stage, to = s_kv + stage * S::kTileBytes;
+                        barrier_expect(bar, S::kTileBytes);
+                        for (int c = 0; c < S::kBlocks; ++c)
+                            copy_box(to + c * kBlockBytes, half ? &a.v : &a.k, bar, c * 64, i * kKeyTile,
+                                     key_head * (half ? a.v_head : a.k_head), g.item * (half ? a.v_item : a.k_item));
+                    }
+                ++seg;
+            }
+        }
+    } else if (warp == 9) {
+        // ---- products ----
+        if (elect_one()) {
+            const uint32_t form_s = product_form<T>(kKeyTile, false);
+            const uint32_t form_o = product_form<T>((a.dim + 15) & ~15, true);
+            const int steps = (a.dim + 15) / 16;
+            uint32_t kv = 0, seg = 0, p[2] = {0, 0};
+            while (walk.next(g)) {
+                if (g.length == 0) continue;
+                const int head = g.tile / row_tiles, row0 = (g.tile - head * row_tiles) * 2 * kRowTile;
+                const int tiles = a.q_len - row0 > kRowTile ? 2 : 1;
+                barrier_wait(b_q, seg & 1, guard);
+                auto stage_at = [&](uint32_t n) { return s_kv + n % S::kStages * S::kTileBytes; };
+                auto await = [&](uint32_t n) {
+                    barrier_wait(b_kv + 8 * (n % S::kStages), n / S::kStages & 1, guard);
+                };
+                auto release = [&](uint32_t n) { product_commit(b_kv_free + 8 * (n % S::kStages)); };
+                await(kv);
+                tmem_fence_after();
+                for (int t = 0; t < tiles; ++t) {
+                    product_rows(tmem + t * kKeyTile, s_q + t * S::kTileBytes, stage_at(kv), form_s, steps);
+                    product_commit(b_s + 8 * t);
+                }
+                release(kv);
+                for (int i = g.begin; i < g.end; ++i, kv += 2) {
+                    const bool more = i + 1 < g.end;
+                    await(kv + 1);
+                    if (more) await(kv + 2);
+                    for (int t = 0; t < tiles; ++t) {
+                        barrier_wait(b_p + 8 * t, p[t]++ & 1, guard);
+                        tmem_fence_after();
+                        product_across(tmem + S::kOut + t * HD, tmem + t * kKeyTile, stage_at(kv + 1), form_o,
+                                       i > g.begin);
+                        if (more) {
+                            product_rows(tmem + t * kKeyTile, s_q + t * S::kTileBytes, stage_at(kv + 2), form_s,
+                                         steps);
+                            product_commit(b_s + 8 * t);
+                        } else {
+                            product_commit(b_o + 8 * t);
+                        }
+                    }
+                    release(kv + 1);
+                    if (more) release(kv + 2);
+                }
+                product_commit(b_q_free);
+                ++seg;
+            }
+        }
+    }
+    } else {
+        take_registers();
+        // ---- softmax: one row a thread ----
+        const int t = warp / 4;                                     // row tile
+        const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;     // this warp's lanes of tensor memory
+        const uint32_t at_s = tmem + lanes + t * kKeyTile, at_o = tmem + lanes + S::kOut + t * HD;
+        const int row_in_tile = warp % 4 * 32 + lane;
+        const float c = a.scale_log2;
+        uint32_t kv = 0, n_s = 0, n_o = 0;
+        while (walk.next(g)) {
+            const int head = g.tile / row_tiles, row0 = (g.tile - head * row_tiles) * 2 * kRowTile + t * kRowTile;
+            const int row = row0 + row_in_tile;
+            const bool whole = g.whole();
+            float m = -INFINITY, l = 0.0f;
+            const bool active = row0 < a.q_len;
+            if (g.length > 0 && active) {
+                for (int i = g.begin; i < g.end; ++i) {
+                    barrier_wait(b_s + 8 * t, n_s++ & 1, guard);
+                    tmem_fence_after();
+                    uint32_t r[4][32];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) tmem_load32(r[x], at_s + x * 32);
+                    tmem_wait_load();
+                    const int valid = g.length - i * kKeyTile;
+                    if (valid < kKeyTile) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+#pragma unroll
+                            for (int y = 0; y < 32; ++y)
+                                if (x * 32 + y >= valid) r[x][y] = __float_as_uint(-INFINITY);
+                        if (t == 0) {
+                            // What lies behind the item's last key must not meet the
+                            // zero probabilities as infinities or NaN.
+                            const uint32_t n = kv + 2 * (i - g.begin) + 1;
+                            barrier_wait(b_kv + 8 * (n % S::kStages), n / S::kStages & 1, guard);
+                            if (row_in_tile >= valid) {
+                                unsigned char *v = s_raw + (s_kv - raw) + n % S::kStages * S::kTileBytes +
+                                                   row_in_tile * 128;
+                                for (int b = 0; b < S::kBlocks; ++b)
+                                    for (int e = 0; e < 8; ++e)
+                                        *(uint4 *)(v + b * kBlockBytes + e * 16) = make_uint4(0, 0, 0, 0);
+                            }
+                            fence_async();
+                        }
+                    }
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+#pragma unroll
+                        for (int y = 0; y < 32; y += 2)
+                            top = fmaxf(top, fmaxf(__uint_as_float(r[x][y]), __uint_as_float(r[x][y + 1])));
+                    if (i == g.begin) {
+                        m = top;
+                    } else if (__any_sync(~0u, top * c > m * c + 8.0f)) {
+                        const float next = fmaxf(m, top);
+                        const float keep = exp2_fast((m - (next == -INFINITY ? 0.0f : next)) * c);
+                        m = next;
+                        l *= keep;
+                        for (int x = 0; x < HD; x += 32) {
+                            uint32_t o[32];
+                            tmem_load32(o, at_o + x);
+                            tmem_wait_load();
+#pragma unroll
+                            for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * keep);
+                            tmem_store32(at_o + x, o);
+                        }
+                    }
+                    const float shift = m == -INFINITY ? 0.0f : -m * c;
+                    const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
+                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        uint32_t packed[16];
+#pragma unroll
+                        for (int y = 0; y < 32; y += 2) {
+                            float2 e = fma2(make_float2(__uint_as_float(r[x][y]), __uint_as_float(r[x][y + 1])), c2,
+                                            shift2);
+                            e.x = exp2_fast(e.x);
+                            e.y = exp2_fast(e.y);
+                            sum[y / 2 & 1] = add2(sum[y / 2 & 1], e);
+                            packed[y / 2] = pack2<T>(e.x, e.y);
+                        }
+                        tmem_store16(at_s + x * 16, packed);
+                    }
+                    tmem_wait_store();
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0) barrier_arrive(b_p + 8 * t);
+                    l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+                }
+                barrier_wait(b_o + 8 * t, n_o++ & 1, guard);
+                tmem_fence_after();
+            }
+            if (g.length > 0) kv += 2 * (g.end - g.begin);
+            if (!active) continue;
+            const bool store = row < a.q_len;
+            const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+            const float lse = m * (c * kLn2) + logf(l);
+            const int slot = partial_slot(g, blockIdx.x);
+            T *out = (T *)a.out + g.item * a.out_item + (int64_t)row * a.out_token + head * a.out_head;
+            float *partial = a.partial + ((int64_t)slot * 2 * kRowTile + t * kRowTile + row_in_tile) * a.dim;
+            for (int x = 0; x < HD; x += 32) {
+                if (x >= a.dim) break;
+                uint32_t o[32];
+                __syncwarp();
+                if (g.length > 0) {
+                    tmem_load32(o, at_o + x);
+                    tmem_wait_load();
+                } else {
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) o[y] = 0;
+                }
+                if (store) {
+#pragma unroll
+                    for (int y = 0; y < 32; y += 8)
+                        if (x + y < a.dim) {
+                            float f[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) f[e] = inv == 0.0f ? 0.0f : __uint_as_float(o[y + e]) * inv;
+                            if (whole) {
+                                *(uint4 *)(out + x + y) = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]),
+                                                                     pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
+                            } else {
+                                *(float4 *)(partial + x + y) = make_float4(f[0], f[1], f[2], f[3]);
+                                *(float4 *)(partial + x + y + 4) = make_float4(f[4], f[5], f[6], f[7]);
+                            }
+                        }
+                }
+            }
+            if (store) {
+                if (whole)
+                    a.lse[((int64_t)g.item * a.q_heads + head) * a.q_len + row] = lse;
+                else
+                    a.partial_lse[(int64_t)slot * 2 * kRowTile + t * kRowTile + row_in_tile] = lse;
+            }
+            tmem_fence_before();
+        }
+    }
+    __syncwarp();
+    drain_if_aborted(guard);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    __syncwarp();
+    if (warp == 9) tmem_free(tmem, S::kColumns);
+}
+
+// Joins the parts of a cut tile: weights exp(lse_part - lse), one warp a row.
+// Block x handles the tile that the start of share x + 1 cuts, if it is the first
+// share that starts inside that tile.
+constexpr int kJoinBlock = 256;
+constexpr int kJoinRows = 16;
+
+template <typename T>
+__global__ void __launch_bounds__(kJoinBlock) k_attention_join(const __grid_constant__ ForwardArgs a, int grid)
+{
+    grid_dependency_begin();
+    const int64_t line = QueryWalk::line(a.work);
+    const int blocks = busy_blocks(line, grid), first = blockIdx.x + 1;
+    if (first >= blocks) return;
+    const int64_t cut = share_begin(line, first, blocks);
+    QueryWalk walk(a.work, cut, line);
+    Segment g;
+    walk.next(g);
+    const int64_t start = cut - g.begin, stop = start + g.total;
+    if (g.begin == 0 || share_begin(line, first - 1, blocks) > start) return;
+    const int head = g.tile / a.row_tiles, row0 = (g.tile - head * a.row_tiles) * 2 * kRowTile;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    int last = first;   // blocks first - 1 .. last hold parts
+    while (last + 1 < blocks && share_begin(line, last + 1, blocks) < stop) ++last;
+    for (int r = blockIdx.y * kJoinRows + warp; r < (int)(blockIdx.y + 1) * kJoinRows; r += kJoinBlock / 32) {
+        const int row = row0 + r;
+        if (row >= a.q_len) return;
+        auto slot = [&](int block) { return (int64_t)(2 * block + (block == first - 1 ? 1 : 0)) * 2 * kRowTile + r; };
+        float top = -INFINITY;
+        for (int b = first - 1 + lane; b <= last; b += 32) top = fmaxf(top, a.partial_lse[slot(b)]);
+        for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+        const float shift = top == -INFINITY ? 0.0f : top;
+        float total = 0.0f;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int b = first - 1; b <= last; ++b) {
+            const float w = expf(a.partial_lse[slot(b)] - shift);
+            total += w;
+            if (lane * 4 < a.dim) {
+                const float4 f = *(const float4 *)(a.partial + slot(b) * a.dim + lane * 4);
+                if (w != 0.0f) {
+                    o.x = fmaf(w, f.x, o.x);
+                    o.y = fmaf(w, f.y, o.y);
+                    o.z = fmaf(w, f.z, o.z);
+                    o.w = fmaf(w, f.w, o.w);
+                }
+            }
+        }
+        const float inv = total > 0.0f ? 1.0f / total : (total == 0.0f ? 0.0f : total);
+        if (lane * 4 < a.dim) {
+            T *out = (T *)a.out + g.item * a.out_item + (int64_t)row * a.out_token + head * a.out_head + lane * 4;
+            *(uint2 *)out = make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
+        }
+        if (lane == 0) a.lse[((int64_t)g.item * a.q_heads + head) * a.q_len + row] = top + logf(total);
+    }
+}
+
+// Rows of an item without keys.
+template <typename T>
+__global__ void __launch_bounds__(256) k_attention_no_keys(void *out, int64_t item_stride, int64_t token_stride,
+                                                           int64_t head_stride, float *lse, int64_t rows, int q_len,
+                                                           int q_heads, int dim)
+{
+    grid_dependency_begin();
+    const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (r >= rows) return;
+    const int64_t i = r % q_len, h = r / q_len % q_heads, b = r / q_len / q_heads;
+    T *o = (T *)out + b * item_stride + i * token_stride + h * head_stride;
+    for (int c = 0; c < dim; c += 8) *(uint4 *)(o + c) = make_uint4(0, 0, 0, 0);
+    if (lse) lse[r] = -INFINITY;
+}
+
+template <typename T, int HD>
+int launch_forward(gsr_ctx *ctx, ForwardArgs &a, int blocks, cudaStream_t stream)
+{
+    auto *kernel = k_attention_forward<T, HD>;
+    constexpr int smem = ForwardShape<HD>::kSmem;
+    if (int rc = cuda_check(ctx, cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
+                            "k_attention_forward"))
+        return rc;
+    if (int rc = check_registers(ctx, (const void *)kernel, "k_attention_forward")) return rc;
+    if (int rc = cuda_check(ctx, launch_kernel_smem(ctx, kernel, dim3((unsigned)blocks), kForwardThreads, smem, stream, a),
+                            "k_attention_forward"))
+        return rc;
+    if (blocks == 1) return GSR_OK;
+    return cuda_check(ctx, launch_kernel(ctx, k_attention_join<T>, dim3((unsigned)blocks - 1, 2 * kRowTile / kJoinRows),
+                                         kJoinBlock, stream, a, blocks),
+                      "k_attention_join");
+}
+
+template <typename T>
+int forward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr_heads &k, const gsr_heads &v,
+            const gsr_heads &out, float *lse, cudaStream_t stream)
+{
+    if (d.kv_len == 0) {
+        const int64_t rows = (int64_t)d.batch * d.q_heads * d.q_len;
+        return cuda_check(ctx, launch_kernel(ctx, k_attention_no_keys<T>, dim3((unsigned)((rows + 255) / 256)), 256,
+                                             stream, out.data, out.batch_stride, out.token_stride, out.head_stride,
+                                             lse, rows, (int)d.q_len, (int)d.q_heads, (int)d.head_dim),
+                          "k_attention_no_keys");
+    }
+    ForwardArgs a = {};
+    a.q_len = d.q_len;
+    a.q_heads = d.q_heads;
+    a.group = d.q_heads / d.kv_heads;
+    a.dim = d.head_dim;
+    a.row_tiles = (d.q_len + 2 * kRowTile - 1) / (2 * kRowTile);
+    a.scale_log2 = d.scale * kLog2e;
+    a.out = out.data;
+    a.out_item = out.batch_stride;
+    a.out_token = out.token_stride;
+    a.out_head = out.head_stride;
+    a.lse = lse;
+    a.work = {d.batch, d.q_heads * a.row_tiles, 1, d.kv_lengths, d.kv_len};
+    const int64_t line = (int64_t)d.batch * a.work.tiles * ((d.kv_len + kKeyTile - 1) / kKeyTile);
+    const int blocks = (int)(line < ctx->num_sms ? line : ctx->num_sms);
+    const size_t rows = (size_t)2 * blocks * 2 * kRowTile;
+    const size_t packed = d.key_mask ? round_up(packed_bytes(d), 256) : 0;
+    const size_t partial = round_up(rows * d.head_dim * sizeof(float), 256);
+    void *work;
+    if (int rc = workspace(ctx, packed + partial + rows * sizeof(float), stream, &work)) return rc;
+    a.partial = (float *)((unsigned char *)work + packed);
+    a.partial_lse = (float *)((unsigned char *)work + packed + partial);
+    a.status = ctx->status_dev;
+    gsr_heads keys = k, values = v;
+    if (d.key_mask) {
+        Packed p;
+        if (int rc = cuda_check(ctx, pack_keys(ctx, d, k, v, work, &p, stream), "k_pack_keys")) return rc;
+        keys = p.k;
+        values = p.v;
+        a.work.lengths = p.counts;
+    }
+    a.q_item = q.batch_stride != 0;
+    a.q_head = q.head_stride != 0;
+    a.k_item = keys.batch_stride != 0;
+    a.k_head = keys.head_stride != 0;
+    a.v_item = values.batch_stride != 0;
+    a.v_head = values.head_stride != 0;
+    if (int rc = heads_map(ctx, &a.q, q, d.dtype, d.batch, d.q_len, d.q_heads, d.head_dim, kRowTile)) return rc;
+    if (int rc = heads_map(ctx, &a.k, keys, d.dtype, d.batch, d.kv_len, d.kv_heads, d.head_dim, kKeyTile)) return rc;
+    if (int rc = heads_map(ctx, &a.v, values, d.dtype, d.batch, d.kv_len, d.kv_heads, d.head_dim, kKeyTile)) return rc;
+    const int rc = d.head_dim <= 64 ? launch_forward<T, 64>(ctx, a, blocks, stream)
+                                    : launch_forward<T, 128>(ctx, a, blocks, stream);
+    if (rc) return rc;
+    return workspace_done(ctx, stream);
+}
+
+}  // namespace
+
+int cross_attention_forward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr_heads &k,
+                            const gsr_heads &v, const gsr_heads &out, float *lse, cudaStream_t stream)
+{
+    if (int rc = check_status(ctx)) return rc;
+    return d.dtype == GSR_BF16 ? forward<__nv_bfloat16>(ctx, d, q, k, v, out, lse, stream)
+                               : forward<__half>(ctx, d, q, k, v, out, lse, stream);
+}
+
+}  // namespace gsr

@@ -79,6 +79,8 @@ struct gsr_ctx {
     cudaStream_t work_stream = nullptr;         // stream of the last call that used it
     cudaEvent_t work_event = nullptr;           // recorded after that call
     bool work_pending = false;                  // work_event holds a record
+    uint32_t *status_host = nullptr;            // pinned: set by a kernel whose bounded wait ran out
+    uint32_t *status_dev = nullptr;             // its device address
 
     // Last binning, for gsr_get_bin_stats and gsr_num_pairs.
     cudaStream_t last_stream = nullptr;

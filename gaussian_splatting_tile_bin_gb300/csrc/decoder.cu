@@ -27,6 +27,20 @@ int workspace(gsr_ctx *ctx, size_t bytes, cudaStream_t stream, void **out)
         ctx->cap_work = grown;
         ctx->work_pending = false;
     }
+    if (!ctx->status_host) {
+        if (capture != cudaStreamCaptureStatusNone)
+            return fail(ctx, GSR_ERR_CUDA, "the workspace must be made before a capture: make one such call before it");
+        void *host = nullptr, *dev = nullptr;
+        if (int rc = cuda_check(ctx, cudaHostAlloc(&host, sizeof(uint32_t), cudaHostAllocMapped), "status word"))
+            return rc;
+        *(uint32_t *)host = 0;
+        if (int rc = cuda_check(ctx, cudaHostGetDevicePointer(&dev, host, 0), "status word")) {
+            cudaFreeHost(host);
+            return rc;
+        }
+        ctx->status_host = (uint32_t *)host;
+        ctx->status_dev = (uint32_t *)dev;
+    }
     // A captured call is ordered by its graph; events of the live streams stay out of it.
     if (capture == cudaStreamCaptureStatusNone && ctx->work_pending && ctx->work_stream != stream)
         if (int rc = cuda_check(ctx, cudaStreamWaitEvent(stream, ctx->work_event, 0), "workspace order")) return rc;
@@ -47,6 +61,14 @@ int workspace_done(gsr_ctx *ctx, cudaStream_t stream)
     ctx->work_stream = stream;
     ctx->work_pending = true;
     return GSR_OK;
+}
+
+int check_status(gsr_ctx *ctx)
+{
+    if (!ctx->status_host || *(volatile uint32_t *)ctx->status_host == 0) return GSR_OK;
+    *(volatile uint32_t *)ctx->status_host = 0;
+    return fail(ctx, GSR_ERR_CUDA, "a kernel of an earlier call gave up waiting for its own copies or products: "
+                                   "that call's results are not valid");
 }
 
 }  // namespace gsr

@@ -33,6 +33,9 @@ struct alignas(sizeof(T) * V) Vec {
 int workspace(gsr_ctx *ctx, size_t bytes, cudaStream_t stream, void **out);
 int workspace_done(gsr_ctx *ctx, cudaStream_t stream);
 
+// GSR_ERR_CUDA, once, if a kernel's bounded wait ran out in an earlier call.
+int check_status(gsr_ctx *ctx);
+
 inline size_t round_up(size_t n, size_t unit) { return (n + unit - 1) / unit * unit; }
 
 }  // namespace gsr

@@ -1,0 +1,325 @@
+// tensor.cuh -- the pieces of sm_103a that the attention kernels are built from:
+// barriers in shared memory, bulk tensor copies, tensor-core products with
+// operands in shared or tensor memory, and tensor memory itself.
+//
+// Operand tiles.  A tile is rows of 64 elements (128 bytes) in the 128-byte
+// swizzle, 8 rows to a 1 KB atom; wider rows are several such blocks one behind
+// the other.  The same tile serves as an operand whose contraction runs along
+// the row (major_k: 32 bytes further per 16 elements) and as one whose
+// contraction runs across the rows (major_mn: 2 KB further per 16 rows).
+#pragma once
+
+#include <cuda.h>
+
+#include <type_traits>
+
+#include "decoder.cuh"
+
+namespace gsr {
+
+constexpr int kBlockBytes = 128 * 128;   // 128 rows of 64 16-bit elements
+
+__device__ __forceinline__ uint32_t smem_address(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t pred;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(pred));
+    return pred != 0;
+}
+
+// ---- barriers -----------------------------------------------------------------
+
+__device__ __forceinline__ void barrier_init(uint32_t bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void barrier_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void barrier_expect(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
+// Waits end: one that has run for kWaitCycles (seconds; a step takes
+// microseconds) marks the block as aborted, reports to the host's status word
+// and returns, and every later wait of the block returns at once, so the kernel
+// runs to its end with results that the host then refuses.
+constexpr long long kWaitCycles = 4000000000ll;
+
+struct WaitGuard {
+    volatile uint32_t *aborted;   // shared
+    uint32_t *status;             // the context's status word (host memory)
+};
+
+__device__ __forceinline__ void barrier_wait(uint32_t bar, uint32_t parity, const WaitGuard &g)
+{
+    if (barrier_try(bar, parity)) return;
+    const long long start = clock64();
+    while (!barrier_try(bar, parity)) {
+        if (*g.aborted) return;
+        if (clock64() - start > kWaitCycles) {
+            *g.aborted = 1;
+            *(volatile uint32_t *)g.status = 1;
+            return;
+        }
+    }
+}
+
+// At the end of an aborted block: time for copies and products in flight to land
+// before its shared memory is given to another block.
+__device__ __forceinline__ void drain_if_aborted(const WaitGuard &g)
+{
+    if (!*g.aborted) return;
+    const long long start = clock64();
+    while (clock64() - start < 20000000ll) {
+    }
+}
+
+// ---- copies ----------------------------------------------------------------------
+
+// The box at (x, row, head, item) of a [item, head, row, x] tensor map into
+// shared memory; elements outside the tensor arrive as zeros.
+__device__ __forceinline__ void copy_box(uint32_t to, const CUtensorMap *map, uint32_t bar, int x, int row, int head,
+                                         int item)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+        "[%2];" ::"r"(to),
+        "l"(map), "r"(bar), "r"(x), "r"(row), "r"(head), "r"(item)
+        : "memory");
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+// Makes this thread's ordinary writes to shared memory visible to copies and products.
+__device__ __forceinline__ void fence_async()
+{
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// ---- tensor memory ------------------------------------------------------------------
+
+__device__ __forceinline__ void tmem_alloc(uint32_t to, uint32_t columns)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to), "r"(columns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_free(uint32_t base, uint32_t columns)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(columns) : "memory");
+}
+
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 columns of the calling thread's lane.
+__device__ __forceinline__ void tmem_load32(uint32_t (&r)[32], uint32_t at)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+        "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(at)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
+        : "memory");
+}
+
+// ---- products -------------------------------------------------------------------------
+
+// Shared-memory operand descriptors (128-byte swizzle, 8-row atoms 1 KB apart):
+// contraction along the row, and across the rows (blocks of 64 along the free
+// dimension kBlockBytes apart).
+constexpr uint64_t kOperandForm = (1ull << 46) | (2ull << 61) | ((uint64_t)(1024 >> 4) << 32);
+
+__device__ __forceinline__ uint64_t operand_rows(uint32_t address)
+{
+    return kOperandForm | (1ull << 16) | ((address >> 4) & 0x3fff);
+}
+
+__device__ __forceinline__ uint64_t operand_across(uint32_t address)
+{
+    return kOperandForm | ((uint64_t)(kBlockBytes >> 4) << 16) | ((address >> 4) & 0x3fff);
+}
+
+// Instruction descriptor: f32 sums of 16-bit operands of one type, M = 128.
+template <typename T>
+__device__ __forceinline__ uint32_t product_form(int n, bool b_major_mn)
+{
+    constexpr uint32_t kType = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
+    return (1u << 4) | (kType << 7) | (kType << 10) | ((b_major_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+           ((128u >> 4) << 24);
+}
+
+// d (128 x n, tensor memory) = a b (+ d), one instruction's 16 terms.
+__device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t form, bool add)
+{
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(form), "r"((uint32_t)add)
+        : "memory");
+}
+
+__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t form, bool add)
+{
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(form), "r"((uint32_t)add)
+        : "memory");
+}
+
+// Arrives on the barrier once every product this thread has issued is complete.
+__device__ __forceinline__ void product_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// d = a b^T over `steps` x 16 elements along both tiles' rows of a (128 rows) and b.
+__device__ __forceinline__ void product_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t form, int steps)
+{
+#pragma unroll 1
+    for (int k = 0; k < steps; ++k) {
+        const uint32_t at = (k >> 2) * kBlockBytes + (k & 3) * 32;
+        product_ss(d, operand_rows(a + at), operand_rows(b + at), form, k != 0);
+    }
+}
+
+// d (+)= a b with a (128 x 128, 16-bit pairs in tensor memory) against the rows of tile b.
+__device__ __forceinline__ void product_across(uint32_t d, uint32_t a, uint32_t b, uint32_t form, bool add)
+{
+#pragma unroll 1
+    for (int k = 0; k < 8; ++k) product_ts(d, a + k * 8, operand_across(b + k * 2048), form, add || k != 0);
+}
+
+// ---- registers ------------------------------------------------------------------------------
+
+// Blocks of 384 threads start with kStartRegisters a thread; the four warps that
+// copy and issue products give most of theirs to the other eight, which hold a
+// row of scores each.
+constexpr int kStartRegisters = 168, kFewRegisters = 56, kManyRegisters = 224;
+static_assert(128 * kFewRegisters + 256 * kManyRegisters <= 384 * kStartRegisters,
+              "the shares must fit what the block starts with");
+
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 56;"); }
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 224;"); }
+
+// ---- arithmetic --------------------------------------------------------------------------
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n.reg .b64 a, b, c, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmov.b64 c, {%6, %7};\n"
+        "fma.rn.f32x2 d, a, b, c;\nmov.b64 {%0, %1}, d;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n.reg .b64 a, b, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nadd.rn.f32x2 d, a, b;\n"
+        "mov.b64 {%0, %1}, d;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n.reg .b64 a, b, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmul.rn.f32x2 d, a, b;\n"
+        "mov.b64 {%0, %1}, d;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// Two values as a 16-bit pair, the first in the low half.
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// ---- host ------------------------------------------------------------------------------------
+
+// Tensor map of a [batch, tokens, heads, dim] array for boxes of 64 elements of
+// `rows` tokens of one head.  A stride of 0 (one array for all items or heads)
+// becomes an extent of 1; the kernels multiply such a coordinate by 0.
+// (A kernel compiled to start with fewer registers than the shares add up to
+// would wait for them forever: refuse to launch it.)
+int check_registers(gsr_ctx *ctx, const void *kernel, const char *name);
+int heads_map(gsr_ctx *ctx, CUtensorMap *map, const gsr_heads &t, int dtype, int64_t batch, int64_t tokens,
+              int64_t heads, int dim, int rows);
+
+}  // namespace gsr
