@@ -1,0 +1,902 @@
+// attention_backward.cu -- cross attention to an encoder's states of another
+// length, backward.
+//
+//   p = exp(s - lse),  dp = do . v,  delta = do . o,  ds = p (dp - delta)
+//   dq = scale sum ds k,   dk = scale sum ds q,   dv = sum p do
+//
+// Two kernels, one whose blocks hold 128 queries and walk the keys (dq) and one
+// whose blocks hold 128 keys and walk the queries of every head of the group (dk
+// and dv).  Each computes s and dp for itself: seven products instead of five,
+// but each gradient is a sum that one accumulator in tensor memory takes in a
+// fixed order, with no atomics and no traffic of partial gradients through L2.
+//
+// In both, two warpgroups take the exponentials and ds, each for half of the
+// columns of S and dP, and one thread issues the products.  S of the next step
+// runs while ds of this one is computed, so the tensor cores stay busy.  16-bit
+// p and ds go back to tensor memory, where the sums' products read them as their
+// first operand: over the columns they came from (keys as rows), or into two
+// buffers in turn (queries as rows).
+//
+// Rounding.  p and ds are rounded to the storage type, as the tensor cores take
+// operands of one type.  f16 has few exponents: p is held times 2^14 (p <= 1),
+// and ds times a power of two that brings the largest |do| to about 1; both
+// powers are divided out of the float sums at the end.
+#include <math.h>
+
+#include "attention.cuh"
+
+namespace gsr {
+namespace {
+
+constexpr int kRowTile = 128;
+constexpr int kBackwardThreads = 384;   // two groups of 128 that compute; four warps of which one copies and one issues
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Powers that keep f16 p and ds in range.
+struct RangeShift {
+    float p;        // p is held times this
+    float ds;       // ds is held times this
+};
+
+struct BackwardArgs {
+    CUtensorMap q, k, v, dout;
+    Schedule work;
+    const float *lse2, *delta;   // [batch, q_heads, q_pad]: lse log2e - log2(shift.p), delta shift.ds / shift.p
+    const RangeShift *shift;
+    void *dq, *dk, *dv;
+    int64_t dq_item, dq_token, dq_head, dk_item, dk_token, dk_head, dv_item, dv_token, dv_head;
+    const int32_t *index;        // original keys of packed ones, [batch, kv_len], or NULL
+    float *partial;              // [2 blocks][128][dim] (dq) or [2 blocks][128][2 dim] (dk, dv)
+    uint32_t *status;
+    int q_len, q_pad, kv_len, q_heads, group, dim;
+    int q_tiles;                 // tiles of 128 queries per head
+    int q_item, q_head, dout_item, dout_head, k_item, k_head, v_item, v_head;
+    float scale, scale_log2;
+};
+
+template <int HD>
+struct BackwardShape {
+    static constexpr int kBlocks = HD / 64;
+    static constexpr int kTileBytes = kBlocks * kBlockBytes;
+    static constexpr int kStages = HD == 128 ? 5 : 8;
+    static constexpr int kStatBytes = kRowTile * 4;   // a query tile's lse2 (with Q) or delta (with dO)
+    static constexpr int kBarriers = 2 + 2 * kStages + 6;
+    static constexpr int kSmemQ = (2 + kStages) * kTileBytes + kBarriers * 8 + 16;
+    static constexpr int kSmemK = kSmemQ + kStages * kStatBytes;
+    static_assert(kSmemK <= 232448, "more shared memory than a block can have");
+    static constexpr int kS = 0, kDp = 128, kOut = 256, kDs = 384;   // tensor memory columns
+    static constexpr int kColumns = 512;
+};
+
+// Barriers of a block, in shared memory.
+template <int HD>
+struct Bars {
+    uint32_t own, own_free, ring, ring_free, s, dp, s_read, ready, done, p_ready;
+    __device__ explicit Bars(uint32_t at)
+    {
+        own = at;
+        own_free = at + 8;
+        ring = at + 16;
+        ring_free = ring + 8 * BackwardShape<HD>::kStages;
+        s = ring_free + 8 * BackwardShape<HD>::kStages;
+        dp = s + 8;
+        s_read = dp + 8;
+        p_ready = s_read;   // queries as rows: scores read; keys as rows: p written
+        ready = s_read + 8;
+        done = ready + 8;
+    }
+    __device__ void init() const
+    {
+        barrier_init(own, 1);
+        barrier_init(own_free, 1);
+        for (int i = 0; i < BackwardShape<HD>::kStages; ++i) {
+            barrier_init(ring + 8 * i, 1);
+            barrier_init(ring_free + 8 * i, 1);
+        }
+        barrier_init(s, 1);
+        barrier_init(dp, 1);
+        barrier_init(s_read, 8);
+        barrier_init(ready, 8);
+        barrier_init(done, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async();
+    }
+};
+
+__device__ __forceinline__ void copy_bytes(uint32_t to, const void *from, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
+                 "l"(from), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// 64 columns of this thread's lane.
+__device__ __forceinline__ void load64(uint32_t (&r)[64], uint32_t at)
+{
+    tmem_load32(*(uint32_t(*)[32])&r[0], at);
+    tmem_load32(*(uint32_t(*)[32])&r[32], at + 32);
+    tmem_wait_load();
+}
+
+__device__ __forceinline__ float2 pair(const uint32_t (&r)[64], int i)
+{
+    return make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+}
+
+// ---- dq: queries as rows -----------------------------------------------------------
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const __grid_constant__ BackwardArgs a)
+{
+    grid_dependency_begin();
+    using S = BackwardShape<HD>;
+    extern __shared__ __align__(1024) unsigned char s_raw[];
+    const uint32_t raw = smem_address(s_raw), base = raw;
+    if (base % 1024 != 0) {   // the swizzle needs it; there is no room to round up
+        *(volatile uint32_t *)a.status = 1;
+        return;
+    }
+    const uint32_t s_own = base, s_ring = base + 2 * S::kTileBytes, at_bars = s_ring + S::kStages * S::kTileBytes;
+    const Bars<HD> bar(at_bars);
+    const uint32_t tail = at_bars + S::kBarriers * 8;
+    uint32_t *s_words = (uint32_t *)(s_raw + (tail - raw));
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const WaitGuard guard = {s_words + 1, a.status};
+    if (threadIdx.x == 0) {
+        s_words[1] = 0;
+        bar.init();
+    }
+    if (warp == 9) tmem_alloc(tail, S::kColumns);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = s_words[0];
+    Walk<QueryLine> walk = walk_share<QueryLine>(a.work);
+    Segment g;
+
+    if (warp >= 8) {
+        give_registers();
+        if (warp == 8 && elect_one()) {
+            uint32_t n = 0, seg = 0;
+            while (walk.next(g)) {
+                if (g.length == 0) continue;
+                const int head = g.tile / a.q_tiles, row0 = (g.tile - head * a.q_tiles) * kRowTile;
+                const int key_head = head / a.group;
+                if (seg > 0) barrier_wait(bar.own_free, (seg - 1) & 1, guard);
+                barrier_expect(bar.own, 2 * S::kTileBytes);
+                for (int c = 0; c < S::kBlocks; ++c) {
+                    copy_box(s_own + c * kBlockBytes, &a.q, bar.own, c * 64, row0, head * a.q_head, g.item * a.q_item);
+                    copy_box(s_own + S::kTileBytes + c * kBlockBytes, &a.dout, bar.own, c * 64, row0,
+                             head * a.dout_head, g.item * a.dout_item);
+                }
+                for (int i = g.begin; i < g.end; ++i)
+                    for (int half = 0; half < 2; ++half, ++n) {
+                        const uint32_t stage = n % S::kStages, round = n / S::kStages;
+                        if (round > 0) barrier_wait(bar.ring_free + 8 * stage, (round - 1) & 1, guard);
+                        const uint32_t full = bar.ring + 8 * stage, to = s_ring + stage * S::kTileBytes;
+                        barrier_expect(full, S::kTileBytes);
+                        for (int c = 0; c < S::kBlocks; ++c)
+                            copy_box(to + c * kBlockBytes, half ? &a.v : &a.k, full, c * 64, i * kKeyTile,
+                                     key_head * (half ? a.v_head : a.k_head), g.item * (half ? a.v_item : a.k_item));
+                    }
+                ++seg;
+            }
+        } else if (warp == 9 && elect_one()) {
+            const uint32_t form_s = product_form<T>(kKeyTile, false);
+            const uint32_t form_o = product_form<T>((a.dim + 15) & ~15, true);
+            const int steps = (a.dim + 15) / 16;
+            auto stage_at = [&](uint32_t x) { return s_ring + x % S::kStages * S::kTileBytes; };
+            auto await = [&](uint32_t x) {
+                barrier_wait(bar.ring + 8 * (x % S::kStages), x / S::kStages & 1, guard);
+                tmem_fence_after();
+            };
+            auto release = [&](uint32_t x) { product_commit(bar.ring_free + 8 * (x % S::kStages)); };
+            uint32_t n = 0, seg = 0, step = 0;
+            while (walk.next(g)) {
+                if (g.length == 0) continue;
+                barrier_wait(bar.own, seg & 1, guard);
+                const uint32_t s_q = s_own, s_do = s_own + S::kTileBytes;
+                auto scores = [&](uint32_t x) {
+                    await(x);
+                    product_rows(tmem + S::kS, s_q, stage_at(x), form_s, steps);
+                    product_commit(bar.s);
+                };
+                auto dp = [&](uint32_t x) {
+                    await(x);
+                    product_rows(tmem + S::kDp, s_do, stage_at(x), form_s, steps);
+                    product_commit(bar.dp);
+                    release(x);
+                };
+                scores(n);
+                dp(n + 1);
+                for (int i = g.begin; i < g.end; ++i, n += 2, ++step) {
+                    const bool more = i + 1 < g.end;
+                    barrier_wait(bar.s_read, step & 1, guard);
+                    tmem_fence_after();
+                    if (more) scores(n + 2);
+                    barrier_wait(bar.ready, step & 1, guard);
+                    tmem_fence_after();
+                    product_across(tmem + S::kOut, tmem + S::kDs + (step & 1) * 64, stage_at(n), form_o, i > g.begin);
+                    release(n);
+                    if (more)
+                        dp(n + 3);
+                    else
+                        product_commit(bar.done);
+                }
+                product_commit(bar.own_free);
+                ++seg;
+            }
+        }
+    } else {
+        take_registers();
+        const int half = warp / 4;                                  // columns 64 half .. of S and dP
+        const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
+        const uint32_t at_s = tmem + lanes + S::kS + half * 64, at_dp = tmem + lanes + S::kDp + half * 64;
+        const int row_in_tile = warp % 4 * 32 + lane;
+        const float c = a.scale_log2;
+        const RangeShift shift = *a.shift;
+        const float f_dp = shift.ds / shift.p, f_out = a.scale / shift.ds;
+        uint32_t n = 0, seg = 0, step = 0;
+        while (walk.next(g)) {
+            const int head = g.tile / a.q_tiles, row0 = (g.tile - head * a.q_tiles) * kRowTile;
+            const int row = row0 + row_in_tile;
+            if (g.length > 0) {
+                const int64_t at = ((int64_t)g.item * a.q_heads + head) * a.q_pad + row;
+                const float2 c2 = make_float2(c, c), f2 = make_float2(f_dp, f_dp);
+                const float lse = -a.lse2[at], delta = -a.delta[at];
+                const float2 lse2 = make_float2(lse, lse), delta2 = make_float2(delta, delta);
+                for (int i = g.begin; i < g.end; ++i, n += 2, ++step) {
+                    uint32_t r[64];
+                    barrier_wait(bar.s, step & 1, guard);
+                    tmem_fence_after();
+                    load64(r, at_s);
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0) barrier_arrive(bar.s_read);
+                    const int valid = g.length - i * kKeyTile;
+                    float2 p[32];
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) {
+                        p[y] = fma2(pair(r, 2 * y), c2, lse2);
+                        p[y].x = exp2_fast(p[y].x);
+                        p[y].y = exp2_fast(p[y].y);
+                    }
+                    barrier_wait(bar.dp, step & 1, guard);
+                    tmem_fence_after();
+                    load64(r, at_dp);
+                    uint32_t packed[32];
+                    if (valid < kKeyTile) {
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) {
+                            const float2 ds = mul2(p[y], fma2(pair(r, 2 * y), f2, delta2));
+                            packed[y] = pack2<T>(half * 64 + 2 * y < valid ? ds.x : 0.0f,
+                                                 half * 64 + 2 * y + 1 < valid ? ds.y : 0.0f);
+                        }
+                        if (half == 0) {
+                            // What lies behind the item's last key must not meet the zero ds as infinities or NaN.
+                            barrier_wait(bar.ring + 8 * (n % S::kStages), n / S::kStages & 1, guard);
+                            if (row_in_tile >= valid) {
+                                unsigned char *k = s_raw + (s_ring - raw) + n % S::kStages * S::kTileBytes +
+                                                   row_in_tile * 128;
+                                for (int b = 0; b < S::kBlocks; ++b)
+                                    for (int e = 0; e < 8; ++e)
+                                        *(uint4 *)(k + b * kBlockBytes + e * 16) = make_uint4(0, 0, 0, 0);
+                            }
+                            fence_async();
+                        }
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) {
+                            const float2 ds = mul2(p[y], fma2(pair(r, 2 * y), f2, delta2));
+                            packed[y] = pack2<T>(ds.x, ds.y);
+                        }
+                    }
+                    __syncwarp();
+                    tmem_store32(tmem + lanes + S::kDs + (step & 1) * 64 + half * 32, packed);
+                    tmem_wait_store();
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0) barrier_arrive(bar.ready);
+                }
+                barrier_wait(bar.done, seg++ & 1, guard);
+                tmem_fence_after();
+            }
+            const bool store = row < a.q_len, whole = g.whole();
+            T *out = (T *)a.dq + g.item * a.dq_item + (int64_t)row * a.dq_token + head * a.dq_head;
+            float *partial = a.partial + ((int64_t)partial_slot(g, blockIdx.x) * kRowTile + row_in_tile) * a.dim;
+            for (int x = half * (HD / 2); x < (half + 1) * (HD / 2); x += 32) {
+                if (x >= a.dim) break;
+                uint32_t o[32];
+                __syncwarp();
+                if (g.length > 0) {
+                    tmem_load32(o, tmem + lanes + S::kOut + x);
+                    tmem_wait_load();
+                } else {
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) o[y] = 0;
+                }
+                if (store) {
+#pragma unroll
+                    for (int y = 0; y < 32; y += 8)
+                        if (x + y < a.dim) {
+                            float f[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(o[y + e]) * f_out;
+                            if (whole) {
+                                *(uint4 *)(out + x + y) = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]),
+                                                                     pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
+                            } else {
+                                *(float4 *)(partial + x + y) = make_float4(f[0], f[1], f[2], f[3]);
+                                *(float4 *)(partial + x + y + 4) = make_float4(f[4], f[5], f[6], f[7]);
+                            }
+                        }
+                }
+            }
+            tmem_fence_before();
+        }
+    }
+    __syncwarp();
+    drain_if_aborted(guard);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    __syncwarp();
+    if (warp == 9) tmem_free(tmem, S::kColumns);
+}
+
+// ---- dk and dv: keys as rows ----------------------------------------------------------
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const __grid_constant__ BackwardArgs a)
+{
+    grid_dependency_begin();
+    using S = BackwardShape<HD>;
+    constexpr int kOutV = S::kOut, kOutK = S::kOut + HD;
+    extern __shared__ __align__(1024) unsigned char s_raw[];
+    const uint32_t raw = smem_address(s_raw), base = raw;
+    if (base % 1024 != 0) {   // the swizzle needs it; there is no room to round up
+        *(volatile uint32_t *)a.status = 1;
+        return;
+    }
+    const uint32_t s_own = base, s_ring = base + 2 * S::kTileBytes, s_stat = s_ring + S::kStages * S::kTileBytes;
+    const uint32_t at_bars = s_stat + S::kStages * S::kStatBytes;
+    const Bars<HD> bar(at_bars);
+    const uint32_t tail = at_bars + S::kBarriers * 8;
+    uint32_t *s_words = (uint32_t *)(s_raw + (tail - raw));
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const WaitGuard guard = {s_words + 1, a.status};
+    if (threadIdx.x == 0) {
+        s_words[1] = 0;
+        bar.init();
+    }
+    if (warp == 9) tmem_alloc(tail, S::kColumns);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = s_words[0];
+    Walk<KeyLine> walk = walk_share<KeyLine>(a.work);
+    Segment g;
+
+    if (warp >= 8) {
+        give_registers();
+        if (warp == 8 && elect_one()) {
+            uint32_t n = 0, seg = 0;
+            while (walk.next(g)) {
+                if (g.tile * kKeyTile >= g.length) continue;
+                if (seg > 0) barrier_wait(bar.own_free, (seg - 1) & 1, guard);
+                barrier_expect(bar.own, 2 * S::kTileBytes);
+                for (int c = 0; c < S::kBlocks; ++c) {
+                    copy_box(s_own + c * kBlockBytes, &a.k, bar.own, c * 64, g.tile * kKeyTile, g.head * a.k_head,
+                             g.item * a.k_item);
+                    copy_box(s_own + S::kTileBytes + c * kBlockBytes, &a.v, bar.own, c * 64, g.tile * kKeyTile,
+                             g.head * a.v_head, g.item * a.v_item);
+                }
+                for (int i = g.begin; i < g.end; ++i) {
+                    const int head = g.head * a.group + i / a.q_tiles, row0 = i % a.q_tiles * kRowTile;
+                    for (int half = 0; half < 2; ++half, ++n) {
+                        const uint32_t stage = n % S::kStages, round = n / S::kStages;
+                        if (round > 0) barrier_wait(bar.ring_free + 8 * stage, (round - 1) & 1, guard);
+                        const uint32_t full = bar.ring + 8 * stage, to = s_ring + stage * S::kTileBytes;
+                        barrier_expect(full, S::kTileBytes + S::kStatBytes);
+                        for (int c = 0; c < S::kBlocks; ++c)
+                            copy_box(to + c * kBlockBytes, half ? &a.dout : &a.q, full, c * 64, row0,
+                                     head * (half ? a.dout_head : a.q_head), g.item * (half ? a.dout_item : a.q_item));
+                        const int64_t at = ((int64_t)g.item * a.q_heads + head) * a.q_pad + row0;
+                        copy_bytes(s_stat + stage * S::kStatBytes, (half ? a.delta : a.lse2) + at, S::kStatBytes,
+                                   full);
+                    }
+                }
+                ++seg;
+            }
+        } else if (warp == 9 && elect_one()) {
+            const uint32_t form_s = product_form<T>(kRowTile, false);
+            const uint32_t form_o = product_form<T>((a.dim + 15) & ~15, true);
+            const int steps = (a.dim + 15) / 16;
+            auto stage_at = [&](uint32_t x) { return s_ring + x % S::kStages * S::kTileBytes; };
+            auto await = [&](uint32_t x) {
+                barrier_wait(bar.ring + 8 * (x % S::kStages), x / S::kStages & 1, guard);
+                tmem_fence_after();
+            };
+            auto release = [&](uint32_t x) { product_commit(bar.ring_free + 8 * (x % S::kStages)); };
+            uint32_t n = 0, seg = 0, step = 0;
+            while (walk.next(g)) {
+                if (g.tile * kKeyTile >= g.length) continue;
+                barrier_wait(bar.own, seg & 1, guard);
+                auto scores = [&](uint32_t x) {
+                    await(x);
+                    product_rows(tmem + S::kS, s_own, stage_at(x), form_s, steps);
+                    product_commit(bar.s);
+                };
+                auto dp = [&](uint32_t x) {
+                    await(x);
+                    product_rows(tmem + S::kDp, s_own + S::kTileBytes, stage_at(x), form_s, steps);
+                    product_commit(bar.dp);
+                };
+                scores(n);
+                dp(n + 1);
+                for (int i = g.begin; i < g.end; ++i, n += 2, ++step) {
+                    const bool more = i + 1 < g.end;
+                    barrier_wait(bar.p_ready, step & 1, guard);
+                    tmem_fence_after();
+                    product_halves(tmem + kOutV, tmem + S::kS, stage_at(n + 1), form_o, i > g.begin);
+                    if (more) scores(n + 2);
+                    barrier_wait(bar.ready, step & 1, guard);
+                    tmem_fence_after();
+                    product_halves(tmem + kOutK, tmem + S::kDp, stage_at(n), form_o, i > g.begin);
+                    release(n);
+                    release(n + 1);
+                    if (more)
+                        dp(n + 3);
+                    else
+                        product_commit(bar.done);
+                }
+                product_commit(bar.own_free);
+                ++seg;
+            }
+        }
+    } else {
+        take_registers();
+        const int half = warp / 4;                                  // columns 64 half .. of S and dP
+        const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
+        const uint32_t at_s = tmem + lanes + S::kS + half * 64, at_dp = tmem + lanes + S::kDp + half * 64;
+        const int row_in_tile = warp % 4 * 32 + lane;
+        const float c = a.scale_log2;
+        const RangeShift shift = *a.shift;
+        const float f_dp = shift.ds / shift.p, f_k = a.scale / shift.ds, f_v = 1.0f / shift.p;
+        const float2 c2 = make_float2(c, c), f2 = make_float2(f_dp, f_dp);
+        uint32_t n = 0, seg = 0, step = 0;
+        while (walk.next(g)) {
+            const int row = g.tile * kKeyTile + row_in_tile;        // key (packed)
+            const bool any = g.tile * kKeyTile < g.length, live = row < g.length;
+            if (any) {
+                const bool tail_tile = g.length - g.tile * kKeyTile < kKeyTile;
+                for (int i = g.begin; i < g.end; ++i, n += 2, ++step) {
+                    const float4 *lse4 = (const float4 *)(s_raw + (s_stat - raw) + n % S::kStages * S::kStatBytes) +
+                                         half * 16;
+                    const float4 *delta4 =
+                        (const float4 *)(s_raw + (s_stat - raw) + (n + 1) % S::kStages * S::kStatBytes) + half * 16;
+                    uint32_t r[64], packed[32];
+                    float2 p[32];
+                    barrier_wait(bar.ring + 8 * (n % S::kStages), n / S::kStages & 1, guard);   // lse2
+                    barrier_wait(bar.s, step & 1, guard);
+                    tmem_fence_after();
+                    load64(r, at_s);
+#pragma unroll
+                    for (int y = 0; y < 32; y += 2) {
+                        const float4 l = lse4[y / 2];
+                        p[y] = fma2(pair(r, 2 * y), c2, make_float2(-l.x, -l.y));
+                        p[y + 1] = fma2(pair(r, 2 * y + 2), c2, make_float2(-l.z, -l.w));
+                    }
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) {
+                        p[y].x = exp2_fast(p[y].x);
+                        p[y].y = exp2_fast(p[y].y);
+                    }
+                    if (tail_tile && !live)
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) p[y] = make_float2(0.0f, 0.0f);
+#pragma unroll
+                    for (int y = 0; y < 32; ++y) packed[y] = pack2<T>(p[y].x, p[y].y);
+                    __syncwarp();
+                    tmem_store32(at_s, packed);
+                    tmem_wait_store();
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0) barrier_arrive(bar.p_ready);
+                    barrier_wait(bar.ring + 8 * ((n + 1) % S::kStages), (n + 1) / S::kStages & 1, guard);   // delta
+                    barrier_wait(bar.dp, step & 1, guard);
+                    tmem_fence_after();
+                    load64(r, at_dp);
+#pragma unroll
+                    for (int y = 0; y < 32; y += 2) {
+                        const float4 d = delta4[y / 2];
+                        const float2 one = mul2(p[y], fma2(pair(r, 2 * y), f2, make_float2(-d.x, -d.y)));
+                        const float2 two = mul2(p[y + 1], fma2(pair(r, 2 * y + 2), f2, make_float2(-d.z, -d.w)));
+                        packed[y] = pack2<T>(one.x, one.y);
+                        packed[y + 1] = pack2<T>(two.x, two.y);
+                    }
+                    if (tail_tile && !live)
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) packed[y] = 0;
+                    __syncwarp();
+                    tmem_store32(at_dp, packed);
+                    tmem_wait_store();
+                    tmem_fence_before();
+                    __syncwarp();
+                    if (lane == 0) barrier_arrive(bar.ready);
+                }
+                barrier_wait(bar.done, seg++ & 1, guard);
+                tmem_fence_after();
+            }
+            // Rows behind the item's keys are zeros; packed ones have no place of their own.
+            const bool store = a.index ? live : row < a.kv_len, whole = g.whole();
+            const int64_t key = a.index && live ? a.index[(int64_t)g.item * a.kv_len + row] : row;
+            T *out_k = (T *)a.dk + g.item * a.dk_item + key * a.dk_token + g.head * a.dk_head;
+            T *out_v = (T *)a.dv + g.item * a.dv_item + key * a.dv_token + g.head * a.dv_head;
+            float *partial = a.partial + ((int64_t)partial_slot(g, blockIdx.x) * kRowTile + row_in_tile) * 2 * a.dim;
+            for (int x = half * (HD / 2); x < (half + 1) * (HD / 2); x += 32) {
+                if (x >= a.dim) break;
+                for (int which = 0; which < 2; ++which) {
+                    uint32_t o[32];
+                    __syncwarp();
+                    if (any) {
+                        tmem_load32(o, tmem + lanes + (which ? kOutV : kOutK) + x);
+                        tmem_wait_load();
+                    } else {
+#pragma unroll
+                        for (int y = 0; y < 32; ++y) o[y] = 0;
+                    }
+                    if (store) {
+                        const float factor = which ? f_v : f_k;
+                        T *out = which ? out_v : out_k;
+#pragma unroll
+                        for (int y = 0; y < 32; y += 8)
+                            if (x + y < a.dim) {
+                                float f[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    f[e] = live ? __uint_as_float(o[y + e]) * factor : 0.0f;
+                                if (whole) {
+                                    *(uint4 *)(out + x + y) = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]),
+                                                                         pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
+                                } else {
+                                    float *to = partial + which * a.dim + x + y;
+                                    *(float4 *)to = make_float4(f[0], f[1], f[2], f[3]);
+                                    *(float4 *)(to + 4) = make_float4(f[4], f[5], f[6], f[7]);
+                                }
+                            }
+                    }
+                }
+            }
+            tmem_fence_before();
+        }
+    }
+    __syncwarp();
+    drain_if_aborted(guard);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    __syncwarp();
+    if (warp == 9) tmem_free(tmem, S::kColumns);
+}
+
+// ---- sums of cut tiles' parts -----------------------------------------------------------
+
+constexpr int kSumBlock = 256;
+constexpr int kSumRows = 16;
+
+template <typename T>
+__device__ __forceinline__ void sum_row(const float *partial, int64_t slot_stride, int first, int last, T *out)
+{
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int b = first - 1; b <= last; ++b) {
+        const float4 f = *(const float4 *)(partial + (2 * b + (b == first - 1 ? 1 : 0)) * slot_stride);
+        o.x += f.x;
+        o.y += f.y;
+        o.z += f.z;
+        o.w += f.w;
+    }
+    *(uint2 *)out = make_uint2(pack2<T>(o.x, o.y), pack2<T>(o.z, o.w));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kSumBlock) k_attention_sum_q(const __grid_constant__ BackwardArgs a, int grid)
+{
+    grid_dependency_begin();
+    Segment g;
+    const int first = blockIdx.x + 1;
+    int last;
+    if (!cut_tile<QueryLine>(a.work, grid, first, g, last)) return;
+    const int head = g.tile / a.q_tiles, row0 = (g.tile - head * a.q_tiles) * kRowTile;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (lane * 4 >= a.dim) return;
+    for (int r = blockIdx.y * kSumRows + warp; r < (int)(blockIdx.y + 1) * kSumRows; r += kSumBlock / 32) {
+        const int64_t row = row0 + r;
+        if (row >= a.q_len) return;
+        sum_row(a.partial + (int64_t)r * a.dim + lane * 4, (int64_t)kRowTile * a.dim, first, last,
+                (T *)a.dq + g.item * a.dq_item + row * a.dq_token + head * a.dq_head + lane * 4);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kSumBlock) k_attention_sum_kv(const __grid_constant__ BackwardArgs a, int grid)
+{
+    grid_dependency_begin();
+    Segment g;
+    const int first = blockIdx.x + 1;
+    int last;
+    if (!cut_tile<KeyLine>(a.work, grid, first, g, last)) return;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (lane * 4 >= a.dim) return;
+    for (int r = blockIdx.y * kSumRows + warp; r < (int)(blockIdx.y + 1) * kSumRows; r += kSumBlock / 32) {
+        const int row = g.tile * kKeyTile + r;
+        if (a.index ? row >= g.length : row >= a.kv_len) return;
+        const int64_t key = a.index ? a.index[(int64_t)g.item * a.kv_len + row] : row;
+        const float *part = a.partial + (int64_t)r * 2 * a.dim + lane * 4;
+        const int64_t stride = (int64_t)kRowTile * 2 * a.dim;
+        sum_row(part, stride, first, last,
+                (T *)a.dk + g.item * a.dk_item + key * a.dk_token + g.head * a.dk_head + lane * 4);
+        sum_row(part + a.dim, stride, first, last,
+                (T *)a.dv + g.item * a.dv_item + key * a.dv_token + g.head * a.dv_head + lane * 4);
+    }
+}
+
+// ---- statistics of the rows ----------------------------------------------------------------
+
+struct RowArgs {
+    gsr_heads out, dout;
+    const float *lse;
+    float *lse2, *delta;
+    RangeShift *shift;
+    uint32_t *amax;          // bits of the largest |do| (f16)
+    int64_t rows;            // batch x q_pad x q_heads
+    int q_len, q_pad, q_heads, dim;
+};
+
+constexpr int kRowLanes = 16;   // lanes of a row, 8 elements each
+
+template <typename T>
+__global__ void __launch_bounds__(256) k_attention_largest(const RowArgs a)
+{
+    grid_dependency_begin();
+    __shared__ uint32_t s_max;
+    if (threadIdx.x == 0) s_max = 0;
+    __syncthreads();
+    const int c = threadIdx.x % kRowLanes * 8;
+    uint32_t top = 0;
+    for (int64_t r = (int64_t)blockIdx.x * (256 / kRowLanes) + threadIdx.x / kRowLanes; r < a.rows;
+         r += (int64_t)gridDim.x * (256 / kRowLanes)) {
+        const int64_t h = r % a.q_heads, i = r / a.q_heads % a.q_pad, b = r / a.q_heads / a.q_pad;
+        if (i >= a.q_len || c >= a.dim) continue;
+        const Vec<T, 8> v = *(const Vec<T, 8> *)((const T *)a.dout.data + b * a.dout.batch_stride +
+                                                  i * a.dout.token_stride + h * a.dout.head_stride + c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(fabsf(to_float(v.e[e]))));
+    }
+    top = __reduce_max_sync(~0u, top);
+    if (threadIdx.x % 32 == 0) atomicMax(&s_max, top);
+    __syncthreads();
+    // The largest of all is the same in any order.
+    if (threadIdx.x == 0) atomicMax(a.amax, s_max);
+}
+
+// lse in base 2 and delta, with the shifts of p and ds folded in; rows behind
+// q_len, and rows without keys, get p = 0.
+template <typename T>
+__global__ void __launch_bounds__(256) k_attention_rows(const RowArgs a)
+{
+    grid_dependency_begin();
+    RangeShift shift = {1.0f, 1.0f};
+    if (a.amax) {
+        const float top = __uint_as_float(*a.amax);
+        shift.p = 16384.0f;
+        if (top > 0.0f && top < INFINITY) shift.ds = exp2f((float)-ilogbf(top));
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.shift = shift;
+    const int64_t r = (int64_t)blockIdx.x * (256 / kRowLanes) + threadIdx.x / kRowLanes;
+    const int c = threadIdx.x % kRowLanes * 8;
+    float sum = 0.0f;
+    const int64_t h = r % a.q_heads, i = r / a.q_heads % a.q_pad, b = r / a.q_heads / a.q_pad;
+    if (r < a.rows && i < a.q_len && c < a.dim) {
+        const Vec<T, 8> o = *(const Vec<T, 8> *)((const T *)a.out.data + b * a.out.batch_stride +
+                                                  i * a.out.token_stride + h * a.out.head_stride + c);
+        const Vec<T, 8> d = *(const Vec<T, 8> *)((const T *)a.dout.data + b * a.dout.batch_stride +
+                                                  i * a.dout.token_stride + h * a.dout.head_stride + c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum = fmaf(to_float(o.e[e]), to_float(d.e[e]), sum);
+    }
+    for (int d = kRowLanes / 2; d > 0; d /= 2) sum += __shfl_xor_sync(~0u, sum, d);
+    if (r < a.rows && c == 0) {
+        const int64_t at = (b * a.q_heads + h) * a.q_pad + i;
+        float lse = INFINITY;
+        if (i < a.q_len) {
+            lse = a.lse[(b * a.q_heads + h) * a.q_len + i];
+            lse = lse == -INFINITY ? INFINITY : lse * kLog2e - log2f(shift.p);
+        }
+        a.lse2[at] = lse;
+        a.delta[at] = sum * (shift.ds / shift.p);
+    }
+}
+
+// Zeros: rows of an array, all of them or those of masked keys.
+template <typename T>
+__global__ void __launch_bounds__(256) k_attention_zero_rows(gsr_heads t, int64_t rows, int tokens, int heads, int dim,
+                                                             const uint8_t *mask, const int32_t *lengths)
+{
+    grid_dependency_begin();
+    const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (r >= rows) return;
+    const int64_t h = r % heads, i = r / heads % tokens, b = r / heads / tokens;
+    if (mask && i < item_length(lengths, tokens, (int)b) && mask[b * tokens + i] != 0) return;
+    T *o = (T *)t.data + b * t.batch_stride + i * t.token_stride + h * t.head_stride;
+    for (int c = 0; c < dim; c += 8) *(uint4 *)(o + c) = make_uint4(0, 0, 0, 0);
+}
+
+template <typename T>
+int zero_rows(gsr_ctx *ctx, const gsr_heads &t, const gsr_attention &d, int tokens, int heads, bool masked,
+              cudaStream_t stream)
+{
+    const int64_t rows = (int64_t)d.batch * tokens * heads;
+    if (rows == 0) return GSR_OK;
+    return cuda_check(ctx, launch_kernel(ctx, k_attention_zero_rows<T>, dim3((unsigned)((rows + 255) / 256)), 256, stream,
+                                         t, rows, tokens, heads, (int)d.head_dim, masked ? d.key_mask : nullptr,
+                                         masked ? d.kv_lengths : nullptr),
+                      "k_attention_zero_rows");
+}
+
+template <typename Kernel>
+int launch_big(gsr_ctx *ctx, Kernel *kernel, const char *name, int blocks, int smem, const BackwardArgs &a,
+               cudaStream_t stream)
+{
+    if (int rc = cuda_check(ctx, cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem), name))
+        return rc;
+    if (int rc = check_registers(ctx, (const void *)kernel, name)) return rc;
+    return cuda_check(ctx, launch_kernel_smem(ctx, kernel, dim3((unsigned)blocks), kBackwardThreads, smem, stream, a),
+                      name);
+}
+
+template <typename T, int HD>
+int launch_backward(gsr_ctx *ctx, BackwardArgs &a, const Schedule &by_query, const Schedule &by_key, int blocks_q,
+                    int blocks_k, cudaStream_t stream)
+{
+    const dim3 rows(1, kRowTile / kSumRows);
+    a.work = by_key;
+    if (int rc = launch_big(ctx, k_attention_grad_kv<T, HD>, "k_attention_grad_kv", blocks_k,
+                            BackwardShape<HD>::kSmemK, a, stream))
+        return rc;
+    if (blocks_k > 1)
+        if (int rc = cuda_check(ctx, launch_kernel(ctx, k_attention_sum_kv<T>, dim3((unsigned)blocks_k - 1, rows.y),
+                                                   kSumBlock, stream, a, blocks_k),
+                                "k_attention_sum_kv"))
+            return rc;
+    a.work = by_query;
+    if (int rc = launch_big(ctx, k_attention_grad_q<T, HD>, "k_attention_grad_q", blocks_q, BackwardShape<HD>::kSmemQ, a,
+                            stream))
+        return rc;
+    if (blocks_q == 1) return GSR_OK;
+    return cuda_check(ctx, launch_kernel(ctx, k_attention_sum_q<T>, dim3((unsigned)blocks_q - 1, rows.y), kSumBlock,
+                                         stream, a, blocks_q),
+                      "k_attention_sum_q");
+}
+
+template <typename T>
+int backward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr_heads &k, const gsr_heads &v,
+             const gsr_heads &out, const float *lse, const gsr_heads &dout, const gsr_heads &dq, const gsr_heads &dk,
+             const gsr_heads &dv, cudaStream_t stream)
+{
+    if (d.kv_len == 0) return zero_rows<T>(ctx, dq, d, d.q_len, d.q_heads, false, stream);
+    if (d.q_len == 0) {
+        if (int rc = zero_rows<T>(ctx, dk, d, d.kv_len, d.kv_heads, false, stream)) return rc;
+        return zero_rows<T>(ctx, dv, d, d.kv_len, d.kv_heads, false, stream);
+    }
+    BackwardArgs a = {};
+    a.q_len = d.q_len;
+    a.kv_len = d.kv_len;
+    a.q_heads = d.q_heads;
+    a.group = d.q_heads / d.kv_heads;
+    a.dim = d.head_dim;
+    a.q_tiles = (d.q_len + kRowTile - 1) / kRowTile;
+    a.q_pad = a.q_tiles * kRowTile;
+    a.scale = d.scale;
+    a.scale_log2 = d.scale * kLog2e;
+    a.dq = dq.data;
+    a.dq_item = dq.batch_stride;
+    a.dq_token = dq.token_stride;
+    a.dq_head = dq.head_stride;
+    a.dk = dk.data;
+    a.dk_item = dk.batch_stride;
+    a.dk_token = dk.token_stride;
+    a.dk_head = dk.head_stride;
+    a.dv = dv.data;
+    a.dv_item = dv.batch_stride;
+    a.dv_token = dv.token_stride;
+    a.dv_head = dv.head_stride;
+    const int key_tiles = (d.kv_len + kKeyTile - 1) / kKeyTile;
+    Schedule by_query = {d.batch, d.q_heads * a.q_tiles, 0, 0, d.kv_lengths, d.kv_len};
+    Schedule by_key = {d.batch, key_tiles, d.kv_heads, a.group * a.q_tiles, d.kv_lengths, d.kv_len};
+    const int64_t line = (int64_t)d.batch * d.q_heads * a.q_tiles * key_tiles;   // both ways
+    const int blocks = (int)(line < ctx->num_sms ? line : ctx->num_sms);
+
+    const int64_t rows = (int64_t)d.batch * d.q_heads * a.q_pad;
+    const size_t packed = d.key_mask ? round_up(packed_bytes(d), 256) : 0;
+    const size_t stats = round_up((size_t)rows * sizeof(float), 512);
+    const size_t partial = round_up((size_t)2 * blocks * kRowTile * 2 * d.head_dim * sizeof(float), 256);
+    void *work;
+    if (int rc = workspace(ctx, packed + 2 * stats + partial + 256, stream, &work)) return rc;
+    unsigned char *p = (unsigned char *)work + packed;
+    float *lse2 = (float *)p, *delta = (float *)(p + stats);
+    a.partial = (float *)(p + 2 * stats);
+    RangeShift *shift = (RangeShift *)(p + 2 * stats + partial);
+    a.lse2 = lse2;
+    a.delta = delta;
+    a.shift = shift;
+    a.status = ctx->status_dev;
+
+    RowArgs r = {};
+    r.out = out;
+    r.dout = dout;
+    r.lse = lse;
+    r.lse2 = lse2;
+    r.delta = delta;
+    r.shift = shift;
+    r.rows = rows;
+    r.q_len = d.q_len;
+    r.q_pad = a.q_pad;
+    r.q_heads = d.q_heads;
+    r.dim = d.head_dim;
+    const int64_t row_blocks = (rows + 256 / kRowLanes - 1) / (256 / kRowLanes);
+    if (d.dtype == GSR_F16) {
+        r.amax = (uint32_t *)(shift + 1);
+        if (int rc = cuda_check(ctx, cudaMemsetAsync(r.amax, 0, sizeof(uint32_t), stream), "k_attention_largest"))
+            return rc;
+        const int64_t most = 8 * (int64_t)ctx->num_sms;
+        if (int rc = cuda_check(ctx, launch_kernel(ctx, k_attention_largest<T>,
+                                                   dim3((unsigned)(row_blocks < most ? row_blocks : most)), 256, stream, r),
+                                "k_attention_largest"))
+            return rc;
+    }
+    if (int rc = cuda_check(ctx, launch_kernel(ctx, k_attention_rows<T>, dim3((unsigned)row_blocks), 256, stream, r),
+                            "k_attention_rows"))
+        return rc;
+
+    gsr_heads keys = k, values = v;
+    if (d.key_mask) {
+        Packed pack;
+        if (int rc = cuda_check(ctx, pack_keys(ctx, d, k, v, work, &pack, stream), "k_pack_keys")) return rc;
+        keys = pack.k;
+        values = pack.v;
+        by_query.lengths = by_key.lengths = pack.counts;
+        a.index = pack.index;
+        if (int rc = zero_rows<T>(ctx, dk, d, d.kv_len, d.kv_heads, true, stream)) return rc;
+        if (int rc = zero_rows<T>(ctx, dv, d, d.kv_len, d.kv_heads, true, stream)) return rc;
+    }
+    a.q_item = q.batch_stride != 0;
+    a.q_head = q.head_stride != 0;
+    a.dout_item = dout.batch_stride != 0;
+    a.dout_head = dout.head_stride != 0;
+    a.k_item = keys.batch_stride != 0;
+    a.k_head = keys.head_stride != 0;
+    a.v_item = values.batch_stride != 0;
+    a.v_head = values.head_stride != 0;
+    if (int rc = heads_map(ctx, &a.q, q, d.dtype, d.batch, d.q_len, d.q_heads, d.head_dim, kRowTile)) return rc;
+    if (int rc = heads_map(ctx, &a.dout, dout, d.dtype, d.batch, d.q_len, d.q_heads, d.head_dim, kRowTile)) return rc;
+    if (int rc = heads_map(ctx, &a.k, keys, d.dtype, d.batch, d.kv_len, d.kv_heads, d.head_dim, kKeyTile)) return rc;
+    if (int rc = heads_map(ctx, &a.v, values, d.dtype, d.batch, d.kv_len, d.kv_heads, d.head_dim, kKeyTile)) return rc;
+    const int rc = d.head_dim <= 64 ? launch_backward<T, 64>(ctx, a, by_query, by_key, blocks, blocks, stream)
+                                    : launch_backward<T, 128>(ctx, a, by_query, by_key, blocks, blocks, stream);
+    if (rc) return rc;
+    return workspace_done(ctx, stream);
+}
+
+}  // namespace
+
+int cross_attention_backward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr_heads &k,
+                             const gsr_heads &v, const gsr_heads &out, const float *lse, const gsr_heads &dout,
+                             const gsr_heads &dq, const gsr_heads &dk, const gsr_heads &dv, cudaStream_t stream)
+{
+    if (int rc = check_status(ctx)) return rc;
+    return d.dtype == GSR_BF16 ? backward<__nv_bfloat16>(ctx, d, q, k, v, out, lse, dout, dq, dk, dv, stream)
+                               : backward<__half>(ctx, d, q, k, v, out, lse, dout, dq, dk, dv, stream);
+}
+
+}  // namespace gsr

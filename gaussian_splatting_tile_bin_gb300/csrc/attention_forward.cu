@@ -89,10 +89,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
     tmem_fence_after();
     const uint32_t tmem = s_words[0];
 
-    const int64_t line = QueryWalk::line(a.work);
-    const int blocks = busy_blocks(line, gridDim.x), block = min((int)blockIdx.x, blocks);
-    QueryWalk walk(a.work, share_begin(line, block, blocks),
-                   block < blocks ? share_begin(line, block + 1, blocks) : line);
+    Walk<QueryLine> walk = walk_share<QueryLine>(a.work);
     Segment g;
     const int row_tiles = a.row_tiles;   // of 256 rows, per head
 
@@ -335,19 +332,12 @@ template <typename T>
 __global__ void __launch_bounds__(kJoinBlock) k_attention_join(const __grid_constant__ ForwardArgs a, int grid)
 {
     grid_dependency_begin();
-    const int64_t line = QueryWalk::line(a.work);
-    const int blocks = busy_blocks(line, grid), first = blockIdx.x + 1;
-    if (first >= blocks) return;
-    const int64_t cut = share_begin(line, first, blocks);
-    QueryWalk walk(a.work, cut, line);
     Segment g;
-    walk.next(g);
-    const int64_t start = cut - g.begin, stop = start + g.total;
-    if (g.begin == 0 || share_begin(line, first - 1, blocks) > start) return;
+    const int first = blockIdx.x + 1;
+    int last;
+    if (!cut_tile<QueryLine>(a.work, grid, first, g, last)) return;
     const int head = g.tile / a.row_tiles, row0 = (g.tile - head * a.row_tiles) * 2 * kRowTile;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    int last = first;   // blocks first - 1 .. last hold parts
-    while (last + 1 < blocks && share_begin(line, last + 1, blocks) < stop) ++last;
     for (int r = blockIdx.y * kJoinRows + warp; r < (int)(blockIdx.y + 1) * kJoinRows; r += kJoinBlock / 32) {
         const int row = row0 + r;
         if (row >= a.q_len) return;
@@ -358,7 +348,7 @@ __global__ void __launch_bounds__(kJoinBlock) k_attention_join(const __grid_cons
         const float shift = top == -INFINITY ? 0.0f : top;
         float total = 0.0f;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int b = first - 1; b <= last; ++b) {
+        for (int b = first - 1; b <= last; ++b) {   // blocks first - 1 .. last hold parts
             const float w = expf(a.partial_lse[slot(b)] - shift);
             total += w;
             if (lane * 4 < a.dim) {
@@ -436,7 +426,7 @@ int forward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr_
     a.out_token = out.token_stride;
     a.out_head = out.head_stride;
     a.lse = lse;
-    a.work = {d.batch, d.q_heads * a.row_tiles, 1, d.kv_lengths, d.kv_len};
+    a.work = {d.batch, d.q_heads * a.row_tiles, 0, 0, d.kv_lengths, d.kv_len};
     const int64_t line = (int64_t)d.batch * a.work.tiles * ((d.kv_len + kKeyTile - 1) / kKeyTile);
     const int blocks = (int)(line < ctx->num_sms ? line : ctx->num_sms);
     const size_t rows = (size_t)2 * blocks * 2 * kRowTile;

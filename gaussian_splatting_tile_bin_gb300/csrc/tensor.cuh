@@ -242,6 +242,14 @@ __device__ __forceinline__ void product_across(uint32_t d, uint32_t a, uint32_t 
     for (int k = 0; k < 8; ++k) product_ts(d, a + k * 8, operand_across(b + k * 2048), form, add || k != 0);
 }
 
+// The same with a's two halves of 64 terms at columns 0 and 64.
+__device__ __forceinline__ void product_halves(uint32_t d, uint32_t a, uint32_t b, uint32_t form, bool add)
+{
+#pragma unroll 1
+    for (int k = 0; k < 8; ++k)
+        product_ts(d, a + (k & 3) * 8 + (k >> 2) * 64, operand_across(b + k * 2048), form, add || k != 0);
+}
+
 // ---- registers ------------------------------------------------------------------------------
 
 // Blocks of 384 threads start with kStartRegisters a thread; the four warps that
