@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    const uint32_t tmem = s_words[0];
+    const uint32_t tmem = __shfl_sync(~0u, s_words[0], 0);
     Walk<QueryLine> walk = walk_share<QueryLine>(a.work);
     Segment g;
 
@@ -181,7 +181,8 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                     }
                 ++seg;
             }
-        } else if (warp == 9 && elect_one()) {
+        } else if (warp == 9) {
+            const bool leader = elect_one();
             const uint32_t form_s = product_form<T>(kKeyTile, false);
             const uint32_t form_o = product_form<T>((a.dim + 15) & ~15, true);
             const int steps = (a.dim + 15) / 16;
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                 barrier_wait(bar.ring + 8 * (x % S::kStages), x / S::kStages & 1, guard);
                 tmem_fence_after();
             };
-            auto release = [&](uint32_t x) { product_commit(bar.ring_free + 8 * (x % S::kStages)); };
+            auto release = [&](uint32_t x) { product_commit(leader, bar.ring_free + 8 * (x % S::kStages)); };
             uint32_t n = 0, seg = 0, step = 0;
             while (walk.next(g)) {
                 if (g.length == 0) continue;
@@ -198,13 +199,13 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                 const uint32_t s_q = s_own, s_do = s_own + S::kTileBytes;
                 auto scores = [&](uint32_t x) {
                     await(x);
-                    product_rows(tmem + S::kS, s_q, stage_at(x), form_s, steps);
-                    product_commit(bar.s);
+                    product_rows<HD>(leader, tmem + S::kS, s_q, stage_at(x), form_s, steps);
+                    product_commit(leader, bar.s);
                 };
                 auto dp = [&](uint32_t x) {
                     await(x);
-                    product_rows(tmem + S::kDp, s_do, stage_at(x), form_s, steps);
-                    product_commit(bar.dp);
+                    product_rows<HD>(leader, tmem + S::kDp, s_do, stage_at(x), form_s, steps);
+                    product_commit(leader, bar.dp);
                     release(x);
                 };
                 scores(n);
@@ -216,14 +217,14 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                     if (more) scores(n + 2);
                     barrier_wait(bar.ready, step & 1, guard);
                     tmem_fence_after();
-                    product_across(tmem + S::kOut, tmem + S::kDs + (step & 1) * 64, stage_at(n), form_o, i > g.begin);
+                    product_across<0, 8>(leader, tmem + S::kOut, tmem + S::kDs + (step & 1) * 64, stage_at(n), form_o, i > g.begin);
                     release(n);
                     if (more)
                         dp(n + 3);
                     else
-                        product_commit(bar.done);
+                        product_commit(leader, bar.done);
                 }
-                product_commit(bar.own_free);
+                product_commit(leader, bar.own_free);
                 ++seg;
             }
         }
@@ -373,7 +374,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    const uint32_t tmem = s_words[0];
+    const uint32_t tmem = __shfl_sync(~0u, s_words[0], 0);
     Walk<KeyLine> walk = walk_share<KeyLine>(a.work);
     Segment g;
 
@@ -408,7 +409,8 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
                 }
                 ++seg;
             }
-        } else if (warp == 9 && elect_one()) {
+        } else if (warp == 9) {
+            const bool leader = elect_one();
             const uint32_t form_s = product_form<T>(kRowTile, false);
             const uint32_t form_o = product_form<T>((a.dim + 15) & ~15, true);
             const int steps = (a.dim + 15) / 16;
@@ -417,20 +419,20 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
                 barrier_wait(bar.ring + 8 * (x % S::kStages), x / S::kStages & 1, guard);
                 tmem_fence_after();
             };
-            auto release = [&](uint32_t x) { product_commit(bar.ring_free + 8 * (x % S::kStages)); };
+            auto release = [&](uint32_t x) { product_commit(leader, bar.ring_free + 8 * (x % S::kStages)); };
             uint32_t n = 0, seg = 0, step = 0;
             while (walk.next(g)) {
                 if (g.tile * kKeyTile >= g.length) continue;
                 barrier_wait(bar.own, seg & 1, guard);
                 auto scores = [&](uint32_t x) {
                     await(x);
-                    product_rows(tmem + S::kS, s_own, stage_at(x), form_s, steps);
-                    product_commit(bar.s);
+                    product_rows<HD>(leader, tmem + S::kS, s_own, stage_at(x), form_s, steps);
+                    product_commit(leader, bar.s);
                 };
                 auto dp = [&](uint32_t x) {
                     await(x);
-                    product_rows(tmem + S::kDp, s_own + S::kTileBytes, stage_at(x), form_s, steps);
-                    product_commit(bar.dp);
+                    product_rows<HD>(leader, tmem + S::kDp, s_own + S::kTileBytes, stage_at(x), form_s, steps);
+                    product_commit(leader, bar.dp);
                 };
                 scores(n);
                 dp(n + 1);
@@ -438,19 +440,19 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
                     const bool more = i + 1 < g.end;
                     barrier_wait(bar.p_ready, step & 1, guard);
                     tmem_fence_after();
-                    product_halves(tmem + kOutV, tmem + S::kS, stage_at(n + 1), form_o, i > g.begin);
+                    product_across<0, 8>(leader, tmem + kOutV, tmem + S::kS, stage_at(n + 1), form_o, i > g.begin, 64);
                     if (more) scores(n + 2);
                     barrier_wait(bar.ready, step & 1, guard);
                     tmem_fence_after();
-                    product_halves(tmem + kOutK, tmem + S::kDp, stage_at(n), form_o, i > g.begin);
+                    product_across<0, 8>(leader, tmem + kOutK, tmem + S::kDp, stage_at(n), form_o, i > g.begin, 64);
                     release(n);
                     release(n + 1);
                     if (more)
                         dp(n + 3);
                     else
-                        product_commit(bar.done);
+                        product_commit(leader, bar.done);
                 }
-                product_commit(bar.own_free);
+                product_commit(leader, bar.own_free);
                 ++seg;
             }
         }

@@ -46,7 +46,7 @@ struct ForwardShape {
     static constexpr int kBlocks = HD / 64;
     static constexpr int kTileBytes = kBlocks * kBlockBytes;
     static constexpr int kStages = HD == 128 ? 5 : 8;
-    static constexpr int kBarriers = 2 + 2 * kStages + 6;
+    static constexpr int kBarriers = 2 + 2 * kStages + 8;
     static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + kBarriers * 8 + 16;
     static constexpr int kOut = 256;   // tensor memory column of the outputs
     static constexpr int kColumns = 512;
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
     const uint32_t base = (raw + 1023) & ~1023u;
     const uint32_t s_q = base, s_kv = base + 2 * S::kTileBytes, bars = s_kv + S::kStages * S::kTileBytes;
     const uint32_t b_q = bars, b_q_free = bars + 8, b_kv = bars + 16, b_kv_free = b_kv + 8 * S::kStages;
-    const uint32_t b_s = b_kv_free + 8 * S::kStages, b_p = b_s + 16, b_o = b_p + 16, tail = b_o + 16;
+    const uint32_t b_s = b_kv_free + 8 * S::kStages, b_p = b_s + 16, b_p2 = b_p + 16, b_o = b_p2 + 16, tail = b_o + 16;
     uint32_t *s_words = (uint32_t *)(s_raw + (tail - raw));   // tensor memory base, abort flag
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const WaitGuard guard = {s_words + 1, a.status};
@@ -78,6 +78,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
         for (int i = 0; i < 2; ++i) {
             barrier_init(b_s + 8 * i, 1);
             barrier_init(b_p + 8 * i, 4);
+            barrier_init(b_p2 + 8 * i, 4);
             barrier_init(b_o + 8 * i, 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -87,7 +88,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    const uint32_t tmem = s_words[0];
+    const uint32_t tmem = __shfl_sync(~0u, s_words[0], 0);
 
     Walk<QueryLine> walk = walk_share<QueryLine>(a.work);
     Segment g;
@@ -128,7 +129,8 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
         }
     } else if (warp == 9) {
         // ---- products ----
-        if (elect_one()) {
+        {
+            const bool leader = elect_one();
             const uint32_t form_s = product_form<T>(kKeyTile, false);
             const uint32_t form_o = product_form<T>((a.dim + 15) & ~15, true);
             const int steps = (a.dim + 15) / 16;
@@ -142,12 +144,12 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
                 auto await = [&](uint32_t n) {
                     barrier_wait(b_kv + 8 * (n % S::kStages), n / S::kStages & 1, guard);
                 };
-                auto release = [&](uint32_t n) { product_commit(b_kv_free + 8 * (n % S::kStages)); };
+                auto release = [&](uint32_t n) { product_commit(leader, b_kv_free + 8 * (n % S::kStages)); };
                 await(kv);
                 tmem_fence_after();
                 for (int t = 0; t < tiles; ++t) {
-                    product_rows(tmem + t * kKeyTile, s_q + t * S::kTileBytes, stage_at(kv), form_s, steps);
-                    product_commit(b_s + 8 * t);
+                    product_rows<HD>(leader, tmem + t * kKeyTile, s_q + t * S::kTileBytes, stage_at(kv), form_s, steps);
+                    product_commit(leader, b_s + 8 * t);
                 }
                 release(kv);
                 for (int i = g.begin; i < g.end; ++i, kv += 2) {
@@ -155,22 +157,25 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
                     await(kv + 1);
                     if (more) await(kv + 2);
                     for (int t = 0; t < tiles; ++t) {
-                        barrier_wait(b_p + 8 * t, p[t]++ & 1, guard);
+                        const uint32_t o = tmem + S::kOut + t * HD, p_at = tmem + t * kKeyTile;
+                        barrier_wait(b_p + 8 * t, p[t] & 1, guard);
                         tmem_fence_after();
-                        product_across(tmem + S::kOut + t * HD, tmem + t * kKeyTile, stage_at(kv + 1), form_o,
-                                       i > g.begin);
+                        product_across<0, 4>(leader, o, p_at, stage_at(kv + 1), form_o, i > g.begin);
+                        barrier_wait(b_p2 + 8 * t, p[t]++ & 1, guard);
+                        tmem_fence_after();
+                        product_across<4, 8>(leader, o, p_at, stage_at(kv + 1), form_o, true);
                         if (more) {
-                            product_rows(tmem + t * kKeyTile, s_q + t * S::kTileBytes, stage_at(kv + 2), form_s,
+                            product_rows<HD>(leader, tmem + t * kKeyTile, s_q + t * S::kTileBytes, stage_at(kv + 2), form_s,
                                          steps);
-                            product_commit(b_s + 8 * t);
+                            product_commit(leader, b_s + 8 * t);
                         } else {
-                            product_commit(b_o + 8 * t);
+                            product_commit(leader, b_o + 8 * t);
                         }
                     }
                     release(kv + 1);
                     if (more) release(kv + 2);
                 }
-                product_commit(b_q_free);
+                product_commit(leader, b_q_free);
                 ++seg;
             }
         }
@@ -220,12 +225,19 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
                             fence_async();
                         }
                     }
-                    float top = -INFINITY;
+                    // Eight chains: a row's maximum is on the path between two products.
+                    float part[8];
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
+                    for (int x = 0; x < 8; ++x) part[x] = __uint_as_float(r[x / 2][x % 2]);
 #pragma unroll
-                        for (int y = 0; y < 32; y += 2)
-                            top = fmaxf(top, fmaxf(__uint_as_float(r[x][y]), __uint_as_float(r[x][y + 1])));
+                    for (int y = 2; y < 32; y += 2)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            part[2 * x] = fmaxf(part[2 * x], __uint_as_float(r[x][y]));
+                            part[2 * x + 1] = fmaxf(part[2 * x + 1], __uint_as_float(r[x][y + 1]));
+                        }
+                    const float top = fmaxf(fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])),
+                                            fmaxf(fmaxf(part[4], part[5]), fmaxf(part[6], part[7])));
                     if (i == g.begin) {
                         m = top;
                     } else if (__any_sync(~0u, top * c > m * c + 8.0f)) {
@@ -257,12 +269,18 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
                             sum[y / 2 & 1] = add2(sum[y / 2 & 1], e);
                             packed[y / 2] = pack2<T>(e.x, e.y);
                         }
+                        if (x == 2) {   // the first 64 keys' stores have had the time of 32 exponentials
+                            tmem_wait_store();
+                            tmem_fence_before();
+                            __syncwarp();
+                            if (lane == 0) barrier_arrive(b_p + 8 * t);
+                        }
                         tmem_store16(at_s + x * 16, packed);
                     }
                     tmem_wait_store();
                     tmem_fence_before();
                     __syncwarp();
-                    if (lane == 0) barrier_arrive(b_p + 8 * t);
+                    if (lane == 0) barrier_arrive(b_p2 + 8 * t);
                     l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
                 }
                 barrier_wait(b_o + 8 * t, n_o++ & 1, guard);

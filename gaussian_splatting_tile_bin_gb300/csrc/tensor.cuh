@@ -176,19 +176,17 @@ __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16
 
 // ---- products -------------------------------------------------------------------------
 
-// Shared-memory operand descriptors (128-byte swizzle, 8-row atoms 1 KB apart):
-// contraction along the row, and across the rows (blocks of 64 along the free
-// dimension kBlockBytes apart).
-constexpr uint64_t kOperandForm = (1ull << 46) | (2ull << 61) | ((uint64_t)(1024 >> 4) << 32);
+// Shared-memory operand descriptors (128-byte swizzle, 8-row atoms 1 KB apart).
+// The low word holds the address, which alone changes from one to the next, and
+// the distance of blocks of 64 along the free dimension (for a contraction
+// across the rows; 1 where there is none), both in units of 16 bytes.
+constexpr uint32_t kOperandHigh = (1u << 14) | (2u << 29) | (1024 >> 4);
 
-__device__ __forceinline__ uint64_t operand_rows(uint32_t address)
-{
-    return kOperandForm | (1ull << 16) | ((address >> 4) & 0x3fff);
-}
+__device__ __forceinline__ uint32_t operand_rows(uint32_t address) { return (1u << 16) | (address >> 4); }
 
-__device__ __forceinline__ uint64_t operand_across(uint32_t address)
+__device__ __forceinline__ uint32_t operand_across(uint32_t address)
 {
-    return kOperandForm | ((uint64_t)(kBlockBytes >> 4) << 16) | ((address >> 4) & 0x3fff);
+    return ((uint32_t)(kBlockBytes >> 4) << 16) | (address >> 4);
 }
 
 // Instruction descriptor: f32 sums of 16-bit operands of one type, M = 128.
@@ -200,54 +198,60 @@ __device__ __forceinline__ uint32_t product_form(int n, bool b_major_mn)
            ((128u >> 4) << 24);
 }
 
-// d (128 x n, tensor memory) = a b (+ d), one instruction's 16 terms.
-__device__ __forceinline__ void product_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t form, bool add)
+// d (128 x n, tensor memory) = a b (+ d), one instruction's 16 terms.  Called by a
+// whole converged warp, issued by its leader.
+__device__ __forceinline__ void product_ss(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t form, bool add)
 {
     asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(form), "r"((uint32_t)add)
+        "{\n.reg .pred p, q;\n.reg .b64 a, b;\nsetp.ne.u32 p, %4, 0;\nsetp.ne.u32 q, %5, 0;\n"
+        "mov.b64 a, {%1, %6};\nmov.b64 b, {%2, %6};\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(form), "r"((uint32_t)add), "r"((uint32_t)leader), "n"(kOperandHigh)
         : "memory");
 }
 
-__device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t form, bool add)
+__device__ __forceinline__ void product_ts(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t form, bool add)
 {
     asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(form), "r"((uint32_t)add)
+        "{\n.reg .pred p, q;\n.reg .b64 b;\nsetp.ne.u32 p, %4, 0;\nsetp.ne.u32 q, %5, 0;\n"
+        "mov.b64 b, {%2, %6};\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(form), "r"((uint32_t)add), "r"((uint32_t)leader), "n"(kOperandHigh)
         : "memory");
 }
 
-// Arrives on the barrier once every product this thread has issued is complete.
-__device__ __forceinline__ void product_commit(uint32_t bar)
+// Arrives on the barrier once every product the leader has issued is complete.
+__device__ __forceinline__ void product_commit(bool leader, uint32_t bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    asm volatile(
+        "{\n.reg .pred q;\nsetp.ne.u32 q, %1, 0;\n"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+        "r"((uint32_t)leader)
+        : "memory");
 }
 
 // d = a b^T over `steps` x 16 elements along both tiles' rows of a (128 rows) and b.
-__device__ __forceinline__ void product_rows(uint32_t d, uint32_t a, uint32_t b, uint32_t form, int steps)
+template <int HD>
+__device__ __forceinline__ void product_rows(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t form, int steps)
 {
-#pragma unroll 1
-    for (int k = 0; k < steps; ++k) {
-        const uint32_t at = (k >> 2) * kBlockBytes + (k & 3) * 32;
-        product_ss(d, operand_rows(a + at), operand_rows(b + at), form, k != 0);
+    const uint32_t a0 = operand_rows(a), b0 = operand_rows(b);
+#pragma unroll
+    for (int k = 0; k < HD / 16; ++k) {
+        const uint32_t at = ((k >> 2) * kBlockBytes + (k & 3) * 32) >> 4;
+        if (k < steps) product_ss(leader, d, a0 + at, b0 + at, form, k != 0);
     }
 }
 
-// d (+)= a b with a (128 x 128, 16-bit pairs in tensor memory) against the rows of tile b.
-__device__ __forceinline__ void product_across(uint32_t d, uint32_t a, uint32_t b, uint32_t form, bool add)
+// d (+)= a b with a (128 rows, 16-bit pairs in tensor memory) against rows
+// 16 K0 .. 16 K1 - 1 of tile b; `half` is the column distance of a's second 64 terms.
+template <int K0, int K1>
+__device__ __forceinline__ void product_across(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t form, bool add,
+                                               int half = 32)
 {
-#pragma unroll 1
-    for (int k = 0; k < 8; ++k) product_ts(d, a + k * 8, operand_across(b + k * 2048), form, add || k != 0);
-}
-
-// The same with a's two halves of 64 terms at columns 0 and 64.
-__device__ __forceinline__ void product_halves(uint32_t d, uint32_t a, uint32_t b, uint32_t form, bool add)
-{
-#pragma unroll 1
-    for (int k = 0; k < 8; ++k)
-        product_ts(d, a + (k & 3) * 8 + (k >> 2) * 64, operand_across(b + k * 2048), form, add || k != 0);
+    const uint32_t b0 = operand_across(b);
+#pragma unroll
+    for (int k = K0; k < K1; ++k)
+        product_ts(leader, d, a + (k & 3) * 8 + (k >> 2) * half, b0 + (k * 2048 >> 4), form, add || k != 0);
 }
 
 // ---- registers ------------------------------------------------------------------------------
@@ -255,12 +259,12 @@ __device__ __forceinline__ void product_halves(uint32_t d, uint32_t a, uint32_t 
 // Blocks of 384 threads start with kStartRegisters a thread; the four warps that
 // copy and issue products give most of theirs to the other eight, which hold a
 // row of scores each.
-constexpr int kStartRegisters = 168, kFewRegisters = 56, kManyRegisters = 224;
+constexpr int kStartRegisters = 168, kFewRegisters = 72, kManyRegisters = 216;
 static_assert(128 * kFewRegisters + 256 * kManyRegisters <= 384 * kStartRegisters,
               "the shares must fit what the block starts with");
 
-__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 56;"); }
-__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 224;"); }
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); }
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 216;"); }
 
 // ---- arithmetic --------------------------------------------------------------------------
 
