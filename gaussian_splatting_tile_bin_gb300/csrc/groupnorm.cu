@@ -6,24 +6,55 @@
 // elements in a group,
 //   dx = rstd (w dz - sum(w dz) / M - xh sum(w dz xh) / M).
 //
-// Bound by HBM.  Both directions are a pass that reduces over the positions per
-// channel, a small kernel that merges the blocks' partial sums into groups, and
-// a pass that writes.  Channels stay the fastest axis throughout: a thread owns
-// one vector of channels and walks positions, so accesses are contiguous for
-// any group width.
+// Bound by HBM.  Channels stay the fastest axis throughout: a thread owns one
+// vector of channels and walks positions, so accesses are contiguous for any
+// group width.  Two forms:
+//   - resident: a cluster of blocks keeps a sample's slab of whole groups in
+//     shared memory between the statistics and the result, one kernel and one
+//     read of the inputs.  For slabs that a cluster holds.
+//   - passes: a pass that reduces over the positions per channel, a small kernel
+//     that merges the blocks' partial sums into groups, and a pass that writes,
+//     over waves of samples whose inputs stay in L2 for the second pass.
 //
 // Numerics.  The variance is a merge of centred squares: a thread takes the mean
 // and the centred squares of kRun values at a time and merges (n, mean, M2)
 // pairs by Chan, Golub and LeVeque's formula, which cancels nothing when the
 // mean is far from 0.  All merges run in a fixed order.
+#include <cooperative_groups.h>
+
 #include "decoder.cuh"
 
 namespace gsr {
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kNormBlock = 256;
-constexpr int kRun = 8;          // positions a thread reads at a time
-constexpr int kMergeBlock = 128;
+constexpr int kRun = 4;          // positions a thread reads at a time
+constexpr int kMergeBlock = 256;
+// Blocks an SM holds: one wave of them takes all chunks.
+constexpr int kNormOccupancy = 4, kNormGradOccupancy = 3;
+
+// Accesses that nothing follows: the result, and the second pass' inputs.
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> load_last(const T *p)
+{
+    if constexpr (sizeof(T) * V == 16) {
+        const uint4 r = __ldcs((const uint4 *)p);
+        return *(const Vec<T, V> *)&r;
+    } else {
+        return *(const Vec<T, V> *)p;
+    }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_last(T *p, const Vec<T, V> &v)
+{
+    if constexpr (sizeof(T) * V == 16)
+        __stcs((uint4 *)p, *(const uint4 *)&v);
+    else
+        *(Vec<T, V> *)p = v;
+}
 
 struct NormArgs {
     const void *x, *dout;
@@ -46,37 +77,47 @@ struct NormArgs {
 template <typename T>
 constexpr bool kFast = sizeof(T) == 2;   // 16-bit outputs hide the fast exponential's 1e-6
 
+constexpr float kLog2e = 1.4426950408889634f;
+
+// sigmoid(z) = 1 / (1 + 2^(-z log2 e)); 0 where the exponential overflows.
 template <typename T>
-__device__ __forceinline__ float sigmoid_of(float z)
+__device__ __forceinline__ float2 sigmoid2(float2 z)
 {
-    if (kFast<T>) return __fdividef(1.0f, 1.0f + __expf(-z));
-    return 1.0f / (1.0f + expf(-z));
+    if constexpr (kFast<T>) {
+        const float2 e = mul2(z, make_float2(-kLog2e, -kLog2e));
+        const float2 d = add2(make_float2(exp2_fast(e.x), exp2_fast(e.y)), make_float2(1.0f, 1.0f));
+        return make_float2(rcp_fast(d.x), rcp_fast(d.y));
+    } else {
+        return make_float2(1.0f / (1.0f + expf(-z.x)), 1.0f / (1.0f + expf(-z.y)));
+    }
 }
 
 template <typename T, int ACT>
-__device__ __forceinline__ float activate(float z)
+__device__ __forceinline__ float2 activate2(float2 z)
 {
-    if (ACT == GSR_ACT_SILU) {
-        // z sigmoid(z); sigmoid underflows to 0 for z < -88, and -inf gives 0 as the limit does.
-        const float s = sigmoid_of<T>(z);
-        return s == 0.0f ? 0.0f : z * s;
-    }
-    if (ACT == GSR_ACT_GELU) return 0.5f * z * erfcf(-0.70710678f * z);
+    if constexpr (ACT == GSR_ACT_SILU) return mul2(z, sigmoid2<T>(z));
+    if constexpr (ACT == GSR_ACT_GELU)
+        return make_float2(0.5f * z.x * erfcf(-0.70710678f * z.x), 0.5f * z.y * erfcf(-0.70710678f * z.y));
     return z;
 }
 
-template <typename T, int ACT>
-__device__ __forceinline__ float activate_slope(float z)
+template <typename T>
+__device__ __forceinline__ float gelu_slope(float z)
 {
-    if (ACT == GSR_ACT_SILU) {
-        const float s = sigmoid_of<T>(z);
-        return s == 0.0f ? 0.0f : s * (1.0f + z * (1.0f - s));
+    const float bell = kFast<T> ? __expf(-0.5f * z * z) : expf(-0.5f * z * z);
+    return 0.5f * erfcf(-0.70710678f * z) + 0.39894228f * z * bell;
+}
+
+// act'(z): sigmoid + z sigmoid (1 - sigmoid), Phi + z phi, 1.
+template <typename T, int ACT>
+__device__ __forceinline__ float2 slope2(float2 z)
+{
+    if constexpr (ACT == GSR_ACT_SILU) {
+        const float2 s = sigmoid2<T>(z);
+        return fma2(z, fma2(make_float2(-s.x, -s.y), s, s), s);
     }
-    if (ACT == GSR_ACT_GELU) {
-        const float bell = kFast<T> ? __expf(-0.5f * z * z) : expf(-0.5f * z * z);
-        return 0.5f * erfcf(-0.70710678f * z) + 0.39894228f * z * bell;
-    }
-    return 1.0f;
+    if constexpr (ACT == GSR_ACT_GELU) return make_float2(gelu_slope<T>(z.x), gelu_slope<T>(z.y));
+    return make_float2(1.0f, 1.0f);
 }
 
 struct Moments {
@@ -87,13 +128,47 @@ __device__ __forceinline__ Moments merge(const Moments &a, const Moments &b)
 {
     const float n = a.n + b.n;
     if (n == 0.0f) return a;
-    const float d = b.mean - a.mean, share = b.n / n;
+    const float d = b.mean - a.mean, share = __fdividef(b.n, n);
     return {n, fmaf(d, share, a.mean), a.m2 + b.m2 + d * d * (a.n * share)};
 }
 
+// A thread's moments of its V channels, which share n.
+template <typename T, int V>
+struct ChannelMoments {
+    float n = 0.0f, mean[V] = {}, m2[V] = {};
+    __device__ __forceinline__ void add(const Vec<T, V> (&v)[kRun])
+    {
+        const float total = n + kRun, share = __fdividef(kRun, total);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            float f[kRun], sum = 0.0f, sq = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kRun; ++k) sum += f[k] = to_float(v[k].e[j]);
+            const float mu = sum * (1.0f / kRun);
+#pragma unroll
+            for (int k = 0; k < kRun; ++k) sq = fmaf(f[k] - mu, f[k] - mu, sq);
+            const float d = mu - mean[j];
+            mean[j] = fmaf(d, share, mean[j]);
+            m2[j] += fmaf(d * d, n * share, sq);
+        }
+        n = total;
+    }
+    __device__ __forceinline__ void add(const Vec<T, V> &v)
+    {
+        n += 1.0f;
+        const float share = __fdividef(1.0f, n);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float f = to_float(v.e[j]), d = f - mean[j];
+            mean[j] = fmaf(d, share, mean[j]);
+            m2[j] = fmaf(d, f - mean[j], m2[j]);
+        }
+    }
+};
+
 // Per channel and chunk of positions: (mean, M2) of x.
 template <typename T, int V>
-__global__ void __launch_bounds__(kNormBlock) k_norm_moments(const NormArgs a)
+__global__ void __launch_bounds__(kNormBlock, kNormOccupancy) k_norm_moments(const NormArgs a)
 {
     grid_dependency_begin();
     __shared__ float s_mean[kNormBlock * V], s_m2[kNormBlock * V], s_n[kNormBlock];
@@ -104,10 +179,7 @@ __global__ void __launch_bounds__(kNormBlock) k_norm_moments(const NormArgs a)
     const int64_t p0 = (int64_t)blockIdx.x * a.rows_per_chunk;
     const int64_t p1 = min(a.positions, p0 + a.rows_per_chunk);
     const bool live = row < rows && vec * V < a.channels;
-    float mean[V], m2[V];
-    float n = 0.0f;
-#pragma unroll
-    for (int j = 0; j < V; ++j) mean[j] = m2[j] = 0.0f;
+    ChannelMoments<T, V> own;
     if (live) {
         const T *x = (const T *)a.x + (int64_t)sample * a.positions * a.channels + (int64_t)vec * V;
         int64_t p = p0 + row;
@@ -115,40 +187,16 @@ __global__ void __launch_bounds__(kNormBlock) k_norm_moments(const NormArgs a)
             Vec<T, V> v[kRun];
 #pragma unroll
             for (int k = 0; k < kRun; ++k) v[k] = *(const Vec<T, V> *)(x + (p + (int64_t)k * rows) * a.channels);
-            const float total = n + kRun;
-            const float share = kRun / total;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                float f[kRun], sum = 0.0f, sq = 0.0f;
-#pragma unroll
-                for (int k = 0; k < kRun; ++k) sum += f[k] = to_float(v[k].e[j]);
-                const float mu = sum * (1.0f / kRun);
-#pragma unroll
-                for (int k = 0; k < kRun; ++k) sq = fmaf(f[k] - mu, f[k] - mu, sq);
-                const float d = mu - mean[j];
-                mean[j] = fmaf(d, share, mean[j]);
-                m2[j] += fmaf(d * d, n * share, sq);
-            }
-            n = total;
+            own.add(v);
         }
-        for (; p < p1; p += rows) {
-            const Vec<T, V> v = *(const Vec<T, V> *)(x + p * a.channels);
-            n += 1.0f;
-            const float share = 1.0f / n;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float f = to_float(v.e[j]), d = f - mean[j];
-                mean[j] = fmaf(d, share, mean[j]);
-                m2[j] = fmaf(d, f - mean[j], m2[j]);
-            }
-        }
+        for (; p < p1; p += rows) own.add(*(const Vec<T, V> *)(x + p * a.channels));
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        s_mean[threadIdx.x * V + j] = mean[j];
-        s_m2[threadIdx.x * V + j] = m2[j];
+        s_mean[threadIdx.x * V + j] = own.mean[j];
+        s_m2[threadIdx.x * V + j] = own.m2[j];
     }
-    s_n[threadIdx.x] = n;
+    s_n[threadIdx.x] = own.n;
     __syncthreads();
     float2 *out = a.partial + ((int64_t)blockIdx.y * a.chunks + blockIdx.x) * a.channels + (int64_t)blockIdx.z * cols * V;
     for (int c = threadIdx.x; c < cols * V && (int)(blockIdx.z * cols * V) + c < a.channels; c += kNormBlock) {
@@ -161,63 +209,146 @@ __global__ void __launch_bounds__(kNormBlock) k_norm_moments(const NormArgs a)
     }
 }
 
-__device__ __forceinline__ Moments warp_merge(Moments m)
+__device__ __forceinline__ float block_sum(float x, float *s_warp)
 {
-    for (int d = 16; d > 0; d /= 2) {
-        const Moments o = {__shfl_down_sync(~0u, m.n, d), __shfl_down_sync(~0u, m.mean, d),
-                           __shfl_down_sync(~0u, m.m2, d)};
-        m = merge(m, o);
-    }
-    return m;
+    for (int d = 16; d > 0; d /= 2) x += __shfl_xor_sync(~0u, x, d);
+    __syncthreads();
+    if (threadIdx.x % 32 == 0) s_warp[threadIdx.x / 32] = x;
+    __syncthreads();
+    float sum = 0.0f;
+    for (int w = 0; w < kMergeBlock / 32; ++w) sum += s_warp[w];
+    return sum;
 }
 
-// Merges the chunks' and channels' moments of one (group, sample).
+// Merges the chunks' and channels' moments of one (group, sample): the weighted
+// mean of the means, then M2 = sum (M2_i + n_i (mean_i - mean)^2).
 __global__ void __launch_bounds__(kMergeBlock) k_norm_merge(const NormArgs a)
 {
     grid_dependency_begin();
-    __shared__ Moments s[kMergeBlock / 32];
+    __shared__ float s_warp[kMergeBlock / 32];
     const int g = blockIdx.x, sample = a.sample0 + blockIdx.y;
     const float2 *in = a.partial + (int64_t)blockIdx.y * a.chunks * a.channels + g * a.per_group;
-    Moments m = {0.0f, 0.0f, 0.0f};
+    const float rows = (float)a.rows_per_chunk;
+    const float last = (float)(a.positions - (a.chunks - 1) * a.rows_per_chunk);
     const int count = a.chunks * a.per_group;
+    auto entry = [&](int i, float &n) {
+        const int chunk = (unsigned)i / (unsigned)a.per_group, c = i - chunk * a.per_group;
+        n = chunk == a.chunks - 1 ? last : rows;
+        return in[(int64_t)chunk * a.channels + c];
+    };
+    const float total = (float)a.per_group * (float)a.positions;
+    float sum = 0.0f;
+#pragma unroll 8
     for (int i = threadIdx.x; i < count; i += kMergeBlock) {
-        const int chunk = i / a.per_group, c = i - chunk * a.per_group;
-        const float2 v = in[(int64_t)chunk * a.channels + c];
-        const float n = (float)(min(a.positions, (chunk + 1) * a.rows_per_chunk) - chunk * a.rows_per_chunk);
-        m = merge(m, {n, v.x, v.y});
+        float n;
+        const float2 v = entry(i, n);
+        sum = fmaf(n / total, v.x, sum);
     }
-    m = warp_merge(m);
-    if (threadIdx.x % 32 == 0) s[threadIdx.x / 32] = m;
-    __syncthreads();
+    const float mean = block_sum(sum, s_warp);
+    sum = 0.0f;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < count; i += kMergeBlock) {
+        float n;
+        const float2 v = entry(i, n);
+        const float d = v.x - mean;
+        sum += fmaf(n * d, d, v.y);
+    }
+    const float m2 = block_sum(sum, s_warp);
     if (threadIdx.x == 0) {
-        for (int w = 1; w < kMergeBlock / 32; ++w) m = merge(m, s[w]);
-        const float var = m.m2 / ((float)a.per_group * (float)a.positions);
-        a.mean[(int64_t)sample * a.groups + g] = m.mean;
-        a.rstd[(int64_t)sample * a.groups + g] = 1.0f / sqrtf(var + a.eps);
+        a.mean[(int64_t)sample * a.groups + g] = mean;
+        a.rstd[(int64_t)sample * a.groups + g] = 1.0f / sqrtf(m2 / total + a.eps);
     }
 }
 
-// A thread's channel constants.
+// A thread's channel constants, in pairs.
+template <int V>
+constexpr int kPairs = (V + 1) / 2;
+
 template <int V>
 struct Channel {
-    float mean[V], rstd[V], weight[V], bias[V];
+    float2 minus_mean[kPairs<V>], rstd[kPairs<V>], weight[kPairs<V>], bias[kPairs<V>];
     __device__ __forceinline__ void load(const NormArgs &a, int sample, int c0)
     {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int64_t at = (int64_t)sample * a.groups + (c0 + j) / a.per_group;
-            mean[j] = a.mean[at];
-            rstd[j] = a.rstd[at];
-            weight[j] = a.weight ? a.weight[c0 + j] : 1.0f;
-            bias[j] = a.bias ? a.bias[c0 + j] : 0.0f;
+        for (int j = 0; j < 2 * kPairs<V>; ++j) {
+            const int c = c0 + (j < V ? j : 0);
+            const int64_t at = (int64_t)sample * a.groups + c / a.per_group;
+            (&minus_mean[j / 2].x)[j % 2] = -a.mean[at];
+            (&rstd[j / 2].x)[j % 2] = a.rstd[at];
+            (&weight[j / 2].x)[j % 2] = a.weight ? a.weight[c] : 1.0f;
+            (&bias[j / 2].x)[j % 2] = a.bias ? a.bias[c] : 0.0f;
         }
     }
+    // (x - mean) rstd, and dz = dout act'(xh w + b).
+    __device__ __forceinline__ float2 hat(float2 x, int j) const { return mul2(add2(x, minus_mean[j]), rstd[j]); }
+    template <typename T, int ACT>
+    __device__ __forceinline__ float2 dz(float2 dout, float2 xh, int j) const
+    {
+        return mul2(dout, slope2<T, ACT>(fma2(xh, weight[j], bias[j])));
+    }
 };
+
+// What an output needs of its channels.
+template <int V>
+struct Affine {
+    float2 minus_mean[kPairs<V>], scale[kPairs<V>], bias[kPairs<V>];
+    __device__ __forceinline__ void from(const Channel<V> &c)
+    {
+#pragma unroll
+        for (int j = 0; j < kPairs<V>; ++j) {
+            minus_mean[j] = c.minus_mean[j];
+            scale[j] = mul2(c.rstd[j], c.weight[j]);
+            bias[j] = c.bias[j];
+        }
+    }
+    template <typename T, int ACT>
+    __device__ __forceinline__ void apply(Vec<T, V> &v) const
+    {
+#pragma unroll
+        for (int j = 0; j < kPairs<V>; ++j)
+            set_pair(v, 2 * j, activate2<T, ACT>(fma2(add2(pair_of(v, 2 * j), minus_mean[j]), scale[j], bias[j])));
+    }
+};
+
+// The backward of a vector: sums, and dx = rstd (w dz - m1 - xh m2).
+template <int V>
+struct Gradient {
+    float2 b[kPairs<V>] = {}, w[kPairs<V>] = {};
+    template <typename T, int ACT>
+    __device__ __forceinline__ void add(const Channel<V> &c, const Vec<T, V> &x, const Vec<T, V> &dout)
+    {
+#pragma unroll
+        for (int j = 0; j < kPairs<V>; ++j) {
+            const float2 xh = c.hat(pair_of(x, 2 * j), j);
+            const float2 dz = c.template dz<T, ACT>(pair_of(dout, 2 * j), xh, j);
+            b[j] = add2(b[j], dz);
+            w[j] = fma2(dz, xh, w[j]);
+        }
+    }
+    __device__ __forceinline__ float sum_b(int j) const { return (&b[j / 2].x)[j % 2]; }
+    __device__ __forceinline__ float sum_w(int j) const { return (&w[j / 2].x)[j % 2]; }
+};
+
+template <typename T, int V, int ACT>
+__device__ __forceinline__ void input_gradient(const Channel<V> &c, const float2 (&m1)[kPairs<V>],
+                                               const float2 (&m2)[kPairs<V>], Vec<T, V> &x, const Vec<T, V> &dout)
+{
+#pragma unroll
+    for (int j = 0; j < kPairs<V>; ++j) {
+        const float2 xh = c.hat(pair_of(x, 2 * j), j);
+        const float2 dz = c.template dz<T, ACT>(pair_of(dout, 2 * j), xh, j);
+        const float2 t = fma2(c.weight[j], dz, make_float2(-m1[j].x, -m1[j].y));
+        set_pair(x, 2 * j, mul2(c.rstd[j], fma2(make_float2(-xh.x, -xh.y), m2[j], t)));
+    }
+}
+
+// Walks a thread's rows p0 + row, + rows, ... below p1, kUnroll at a time.
+constexpr int kUnroll = 4;
 
 // out = act((x - mean) rstd w + b).  Blocks take the chunks from the last to the
 // first: what the moments pass read last is what L2 still holds.
 template <typename T, int V, int ACT>
-__global__ void __launch_bounds__(kNormBlock) k_norm_apply(const NormArgs a)
+__global__ void __launch_bounds__(kNormBlock, kNormOccupancy) k_norm_apply(const NormArgs a)
 {
     grid_dependency_begin();
     const int cols = a.vectors;
@@ -227,35 +358,37 @@ __global__ void __launch_bounds__(kNormBlock) k_norm_apply(const NormArgs a)
     const int local = gridDim.y - 1 - blockIdx.y, sample = a.sample0 + local;
     const int64_t p0 = (int64_t)(gridDim.x - 1 - blockIdx.x) * a.rows_per_chunk;
     const int64_t p1 = min(a.positions, p0 + a.rows_per_chunk);
-    Channel<V> ch;
-    ch.load(a, sample, vec * V);
-    float scale[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) scale[j] = ch.rstd[j] * ch.weight[j];
-    const int64_t base = (int64_t)sample * a.positions * a.channels + (int64_t)vec * V;
-    const T *x = (const T *)a.x + base;
-    T *y = (T *)a.y + base;
-    constexpr int kUnroll = 4;
-    for (int64_t p = p0 + row; p < p1; p += (int64_t)kUnroll * rows) {
+    Affine<V> affine;
+    {
+        Channel<V> ch;
+        ch.load(a, sample, vec * V);
+        affine.from(ch);
+    }
+    const int64_t first = ((int64_t)sample * a.positions + p0 + row) * a.channels + (int64_t)vec * V;
+    const int64_t stride = (int64_t)rows * a.channels;
+    const T *x = (const T *)a.x + first;
+    T *y = (T *)a.y + first;
+    int left = (int)((p1 - p0 - row + rows - 1) / rows);   // rows of this thread
+    for (; left >= kUnroll; left -= kUnroll, x += kUnroll * stride, y += kUnroll * stride) {
         Vec<T, V> v[kUnroll];
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k)
-            if (p + (int64_t)k * rows < p1) v[k] = *(const Vec<T, V> *)(x + (p + (int64_t)k * rows) * a.channels);
+        for (int k = 0; k < kUnroll; ++k) v[k] = load_last<T, V>(x + k * stride);
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k)
-            if (p + (int64_t)k * rows < p1) {
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    v[k].e[j] = from_float<T>(
-                        activate<T, ACT>(fmaf(to_float(v[k].e[j]) - ch.mean[j], scale[j], ch.bias[j])));
-                *(Vec<T, V> *)(y + (p + (int64_t)k * rows) * a.channels) = v[k];
-            }
+        for (int k = 0; k < kUnroll; ++k) {
+            affine.template apply<T, ACT>(v[k]);
+            store_last<T, V>(y + k * stride, v[k]);
+        }
+    }
+    for (; left > 0; --left, x += stride, y += stride) {
+        Vec<T, V> v = load_last<T, V>(x);
+        affine.template apply<T, ACT>(v);
+        store_last<T, V>(y, v);
     }
 }
 
 // Per channel and chunk: (sum dz, sum dz xh).
 template <typename T, int V, int ACT>
-__global__ void __launch_bounds__(kNormBlock) k_norm_grad_sums(const NormArgs a)
+__global__ void __launch_bounds__(kNormBlock, kNormGradOccupancy) k_norm_grad_sums(const NormArgs a)
 {
     grid_dependency_begin();
     __shared__ float s_b[kNormBlock * V], s_w[kNormBlock * V];
@@ -265,41 +398,31 @@ __global__ void __launch_bounds__(kNormBlock) k_norm_grad_sums(const NormArgs a)
     const int sample = a.sample0 + blockIdx.y;
     const int64_t p0 = (int64_t)blockIdx.x * a.rows_per_chunk;
     const int64_t p1 = min(a.positions, p0 + a.rows_per_chunk);
-    float sb[V], sw[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) sb[j] = sw[j] = 0.0f;
+    Gradient<V> grad;
     if (row < rows && vec * V < a.channels) {
         Channel<V> ch;
         ch.load(a, sample, vec * V);
-        const int64_t base = (int64_t)sample * a.positions * a.channels + (int64_t)vec * V;
-        const T *x = (const T *)a.x + base, *dout = (const T *)a.dout + base;
-        constexpr int kUnroll = 4;
-        for (int64_t p = p0 + row; p < p1; p += (int64_t)kUnroll * rows) {
+        const int64_t first = ((int64_t)sample * a.positions + p0 + row) * a.channels + (int64_t)vec * V;
+        const int64_t stride = (int64_t)rows * a.channels;
+        const T *x = (const T *)a.x + first, *dout = (const T *)a.dout + first;
+        int left = (int)((p1 - p0 - row + rows - 1) / rows);
+        for (; left >= kUnroll; left -= kUnroll, x += kUnroll * stride, dout += kUnroll * stride) {
             Vec<T, V> vx[kUnroll], vd[kUnroll];
 #pragma unroll
-            for (int k = 0; k < kUnroll; ++k)
-                if (p + (int64_t)k * rows < p1) {
-                    vx[k] = *(const Vec<T, V> *)(x + (p + (int64_t)k * rows) * a.channels);
-                    vd[k] = *(const Vec<T, V> *)(dout + (p + (int64_t)k * rows) * a.channels);
-                }
+            for (int k = 0; k < kUnroll; ++k) {
+                vx[k] = *(const Vec<T, V> *)(x + k * stride);
+                vd[k] = *(const Vec<T, V> *)(dout + k * stride);
+            }
 #pragma unroll
-            for (int k = 0; k < kUnroll; ++k)
-                if (p + (int64_t)k * rows < p1) {
-#pragma unroll
-                    for (int j = 0; j < V; ++j) {
-                        const float xh = (to_float(vx[k].e[j]) - ch.mean[j]) * ch.rstd[j];
-                        const float dz = to_float(vd[k].e[j]) *
-                                         activate_slope<T, ACT>(fmaf(xh, ch.weight[j], ch.bias[j]));
-                        sb[j] += dz;
-                        sw[j] = fmaf(dz, xh, sw[j]);
-                    }
-                }
+            for (int k = 0; k < kUnroll; ++k) grad.template add<T, ACT>(ch, vx[k], vd[k]);
         }
+        for (; left > 0; --left, x += stride, dout += stride)
+            grad.template add<T, ACT>(ch, *(const Vec<T, V> *)x, *(const Vec<T, V> *)dout);
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        s_b[threadIdx.x * V + j] = sb[j];
-        s_w[threadIdx.x * V + j] = sw[j];
+        s_b[threadIdx.x * V + j] = grad.sum_b(j);
+        s_w[threadIdx.x * V + j] = grad.sum_w(j);
     }
     __syncthreads();
     float2 *out = a.partial + ((int64_t)blockIdx.y * a.chunks + blockIdx.x) * a.channels + (int64_t)blockIdx.z * cols * V;
@@ -366,7 +489,7 @@ __global__ void __launch_bounds__(kMergeBlock) k_norm_grad_merge(const NormArgs 
 // dx = rstd (w dz - m1 - xh m2).  The blocks of the last launch's first chunk
 // also sum the parameter gradients over the samples.
 template <typename T, int V, int ACT>
-__global__ void __launch_bounds__(kNormBlock) k_norm_grad_apply(const NormArgs a)
+__global__ void __launch_bounds__(kNormBlock, kNormGradOccupancy) k_norm_grad_apply(const NormArgs a)
 {
     grid_dependency_begin();
     if (blockIdx.x == 0 && blockIdx.y == 0 && a.sample0 + (int)gridDim.y == a.samples) {
@@ -390,40 +513,363 @@ __global__ void __launch_bounds__(kNormBlock) k_norm_grad_apply(const NormArgs a
     const int64_t p1 = min(a.positions, p0 + a.rows_per_chunk);
     Channel<V> ch;
     ch.load(a, sample, vec * V);
-    float m1[V], m2[V];
+    float2 m1[kPairs<V>], m2[kPairs<V>];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const float2 m = a.group_sums[(int64_t)sample * a.groups + (vec * V + j) / a.per_group];
-        m1[j] = m.x;
-        m2[j] = m.y;
+    for (int j = 0; j < 2 * kPairs<V>; ++j) {
+        const float2 m = a.group_sums[(int64_t)sample * a.groups + (vec * V + (j < V ? j : 0)) / a.per_group];
+        (&m1[j / 2].x)[j % 2] = m.x;
+        (&m2[j / 2].x)[j % 2] = m.y;
     }
-    const int64_t base = (int64_t)sample * a.positions * a.channels + (int64_t)vec * V;
-    const T *x = (const T *)a.x + base, *dout = (const T *)a.dout + base;
-    T *y = (T *)a.y + base;
-    constexpr int kUnroll = 4;
-    for (int64_t p = p0 + row; p < p1; p += (int64_t)kUnroll * rows) {
-        Vec<T, V> vx[kUnroll], vd[kUnroll];
+    const int64_t first = ((int64_t)sample * a.positions + p0 + row) * a.channels + (int64_t)vec * V;
+    const int64_t stride = (int64_t)rows * a.channels;
+    const T *x = (const T *)a.x + first, *dout = (const T *)a.dout + first;
+    T *y = (T *)a.y + first;
+    int left = (int)((p1 - p0 - row + rows - 1) / rows);
+    constexpr int kTwo = kUnroll / 2;   // two inputs and twice the constants: half the rows at a time
+    for (; left >= kTwo; left -= kTwo, x += kTwo * stride, dout += kTwo * stride, y += kTwo * stride) {
+        Vec<T, V> vx[kTwo], vd[kTwo];
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k)
-            if (p + (int64_t)k * rows < p1) {
-                vx[k] = *(const Vec<T, V> *)(x + (p + (int64_t)k * rows) * a.channels);
-                vd[k] = *(const Vec<T, V> *)(dout + (p + (int64_t)k * rows) * a.channels);
-            }
+        for (int k = 0; k < kTwo; ++k) {
+            vx[k] = load_last<T, V>(x + k * stride);
+            vd[k] = load_last<T, V>(dout + k * stride);
+        }
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k)
-            if (p + (int64_t)k * rows < p1) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const float xh = (to_float(vx[k].e[j]) - ch.mean[j]) * ch.rstd[j];
-                    const float dz =
-                        to_float(vd[k].e[j]) * activate_slope<T, ACT>(fmaf(xh, ch.weight[j], ch.bias[j]));
-                    const float dxh = fmaf(ch.weight[j], dz, -m1[j]);
-                    vx[k].e[j] = from_float<T>(ch.rstd[j] * fmaf(-xh, m2[j], dxh));
-                }
-                *(Vec<T, V> *)(y + (p + (int64_t)k * rows) * a.channels) = vx[k];
-            }
+        for (int k = 0; k < kTwo; ++k) {
+            input_gradient<T, V, ACT>(ch, m1, m2, vx[k], vd[k]);
+            store_last<T, V>(y + k * stride, vx[k]);
+        }
+    }
+    for (; left > 0; --left, x += stride, dout += stride, y += stride) {
+        Vec<T, V> vx = load_last<T, V>(x);
+        const Vec<T, V> vd = load_last<T, V>(dout);
+        input_gradient<T, V, ACT>(ch, m1, m2, vx, vd);
+        store_last<T, V>(y, vx);
     }
 }
+
+// ---- resident form ---------------------------------------------------------------
+
+constexpr int kResidentBlock = 512;
+constexpr int kResidentChannels = 512;              // of a slab, at most
+constexpr int kResidentCluster = 8;
+constexpr size_t kResidentData = 172 * 1024;        // of a block's shared memory, at most
+
+struct ResidentArgs {
+    NormArgs n;
+    int slabs, slab_groups, slab_channels;
+    int64_t rows_per_block;
+    int row_capacity;                               // rows_per_block, as the shared layout has it
+};
+
+__device__ __forceinline__ void copy16(void *to, const void *from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from)
+                 : "memory");
+}
+
+__device__ __forceinline__ void copies_done()
+{
+    asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
+}
+
+// A block's place: its sample, slab and rows, and a thread's column and rows.
+template <int V>
+struct Place {
+    int sample, slab, cols, col, row, rows, channel0;
+    int64_t p0, p1, base;                           // base: element of (p0, this thread's vector)
+    bool live;
+    __device__ Place(const ResidentArgs &a, int rank, int cluster)
+    {
+        const int unit = blockIdx.x / cluster;
+        sample = unit / a.slabs;
+        slab = unit - sample * a.slabs;
+        cols = a.slab_channels / V;
+        col = threadIdx.x % cols;
+        row = threadIdx.x / cols;
+        rows = kResidentBlock / cols;
+        live = row < rows;
+        channel0 = slab * a.slab_channels + col * V;
+        p0 = min(a.n.positions, rank * a.rows_per_block);
+        p1 = min(a.n.positions, p0 + a.rows_per_block);
+        base = ((int64_t)sample * a.n.positions + p0) * a.n.channels + channel0;
+    }
+    __device__ int count() const { return (int)(p1 - p0); }
+};
+
+template <typename T, int V, int ACT>
+__global__ void __launch_bounds__(kResidentBlock) k_norm_resident(const __grid_constant__ ResidentArgs a)
+{
+    grid_dependency_begin();
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    extern __shared__ __align__(16) unsigned char s_raw[];
+    Vec<T, V> *s_x = (Vec<T, V> *)s_raw;                                      // [row_capacity][cols]
+    const Place<V> at(a, rank, ranks);
+    float *s_mean = (float *)(s_x + (size_t)a.row_capacity * at.cols), *s_m2 = s_mean + kResidentBlock * V;
+    float *s_n = s_m2 + kResidentBlock * V;                                   // [kResidentBlock]
+    Moments *s_part = (Moments *)(s_n + kResidentBlock);                      // [parts][channels]
+    Moments *s_group = s_part + kResidentBlock;                               // [slab_groups]
+    float2 *s_stat = (float2 *)(s_group + kResidentChannels);                 // [slab_groups]: mean, rstd
+    const T *x = (const T *)a.n.x + at.base;
+    const int count = at.count();
+    ChannelMoments<T, V> own;
+    if (at.live) {
+        for (int p = at.row; p < count; p += at.rows)
+            copy16(&s_x[p * at.cols + at.col], x + (int64_t)p * a.n.channels);
+        copies_done();
+        // A thread reads only what it copied itself.
+        int p = at.row;
+        for (; p + (kRun - 1) * at.rows < count; p += kRun * at.rows) {
+            Vec<T, V> v[kRun];
+#pragma unroll
+            for (int k = 0; k < kRun; ++k) v[k] = s_x[(p + k * at.rows) * at.cols + at.col];
+            own.add(v);
+        }
+        for (; p < count; p += at.rows) own.add(s_x[p * at.cols + at.col]);
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        s_mean[threadIdx.x * V + j] = own.mean[j];
+        s_m2[threadIdx.x * V + j] = own.m2[j];
+    }
+    s_n[threadIdx.x] = own.n;
+    __syncthreads();
+    const int channels = a.slab_channels, parts = kResidentBlock / channels;
+    if ((int)threadIdx.x < parts * channels) {
+        const int c = threadIdx.x % channels, part = threadIdx.x / channels;
+        Moments m = {0.0f, 0.0f, 0.0f};
+        for (int r = part; r < at.rows; r += parts) {
+            const int t = r * at.cols + c / V;
+            m = merge(m, {s_n[t], s_mean[t * V + c % V], s_m2[t * V + c % V]});
+        }
+        s_part[threadIdx.x] = m;
+    }
+    __syncthreads();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, per_group = a.n.per_group;
+    for (int g = warp; g < a.slab_groups; g += kResidentBlock / 32) {
+        Moments m = {0.0f, 0.0f, 0.0f};
+        for (int i = lane; i < parts * per_group; i += 32) {
+            const int part = i / per_group;
+            m = merge(m, s_part[part * channels + g * per_group + i - part * per_group]);
+        }
+        for (int d = 16; d > 0; d /= 2)
+            m = merge(m, {__shfl_down_sync(~0u, m.n, d), __shfl_down_sync(~0u, m.mean, d),
+                          __shfl_down_sync(~0u, m.m2, d)});
+        if (lane == 0) s_group[g] = m;
+    }
+    cluster.sync();
+    for (int g = threadIdx.x; g < a.slab_groups; g += kResidentBlock) {
+        Moments m = {0.0f, 0.0f, 0.0f};
+        for (int r = 0; r < ranks; ++r) m = merge(m, *cluster.map_shared_rank(&s_group[g], r));
+        const float rstd = 1.0f / sqrtf(m.m2 / m.n + a.n.eps);
+        s_stat[g] = make_float2(m.mean, rstd);
+        if (rank == 0) {
+            const int64_t to = (int64_t)at.sample * a.n.groups + at.slab * a.slab_groups + g;
+            a.n.mean[to] = m.mean;
+            a.n.rstd[to] = rstd;
+        }
+    }
+    __syncthreads();
+    if (at.live) {
+        Affine<V> affine;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float2 st = s_stat[(at.col * V + j) / per_group];
+            (&affine.minus_mean[j / 2].x)[j % 2] = -st.x;
+            (&affine.scale[j / 2].x)[j % 2] = st.y * (a.n.weight ? a.n.weight[at.channel0 + j] : 1.0f);
+            (&affine.bias[j / 2].x)[j % 2] = a.n.bias ? a.n.bias[at.channel0 + j] : 0.0f;
+        }
+        T *y = (T *)a.n.y + at.base;
+#pragma unroll 2
+        for (int p = at.row; p < count; p += at.rows) {
+            Vec<T, V> v = s_x[p * at.cols + at.col];
+            affine.template apply<T, ACT>(v);
+            *(Vec<T, V> *)(y + (int64_t)p * a.n.channels) = v;
+        }
+    }
+    cluster.sync();   // no block leaves while another may read its shared memory
+}
+
+template <typename T, int V, int ACT>
+__global__ void __launch_bounds__(kResidentBlock) k_norm_grad_resident(const __grid_constant__ ResidentArgs a)
+{
+    grid_dependency_begin();
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    extern __shared__ __align__(16) unsigned char s_raw[];
+    const Place<V> at(a, rank, ranks);
+    Vec<T, V> *s_x = (Vec<T, V> *)s_raw, *s_d = s_x + (size_t)a.row_capacity * at.cols;
+    float *s_b = (float *)(s_d + (size_t)a.row_capacity * at.cols), *s_w = s_b + kResidentBlock * V;
+    float2 *s_part = (float2 *)(s_w + kResidentBlock * V);                    // [parts][channels]
+    float2 *s_mine = s_part + kResidentBlock;                                 // [channels] of this block
+    float2 *s_all = s_mine + kResidentChannels;                               // [channels] of the cluster
+    float2 *s_group = s_all + kResidentChannels;                              // [slab_groups]
+    const int count = at.count(), per_group = a.n.per_group;
+    const T *x = (const T *)a.n.x + at.base, *dout = (const T *)a.n.dout + at.base;
+    Gradient<V> grad;
+    Channel<V> ch;
+    if (at.live) {
+        for (int p = at.row; p < count; p += at.rows) {
+            copy16(&s_x[p * at.cols + at.col], x + (int64_t)p * a.n.channels);
+            copy16(&s_d[p * at.cols + at.col], dout + (int64_t)p * a.n.channels);
+        }
+        ch.load(a.n, at.sample, at.channel0);
+        copies_done();
+#pragma unroll 2
+        for (int p = at.row; p < count; p += at.rows) {
+            grad.template add<T, ACT>(ch, s_x[p * at.cols + at.col], s_d[p * at.cols + at.col]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        s_b[threadIdx.x * V + j] = grad.sum_b(j);
+        s_w[threadIdx.x * V + j] = grad.sum_w(j);
+    }
+    __syncthreads();
+    const int channels = a.slab_channels, parts = kResidentBlock / channels;
+    if ((int)threadIdx.x < parts * channels) {
+        const int c = threadIdx.x % channels, part = threadIdx.x / channels;
+        float2 m = make_float2(0.0f, 0.0f);
+        for (int r = part; r < at.rows; r += parts) {
+            const int t = (r * at.cols + c / V) * V + c % V;
+            m.x += s_b[t];
+            m.y += s_w[t];
+        }
+        s_part[threadIdx.x] = m;
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < channels) {
+        float2 m = make_float2(0.0f, 0.0f);
+        for (int part = 0; part < parts; ++part) {
+            m.x += s_part[part * channels + threadIdx.x].x;
+            m.y += s_part[part * channels + threadIdx.x].y;
+        }
+        s_mine[threadIdx.x] = m;
+    }
+    cluster.sync();
+    if ((int)threadIdx.x < channels) {
+        float2 m = make_float2(0.0f, 0.0f);
+        for (int r = 0; r < ranks; ++r) {
+            const float2 v = *cluster.map_shared_rank(&s_mine[threadIdx.x], r);
+            m.x += v.x;
+            m.y += v.y;
+        }
+        const int c = at.slab * channels + threadIdx.x;
+        if (rank == 0) a.n.sums[(int64_t)at.sample * a.n.channels + c] = m;
+        const float w = a.n.weight ? a.n.weight[c] : 1.0f;
+        s_all[threadIdx.x] = make_float2(w * m.x, w * m.y);
+    }
+    __syncthreads();
+    for (int g = threadIdx.x; g < a.slab_groups; g += kResidentBlock) {
+        float2 m = make_float2(0.0f, 0.0f);
+        for (int c = g * per_group; c < (g + 1) * per_group; ++c) {
+            m.x += s_all[c].x;
+            m.y += s_all[c].y;
+        }
+        const float inv = 1.0f / ((float)per_group * (float)a.n.positions);
+        s_group[g] = make_float2(m.x * inv, m.y * inv);
+    }
+    __syncthreads();
+    if (at.live) {
+        float2 m1[kPairs<V>], m2[kPairs<V>];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float2 m = s_group[(at.col * V + j) / per_group];
+            (&m1[j / 2].x)[j % 2] = m.x;
+            (&m2[j / 2].x)[j % 2] = m.y;
+        }
+        T *y = (T *)a.n.y + at.base;
+#pragma unroll 2
+        for (int p = at.row; p < count; p += at.rows) {
+            Vec<T, V> vx = s_x[p * at.cols + at.col];
+            input_gradient<T, V, ACT>(ch, m1, m2, vx, s_d[p * at.cols + at.col]);
+            *(Vec<T, V> *)(y + (int64_t)p * a.n.channels) = vx;
+        }
+    }
+    cluster.sync();   // no block leaves while another may read its shared memory
+}
+
+// Parameter gradients: the samples' channel sums in order.
+__global__ void __launch_bounds__(kNormBlock) k_norm_param_grads(const NormArgs a)
+{
+    grid_dependency_begin();
+    const int c = blockIdx.x * kNormBlock + threadIdx.x;
+    if (c >= a.channels) return;
+    float2 m = make_float2(0.0f, 0.0f);
+    for (int n = 0; n < a.samples; ++n) {
+        const float2 v = a.sums[(int64_t)n * a.channels + c];
+        m.x += v.x;
+        m.y += v.y;
+    }
+    if (a.dbias) a.dbias[c] = m.x;
+    if (a.dweight) a.dweight[c] = m.y;
+}
+
+struct ResidentPlan {
+    bool fits = false;
+    int slab_groups, slabs, cluster;
+    int64_t rows;
+    size_t smem;
+};
+
+// Slabs of whole groups and whole vectors, 64 bytes wide where the groups allow
+// (narrower rows waste DRAM sectors), over as few blocks as hold 32 KB each and as
+// many as a cluster has.
+ResidentPlan resident_plan(const gsr_group_norm &d, int width, bool backward)
+{
+    ResidentPlan p;
+    const int size = d.dtype == GSR_F32 ? 4 : 2, per_group = d.channels / d.groups;
+    if (width == 1) return p;
+    int groups = 1;
+    for (; groups <= d.groups; ++groups)
+        if (d.groups % groups == 0 && groups * per_group % width == 0 &&
+            (groups == d.groups || groups * per_group * size >= 64))
+            break;
+    const int channels = groups * per_group, arrays = backward ? 2 : 1;
+    if (groups > d.groups || channels > kResidentChannels) return p;
+    const int64_t row_bytes = (int64_t)channels * size * arrays, bytes = d.positions * row_bytes;
+    int64_t cluster = (bytes + 32 * 1024 - 1) / (32 * 1024);
+    if (cluster > kResidentCluster) cluster = kResidentCluster;
+    const int64_t rows = (d.positions + cluster - 1) / cluster;
+    if (rows * row_bytes > (int64_t)kResidentData) return p;
+    p.fits = true;
+    p.slab_groups = groups;
+    p.slabs = d.groups / groups;
+    p.cluster = (int)cluster;
+    p.rows = rows;
+    const size_t sums = (size_t)kResidentBlock * width * 2 * sizeof(float);
+    const size_t rest = backward ? (kResidentBlock + 3 * kResidentChannels) * sizeof(float2)
+                                 : kResidentBlock * (sizeof(float) + sizeof(Moments)) +
+                                       kResidentChannels * (sizeof(Moments) + sizeof(float2));
+    p.smem = (size_t)(rows * row_bytes) + sums + rest;
+    return p;
+}
+
+template <typename Kernel>
+cudaError_t launch_cluster(gsr_ctx *ctx, Kernel *kernel, const ResidentPlan &p, const ResidentArgs &a,
+                           cudaStream_t stream)
+{
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((int64_t)a.n.samples * a.slabs * p.cluster));
+    cfg.blockDim = dim3(kResidentBlock);
+    cfg.dynamicSmemBytes = p.smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = ctx->opt_pdl ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    ++ctx->launches;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+// ---- host ---------------------------------------------------------------------------
 
 // Splits of the positions: enough blocks for every SM, a few runs of rows each.
 struct NormPlan {
@@ -431,7 +877,7 @@ struct NormPlan {
     int64_t rows_per_chunk;
 };
 
-NormPlan norm_plan(const gsr_ctx *ctx, const gsr_group_norm &d, int width, int arrays)
+NormPlan norm_plan(const gsr_ctx *ctx, const gsr_group_norm &d, int width, bool backward)
 {
     NormPlan p;
     const int vectors = (d.channels + width - 1) / width;
@@ -439,13 +885,13 @@ NormPlan norm_plan(const gsr_ctx *ctx, const gsr_group_norm &d, int width, int a
     p.slabs = (vectors + p.vectors - 1) / p.vectors;
     const int rows = kNormBlock / p.vectors;
     // A wave of samples whose arrays stay in L2 between the two passes over them.
-    const int64_t sample_bytes = d.positions * d.channels * (d.dtype == GSR_F32 ? 4 : 2) * arrays;
-    constexpr int64_t kL2Share = (int64_t)64 << 20;
+    const int64_t sample_bytes = d.positions * d.channels * (d.dtype == GSR_F32 ? 4 : 2) * (backward ? 2 : 1);
+    constexpr int64_t kL2Share = (int64_t)96 << 20;
     int64_t wave = kL2Share / (sample_bytes > 0 ? sample_bytes : 1);
     wave = wave < 1 ? 1 : wave;
     p.wave = (int)(wave < d.samples ? wave : d.samples);
     if (p.wave > 65535) p.wave = 65535;
-    int64_t chunks = (4 * (int64_t)ctx->num_sms + (int64_t)p.wave * p.slabs - 1) / ((int64_t)p.wave * p.slabs);
+    int64_t chunks = (int64_t)(backward ? kNormGradOccupancy : kNormOccupancy) * ctx->num_sms / ((int64_t)p.wave * p.slabs);
     const int64_t most = (d.positions + (int64_t)rows * kRun - 1) / ((int64_t)rows * kRun);
     if (chunks > most) chunks = most;
     if (chunks < 1) chunks = 1;
@@ -491,27 +937,47 @@ cudaError_t norm_backward(gsr_ctx *ctx, NormArgs &a, const NormPlan &p, cudaStre
     return cudaSuccess;
 }
 
+template <typename T, int V, int ACT>
+cudaError_t norm_resident(gsr_ctx *ctx, const NormArgs &n, const ResidentPlan &p, bool backward, cudaStream_t stream)
+{
+    ResidentArgs a = {};
+    a.n = n;
+    a.slabs = p.slabs;
+    a.slab_groups = p.slab_groups;
+    a.slab_channels = p.slab_groups * n.per_group;
+    a.rows_per_block = p.rows;
+    a.row_capacity = (int)p.rows;
+    if (!backward) return launch_cluster(ctx, k_norm_resident<T, V, ACT>, p, a, stream);
+    const cudaError_t e = launch_cluster(ctx, k_norm_grad_resident<T, V, ACT>, p, a, stream);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(ctx, k_norm_param_grads, dim3((unsigned)((n.channels + kNormBlock - 1) / kNormBlock)),
+                         kNormBlock, stream, n);
+}
+
 template <typename T, int ACT>
-cudaError_t dispatch_width(gsr_ctx *ctx, NormArgs &a, const NormPlan &p, int width, bool backward, cudaStream_t s)
+cudaError_t dispatch_width(gsr_ctx *ctx, NormArgs &a, const NormPlan &p, const ResidentPlan &r, int width,
+                           bool backward, cudaStream_t s)
 {
     constexpr int kFull = 16 / (int)sizeof(T);
+    if (r.fits) return norm_resident<T, kFull, ACT>(ctx, a, r, backward, s);
     if (width == kFull) return backward ? norm_backward<T, kFull, ACT>(ctx, a, p, s) : norm_forward<T, kFull, ACT>(ctx, a, p, s);
     return backward ? norm_backward<T, 1, ACT>(ctx, a, p, s) : norm_forward<T, 1, ACT>(ctx, a, p, s);
 }
 
 template <typename T>
-cudaError_t dispatch_act(gsr_ctx *ctx, NormArgs &a, const NormPlan &p, int act, int width, bool backward,
-                         cudaStream_t s)
+cudaError_t dispatch_act(gsr_ctx *ctx, NormArgs &a, const NormPlan &p, const ResidentPlan &r, int act, int width,
+                         bool backward, cudaStream_t s)
 {
-    if (act == GSR_ACT_SILU) return dispatch_width<T, GSR_ACT_SILU>(ctx, a, p, width, backward, s);
-    if (act == GSR_ACT_GELU) return dispatch_width<T, GSR_ACT_GELU>(ctx, a, p, width, backward, s);
-    return dispatch_width<T, GSR_ACT_NONE>(ctx, a, p, width, backward, s);
+    if (act == GSR_ACT_SILU) return dispatch_width<T, GSR_ACT_SILU>(ctx, a, p, r, width, backward, s);
+    if (act == GSR_ACT_GELU) return dispatch_width<T, GSR_ACT_GELU>(ctx, a, p, r, width, backward, s);
+    return dispatch_width<T, GSR_ACT_NONE>(ctx, a, p, r, width, backward, s);
 }
 
 int run_norm(gsr_ctx *ctx, const gsr_group_norm &d, NormArgs &a, bool backward, cudaStream_t stream)
 {
     const int width = norm_width(d, a.x, a.dout, a.y);
-    const NormPlan p = norm_plan(ctx, d, width, backward ? 3 : 2);
+    const ResidentPlan r = resident_plan(d, width, backward);
+    const NormPlan p = norm_plan(ctx, d, width, backward);
     a.samples = d.samples;
     a.channels = d.channels;
     a.groups = d.groups;
@@ -521,7 +987,7 @@ int run_norm(gsr_ctx *ctx, const gsr_group_norm &d, NormArgs &a, bool backward, 
     a.chunks = p.chunks;
     a.vectors = p.vectors;
     a.eps = d.eps;
-    const size_t partial = (size_t)p.wave * p.chunks * d.channels * sizeof(float2);
+    const size_t partial = r.fits ? 0 : round_up((size_t)p.wave * p.chunks * d.channels * sizeof(float2), 256);
     const size_t sums = backward ? (size_t)d.samples * d.channels * sizeof(float2) : 0;
     const size_t group_sums = backward ? (size_t)d.samples * d.groups * sizeof(float2) : 0;
     void *work;
@@ -531,11 +997,11 @@ int run_norm(gsr_ctx *ctx, const gsr_group_norm &d, NormArgs &a, bool backward, 
     a.group_sums = (float2 *)((unsigned char *)work + partial + sums);
     cudaError_t e;
     if (d.dtype == GSR_F32)
-        e = dispatch_act<float>(ctx, a, p, d.activation, width, backward, stream);
+        e = dispatch_act<float>(ctx, a, p, r, d.activation, width, backward, stream);
     else if (d.dtype == GSR_BF16)
-        e = dispatch_act<__nv_bfloat16>(ctx, a, p, d.activation, width, backward, stream);
+        e = dispatch_act<__nv_bfloat16>(ctx, a, p, r, d.activation, width, backward, stream);
     else
-        e = dispatch_act<__half>(ctx, a, p, d.activation, width, backward, stream);
+        e = dispatch_act<__half>(ctx, a, p, r, d.activation, width, backward, stream);
     if (int rc = cuda_check(ctx, e, backward ? "group norm backward" : "group norm forward")) return rc;
     return workspace_done(ctx, stream);
 }

@@ -5,16 +5,19 @@
 // holds i: (u, v) -> (u cos - v sin, u sin + v cos).  The backward is the
 // rotation by -theta, so both directions are one kernel with a sign.
 //
-// Bound by HBM: every element is read and written once, and a token's sines and
-// cosines serve all of its heads, so a thread owns one run of pairs of a token,
-// evaluates their angles once and walks the heads with them.
+// Bound by HBM: every element is read and written once.  A token's sines and
+// cosines serve all of its heads, so a block takes a few tokens, evaluates their
+// angles once into shared memory while its loads of x are in flight, and turns.
 #include "decoder.cuh"
 
 namespace gsr {
 namespace {
 
 constexpr int kRotaryBlock = 256;
-constexpr int kRotaryHeads = 4;   // heads whose loads are in flight together
+// Items of a thread whose loads are in flight together: 64 bytes of them.
+template <int V, bool INTERLEAVED>
+constexpr int kRotaryItems = !INTERLEAVED && V > 1 ? 2 : 4;
+constexpr int kRotaryTable = 4096;   // (token, pair) angles of a block
 
 struct RotaryArgs {
     const void *x;
@@ -23,8 +26,9 @@ struct RotaryArgs {
     const void *positions;
     const float *frequencies;
     int64_t positions_batch;
-    int64_t items;          // (token, run) items
-    int tokens, heads, heads_per_block;
+    int64_t all_tokens;     // batch * tokens
+    int block_runs, slots;  // runs of a block, and threads of a run
+    int tokens, heads, block_tokens;
     int pairs, dim;
     int turn_runs, runs;    // runs that turn, and with the copied ones
     int axes, positions_int;
@@ -48,85 +52,111 @@ __device__ __forceinline__ void sincos_product(float p_hi, float p_lo, float f, 
 }
 
 // V is the width of an access in elements; a run is V pairs (halves) or V / 2
-// pairs (interleaved), one pair with scalar accesses.
+// pairs (interleaved), one pair with scalar accesses, or V copied dimensions.  An
+// item is one run of one head of one token.
 template <typename T, int V, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRotaryBlock) k_rotary(const RotaryArgs a)
+__global__ void __launch_bounds__(kRotaryBlock, 4) k_rotary(const RotaryArgs a)
 {
     grid_dependency_begin();
+    extern __shared__ float2 s_turn[];   // (cos, sin) of [token][pair]
     constexpr int P = INTERLEAVED ? (V > 1 ? V / 2 : 1) : V;
+    // Vectorised interleaved pairs sit in one access, the others in two.
+    constexpr bool kOne = INTERLEAVED && V > 1;
+    constexpr int kItems = kRotaryItems<V, INTERLEAVED>;
     using Access = Vec<T, V>;
-    const int64_t item = (int64_t)blockIdx.x * kRotaryBlock + threadIdx.x;
-    if (item >= a.items) return;
-    int64_t token;
-    int run;
-    if (a.items <= 0x7fffffff) {
-        token = (uint32_t)item / (uint32_t)a.runs;
-        run = (int)((uint32_t)item - (uint32_t)token * (uint32_t)a.runs);
-    } else {
-        token = item / a.runs;
-        run = (int)(item - token * a.runs);
-    }
-    const int64_t b = token / a.tokens;
-    const int64_t t = token - b * a.tokens;
-    const int head0 = blockIdx.y * a.heads_per_block;
-    const int head1 = min(a.heads, head0 + a.heads_per_block);
-    const T *x = (const T *)a.x + b * a.x_batch + t * a.x_token;
-    T *out = (T *)a.out + b * a.out_batch + t * a.out_token;
-
-    if (run >= a.turn_runs) {   // dimensions behind the pairs
-        const int d = 2 * a.pairs + (run - a.turn_runs) * V;
-        for (int h = head0; h < head1; ++h)
-            *(Access *)(out + h * a.out_head + d) = *(const Access *)(x + h * a.x_head + d);
-        return;
-    }
-
-    float s[P], c[P];
-    const int64_t at = b * a.positions_batch + t * a.axes;
+    const int64_t token0 = (int64_t)blockIdx.x * a.block_tokens;
+    const int count = (int)min((int64_t)a.block_tokens, a.all_tokens - token0);
+    // A thread keeps its run; its rows (token, head) are `slots` apart.
+    const int run = blockIdx.y * a.block_runs + threadIdx.x % a.block_runs, slot = threadIdx.x / a.block_runs;
+    const int64_t item0 = token0 / a.tokens;
+    const int at0 = (int)(token0 - item0 * a.tokens);
+    const bool turns = run < a.turn_runs;
+    const int second = INTERLEAVED ? 1 : a.pairs;
+    const int d = turns ? (INTERLEAVED ? 2 * P : P) * run : 2 * a.pairs + (run - a.turn_runs) * V;
+    const T *x = (const T *)a.x + d;
+    T *out = (T *)a.out + d;
+    const int step_t = a.slots / a.heads, step_h = a.slots - step_t * a.heads;
+    struct Row {
+        int t, h;
+    };
+    auto advance = [&](Row &r) {
+        r.t += step_t;
+        r.h += step_h;
+        if (r.h >= a.heads) {
+            r.h -= a.heads;
+            ++r.t;
+        }
+    };
+    // Element offset of a row; a block's tokens may run over an item's end.
+    auto offset = [&](const Row &r, int64_t batch, int64_t token, int64_t head) {
+        int64_t b = item0;
+        int at = at0 + r.t;
+        if (at >= a.tokens) {
+            b += at / a.tokens;
+            at %= a.tokens;
+        }
+        return b * batch + at * token + r.h * head;
+    };
+    const bool mine = slot < a.slots && run < a.runs;
+    Row row = {slot / a.heads, slot - slot / a.heads * a.heads};
+    Row rows[kItems];
+    Access u[kItems], v[kItems];
+    auto load = [&] {
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-        const int i = run * P + j;
+        for (int k = 0; k < kItems; ++k) {
+            rows[k] = row;
+            advance(row);
+            if (mine && rows[k].t < count) {
+                const T *from = x + offset(rows[k], a.x_batch, a.x_token, a.x_head);
+                u[k] = *(const Access *)from;
+                if (!kOne && turns) v[k] = *(const Access *)(from + second);
+            }
+        }
+    };
+    load();
+
+    for (int i = threadIdx.x; i < count * a.pairs; i += kRotaryBlock) {
+        const int t = i / a.pairs, j = i - t * a.pairs;
         int axis = 0;
 #pragma unroll
         for (int k = 0; k < GSR_MAX_AXES - 1; ++k)
-            if (k < a.axes - 1 && i >= a.section_end[k]) axis = k + 1;
+            if (k < a.axes - 1 && j >= a.section_end[k]) axis = k + 1;
+        const int64_t at = offset({t, 0}, a.positions_batch, a.axes, 0) + axis;
         float hi, lo = 0.0f;
         if (a.positions_int) {
-            const int p = ((const int *)a.positions)[at + axis];
+            const int p = ((const int *)a.positions)[at];
             hi = (float)p;
-            lo = (float)((double)p - (double)hi);
+            if (abs(p) >= 1 << 24 || p < -(1 << 24)) lo = (float)((long long)p - (long long)hi);
         } else {
-            hi = ((const float *)a.positions)[at + axis];
+            hi = ((const float *)a.positions)[at];
         }
-        sincos_product(hi, lo, a.frequencies[i], &s[j], &c[j]);
-        s[j] *= a.sign;
+        float s, c;
+        sincos_product(hi, lo, a.frequencies[j], &s, &c);
+        s_turn[i] = make_float2(c, s * a.sign);
     }
+    __syncthreads();
 
-    const int first = INTERLEAVED ? run * P * 2 : run * P;
-    const int second = INTERLEAVED ? first + 1 : first + a.pairs;
-    // Vectorised interleaved pairs sit in one access, the others in two.
-    constexpr bool kOne = INTERLEAVED && V > 1;
-    for (int h = head0; h < head1; h += kRotaryHeads) {
-        Access u[kRotaryHeads], v[kRotaryHeads];
+    for (;;) {
 #pragma unroll
-        for (int k = 0; k < kRotaryHeads; ++k)
-            if (h + k < head1) {
-                u[k] = *(const Access *)(x + (h + k) * a.x_head + first);
-                if (!kOne) v[k] = *(const Access *)(x + (h + k) * a.x_head + second);
-            }
-#pragma unroll
-        for (int k = 0; k < kRotaryHeads; ++k)
-            if (h + k < head1) {
+        for (int k = 0; k < kItems; ++k) {
+            if (!mine || rows[k].t >= count) continue;
+            T *to = out + offset(rows[k], a.out_batch, a.out_token, a.out_head);
+            if (turns) {
+                const float2 *turn = s_turn + rows[k].t * a.pairs + run * P;
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
                     T &eu = kOne ? u[k].e[(2 * j) % V] : u[k].e[j % V];
                     T &ev = kOne ? u[k].e[(2 * j + 1) % V] : v[k].e[j % V];
                     const float fu = to_float(eu), fv = to_float(ev);
-                    eu = from_float<T>(fmaf(fu, c[j], -fv * s[j]));
-                    ev = from_float<T>(fmaf(fu, s[j], fv * c[j]));
+                    eu = from_float<T>(fmaf(fu, turn[j].x, -fv * turn[j].y));
+                    ev = from_float<T>(fmaf(fu, turn[j].y, fv * turn[j].x));
                 }
-                *(Access *)(out + (h + k) * a.out_head + first) = u[k];
-                if (!kOne) *(Access *)(out + (h + k) * a.out_head + second) = v[k];
+                if (!kOne) *(Access *)(to + second) = v[k];
             }
+            *(Access *)to = u[k];
+        }
+        if (!mine || row.t >= count) break;
+        load();
     }
 }
 
@@ -136,18 +166,22 @@ cudaError_t launch_rotary(gsr_ctx *ctx, RotaryArgs &a, bool interleaved, int64_t
     const int per_run = interleaved ? (V > 1 ? V / 2 : 1) : V;
     a.turn_runs = a.pairs / per_run;
     a.runs = a.turn_runs + (a.dim - 2 * a.pairs) / V;
-    a.items = tokens * a.runs;
-    const int64_t blocks = (a.items + kRotaryBlock - 1) / kRotaryBlock;
-    // All heads in one thread share its sines and cosines; few tokens spread them
-    // over more blocks so that every SM has work.
-    const int64_t want = (8 * (int64_t)ctx->num_sms + blocks - 1) / blocks;
-    int64_t parts = (a.heads + kRotaryHeads - 1) / kRotaryHeads;
-    if (parts > want) parts = want;
-    a.heads_per_block = (int)((a.heads + parts - 1) / parts);
-    a.heads_per_block = (a.heads_per_block + kRotaryHeads - 1) / kRotaryHeads * kRotaryHeads;
-    const dim3 grid((unsigned)blocks, (unsigned)((a.heads + a.heads_per_block - 1) / a.heads_per_block));
-    if (interleaved) return launch_kernel(ctx, k_rotary<T, V, true>, grid, kRotaryBlock, stream, a);
-    return launch_kernel(ctx, k_rotary<T, V, false>, grid, kRotaryBlock, stream, a);
+    a.all_tokens = tokens;
+    a.block_runs = a.runs < kRotaryBlock ? a.runs : kRotaryBlock;
+    a.slots = kRotaryBlock / a.block_runs;
+    // Tokens of a block: two rounds of loads a thread; fewer where that leaves SMs
+    // idle, and no more angles than the table holds.
+    const int items = interleaved ? kRotaryItems<V, true> : kRotaryItems<V, false>;
+    int64_t n = 2 * items * kRotaryBlock / ((int64_t)a.heads * a.runs);
+    const int64_t spread = (tokens + 2 * ctx->num_sms - 1) / (2 * ctx->num_sms);
+    if (n > spread) n = spread;
+    if (a.pairs > 0 && n > kRotaryTable / a.pairs) n = kRotaryTable / a.pairs;
+    a.block_tokens = (int)(n < 1 ? 1 : n);
+    const dim3 grid((unsigned)((tokens + a.block_tokens - 1) / a.block_tokens),
+                    (unsigned)((a.runs + a.block_runs - 1) / a.block_runs));
+    const size_t table = (size_t)a.block_tokens * a.pairs * sizeof(float2);
+    if (interleaved) return launch_kernel_smem(ctx, k_rotary<T, V, true>, grid, kRotaryBlock, table, stream, a);
+    return launch_kernel_smem(ctx, k_rotary<T, V, false>, grid, kRotaryBlock, table, stream, a);
 }
 
 // Largest access of at most 16 bytes that divides every offset the kernel forms.

@@ -468,7 +468,8 @@ typedef struct gsr_heads {
  *   frequencies  device, [sum(sections)] float
  *   x, out       out may be x itself (same data and strides)
  * The angle's product is kept to twice float's length before its sine and
- * cosine, so long positions lose nothing.
+ * cosine: positions of up to 2^24 in magnitude lose nothing, larger int32 ones a
+ * few 1e-6 of the angle.
  * Errors: GSR_ERR_INVALID_ARG (null or misaligned arrays; negative sizes;
  * sizes above GSR_MAX_TOKENS, GSR_MAX_HEADS, GSR_MAX_HEAD_DIM; pairs beyond
  * head_dim; out with a stride of 0 over more than one item), GSR_ERR_CUDA. */
