@@ -175,6 +175,12 @@ struct Packed {
     int32_t *index;          // [batch, kv_len]
 };
 
+// Query rows that the kernel for few rows takes (attention_few.cu): the tokens of
+// all query heads of a key head.
+constexpr int kFewRows = 16;
+int few_rows_forward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr_heads &k, const gsr_heads &v,
+                     const gsr_heads &out, float *lse, cudaStream_t stream);
+
 size_t packed_bytes(const gsr_attention &d);
 cudaError_t pack_keys(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &k, const gsr_heads &v, void *work,
                       Packed *out, cudaStream_t stream);

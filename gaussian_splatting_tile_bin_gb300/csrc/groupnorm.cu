@@ -13,8 +13,8 @@
 //     shared memory between the statistics and the result, one kernel and one
 //     read of the inputs.  For slabs that a cluster holds.
 //   - passes: a pass that reduces over the positions per channel, a small kernel
-//     that merges the blocks' partial sums into groups, and a pass that writes,
-//     over waves of samples whose inputs stay in L2 for the second pass.
+//     that merges the blocks' partial sums into groups, and a pass that writes
+//     and walks back, from what L2 still holds of the first.
 //
 // Numerics.  The variance is a merge of centred squares: a thread takes the mean
 // and the centred squares of kRun values at a time and merges (n, mean, M2)
@@ -30,10 +30,10 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kNormBlock = 256;
-constexpr int kRun = 4;          // positions a thread reads at a time
+constexpr int kRun = 8;          // positions a thread reads at a time
 constexpr int kMergeBlock = 256;
 // Blocks an SM holds: one wave of them takes all chunks.
-constexpr int kNormOccupancy = 4, kNormGradOccupancy = 3;
+constexpr int kNormOccupancy = 3, kNormGradOccupancy = 2;
 
 // Accesses that nothing follows: the result, and the second pass' inputs.
 template <typename T, int V>
@@ -343,10 +343,9 @@ __device__ __forceinline__ void input_gradient(const Channel<V> &c, const float2
 }
 
 // Walks a thread's rows p0 + row, + rows, ... below p1, kUnroll at a time.
-constexpr int kUnroll = 4;
+constexpr int kUnroll = 8;
 
-// out = act((x - mean) rstd w + b).  Blocks take the chunks from the last to the
-// first: what the moments pass read last is what L2 still holds.
+// out = act((x - mean) rstd w + b).
 template <typename T, int V, int ACT>
 __global__ void __launch_bounds__(kNormBlock, kNormOccupancy) k_norm_apply(const NormArgs a)
 {
@@ -355,8 +354,8 @@ __global__ void __launch_bounds__(kNormBlock, kNormOccupancy) k_norm_apply(const
     const int col = threadIdx.x % cols, row = threadIdx.x / cols, rows = kNormBlock / cols;
     const int vec = blockIdx.z * cols + col;
     if (row >= rows || vec * V >= a.channels) return;
-    const int local = gridDim.y - 1 - blockIdx.y, sample = a.sample0 + local;
-    const int64_t p0 = (int64_t)(gridDim.x - 1 - blockIdx.x) * a.rows_per_chunk;
+    const int sample = a.sample0 + blockIdx.y;
+    const int64_t p0 = (int64_t)blockIdx.x * a.rows_per_chunk;
     const int64_t p1 = min(a.positions, p0 + a.rows_per_chunk);
     Affine<V> affine;
     {
@@ -364,11 +363,14 @@ __global__ void __launch_bounds__(kNormBlock, kNormOccupancy) k_norm_apply(const
         ch.load(a, sample, vec * V);
         affine.from(ch);
     }
-    const int64_t first = ((int64_t)sample * a.positions + p0 + row) * a.channels + (int64_t)vec * V;
-    const int64_t stride = (int64_t)rows * a.channels;
+    if (p0 + row >= p1) return;
+    // From the last row back: what the first pass read last is what L2 still holds.
+    int left = (int)((p1 - p0 - row + rows - 1) / rows);   // rows of this thread
+    const int64_t first = ((int64_t)sample * a.positions + p0 + row + (int64_t)(left - 1) * rows) * a.channels +
+                          (int64_t)vec * V;
+    const int64_t stride = -(int64_t)rows * a.channels;
     const T *x = (const T *)a.x + first;
     T *y = (T *)a.y + first;
-    int left = (int)((p1 - p0 - row + rows - 1) / rows);   // rows of this thread
     for (; left >= kUnroll; left -= kUnroll, x += kUnroll * stride, y += kUnroll * stride) {
         Vec<T, V> v[kUnroll];
 #pragma unroll
@@ -508,8 +510,8 @@ __global__ void __launch_bounds__(kNormBlock, kNormGradOccupancy) k_norm_grad_ap
     const int col = threadIdx.x % cols, row = threadIdx.x / cols, rows = kNormBlock / cols;
     const int vec = blockIdx.z * cols + col;
     if (row >= rows || vec * V >= a.channels) return;
-    const int local = gridDim.y - 1 - blockIdx.y, sample = a.sample0 + local;
-    const int64_t p0 = (int64_t)(gridDim.x - 1 - blockIdx.x) * a.rows_per_chunk;
+    const int sample = a.sample0 + blockIdx.y;
+    const int64_t p0 = (int64_t)blockIdx.x * a.rows_per_chunk;
     const int64_t p1 = min(a.positions, p0 + a.rows_per_chunk);
     Channel<V> ch;
     ch.load(a, sample, vec * V);
@@ -520,11 +522,13 @@ __global__ void __launch_bounds__(kNormBlock, kNormGradOccupancy) k_norm_grad_ap
         (&m1[j / 2].x)[j % 2] = m.x;
         (&m2[j / 2].x)[j % 2] = m.y;
     }
-    const int64_t first = ((int64_t)sample * a.positions + p0 + row) * a.channels + (int64_t)vec * V;
-    const int64_t stride = (int64_t)rows * a.channels;
+    if (p0 + row >= p1) return;
+    int left = (int)((p1 - p0 - row + rows - 1) / rows);
+    const int64_t first = ((int64_t)sample * a.positions + p0 + row + (int64_t)(left - 1) * rows) * a.channels +
+                          (int64_t)vec * V;
+    const int64_t stride = -(int64_t)rows * a.channels;
     const T *x = (const T *)a.x + first, *dout = (const T *)a.dout + first;
     T *y = (T *)a.y + first;
-    int left = (int)((p1 - p0 - row + rows - 1) / rows);
     constexpr int kTwo = kUnroll / 2;   // two inputs and twice the constants: half the rows at a time
     for (; left >= kTwo; left -= kTwo, x += kTwo * stride, dout += kTwo * stride, y += kTwo * stride) {
         Vec<T, V> vx[kTwo], vd[kTwo];
@@ -884,13 +888,7 @@ NormPlan norm_plan(const gsr_ctx *ctx, const gsr_group_norm &d, int width, bool 
     p.vectors = vectors < kNormBlock ? vectors : kNormBlock;
     p.slabs = (vectors + p.vectors - 1) / p.vectors;
     const int rows = kNormBlock / p.vectors;
-    // A wave of samples whose arrays stay in L2 between the two passes over them.
-    const int64_t sample_bytes = d.positions * d.channels * (d.dtype == GSR_F32 ? 4 : 2) * (backward ? 2 : 1);
-    constexpr int64_t kL2Share = (int64_t)96 << 20;
-    int64_t wave = kL2Share / (sample_bytes > 0 ? sample_bytes : 1);
-    wave = wave < 1 ? 1 : wave;
-    p.wave = (int)(wave < d.samples ? wave : d.samples);
-    if (p.wave > 65535) p.wave = 65535;
+    p.wave = d.samples < 65535 ? d.samples : 65535;   // samples of a launch (a grid's limit)
     int64_t chunks = (int64_t)(backward ? kNormGradOccupancy : kNormOccupancy) * ctx->num_sms / ((int64_t)p.wave * p.slabs);
     const int64_t most = (d.positions + (int64_t)rows * kRun - 1) / ((int64_t)rows * kRun);
     if (chunks > most) chunks = most;
