@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -43,32 +44,16 @@ class _Camera(ctypes.Structure):
     _fields_ = [("v", ctypes.c_float * CAMERA_FIELDS)]
 
 
-class _GroupNorm(ctypes.Structure):
-    _fields_ = [("dtype", ctypes.c_int32), ("samples", ctypes.c_int32), ("channels", ctypes.c_int32),
-                ("groups", ctypes.c_int32), ("positions", ctypes.c_int64), ("activation", ctypes.c_int32),
-                ("eps", ctypes.c_float)]
-
-
-class _Heads(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
-                ("head_stride", ctypes.c_int64)]
-
-
+# gsr_group_norm, gsr_heads, gsr_rotary and gsr_attention, packed per call: an
+# order of magnitude quicker than filling ctypes structures, which these calls of
+# a few microseconds would notice.
 MAX_AXES = 4
-
-
-class _Rotary(ctypes.Structure):
-    _fields_ = [("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("tokens", ctypes.c_int32),
-                ("heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
-                ("axes", ctypes.c_int32), ("sections", ctypes.c_int32 * MAX_AXES),
-                ("positions_int", ctypes.c_int32), ("positions_batch_stride", ctypes.c_int64)]
-
-
-class _Attention(ctypes.Structure):
-    _fields_ = [("dtype", ctypes.c_int32), ("batch", ctypes.c_int32), ("q_len", ctypes.c_int32),
-                ("kv_len", ctypes.c_int32), ("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
-                ("head_dim", ctypes.c_int32), ("scale", ctypes.c_float), ("kv_lengths", ctypes.c_void_p),
-                ("key_mask", ctypes.c_void_p)]
+GROUP_NORM = struct.Struct("@4iqif")   # dtype, samples, channels, groups, positions, activation, eps
+HEADS = struct.Struct("@P3q")          # data, batch, token and head strides
+ROTARY = struct.Struct("@12iq")        # dtype, batch, tokens, heads, head_dim, interleaved, axes, sections[4],
+                                       # positions_int, positions_batch_stride
+ATTENTION = struct.Struct("@7if2P")    # dtype, batch, q_len, kv_len, q_heads, kv_heads, head_dim, scale,
+                                       # kv_lengths, key_mask
 
 
 class _BinStats(ctypes.Structure):
@@ -114,18 +99,11 @@ def _load():
     lib.gsr_exp_neg.restype = ctypes.c_int
     lib.gsr_peak_kernel.argtypes = [P, ctypes.c_int, i32, P, ctypes.POINTER(ctypes.c_uint64), P]
     lib.gsr_peak_kernel.restype = ctypes.c_int
-    norm, rotary, attention, heads = (ctypes.POINTER(t) for t in (_GroupNorm, _Rotary, _Attention, _Heads))
-    lib.gsr_group_norm_forward.argtypes = [P, norm] + [P] * 7
-    lib.gsr_group_norm_forward.restype = ctypes.c_int
-    lib.gsr_group_norm_backward.argtypes = [P, norm] + [P] * 10
-    lib.gsr_group_norm_backward.restype = ctypes.c_int
-    for name in ("gsr_rotary_forward", "gsr_rotary_backward"):
-        getattr(lib, name).argtypes = [P, rotary, heads, P, P, heads, P]
+    for name, pointers in (("gsr_group_norm_forward", 9), ("gsr_group_norm_backward", 12), ("gsr_rotary_forward", 7),
+                           ("gsr_rotary_backward", 7), ("gsr_cross_attention_forward", 8),
+                           ("gsr_cross_attention_backward", 12)):
+        getattr(lib, name).argtypes = [P] * pointers
         getattr(lib, name).restype = ctypes.c_int
-    lib.gsr_cross_attention_forward.argtypes = [P, attention] + [heads] * 4 + [P, P]
-    lib.gsr_cross_attention_forward.restype = ctypes.c_int
-    lib.gsr_cross_attention_backward.argtypes = [P, attention] + [heads] * 4 + [P] + [heads] * 4 + [P]
-    lib.gsr_cross_attention_backward.restype = ctypes.c_int
     return lib
 
 
@@ -395,40 +373,73 @@ def project_backward(ctx: Context, gauss: torch.Tensor, camera, dl_dsplat: torch
 
 
 # -- the operators of an image-to-Gaussians decoder ---------------------------
+#
+# The smallest of these calls are bound by the host, so the checks test the usual
+# case in one condition and look for the reason only when it fails.
 
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2}
+_F32 = torch.float32
+_HALVES = (torch.bfloat16, torch.float16)
 
 
-def _dtype(t: torch.Tensor, name, among):
+def _first(t, name, among):
+    """Checks the tensor that decides a call's dtype and device; returns the device's index."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in among:
         raise ValueError(f"{name} must be one of {', '.join(map(str, among))}, got {t.dtype}")
-    return t.dtype
+    return t.get_device()
 
 
-def _heads(t: torch.Tensor, name, dtype, shape, device) -> _Heads:
-    """A [batch, tokens, heads, head_dim] tensor, any strides but a contiguous last dimension."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
-        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+def _refuse(t, name, dtype, shape, index):
+    if not isinstance(t, torch.Tensor) or t.get_device() != index:
+        raise ValueError(f"{name} must be a CUDA tensor on cuda:{index}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.shape[3] > 1 and t.stride(3) != 1:
+
+
+def _array(t, name, dtype, shape, index):
+    """The address of a contiguous tensor."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index):
+        _refuse(t, name, dtype, shape, index)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _heads(t, name, dtype, shape, index):
+    """A packed gsr_heads of a [batch, tokens, heads, head_dim] tensor, any strides
+    but a contiguous last dimension."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index):
+        _refuse(t, name, dtype, shape, index)
+    return _strides(t, name)
+
+
+def _strides(t, name):
+    batch, token, head, last = t.stride()
+    if last != 1 and t.shape[3] > 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
-    return _Heads(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+    return HEADS.pack(t.data_ptr(), batch, token, head)
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}, got {t.device}")
+def _heads_out(t, name, dtype, shape, index, device, stream):
+    """An output [batch, tokens, heads, head_dim], made if None, and its packed gsr_heads."""
+    if t is not None:
+        return t, _heads(t, name, dtype, shape, index)
+    t = _new(shape, dtype, device, stream)
+    _, tokens, heads, dim = shape
+    return t, HEADS.pack(t.data_ptr(), tokens * heads * dim, heads * dim, dim)
 
 
-def _ptr(t):
-    return ctypes.c_void_p(None if t is None else t.data_ptr())
+def _array_out(t, name, dtype, shape, index, device, stream):
+    """A contiguous output, made if None, and its address."""
+    if t is not None:
+        return t, _array(t, name, dtype, shape, index)
+    t = _new(shape, dtype, device, stream)
+    return t, t.data_ptr()
 
 
 def _new(shape, dtype, device, stream):
@@ -442,16 +453,25 @@ def _new(shape, dtype, device, stream):
     return t
 
 
+# The current stream's handle without a Stream object around it, where torch has it.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _raw_stream(stream, index):
+    return _current_raw_stream(index) if stream is None else stream.cuda_stream
+
+
 def _norm_desc(x, groups, eps, activation):
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}, got {activation!r}")
-    if x.dim() < 2:
-        raise ValueError(f"x must have shape [samples, ..., channels], got {tuple(x.shape)}")
+    shape = x.shape
+    if len(shape) < 2:
+        raise ValueError(f"x must have shape [samples, ..., channels], got {tuple(shape)}")
     positions = 1
-    for extent in x.shape[1:-1]:
+    for extent in shape[1:-1]:
         positions *= extent
-    return _GroupNorm(DTYPES[x.dtype], x.shape[0], x.shape[-1], int(groups), positions, ACTIVATIONS[activation],
-                      float(eps))
+    return GROUP_NORM.pack(DTYPES[x.dtype], shape[0], shape[-1], groups, positions, ACTIVATIONS[activation], eps)
 
 
 def group_norm_forward(ctx: Context, x: torch.Tensor, groups: int, weight=None, bias=None, eps: float = 1e-5,
@@ -460,25 +480,18 @@ def group_norm_forward(ctx: Context, x: torch.Tensor, groups: int, weight=None, 
     (f32, bf16 or f16; weight and bias [channels] f32 or None).  `activation` is
     "none", "silu" or "gelu".  Returns (out, mean, rstd), the last two
     [samples, groups] f32 for the backward.  out may be x."""
-    dtype = _dtype(x, "x", DTYPES)
-    _need(x, "x", dtype)
-    desc, dev, c = _norm_desc(x, groups, eps, activation), x.device, x.shape[-1]
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None:
-            _need(t, name, torch.float32, (c,))
-    stats = (x.shape[0], int(groups))
-    if out is None:
-        out = _new(x.shape, dtype, dev, stream)
-    if mean is None:
-        mean = _new(stats, torch.float32, dev, stream)
-    if rstd is None:
-        rstd = _new(stats, torch.float32, dev, stream)
-    _need(out, "out", dtype, x.shape)
-    _need(mean, "mean", torch.float32, stats)
-    _need(rstd, "rstd", torch.float32, stats)
-    _same_device(dev, weight=weight, bias=bias, out=out, mean=mean, rstd=rstd)
-    ctx._check(lib.gsr_group_norm_forward(ctx._h, ctypes.byref(desc), _ptr(x), _ptr(weight), _ptr(bias), _ptr(out),
-                                          _ptr(mean), _ptr(rstd), _stream_ptr(stream, dev)))
+    index = _first(x, "x", DTYPES)
+    dtype, shape, dev = x.dtype, x.shape, x.device
+    desc = _norm_desc(x, groups, eps, activation)
+    channels, stats = shape[-1:], (shape[0], max(int(groups), 0))
+    out, at_out = _array_out(out, "out", dtype, shape, index, dev, stream)
+    mean, at_mean = _array_out(mean, "mean", _F32, stats, index, dev, stream)
+    rstd, at_rstd = _array_out(rstd, "rstd", _F32, stats, index, dev, stream)
+    ctx._check(lib.gsr_group_norm_forward(
+        ctx._h, desc, _array(x, "x", dtype, shape, index),
+        None if weight is None else _array(weight, "weight", _F32, channels, index),
+        None if bias is None else _array(bias, "bias", _F32, channels, index), at_out, at_mean, at_rstd,
+        _raw_stream(stream, index)))
     return out, mean, rstd
 
 
@@ -487,30 +500,19 @@ def group_norm_backward(ctx: Context, dl_dout: torch.Tensor, x: torch.Tensor, gr
                         dl_dweight=None, dl_dbias=None, stream=None):
     """Returns (dL/dx as x, dL/dweight [channels] f32, dL/dbias [channels] f32) for
     dL/dout, with the forward's x, weight, bias, mean and rstd.  dl_dx may be dl_dout."""
-    dtype = _dtype(x, "x", DTYPES)
-    _need(x, "x", dtype)
-    _need(dl_dout, "dl_dout", dtype, x.shape)
-    desc, dev, c = _norm_desc(x, groups, 1.0, activation), x.device, x.shape[-1]
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None:
-            _need(t, name, torch.float32, (c,))
-    stats = (x.shape[0], int(groups))
-    _need(mean, "mean", torch.float32, stats)
-    _need(rstd, "rstd", torch.float32, stats)
-    if dl_dx is None:
-        dl_dx = _new(x.shape, dtype, dev, stream)
-    if dl_dweight is None:
-        dl_dweight = _new((c,), torch.float32, dev, stream)
-    if dl_dbias is None:
-        dl_dbias = _new((c,), torch.float32, dev, stream)
-    _need(dl_dx, "dl_dx", dtype, x.shape)
-    _need(dl_dweight, "dl_dweight", torch.float32, (c,))
-    _need(dl_dbias, "dl_dbias", torch.float32, (c,))
-    _same_device(dev, dl_dout=dl_dout, weight=weight, bias=bias, mean=mean, rstd=rstd, dl_dx=dl_dx,
-                 dl_dweight=dl_dweight, dl_dbias=dl_dbias)
-    ctx._check(lib.gsr_group_norm_backward(ctx._h, ctypes.byref(desc), _ptr(dl_dout), _ptr(x), _ptr(weight),
-                                           _ptr(bias), _ptr(mean), _ptr(rstd), _ptr(dl_dx), _ptr(dl_dweight),
-                                           _ptr(dl_dbias), _stream_ptr(stream, dev)))
+    index = _first(x, "x", DTYPES)
+    dtype, shape, dev = x.dtype, x.shape, x.device
+    desc = _norm_desc(x, groups, 1.0, activation)
+    channels, stats = shape[-1:], (shape[0], int(groups))
+    dl_dx, at_dx = _array_out(dl_dx, "dl_dx", dtype, shape, index, dev, stream)
+    dl_dweight, at_dweight = _array_out(dl_dweight, "dl_dweight", _F32, channels, index, dev, stream)
+    dl_dbias, at_dbias = _array_out(dl_dbias, "dl_dbias", _F32, channels, index, dev, stream)
+    ctx._check(lib.gsr_group_norm_backward(
+        ctx._h, desc, _array(dl_dout, "dl_dout", dtype, shape, index), _array(x, "x", dtype, shape, index),
+        None if weight is None else _array(weight, "weight", _F32, channels, index),
+        None if bias is None else _array(bias, "bias", _F32, channels, index),
+        _array(mean, "mean", _F32, stats, index), _array(rstd, "rstd", _F32, stats, index), at_dx, at_dweight,
+        at_dbias, _raw_stream(stream, index)))
     return dl_dx, dl_dweight, dl_dbias
 
 
@@ -522,29 +524,26 @@ def rotary_frequencies(sections, base: float = 10000.0, device="cuda") -> torch.
 
 
 def _rotary(call, name, ctx, x, positions, frequencies, sections, interleaved, out, out_name, stream):
-    dtype = _dtype(x, name, DTYPES)
-    if x.dim() != 4:
-        raise ValueError(f"{name} must have shape [batch, tokens, heads, head_dim], got {tuple(x.shape)}")
-    dev, (batch, tokens, heads, dim) = x.device, x.shape
-    sections = [int(s) for s in sections]
-    if not 1 <= len(sections) <= MAX_AXES:
-        raise ValueError(f"sections must hold 1 to {MAX_AXES} numbers of pairs, got {len(sections)}")
-    _need(frequencies, "frequencies", torch.float32, (sum(sections),))
-    _dtype(positions, "positions", (torch.int32, torch.float32))
-    shapes = ((tokens, len(sections)), (batch, tokens, len(sections)))
-    if tuple(positions.shape) not in shapes:
-        raise ValueError(f"positions must have shape {shapes[0]} or {shapes[1]}, got {tuple(positions.shape)}")
-    _need(positions, "positions", positions.dtype)
-    _same_device(dev, positions=positions, frequencies=frequencies)
-    src = _heads(x, name, dtype, x.shape, dev)
-    if out is None:
-        out = _new(x.shape, dtype, dev, stream)
-    dst = _heads(out, out_name, dtype, x.shape, dev)
-    desc = _Rotary(DTYPES[dtype], batch, tokens, heads, dim, int(bool(interleaved)), len(sections),
-                   (ctypes.c_int32 * MAX_AXES)(*sections), int(positions.dtype == torch.int32),
-                   tokens * len(sections) if positions.dim() == 3 else 0)
-    ctx._check(call(ctx._h, ctypes.byref(desc), ctypes.byref(src), _ptr(positions), _ptr(frequencies),
-                    ctypes.byref(dst), _stream_ptr(stream, dev)))
+    index = _first(x, name, DTYPES)
+    dtype, shape = x.dtype, x.shape
+    if len(shape) != 4:
+        raise ValueError(f"{name} must have shape [batch, tokens, heads, head_dim], got {tuple(shape)}")
+    batch, tokens, heads, dim = shape
+    axes = len(sections)
+    if not 1 <= axes <= MAX_AXES:
+        raise ValueError(f"sections must hold 1 to {MAX_AXES} numbers of pairs, got {axes}")
+    at_frequencies = _array(frequencies, "frequencies", _F32, (sum(sections),), index)
+    _first(positions, "positions", (torch.int32, torch.float32))
+    each = len(positions.shape) == 3
+    if positions.shape != ((batch, tokens, axes) if each else (tokens, axes)):
+        raise ValueError(f"positions must have shape {(tokens, axes)} or {(batch, tokens, axes)}, "
+                         f"got {tuple(positions.shape)}")
+    at_positions = _array(positions, "positions", positions.dtype, positions.shape, index)
+    out, at_out = _heads_out(out, out_name, dtype, shape, index, x.device, stream)
+    desc = ROTARY.pack(DTYPES[dtype], batch, tokens, heads, dim, bool(interleaved), axes, *sections,
+                       *(0,) * (MAX_AXES - axes), positions.dtype is torch.int32, tokens * axes if each else 0)
+    ctx._check(call(ctx._h, desc, _strides(x, name), at_positions, at_frequencies, at_out,
+                    _raw_stream(stream, index)))
     return out
 
 
@@ -566,24 +565,25 @@ def rotary_backward(ctx: Context, dl_dout: torch.Tensor, positions: torch.Tensor
                    dl_dx, "dl_dx", stream)
 
 
-def _attention_desc(q, k, v, kv_lengths, key_mask, scale):
-    dtype = _dtype(q, "q", (torch.bfloat16, torch.float16))
-    if q.dim() != 4 or not isinstance(k, torch.Tensor) or k.dim() != 4:
+def _attention(q, k, v, kv_lengths, key_mask, scale):
+    """The packed description and q, k, v; the device's index and k's shape."""
+    index = _first(q, "q", _HALVES)
+    dtype, shape = q.dtype, q.shape
+    if len(shape) != 4 or not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("q, k and v must have shape [batch, tokens, heads, head_dim]")
-    batch, q_len, q_heads, dim = q.shape
-    kv_len, kv_heads = k.shape[1], k.shape[2]
-    dev = q.device
-    if kv_lengths is not None:
-        _need(kv_lengths, "kv_lengths", torch.int32, (batch,))
-    if key_mask is not None:
-        _dtype(key_mask, "key_mask", (torch.bool, torch.uint8))
-        _need(key_mask, "key_mask", key_mask.dtype, (batch, kv_len))
-    _same_device(dev, kv_lengths=kv_lengths, key_mask=key_mask)
-    desc = _Attention(DTYPES[dtype], batch, q_len, kv_len, q_heads, kv_heads, dim,
-                      float(dim ** -0.5 if scale is None else scale), _ptr(kv_lengths), _ptr(key_mask))
+    batch, q_len, q_heads, dim = shape
+    kv_len, kv_heads = k.shape[1:3]
     keys = (batch, kv_len, kv_heads, dim)
-    return desc, dtype, dev, keys, [_heads(q, "q", dtype, q.shape, dev), _heads(k, "k", dtype, keys, dev),
-                                    _heads(v, "v", dtype, keys, dev)]
+    at_lengths = at_mask = 0
+    if kv_lengths is not None:
+        at_lengths = _array(kv_lengths, "kv_lengths", torch.int32, (batch,), index)
+    if key_mask is not None:
+        _first(key_mask, "key_mask", (torch.bool, torch.uint8))
+        at_mask = _array(key_mask, "key_mask", key_mask.dtype, (batch, kv_len), index)
+    desc = ATTENTION.pack(DTYPES[dtype], batch, q_len, kv_len, q_heads, kv_heads, dim,
+                          dim ** -0.5 if scale is None else scale, at_lengths, at_mask)
+    return index, keys, desc, _strides(q, "q"), _heads(k, "k", dtype, keys, index), \
+        _heads(v, "v", dtype, keys, index)
 
 
 def cross_attention_forward(ctx: Context, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, kv_lengths=None,
@@ -594,17 +594,13 @@ def cross_attention_forward(ctx: Context, q: torch.Tensor, k: torch.Tensor, v: t
     (bool or uint8) is 0, take no part; a row without any gives 0 and lse -inf.
     `scale` defaults to head_dim ** -0.5.  Returns (out as q, lse [batch, q_heads,
     q_len] f32)."""
-    desc, dtype, dev, _, (hq, hk, hv) = _attention_desc(q, k, v, kv_lengths, key_mask, scale)
-    rows = (q.shape[0], q.shape[2], q.shape[1])
-    if out is None:
-        out = _new(q.shape, dtype, dev, stream)
-    if lse is None:
-        lse = _new(rows, torch.float32, dev, stream)
-    ho = _heads(out, "out", dtype, q.shape, dev)
-    _need(lse, "lse", torch.float32, rows)
-    _same_device(dev, lse=lse)
-    ctx._check(lib.gsr_cross_attention_forward(ctx._h, ctypes.byref(desc), *map(ctypes.byref, (hq, hk, hv, ho)),
-                                               _ptr(lse), _stream_ptr(stream, dev)))
+    index, _, desc, at_q, at_k, at_v = _attention(q, k, v, kv_lengths, key_mask, scale)
+    dtype, shape = q.dtype, q.shape
+    rows = (shape[0], shape[2], shape[1])
+    out, at_out = _heads_out(out, "out", dtype, shape, index, q.device, stream)
+    lse, at_lse = _array_out(lse, "lse", _F32, rows, index, q.device, stream)
+    ctx._check(lib.gsr_cross_attention_forward(ctx._h, desc, at_q, at_k, at_v, at_out, at_lse,
+                                               _raw_stream(stream, index)))
     return out, lse
 
 
@@ -613,19 +609,13 @@ def cross_attention_backward(ctx: Context, q: torch.Tensor, k: torch.Tensor, v: 
                              dl_dq=None, dl_dk=None, dl_dv=None, stream=None):
     """Returns (dL/dq, dL/dk, dL/dv) for dL/dout, with the forward's arguments, out
     and lse.  Keys that took no part get zeros."""
-    desc, dtype, dev, keys, (hq, hk, hv) = _attention_desc(q, k, v, kv_lengths, key_mask, scale)
-    _need(lse, "lse", torch.float32, (q.shape[0], q.shape[2], q.shape[1]))
-    _same_device(dev, lse=lse)
-    if dl_dq is None:
-        dl_dq = _new(q.shape, dtype, dev, stream)
-    if dl_dk is None:
-        dl_dk = _new(keys, dtype, dev, stream)
-    if dl_dv is None:
-        dl_dv = _new(keys, dtype, dev, stream)
-    ho, hd = _heads(out, "out", dtype, q.shape, dev), _heads(dl_dout, "dl_dout", dtype, q.shape, dev)
-    gq = _heads(dl_dq, "dl_dq", dtype, q.shape, dev)
-    gk, gv = _heads(dl_dk, "dl_dk", dtype, keys, dev), _heads(dl_dv, "dl_dv", dtype, keys, dev)
+    index, keys, desc, at_q, at_k, at_v = _attention(q, k, v, kv_lengths, key_mask, scale)
+    dtype, shape, dev = q.dtype, q.shape, q.device
+    dl_dq, at_dq = _heads_out(dl_dq, "dl_dq", dtype, shape, index, dev, stream)
+    dl_dk, at_dk = _heads_out(dl_dk, "dl_dk", dtype, keys, index, dev, stream)
+    dl_dv, at_dv = _heads_out(dl_dv, "dl_dv", dtype, keys, index, dev, stream)
     ctx._check(lib.gsr_cross_attention_backward(
-        ctx._h, ctypes.byref(desc), *map(ctypes.byref, (hq, hk, hv, ho)), _ptr(lse),
-        *map(ctypes.byref, (hd, gq, gk, gv)), _stream_ptr(stream, dev)))
+        ctx._h, desc, at_q, at_k, at_v, _heads(out, "out", dtype, shape, index),
+        _array(lse, "lse", _F32, (shape[0], shape[2], shape[1]), index),
+        _heads(dl_dout, "dl_dout", dtype, shape, index), at_dq, at_dk, at_dv, _raw_stream(stream, index)))
     return dl_dq, dl_dk, dl_dv
