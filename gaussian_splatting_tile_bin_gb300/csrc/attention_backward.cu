@@ -29,7 +29,10 @@ namespace gsr {
 namespace {
 
 constexpr int kRowTile = 128;
-constexpr int kBackwardThreads = 384;   // two groups of 128 that compute; four warps of which one copies and one issues
+constexpr int kGroups = 2;              // warpgroups that compute, each its share of the columns of S and dP
+constexpr int kColumnsEach = 128 / kGroups;
+constexpr int kComputeWarps = 4 * kGroups;
+constexpr int kBackwardThreads = 128 * kGroups + 128;   // and four warps of which one copies and one issues
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Powers that keep f16 p and ds in range.
@@ -41,7 +44,7 @@ struct RangeShift {
 struct BackwardArgs {
     CUtensorMap q, k, v, dout;
     Schedule work;
-    const float *lse2, *delta;   // [batch, q_heads, q_pad]: lse log2e - log2(shift.p), delta shift.ds / shift.p
+    const float *lse2, *delta;   // [batch, q_heads, q_pad]: log2(shift.p) - lse log2e, -delta shift.ds / shift.p
     const RangeShift *shift;
     void *dq, *dk, *dv;
     int64_t dq_item, dq_token, dq_head, dk_item, dk_token, dk_head, dv_item, dv_token, dv_head;
@@ -95,8 +98,8 @@ struct Bars {
         }
         barrier_init(s, 1);
         barrier_init(dp, 1);
-        barrier_init(s_read, 8);
-        barrier_init(ready, 8);
+        barrier_init(s_read, kComputeWarps);
+        barrier_init(ready, kComputeWarps);
         barrier_init(done, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async();
@@ -110,15 +113,29 @@ __device__ __forceinline__ void copy_bytes(uint32_t to, const void *from, uint32
                  : "memory");
 }
 
-// 64 columns of this thread's lane.
-__device__ __forceinline__ void load64(uint32_t (&r)[64], uint32_t at)
+using Columns = uint32_t[kColumnsEach];
+
+// This thread's columns of its lane.
+__device__ __forceinline__ void load_columns(Columns &r, uint32_t at)
 {
-    tmem_load32(*(uint32_t(*)[32])&r[0], at);
-    tmem_load32(*(uint32_t(*)[32])&r[32], at + 32);
+#pragma unroll
+    for (int x = 0; x < kColumnsEach; x += 32) tmem_load32(*(uint32_t(*)[32])&r[x], at + x);
     tmem_wait_load();
 }
 
-__device__ __forceinline__ float2 pair(const uint32_t (&r)[64], int i)
+// Their 16-bit pairs.
+__device__ __forceinline__ void store_pairs(uint32_t at, const uint32_t (&r)[32])
+{
+    tmem_store32(at, r);
+    tmem_wait_store();
+}
+__device__ __forceinline__ void store_pairs(uint32_t at, const uint32_t (&r)[16])
+{
+    tmem_store16(at, r);
+    tmem_wait_store();
+}
+
+__device__ __forceinline__ float2 pair(const Columns &r, int i)
 {
     return make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
 }
@@ -146,7 +163,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
         s_words[1] = 0;
         bar.init();
     }
-    if (warp == 9) tmem_alloc(tail, S::kColumns);
+    if (warp == kComputeWarps + 1) tmem_alloc(tail, S::kColumns);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
@@ -154,9 +171,9 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
     Walk<QueryLine> walk = walk_share<QueryLine>(a.work);
     Segment g;
 
-    if (warp >= 8) {
-        give_registers();
-        if (warp == 8 && elect_one()) {
+    if (warp >= kComputeWarps) {
+        give_registers<kGroups>();
+        if (warp == kComputeWarps && elect_one()) {
             uint32_t n = 0, seg = 0;
             while (walk.next(g)) {
                 if (g.length == 0) continue;
@@ -181,7 +198,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                     }
                 ++seg;
             }
-        } else if (warp == 9) {
+        } else if (warp == kComputeWarps + 1) {
             const bool leader = elect_one();
             const uint32_t form_s = product_form<T>(kKeyTile, false);
             const uint32_t form_o = product_form<T>((a.dim + 15) & ~15, true);
@@ -229,10 +246,10 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
             }
         }
     } else {
-        take_registers();
-        const int half = warp / 4;                                  // columns 64 half .. of S and dP
+        take_registers<kGroups>();
+        const int part = warp / 4, column0 = part * kColumnsEach;   // columns of S and dP
         const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
-        const uint32_t at_s = tmem + lanes + S::kS + half * 64, at_dp = tmem + lanes + S::kDp + half * 64;
+        const uint32_t at_s = tmem + lanes + S::kS + column0, at_dp = tmem + lanes + S::kDp + column0;
         const int row_in_tile = warp % 4 * 32 + lane;
         const float c = a.scale_log2;
         const RangeShift shift = *a.shift;
@@ -244,36 +261,36 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
             if (g.length > 0) {
                 const int64_t at = ((int64_t)g.item * a.q_heads + head) * a.q_pad + row;
                 const float2 c2 = make_float2(c, c), f2 = make_float2(f_dp, f_dp);
-                const float lse = -a.lse2[at], delta = -a.delta[at];
+                const float lse = a.lse2[at], delta = a.delta[at];
                 const float2 lse2 = make_float2(lse, lse), delta2 = make_float2(delta, delta);
                 for (int i = g.begin; i < g.end; ++i, n += 2, ++step) {
-                    uint32_t r[64];
+                    Columns r;
                     barrier_wait(bar.s, step & 1, guard);
                     tmem_fence_after();
-                    load64(r, at_s);
+                    load_columns(r, at_s);
                     tmem_fence_before();
                     __syncwarp();
                     if (lane == 0) barrier_arrive(bar.s_read);
                     const int valid = g.length - i * kKeyTile;
-                    float2 p[32];
+                    float2 p[kColumnsEach / 2];
 #pragma unroll
-                    for (int y = 0; y < 32; ++y) {
+                    for (int y = 0; y < kColumnsEach / 2; ++y) {
                         p[y] = fma2(pair(r, 2 * y), c2, lse2);
                         p[y].x = exp2_fast(p[y].x);
                         p[y].y = exp2_fast(p[y].y);
                     }
                     barrier_wait(bar.dp, step & 1, guard);
                     tmem_fence_after();
-                    load64(r, at_dp);
-                    uint32_t packed[32];
+                    load_columns(r, at_dp);
+                    uint32_t packed[kColumnsEach / 2];
                     if (valid < kKeyTile) {
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) {
+                        for (int y = 0; y < kColumnsEach / 2; ++y) {
                             const float2 ds = mul2(p[y], fma2(pair(r, 2 * y), f2, delta2));
-                            packed[y] = pack2<T>(half * 64 + 2 * y < valid ? ds.x : 0.0f,
-                                                 half * 64 + 2 * y + 1 < valid ? ds.y : 0.0f);
+                            packed[y] = pack2<T>(column0 + 2 * y < valid ? ds.x : 0.0f,
+                                                 column0 + 2 * y + 1 < valid ? ds.y : 0.0f);
                         }
-                        if (half == 0) {
+                        if (part == 0) {
                             // What lies behind the item's last key must not meet the zero ds as infinities or NaN.
                             barrier_wait(bar.ring + 8 * (n % S::kStages), n / S::kStages & 1, guard);
                             if (row_in_tile >= valid) {
@@ -287,14 +304,13 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                         }
                     } else {
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) {
+                        for (int y = 0; y < kColumnsEach / 2; ++y) {
                             const float2 ds = mul2(p[y], fma2(pair(r, 2 * y), f2, delta2));
                             packed[y] = pack2<T>(ds.x, ds.y);
                         }
                     }
                     __syncwarp();
-                    tmem_store32(tmem + lanes + S::kDs + (step & 1) * 64 + half * 32, packed);
-                    tmem_wait_store();
+                    store_pairs(tmem + lanes + S::kDs + (step & 1) * 64 + column0 / 2, packed);
                     tmem_fence_before();
                     __syncwarp();
                     if (lane == 0) barrier_arrive(bar.ready);
@@ -305,8 +321,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
             const bool store = row < a.q_len, whole = g.whole();
             T *out = (T *)a.dq + g.item * a.dq_item + (int64_t)row * a.dq_token + head * a.dq_head;
             float *partial = a.partial + ((int64_t)partial_slot(g, blockIdx.x) * kRowTile + row_in_tile) * a.dim;
-            for (int x = half * (HD / 2); x < (half + 1) * (HD / 2); x += 32) {
-                if (x >= a.dim) break;
+            for (int x = part * 32; x < HD && x < a.dim; x += kGroups * 32) {
                 uint32_t o[32];
                 __syncwarp();
                 if (g.length > 0) {
@@ -342,7 +357,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
     __syncthreads();
     tmem_fence_after();
     __syncwarp();
-    if (warp == 9) tmem_free(tmem, S::kColumns);
+    if (warp == kComputeWarps + 1) tmem_free(tmem, S::kColumns);
 }
 
 // ---- dk and dv: keys as rows ----------------------------------------------------------
@@ -370,7 +385,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
         s_words[1] = 0;
         bar.init();
     }
-    if (warp == 9) tmem_alloc(tail, S::kColumns);
+    if (warp == kComputeWarps + 1) tmem_alloc(tail, S::kColumns);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
@@ -378,9 +393,9 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
     Walk<KeyLine> walk = walk_share<KeyLine>(a.work);
     Segment g;
 
-    if (warp >= 8) {
-        give_registers();
-        if (warp == 8 && elect_one()) {
+    if (warp >= kComputeWarps) {
+        give_registers<kGroups>();
+        if (warp == kComputeWarps && elect_one()) {
             uint32_t n = 0, seg = 0;
             while (walk.next(g)) {
                 if (g.tile * kKeyTile >= g.length) continue;
@@ -409,7 +424,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
                 }
                 ++seg;
             }
-        } else if (warp == 9) {
+        } else if (warp == kComputeWarps + 1) {
             const bool leader = elect_one();
             const uint32_t form_s = product_form<T>(kRowTile, false);
             const uint32_t form_o = product_form<T>((a.dim + 15) & ~15, true);
@@ -440,11 +455,11 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
                     const bool more = i + 1 < g.end;
                     barrier_wait(bar.p_ready, step & 1, guard);
                     tmem_fence_after();
-                    product_across<0, 8>(leader, tmem + kOutV, tmem + S::kS, stage_at(n + 1), form_o, i > g.begin, 64);
+                    product_across<0, 8>(leader, tmem + kOutV, tmem + S::kS, stage_at(n + 1), form_o, i > g.begin, kGroups);
                     if (more) scores(n + 2);
                     barrier_wait(bar.ready, step & 1, guard);
                     tmem_fence_after();
-                    product_across<0, 8>(leader, tmem + kOutK, tmem + S::kDp, stage_at(n), form_o, i > g.begin, 64);
+                    product_across<0, 8>(leader, tmem + kOutK, tmem + S::kDp, stage_at(n), form_o, i > g.begin, kGroups);
                     release(n);
                     release(n + 1);
                     if (more)
@@ -457,10 +472,10 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
             }
         }
     } else {
-        take_registers();
-        const int half = warp / 4;                                  // columns 64 half .. of S and dP
+        take_registers<kGroups>();
+        const int part = warp / 4, column0 = part * kColumnsEach;   // columns of S and dP
         const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
-        const uint32_t at_s = tmem + lanes + S::kS + half * 64, at_dp = tmem + lanes + S::kDp + half * 64;
+        const uint32_t at_s = tmem + lanes + S::kS + column0, at_dp = tmem + lanes + S::kDp + column0;
         const int row_in_tile = warp % 4 * 32 + lane;
         const float c = a.scale_log2;
         const RangeShift shift = *a.shift;
@@ -474,55 +489,54 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
                 const bool tail_tile = g.length - g.tile * kKeyTile < kKeyTile;
                 for (int i = g.begin; i < g.end; ++i, n += 2, ++step) {
                     const float4 *lse4 = (const float4 *)(s_raw + (s_stat - raw) + n % S::kStages * S::kStatBytes) +
-                                         half * 16;
+                                         column0 / 4;
                     const float4 *delta4 =
-                        (const float4 *)(s_raw + (s_stat - raw) + (n + 1) % S::kStages * S::kStatBytes) + half * 16;
-                    uint32_t r[64], packed[32];
-                    float2 p[32];
+                        (const float4 *)(s_raw + (s_stat - raw) + (n + 1) % S::kStages * S::kStatBytes) + column0 / 4;
+                    Columns r;
+                    uint32_t packed[kColumnsEach / 2];
+                    float2 p[kColumnsEach / 2];
                     barrier_wait(bar.ring + 8 * (n % S::kStages), n / S::kStages & 1, guard);   // lse2
                     barrier_wait(bar.s, step & 1, guard);
                     tmem_fence_after();
-                    load64(r, at_s);
+                    load_columns(r, at_s);
 #pragma unroll
-                    for (int y = 0; y < 32; y += 2) {
+                    for (int y = 0; y < kColumnsEach / 2; y += 2) {
                         const float4 l = lse4[y / 2];
-                        p[y] = fma2(pair(r, 2 * y), c2, make_float2(-l.x, -l.y));
-                        p[y + 1] = fma2(pair(r, 2 * y + 2), c2, make_float2(-l.z, -l.w));
+                        p[y] = fma2(pair(r, 2 * y), c2, make_float2(l.x, l.y));
+                        p[y + 1] = fma2(pair(r, 2 * y + 2), c2, make_float2(l.z, l.w));
                     }
 #pragma unroll
-                    for (int y = 0; y < 32; ++y) {
+                    for (int y = 0; y < kColumnsEach / 2; ++y) {
                         p[y].x = exp2_fast(p[y].x);
                         p[y].y = exp2_fast(p[y].y);
                     }
                     if (tail_tile && !live)
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) p[y] = make_float2(0.0f, 0.0f);
+                        for (int y = 0; y < kColumnsEach / 2; ++y) p[y] = make_float2(0.0f, 0.0f);
 #pragma unroll
-                    for (int y = 0; y < 32; ++y) packed[y] = pack2<T>(p[y].x, p[y].y);
+                    for (int y = 0; y < kColumnsEach / 2; ++y) packed[y] = pack2<T>(p[y].x, p[y].y);
                     __syncwarp();
-                    tmem_store32(at_s, packed);
-                    tmem_wait_store();
+                    store_pairs(at_s, packed);
                     tmem_fence_before();
                     __syncwarp();
                     if (lane == 0) barrier_arrive(bar.p_ready);
                     barrier_wait(bar.ring + 8 * ((n + 1) % S::kStages), (n + 1) / S::kStages & 1, guard);   // delta
                     barrier_wait(bar.dp, step & 1, guard);
                     tmem_fence_after();
-                    load64(r, at_dp);
+                    load_columns(r, at_dp);
 #pragma unroll
-                    for (int y = 0; y < 32; y += 2) {
+                    for (int y = 0; y < kColumnsEach / 2; y += 2) {
                         const float4 d = delta4[y / 2];
-                        const float2 one = mul2(p[y], fma2(pair(r, 2 * y), f2, make_float2(-d.x, -d.y)));
-                        const float2 two = mul2(p[y + 1], fma2(pair(r, 2 * y + 2), f2, make_float2(-d.z, -d.w)));
+                        const float2 one = mul2(p[y], fma2(pair(r, 2 * y), f2, make_float2(d.x, d.y)));
+                        const float2 two = mul2(p[y + 1], fma2(pair(r, 2 * y + 2), f2, make_float2(d.z, d.w)));
                         packed[y] = pack2<T>(one.x, one.y);
                         packed[y + 1] = pack2<T>(two.x, two.y);
                     }
                     if (tail_tile && !live)
 #pragma unroll
-                        for (int y = 0; y < 32; ++y) packed[y] = 0;
+                        for (int y = 0; y < kColumnsEach / 2; ++y) packed[y] = 0;
                     __syncwarp();
-                    tmem_store32(at_dp, packed);
-                    tmem_wait_store();
+                    store_pairs(at_dp, packed);
                     tmem_fence_before();
                     __syncwarp();
                     if (lane == 0) barrier_arrive(bar.ready);
@@ -536,8 +550,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
             T *out_k = (T *)a.dk + g.item * a.dk_item + key * a.dk_token + g.head * a.dk_head;
             T *out_v = (T *)a.dv + g.item * a.dv_item + key * a.dv_token + g.head * a.dv_head;
             float *partial = a.partial + ((int64_t)partial_slot(g, blockIdx.x) * kRowTile + row_in_tile) * 2 * a.dim;
-            for (int x = half * (HD / 2); x < (half + 1) * (HD / 2); x += 32) {
-                if (x >= a.dim) break;
+            for (int x = part * 32; x < HD && x < a.dim; x += kGroups * 32) {
                 for (int which = 0; which < 2; ++which) {
                     uint32_t o[32];
                     __syncwarp();
@@ -579,26 +592,27 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
     __syncthreads();
     tmem_fence_after();
     __syncwarp();
-    if (warp == 9) tmem_free(tmem, S::kColumns);
+    if (warp == kComputeWarps + 1) tmem_free(tmem, S::kColumns);
 }
 
 // ---- sums of cut tiles' parts -----------------------------------------------------------
 
 constexpr int kSumBlock = 256;
-constexpr int kSumRows = 16;
+constexpr int kSumItems = 4;    // items of 8 elements a thread takes, whose loads are in flight together
 
+// Adds up the parts of 8 elements at `at` of every slot; parts first - 1 .. last.
 template <typename T>
-__device__ __forceinline__ void sum_row(const float *partial, int64_t slot_stride, int first, int last, T *out)
+__device__ __forceinline__ void sum_parts(const float *at, int64_t slot_stride, int first, int last, T *out)
 {
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int b = first - 1; b <= last; ++b) {
-        const float4 f = *(const float4 *)(partial + (2 * b + (b == first - 1 ? 1 : 0)) * slot_stride);
-        o.x += f.x;
-        o.y += f.y;
-        o.z += f.z;
-        o.w += f.w;
+    const float4 *p = (const float4 *)(at + (2 * first - 1) * slot_stride);
+    float4 lo = p[0], hi = p[1];
+    for (int b = first; b <= last; ++b) {
+        p = (const float4 *)(at + 2 * b * slot_stride);
+        const float4 f = p[0], g = p[1];
+        lo = make_float4(lo.x + f.x, lo.y + f.y, lo.z + f.z, lo.w + f.w);
+        hi = make_float4(hi.x + g.x, hi.y + g.y, hi.z + g.z, hi.w + g.w);
     }
-    *(uint2 *)out = make_uint2(pack2<T>(o.x, o.y), pack2<T>(o.z, o.w));
+    *(uint4 *)out = make_uint4(pack2<T>(lo.x, lo.y), pack2<T>(lo.z, lo.w), pack2<T>(hi.x, hi.y), pack2<T>(hi.z, hi.w));
 }
 
 template <typename T>
@@ -606,17 +620,17 @@ __global__ void __launch_bounds__(kSumBlock) k_attention_sum_q(const __grid_cons
 {
     grid_dependency_begin();
     Segment g;
-    const int first = blockIdx.x + 1;
+    const int first = blockIdx.x + 1, chunks = a.dim / 8;
     int last;
     if (!cut_tile<QueryLine>(a.work, grid, first, g, last)) return;
     const int head = g.tile / a.q_tiles, row0 = (g.tile - head * a.q_tiles) * kRowTile;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    if (lane * 4 >= a.dim) return;
-    for (int r = blockIdx.y * kSumRows + warp; r < (int)(blockIdx.y + 1) * kSumRows; r += kSumBlock / 32) {
+#pragma unroll
+    for (int k = 0; k < kSumItems; ++k) {
+        const int i = (blockIdx.y * kSumItems + k) * kSumBlock + threadIdx.x, r = i / chunks, c = (i - r * chunks) * 8;
         const int64_t row = row0 + r;
-        if (row >= a.q_len) return;
-        sum_row(a.partial + (int64_t)r * a.dim + lane * 4, (int64_t)kRowTile * a.dim, first, last,
-                (T *)a.dq + g.item * a.dq_item + row * a.dq_token + head * a.dq_head + lane * 4);
+        if (r >= kRowTile || row >= a.q_len) continue;
+        sum_parts(a.partial + (int64_t)r * a.dim + c, (int64_t)kRowTile * a.dim, first, last,
+                  (T *)a.dq + g.item * a.dq_item + row * a.dq_token + head * a.dq_head + c);
     }
 }
 
@@ -625,21 +639,19 @@ __global__ void __launch_bounds__(kSumBlock) k_attention_sum_kv(const __grid_con
 {
     grid_dependency_begin();
     Segment g;
-    const int first = blockIdx.x + 1;
+    const int first = blockIdx.x + 1, chunks = a.dim / 8;
     int last;
     if (!cut_tile<KeyLine>(a.work, grid, first, g, last)) return;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    if (lane * 4 >= a.dim) return;
-    for (int r = blockIdx.y * kSumRows + warp; r < (int)(blockIdx.y + 1) * kSumRows; r += kSumBlock / 32) {
+#pragma unroll
+    for (int k = 0; k < kSumItems; ++k) {
+        const int i = (blockIdx.y * kSumItems + k) * kSumBlock + threadIdx.x;
+        const int r2 = i / chunks, c = (i - r2 * chunks) * 8, r = r2 >> 1, which = r2 & 1;   // dk, dv
         const int row = g.tile * kKeyTile + r;
-        if (a.index ? row >= g.length : row >= a.kv_len) return;
+        if (r >= kKeyTile || row >= (a.index ? g.length : a.kv_len)) continue;
         const int64_t key = a.index ? a.index[(int64_t)g.item * a.kv_len + row] : row;
-        const float *part = a.partial + (int64_t)r * 2 * a.dim + lane * 4;
-        const int64_t stride = (int64_t)kRowTile * 2 * a.dim;
-        sum_row(part, stride, first, last,
-                (T *)a.dk + g.item * a.dk_item + key * a.dk_token + g.head * a.dk_head + lane * 4);
-        sum_row(part + a.dim, stride, first, last,
-                (T *)a.dv + g.item * a.dv_item + key * a.dv_token + g.head * a.dv_head + lane * 4);
+        T *out = which ? (T *)a.dv + g.item * a.dv_item + key * a.dv_token + g.head * a.dv_head
+                       : (T *)a.dk + g.item * a.dk_item + key * a.dk_token + g.head * a.dk_head;
+        sum_parts(a.partial + ((int64_t)r * 2 + which) * a.dim + c, (int64_t)kRowTile * 2 * a.dim, first, last, out + c);
     }
 }
 
@@ -655,23 +667,45 @@ struct RowArgs {
     int q_len, q_pad, q_heads, dim;
 };
 
-constexpr int kRowLanes = 16;   // lanes of a row, 8 elements each
+// Lanes of a row, 8 elements each, and a row's place: rows run over heads, then
+// tokens, as they lie in memory.
+template <int LANES>
+struct RowPlace {
+    int64_t row;
+    uint32_t item, token, head;
+    int c;
+    bool live;               // elements of a query (not of the padding)
+    __device__ RowPlace(const RowArgs &a, int64_t block)
+    {
+        row = block * (256 / LANES) + threadIdx.x / LANES;
+        c = threadIdx.x % LANES * 8;
+        const uint32_t r = (uint32_t)row, t = r / a.q_heads;
+        head = r - t * a.q_heads;
+        item = t / a.q_pad;
+        token = t - item * a.q_pad;
+        live = row < a.rows && token < (uint32_t)a.q_len && c < a.dim;
+    }
+    template <typename T>
+    __device__ Vec<T, 8> load(const gsr_heads &t) const
+    {
+        return *(const Vec<T, 8> *)((const T *)t.data + item * t.batch_stride + token * t.token_stride +
+                                    head * t.head_stride + c);
+    }
+};
 
-template <typename T>
+template <typename T, int LANES>
 __global__ void __launch_bounds__(256) k_attention_largest(const RowArgs a)
 {
     grid_dependency_begin();
     __shared__ uint32_t s_max;
     if (threadIdx.x == 0) s_max = 0;
     __syncthreads();
-    const int c = threadIdx.x % kRowLanes * 8;
+    const int64_t blocks = (a.rows + 256 / LANES - 1) / (256 / LANES);
     uint32_t top = 0;
-    for (int64_t r = (int64_t)blockIdx.x * (256 / kRowLanes) + threadIdx.x / kRowLanes; r < a.rows;
-         r += (int64_t)gridDim.x * (256 / kRowLanes)) {
-        const int64_t h = r % a.q_heads, i = r / a.q_heads % a.q_pad, b = r / a.q_heads / a.q_pad;
-        if (i >= a.q_len || c >= a.dim) continue;
-        const Vec<T, 8> v = *(const Vec<T, 8> *)((const T *)a.dout.data + b * a.dout.batch_stride +
-                                                  i * a.dout.token_stride + h * a.dout.head_stride + c);
+    for (int64_t block = blockIdx.x; block < blocks; block += gridDim.x) {
+        const RowPlace<LANES> at(a, block);
+        if (!at.live) continue;
+        const Vec<T, 8> v = at.template load<T>(a.dout);
 #pragma unroll
         for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(fabsf(to_float(v.e[e]))));
     }
@@ -682,9 +716,9 @@ __global__ void __launch_bounds__(256) k_attention_largest(const RowArgs a)
     if (threadIdx.x == 0) atomicMax(a.amax, s_max);
 }
 
-// lse in base 2 and delta, with the shifts of p and ds folded in; rows behind
+// -lse in base 2 and -delta, with the shifts of p and ds folded in; rows behind
 // q_len, and rows without keys, get p = 0.
-template <typename T>
+template <typename T, int LANES>
 __global__ void __launch_bounds__(256) k_attention_rows(const RowArgs a)
 {
     grid_dependency_begin();
@@ -695,54 +729,68 @@ __global__ void __launch_bounds__(256) k_attention_rows(const RowArgs a)
         if (top > 0.0f && top < INFINITY) shift.ds = exp2f((float)-ilogbf(top));
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.shift = shift;
-    const int64_t r = (int64_t)blockIdx.x * (256 / kRowLanes) + threadIdx.x / kRowLanes;
-    const int c = threadIdx.x % kRowLanes * 8;
+    const RowPlace<LANES> at(a, blockIdx.x);
     float sum = 0.0f;
-    const int64_t h = r % a.q_heads, i = r / a.q_heads % a.q_pad, b = r / a.q_heads / a.q_pad;
-    if (r < a.rows && i < a.q_len && c < a.dim) {
-        const Vec<T, 8> o = *(const Vec<T, 8> *)((const T *)a.out.data + b * a.out.batch_stride +
-                                                  i * a.out.token_stride + h * a.out.head_stride + c);
-        const Vec<T, 8> d = *(const Vec<T, 8> *)((const T *)a.dout.data + b * a.dout.batch_stride +
-                                                  i * a.dout.token_stride + h * a.dout.head_stride + c);
+    if (at.live) {
+        const Vec<T, 8> o = at.template load<T>(a.out), d = at.template load<T>(a.dout);
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum = fmaf(to_float(o.e[e]), to_float(d.e[e]), sum);
     }
-    for (int d = kRowLanes / 2; d > 0; d /= 2) sum += __shfl_xor_sync(~0u, sum, d);
-    if (r < a.rows && c == 0) {
-        const int64_t at = (b * a.q_heads + h) * a.q_pad + i;
+    for (int d = LANES / 2; d > 0; d /= 2) sum += __shfl_xor_sync(~0u, sum, d);
+    if (at.row < a.rows && at.c == 0) {
+        const int64_t row = (int64_t)at.item * a.q_heads + at.head, to = row * a.q_pad + at.token;
         float lse = INFINITY;
-        if (i < a.q_len) {
-            lse = a.lse[(b * a.q_heads + h) * a.q_len + i];
+        if (at.token < (uint32_t)a.q_len) {
+            lse = a.lse[row * a.q_len + at.token];
             lse = lse == -INFINITY ? INFINITY : lse * kLog2e - log2f(shift.p);
         }
-        a.lse2[at] = lse;
-        a.delta[at] = sum * (shift.ds / shift.p);
+        a.lse2[to] = -lse;
+        a.delta[to] = -sum * (shift.ds / shift.p);
     }
 }
 
-// Zeros: rows of an array, all of them or those of masked keys.
-template <typename T>
-__global__ void __launch_bounds__(256) k_attention_zero_rows(gsr_heads t, int64_t rows, int tokens, int heads, int dim,
-                                                             const uint8_t *mask, const int32_t *lengths)
+template <typename T, int LANES>
+int row_statistics(gsr_ctx *ctx, const RowArgs &r, cudaStream_t stream)
 {
-    grid_dependency_begin();
-    const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (r >= rows) return;
-    const int64_t h = r % heads, i = r / heads % tokens, b = r / heads / tokens;
-    if (mask && i < item_length(lengths, tokens, (int)b) && mask[b * tokens + i] != 0) return;
-    T *o = (T *)t.data + b * t.batch_stride + i * t.token_stride + h * t.head_stride;
-    for (int c = 0; c < dim; c += 8) *(uint4 *)(o + c) = make_uint4(0, 0, 0, 0);
+    const int64_t blocks = (r.rows + 256 / LANES - 1) / (256 / LANES), most = 8 * (int64_t)ctx->num_sms;
+    if (r.amax) {
+        if (int rc = cuda_check(ctx, cudaMemsetAsync(r.amax, 0, sizeof(uint32_t), stream), "k_attention_largest"))
+            return rc;
+        if (int rc = cuda_check(ctx, launch_kernel(ctx, k_attention_largest<T, LANES>,
+                                                   dim3((unsigned)(blocks < most ? blocks : most)), 256, stream, r),
+                                "k_attention_largest"))
+            return rc;
+    }
+    return cuda_check(ctx, launch_kernel(ctx, k_attention_rows<T, LANES>, dim3((unsigned)blocks), 256, stream, r),
+                      "k_attention_rows");
 }
 
-template <typename T>
-int zero_rows(gsr_ctx *ctx, const gsr_heads &t, const gsr_attention &d, int tokens, int heads, bool masked,
-              cudaStream_t stream)
+// Zeros: rows of one or two arrays of the same shape, all of them or those of
+// masked keys.
+__global__ void __launch_bounds__(256) k_attention_zero_rows(gsr_heads t, gsr_heads t2, uint32_t rows, uint32_t tokens,
+                                                             uint32_t heads, int dim, const uint8_t *mask,
+                                                             const int32_t *lengths)
 {
-    const int64_t rows = (int64_t)d.batch * tokens * heads;
+    grid_dependency_begin();
+    const uint32_t r = blockIdx.x * 256 + threadIdx.x;
+    if (r >= rows) return;
+    const uint32_t bi = r / heads, h = r - bi * heads, b = bi / tokens, i = bi - b * tokens;
+    if (mask && (int)i < item_length(lengths, (int)tokens, (int)b) && mask[(int64_t)b * tokens + i] != 0) return;
+    for (const gsr_heads *x : {&t, &t2}) {
+        if (!x->data) continue;
+        uint16_t *o = (uint16_t *)x->data + b * x->batch_stride + i * x->token_stride + h * x->head_stride;
+        for (int c = 0; c < dim; c += 8) *(uint4 *)(o + c) = make_uint4(0, 0, 0, 0);
+    }
+}
+
+int zero_rows(gsr_ctx *ctx, const gsr_heads &t, const gsr_heads &t2, const gsr_attention &d, int tokens, int heads,
+              bool masked, cudaStream_t stream)
+{
+    const int64_t rows = (int64_t)d.batch * tokens * heads;   // at most 2^31 - 1, as the arguments' check has it
     if (rows == 0) return GSR_OK;
-    return cuda_check(ctx, launch_kernel(ctx, k_attention_zero_rows<T>, dim3((unsigned)((rows + 255) / 256)), 256, stream,
-                                         t, rows, tokens, heads, (int)d.head_dim, masked ? d.key_mask : nullptr,
-                                         masked ? d.kv_lengths : nullptr),
+    return cuda_check(ctx, launch_kernel(ctx, k_attention_zero_rows, dim3((unsigned)((rows + 255) / 256)), 256, stream, t,
+                                         t2, (uint32_t)rows, (uint32_t)tokens, (uint32_t)heads, (int)d.head_dim,
+                                         masked ? d.key_mask : nullptr, masked ? d.kv_lengths : nullptr),
                       "k_attention_zero_rows");
 }
 
@@ -752,7 +800,7 @@ int launch_big(gsr_ctx *ctx, Kernel *kernel, const char *name, int blocks, int s
 {
     if (int rc = cuda_check(ctx, cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem), name))
         return rc;
-    if (int rc = check_registers(ctx, (const void *)kernel, name)) return rc;
+    if (int rc = check_registers(ctx, (const void *)kernel, name, Registers<kGroups>::kStart)) return rc;
     return cuda_check(ctx, launch_kernel_smem(ctx, kernel, dim3((unsigned)blocks), kBackwardThreads, smem, stream, a),
                       name);
 }
@@ -761,13 +809,14 @@ template <typename T, int HD>
 int launch_backward(gsr_ctx *ctx, BackwardArgs &a, const Schedule &by_query, const Schedule &by_key, int blocks_q,
                     int blocks_k, cudaStream_t stream)
 {
-    const dim3 rows(1, kRowTile / kSumRows);
+    // Blocks of a cut tile's sum: its rows' vectors over a block's items.
+    const int vectors = kRowTile * a.dim / 8, each = kSumBlock * kSumItems;
     a.work = by_key;
     if (int rc = launch_big(ctx, k_attention_grad_kv<T, HD>, "k_attention_grad_kv", blocks_k,
                             BackwardShape<HD>::kSmemK, a, stream))
         return rc;
     if (blocks_k > 1)
-        if (int rc = cuda_check(ctx, launch_kernel(ctx, k_attention_sum_kv<T>, dim3((unsigned)blocks_k - 1, rows.y),
+        if (int rc = cuda_check(ctx, launch_kernel(ctx, k_attention_sum_kv<T>, dim3((unsigned)blocks_k - 1, (unsigned)((2 * vectors + each - 1) / each)),
                                                    kSumBlock, stream, a, blocks_k),
                                 "k_attention_sum_kv"))
             return rc;
@@ -776,7 +825,7 @@ int launch_backward(gsr_ctx *ctx, BackwardArgs &a, const Schedule &by_query, con
                             stream))
         return rc;
     if (blocks_q == 1) return GSR_OK;
-    return cuda_check(ctx, launch_kernel(ctx, k_attention_sum_q<T>, dim3((unsigned)blocks_q - 1, rows.y), kSumBlock,
+    return cuda_check(ctx, launch_kernel(ctx, k_attention_sum_q<T>, dim3((unsigned)blocks_q - 1, (unsigned)((vectors + each - 1) / each)), kSumBlock,
                                          stream, a, blocks_q),
                       "k_attention_sum_q");
 }
@@ -786,11 +835,8 @@ int backward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr
              const gsr_heads &out, const float *lse, const gsr_heads &dout, const gsr_heads &dq, const gsr_heads &dk,
              const gsr_heads &dv, cudaStream_t stream)
 {
-    if (d.kv_len == 0) return zero_rows<T>(ctx, dq, d, d.q_len, d.q_heads, false, stream);
-    if (d.q_len == 0) {
-        if (int rc = zero_rows<T>(ctx, dk, d, d.kv_len, d.kv_heads, false, stream)) return rc;
-        return zero_rows<T>(ctx, dv, d, d.kv_len, d.kv_heads, false, stream);
-    }
+    if (d.kv_len == 0) return zero_rows(ctx, dq, gsr_heads{}, d, d.q_len, d.q_heads, false, stream);
+    if (d.q_len == 0) return zero_rows(ctx, dk, dv, d, d.kv_len, d.kv_heads, false, stream);
     BackwardArgs a = {};
     a.q_len = d.q_len;
     a.kv_len = d.kv_len;
@@ -846,20 +892,8 @@ int backward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr
     r.q_pad = a.q_pad;
     r.q_heads = d.q_heads;
     r.dim = d.head_dim;
-    const int64_t row_blocks = (rows + 256 / kRowLanes - 1) / (256 / kRowLanes);
-    if (d.dtype == GSR_F16) {
-        r.amax = (uint32_t *)(shift + 1);
-        if (int rc = cuda_check(ctx, cudaMemsetAsync(r.amax, 0, sizeof(uint32_t), stream), "k_attention_largest"))
-            return rc;
-        const int64_t most = 8 * (int64_t)ctx->num_sms;
-        if (int rc = cuda_check(ctx, launch_kernel(ctx, k_attention_largest<T>,
-                                                   dim3((unsigned)(row_blocks < most ? row_blocks : most)), 256, stream, r),
-                                "k_attention_largest"))
-            return rc;
-    }
-    if (int rc = cuda_check(ctx, launch_kernel(ctx, k_attention_rows<T>, dim3((unsigned)row_blocks), 256, stream, r),
-                            "k_attention_rows"))
-        return rc;
+    if (d.dtype == GSR_F16) r.amax = (uint32_t *)(shift + 1);
+    if (int rc = d.head_dim <= 64 ? row_statistics<T, 8>(ctx, r, stream) : row_statistics<T, 16>(ctx, r, stream)) return rc;
 
     gsr_heads keys = k, values = v;
     if (d.key_mask) {
@@ -869,8 +903,7 @@ int backward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr
         values = pack.v;
         by_query.lengths = by_key.lengths = pack.counts;
         a.index = pack.index;
-        if (int rc = zero_rows<T>(ctx, dk, d, d.kv_len, d.kv_heads, true, stream)) return rc;
-        if (int rc = zero_rows<T>(ctx, dv, d, d.kv_len, d.kv_heads, true, stream)) return rc;
+        if (int rc = zero_rows(ctx, dk, dv, d, d.kv_len, d.kv_heads, true, stream)) return rc;
     }
     a.q_item = q.batch_stride != 0;
     a.q_head = q.head_stride != 0;

@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
     const int row_tiles = a.row_tiles;   // of 256 rows, per head
 
     if (warp >= 8) {
-    give_registers();
+    give_registers<2>();
     if (warp == 8) {
         // ---- copies: Q of a segment, then K and V of every step ----
         if (elect_one()) {
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
         }
     }
     } else {
-        take_registers();
+        take_registers<2>();
         // ---- softmax: one row a thread ----
         const int t = warp / 4;                                     // row tile
         const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;     // this warp's lanes of tensor memory
@@ -340,51 +340,56 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
     if (warp == 9) tmem_free(tmem, S::kColumns);
 }
 
-// Joins the parts of a cut tile: weights exp(lse_part - lse), one warp a row.
-// Block x handles the tile that the start of share x + 1 cuts, if it is the first
-// share that starts inside that tile.
+// Joins the parts of a cut tile: weights exp(lse_part - lse).  Block x handles the
+// tile that the start of share x + 1 cuts, if that is the first share to start
+// inside it; a thread takes 8 elements of kJoinItems rows.
 constexpr int kJoinBlock = 256;
-constexpr int kJoinRows = 16;
+constexpr int kJoinItems = 4;
 
 template <typename T>
 __global__ void __launch_bounds__(kJoinBlock) k_attention_join(const __grid_constant__ ForwardArgs a, int grid)
 {
     grid_dependency_begin();
     Segment g;
-    const int first = blockIdx.x + 1;
+    const int first = blockIdx.x + 1, chunks = a.dim / 8;
     int last;
     if (!cut_tile<QueryLine>(a.work, grid, first, g, last)) return;
     const int head = g.tile / a.row_tiles, row0 = (g.tile - head * a.row_tiles) * 2 * kRowTile;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    for (int r = blockIdx.y * kJoinRows + warp; r < (int)(blockIdx.y + 1) * kJoinRows; r += kJoinBlock / 32) {
+    constexpr int kRows = 2 * kRowTile;
+    const int slot0 = 2 * first - 1;   // then 2 b of the blocks b = first .. last
+#pragma unroll
+    for (int k = 0; k < kJoinItems; ++k) {
+        const int i = (blockIdx.y * kJoinItems + k) * kJoinBlock + threadIdx.x, r = i / chunks, c = (i - r * chunks) * 8;
         const int row = row0 + r;
-        if (row >= a.q_len) return;
-        auto slot = [&](int block) { return (int64_t)(2 * block + (block == first - 1 ? 1 : 0)) * 2 * kRowTile + r; };
-        float top = -INFINITY;
-        for (int b = first - 1 + lane; b <= last; b += 32) top = fmaxf(top, a.partial_lse[slot(b)]);
-        for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+        if (r >= kRows || row >= a.q_len) continue;
+        const float lse0 = a.partial_lse[(int64_t)slot0 * kRows + r];
+        float top = lse0;
+        for (int b = first; b <= last; ++b) top = fmaxf(top, a.partial_lse[(int64_t)2 * b * kRows + r]);
         const float shift = top == -INFINITY ? 0.0f : top;
-        float total = 0.0f;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int b = first - 1; b <= last; ++b) {   // blocks first - 1 .. last hold parts
-            const float w = expf(a.partial_lse[slot(b)] - shift);
+        float total = 0.0f, o[8] = {};
+        auto add = [&](int64_t slot, float lse) {
+            const float w = expf(lse - shift);
             total += w;
-            if (lane * 4 < a.dim) {
-                const float4 f = *(const float4 *)(a.partial + slot(b) * a.dim + lane * 4);
-                if (w != 0.0f) {
-                    o.x = fmaf(w, f.x, o.x);
-                    o.y = fmaf(w, f.y, o.y);
-                    o.z = fmaf(w, f.z, o.z);
-                    o.w = fmaf(w, f.w, o.w);
-                }
+            const float4 *p = (const float4 *)(a.partial + (slot * kRows + r) * a.dim + c);
+            const float4 f = p[0], h = p[1];
+            if (w != 0.0f) {
+                o[0] = fmaf(w, f.x, o[0]);
+                o[1] = fmaf(w, f.y, o[1]);
+                o[2] = fmaf(w, f.z, o[2]);
+                o[3] = fmaf(w, f.w, o[3]);
+                o[4] = fmaf(w, h.x, o[4]);
+                o[5] = fmaf(w, h.y, o[5]);
+                o[6] = fmaf(w, h.z, o[6]);
+                o[7] = fmaf(w, h.w, o[7]);
             }
-        }
+        };
+        add(slot0, lse0);
+        for (int b = first; b <= last; ++b) add(2 * b, a.partial_lse[(int64_t)2 * b * kRows + r]);
         const float inv = total > 0.0f ? 1.0f / total : (total == 0.0f ? 0.0f : total);
-        if (lane * 4 < a.dim) {
-            T *out = (T *)a.out + g.item * a.out_item + (int64_t)row * a.out_token + head * a.out_head + lane * 4;
-            *(uint2 *)out = make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
-        }
-        if (lane == 0) a.lse[((int64_t)g.item * a.q_heads + head) * a.q_len + row] = top + logf(total);
+        T *out = (T *)a.out + g.item * a.out_item + (int64_t)row * a.out_token + head * a.out_head + c;
+        *(uint4 *)out = make_uint4(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv),
+                                   pack2<T>(o[4] * inv, o[5] * inv), pack2<T>(o[6] * inv, o[7] * inv));
+        if (c == 0) a.lse[((int64_t)g.item * a.q_heads + head) * a.q_len + row] = top + logf(total);
     }
 }
 
@@ -411,13 +416,15 @@ int launch_forward(gsr_ctx *ctx, ForwardArgs &a, int blocks, cudaStream_t stream
     if (int rc = cuda_check(ctx, cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
                             "k_attention_forward"))
         return rc;
-    if (int rc = check_registers(ctx, (const void *)kernel, "k_attention_forward")) return rc;
+    if (int rc = check_registers(ctx, (const void *)kernel, "k_attention_forward", Registers<2>::kStart)) return rc;
     if (int rc = cuda_check(ctx, launch_kernel_smem(ctx, kernel, dim3((unsigned)blocks), kForwardThreads, smem, stream, a),
                             "k_attention_forward"))
         return rc;
     if (blocks == 1) return GSR_OK;
-    return cuda_check(ctx, launch_kernel(ctx, k_attention_join<T>, dim3((unsigned)blocks - 1, 2 * kRowTile / kJoinRows),
-                                         kJoinBlock, stream, a, blocks),
+    const int vectors = 2 * kRowTile * a.dim / 8, each = kJoinBlock * kJoinItems;
+    return cuda_check(ctx, launch_kernel(ctx, k_attention_join<T>,
+                                         dim3((unsigned)blocks - 1, (unsigned)((vectors + each - 1) / each)), kJoinBlock,
+                                         stream, a, blocks),
                       "k_attention_join");
 }
 

@@ -24,6 +24,7 @@ EncodeTiled encoder()
 }
 
 constexpr int kPackBlock = 1024;
+constexpr int kPackKeys = 8;   // neighbouring keys of a thread
 
 // Item b's kept keys in ascending order, and how many they are.
 __global__ void __launch_bounds__(kPackBlock) k_pack_index(const uint8_t *mask, const int32_t *lengths, int kv_len,
@@ -36,52 +37,60 @@ __global__ void __launch_bounds__(kPackBlock) k_pack_index(const uint8_t *mask, 
     mask += (int64_t)b * kv_len;
     index += (int64_t)b * kv_len;
     int base = 0;
-    for (int j0 = 0; j0 < length; j0 += kPackBlock) {
-        const int j = j0 + threadIdx.x;
-        const bool keep = j < length && mask[j] != 0;
-        const unsigned votes = __ballot_sync(~0u, keep);
-        if (lane == 0) s_warp[warp] = __popc(votes);
-        __syncthreads();
-        int before = 0, all = 0;
-        for (int w = 0; w < kPackBlock / 32; ++w) {
-            if (w < warp) before += s_warp[w];
-            all += s_warp[w];
+    for (int j0 = 0; j0 < length; j0 += kPackBlock * kPackKeys) {
+        const int j = j0 + threadIdx.x * kPackKeys;
+        uint32_t keep = 0;
+#pragma unroll
+        for (int k = 0; k < kPackKeys; ++k)
+            if (j + k < length && mask[j + k] != 0) keep |= 1u << k;
+        const int mine = __popc(keep);
+        int before = mine;                                   // inclusive over the warp
+        for (int d = 1; d < 32; d *= 2) {
+            const int other = __shfl_up_sync(~0u, before, d);
+            if (lane >= d) before += other;
         }
-        if (keep) index[base + before + __popc(votes & ((1u << lane) - 1))] = j;
-        base += all;
+        if (lane == 31) s_warp[warp] = before;
+        __syncthreads();
+        int all = s_warp[lane];                              // as many warps as lanes
+        for (int d = 1; d < 32; d *= 2) {
+            const int other = __shfl_up_sync(~0u, all, d);
+            if (lane >= d) all += other;
+        }
+        const int warps_before = __shfl_sync(~0u, all, warp) - s_warp[warp];
+        int at = base + warps_before + before - mine;
+#pragma unroll
+        for (int k = 0; k < kPackKeys; ++k)
+            if (keep >> k & 1) index[at++] = j + k;
+        base += __shfl_sync(~0u, all, 31);
         __syncthreads();
     }
     if (threadIdx.x == 0) counts[b] = base;
 }
+static_assert(kPackBlock / 32 == 32, "one warp scans the warps' counts");
 
-// Copies the kept keys' rows of k and v, 16 bytes a thread.
-__global__ void __launch_bounds__(256) k_pack_rows(gsr_heads k, gsr_heads v, uint4 *to_k, uint4 *to_v, int64_t items,
-                                                   int kv_len, int heads, int chunks, const int32_t *counts,
-                                                   const int32_t *index)
+// Copies the kept keys' rows of k and v, 16 bytes a thread; block y is the
+// head, z the item; rows of a head lie one behind the other.
+__global__ void __launch_bounds__(256) k_pack_rows(gsr_heads k, gsr_heads v, uint4 *to_k, uint4 *to_v, int kv_len,
+                                                   int heads, int chunks, const int32_t *counts, const int32_t *index)
 {
     grid_dependency_begin();
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= items) return;
-    const int c = (int)(i % chunks);
-    const int64_t row = i / chunks;              // [item][head][token]
-    const int t = (int)(row % kv_len);
-    const int h = (int)(row / kv_len % heads);
-    const int64_t b = row / kv_len / heads;
+    const int i = blockIdx.x * 256 + threadIdx.x, t = i / chunks, c = i - t * chunks;
+    const int64_t b = blockIdx.z, h = blockIdx.y;
     if (t >= counts[b]) return;
-    const int64_t j = index[b * kv_len + t];
-    to_k[i] = *(const uint4 *)((const uint16_t *)k.data + b * k.batch_stride + j * k.token_stride + h * k.head_stride +
-                               c * 8);
-    to_v[i] = *(const uint4 *)((const uint16_t *)v.data + b * v.batch_stride + j * v.token_stride + h * v.head_stride +
-                               c * 8);
+    const int64_t j = index[b * kv_len + t], to = (b * heads + h) * ((int64_t)kv_len * chunks) + i;
+    to_k[to] = *(const uint4 *)((const uint16_t *)k.data + b * k.batch_stride + j * k.token_stride + h * k.head_stride +
+                                c * 8);
+    to_v[to] = *(const uint4 *)((const uint16_t *)v.data + b * v.batch_stride + j * v.token_stride + h * v.head_stride +
+                                c * 8);
 }
 
 }  // namespace
 
-int check_registers(gsr_ctx *ctx, const void *kernel, const char *name)
+int check_registers(gsr_ctx *ctx, const void *kernel, const char *name, int start)
 {
     cudaFuncAttributes attributes;
     if (int rc = cuda_check(ctx, cudaFuncGetAttributes(&attributes, kernel), name)) return rc;
-    if (attributes.numRegs < kStartRegisters)
+    if (attributes.numRegs < start)
         return fail(ctx, GSR_ERR_CUDA, std::string(name) + " was compiled to start with too few registers");
     return GSR_OK;
 }
@@ -127,11 +136,19 @@ cudaError_t pack_keys(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &k, 
     cudaError_t e = launch_kernel(ctx, k_pack_index, dim3((unsigned)d.batch), kPackBlock, stream, d.key_mask,
                                   d.kv_lengths, (int)d.kv_len, out->counts, out->index);
     const int chunks = d.head_dim / 8;
-    const int64_t items = (int64_t)d.batch * d.kv_heads * d.kv_len * chunks;
-    if (e == cudaSuccess)
-        e = launch_kernel(ctx, k_pack_rows, dim3((unsigned)((items + 255) / 256)), 256, stream, k, v,
-                          (uint4 *)out->k.data, (uint4 *)out->v.data, items, (int)d.kv_len, (int)d.kv_heads, chunks,
-                          (const int32_t *)out->counts, (const int32_t *)out->index);
+    // Items beyond a grid's z go in further launches.
+    for (int b = 0; e == cudaSuccess && b < d.batch; b += 65535) {
+        const int n = d.batch - b < 65535 ? d.batch - b : 65535;
+        gsr_heads kb = k, vb = v;
+        kb.data = (uint16_t *)k.data + b * k.batch_stride;
+        vb.data = (uint16_t *)v.data + b * v.batch_stride;
+        const int64_t first = (int64_t)b * d.kv_heads * d.kv_len * chunks;
+        e = launch_kernel(ctx, k_pack_rows, dim3((unsigned)(((int64_t)d.kv_len * chunks + 255) / 256),
+                                                 (unsigned)d.kv_heads, (unsigned)n),
+                          256, stream, kb, vb, (uint4 *)out->k.data + first, (uint4 *)out->v.data + first, (int)d.kv_len,
+                          (int)d.kv_heads, chunks, (const int32_t *)out->counts + b,
+                          (const int32_t *)out->index + (int64_t)b * d.kv_len);
+    }
     return e;
 }
 

@@ -243,28 +243,49 @@ __device__ __forceinline__ void product_rows(bool leader, uint32_t d, uint32_t a
 }
 
 // d (+)= a b with a (128 rows, 16-bit pairs in tensor memory) against rows
-// 16 K0 .. 16 K1 - 1 of tile b; `half` is the column distance of a's second 64 terms.
+// 16 K0 .. 16 K1 - 1 of tile b.  a's 128 terms lie in `groups` runs, each at the
+// start of its own 128 / groups columns (1: one run of 64 columns).
 template <int K0, int K1>
 __device__ __forceinline__ void product_across(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t form, bool add,
-                                               int half = 32)
+                                               int groups = 1)
 {
     const uint32_t b0 = operand_across(b);
 #pragma unroll
-    for (int k = K0; k < K1; ++k)
-        product_ts(leader, d, a + (k & 3) * 8 + (k >> 2) * half, b0 + (k * 2048 >> 4), form, add || k != 0);
+    for (int k = K0; k < K1; ++k) {
+        const int each = 8 / groups;
+        product_ts(leader, d, a + k / each * (128 / groups) + k % each * 8, b0 + (k * 2048 >> 4), form, add || k != 0);
+    }
 }
 
 // ---- registers ------------------------------------------------------------------------------
 
-// Blocks of 384 threads start with kStartRegisters a thread; the four warps that
-// copy and issue products give most of theirs to the other eight, which hold a
-// row of scores each.
-constexpr int kStartRegisters = 168, kFewRegisters = 72, kManyRegisters = 216;
-static_assert(128 * kFewRegisters + 256 * kManyRegisters <= 384 * kStartRegisters,
-              "the shares must fit what the block starts with");
+// A block has `groups` warpgroups that compute, each thread with a row of scores
+// or a part of one, and one whose warps copy and issue products and give most of
+// their registers to the others.
+template <int GROUPS>
+struct Registers;
+template <>
+struct Registers<2> {
+    static constexpr int kStart = 168, kFew = 72, kMany = 216;
+};
+template <>
+struct Registers<4> {
+    static constexpr int kStart = 96, kFew = 64, kMany = 104;
+};
 
-__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); }
-__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 216;"); }
+template <int GROUPS>
+__device__ __forceinline__ void give_registers()
+{
+    using R = Registers<GROUPS>;
+    static_assert(R::kFew + GROUPS * R::kMany <= (GROUPS + 1) * R::kStart, "the shares must fit what the block starts with");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kFew));
+}
+
+template <int GROUPS>
+__device__ __forceinline__ void take_registers()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Registers<GROUPS>::kMany));
+}
 
 // ---- host ------------------------------------------------------------------------------------
 
@@ -273,7 +294,7 @@ __device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.
 // becomes an extent of 1; the kernels multiply such a coordinate by 0.
 // (A kernel compiled to start with fewer registers than the shares add up to
 // would wait for them forever: refuse to launch it.)
-int check_registers(gsr_ctx *ctx, const void *kernel, const char *name);
+int check_registers(gsr_ctx *ctx, const void *kernel, const char *name, int start);
 int heads_map(gsr_ctx *ctx, CUtensorMap *map, const gsr_heads &t, int dtype, int64_t batch, int64_t tokens,
               int64_t heads, int dim, int rows);
 
