@@ -121,6 +121,8 @@ __device__ __forceinline__ void load_columns(Columns &r, uint32_t at)
 #pragma unroll
     for (int x = 0; x < kColumnsEach; x += 32) tmem_load32(*(uint32_t(*)[32])&r[x], at + x);
     tmem_wait_load();
+#pragma unroll
+    for (int x = 0; x < kColumnsEach; x += 32) pin(*(uint32_t(*)[32])&r[x]);
 }
 
 // Their 16-bit pairs.
@@ -163,7 +165,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
         s_words[1] = 0;
         bar.init();
     }
-    if (warp == kComputeWarps + 1) tmem_alloc(tail, S::kColumns);
+    if (warp == kComputeWarps + 2) tmem_alloc(tail, S::kColumns);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
@@ -188,6 +190,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                 }
                 for (int i = g.begin; i < g.end; ++i)
                     for (int half = 0; half < 2; ++half, ++n) {
+                        if (guard.stop()) goto done;
                         const uint32_t stage = n % S::kStages, round = n / S::kStages;
                         if (round > 0) barrier_wait(bar.ring_free + 8 * stage, (round - 1) & 1, guard);
                         const uint32_t full = bar.ring + 8 * stage, to = s_ring + stage * S::kTileBytes;
@@ -205,14 +208,14 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
             const int steps = (a.dim + 15) / 16;
             auto stage_at = [&](uint32_t x) { return s_ring + x % S::kStages * S::kTileBytes; };
             auto await = [&](uint32_t x) {
-                barrier_wait(bar.ring + 8 * (x % S::kStages), x / S::kStages & 1, guard);
+                barrier_wait_warp(bar.ring + 8 * (x % S::kStages), x / S::kStages & 1, guard);
                 tmem_fence_after();
             };
             auto release = [&](uint32_t x) { product_commit(leader, bar.ring_free + 8 * (x % S::kStages)); };
             uint32_t n = 0, seg = 0, step = 0;
             while (walk.next(g)) {
                 if (g.length == 0) continue;
-                barrier_wait(bar.own, seg & 1, guard);
+                barrier_wait_warp(bar.own, seg & 1, guard);
                 const uint32_t s_q = s_own, s_do = s_own + S::kTileBytes;
                 auto scores = [&](uint32_t x) {
                     await(x);
@@ -229,10 +232,10 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                 dp(n + 1);
                 for (int i = g.begin; i < g.end; ++i, n += 2, ++step) {
                     const bool more = i + 1 < g.end;
-                    barrier_wait(bar.s_read, step & 1, guard);
+                    barrier_wait_warp(bar.s_read, step & 1, guard);
                     tmem_fence_after();
                     if (more) scores(n + 2);
-                    barrier_wait(bar.ready, step & 1, guard);
+                    barrier_wait_warp(bar.ready, step & 1, guard);
                     tmem_fence_after();
                     product_across<0, 8>(leader, tmem + S::kOut, tmem + S::kDs + (step & 1) * 64, stage_at(n), form_o, i > g.begin);
                     release(n);
@@ -265,7 +268,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                 const float2 lse2 = make_float2(lse, lse), delta2 = make_float2(delta, delta);
                 for (int i = g.begin; i < g.end; ++i, n += 2, ++step) {
                     Columns r;
-                    barrier_wait(bar.s, step & 1, guard);
+                    barrier_wait_warp(bar.s, step & 1, guard);
                     tmem_fence_after();
                     load_columns(r, at_s);
                     tmem_fence_before();
@@ -279,7 +282,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                         p[y].x = exp2_fast(p[y].x);
                         p[y].y = exp2_fast(p[y].y);
                     }
-                    barrier_wait(bar.dp, step & 1, guard);
+                    barrier_wait_warp(bar.dp, step & 1, guard);
                     tmem_fence_after();
                     load_columns(r, at_dp);
                     uint32_t packed[kColumnsEach / 2];
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                         }
                         if (part == 0) {
                             // What lies behind the item's last key must not meet the zero ds as infinities or NaN.
-                            barrier_wait(bar.ring + 8 * (n % S::kStages), n / S::kStages & 1, guard);
+                            barrier_wait_warp(bar.ring + 8 * (n % S::kStages), n / S::kStages & 1, guard);
                             if (row_in_tile >= valid) {
                                 unsigned char *k = s_raw + (s_ring - raw) + n % S::kStages * S::kTileBytes +
                                                    row_in_tile * 128;
@@ -315,7 +318,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                     __syncwarp();
                     if (lane == 0) barrier_arrive(bar.ready);
                 }
-                barrier_wait(bar.done, seg++ & 1, guard);
+                barrier_wait_warp(bar.done, seg++ & 1, guard);
                 tmem_fence_after();
             }
             const bool store = row < a.q_len, whole = g.whole();
@@ -327,6 +330,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                 if (g.length > 0) {
                     tmem_load32(o, tmem + lanes + S::kOut + x);
                     tmem_wait_load();
+                    pin(o);
                 } else {
 #pragma unroll
                     for (int y = 0; y < 32; ++y) o[y] = 0;
@@ -351,13 +355,14 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
             tmem_fence_before();
         }
     }
+done:
     __syncwarp();
     drain_if_aborted(guard);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
     __syncwarp();
-    if (warp == kComputeWarps + 1) tmem_free(tmem, S::kColumns);
+    if (warp == kComputeWarps + 2) tmem_free(tmem, S::kColumns);
 }
 
 // ---- dk and dv: keys as rows ----------------------------------------------------------
@@ -385,7 +390,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
         s_words[1] = 0;
         bar.init();
     }
-    if (warp == kComputeWarps + 1) tmem_alloc(tail, S::kColumns);
+    if (warp == kComputeWarps + 2) tmem_alloc(tail, S::kColumns);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
@@ -410,6 +415,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
                 for (int i = g.begin; i < g.end; ++i) {
                     const int head = g.head * a.group + i / a.q_tiles, row0 = i % a.q_tiles * kRowTile;
                     for (int half = 0; half < 2; ++half, ++n) {
+                        if (guard.stop()) goto done;
                         const uint32_t stage = n % S::kStages, round = n / S::kStages;
                         if (round > 0) barrier_wait(bar.ring_free + 8 * stage, (round - 1) & 1, guard);
                         const uint32_t full = bar.ring + 8 * stage, to = s_ring + stage * S::kTileBytes;
@@ -431,14 +437,14 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
             const int steps = (a.dim + 15) / 16;
             auto stage_at = [&](uint32_t x) { return s_ring + x % S::kStages * S::kTileBytes; };
             auto await = [&](uint32_t x) {
-                barrier_wait(bar.ring + 8 * (x % S::kStages), x / S::kStages & 1, guard);
+                barrier_wait_warp(bar.ring + 8 * (x % S::kStages), x / S::kStages & 1, guard);
                 tmem_fence_after();
             };
             auto release = [&](uint32_t x) { product_commit(leader, bar.ring_free + 8 * (x % S::kStages)); };
             uint32_t n = 0, seg = 0, step = 0;
             while (walk.next(g)) {
                 if (g.tile * kKeyTile >= g.length) continue;
-                barrier_wait(bar.own, seg & 1, guard);
+                barrier_wait_warp(bar.own, seg & 1, guard);
                 auto scores = [&](uint32_t x) {
                     await(x);
                     product_rows<HD>(leader, tmem + S::kS, s_own, stage_at(x), form_s, steps);
@@ -453,11 +459,11 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
                 dp(n + 1);
                 for (int i = g.begin; i < g.end; ++i, n += 2, ++step) {
                     const bool more = i + 1 < g.end;
-                    barrier_wait(bar.p_ready, step & 1, guard);
+                    barrier_wait_warp(bar.p_ready, step & 1, guard);
                     tmem_fence_after();
                     product_across<0, 8>(leader, tmem + kOutV, tmem + S::kS, stage_at(n + 1), form_o, i > g.begin, kGroups);
                     if (more) scores(n + 2);
-                    barrier_wait(bar.ready, step & 1, guard);
+                    barrier_wait_warp(bar.ready, step & 1, guard);
                     tmem_fence_after();
                     product_across<0, 8>(leader, tmem + kOutK, tmem + S::kDp, stage_at(n), form_o, i > g.begin, kGroups);
                     release(n);
@@ -495,8 +501,8 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
                     Columns r;
                     uint32_t packed[kColumnsEach / 2];
                     float2 p[kColumnsEach / 2];
-                    barrier_wait(bar.ring + 8 * (n % S::kStages), n / S::kStages & 1, guard);   // lse2
-                    barrier_wait(bar.s, step & 1, guard);
+                    barrier_wait_warp(bar.ring + 8 * (n % S::kStages), n / S::kStages & 1, guard);   // lse2
+                    barrier_wait_warp(bar.s, step & 1, guard);
                     tmem_fence_after();
                     load_columns(r, at_s);
 #pragma unroll
@@ -520,8 +526,8 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
                     tmem_fence_before();
                     __syncwarp();
                     if (lane == 0) barrier_arrive(bar.p_ready);
-                    barrier_wait(bar.ring + 8 * ((n + 1) % S::kStages), (n + 1) / S::kStages & 1, guard);   // delta
-                    barrier_wait(bar.dp, step & 1, guard);
+                    barrier_wait_warp(bar.ring + 8 * ((n + 1) % S::kStages), (n + 1) / S::kStages & 1, guard);   // delta
+                    barrier_wait_warp(bar.dp, step & 1, guard);
                     tmem_fence_after();
                     load_columns(r, at_dp);
 #pragma unroll
@@ -541,7 +547,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
                     __syncwarp();
                     if (lane == 0) barrier_arrive(bar.ready);
                 }
-                barrier_wait(bar.done, seg++ & 1, guard);
+                barrier_wait_warp(bar.done, seg++ & 1, guard);
                 tmem_fence_after();
             }
             // Rows behind the item's keys are zeros; packed ones have no place of their own.
@@ -557,6 +563,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
                     if (any) {
                         tmem_load32(o, tmem + lanes + (which ? kOutV : kOutK) + x);
                         tmem_wait_load();
+                        pin(o);
                     } else {
 #pragma unroll
                         for (int y = 0; y < 32; ++y) o[y] = 0;
@@ -586,13 +593,14 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
             tmem_fence_before();
         }
     }
+done:
     __syncwarp();
     drain_if_aborted(guard);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
     __syncwarp();
-    if (warp == kComputeWarps + 1) tmem_free(tmem, S::kColumns);
+    if (warp == kComputeWarps + 2) tmem_free(tmem, S::kColumns);
 }
 
 // ---- sums of cut tiles' parts -----------------------------------------------------------

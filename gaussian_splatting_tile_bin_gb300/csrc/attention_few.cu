@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(kFewThreads) k_attention_few(const __grid_cons
     if (warp == kWarps) {
         if (elect_one()) {
             for (int i = first; i < last; ++i) {
+                if (guard.stop()) goto done;
                 const int n = i - first, stage = n % kStages, round = n / kStages;
                 if (round > 0) barrier_wait(b_free + 8 * stage, (round - 1) & 1, guard);
                 const uint32_t bar = b_full + 8 * stage, to = ring + stage * S::kStageBytes;
@@ -147,7 +148,6 @@ __global__ void __launch_bounds__(kFewThreads) k_attention_few(const __grid_cons
                 }
             }
         }
-        __syncwarp();
     } else {
         uint32_t q[HD / 16][4];
 #pragma unroll
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kFewThreads) k_attention_few(const __grid_cons
             const int n = i - first, stage = n % kStages;
             const uint32_t live = __ballot_sync(~0u, valid) & 0xffff;
             valid = takes_part(i + 1);
-            barrier_wait(b_full + 8 * stage, n / kStages & 1, guard);
+            barrier_wait_warp(b_full + 8 * stage, n / kStages & 1, guard);
             const uint32_t at_k = ring + stage * S::kStageBytes, at_v = at_k + S::kTileBytes;
             float s[2][4] = {};
 #pragma unroll
@@ -231,6 +231,10 @@ __global__ void __launch_bounds__(kFewThreads) k_attention_few(const __grid_cons
         }
     }
 
+done:
+    __syncwarp();
+    drain_if_aborted(guard);
+
     // The four warps' parts: [warp][row][dim], then maxima and sums, over the ring
     // (every copy has landed: each was waited for by every warp).
     __syncthreads();
@@ -278,7 +282,6 @@ __global__ void __launch_bounds__(kFewThreads) k_attention_few(const __grid_cons
             if (d == 0) a.partial_lse[part] = lse;
         }
     }
-    drain_if_aborted(guard);
 }
 
 // Joins the splits of a row, one warp a row, four dimensions a lane.

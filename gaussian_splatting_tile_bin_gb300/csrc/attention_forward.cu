@@ -3,7 +3,7 @@
 //
 //   s = scale q . k,  o = sum exp(s - m) v / l,  l = sum exp(s - m),  lse = m + log l
 //
-// One pass over the keys with the running maximum m and sum l of each row.  A
+// One pass over the keys with a running reference m and sum l of each row.  A
 // block holds two tiles of 128 query rows, each with its own 128 threads (one
 // row a thread) and its own score and output accumulators in tensor memory.  One
 // thread issues the products: scores S = Q K^T (operands in shared memory) and
@@ -12,10 +12,13 @@
 // for the other tile, so both pipes stay busy.  K and V tiles arrive by bulk
 // tensor copies through a ring of stages.
 //
-// The output is rescaled only when a row's maximum grows by more than 2^8: until
-// then P exceeds 1 by at most that factor, which 16-bit P and float sums hold
-// without loss.  P is rounded to the storage type (the tensor cores take 16-bit
-// operands at the full rate); l sums the unrounded values in float.
+// m is the maximum of the row's first keys.  It moves only when some keys' sum of
+// exp(s - m) exceeds 2^12, which tells that without a maximum of every tile (the
+// comparisons took a third of the softmax' time): the row then takes its true
+// maximum and the sum and the output so far are rescaled.  Until then P exceeds 1 by at
+// most that factor, which 16-bit P and float sums hold without loss.  P is
+// rounded to the storage type (the tensor cores take 16-bit operands at the full
+// rate); l sums the unrounded values in float.
 #include <math.h>
 
 #include "attention.cuh"
@@ -26,6 +29,7 @@ namespace {
 constexpr int kRowTile = 128;
 constexpr int kForwardThreads = 384;   // two row groups of 128; four warps of which one copies and one issues
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLargestSum = 4096.0f;
 
 struct ForwardArgs {
     CUtensorMap q, k, v;
@@ -46,7 +50,7 @@ struct ForwardShape {
     static constexpr int kBlocks = HD / 64;
     static constexpr int kTileBytes = kBlocks * kBlockBytes;
     static constexpr int kStages = HD == 128 ? 5 : 8;
-    static constexpr int kBarriers = 2 + 2 * kStages + 8;
+    static constexpr int kBarriers = 2 + 2 * kStages + 6;
     static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + kBarriers * 8 + 16;
     static constexpr int kOut = 256;   // tensor memory column of the outputs
     static constexpr int kColumns = 512;
@@ -62,7 +66,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
     const uint32_t base = (raw + 1023) & ~1023u;
     const uint32_t s_q = base, s_kv = base + 2 * S::kTileBytes, bars = s_kv + S::kStages * S::kTileBytes;
     const uint32_t b_q = bars, b_q_free = bars + 8, b_kv = bars + 16, b_kv_free = b_kv + 8 * S::kStages;
-    const uint32_t b_s = b_kv_free + 8 * S::kStages, b_p = b_s + 16, b_p2 = b_p + 16, b_o = b_p2 + 16, tail = b_o + 16;
+    const uint32_t b_s = b_kv_free + 8 * S::kStages, b_p = b_s + 16, b_o = b_p + 16, tail = b_o + 16;
     uint32_t *s_words = (uint32_t *)(s_raw + (tail - raw));   // tensor memory base, abort flag
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const WaitGuard guard = {s_words + 1, a.status};
@@ -75,16 +79,15 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
             barrier_init(b_kv + 8 * i, 1);
             barrier_init(b_kv_free + 8 * i, 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 2; ++i) {   // of a row tile
             barrier_init(b_s + 8 * i, 1);
             barrier_init(b_p + 8 * i, 4);
-            barrier_init(b_p2 + 8 * i, 4);
             barrier_init(b_o + 8 * i, 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async();
     }
-    if (warp == 9) tmem_alloc(tail, S::kColumns);
+    if (warp == 10) tmem_alloc(tail, S::kColumns);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
@@ -116,6 +119,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
                                  head * a.q_head, g.item * a.q_item);
                 for (int i = g.begin; i < g.end; ++i)
                     for (int half = 0; half < 2; ++half, ++kv) {
+                        if (guard.stop()) goto done;
                         const uint32_t stage = kv % S::kStages, round = kv / S::kStages;
                         if (round > 0) barrier_wait(b_kv_free + 8 * stage, (round - 1) & 1, guard);
                         const uint32_t bar = b_kv + 8 * stage, to = s_kv + stage * S::kTileBytes;
@@ -129,55 +133,46 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
         }
     } else if (warp == 9) {
         // ---- products ----
-        {
-            const bool leader = elect_one();
-            const uint32_t form_s = product_form<T>(kKeyTile, false);
-            const uint32_t form_o = product_form<T>((a.dim + 15) & ~15, true);
-            const int steps = (a.dim + 15) / 16;
-            uint32_t kv = 0, seg = 0, p[2] = {0, 0};
-            while (walk.next(g)) {
-                if (g.length == 0) continue;
-                const int head = g.tile / row_tiles, row0 = (g.tile - head * row_tiles) * 2 * kRowTile;
-                const int tiles = a.q_len - row0 > kRowTile ? 2 : 1;
-                barrier_wait(b_q, seg & 1, guard);
-                auto stage_at = [&](uint32_t n) { return s_kv + n % S::kStages * S::kTileBytes; };
-                auto await = [&](uint32_t n) {
-                    barrier_wait(b_kv + 8 * (n % S::kStages), n / S::kStages & 1, guard);
-                };
-                auto release = [&](uint32_t n) { product_commit(leader, b_kv_free + 8 * (n % S::kStages)); };
-                await(kv);
-                tmem_fence_after();
+        const bool leader = elect_one();
+        const uint32_t form_s = product_form<T>(kKeyTile, false);
+        const uint32_t form_o = product_form<T>((a.dim + 15) & ~15, true);
+        const int steps = (a.dim + 15) / 16;
+        uint32_t kv = 0, seg = 0, p[2] = {0, 0};
+        auto stage_at = [&](uint32_t n) { return s_kv + n % S::kStages * S::kTileBytes; };
+        auto await = [&](uint32_t n) { barrier_wait_warp(b_kv + 8 * (n % S::kStages), n / S::kStages & 1, guard); };
+        auto release = [&](uint32_t n) { product_commit(leader, b_kv_free + 8 * (n % S::kStages)); };
+        auto scores = [&](int t, uint32_t n) {
+            product_rows<HD>(leader, tmem + t * kKeyTile, s_q + t * S::kTileBytes, stage_at(n), form_s, steps);
+            product_commit(leader, b_s + 8 * t);
+        };
+        while (walk.next(g)) {
+            if (g.length == 0) continue;
+            const int head = g.tile / row_tiles, row0 = (g.tile - head * row_tiles) * 2 * kRowTile;
+            const int tiles = a.q_len - row0 > kRowTile ? 2 : 1;
+            barrier_wait_warp(b_q, seg & 1, guard);
+            await(kv);
+            tmem_fence_after();
+            for (int t = 0; t < tiles; ++t) scores(t, kv);
+            release(kv);
+            for (int i = g.begin; i < g.end; ++i, kv += 2) {
+                const bool more = i + 1 < g.end;
+                await(kv + 1);
                 for (int t = 0; t < tiles; ++t) {
-                    product_rows<HD>(leader, tmem + t * kKeyTile, s_q + t * S::kTileBytes, stage_at(kv), form_s, steps);
-                    product_commit(leader, b_s + 8 * t);
-                }
-                release(kv);
-                for (int i = g.begin; i < g.end; ++i, kv += 2) {
-                    const bool more = i + 1 < g.end;
-                    await(kv + 1);
-                    if (more) await(kv + 2);
-                    for (int t = 0; t < tiles; ++t) {
-                        const uint32_t o = tmem + S::kOut + t * HD, p_at = tmem + t * kKeyTile;
-                        barrier_wait(b_p + 8 * t, p[t] & 1, guard);
-                        tmem_fence_after();
-                        product_across<0, 4>(leader, o, p_at, stage_at(kv + 1), form_o, i > g.begin);
-                        barrier_wait(b_p2 + 8 * t, p[t]++ & 1, guard);
-                        tmem_fence_after();
-                        product_across<4, 8>(leader, o, p_at, stage_at(kv + 1), form_o, true);
-                        if (more) {
-                            product_rows<HD>(leader, tmem + t * kKeyTile, s_q + t * S::kTileBytes, stage_at(kv + 2), form_s,
-                                         steps);
-                            product_commit(leader, b_s + 8 * t);
-                        } else {
-                            product_commit(leader, b_o + 8 * t);
-                        }
+                    barrier_wait_warp(b_p + 8 * t, p[t]++ & 1, guard);
+                    tmem_fence_after();
+                    product_across<0, 8>(leader, tmem + S::kOut + t * HD, tmem + t * kKeyTile, stage_at(kv + 1), form_o,
+                                         i > g.begin);
+                    product_commit(leader, b_o + 8 * t);
+                    if (more) {
+                        if (t == 0) await(kv + 2);
+                        scores(t, kv + 2);
                     }
-                    release(kv + 1);
-                    if (more) release(kv + 2);
                 }
-                product_commit(leader, b_q_free);
-                ++seg;
+                release(kv + 1);
+                if (more) release(kv + 2);
             }
+            product_commit(leader, b_q_free);
+            ++seg;
         }
     }
     } else {
@@ -185,10 +180,11 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
         // ---- softmax: one row a thread ----
         const int t = warp / 4;                                     // row tile
         const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;     // this warp's lanes of tensor memory
-        const uint32_t at_s = tmem + lanes + t * kKeyTile, at_o = tmem + lanes + S::kOut + t * HD;
+        const uint32_t at_o = tmem + lanes + S::kOut + t * HD;
         const int row_in_tile = warp % 4 * 32 + lane;
         const float c = a.scale_log2;
-        uint32_t kv = 0, n_s = 0, n_o = 0;
+        const uint32_t at_s = tmem + lanes + t * kKeyTile;
+        uint32_t kv = 0, n = 0;   // ring position; key tiles this row tile has seen
         while (walk.next(g)) {
             const int head = g.tile / row_tiles, row0 = (g.tile - head * row_tiles) * 2 * kRowTile + t * kRowTile;
             const int row = row0 + row_in_tile;
@@ -196,94 +192,106 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
             float m = -INFINITY, l = 0.0f;
             const bool active = row0 < a.q_len;
             if (g.length > 0 && active) {
-                for (int i = g.begin; i < g.end; ++i) {
-                    barrier_wait(b_s + 8 * t, n_s++ & 1, guard);
+                for (int i = g.begin; i < g.end; ++i, ++n) {
+                    barrier_wait_warp(b_s + 8 * t, n & 1, guard);
                     tmem_fence_after();
+                    // The second half of the scores arrives while the first is worked on.
                     uint32_t r[4][32];
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) tmem_load32(r[x], at_s + x * 32);
+                    tmem_load32(r[0], at_s);
+                    tmem_load32(r[1], at_s + 32);
                     tmem_wait_load();
+                    pin(r[0]);
+                    pin(r[1]);
+                    tmem_load32(r[2], at_s + 64);
+                    tmem_load32(r[3], at_s + 96);
                     const int valid = g.length - i * kKeyTile;
-                    if (valid < kKeyTile) {
+                    const bool ragged = valid < kKeyTile;
+                    if (ragged && t == 0) {
+                        // What lies behind the item's last key must not meet the zero
+                        // probabilities as infinities or NaN.
+                        const uint32_t at_v = kv + 2 * (i - g.begin) + 1;
+                        barrier_wait_warp(b_kv + 8 * (at_v % S::kStages), at_v / S::kStages & 1, guard);
+                        if (row_in_tile >= valid) {
+                            unsigned char *v = s_raw + (s_kv - raw) + at_v % S::kStages * S::kTileBytes +
+                                               row_in_tile * 128;
+                            for (int b = 0; b < S::kBlocks; ++b)
+                                for (int e = 0; e < 8; ++e)
+                                    *(uint4 *)(v + b * kBlockBytes + e * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        fence_async();
+                    }
+                    auto clear_ragged = [&](int h) {
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
+                        for (int x = 0; x < 2; ++x)
 #pragma unroll
                             for (int y = 0; y < 32; ++y)
-                                if (x * 32 + y >= valid) r[x][y] = __float_as_uint(-INFINITY);
-                        if (t == 0) {
-                            // What lies behind the item's last key must not meet the
-                            // zero probabilities as infinities or NaN.
-                            const uint32_t n = kv + 2 * (i - g.begin) + 1;
-                            barrier_wait(b_kv + 8 * (n % S::kStages), n / S::kStages & 1, guard);
-                            if (row_in_tile >= valid) {
-                                unsigned char *v = s_raw + (s_kv - raw) + n % S::kStages * S::kTileBytes +
-                                                   row_in_tile * 128;
-                                for (int b = 0; b < S::kBlocks; ++b)
-                                    for (int e = 0; e < 8; ++e)
-                                        *(uint4 *)(v + b * kBlockBytes + e * 16) = make_uint4(0, 0, 0, 0);
+                                if (h * 64 + x * 32 + y >= valid) r[2 * h + x][y] = __float_as_uint(-INFINITY);
+                    };
+                    auto largest = [&](int h) {
+                        float part[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+#pragma unroll
+                            for (int y = 0; y < 32; ++y)
+                                part[y % 4] = fmaxf(part[y % 4], __uint_as_float(r[2 * h + x][y]));
+                        return fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+                    };
+                    // exp(s - m) of 64 keys into tensor memory, and their sum.
+                    auto exponentials = [&](int h) {
+                        const float shift = m == -INFINITY ? 0.0f : -m * c;
+                        const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
+                        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            uint32_t packed[16];
+#pragma unroll
+                            for (int y = 0; y < 32; y += 2) {
+                                float2 e = fma2(make_float2(__uint_as_float(r[2 * h + x][y]),
+                                                            __uint_as_float(r[2 * h + x][y + 1])),
+                                                c2, shift2);
+                                e.x = exp2_fast(e.x);
+                                e.y = exp2_fast(e.y);
+                                sum[y / 2 & 1] = add2(sum[y / 2 & 1], e);
+                                packed[y / 2] = pack2<T>(e.x, e.y);
                             }
-                            fence_async();
+                            tmem_store16(at_s + h * 32 + x * 16, packed);
                         }
-                    }
-                    // Eight chains: a row's maximum is on the path between two products.
-                    float part[8];
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) part[x] = __uint_as_float(r[x / 2][x % 2]);
-#pragma unroll
-                    for (int y = 2; y < 32; y += 2)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            part[2 * x] = fmaxf(part[2 * x], __uint_as_float(r[x][y]));
-                            part[2 * x + 1] = fmaxf(part[2 * x + 1], __uint_as_float(r[x][y + 1]));
-                        }
-                    const float top = fmaxf(fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3])),
-                                            fmaxf(fmaxf(part[4], part[5]), fmaxf(part[6], part[7])));
-                    if (i == g.begin) {
-                        m = top;
-                    } else if (__any_sync(~0u, top * c > m * c + 8.0f)) {
-                        const float next = fmaxf(m, top);
+                        return (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+                    };
+                    if (ragged) clear_ragged(0);
+                    if (i == g.begin) m = largest(0);
+                    float sum = exponentials(0);
+                    tmem_wait_load();
+                    pin(r[2]);
+                    pin(r[3]);
+                    if (ragged) clear_ragged(1);
+                    sum += exponentials(1);
+                    if (__any_sync(~0u, sum > kLargestSum)) {
+                        const float next = fmaxf(m, fmaxf(largest(0), largest(1)));
                         const float keep = exp2_fast((m - (next == -INFINITY ? 0.0f : next)) * c);
                         m = next;
                         l *= keep;
-                        for (int x = 0; x < HD; x += 32) {
-                            uint32_t o[32];
-                            tmem_load32(o, at_o + x);
-                            tmem_wait_load();
+                        // The products of the keys before are complete: these scores came behind them.
+                        if (i > g.begin)
+                            for (int x = 0; x < HD; x += 32) {
+                                uint32_t o[32];
+                                tmem_load32(o, at_o + x);
+                                tmem_wait_load();
+                                pin(o);
 #pragma unroll
-                            for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * keep);
-                            tmem_store32(at_o + x, o);
-                        }
+                                for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * keep);
+                                tmem_store32(at_o + x, o);
+                            }
+                        sum = exponentials(0);
+                        sum += exponentials(1);
                     }
-                    const float shift = m == -INFINITY ? 0.0f : -m * c;
-                    const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
-                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        uint32_t packed[16];
-#pragma unroll
-                        for (int y = 0; y < 32; y += 2) {
-                            float2 e = fma2(make_float2(__uint_as_float(r[x][y]), __uint_as_float(r[x][y + 1])), c2,
-                                            shift2);
-                            e.x = exp2_fast(e.x);
-                            e.y = exp2_fast(e.y);
-                            sum[y / 2 & 1] = add2(sum[y / 2 & 1], e);
-                            packed[y / 2] = pack2<T>(e.x, e.y);
-                        }
-                        if (x == 2) {   // the first 64 keys' stores have had the time of 32 exponentials
-                            tmem_wait_store();
-                            tmem_fence_before();
-                            __syncwarp();
-                            if (lane == 0) barrier_arrive(b_p + 8 * t);
-                        }
-                        tmem_store16(at_s + x * 16, packed);
-                    }
+                    l += sum;
                     tmem_wait_store();
                     tmem_fence_before();
                     __syncwarp();
-                    if (lane == 0) barrier_arrive(b_p2 + 8 * t);
-                    l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+                    if (lane == 0) barrier_arrive(b_p + 8 * t);
                 }
-                barrier_wait(b_o + 8 * t, n_o++ & 1, guard);
+                barrier_wait_warp(b_o + 8 * t, (n - 1) & 1, guard);
                 tmem_fence_after();
             }
             if (g.length > 0) kv += 2 * (g.end - g.begin);
@@ -301,6 +309,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
                 if (g.length > 0) {
                     tmem_load32(o, at_o + x);
                     tmem_wait_load();
+                    pin(o);
                 } else {
 #pragma unroll
                     for (int y = 0; y < 32; ++y) o[y] = 0;
@@ -331,13 +340,14 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
             tmem_fence_before();
         }
     }
+done:
     __syncwarp();
     drain_if_aborted(guard);
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
     __syncwarp();
-    if (warp == 9) tmem_free(tmem, S::kColumns);
+    if (warp == 10) tmem_free(tmem, S::kColumns);
 }
 
 // Joins the parts of a cut tile: weights exp(lse_part - lse).  Block x handles the

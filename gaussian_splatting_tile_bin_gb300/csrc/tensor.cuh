@@ -58,14 +58,17 @@ __device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity)
 }
 
 // Waits end: one that has run for kWaitCycles (seconds; a step takes
-// microseconds) marks the block as aborted, reports to the host's status word
-// and returns, and every later wait of the block returns at once, so the kernel
-// runs to its end with results that the host then refuses.
+// microseconds) marks the block as aborted and reports to the host's status
+// word, and every later wait of the block returns at once: the copying thread
+// then stops (its barriers could not count copies that nothing waits for), the
+// others run through the rest of their loops, and the host refuses the results.
 constexpr long long kWaitCycles = 4000000000ll;
 
 struct WaitGuard {
     volatile uint32_t *aborted;   // shared
     uint32_t *status;             // the context's status word (host memory)
+
+    __device__ __forceinline__ bool stop() const { return *aborted != 0; }
 };
 
 __device__ __forceinline__ void barrier_wait(uint32_t bar, uint32_t parity, const WaitGuard &g)
@@ -80,6 +83,16 @@ __device__ __forceinline__ void barrier_wait(uint32_t bar, uint32_t parity, cons
             return;
         }
     }
+}
+
+// The same for a whole warp, which leaves it converged: its lanes may see the
+// barrier turn at different tries, and warp-wide instructions on tensor memory or
+// matrix fragments are undefined for lanes that have come apart.  So may a lane
+// fall two phases behind, and wait for one that has gone.
+__device__ __forceinline__ void barrier_wait_warp(uint32_t bar, uint32_t parity, const WaitGuard &g)
+{
+    barrier_wait(bar, parity, g);
+    __syncwarp();
 }
 
 // At the end of an aborted block: time for copies and products in flight to land
@@ -133,8 +146,19 @@ __device__ __forceinline__ void tmem_free(uint32_t base, uint32_t columns)
 
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// (The registers of a load hold their values only behind this wait: `pin` keeps
+// their uses there.)
 __device__ __forceinline__ void tmem_wait_load() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void pin(uint32_t (&r)[32])
+{
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+        asm volatile(""
+                     : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                       "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
 
 // 32 columns of the calling thread's lane.
 __device__ __forceinline__ void tmem_load32(uint32_t (&r)[32], uint32_t at)

@@ -116,6 +116,25 @@ def test_long(gsr, ctx, lq, lk):
     _compare(gsr, ctx, *_inputs(1, lq, lk, 2, 1, 128, BF16, lk), lengths=torch.tensor([lk - 3], dtype=torch.int32))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d", [40, 64, 128])
+@pytest.mark.parametrize("b,hq,hk,lq,lk,lengths", [(2, 8, 4, 600, 1000, None), (3, 8, 8, 520, 1300, [1300, 0, 401]),
+                                                   (1, 16, 4, 1100, 2100, None), (5, 12, 12, 260, 140, [140, 1, 128, 129, 77])])
+def test_many_tiles(gsr, ctx, dtype, d, b, hq, hk, lq, lk, lengths):
+    """Several steps per tile and several tiles per SM, whole and cut."""
+    lengths = None if lengths is None else torch.tensor(lengths, dtype=torch.int32)
+    _compare(gsr, ctx, *_inputs(b, lq, lk, hq, hk, d, dtype, d + lq), lengths=lengths)
+
+
+def test_growing_scores_over_many_tiles(gsr, ctx):
+    """Scores that grow along the keys, tile after tile, and rows that grow alone."""
+    for d in (64, 128):
+        q, k, v, dout = _inputs(1, 700, 1500, 8, 8, d, BF16, d)
+        k = (k * torch.linspace(0.1, 12.0, 1500)[None, :, None, None]).to(BF16)
+        q[:, ::37] *= 4.0
+        _compare(gsr, ctx, q, k, v, dout)
+
+
 def test_large_scores(gsr, ctx):
     """Scores of several hundred: one key takes a row, and the running maximum moves late."""
     q, k, v, dout = _inputs(1, 200, 400, 2, 2, 64, F16, 3, size=30.0)
