@@ -44,7 +44,8 @@ struct RangeShift {
 struct BackwardArgs {
     CUtensorMap q, k, v, dout;
     Schedule work;
-    const float *lse2, *delta;   // [batch, q_heads, q_pad]: log2(shift.p) - lse log2e, -delta shift.ds / shift.p
+    const float *lse2;           // [batch, q_heads, q_pad]: log2(shift.p) - lse log2e
+    float *delta;                // the same: -delta shift.ds / shift.p
     const RangeShift *shift;
     void *dq, *dk, *dv;
     int64_t dq_item, dq_token, dq_head, dk_item, dk_token, dk_head, dv_item, dv_token, dv_head;
@@ -64,9 +65,10 @@ struct BackwardShape {
     static constexpr int kStages = HD == 128 ? 5 : 8;
     static constexpr int kStatBytes = kRowTile * 4;   // a query tile's lse2 (with Q) or delta (with dO)
     static constexpr int kBarriers = 2 + 2 * kStages + 6;
-    static constexpr int kSmemQ = (2 + kStages) * kTileBytes + kBarriers * 8 + 16;
-    static constexpr int kSmemK = kSmemQ + kStages * kStatBytes;
-    static_assert(kSmemK <= 232448, "more shared memory than a block can have");
+    static constexpr int kSmemBoth = (2 + kStages) * kTileBytes + kBarriers * 8 + 16;
+    static constexpr int kSmemQ = kSmemBoth + kGroups * kStatBytes;   // sums of a row
+    static constexpr int kSmemK = kSmemBoth + kStages * kStatBytes;   // statistics of a stage
+    static_assert(kSmemK <= 232448 && kSmemQ <= 232448, "more shared memory than a block can have");
     static constexpr int kS = 0, kDp = 128, kOut = 256, kDs = 384;   // tensor memory columns
     static constexpr int kColumns = 512;
 };
@@ -159,6 +161,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
     const Bars<HD> bar(at_bars);
     const uint32_t tail = at_bars + S::kBarriers * 8;
     uint32_t *s_words = (uint32_t *)(s_raw + (tail - raw));
+    float *s_sum = (float *)(s_words + 4);   // [part][row]
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const WaitGuard guard = {s_words + 1, a.status};
     if (threadIdx.x == 0) {
@@ -265,7 +268,8 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                 const int64_t at = ((int64_t)g.item * a.q_heads + head) * a.q_pad + row;
                 const float2 c2 = make_float2(c, c), f2 = make_float2(f_dp, f_dp);
                 const float lse = a.lse2[at], delta = a.delta[at];
-                const float2 lse2 = make_float2(lse, lse), delta2 = make_float2(delta, delta);
+                const float2 lse2 = make_float2(lse, lse);
+                float2 delta2 = make_float2(delta, delta);
                 for (int i = g.begin; i < g.end; ++i, n += 2, ++step) {
                     Columns r;
                     barrier_wait_warp(bar.s, step & 1, guard);
@@ -285,6 +289,24 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                     barrier_wait_warp(bar.dp, step & 1, guard);
                     tmem_fence_after();
                     load_columns(r, at_dp);
+                    if (g.total == 1) {
+                        // Few keys, whose ds nearly cancel: delta from p and dp themselves, here and
+                        // for the key gradients, instead of from the rounded output.
+                        float sum = 0.0f;
+#pragma unroll
+                        for (int y = 0; y < kColumnsEach / 2; ++y) {
+                            const float2 t = mul2(p[y], pair(r, 2 * y));
+                            sum += (column0 + 2 * y < valid ? t.x : 0.0f) + (column0 + 2 * y + 1 < valid ? t.y : 0.0f);
+                        }
+                        s_sum[part * kRowTile + row_in_tile] = sum;
+                        asm volatile("bar.sync 1, %0;" ::"n"(kComputeWarps * 32) : "memory");
+                        sum = 0.0f;
+#pragma unroll
+                        for (int x = 0; x < kGroups; ++x) sum += s_sum[x * kRowTile + row_in_tile];
+                        const float mine = -sum * (f_dp / shift.p);
+                        delta2 = make_float2(mine, mine);
+                        if (part == 0) a.delta[at] = mine;
+                    }
                     uint32_t packed[kColumnsEach / 2];
                     if (valid < kKeyTile) {
 #pragma unroll
@@ -819,23 +841,26 @@ int launch_backward(gsr_ctx *ctx, BackwardArgs &a, const Schedule &by_query, con
 {
     // Blocks of a cut tile's sum: its rows' vectors over a block's items.
     const int vectors = kRowTile * a.dim / 8, each = kSumBlock * kSumItems;
-    a.work = by_key;
-    if (int rc = launch_big(ctx, k_attention_grad_kv<T, HD>, "k_attention_grad_kv", blocks_k,
-                            BackwardShape<HD>::kSmemK, a, stream))
-        return rc;
-    if (blocks_k > 1)
-        if (int rc = cuda_check(ctx, launch_kernel(ctx, k_attention_sum_kv<T>, dim3((unsigned)blocks_k - 1, (unsigned)((2 * vectors + each - 1) / each)),
-                                                   kSumBlock, stream, a, blocks_k),
-                                "k_attention_sum_kv"))
-            return rc;
+    // Queries first: they correct delta where the keys are few.
     a.work = by_query;
     if (int rc = launch_big(ctx, k_attention_grad_q<T, HD>, "k_attention_grad_q", blocks_q, BackwardShape<HD>::kSmemQ, a,
                             stream))
         return rc;
-    if (blocks_q == 1) return GSR_OK;
-    return cuda_check(ctx, launch_kernel(ctx, k_attention_sum_q<T>, dim3((unsigned)blocks_q - 1, (unsigned)((vectors + each - 1) / each)), kSumBlock,
-                                         stream, a, blocks_q),
-                      "k_attention_sum_q");
+    if (blocks_q > 1 && a.kv_len > kKeyTile)   // tiles of one step are never cut
+        if (int rc = cuda_check(ctx, launch_kernel(ctx, k_attention_sum_q<T>,
+                                                   dim3((unsigned)blocks_q - 1, (unsigned)((vectors + each - 1) / each)),
+                                                   kSumBlock, stream, a, blocks_q),
+                                "k_attention_sum_q"))
+            return rc;
+    a.work = by_key;
+    if (int rc = launch_big(ctx, k_attention_grad_kv<T, HD>, "k_attention_grad_kv", blocks_k,
+                            BackwardShape<HD>::kSmemK, a, stream))
+        return rc;
+    if (blocks_k == 1 || by_key.inner == 1) return GSR_OK;
+    return cuda_check(ctx, launch_kernel(ctx, k_attention_sum_kv<T>,
+                                         dim3((unsigned)blocks_k - 1, (unsigned)((2 * vectors + each - 1) / each)), kSumBlock,
+                                         stream, a, blocks_k),
+                      "k_attention_sum_kv");
 }
 
 template <typename T>

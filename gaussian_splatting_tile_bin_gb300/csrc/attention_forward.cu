@@ -430,7 +430,7 @@ int launch_forward(gsr_ctx *ctx, ForwardArgs &a, int blocks, cudaStream_t stream
     if (int rc = cuda_check(ctx, launch_kernel_smem(ctx, kernel, dim3((unsigned)blocks), kForwardThreads, smem, stream, a),
                             "k_attention_forward"))
         return rc;
-    if (blocks == 1) return GSR_OK;
+    if (blocks == 1 || a.work.length <= kKeyTile) return GSR_OK;   // tiles of one step are never cut
     const int vectors = 2 * kRowTile * a.dim / 8, each = kJoinBlock * kJoinItems;
     return cuda_check(ctx, launch_kernel(ctx, k_attention_join<T>,
                                          dim3((unsigned)blocks - 1, (unsigned)((vectors + each - 1) / each)), kJoinBlock,

@@ -30,23 +30,13 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kNormBlock = 256;
-constexpr int kRun = 8;          // positions a thread reads at a time
+constexpr int kRun = 4;          // values whose mean and centred squares are taken together
 constexpr int kMergeBlock = 256;
-// Blocks an SM holds: one wave of them takes all chunks.
-constexpr int kNormOccupancy = 3, kNormGradOccupancy = 2;
+// Blocks an SM holds (their rings fill its shared memory): one wave of them takes
+// all chunks.
+constexpr int kNormOccupancy = 4, kNormGradOccupancy = 2;
 
-// Accesses that nothing follows: the result, and the second pass' inputs.
-template <typename T, int V>
-__device__ __forceinline__ Vec<T, V> load_last(const T *p)
-{
-    if constexpr (sizeof(T) * V == 16) {
-        const uint4 r = __ldcs((const uint4 *)p);
-        return *(const Vec<T, V> *)&r;
-    } else {
-        return *(const Vec<T, V> *)p;
-    }
-}
-
+// A result, which nothing here reads again.
 template <typename T, int V>
 __device__ __forceinline__ void store_last(T *p, const Vec<T, V> &v)
 {
@@ -136,7 +126,7 @@ __device__ __forceinline__ Moments merge(const Moments &a, const Moments &b)
 template <typename T, int V>
 struct ChannelMoments {
     float n = 0.0f, mean[V] = {}, m2[V] = {};
-    __device__ __forceinline__ void add(const Vec<T, V> (&v)[kRun])
+    __device__ __forceinline__ void add(const Vec<T, V>(&v)[kRun])
     {
         const float total = n + kRun, share = __fdividef(kRun, total);
 #pragma unroll
@@ -165,49 +155,6 @@ struct ChannelMoments {
         }
     }
 };
-
-// Per channel and chunk of positions: (mean, M2) of x.
-template <typename T, int V>
-__global__ void __launch_bounds__(kNormBlock, kNormOccupancy) k_norm_moments(const NormArgs a)
-{
-    grid_dependency_begin();
-    __shared__ float s_mean[kNormBlock * V], s_m2[kNormBlock * V], s_n[kNormBlock];
-    const int cols = a.vectors;
-    const int col = threadIdx.x % cols, row = threadIdx.x / cols, rows = kNormBlock / cols;
-    const int vec = blockIdx.z * cols + col;
-    const int sample = a.sample0 + blockIdx.y;
-    const int64_t p0 = (int64_t)blockIdx.x * a.rows_per_chunk;
-    const int64_t p1 = min(a.positions, p0 + a.rows_per_chunk);
-    const bool live = row < rows && vec * V < a.channels;
-    ChannelMoments<T, V> own;
-    if (live) {
-        const T *x = (const T *)a.x + (int64_t)sample * a.positions * a.channels + (int64_t)vec * V;
-        int64_t p = p0 + row;
-        for (; p + (int64_t)(kRun - 1) * rows < p1; p += (int64_t)kRun * rows) {
-            Vec<T, V> v[kRun];
-#pragma unroll
-            for (int k = 0; k < kRun; ++k) v[k] = *(const Vec<T, V> *)(x + (p + (int64_t)k * rows) * a.channels);
-            own.add(v);
-        }
-        for (; p < p1; p += rows) own.add(*(const Vec<T, V> *)(x + p * a.channels));
-    }
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        s_mean[threadIdx.x * V + j] = own.mean[j];
-        s_m2[threadIdx.x * V + j] = own.m2[j];
-    }
-    s_n[threadIdx.x] = own.n;
-    __syncthreads();
-    float2 *out = a.partial + ((int64_t)blockIdx.y * a.chunks + blockIdx.x) * a.channels + (int64_t)blockIdx.z * cols * V;
-    for (int c = threadIdx.x; c < cols * V && (int)(blockIdx.z * cols * V) + c < a.channels; c += kNormBlock) {
-        Moments m = {0.0f, 0.0f, 0.0f};
-        for (int r = 0; r < rows; ++r) {
-            const int t = r * cols + c / V;
-            m = merge(m, {s_n[t], s_mean[t * V + c % V], s_m2[t * V + c % V]});
-        }
-        out[c] = make_float2(m.mean, m.m2);
-    }
-}
 
 __device__ __forceinline__ float block_sum(float x, float *s_warp)
 {
@@ -342,50 +289,156 @@ __device__ __forceinline__ void input_gradient(const Channel<V> &c, const float2
     }
 }
 
-// Walks a thread's rows p0 + row, + rows, ... below p1, kUnroll at a time.
-constexpr int kUnroll = 8;
+// A thread's rows through a ring of its own in shared memory: asynchronous copies
+// of kUnroll rows of each of N arrays, kDepth - 1 batches ahead, so that the loads
+// in flight do not depend on registers and no thread waits for another.  f is
+// called with a batch: its first row's number, how many rows, and the values.
+// Scalar accesses (which have no such copies) are read directly.
+constexpr int kUnroll = 4;
+constexpr int kDepth = 3;
+static_assert(kUnroll == kRun, "a batch is a run of the moments");
 
-// out = act((x - mean) rstd w + b).
+__device__ __forceinline__ void copy16(void *to, const void *from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from)
+                 : "memory");
+}
+
+template <int N>
+constexpr size_t kRingBytes = (size_t)kNormBlock * 16 * kUnroll * kDepth * N;
+
+template <typename T, int V, int N, typename F>
+__device__ __forceinline__ void walk_rows(unsigned char *ring, const T *const (&from)[N], int64_t stride, int rows, F f)
+{
+    using Access = Vec<T, V>;
+    Access v[N][kUnroll];
+    if constexpr (sizeof(Access) == 16) {
+        Access *mine = (Access *)ring + threadIdx.x;
+        auto slot = [&](int batch, int n, int k) { return mine + (((batch % kDepth) * N + n) * kUnroll + k) * kNormBlock; };
+        const int batches = (rows + kUnroll - 1) / kUnroll;
+        auto issue = [&](int batch) {
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k)
+                if (batch * kUnroll + k < rows)
+#pragma unroll
+                    for (int n = 0; n < N; ++n)
+                        copy16(slot(batch, n, k), from[n] + (int64_t)(batch * kUnroll + k) * stride);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        for (int b = 0; b < kDepth - 1; ++b) issue(b);
+        for (int b = 0; b < batches; ++b) {
+            issue(b + kDepth - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+            const int count = min(kUnroll, rows - b * kUnroll);
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int k = 0; k < kUnroll; ++k)
+                    if (k < count) v[n][k] = *slot(b, n, k);
+            f(b * kUnroll, count, v);
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+    } else {
+        for (int b = 0; b < rows; b += kUnroll) {
+            const int count = min(kUnroll, rows - b);
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+#pragma unroll
+                for (int k = 0; k < kUnroll; ++k)
+                    if (k < count) v[n][k] = *(const Access *)(from[n] + (int64_t)(b + k) * stride);
+            f(b, count, v);
+        }
+    }
+}
+
+// The rows of a thread in the chunk, and its place.
+template <int V>
+struct RowWalk {
+    int sample, col, row, rows, vec, left;
+    int64_t first, last, stride;        // elements: the first and the last row's vector, and a row's distance
+    bool live;
+    __device__ RowWalk(const NormArgs &a)
+    {
+        col = threadIdx.x % a.vectors;
+        row = threadIdx.x / a.vectors;
+        rows = kNormBlock / a.vectors;
+        vec = blockIdx.z * a.vectors + col;
+        sample = a.sample0 + blockIdx.y;
+        const int64_t p0 = (int64_t)blockIdx.x * a.rows_per_chunk, p1 = min(a.positions, p0 + a.rows_per_chunk);
+        left = p0 + row < p1 ? (int)((p1 - p0 - row + rows - 1) / rows) : 0;
+        live = row < rows && vec * V < a.channels && left > 0;
+        stride = (int64_t)rows * a.channels;
+        first = ((int64_t)sample * a.positions + p0 + row) * a.channels + (int64_t)vec * V;
+        last = first + (left - 1) * stride;
+    }
+};
+
+// Per channel and chunk of positions: (mean, M2) of x.
+template <typename T, int V>
+__global__ void __launch_bounds__(kNormBlock, kNormOccupancy) k_norm_moments(const NormArgs a)
+{
+    grid_dependency_begin();
+    extern __shared__ __align__(16) unsigned char s_raw[];
+    const RowWalk<V> at(a);
+    ChannelMoments<T, V> own;
+    if (at.live) {
+        const T *const from[1] = {(const T *)a.x + at.first};
+        walk_rows<T, V, 1>(s_raw, from, at.stride, at.left, [&](int, int count, const Vec<T, V>(&v)[1][kUnroll]) {
+            if (count == kUnroll) {
+                own.add(v[0]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < kUnroll; ++k)
+                    if (k < count) own.add(v[0][k]);
+            }
+        });
+    }
+    __syncthreads();   // the ring becomes the threads' sums
+    float *s_mean = (float *)s_raw, *s_m2 = s_mean + kNormBlock * V, *s_n = s_m2 + kNormBlock * V;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        s_mean[threadIdx.x * V + j] = own.mean[j];
+        s_m2[threadIdx.x * V + j] = own.m2[j];
+    }
+    s_n[threadIdx.x] = own.n;
+    __syncthreads();
+    const int cols = a.vectors, c0 = blockIdx.z * cols * V;
+    float2 *out = a.partial + ((int64_t)blockIdx.y * a.chunks + blockIdx.x) * a.channels + c0;
+    for (int c = threadIdx.x; c < cols * V && c0 + c < a.channels; c += kNormBlock) {
+        Moments m = {0.0f, 0.0f, 0.0f};
+        for (int r = 0; r < at.rows; ++r) {
+            const int t = r * cols + c / V;
+            m = merge(m, {s_n[t], s_mean[t * V + c % V], s_m2[t * V + c % V]});
+        }
+        out[c] = make_float2(m.mean, m.m2);
+    }
+}
+
+// out = act((x - mean) rstd w + b), from the last row back: what the first pass
+// read last is what L2 still holds.
 template <typename T, int V, int ACT>
 __global__ void __launch_bounds__(kNormBlock, kNormOccupancy) k_norm_apply(const NormArgs a)
 {
     grid_dependency_begin();
-    const int cols = a.vectors;
-    const int col = threadIdx.x % cols, row = threadIdx.x / cols, rows = kNormBlock / cols;
-    const int vec = blockIdx.z * cols + col;
-    if (row >= rows || vec * V >= a.channels) return;
-    const int sample = a.sample0 + blockIdx.y;
-    const int64_t p0 = (int64_t)blockIdx.x * a.rows_per_chunk;
-    const int64_t p1 = min(a.positions, p0 + a.rows_per_chunk);
+    extern __shared__ __align__(16) unsigned char s_raw[];
+    const RowWalk<V> at(a);
+    if (!at.live) return;
     Affine<V> affine;
     {
         Channel<V> ch;
-        ch.load(a, sample, vec * V);
+        ch.load(a, at.sample, at.vec * V);
         affine.from(ch);
     }
-    if (p0 + row >= p1) return;
-    // From the last row back: what the first pass read last is what L2 still holds.
-    int left = (int)((p1 - p0 - row + rows - 1) / rows);   // rows of this thread
-    const int64_t first = ((int64_t)sample * a.positions + p0 + row + (int64_t)(left - 1) * rows) * a.channels +
-                          (int64_t)vec * V;
-    const int64_t stride = -(int64_t)rows * a.channels;
-    const T *x = (const T *)a.x + first;
-    T *y = (T *)a.y + first;
-    for (; left >= kUnroll; left -= kUnroll, x += kUnroll * stride, y += kUnroll * stride) {
-        Vec<T, V> v[kUnroll];
+    const T *const from[1] = {(const T *)a.x + at.last};
+    T *y = (T *)a.y + at.last;
+    walk_rows<T, V, 1>(s_raw, from, -at.stride, at.left, [&](int row, int count, Vec<T, V>(&v)[1][kUnroll]) {
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) v[k] = load_last<T, V>(x + k * stride);
-#pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            affine.template apply<T, ACT>(v[k]);
-            store_last<T, V>(y + k * stride, v[k]);
-        }
-    }
-    for (; left > 0; --left, x += stride, y += stride) {
-        Vec<T, V> v = load_last<T, V>(x);
-        affine.template apply<T, ACT>(v);
-        store_last<T, V>(y, v);
-    }
+        for (int k = 0; k < kUnroll; ++k)
+            if (k < count) {
+                affine.template apply<T, ACT>(v[0][k]);
+                store_last<T, V>(y - (row + k) * at.stride, v[0][k]);
+            }
+    });
 }
 
 // Per channel and chunk: (sum dz, sum dz xh).
@@ -393,44 +446,32 @@ template <typename T, int V, int ACT>
 __global__ void __launch_bounds__(kNormBlock, kNormGradOccupancy) k_norm_grad_sums(const NormArgs a)
 {
     grid_dependency_begin();
-    __shared__ float s_b[kNormBlock * V], s_w[kNormBlock * V];
-    const int cols = a.vectors;
-    const int col = threadIdx.x % cols, row = threadIdx.x / cols, rows = kNormBlock / cols;
-    const int vec = blockIdx.z * cols + col;
-    const int sample = a.sample0 + blockIdx.y;
-    const int64_t p0 = (int64_t)blockIdx.x * a.rows_per_chunk;
-    const int64_t p1 = min(a.positions, p0 + a.rows_per_chunk);
+    extern __shared__ __align__(16) unsigned char s_raw[];
+    const RowWalk<V> at(a);
     Gradient<V> grad;
-    if (row < rows && vec * V < a.channels) {
+    if (at.live) {
         Channel<V> ch;
-        ch.load(a, sample, vec * V);
-        const int64_t first = ((int64_t)sample * a.positions + p0 + row) * a.channels + (int64_t)vec * V;
-        const int64_t stride = (int64_t)rows * a.channels;
-        const T *x = (const T *)a.x + first, *dout = (const T *)a.dout + first;
-        int left = (int)((p1 - p0 - row + rows - 1) / rows);
-        for (; left >= kUnroll; left -= kUnroll, x += kUnroll * stride, dout += kUnroll * stride) {
-            Vec<T, V> vx[kUnroll], vd[kUnroll];
+        ch.load(a, at.sample, at.vec * V);
+        const T *const from[2] = {(const T *)a.x + at.first, (const T *)a.dout + at.first};
+        walk_rows<T, V, 2>(s_raw, from, at.stride, at.left, [&](int, int count, const Vec<T, V>(&v)[2][kUnroll]) {
 #pragma unroll
-            for (int k = 0; k < kUnroll; ++k) {
-                vx[k] = *(const Vec<T, V> *)(x + k * stride);
-                vd[k] = *(const Vec<T, V> *)(dout + k * stride);
-            }
-#pragma unroll
-            for (int k = 0; k < kUnroll; ++k) grad.template add<T, ACT>(ch, vx[k], vd[k]);
-        }
-        for (; left > 0; --left, x += stride, dout += stride)
-            grad.template add<T, ACT>(ch, *(const Vec<T, V> *)x, *(const Vec<T, V> *)dout);
+            for (int k = 0; k < kUnroll; ++k)
+                if (k < count) grad.template add<T, ACT>(ch, v[0][k], v[1][k]);
+        });
     }
+    __syncthreads();   // the ring becomes the threads' sums
+    float *s_b = (float *)s_raw, *s_w = s_b + kNormBlock * V;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         s_b[threadIdx.x * V + j] = grad.sum_b(j);
         s_w[threadIdx.x * V + j] = grad.sum_w(j);
     }
     __syncthreads();
-    float2 *out = a.partial + ((int64_t)blockIdx.y * a.chunks + blockIdx.x) * a.channels + (int64_t)blockIdx.z * cols * V;
-    for (int c = threadIdx.x; c < cols * V && (int)(blockIdx.z * cols * V) + c < a.channels; c += kNormBlock) {
+    const int cols = a.vectors, c0 = blockIdx.z * cols * V;
+    float2 *out = a.partial + ((int64_t)blockIdx.y * a.chunks + blockIdx.x) * a.channels + c0;
+    for (int c = threadIdx.x; c < cols * V && c0 + c < a.channels; c += kNormBlock) {
         float2 m = make_float2(0.0f, 0.0f);
-        for (int r = 0; r < rows; ++r) {
+        for (int r = 0; r < at.rows; ++r) {
             const int t = (r * cols + c / V) * V + c % V;
             m.x += s_b[t];
             m.y += s_w[t];
@@ -506,49 +547,28 @@ __global__ void __launch_bounds__(kNormBlock, kNormGradOccupancy) k_norm_grad_ap
             if (a.dweight) a.dweight[c] = m.y;
         }
     }
-    const int cols = a.vectors;
-    const int col = threadIdx.x % cols, row = threadIdx.x / cols, rows = kNormBlock / cols;
-    const int vec = blockIdx.z * cols + col;
-    if (row >= rows || vec * V >= a.channels) return;
-    const int sample = a.sample0 + blockIdx.y;
-    const int64_t p0 = (int64_t)blockIdx.x * a.rows_per_chunk;
-    const int64_t p1 = min(a.positions, p0 + a.rows_per_chunk);
+    extern __shared__ __align__(16) unsigned char s_raw[];
+    const RowWalk<V> at(a);
+    if (!at.live) return;
     Channel<V> ch;
-    ch.load(a, sample, vec * V);
+    ch.load(a, at.sample, at.vec * V);
     float2 m1[kPairs<V>], m2[kPairs<V>];
 #pragma unroll
     for (int j = 0; j < 2 * kPairs<V>; ++j) {
-        const float2 m = a.group_sums[(int64_t)sample * a.groups + (vec * V + (j < V ? j : 0)) / a.per_group];
+        const float2 m = a.group_sums[(int64_t)at.sample * a.groups + (at.vec * V + (j < V ? j : 0)) / a.per_group];
         (&m1[j / 2].x)[j % 2] = m.x;
         (&m2[j / 2].x)[j % 2] = m.y;
     }
-    if (p0 + row >= p1) return;
-    int left = (int)((p1 - p0 - row + rows - 1) / rows);
-    const int64_t first = ((int64_t)sample * a.positions + p0 + row + (int64_t)(left - 1) * rows) * a.channels +
-                          (int64_t)vec * V;
-    const int64_t stride = -(int64_t)rows * a.channels;
-    const T *x = (const T *)a.x + first, *dout = (const T *)a.dout + first;
-    T *y = (T *)a.y + first;
-    constexpr int kTwo = kUnroll / 2;   // two inputs and twice the constants: half the rows at a time
-    for (; left >= kTwo; left -= kTwo, x += kTwo * stride, dout += kTwo * stride, y += kTwo * stride) {
-        Vec<T, V> vx[kTwo], vd[kTwo];
+    const T *const from[2] = {(const T *)a.x + at.last, (const T *)a.dout + at.last};
+    T *y = (T *)a.y + at.last;
+    walk_rows<T, V, 2>(s_raw, from, -at.stride, at.left, [&](int row, int count, Vec<T, V>(&v)[2][kUnroll]) {
 #pragma unroll
-        for (int k = 0; k < kTwo; ++k) {
-            vx[k] = load_last<T, V>(x + k * stride);
-            vd[k] = load_last<T, V>(dout + k * stride);
-        }
-#pragma unroll
-        for (int k = 0; k < kTwo; ++k) {
-            input_gradient<T, V, ACT>(ch, m1, m2, vx[k], vd[k]);
-            store_last<T, V>(y + k * stride, vx[k]);
-        }
-    }
-    for (; left > 0; --left, x += stride, dout += stride, y += stride) {
-        Vec<T, V> vx = load_last<T, V>(x);
-        const Vec<T, V> vd = load_last<T, V>(dout);
-        input_gradient<T, V, ACT>(ch, m1, m2, vx, vd);
-        store_last<T, V>(y, vx);
-    }
+        for (int k = 0; k < kUnroll; ++k)
+            if (k < count) {
+                input_gradient<T, V, ACT>(ch, m1, m2, v[0][k], v[1][k]);
+                store_last<T, V>(y - (row + k) * at.stride, v[0][k]);
+            }
+    });
 }
 
 // ---- resident form ---------------------------------------------------------------
@@ -564,12 +584,6 @@ struct ResidentArgs {
     int64_t rows_per_block;
     int row_capacity;                               // rows_per_block, as the shared layout has it
 };
-
-__device__ __forceinline__ void copy16(void *to, const void *from)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from)
-                 : "memory");
-}
 
 __device__ __forceinline__ void copies_done()
 {
@@ -906,15 +920,25 @@ int norm_width(const gsr_group_norm &d, const void *x, const void *dout, const v
     return ok ? full : 1;
 }
 
+// A kernel that walks rows of N arrays: its rings, or the scalar form's sums.
+template <int N, typename Kernel>
+cudaError_t launch_walk(gsr_ctx *ctx, Kernel *kernel, dim3 grid, int width, cudaStream_t stream, const NormArgs &a)
+{
+    const size_t smem = width > 1 ? kRingBytes<N> : (size_t)kNormBlock * 3 * sizeof(float);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_kernel_smem(ctx, kernel, grid, kNormBlock, smem, stream, a);
+}
+
 template <typename T, int V, int ACT>
 cudaError_t norm_forward(gsr_ctx *ctx, NormArgs &a, const NormPlan &p, cudaStream_t stream)
 {
     for (a.sample0 = 0; a.sample0 < a.samples; a.sample0 += p.wave) {
         const unsigned n = (unsigned)(a.samples - a.sample0 < p.wave ? a.samples - a.sample0 : p.wave);
         const dim3 grid((unsigned)p.chunks, n, (unsigned)p.slabs);
-        cudaError_t e = launch_kernel(ctx, k_norm_moments<T, V>, grid, kNormBlock, stream, a);
+        cudaError_t e = launch_walk<1>(ctx, k_norm_moments<T, V>, grid, V, stream, a);
         if (e == cudaSuccess) e = launch_kernel(ctx, k_norm_merge, dim3((unsigned)a.groups, n), kMergeBlock, stream, a);
-        if (e == cudaSuccess) e = launch_kernel(ctx, k_norm_apply<T, V, ACT>, grid, kNormBlock, stream, a);
+        if (e == cudaSuccess) e = launch_walk<1>(ctx, k_norm_apply<T, V, ACT>, grid, V, stream, a);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -926,10 +950,10 @@ cudaError_t norm_backward(gsr_ctx *ctx, NormArgs &a, const NormPlan &p, cudaStre
     for (a.sample0 = 0; a.sample0 < a.samples; a.sample0 += p.wave) {
         const unsigned n = (unsigned)(a.samples - a.sample0 < p.wave ? a.samples - a.sample0 : p.wave);
         const dim3 grid((unsigned)p.chunks, n, (unsigned)p.slabs);
-        cudaError_t e = launch_kernel(ctx, k_norm_grad_sums<T, V, ACT>, grid, kNormBlock, stream, a);
+        cudaError_t e = launch_walk<2>(ctx, k_norm_grad_sums<T, V, ACT>, grid, V, stream, a);
         if (e == cudaSuccess)
             e = launch_kernel(ctx, k_norm_grad_merge, dim3((unsigned)a.groups, n), kMergeBlock, stream, a);
-        if (e == cudaSuccess) e = launch_kernel(ctx, k_norm_grad_apply<T, V, ACT>, grid, kNormBlock, stream, a);
+        if (e == cudaSuccess) e = launch_walk<2>(ctx, k_norm_grad_apply<T, V, ACT>, grid, V, stream, a);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
