@@ -11,10 +11,14 @@
 // group width.  Two forms:
 //   - resident: a cluster of blocks keeps a sample's slab of whole groups in
 //     shared memory between the statistics and the result, one kernel and one
-//     read of the inputs.  For slabs that a cluster holds.
+//     read of the inputs.  For slabs that a cluster holds (3 x 6,767 x 96 in f32:
+//     14 and 21 us where the passes take 20 and 27).
 //   - passes: a pass that reduces over the positions per channel, a small kernel
 //     that merges the blocks' partial sums into groups, and a pass that writes
-//     and walks back, from what L2 still holds of the first.
+//     and walks back, from what L2 still holds of the first.  Moves 3 arrays
+//     forward and 5 backward where 2 and 3 are needed: 4 x 40,000 x 256 in bf16
+//     (82 MB an array) takes 47 us, a training step of 4 x 160,000 x 128 (164 MB)
+//     229 us, 72% and 84% of the copy rate on the bytes moved, L2's share included.
 //
 // Numerics.  The variance is a merge of centred squares: a thread takes the mean
 // and the centred squares of kRun values at a time and merges (n, mean, M2)
@@ -30,11 +34,11 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kNormBlock = 256;
-constexpr int kRun = 4;          // values whose mean and centred squares are taken together
+constexpr int kRun = 8;          // values whose mean and centred squares are taken together
 constexpr int kMergeBlock = 256;
 // Blocks an SM holds (their rings fill its shared memory): one wave of them takes
 // all chunks.
-constexpr int kNormOccupancy = 4, kNormGradOccupancy = 2;
+constexpr int kNormOccupancy = 2;
 
 // A result, which nothing here reads again.
 template <typename T, int V>
@@ -294,9 +298,10 @@ __device__ __forceinline__ void input_gradient(const Channel<V> &c, const float2
 // in flight do not depend on registers and no thread waits for another.  f is
 // called with a batch: its first row's number, how many rows, and the values.
 // Scalar accesses (which have no such copies) are read directly.
-constexpr int kUnroll = 4;
-constexpr int kDepth = 3;
-static_assert(kUnroll == kRun, "a batch is a run of the moments");
+template <int N>
+constexpr int kUnroll = 8 / N;
+constexpr int kDepth = 2;   // (three and four were no faster: 47.2 and 46.8 us, 232 and 229 us)
+static_assert(kUnroll<1> == kRun, "a batch is a run of the moments");
 
 __device__ __forceinline__ void copy16(void *to, const void *from)
 {
@@ -305,46 +310,46 @@ __device__ __forceinline__ void copy16(void *to, const void *from)
 }
 
 template <int N>
-constexpr size_t kRingBytes = (size_t)kNormBlock * 16 * kUnroll * kDepth * N;
+constexpr size_t kRingBytes = (size_t)kNormBlock * 16 * kUnroll<N> * kDepth * N;
 
 template <typename T, int V, int N, typename F>
 __device__ __forceinline__ void walk_rows(unsigned char *ring, const T *const (&from)[N], int64_t stride, int rows, F f)
 {
     using Access = Vec<T, V>;
-    Access v[N][kUnroll];
+    Access v[N][kUnroll<N>];
     if constexpr (sizeof(Access) == 16) {
         Access *mine = (Access *)ring + threadIdx.x;
-        auto slot = [&](int batch, int n, int k) { return mine + (((batch % kDepth) * N + n) * kUnroll + k) * kNormBlock; };
-        const int batches = (rows + kUnroll - 1) / kUnroll;
+        auto slot = [&](int batch, int n, int k) { return mine + (((batch % kDepth) * N + n) * kUnroll<N> + k) * kNormBlock; };
+        const int batches = (rows + kUnroll<N> - 1) / kUnroll<N>;
         auto issue = [&](int batch) {
 #pragma unroll
-            for (int k = 0; k < kUnroll; ++k)
-                if (batch * kUnroll + k < rows)
+            for (int k = 0; k < kUnroll<N>; ++k)
+                if (batch * kUnroll<N> + k < rows)
 #pragma unroll
                     for (int n = 0; n < N; ++n)
-                        copy16(slot(batch, n, k), from[n] + (int64_t)(batch * kUnroll + k) * stride);
+                        copy16(slot(batch, n, k), from[n] + (int64_t)(batch * kUnroll<N> + k) * stride);
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
         for (int b = 0; b < kDepth - 1; ++b) issue(b);
         for (int b = 0; b < batches; ++b) {
             issue(b + kDepth - 1);
             asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
-            const int count = min(kUnroll, rows - b * kUnroll);
+            const int count = min(kUnroll<N>, rows - b * kUnroll<N>);
 #pragma unroll
             for (int n = 0; n < N; ++n)
 #pragma unroll
-                for (int k = 0; k < kUnroll; ++k)
+                for (int k = 0; k < kUnroll<N>; ++k)
                     if (k < count) v[n][k] = *slot(b, n, k);
-            f(b * kUnroll, count, v);
+            f(b * kUnroll<N>, count, v);
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
     } else {
-        for (int b = 0; b < rows; b += kUnroll) {
-            const int count = min(kUnroll, rows - b);
+        for (int b = 0; b < rows; b += kUnroll<N>) {
+            const int count = min(kUnroll<N>, rows - b);
 #pragma unroll
             for (int n = 0; n < N; ++n)
 #pragma unroll
-                for (int k = 0; k < kUnroll; ++k)
+                for (int k = 0; k < kUnroll<N>; ++k)
                     if (k < count) v[n][k] = *(const Access *)(from[n] + (int64_t)(b + k) * stride);
             f(b, count, v);
         }
@@ -383,12 +388,12 @@ __global__ void __launch_bounds__(kNormBlock, kNormOccupancy) k_norm_moments(con
     ChannelMoments<T, V> own;
     if (at.live) {
         const T *const from[1] = {(const T *)a.x + at.first};
-        walk_rows<T, V, 1>(s_raw, from, at.stride, at.left, [&](int, int count, const Vec<T, V>(&v)[1][kUnroll]) {
-            if (count == kUnroll) {
+        walk_rows<T, V, 1>(s_raw, from, at.stride, at.left, [&](int, int count, const Vec<T, V>(&v)[1][kUnroll<1>]) {
+            if (count == kUnroll<1>) {
                 own.add(v[0]);
             } else {
 #pragma unroll
-                for (int k = 0; k < kUnroll; ++k)
+                for (int k = 0; k < kUnroll<1>; ++k)
                     if (k < count) own.add(v[0][k]);
             }
         });
@@ -431,9 +436,9 @@ __global__ void __launch_bounds__(kNormBlock, kNormOccupancy) k_norm_apply(const
     }
     const T *const from[1] = {(const T *)a.x + at.last};
     T *y = (T *)a.y + at.last;
-    walk_rows<T, V, 1>(s_raw, from, -at.stride, at.left, [&](int row, int count, Vec<T, V>(&v)[1][kUnroll]) {
+    walk_rows<T, V, 1>(s_raw, from, -at.stride, at.left, [&](int row, int count, Vec<T, V>(&v)[1][kUnroll<1>]) {
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k)
+        for (int k = 0; k < kUnroll<1>; ++k)
             if (k < count) {
                 affine.template apply<T, ACT>(v[0][k]);
                 store_last<T, V>(y - (row + k) * at.stride, v[0][k]);
@@ -443,7 +448,7 @@ __global__ void __launch_bounds__(kNormBlock, kNormOccupancy) k_norm_apply(const
 
 // Per channel and chunk: (sum dz, sum dz xh).
 template <typename T, int V, int ACT>
-__global__ void __launch_bounds__(kNormBlock, kNormGradOccupancy) k_norm_grad_sums(const NormArgs a)
+__global__ void __launch_bounds__(kNormBlock, kNormOccupancy) k_norm_grad_sums(const NormArgs a)
 {
     grid_dependency_begin();
     extern __shared__ __align__(16) unsigned char s_raw[];
@@ -453,9 +458,9 @@ __global__ void __launch_bounds__(kNormBlock, kNormGradOccupancy) k_norm_grad_su
         Channel<V> ch;
         ch.load(a, at.sample, at.vec * V);
         const T *const from[2] = {(const T *)a.x + at.first, (const T *)a.dout + at.first};
-        walk_rows<T, V, 2>(s_raw, from, at.stride, at.left, [&](int, int count, const Vec<T, V>(&v)[2][kUnroll]) {
+        walk_rows<T, V, 2>(s_raw, from, at.stride, at.left, [&](int, int count, const Vec<T, V>(&v)[2][kUnroll<2>]) {
 #pragma unroll
-            for (int k = 0; k < kUnroll; ++k)
+            for (int k = 0; k < kUnroll<2>; ++k)
                 if (k < count) grad.template add<T, ACT>(ch, v[0][k], v[1][k]);
         });
     }
@@ -532,7 +537,7 @@ __global__ void __launch_bounds__(kMergeBlock) k_norm_grad_merge(const NormArgs 
 // dx = rstd (w dz - m1 - xh m2).  The blocks of the last launch's first chunk
 // also sum the parameter gradients over the samples.
 template <typename T, int V, int ACT>
-__global__ void __launch_bounds__(kNormBlock, kNormGradOccupancy) k_norm_grad_apply(const NormArgs a)
+__global__ void __launch_bounds__(kNormBlock, kNormOccupancy) k_norm_grad_apply(const NormArgs a)
 {
     grid_dependency_begin();
     if (blockIdx.x == 0 && blockIdx.y == 0 && a.sample0 + (int)gridDim.y == a.samples) {
@@ -561,9 +566,9 @@ __global__ void __launch_bounds__(kNormBlock, kNormGradOccupancy) k_norm_grad_ap
     }
     const T *const from[2] = {(const T *)a.x + at.last, (const T *)a.dout + at.last};
     T *y = (T *)a.y + at.last;
-    walk_rows<T, V, 2>(s_raw, from, -at.stride, at.left, [&](int row, int count, Vec<T, V>(&v)[2][kUnroll]) {
+    walk_rows<T, V, 2>(s_raw, from, -at.stride, at.left, [&](int row, int count, Vec<T, V>(&v)[2][kUnroll<2>]) {
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k)
+        for (int k = 0; k < kUnroll<2>; ++k)
             if (k < count) {
                 input_gradient<T, V, ACT>(ch, m1, m2, v[0][k], v[1][k]);
                 store_last<T, V>(y - (row + k) * at.stride, v[0][k]);
@@ -895,7 +900,7 @@ struct NormPlan {
     int64_t rows_per_chunk;
 };
 
-NormPlan norm_plan(const gsr_ctx *ctx, const gsr_group_norm &d, int width, bool backward)
+NormPlan norm_plan(const gsr_ctx *ctx, const gsr_group_norm &d, int width)
 {
     NormPlan p;
     const int vectors = (d.channels + width - 1) / width;
@@ -903,7 +908,7 @@ NormPlan norm_plan(const gsr_ctx *ctx, const gsr_group_norm &d, int width, bool 
     p.slabs = (vectors + p.vectors - 1) / p.vectors;
     const int rows = kNormBlock / p.vectors;
     p.wave = d.samples < 65535 ? d.samples : 65535;   // samples of a launch (a grid's limit)
-    int64_t chunks = (int64_t)(backward ? kNormGradOccupancy : kNormOccupancy) * ctx->num_sms / ((int64_t)p.wave * p.slabs);
+    int64_t chunks = (int64_t)kNormOccupancy * ctx->num_sms / ((int64_t)p.wave * p.slabs);
     const int64_t most = (d.positions + (int64_t)rows * kRun - 1) / ((int64_t)rows * kRun);
     if (chunks > most) chunks = most;
     if (chunks < 1) chunks = 1;
@@ -999,7 +1004,7 @@ int run_norm(gsr_ctx *ctx, const gsr_group_norm &d, NormArgs &a, bool backward, 
 {
     const int width = norm_width(d, a.x, a.dout, a.y);
     const ResidentPlan r = resident_plan(d, width, backward);
-    const NormPlan p = norm_plan(ctx, d, width, backward);
+    const NormPlan p = norm_plan(ctx, d, width);
     a.samples = d.samples;
     a.channels = d.channels;
     a.groups = d.groups;
