@@ -7,7 +7,7 @@
 #include <new>
 #include <string>
 
-#include "internal.cuh"
+#include "decoder.cuh"
 
 namespace gsr {
 

@@ -831,7 +831,7 @@ int launch_big(gsr_ctx *ctx, Kernel *kernel, const char *name, int blocks, int s
     if (int rc = cuda_check(ctx, cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem), name))
         return rc;
     if (int rc = check_registers(ctx, (const void *)kernel, name, Registers<kGroups>::kStart)) return rc;
-    return cuda_check(ctx, launch_kernel_smem(ctx, kernel, dim3((unsigned)blocks), kBackwardThreads, smem, stream, a),
+    return cuda_check(ctx, launch_kernel_smem(ctx, kernel, dim3((unsigned)blocks), kBackwardThreads, smem, 1, stream, a),
                       name);
 }
 

@@ -332,7 +332,7 @@ int launch_few(gsr_ctx *ctx, const FewArgs &a, int64_t units, cudaStream_t strea
     if (int rc = cuda_check(ctx, cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
                             "k_attention_few"))
         return rc;
-    if (int rc = cuda_check(ctx, launch_kernel_smem(ctx, kernel, dim3((unsigned)(units * a.splits)), kFewThreads, smem,
+    if (int rc = cuda_check(ctx, launch_kernel_smem(ctx, kernel, dim3((unsigned)(units * a.splits)), kFewThreads, smem, 1,
                                                     stream, a),
                             "k_attention_few"))
         return rc;

@@ -427,7 +427,7 @@ int launch_forward(gsr_ctx *ctx, ForwardArgs &a, int blocks, cudaStream_t stream
                             "k_attention_forward"))
         return rc;
     if (int rc = check_registers(ctx, (const void *)kernel, "k_attention_forward", Registers<2>::kStart)) return rc;
-    if (int rc = cuda_check(ctx, launch_kernel_smem(ctx, kernel, dim3((unsigned)blocks), kForwardThreads, smem, stream, a),
+    if (int rc = cuda_check(ctx, launch_kernel_smem(ctx, kernel, dim3((unsigned)blocks), kForwardThreads, smem, 1, stream, a),
                             "k_attention_forward"))
         return rc;
     if (blocks == 1 || a.work.length <= kKeyTile) return GSR_OK;   // tiles of one step are never cut

@@ -1,5 +1,6 @@
-// decoder.cuh -- helpers shared by the decoder's operators (group norm, rotary
-// positions, cross attention): element types, vector access, the workspace.
+// decoder.cuh -- the decoder's operators (group norm, rotary positions, cross
+// attention): their host sides, and what they share: element types, vector access,
+// launches with dynamic shared memory, the workspace.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -8,6 +9,45 @@
 #include "internal.cuh"
 
 namespace gsr {
+
+// Host sides (validated arguments).
+int group_norm_forward(gsr_ctx *ctx, const gsr_group_norm &d, const void *x, const float *weight, const float *bias,
+                       void *out, float *mean, float *rstd, cudaStream_t stream);
+int group_norm_backward(gsr_ctx *ctx, const gsr_group_norm &d, const void *dout, const void *x, const float *weight,
+                        const float *bias, const float *mean, const float *rstd, void *dx, float *dweight,
+                        float *dbias, cudaStream_t stream);
+// Rotation by +theta (sign = 1) or -theta (sign = -1).
+int rotary(gsr_ctx *ctx, const gsr_rotary &d, const gsr_heads &x, const void *positions, const float *frequencies,
+           const gsr_heads &out, float sign, cudaStream_t stream);
+int cross_attention_forward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr_heads &k,
+                            const gsr_heads &v, const gsr_heads &out, float *lse, cudaStream_t stream);
+int cross_attention_backward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr_heads &k,
+                             const gsr_heads &v, const gsr_heads &out, const float *lse, const gsr_heads &dout,
+                             const gsr_heads &dq, const gsr_heads &dk, const gsr_heads &dv, cudaStream_t stream);
+
+// launch_kernel with smem bytes of dynamic shared memory, and in clusters of
+// `cluster` blocks.
+template <typename... Params, typename... Args>
+cudaError_t launch_kernel_smem(gsr_ctx *ctx, void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
+                               unsigned cluster, cudaStream_t stream, Args &&...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = ctx->opt_pdl ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    ++ctx->launches;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
 
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }

@@ -874,22 +874,8 @@ cudaError_t launch_cluster(gsr_ctx *ctx, Kernel *kernel, const ResidentPlan &p, 
 {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((int64_t)a.n.samples * a.slabs * p.cluster));
-    cfg.blockDim = dim3(kResidentBlock);
-    cfg.dynamicSmemBytes = p.smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = ctx->opt_pdl ? 1 : 0;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)p.cluster;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    ++ctx->launches;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
+    return launch_kernel_smem(ctx, kernel, dim3((unsigned)((int64_t)a.n.samples * a.slabs * p.cluster)), kResidentBlock,
+                              p.smem, (unsigned)p.cluster, stream, a);
 }
 
 // ---- host ---------------------------------------------------------------------------
@@ -932,7 +918,7 @@ cudaError_t launch_walk(gsr_ctx *ctx, Kernel *kernel, dim3 grid, int width, cuda
     const size_t smem = width > 1 ? kRingBytes<N> : (size_t)kNormBlock * 3 * sizeof(float);
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_kernel_smem(ctx, kernel, grid, kNormBlock, smem, stream, a);
+    return launch_kernel_smem(ctx, kernel, grid, kNormBlock, smem, 1, stream, a);
 }
 
 template <typename T, int V, int ACT>
@@ -1017,8 +1003,10 @@ int run_norm(gsr_ctx *ctx, const gsr_group_norm &d, NormArgs &a, bool backward, 
     const size_t partial = r.fits ? 0 : round_up((size_t)p.wave * p.chunks * d.channels * sizeof(float2), 256);
     const size_t sums = backward ? (size_t)d.samples * d.channels * sizeof(float2) : 0;
     const size_t group_sums = backward ? (size_t)d.samples * d.groups * sizeof(float2) : 0;
-    void *work;
-    if (int rc = workspace(ctx, partial + sums + group_sums, stream, &work)) return rc;
+    const bool scratch = partial + sums + group_sums > 0;
+    void *work = nullptr;
+    if (scratch)
+        if (int rc = workspace(ctx, partial + sums + group_sums, stream, &work)) return rc;
     a.partial = (float2 *)work;
     a.sums = (float2 *)((unsigned char *)work + partial);
     a.group_sums = (float2 *)((unsigned char *)work + partial + sums);
@@ -1030,7 +1018,7 @@ int run_norm(gsr_ctx *ctx, const gsr_group_norm &d, NormArgs &a, bool backward, 
     else
         e = dispatch_act<__half>(ctx, a, p, r, d.activation, width, backward, stream);
     if (int rc = cuda_check(ctx, e, backward ? "group norm backward" : "group norm forward")) return rc;
-    return workspace_done(ctx, stream);
+    return scratch ? workspace_done(ctx, stream) : GSR_OK;
 }
 
 }  // namespace

@@ -63,17 +63,16 @@ __device__ __forceinline__ void race_canary(uint32_t site)
 #define GSR_CANARY(site) ((void)0)
 #endif
 
-// Launches `kernel` on `stream` with smem bytes of dynamic shared memory, with
-// programmatic stream serialisation when the context allows it (GSR_OPT_PDL),
-// and counts the launch.
+// Launches `kernel` on `stream`, with programmatic stream serialisation when the
+// context allows it (GSR_OPT_PDL), and counts the launch.
 template <typename... Params, typename... Args>
-cudaError_t launch_kernel_smem(gsr_ctx *ctx, void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
-                               cudaStream_t stream, Args &&...args)
+cudaError_t launch_kernel(gsr_ctx *ctx, void (*kernel)(Params...), dim3 grid, dim3 block, cudaStream_t stream,
+                          Args &&...args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = 0;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -82,13 +81,6 @@ cudaError_t launch_kernel_smem(gsr_ctx *ctx, void (*kernel)(Params...), dim3 gri
     cfg.numAttrs = 1;
     ++ctx->launches;
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-}
-
-template <typename... Params, typename... Args>
-cudaError_t launch_kernel(gsr_ctx *ctx, void (*kernel)(Params...), dim3 grid, dim3 block, cudaStream_t stream,
-                          Args &&...args)
-{
-    return launch_kernel_smem(ctx, kernel, grid, block, 0, stream, std::forward<Args>(args)...);
 }
 
 // cudaMalloc for the context's arena and scratch.  With the context's test
@@ -136,20 +128,6 @@ int project_backward(gsr_ctx *ctx, const float *gauss, int32_t n, const gsr_came
                      const float *dl_dsplat, float *dl_dg, cudaStream_t stream);
 // out[i] = the raster kernels' exp(-s[i]).
 int exp_neg_eval(gsr_ctx *ctx, const float *s, float *out, int32_t n, cudaStream_t stream);
-// The decoder's operators (validated arguments).
-int group_norm_forward(gsr_ctx *ctx, const gsr_group_norm &d, const void *x, const float *weight, const float *bias,
-                       void *out, float *mean, float *rstd, cudaStream_t stream);
-int group_norm_backward(gsr_ctx *ctx, const gsr_group_norm &d, const void *dout, const void *x, const float *weight,
-                        const float *bias, const float *mean, const float *rstd, void *dx, float *dweight,
-                        float *dbias, cudaStream_t stream);
-// Rotation by +theta (sign = 1) or -theta (sign = -1).
-int rotary(gsr_ctx *ctx, const gsr_rotary &d, const gsr_heads &x, const void *positions, const float *frequencies,
-           const gsr_heads &out, float sign, cudaStream_t stream);
-int cross_attention_forward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr_heads &k,
-                            const gsr_heads &v, const gsr_heads &out, float *lse, cudaStream_t stream);
-int cross_attention_backward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr_heads &k,
-                             const gsr_heads &v, const gsr_heads &out, const float *lse, const gsr_heads &dout,
-                             const gsr_heads &dq, const gsr_heads &dk, const gsr_heads &dv, cudaStream_t stream);
 // One launch of the FP32 / SFU rate kernel (peak.cu); *lane_ops = its lane operations.
 int peak_kernel(gsr_ctx *ctx, int kind, int32_t iters, float *sink, uint64_t *lane_ops, cudaStream_t stream);
 

@@ -192,8 +192,8 @@ cudaError_t launch_rotary(gsr_ctx *ctx, RotaryArgs &a, bool interleaved, int64_t
     const dim3 grid((unsigned)((tokens + a.block_tokens - 1) / a.block_tokens),
                     (unsigned)((a.runs + a.block_runs - 1) / a.block_runs));
     const size_t table = (size_t)a.block_tokens * a.pairs * sizeof(float2);
-    if (interleaved) return launch_kernel_smem(ctx, k_rotary<T, V, true>, grid, kRotaryBlock, table, stream, a);
-    return launch_kernel_smem(ctx, k_rotary<T, V, false>, grid, kRotaryBlock, table, stream, a);
+    if (interleaved) return launch_kernel_smem(ctx, k_rotary<T, V, true>, grid, kRotaryBlock, table, 1, stream, a);
+    return launch_kernel_smem(ctx, k_rotary<T, V, false>, grid, kRotaryBlock, table, 1, stream, a);
 }
 
 // Largest access of at most 16 bytes that divides every offset the kernel forms.
