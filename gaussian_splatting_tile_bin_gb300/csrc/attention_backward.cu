@@ -133,12 +133,6 @@ __device__ __forceinline__ void store_pairs(uint32_t at, const uint32_t (&r)[32]
     tmem_store32(at, r);
     tmem_wait_store();
 }
-__device__ __forceinline__ void store_pairs(uint32_t at, const uint32_t (&r)[16])
-{
-    tmem_store16(at, r);
-    tmem_wait_store();
-}
-
 __device__ __forceinline__ float2 pair(const Columns &r, int i)
 {
     return make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
@@ -177,7 +171,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
     Segment g;
 
     if (warp >= kComputeWarps) {
-        give_registers<kGroups>();
+        give_registers();
         if (warp == kComputeWarps && elect_one()) {
             uint32_t n = 0, seg = 0;
             while (walk.next(g)) {
@@ -252,7 +246,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
             }
         }
     } else {
-        take_registers<kGroups>();
+        take_registers();
         const int part = warp / 4, column0 = part * kColumnsEach;   // columns of S and dP
         const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
         const uint32_t at_s = tmem + lanes + S::kS + column0, at_dp = tmem + lanes + S::kDp + column0;
@@ -421,7 +415,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
     Segment g;
 
     if (warp >= kComputeWarps) {
-        give_registers<kGroups>();
+        give_registers();
         if (warp == kComputeWarps && elect_one()) {
             uint32_t n = 0, seg = 0;
             while (walk.next(g)) {
@@ -500,7 +494,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
             }
         }
     } else {
-        take_registers<kGroups>();
+        take_registers();
         const int part = warp / 4, column0 = part * kColumnsEach;   // columns of S and dP
         const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
         const uint32_t at_s = tmem + lanes + S::kS + column0, at_dp = tmem + lanes + S::kDp + column0;
@@ -796,30 +790,31 @@ int row_statistics(gsr_ctx *ctx, const RowArgs &r, cudaStream_t stream)
 }
 
 // Zeros: rows of one or two arrays of the same shape, all of them or those of
-// masked keys.
-__global__ void __launch_bounds__(256) k_attention_zero_rows(gsr_heads t, gsr_heads t2, uint32_t rows, uint32_t tokens,
-                                                             uint32_t heads, int dim, const uint8_t *mask,
+// masked keys; 16 bytes a thread.
+__global__ void __launch_bounds__(256) k_attention_zero_rows(gsr_heads t, gsr_heads t2, int64_t items, uint32_t tokens,
+                                                             uint32_t heads, uint32_t chunks, const uint8_t *mask,
                                                              const int32_t *lengths)
 {
     grid_dependency_begin();
-    const uint32_t r = blockIdx.x * 256 + threadIdx.x;
-    if (r >= rows) return;
-    const uint32_t bi = r / heads, h = r - bi * heads, b = bi / tokens, i = bi - b * tokens;
-    if (mask && (int)i < item_length(lengths, (int)tokens, (int)b) && mask[(int64_t)b * tokens + i] != 0) return;
-    for (const gsr_heads *x : {&t, &t2}) {
-        if (!x->data) continue;
-        uint16_t *o = (uint16_t *)x->data + b * x->batch_stride + i * x->token_stride + h * x->head_stride;
-        for (int c = 0; c < dim; c += 8) *(uint4 *)(o + c) = make_uint4(0, 0, 0, 0);
-    }
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= items) return;
+    const uint32_t r = (uint32_t)(i / chunks), c = (uint32_t)(i - (int64_t)r * chunks);
+    const uint32_t bt = r / heads, h = r - bt * heads, b = bt / tokens, token = bt - b * tokens;
+    if (mask && (int)token < item_length(lengths, (int)tokens, (int)b) && mask[(int64_t)b * tokens + token] != 0) return;
+    for (const gsr_heads *x : {&t, &t2})
+        if (x->data)
+            *(uint4 *)((uint16_t *)x->data + b * x->batch_stride + token * x->token_stride + h * x->head_stride + c * 8) =
+                make_uint4(0, 0, 0, 0);
 }
 
 int zero_rows(gsr_ctx *ctx, const gsr_heads &t, const gsr_heads &t2, const gsr_attention &d, int tokens, int heads,
               bool masked, cudaStream_t stream)
 {
-    const int64_t rows = (int64_t)d.batch * tokens * heads;   // at most 2^31 - 1, as the arguments' check has it
-    if (rows == 0) return GSR_OK;
-    return cuda_check(ctx, launch_kernel(ctx, k_attention_zero_rows, dim3((unsigned)((rows + 255) / 256)), 256, stream, t,
-                                         t2, (uint32_t)rows, (uint32_t)tokens, (uint32_t)heads, (int)d.head_dim,
+    const int chunks = d.head_dim / 8;   // rows are at most 2^31 - 1, as the arguments' check has it
+    const int64_t items = (int64_t)d.batch * tokens * heads * chunks;
+    if (items == 0) return GSR_OK;
+    return cuda_check(ctx, launch_kernel(ctx, k_attention_zero_rows, dim3((unsigned)((items + 255) / 256)), 256, stream,
+                                         t, t2, items, (uint32_t)tokens, (uint32_t)heads, (uint32_t)chunks,
                                          masked ? d.key_mask : nullptr, masked ? d.kv_lengths : nullptr),
                       "k_attention_zero_rows");
 }
@@ -830,7 +825,7 @@ int launch_big(gsr_ctx *ctx, Kernel *kernel, const char *name, int blocks, int s
 {
     if (int rc = cuda_check(ctx, cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem), name))
         return rc;
-    if (int rc = check_registers(ctx, (const void *)kernel, name, Registers<kGroups>::kStart)) return rc;
+    if (int rc = check_registers(ctx, (const void *)kernel, name)) return rc;
     return cuda_check(ctx, launch_kernel_smem(ctx, kernel, dim3((unsigned)blocks), kBackwardThreads, smem, 1, stream, a),
                       name);
 }

@@ -98,85 +98,85 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
     const int row_tiles = a.row_tiles;   // of 256 rows, per head
 
     if (warp >= 8) {
-    give_registers<2>();
-    if (warp == 8) {
-        // ---- copies: Q of a segment, then K and V of every step ----
-        if (elect_one()) {
-            prefetch_map(&a.q);
-            prefetch_map(&a.k);
-            prefetch_map(&a.v);
-            uint32_t kv = 0, seg = 0;
+        give_registers();
+        if (warp == 8) {
+            // ---- copies: Q of a segment, then K and V of every step ----
+            if (elect_one()) {
+                prefetch_map(&a.q);
+                prefetch_map(&a.k);
+                prefetch_map(&a.v);
+                uint32_t kv = 0, seg = 0;
+                while (walk.next(g)) {
+                    if (g.length == 0) continue;
+                    const int head = g.tile / row_tiles, row0 = (g.tile - head * row_tiles) * 2 * kRowTile;
+                    const int tiles = a.q_len - row0 > kRowTile ? 2 : 1;
+                    const int key_head = head / a.group;
+                    if (seg > 0) barrier_wait(b_q_free, (seg - 1) & 1, guard);
+                    barrier_expect(b_q, tiles * S::kTileBytes);
+                    for (int t = 0; t < tiles; ++t)
+                        for (int c = 0; c < S::kBlocks; ++c)
+                            copy_box(s_q + t * S::kTileBytes + c * kBlockBytes, &a.q, b_q, c * 64, row0 + t * kRowTile,
+                                     head * a.q_head, g.item * a.q_item);
+                    for (int i = g.begin; i < g.end; ++i)
+                        for (int half = 0; half < 2; ++half, ++kv) {
+                            if (guard.stop()) goto done;
+                            const uint32_t stage = kv % S::kStages, round = kv / S::kStages;
+                            if (round > 0) barrier_wait(b_kv_free + 8 * stage, (round - 1) & 1, guard);
+                            const uint32_t bar = b_kv + 8 * stage, to = s_kv + stage * S::kTileBytes;
+                            barrier_expect(bar, S::kTileBytes);
+                            for (int c = 0; c < S::kBlocks; ++c)
+                                copy_box(to + c * kBlockBytes, half ? &a.v : &a.k, bar, c * 64, i * kKeyTile,
+                                         key_head * (half ? a.v_head : a.k_head), g.item * (half ? a.v_item : a.k_item));
+                        }
+                    ++seg;
+                }
+            }
+        } else if (warp == 9) {
+            // ---- products ----
+            const bool leader = elect_one();
+            const uint32_t form_s = product_form<T>(kKeyTile, false);
+            const uint32_t form_o = product_form<T>((a.dim + 15) & ~15, true);
+            const int steps = (a.dim + 15) / 16;
+            uint32_t kv = 0, seg = 0, p[2] = {0, 0};
+            auto stage_at = [&](uint32_t n) { return s_kv + n % S::kStages * S::kTileBytes; };
+            auto await = [&](uint32_t n) { barrier_wait_warp(b_kv + 8 * (n % S::kStages), n / S::kStages & 1, guard); };
+            auto release = [&](uint32_t n) { product_commit(leader, b_kv_free + 8 * (n % S::kStages)); };
+            auto scores = [&](int t, uint32_t n) {
+                product_rows<HD>(leader, tmem + t * kKeyTile, s_q + t * S::kTileBytes, stage_at(n), form_s, steps);
+                product_commit(leader, b_s + 8 * t);
+            };
             while (walk.next(g)) {
                 if (g.length == 0) continue;
                 const int head = g.tile / row_tiles, row0 = (g.tile - head * row_tiles) * 2 * kRowTile;
                 const int tiles = a.q_len - row0 > kRowTile ? 2 : 1;
-                const int key_head = head / a.group;
-                if (seg > 0) barrier_wait(b_q_free, (seg - 1) & 1, guard);
-                barrier_expect(b_q, tiles * S::kTileBytes);
-                for (int t = 0; t < tiles; ++t)
-                    for (int c = 0; c < S::kBlocks; ++c)
-                        copy_box(s_q + t * S::kTileBytes + c * kBlockBytes, &a.q, b_q, c * 64, row0 + t * kRowTile,
-                                 head * a.q_head, g.item * a.q_item);
-                for (int i = g.begin; i < g.end; ++i)
-                    for (int half = 0; half < 2; ++half, ++kv) {
-                        if (guard.stop()) goto done;
-                        const uint32_t stage = kv % S::kStages, round = kv / S::kStages;
-                        if (round > 0) barrier_wait(b_kv_free + 8 * stage, (round - 1) & 1, guard);
-                        const uint32_t bar = b_kv + 8 * stage, to = s_kv + stage * S::kTileBytes;
-                        barrier_expect(bar, S::kTileBytes);
-                        for (int c = 0; c < S::kBlocks; ++c)
-                            copy_box(to + c * kBlockBytes, half ? &a.v : &a.k, bar, c * 64, i * kKeyTile,
-                                     key_head * (half ? a.v_head : a.k_head), g.item * (half ? a.v_item : a.k_item));
+                barrier_wait_warp(b_q, seg & 1, guard);
+                await(kv);
+                tmem_fence_after();
+                for (int t = 0; t < tiles; ++t) scores(t, kv);
+                release(kv);
+                for (int i = g.begin; i < g.end; ++i, kv += 2) {
+                    const bool more = i + 1 < g.end;
+                    await(kv + 1);
+                    for (int t = 0; t < tiles; ++t) {
+                        barrier_wait_warp(b_p + 8 * t, p[t]++ & 1, guard);
+                        tmem_fence_after();
+                        product_across<0, 8>(leader, tmem + S::kOut + t * HD, tmem + t * kKeyTile, stage_at(kv + 1), form_o,
+                                             i > g.begin);
+                        product_commit(leader, b_o + 8 * t);
+                        if (more) {
+                            if (t == 0) await(kv + 2);
+                            scores(t, kv + 2);
+                        }
                     }
+                    release(kv + 1);
+                    if (more) release(kv + 2);
+                }
+                product_commit(leader, b_q_free);
                 ++seg;
             }
         }
-    } else if (warp == 9) {
-        // ---- products ----
-        const bool leader = elect_one();
-        const uint32_t form_s = product_form<T>(kKeyTile, false);
-        const uint32_t form_o = product_form<T>((a.dim + 15) & ~15, true);
-        const int steps = (a.dim + 15) / 16;
-        uint32_t kv = 0, seg = 0, p[2] = {0, 0};
-        auto stage_at = [&](uint32_t n) { return s_kv + n % S::kStages * S::kTileBytes; };
-        auto await = [&](uint32_t n) { barrier_wait_warp(b_kv + 8 * (n % S::kStages), n / S::kStages & 1, guard); };
-        auto release = [&](uint32_t n) { product_commit(leader, b_kv_free + 8 * (n % S::kStages)); };
-        auto scores = [&](int t, uint32_t n) {
-            product_rows<HD>(leader, tmem + t * kKeyTile, s_q + t * S::kTileBytes, stage_at(n), form_s, steps);
-            product_commit(leader, b_s + 8 * t);
-        };
-        while (walk.next(g)) {
-            if (g.length == 0) continue;
-            const int head = g.tile / row_tiles, row0 = (g.tile - head * row_tiles) * 2 * kRowTile;
-            const int tiles = a.q_len - row0 > kRowTile ? 2 : 1;
-            barrier_wait_warp(b_q, seg & 1, guard);
-            await(kv);
-            tmem_fence_after();
-            for (int t = 0; t < tiles; ++t) scores(t, kv);
-            release(kv);
-            for (int i = g.begin; i < g.end; ++i, kv += 2) {
-                const bool more = i + 1 < g.end;
-                await(kv + 1);
-                for (int t = 0; t < tiles; ++t) {
-                    barrier_wait_warp(b_p + 8 * t, p[t]++ & 1, guard);
-                    tmem_fence_after();
-                    product_across<0, 8>(leader, tmem + S::kOut + t * HD, tmem + t * kKeyTile, stage_at(kv + 1), form_o,
-                                         i > g.begin);
-                    product_commit(leader, b_o + 8 * t);
-                    if (more) {
-                        if (t == 0) await(kv + 2);
-                        scores(t, kv + 2);
-                    }
-                }
-                release(kv + 1);
-                if (more) release(kv + 2);
-            }
-            product_commit(leader, b_q_free);
-            ++seg;
-        }
-    }
     } else {
-        take_registers<2>();
+        take_registers();
         // ---- softmax: one row a thread ----
         const int t = warp / 4;                                     // row tile
         const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;     // this warp's lanes of tensor memory
@@ -426,7 +426,7 @@ int launch_forward(gsr_ctx *ctx, ForwardArgs &a, int blocks, cudaStream_t stream
     if (int rc = cuda_check(ctx, cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
                             "k_attention_forward"))
         return rc;
-    if (int rc = check_registers(ctx, (const void *)kernel, "k_attention_forward", Registers<2>::kStart)) return rc;
+    if (int rc = check_registers(ctx, (const void *)kernel, "k_attention_forward")) return rc;
     if (int rc = cuda_check(ctx, launch_kernel_smem(ctx, kernel, dim3((unsigned)blocks), kForwardThreads, smem, 1, stream, a),
                             "k_attention_forward"))
         return rc;

@@ -86,11 +86,11 @@ __global__ void __launch_bounds__(256) k_pack_rows(gsr_heads k, gsr_heads v, uin
 
 }  // namespace
 
-int check_registers(gsr_ctx *ctx, const void *kernel, const char *name, int start)
+int check_registers(gsr_ctx *ctx, const void *kernel, const char *name)
 {
     cudaFuncAttributes attributes;
     if (int rc = cuda_check(ctx, cudaFuncGetAttributes(&attributes, kernel), name)) return rc;
-    if (attributes.numRegs < start)
+    if (attributes.numRegs < kStartRegisters)
         return fail(ctx, GSR_ERR_CUDA, std::string(name) + " was compiled to start with too few registers");
     return GSR_OK;
 }

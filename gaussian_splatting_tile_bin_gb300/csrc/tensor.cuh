@@ -283,32 +283,20 @@ __device__ __forceinline__ void product_across(bool leader, uint32_t d, uint32_t
 
 // ---- registers ------------------------------------------------------------------------------
 
-// A block has `groups` warpgroups that compute, each thread with a row of scores
-// or a part of one, and one whose warps copy and issue products and give most of
-// their registers to the others.
-template <int GROUPS>
-struct Registers;
-template <>
-struct Registers<2> {
-    static constexpr int kStart = 168, kFew = 72, kMany = 216;
-};
-template <>
-struct Registers<4> {
-    static constexpr int kStart = 96, kFew = 64, kMany = 104;
-};
+// A block has two warpgroups that compute, each thread with a row of scores or half
+// of one, and one whose warps copy and issue products and give most of their
+// registers to the others.
+constexpr int kStartRegisters = 168, kFewRegisters = 72, kManyRegisters = 216;
+static_assert(kFewRegisters + 2 * kManyRegisters <= 3 * kStartRegisters, "the shares must fit what the block starts with");
 
-template <int GROUPS>
 __device__ __forceinline__ void give_registers()
 {
-    using R = Registers<GROUPS>;
-    static_assert(R::kFew + GROUPS * R::kMany <= (GROUPS + 1) * R::kStart, "the shares must fit what the block starts with");
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kFew));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegisters));
 }
 
-template <int GROUPS>
 __device__ __forceinline__ void take_registers()
 {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(Registers<GROUPS>::kMany));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegisters));
 }
 
 // ---- host ------------------------------------------------------------------------------------
@@ -318,7 +306,7 @@ __device__ __forceinline__ void take_registers()
 // becomes an extent of 1; the kernels multiply such a coordinate by 0.
 // (A kernel compiled to start with fewer registers than the shares add up to
 // would wait for them forever: refuse to launch it.)
-int check_registers(gsr_ctx *ctx, const void *kernel, const char *name, int start);
+int check_registers(gsr_ctx *ctx, const void *kernel, const char *name);
 int heads_map(gsr_ctx *ctx, CUtensorMap *map, const gsr_heads &t, int dtype, int64_t batch, int64_t tokens,
               int64_t heads, int dim, int rows);
 
