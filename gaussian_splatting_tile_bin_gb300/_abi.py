@@ -425,27 +425,30 @@ def _strides(t, name):
     return HEADS.pack(t.data_ptr(), batch, token, head)
 
 
-def _heads_out(t, name, dtype, shape, index, device, stream):
+def _heads_out(t, name, dtype, shape, index, device, stream, like=None):
     """An output [batch, tokens, heads, head_dim], made if None, and its packed gsr_heads."""
     if t is not None:
         return t, _heads(t, name, dtype, shape, index)
-    t = _new(shape, dtype, device, stream)
+    t = _new(shape, dtype, device, stream, like)
     _, tokens, heads, dim = shape
     return t, HEADS.pack(t.data_ptr(), tokens * heads * dim, heads * dim, dim)
 
 
-def _array_out(t, name, dtype, shape, index, device, stream):
+def _array_out(t, name, dtype, shape, index, device, stream, like=None):
     """A contiguous output, made if None, and its address."""
     if t is not None:
         return t, _array(t, name, dtype, shape, index)
-    t = _new(shape, dtype, device, stream)
+    t = _new(shape, dtype, device, stream, like)
     return t, t.data_ptr()
 
 
-def _new(shape, dtype, device, stream):
-    """An output of this call, allocated for the stream that writes it; the
-    caller's stream, which will read it, is recorded on it as well."""
+def _new(shape, dtype, device, stream, like=None):
+    """A contiguous output of this call, allocated for the stream that writes it;
+    the caller's stream, which will read it, is recorded on it as well.  `like`: a
+    tensor of the same shape and type (the quicker way, if it is contiguous)."""
     if stream is None:
+        if like is not None and like.is_contiguous():
+            return torch.empty_like(like)
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=device)
@@ -484,7 +487,7 @@ def group_norm_forward(ctx: Context, x: torch.Tensor, groups: int, weight=None, 
     dtype, shape, dev = x.dtype, x.shape, x.device
     desc = _norm_desc(x, groups, eps, activation)
     channels, stats = shape[-1:], (shape[0], max(int(groups), 0))
-    out, at_out = _array_out(out, "out", dtype, shape, index, dev, stream)
+    out, at_out = _array_out(out, "out", dtype, shape, index, dev, stream, x)
     mean, at_mean = _array_out(mean, "mean", _F32, stats, index, dev, stream)
     rstd, at_rstd = _array_out(rstd, "rstd", _F32, stats, index, dev, stream)
     ctx._check(lib.gsr_group_norm_forward(
@@ -504,7 +507,7 @@ def group_norm_backward(ctx: Context, dl_dout: torch.Tensor, x: torch.Tensor, gr
     dtype, shape, dev = x.dtype, x.shape, x.device
     desc = _norm_desc(x, groups, 1.0, activation)
     channels, stats = shape[-1:], (shape[0], int(groups))
-    dl_dx, at_dx = _array_out(dl_dx, "dl_dx", dtype, shape, index, dev, stream)
+    dl_dx, at_dx = _array_out(dl_dx, "dl_dx", dtype, shape, index, dev, stream, x)
     dl_dweight, at_dweight = _array_out(dl_dweight, "dl_dweight", _F32, channels, index, dev, stream)
     dl_dbias, at_dbias = _array_out(dl_dbias, "dl_dbias", _F32, channels, index, dev, stream)
     ctx._check(lib.gsr_group_norm_backward(
@@ -539,7 +542,7 @@ def _rotary(call, name, ctx, x, positions, frequencies, sections, interleaved, o
         raise ValueError(f"positions must have shape {(tokens, axes)} or {(batch, tokens, axes)}, "
                          f"got {tuple(positions.shape)}")
     at_positions = _array(positions, "positions", positions.dtype, positions.shape, index)
-    out, at_out = _heads_out(out, out_name, dtype, shape, index, x.device, stream)
+    out, at_out = _heads_out(out, out_name, dtype, shape, index, x.device, stream, x)
     desc = ROTARY.pack(DTYPES[dtype], batch, tokens, heads, dim, bool(interleaved), axes, *sections,
                        *(0,) * (MAX_AXES - axes), positions.dtype is torch.int32, tokens * axes if each else 0)
     ctx._check(call(ctx._h, desc, _strides(x, name), at_positions, at_frequencies, at_out,
@@ -597,7 +600,7 @@ def cross_attention_forward(ctx: Context, q: torch.Tensor, k: torch.Tensor, v: t
     index, _, desc, at_q, at_k, at_v = _attention(q, k, v, kv_lengths, key_mask, scale)
     dtype, shape = q.dtype, q.shape
     rows = (shape[0], shape[2], shape[1])
-    out, at_out = _heads_out(out, "out", dtype, shape, index, q.device, stream)
+    out, at_out = _heads_out(out, "out", dtype, shape, index, q.device, stream, q)
     lse, at_lse = _array_out(lse, "lse", _F32, rows, index, q.device, stream)
     ctx._check(lib.gsr_cross_attention_forward(ctx._h, desc, at_q, at_k, at_v, at_out, at_lse,
                                                _raw_stream(stream, index)))
@@ -611,9 +614,9 @@ def cross_attention_backward(ctx: Context, q: torch.Tensor, k: torch.Tensor, v: 
     and lse.  Keys that took no part get zeros."""
     index, keys, desc, at_q, at_k, at_v = _attention(q, k, v, kv_lengths, key_mask, scale)
     dtype, shape, dev = q.dtype, q.shape, q.device
-    dl_dq, at_dq = _heads_out(dl_dq, "dl_dq", dtype, shape, index, dev, stream)
-    dl_dk, at_dk = _heads_out(dl_dk, "dl_dk", dtype, keys, index, dev, stream)
-    dl_dv, at_dv = _heads_out(dl_dv, "dl_dv", dtype, keys, index, dev, stream)
+    dl_dq, at_dq = _heads_out(dl_dq, "dl_dq", dtype, shape, index, dev, stream, q)
+    dl_dk, at_dk = _heads_out(dl_dk, "dl_dk", dtype, keys, index, dev, stream, k)
+    dl_dv, at_dv = _heads_out(dl_dv, "dl_dv", dtype, keys, index, dev, stream, v)
     ctx._check(lib.gsr_cross_attention_backward(
         ctx._h, desc, at_q, at_k, at_v, _heads(out, "out", dtype, shape, index),
         _array(lse, "lse", _F32, (shape[0], shape[2], shape[1]), index),

@@ -394,7 +394,7 @@ int few_rows_forward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, c
         rc = d.head_dim <= 64 ? launch_few<__half, 64>(ctx, a, units, stream)
                               : launch_few<__half, 128>(ctx, a, units, stream);
     if (rc) return rc;
-    return workspace_done(ctx, stream);
+    return parts > 0 ? workspace_done(ctx, stream) : GSR_OK;
 }
 
 }  // namespace gsr
