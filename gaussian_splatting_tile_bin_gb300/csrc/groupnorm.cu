@@ -26,6 +26,8 @@
 // mean is far from 0.  All merges run in a fixed order.
 #include <cooperative_groups.h>
 
+#include <algorithm>
+
 #include "decoder.cuh"
 
 namespace gsr {
@@ -297,27 +299,33 @@ __device__ __forceinline__ void input_gradient(const Channel<V> &c, const float2
 // of kUnroll rows of each of N arrays, kDepth - 1 batches ahead, so that the loads
 // in flight do not depend on registers and no thread waits for another.  f is
 // called with a batch: its first row's number, how many rows, and the values.
-// Scalar accesses (which have no such copies) are read directly.
+// Accesses of 2 bytes (which have no such copies) are read directly.
 template <int N>
 constexpr int kUnroll = 8 / N;
 constexpr int kDepth = 2;   // (three and four were no faster: 47.2 and 46.8 us, 232 and 229 us)
 static_assert(kUnroll<1> == kRun, "a batch is a run of the moments");
 
-__device__ __forceinline__ void copy16(void *to, const void *from)
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *to, const void *from)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from)
-                 : "memory");
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(BYTES) : "memory");
 }
 
-template <int N>
-constexpr size_t kRingBytes = (size_t)kNormBlock * 16 * kUnroll<N> * kDepth * N;
+// Shared memory of a walk: the ring, then the threads' sums in its place.
+template <typename T, int V, int N>
+constexpr size_t kWalkBytes = std::max((size_t)kNormBlock * sizeof(Vec<T, V>) * kUnroll<N> * kDepth * N,
+                                       (size_t)kNormBlock * (2 * V + 1) * sizeof(float));
 
 template <typename T, int V, int N, typename F>
 __device__ __forceinline__ void walk_rows(unsigned char *ring, const T *const (&from)[N], int64_t stride, int rows, F f)
 {
     using Access = Vec<T, V>;
     Access v[N][kUnroll<N>];
-    if constexpr (sizeof(Access) == 16) {
+    if constexpr (sizeof(Access) >= 4) {
         Access *mine = (Access *)ring + threadIdx.x;
         auto slot = [&](int batch, int n, int k) { return mine + (((batch % kDepth) * N + n) * kUnroll<N> + k) * kNormBlock; };
         const int batches = (rows + kUnroll<N> - 1) / kUnroll<N>;
@@ -327,7 +335,7 @@ __device__ __forceinline__ void walk_rows(unsigned char *ring, const T *const (&
                 if (batch * kUnroll<N> + k < rows)
 #pragma unroll
                     for (int n = 0; n < N; ++n)
-                        copy16(slot(batch, n, k), from[n] + (int64_t)(batch * kUnroll<N> + k) * stride);
+                        copy_async<sizeof(Access)>(slot(batch, n, k), from[n] + (int64_t)(batch * kUnroll<N> + k) * stride);
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
         for (int b = 0; b < kDepth - 1; ++b) issue(b);
@@ -638,7 +646,7 @@ __global__ void __launch_bounds__(kResidentBlock) k_norm_resident(const __grid_c
     ChannelMoments<T, V> own;
     if (at.live) {
         for (int p = at.row; p < count; p += at.rows)
-            copy16(&s_x[p * at.cols + at.col], x + (int64_t)p * a.n.channels);
+            copy_async<16>(&s_x[p * at.cols + at.col], x + (int64_t)p * a.n.channels);
         copies_done();
         // A thread reads only what it copied itself.
         int p = at.row;
@@ -733,8 +741,8 @@ __global__ void __launch_bounds__(kResidentBlock) k_norm_grad_resident(const __g
     Channel<V> ch;
     if (at.live) {
         for (int p = at.row; p < count; p += at.rows) {
-            copy16(&s_x[p * at.cols + at.col], x + (int64_t)p * a.n.channels);
-            copy16(&s_d[p * at.cols + at.col], dout + (int64_t)p * a.n.channels);
+            copy_async<16>(&s_x[p * at.cols + at.col], x + (int64_t)p * a.n.channels);
+            copy_async<16>(&s_d[p * at.cols + at.col], dout + (int64_t)p * a.n.channels);
         }
         ch.load(a.n, at.sample, at.channel0);
         copies_done();
@@ -842,7 +850,7 @@ ResidentPlan resident_plan(const gsr_group_norm &d, int width, bool backward)
 {
     ResidentPlan p;
     const int size = d.dtype == GSR_F32 ? 4 : 2, per_group = d.channels / d.groups;
-    if (width == 1) return p;
+    if (width * size != 16) return p;
     int groups = 1;
     for (; groups <= d.groups; ++groups)
         if (d.groups % groups == 0 && groups * per_group % width == 0 &&
@@ -894,7 +902,9 @@ NormPlan norm_plan(const gsr_ctx *ctx, const gsr_group_norm &d, int width)
     p.slabs = (vectors + p.vectors - 1) / p.vectors;
     const int rows = kNormBlock / p.vectors;
     p.wave = d.samples < 65535 ? d.samples : 65535;   // samples of a launch (a grid's limit)
-    int64_t chunks = (int64_t)kNormOccupancy * ctx->num_sms / ((int64_t)p.wave * p.slabs);
+    // Narrow accesses hold fewer bytes in flight and fewer registers: more blocks.
+    const int blocks = width * (d.dtype == GSR_F32 ? 4 : 2) == 16 ? kNormOccupancy : 3 * kNormOccupancy;
+    int64_t chunks = (int64_t)blocks * ctx->num_sms / ((int64_t)p.wave * p.slabs);
     const int64_t most = (d.positions + (int64_t)rows * kRun - 1) / ((int64_t)rows * kRun);
     if (chunks > most) chunks = most;
     if (chunks < 1) chunks = 1;
@@ -903,19 +913,25 @@ NormPlan norm_plan(const gsr_ctx *ctx, const gsr_group_norm &d, int width)
     return p;
 }
 
+// Elements of an access: 16 bytes, or 4 where the channels or the arrays allow no
+// more, or one.
 int norm_width(const gsr_group_norm &d, const void *x, const void *dout, const void *y)
 {
-    const int full = d.dtype == GSR_F32 ? 4 : 8;
-    const bool ok = d.channels % full == 0 && (uintptr_t)x % 16 == 0 && (uintptr_t)dout % 16 == 0 &&
-                    (uintptr_t)y % 16 == 0;
-    return ok ? full : 1;
+    const int size = d.dtype == GSR_F32 ? 4 : 2;
+    for (int bytes : {16, 4}) {
+        const int width = bytes / size;
+        if (d.channels % width == 0 && (uintptr_t)x % bytes == 0 && (uintptr_t)dout % bytes == 0 &&
+            (uintptr_t)y % bytes == 0)
+            return width;
+    }
+    return 1;
 }
 
-// A kernel that walks rows of N arrays: its rings, or the scalar form's sums.
-template <int N, typename Kernel>
-cudaError_t launch_walk(gsr_ctx *ctx, Kernel *kernel, dim3 grid, int width, cudaStream_t stream, const NormArgs &a)
+// A kernel that walks rows of N arrays.
+template <typename T, int V, int N, typename Kernel>
+cudaError_t launch_walk(gsr_ctx *ctx, Kernel *kernel, dim3 grid, cudaStream_t stream, const NormArgs &a)
 {
-    const size_t smem = width > 1 ? kRingBytes<N> : (size_t)kNormBlock * 3 * sizeof(float);
+    constexpr size_t smem = kWalkBytes<T, V, N>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return launch_kernel_smem(ctx, kernel, grid, kNormBlock, smem, 1, stream, a);
@@ -927,9 +943,9 @@ cudaError_t norm_forward(gsr_ctx *ctx, NormArgs &a, const NormPlan &p, cudaStrea
     for (a.sample0 = 0; a.sample0 < a.samples; a.sample0 += p.wave) {
         const unsigned n = (unsigned)(a.samples - a.sample0 < p.wave ? a.samples - a.sample0 : p.wave);
         const dim3 grid((unsigned)p.chunks, n, (unsigned)p.slabs);
-        cudaError_t e = launch_walk<1>(ctx, k_norm_moments<T, V>, grid, V, stream, a);
+        cudaError_t e = launch_walk<T, V, 1>(ctx, k_norm_moments<T, V>, grid, stream, a);
         if (e == cudaSuccess) e = launch_kernel(ctx, k_norm_merge, dim3((unsigned)a.groups, n), kMergeBlock, stream, a);
-        if (e == cudaSuccess) e = launch_walk<1>(ctx, k_norm_apply<T, V, ACT>, grid, V, stream, a);
+        if (e == cudaSuccess) e = launch_walk<T, V, 1>(ctx, k_norm_apply<T, V, ACT>, grid, stream, a);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -941,10 +957,10 @@ cudaError_t norm_backward(gsr_ctx *ctx, NormArgs &a, const NormPlan &p, cudaStre
     for (a.sample0 = 0; a.sample0 < a.samples; a.sample0 += p.wave) {
         const unsigned n = (unsigned)(a.samples - a.sample0 < p.wave ? a.samples - a.sample0 : p.wave);
         const dim3 grid((unsigned)p.chunks, n, (unsigned)p.slabs);
-        cudaError_t e = launch_walk<2>(ctx, k_norm_grad_sums<T, V, ACT>, grid, V, stream, a);
+        cudaError_t e = launch_walk<T, V, 2>(ctx, k_norm_grad_sums<T, V, ACT>, grid, stream, a);
         if (e == cudaSuccess)
             e = launch_kernel(ctx, k_norm_grad_merge, dim3((unsigned)a.groups, n), kMergeBlock, stream, a);
-        if (e == cudaSuccess) e = launch_walk<2>(ctx, k_norm_grad_apply<T, V, ACT>, grid, V, stream, a);
+        if (e == cudaSuccess) e = launch_walk<T, V, 2>(ctx, k_norm_grad_apply<T, V, ACT>, grid, stream, a);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -974,6 +990,8 @@ cudaError_t dispatch_width(gsr_ctx *ctx, NormArgs &a, const NormPlan &p, const R
     constexpr int kFull = 16 / (int)sizeof(T);
     if (r.fits) return norm_resident<T, kFull, ACT>(ctx, a, r, backward, s);
     if (width == kFull) return backward ? norm_backward<T, kFull, ACT>(ctx, a, p, s) : norm_forward<T, kFull, ACT>(ctx, a, p, s);
+    if constexpr (sizeof(T) == 2)
+        if (width == 2) return backward ? norm_backward<T, 2, ACT>(ctx, a, p, s) : norm_forward<T, 2, ACT>(ctx, a, p, s);
     return backward ? norm_backward<T, 1, ACT>(ctx, a, p, s) : norm_forward<T, 1, ACT>(ctx, a, p, s);
 }
 

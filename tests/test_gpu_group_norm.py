@@ -52,9 +52,11 @@ def test_parity(gsr, ctx, dtype, act, n, s, c, groups):
 
 
 @pytest.mark.parametrize("n,s,c,groups", [(1, 70001, 32, 8), (5, 9001, 128, 32), (300, 5, 16, 4), (2, 40, 2056, 8),
-                                          (1, 65, 4096, 1), (7, 20011, 64, 1)])
+                                          (1, 65, 4096, 1), (7, 20011, 64, 1), (2, 30001, 12, 4), (3, 9000, 6, 1),
+                                          (1, 50003, 3, 3), (2, 7001, 20, 5)])
 def test_parity_long_and_wide(gsr, ctx, n, s, c, groups):
-    _compare(gsr, ctx, *_inputs(n, s, c, BF16, 77 + s), groups, "silu")
+    for dtype in (BF16, F32):
+        _compare(gsr, ctx, *_inputs(n, s, c, dtype, 77 + s), groups, "silu")
 
 
 def test_sizes_around_the_paths(gsr, ctx):
