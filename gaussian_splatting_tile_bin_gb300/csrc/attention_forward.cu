@@ -19,6 +19,15 @@
 // most that factor, which 16-bit P and float sums hold without loss.  P is
 // rounded to the storage type (the tensor cores take 16-bit operands at the full
 // rate); l sums the unrounded values in float.
+//
+// Bound by the tensor cores at head_dim 128: 4,864 queries x 8,192 keys x 16 heads
+// in bf16 take 193 us, 1,690 TFLOP/s, 89% of a large library product's rate (the
+// pipe is active 64% of a quarter of that size, 4 heads in 57 us, where starts and
+// ends weigh more; issue slots 33%, exponentials 32%).  At head_dim 64, 168 us
+// (970 TFLOP/s): a product with 64 columns of output takes the time of one with
+// 128, and each tile's chain of scores, exponentials and output is no shorter.
+// There, four tiles with units of 64 keys took 192 us, two tiles with such units
+// 165 to 197, and turns that keep the two groups' exponentials apart 183.
 #include <math.h>
 
 #include "attention.cuh"
