@@ -51,12 +51,28 @@ struct RangeShift {
     float ds;       // ds is held times this
 };
 
+template <typename T>
+constexpr float kShiftP = std::is_same<T, __half>::value ? 16384.0f : 1.0f;
+
+// amax: bits of the largest |do|.
+template <typename T>
+__device__ __forceinline__ RangeShift range_shift(const uint32_t *amax)
+{
+    RangeShift shift = {kShiftP<T>, 1.0f};
+    if constexpr (std::is_same<T, __half>::value) {
+        const float top = __uint_as_float(*amax);
+        if (top > 0.0f && top < INFINITY) shift.ds = exp2f((float)-ilogbf(top));
+    }
+    return shift;
+}
+
 struct BackwardArgs {
     CUtensorMap q, k, v, dout;
     Schedule work;
     const float *lse2;           // [batch, q_heads, q_pad]: log2(shift.p) - lse log2e
-    float *delta;                // the same: -delta shift.ds / shift.p
-    const RangeShift *shift;
+    const float *row_delta;      // the same: -do . o
+    float *delta;                // the same: -delta shift.ds / shift.p, left by the dq kernel
+    const uint32_t *amax;
     void *dq, *dk, *dv;
     int64_t dq_item, dq_token, dq_head, dk_item, dk_token, dk_head, dv_item, dv_token, dv_head;
     const int32_t *index;        // original keys of packed ones, [batch, kv_len], or NULL
@@ -237,6 +253,8 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                 };
                 scores(n);
                 dp(n + 1);
+                // The next segment's own tiles arrive while this one's last step is computed.
+                if (g.begin + 1 == g.end) product_commit(leader, bar.own_free);
                 for (int i = g.begin; i < g.end; ++i, n += 2, ++step) {
                     const bool more = i + 1 < g.end;
                     barrier_wait_warp(bar.s_read, step & 1, guard);
@@ -250,8 +268,8 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                         dp(n + 3);
                     else
                         product_commit(leader, bar.done);
+                    if (i + 2 == g.end) product_commit(leader, bar.own_free);
                 }
-                product_commit(leader, bar.own_free);
                 ++seg;
             }
         }
@@ -262,7 +280,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
         const uint32_t at_s = tmem + lanes + S::kS + column0, at_dp = tmem + lanes + S::kDp + column0;
         const int row_in_tile = warp % 4 * 32 + lane;
         const float c = a.scale_log2;
-        const RangeShift shift = *a.shift;
+        const RangeShift shift = range_shift<T>(a.amax);
         const float f_dp = shift.ds / shift.p, f_out = a.scale / shift.ds;
         uint32_t n = 0, seg = 0, step = 0;
         while (walk.next(g)) {
@@ -271,9 +289,10 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
             if (g.length > 0) {
                 const int64_t at = ((int64_t)g.item * a.q_heads + head) * a.q_pad + row;
                 const float2 c2 = make_float2(c, c), f2 = make_float2(f_dp, f_dp);
-                const float lse = a.lse2[at], delta = a.delta[at];
+                const float lse = a.lse2[at], delta = a.row_delta[at] * f_dp;
                 const float2 lse2 = make_float2(lse, lse);
                 float2 delta2 = make_float2(delta, delta);
+                if (part == 0 && g.begin == 0 && g.total > 1) a.delta[at] = delta;
                 for (int i = g.begin; i < g.end; ++i, n += 2, ++step) {
                     Columns r;
                     barrier_wait_warp(bar.s, step & 1, guard);
@@ -327,7 +346,8 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                                                    row_in_tile * 128;
                                 for (int b = 0; b < S::kBlocks; ++b)
                                     for (int e = 0; e < 8; ++e)
-                                        *(uint4 *)(k + b * kBlockBytes + e * 16) = make_uint4(0, 0, 0, 0);
+                                        *(uint4 *)(k + b * kBlockBytes + ((e + lane) & 7) * 16) =
+                                            make_uint4(0, 0, 0, 0);
                             }
                             fence_async();
                         }
@@ -483,6 +503,8 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
                 };
                 scores(n);
                 dp(n + 1);
+                // The next segment's own tiles arrive while this one's last step is computed.
+                if (g.begin + 1 == g.end) product_commit(leader, bar.own_free);
                 for (int i = g.begin; i < g.end; ++i, n += 2, ++step) {
                     const bool more = i + 1 < g.end;
                     barrier_wait_warp(bar.p_ready, step & 1, guard);
@@ -498,8 +520,8 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
                         dp(n + 3);
                     else
                         product_commit(leader, bar.done);
+                    if (i + 2 == g.end) product_commit(leader, bar.own_free);
                 }
-                product_commit(leader, bar.own_free);
                 ++seg;
             }
         }
@@ -510,7 +532,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
         const uint32_t at_s = tmem + lanes + S::kS + column0, at_dp = tmem + lanes + S::kDp + column0;
         const int row_in_tile = warp % 4 * 32 + lane;
         const float c = a.scale_log2;
-        const RangeShift shift = *a.shift;
+        const RangeShift shift = range_shift<T>(a.amax);
         const float f_dp = shift.ds / shift.p, f_k = a.scale / shift.ds, f_v = 1.0f / shift.p;
         const float2 c2 = make_float2(c, c), f2 = make_float2(f_dp, f_dp);
         uint32_t n = 0, seg = 0, step = 0;
@@ -695,7 +717,6 @@ struct RowArgs {
     gsr_heads out, dout;
     const float *lse;
     float *lse2, *delta;
-    RangeShift *shift;
     uint32_t *amax;          // bits of the largest |do| (f16)
     int64_t rows;            // batch x q_pad x q_heads
     int q_len, q_pad, q_heads, dim;
@@ -713,10 +734,17 @@ struct RowPlace {
     {
         row = block * (256 / LANES) + threadIdx.x / LANES;
         c = threadIdx.x % LANES * 8;
-        const uint32_t r = (uint32_t)row, t = r / a.q_heads;
-        head = r - t * a.q_heads;
-        item = t / a.q_pad;
-        token = t - item * a.q_pad;
+        if (a.rows >> 32) {   // many items of few queries, padded
+            const int64_t t = row / a.q_heads;
+            head = (uint32_t)(row - t * a.q_heads);
+            item = (uint32_t)(t / a.q_pad);
+            token = (uint32_t)(t - (int64_t)item * a.q_pad);
+        } else {
+            const uint32_t r = (uint32_t)row, t = r / a.q_heads;
+            head = r - t * a.q_heads;
+            item = t / a.q_pad;
+            token = t - item * a.q_pad;
+        }
         live = row < a.rows && token < (uint32_t)a.q_len && c < a.dim;
     }
     template <typename T>
@@ -727,48 +755,22 @@ struct RowPlace {
     }
 };
 
-template <typename T, int LANES>
-__global__ void __launch_bounds__(256) k_attention_largest(const RowArgs a)
-{
-    grid_dependency_begin();
-    __shared__ uint32_t s_max;
-    if (threadIdx.x == 0) s_max = 0;
-    __syncthreads();
-    const int64_t blocks = (a.rows + 256 / LANES - 1) / (256 / LANES);
-    uint32_t top = 0;
-    for (int64_t block = blockIdx.x; block < blocks; block += gridDim.x) {
-        const RowPlace<LANES> at(a, block);
-        if (!at.live) continue;
-        const Vec<T, 8> v = at.template load<T>(a.dout);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(fabsf(to_float(v.e[e]))));
-    }
-    top = __reduce_max_sync(~0u, top);
-    if (threadIdx.x % 32 == 0) atomicMax(&s_max, top);
-    __syncthreads();
-    // The largest of all is the same in any order.
-    if (threadIdx.x == 0) atomicMax(a.amax, s_max);
-}
-
-// -lse in base 2 and -delta, with the shifts of p and ds folded in; rows behind
-// q_len, and rows without keys, get p = 0.
+// -lse in base 2 with p's shift folded in, -delta, and the largest |do| for ds'
+// shift; rows behind q_len, and rows without keys, get p = 0.
 template <typename T, int LANES>
 __global__ void __launch_bounds__(256) k_attention_rows(const RowArgs a)
 {
     grid_dependency_begin();
-    RangeShift shift = {1.0f, 1.0f};
-    if (a.amax) {
-        const float top = __uint_as_float(*a.amax);
-        shift.p = 16384.0f;
-        if (top > 0.0f && top < INFINITY) shift.ds = exp2f((float)-ilogbf(top));
-    }
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.shift = shift;
     const RowPlace<LANES> at(a, blockIdx.x);
     float sum = 0.0f;
+    uint32_t top = 0;
     if (at.live) {
         const Vec<T, 8> o = at.template load<T>(a.out), d = at.template load<T>(a.dout);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(to_float(o.e[e]), to_float(d.e[e]), sum);
+        for (int e = 0; e < 8; ++e) {
+            sum = fmaf(to_float(o.e[e]), to_float(d.e[e]), sum);
+            top = max(top, __float_as_uint(fabsf(to_float(d.e[e]))));
+        }
     }
     for (int d = LANES / 2; d > 0; d /= 2) sum += __shfl_xor_sync(~0u, sum, d);
     if (at.row < a.rows && at.c == 0) {
@@ -776,25 +778,30 @@ __global__ void __launch_bounds__(256) k_attention_rows(const RowArgs a)
         float lse = INFINITY;
         if (at.token < (uint32_t)a.q_len) {
             lse = a.lse[row * a.q_len + at.token];
-            lse = lse == -INFINITY ? INFINITY : lse * kLog2e - log2f(shift.p);
+            lse = lse == -INFINITY ? INFINITY : lse * kLog2e - log2f(kShiftP<T>);
         }
         a.lse2[to] = -lse;
-        a.delta[to] = -sum * (shift.ds / shift.p);
+        a.delta[to] = -sum;
+    }
+    if constexpr (std::is_same<T, __half>::value) {
+        // The largest of all is the same in any order; what is there already needs no atomic.
+        __shared__ uint32_t s_top[8];
+        top = __reduce_max_sync(~0u, top);
+        if (threadIdx.x % 32 == 0) s_top[threadIdx.x / 32] = top;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < 8; ++w) top = max(top, s_top[w]);
+            if (top > *(volatile uint32_t *)a.amax) atomicMax(a.amax, top);
+        }
     }
 }
 
 template <typename T, int LANES>
 int row_statistics(gsr_ctx *ctx, const RowArgs &r, cudaStream_t stream)
 {
-    const int64_t blocks = (r.rows + 256 / LANES - 1) / (256 / LANES), most = 8 * (int64_t)ctx->num_sms;
-    if (r.amax) {
-        if (int rc = cuda_check(ctx, cudaMemsetAsync(r.amax, 0, sizeof(uint32_t), stream), "k_attention_largest"))
-            return rc;
-        if (int rc = cuda_check(ctx, launch_kernel(ctx, k_attention_largest<T, LANES>,
-                                                   dim3((unsigned)(blocks < most ? blocks : most)), 256, stream, r),
-                                "k_attention_largest"))
-            return rc;
-    }
+    const int64_t blocks = (r.rows + 256 / LANES - 1) / (256 / LANES);
+    if (std::is_same<T, __half>::value)
+        if (int rc = cuda_check(ctx, cudaMemsetAsync(r.amax, 0, sizeof(uint32_t), stream), "k_attention_rows")) return rc;
     return cuda_check(ctx, launch_kernel(ctx, k_attention_rows<T, LANES>, dim3((unsigned)blocks), 256, stream, r),
                       "k_attention_rows");
 }
@@ -846,7 +853,7 @@ int launch_backward(gsr_ctx *ctx, BackwardArgs &a, const Schedule &by_query, con
 {
     // Blocks of a cut tile's sum: its rows' vectors over a block's items.
     const int vectors = kRowTile * a.dim / 8, each = kSumBlock * kSumItems;
-    // Queries first: they correct delta where the keys are few.
+    // Queries first: they leave delta as the keys' kernel takes it.
     a.work = by_query;
     if (int rc = launch_big(ctx, k_attention_grad_q<T, HD>, "k_attention_grad_q", blocks_q, BackwardShape<HD>::kSmemQ, a,
                             stream))
@@ -908,14 +915,15 @@ int backward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr
     const size_t stats = round_up((size_t)rows * sizeof(float), 512);
     const size_t partial = round_up((size_t)2 * blocks * kRowTile * 2 * d.head_dim * sizeof(float), 256);
     void *work;
-    if (int rc = workspace(ctx, packed + 2 * stats + partial + 256, stream, &work)) return rc;
+    if (int rc = workspace(ctx, packed + 3 * stats + partial + 256, stream, &work)) return rc;
     unsigned char *p = (unsigned char *)work + packed;
-    float *lse2 = (float *)p, *delta = (float *)(p + stats);
-    a.partial = (float *)(p + 2 * stats);
-    RangeShift *shift = (RangeShift *)(p + 2 * stats + partial);
+    float *lse2 = (float *)p, *row_delta = (float *)(p + stats);
+    a.partial = (float *)(p + 3 * stats);
+    uint32_t *amax = (uint32_t *)(p + 3 * stats + partial);
     a.lse2 = lse2;
-    a.delta = delta;
-    a.shift = shift;
+    a.row_delta = row_delta;
+    a.delta = (float *)(p + 2 * stats);
+    a.amax = amax;
     a.status = ctx->status_dev;
 
     RowArgs r = {};
@@ -923,14 +931,13 @@ int backward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr
     r.dout = dout;
     r.lse = lse;
     r.lse2 = lse2;
-    r.delta = delta;
-    r.shift = shift;
+    r.delta = row_delta;
+    r.amax = amax;
     r.rows = rows;
     r.q_len = d.q_len;
     r.q_pad = a.q_pad;
     r.q_heads = d.q_heads;
     r.dim = d.head_dim;
-    if (d.dtype == GSR_F16) r.amax = (uint32_t *)(shift + 1);
     if (int rc = d.head_dim <= 64 ? row_statistics<T, 8>(ctx, r, stream) : row_statistics<T, 16>(ctx, r, stream)) return rc;
 
     gsr_heads keys = k, values = v;

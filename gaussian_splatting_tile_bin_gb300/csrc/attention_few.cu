@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kFewJoinBlock) k_attention_few_join(const __gr
     float total = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const bool mine = lane * 4 < a.dim;
-#pragma unroll 4
+#pragma unroll 8
     for (int s = 0; s < a.splits; ++s) {
         const float w = expf(a.partial_lse[part0 + s * 16] - shift);
         total += w;

@@ -163,6 +163,8 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
                 tmem_fence_after();
                 for (int t = 0; t < tiles; ++t) scores(t, kv);
                 release(kv);
+                // The next segment's Q arrives while this one's last keys are worked on.
+                if (g.begin + 1 == g.end) product_commit(leader, b_q_free);
                 for (int i = g.begin; i < g.end; ++i, kv += 2) {
                     const bool more = i + 1 < g.end;
                     await(kv + 1);
@@ -179,8 +181,8 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
                     }
                     release(kv + 1);
                     if (more) release(kv + 2);
+                    if (i + 2 == g.end) product_commit(leader, b_q_free);
                 }
-                product_commit(leader, b_q_free);
                 ++seg;
             }
         }
@@ -225,7 +227,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
                                                row_in_tile * 128;
                             for (int b = 0; b < S::kBlocks; ++b)
                                 for (int e = 0; e < 8; ++e)
-                                    *(uint4 *)(v + b * kBlockBytes + e * 16) = make_uint4(0, 0, 0, 0);
+                                    *(uint4 *)(v + b * kBlockBytes + ((e + lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
                         }
                         fence_async();
                     }
