@@ -473,6 +473,10 @@ int check_attention(gsr_ctx *ctx, const gsr_attention *d)
     constexpr int64_t kMost = 0x7fffffff;
     if ((int64_t)d->batch * d->q_len > kMost / d->q_heads || (int64_t)d->batch * d->kv_len > kMost / d->kv_heads)
         return fail(ctx, GSR_ERR_INVALID_ARG, "batch * heads * length above 2^31 - 1");
+    // Steps of 128 x 128 scores, the unit in which the kernels divide their work.
+    const int64_t row_tiles = (int64_t)d->batch * d->q_heads * (((int64_t)d->q_len + 127) / 128);
+    if (((int64_t)d->kv_len + 127) / 128 > kMost / (row_tiles > 1 ? row_tiles : 1))
+        return fail(ctx, GSR_ERR_INVALID_ARG, "2^31 steps of 128 x 128 scores or more");
     if (!aligned(d->kv_lengths, 4)) return fail(ctx, GSR_ERR_INVALID_ARG, "kv_lengths must be 4-byte aligned");
     return GSR_OK;
 }

@@ -81,6 +81,7 @@ struct BackwardArgs {
     int q_len, q_pad, kv_len, q_heads, group, dim;
     int q_tiles;                 // tiles of 128 queries per head
     int q_item, q_head, dout_item, dout_head, k_item, k_head, v_item, v_head;
+    bool wide_q, wide_kv;        // the gradients' rows take 32-byte stores
     float scale, scale_log2;
 };
 
@@ -240,32 +241,36 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                 if (g.length == 0) continue;
                 barrier_wait_warp(bar.own, seg & 1, guard);
                 const uint32_t s_q = s_own, s_do = s_own + S::kTileBytes;
-                auto scores = [&](uint32_t x) {
+                // The tile's last step takes the scores of its keys alone.
+                const uint32_t form_last = product_form<T>(round_keys(g.length - (g.total - 1) * kKeyTile), false);
+                auto scores = [&](uint32_t x, uint32_t form) {
                     await(x);
-                    product_rows<HD>(leader, tmem + S::kS, s_q, stage_at(x), form_s, steps);
+                    product_rows<HD>(leader, tmem + S::kS, s_q, stage_at(x), form, steps);
                     product_commit(leader, bar.s);
                 };
-                auto dp = [&](uint32_t x) {
+                auto dp = [&](uint32_t x, uint32_t form) {
                     await(x);
-                    product_rows<HD>(leader, tmem + S::kDp, s_do, stage_at(x), form_s, steps);
+                    product_rows<HD>(leader, tmem + S::kDp, s_do, stage_at(x), form, steps);
                     product_commit(leader, bar.dp);
                     release(x);
                 };
-                scores(n);
-                dp(n + 1);
+                const uint32_t form_first = g.begin + 1 < g.total ? form_s : form_last;
+                scores(n, form_first);
+                dp(n + 1, form_first);
                 // The next segment's own tiles arrive while this one's last step is computed.
                 if (g.begin + 1 == g.end) product_commit(leader, bar.own_free);
                 for (int i = g.begin; i < g.end; ++i, n += 2, ++step) {
                     const bool more = i + 1 < g.end;
+                    const uint32_t form_next = i + 2 < g.total ? form_s : form_last;
                     barrier_wait_warp(bar.s_read, step & 1, guard);
                     tmem_fence_after();
-                    if (more) scores(n + 2);
+                    if (more) scores(n + 2, form_next);
                     barrier_wait_warp(bar.ready, step & 1, guard);
                     tmem_fence_after();
-                    product_across<0, 8>(leader, tmem + S::kOut, tmem + S::kDs + (step & 1) * 64, stage_at(n), form_o, i > g.begin);
+                    product_across(leader, tmem + S::kOut, tmem + S::kDs + (step & 1) * 64, stage_at(n), form_o, i > g.begin);
                     release(n);
                     if (more)
-                        dp(n + 3);
+                        dp(n + 3, form_next);
                     else
                         product_commit(leader, bar.done);
                     if (i + 2 == g.end) product_commit(leader, bar.own_free);
@@ -282,18 +287,28 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
         const float c = a.scale_log2;
         const RangeShift shift = range_shift<T>(a.amax);
         const float f_dp = shift.ds / shift.p, f_out = a.scale / shift.ds;
+        const float2 c2 = make_float2(c, c), f2 = make_float2(f_dp, f_dp);
         uint32_t n = 0, seg = 0, step = 0;
-        while (walk.next(g)) {
-            const int head = g.tile / a.q_tiles, row0 = (g.tile - head * a.q_tiles) * kRowTile;
-            const int row = row0 + row_in_tile;
-            if (g.length > 0) {
-                const int64_t at = ((int64_t)g.item * a.q_heads + head) * a.q_pad + row;
-                const float2 c2 = make_float2(c, c), f2 = make_float2(f_dp, f_dp);
-                const float lse = a.lse2[at], delta = a.row_delta[at] * f_dp;
+        // The next segment's place and statistics are fetched while one is finished.
+        bool there = walk.next(g);
+        float lse = 0.0f, delta = 0.0f;
+        auto statistics = [&](const Segment &t) {
+            const int head = t.tile / a.q_tiles;
+            return ((int64_t)t.item * a.q_heads + head) * a.q_pad + (t.tile - head * a.q_tiles) * kRowTile + row_in_tile;
+        };
+        auto fetch = [&] {
+            if (!there || g.length == 0) return;
+            lse = a.lse2[statistics(g)];
+            delta = a.row_delta[statistics(g)];
+        };
+        fetch();
+        while (there) {
+            const Segment t = g;
+            if (t.length > 0) {
                 const float2 lse2 = make_float2(lse, lse);
-                float2 delta2 = make_float2(delta, delta);
-                if (part == 0 && g.begin == 0 && g.total > 1) a.delta[at] = delta;
-                for (int i = g.begin; i < g.end; ++i, n += 2, ++step) {
+                float2 delta2 = make_float2(delta * f_dp, delta * f_dp);
+                if (part == 0 && t.begin == 0 && t.total > 1) a.delta[statistics(t)] = delta2.x;
+                for (int i = t.begin; i < t.end; ++i, n += 2, ++step) {
                     Columns r;
                     barrier_wait_warp(bar.s, step & 1, guard);
                     tmem_fence_after();
@@ -301,7 +316,8 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                     tmem_fence_before();
                     __syncwarp();
                     if (lane == 0) barrier_arrive(bar.s_read);
-                    const int valid = g.length - i * kKeyTile;
+                    const int valid = t.length - i * kKeyTile;
+                    const int mine = valid - column0;   // of this thread's columns
                     float2 p[kColumnsEach / 2];
 #pragma unroll
                     for (int y = 0; y < kColumnsEach / 2; ++y) {
@@ -312,50 +328,38 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                     barrier_wait_warp(bar.dp, step & 1, guard);
                     tmem_fence_after();
                     load_columns(r, at_dp);
-                    if (g.total == 1) {
+                    if (t.total == 1) {
                         // Few keys, whose ds nearly cancel: delta from p and dp themselves, here and
                         // for the key gradients, instead of from the rounded output.
                         float sum = 0.0f;
 #pragma unroll
-                        for (int y = 0; y < kColumnsEach / 2; ++y) {
-                            const float2 t = mul2(p[y], pair(r, 2 * y));
-                            sum += (column0 + 2 * y < valid ? t.x : 0.0f) + (column0 + 2 * y + 1 < valid ? t.y : 0.0f);
-                        }
+                        for (int y = 0; y < kColumnsEach / 2; ++y)
+                            if (y / 8 * 16 < mine) {
+                                const float2 e = mul2(p[y], pair(r, 2 * y));
+                                sum += (2 * y < mine ? e.x : 0.0f) + (2 * y + 1 < mine ? e.y : 0.0f);
+                            }
                         s_sum[part * kRowTile + row_in_tile] = sum;
                         asm volatile("bar.sync 1, %0;" ::"n"(kComputeWarps * 32) : "memory");
                         sum = 0.0f;
 #pragma unroll
                         for (int x = 0; x < kGroups; ++x) sum += s_sum[x * kRowTile + row_in_tile];
-                        const float mine = -sum * (f_dp / shift.p);
-                        delta2 = make_float2(mine, mine);
-                        if (part == 0) a.delta[at] = mine;
+                        const float exact = -sum * (f_dp / shift.p);
+                        delta2 = make_float2(exact, exact);
+                        if (part == 0) a.delta[statistics(t)] = exact;
                     }
                     uint32_t packed[kColumnsEach / 2];
+#pragma unroll
+                    for (int y = 0; y < kColumnsEach / 2; ++y) {
+                        const float2 ds = mul2(p[y], fma2(pair(r, 2 * y), f2, delta2));
+                        packed[y] = pack2<T>(ds.x, ds.y);
+                    }
                     if (valid < kKeyTile) {
 #pragma unroll
-                        for (int y = 0; y < kColumnsEach / 2; ++y) {
-                            const float2 ds = mul2(p[y], fma2(pair(r, 2 * y), f2, delta2));
-                            packed[y] = pack2<T>(column0 + 2 * y < valid ? ds.x : 0.0f,
-                                                 column0 + 2 * y + 1 < valid ? ds.y : 0.0f);
-                        }
+                        for (int y = 0; y < kColumnsEach / 2; ++y)
+                            packed[y] = 2 * y + 1 < mine ? packed[y] : 2 * y < mine ? packed[y] & 0xffff : 0;
                         if (part == 0) {
-                            // What lies behind the item's last key must not meet the zero ds as infinities or NaN.
                             barrier_wait_warp(bar.ring + 8 * (n % S::kStages), n / S::kStages & 1, guard);
-                            if (row_in_tile >= valid) {
-                                unsigned char *k = s_raw + (s_ring - raw) + n % S::kStages * S::kTileBytes +
-                                                   row_in_tile * 128;
-                                for (int b = 0; b < S::kBlocks; ++b)
-                                    for (int e = 0; e < 8; ++e)
-                                        *(uint4 *)(k + b * kBlockBytes + ((e + lane) & 7) * 16) =
-                                            make_uint4(0, 0, 0, 0);
-                            }
-                            fence_async();
-                        }
-                    } else {
-#pragma unroll
-                        for (int y = 0; y < kColumnsEach / 2; ++y) {
-                            const float2 ds = mul2(p[y], fma2(pair(r, 2 * y), f2, delta2));
-                            packed[y] = pack2<T>(ds.x, ds.y);
+                            clear_tail<S::kBlocks>(s_raw + (s_ring - raw) + n % S::kStages * S::kTileBytes, row_in_tile, valid);
                         }
                     }
                     __syncwarp();
@@ -364,16 +368,20 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                     __syncwarp();
                     if (lane == 0) barrier_arrive(bar.ready);
                 }
+            }
+            there = walk.next(g);
+            fetch();
+            if (t.length > 0) {
                 barrier_wait_warp(bar.done, seg++ & 1, guard);
                 tmem_fence_after();
             }
-            const bool store = row < a.q_len, whole = g.whole();
-            T *out = (T *)a.dq + g.item * a.dq_item + (int64_t)row * a.dq_token + head * a.dq_head;
-            float *partial = a.partial + ((int64_t)partial_slot(g, blockIdx.x) * kRowTile + row_in_tile) * a.dim;
+            const int head = t.tile / a.q_tiles, row = (t.tile - head * a.q_tiles) * kRowTile + row_in_tile;
+            T *out = (T *)a.dq + t.item * a.dq_item + (int64_t)row * a.dq_token + head * a.dq_head;
+            float *partial = a.partial + ((int64_t)partial_slot(t, blockIdx.x) * kRowTile + row_in_tile) * a.dim;
             for (int x = part * 32; x < HD && x < a.dim; x += kGroups * 32) {
                 uint32_t o[32];
                 __syncwarp();
-                if (g.length > 0) {
+                if (t.length > 0) {
                     tmem_load32(o, tmem + lanes + S::kOut + x);
                     tmem_wait_load();
                     pin(o);
@@ -381,21 +389,11 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
 #pragma unroll
                     for (int y = 0; y < 32; ++y) o[y] = 0;
                 }
-                if (store) {
+                if (row < a.q_len) {
+                    float f[32];
 #pragma unroll
-                    for (int y = 0; y < 32; y += 8)
-                        if (x + y < a.dim) {
-                            float f[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(o[y + e]) * f_out;
-                            if (whole) {
-                                *(uint4 *)(out + x + y) = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]),
-                                                                     pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
-                            } else {
-                                *(float4 *)(partial + x + y) = make_float4(f[0], f[1], f[2], f[3]);
-                                *(float4 *)(partial + x + y + 4) = make_float4(f[4], f[5], f[6], f[7]);
-                            }
-                        }
+                    for (int y = 0; y < 32; ++y) f[y] = __uint_as_float(o[y]) * f_out;
+                    store_results(out + x, partial + x, t.whole(), a.wide_q, a.dim - x, f);
                 }
             }
             tmem_fence_before();
@@ -509,11 +507,11 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
                     const bool more = i + 1 < g.end;
                     barrier_wait_warp(bar.p_ready, step & 1, guard);
                     tmem_fence_after();
-                    product_across<0, 8>(leader, tmem + kOutV, tmem + S::kS, stage_at(n + 1), form_o, i > g.begin, kGroups);
+                    product_across(leader, tmem + kOutV, tmem + S::kS, stage_at(n + 1), form_o, i > g.begin, kGroups);
                     if (more) scores(n + 2);
                     barrier_wait_warp(bar.ready, step & 1, guard);
                     tmem_fence_after();
-                    product_across<0, 8>(leader, tmem + kOutK, tmem + S::kDp, stage_at(n), form_o, i > g.begin, kGroups);
+                    product_across(leader, tmem + kOutK, tmem + S::kDp, stage_at(n), form_o, i > g.begin, kGroups);
                     release(n);
                     release(n + 1);
                     if (more)
@@ -618,23 +616,10 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
                     }
                     if (store) {
                         const float factor = which ? f_v : f_k;
-                        T *out = which ? out_v : out_k;
+                        float f[32];
 #pragma unroll
-                        for (int y = 0; y < 32; y += 8)
-                            if (x + y < a.dim) {
-                                float f[8];
-#pragma unroll
-                                for (int e = 0; e < 8; ++e)
-                                    f[e] = live ? __uint_as_float(o[y + e]) * factor : 0.0f;
-                                if (whole) {
-                                    *(uint4 *)(out + x + y) = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]),
-                                                                         pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
-                                } else {
-                                    float *to = partial + which * a.dim + x + y;
-                                    *(float4 *)to = make_float4(f[0], f[1], f[2], f[3]);
-                                    *(float4 *)(to + 4) = make_float4(f[4], f[5], f[6], f[7]);
-                                }
-                            }
+                        for (int y = 0; y < 32; ++y) f[y] = live ? __uint_as_float(o[y]) * factor : 0.0f;
+                        store_results((which ? out_v : out_k) + x, partial + which * a.dim + x, whole, a.wide_kv, a.dim - x, f);
                     }
                 }
             }
@@ -950,6 +935,8 @@ int backward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr
         a.index = pack.index;
         if (int rc = zero_rows(ctx, dk, dv, d, d.kv_len, d.kv_heads, true, stream)) return rc;
     }
+    a.wide_q = rows_of_32_bytes(dq, d.head_dim);
+    a.wide_kv = rows_of_32_bytes(dk, d.head_dim) && rows_of_32_bytes(dv, d.head_dim);
     a.q_item = q.batch_stride != 0;
     a.q_head = q.head_stride != 0;
     a.dout_item = dout.batch_stride != 0;

@@ -51,6 +51,7 @@ struct ForwardArgs {
     uint32_t *status;
     int q_len, q_heads, group, dim, row_tiles;
     int q_item, q_head, k_item, k_head, v_item, v_head;   // 0: one array for all items / heads
+    bool wide;             // out's rows take 32-byte stores
     float scale_log2;
 };
 
@@ -150,8 +151,8 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
             auto stage_at = [&](uint32_t n) { return s_kv + n % S::kStages * S::kTileBytes; };
             auto await = [&](uint32_t n) { barrier_wait_warp(b_kv + 8 * (n % S::kStages), n / S::kStages & 1, guard); };
             auto release = [&](uint32_t n) { product_commit(leader, b_kv_free + 8 * (n % S::kStages)); };
-            auto scores = [&](int t, uint32_t n) {
-                product_rows<HD>(leader, tmem + t * kKeyTile, s_q + t * S::kTileBytes, stage_at(n), form_s, steps);
+            auto scores = [&](int t, uint32_t n, uint32_t form) {
+                product_rows<HD>(leader, tmem + t * kKeyTile, s_q + t * S::kTileBytes, stage_at(n), form, steps);
                 product_commit(leader, b_s + 8 * t);
             };
             while (walk.next(g)) {
@@ -161,22 +162,25 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
                 barrier_wait_warp(b_q, seg & 1, guard);
                 await(kv);
                 tmem_fence_after();
-                for (int t = 0; t < tiles; ++t) scores(t, kv);
+                // The tile's last step takes the scores of its keys alone.
+                const uint32_t form_last = product_form<T>(round_keys(g.length - (g.total - 1) * kKeyTile), false);
+                for (int t = 0; t < tiles; ++t) scores(t, kv, g.begin + 1 < g.total ? form_s : form_last);
                 release(kv);
                 // The next segment's Q arrives while this one's last keys are worked on.
                 if (g.begin + 1 == g.end) product_commit(leader, b_q_free);
                 for (int i = g.begin; i < g.end; ++i, kv += 2) {
                     const bool more = i + 1 < g.end;
+                    const uint32_t form_next = i + 2 < g.total ? form_s : form_last;
                     await(kv + 1);
                     for (int t = 0; t < tiles; ++t) {
                         barrier_wait_warp(b_p + 8 * t, p[t]++ & 1, guard);
                         tmem_fence_after();
-                        product_across<0, 8>(leader, tmem + S::kOut + t * HD, tmem + t * kKeyTile, stage_at(kv + 1), form_o,
-                                             i > g.begin);
+                        product_across(leader, tmem + S::kOut + t * HD, tmem + t * kKeyTile, stage_at(kv + 1), form_o,
+                                       i > g.begin);
                         product_commit(leader, b_o + 8 * t);
                         if (more) {
                             if (t == 0) await(kv + 2);
-                            scores(t, kv + 2);
+                            scores(t, kv + 2, form_next);
                         }
                     }
                     release(kv + 1);
@@ -222,14 +226,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
                         // probabilities as infinities or NaN.
                         const uint32_t at_v = kv + 2 * (i - g.begin) + 1;
                         barrier_wait_warp(b_kv + 8 * (at_v % S::kStages), at_v / S::kStages & 1, guard);
-                        if (row_in_tile >= valid) {
-                            unsigned char *v = s_raw + (s_kv - raw) + at_v % S::kStages * S::kTileBytes +
-                                               row_in_tile * 128;
-                            for (int b = 0; b < S::kBlocks; ++b)
-                                for (int e = 0; e < 8; ++e)
-                                    *(uint4 *)(v + b * kBlockBytes + ((e + lane) & 7) * 16) = make_uint4(0, 0, 0, 0);
-                        }
-                        fence_async();
+                        clear_tail<S::kBlocks>(s_raw + (s_kv - raw) + at_v % S::kStages * S::kTileBytes, row_in_tile, valid);
                     }
                     auto clear_ragged = [&](int h) {
 #pragma unroll
@@ -326,20 +323,10 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
                     for (int y = 0; y < 32; ++y) o[y] = 0;
                 }
                 if (store) {
+                    float f[32];
 #pragma unroll
-                    for (int y = 0; y < 32; y += 8)
-                        if (x + y < a.dim) {
-                            float f[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) f[e] = inv == 0.0f ? 0.0f : __uint_as_float(o[y + e]) * inv;
-                            if (whole) {
-                                *(uint4 *)(out + x + y) = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]),
-                                                                     pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
-                            } else {
-                                *(float4 *)(partial + x + y) = make_float4(f[0], f[1], f[2], f[3]);
-                                *(float4 *)(partial + x + y + 4) = make_float4(f[4], f[5], f[6], f[7]);
-                            }
-                        }
+                    for (int y = 0; y < 32; ++y) f[y] = inv == 0.0f ? 0.0f : __uint_as_float(o[y]) * inv;
+                    store_results(out + x, partial + x, whole, a.wide, a.dim - x, f);
                 }
             }
             if (store) {
@@ -491,6 +478,7 @@ int forward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr_
         values = p.v;
         a.work.lengths = p.counts;
     }
+    a.wide = rows_of_32_bytes(out, d.head_dim);
     a.q_item = q.batch_stride != 0;
     a.q_head = q.head_stride != 0;
     a.k_item = keys.batch_stride != 0;

@@ -266,16 +266,16 @@ __device__ __forceinline__ void product_rows(bool leader, uint32_t d, uint32_t a
     }
 }
 
-// d (+)= a b with a (128 rows, 16-bit pairs in tensor memory) against rows
-// 16 K0 .. 16 K1 - 1 of tile b.  a's 128 terms lie in `groups` runs, each at the
-// start of its own 128 / groups columns (1: one run of 64 columns).
-template <int K0, int K1>
+// d (+)= a b with a (128 rows, 16-bit pairs in tensor memory) against the 128
+// rows of tile b.  a's 128 terms lie in `groups` runs, each at the start of its
+// own 128 / groups columns (1: one run of 64 columns).  (Fewer steps for a tile's
+// tail made every product's issue slower: 184 us where these take 165.)
 __device__ __forceinline__ void product_across(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t form, bool add,
                                                int groups = 1)
 {
     const uint32_t b0 = operand_across(b);
 #pragma unroll
-    for (int k = K0; k < K1; ++k) {
+    for (int k = 0; k < 8; ++k) {
         const int each = 8 / groups;
         product_ts(leader, d, a + k / each * (128 / groups) + k % each * 8, b0 + (k * 2048 >> 4), form, add || k != 0);
     }

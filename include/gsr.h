@@ -514,7 +514,9 @@ int gsr_rotary_backward(gsr_ctx *ctx, const gsr_rotary *desc, const gsr_heads *d
  * head_dim is a multiple of 8, at most GSR_ATTENTION_MAX_HEAD_DIM; arrays are
  * 16-byte aligned and their strides multiples of 8 elements.
  * Errors: GSR_ERR_INVALID_ARG (the above, negative sizes, q_heads not a multiple
- * of kv_heads, scale not finite or <= 0), GSR_ERR_OOM, GSR_ERR_CUDA. */
+ * of kv_heads or above GSR_MAX_HEADS, scale not finite or <= 0, batch above 2^16,
+ * a length above 2^24, 2^31 rows of q or of k or more, 2^31 steps of 128 x 128
+ * scores or more), GSR_ERR_OOM, GSR_ERR_CUDA. */
 #define GSR_ATTENTION_MAX_HEAD_DIM 128
 typedef struct gsr_attention {
     int32_t dtype;

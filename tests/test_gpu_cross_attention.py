@@ -266,3 +266,20 @@ def test_refusals(gsr, ctx):
                  lambda: f(ctx, q, k, v, lse=torch.ones(2, 2, 4, device="cuda"))):
         with pytest.raises(ValueError):
             call()
+
+
+def test_too_many_steps_are_refused(gsr, ctx):
+    q = torch.zeros(1, 1 << 17, 1, 8, dtype=BF16, device="cuda").expand(1, 1 << 17, 1024, 8)
+    k = torch.zeros(1, 1 << 24, 1, 8, dtype=BF16, device="cuda")
+    with pytest.raises(gsr.GsrError, match="2\\^31 steps") as e:
+        gsr.cross_attention_forward(ctx, q, k, k, out=q)
+    assert e.value.code == 1
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_items_of_many_lengths(gsr, ctx, d):
+    """More items than a warp has lanes, some without keys, shares that start in any of them."""
+    b, lq, lk = 75, 130, 300
+    q, k, v, dout = _inputs(b, lq, lk, 2, 1, d, F16, 71)
+    lengths = torch.tensor([(37 * i) % 301 if i % 5 else 0 for i in range(b)], dtype=torch.int32)
+    _compare(gsr, ctx, q, k, v, dout, lengths=lengths)
