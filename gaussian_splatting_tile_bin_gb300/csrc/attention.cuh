@@ -164,6 +164,26 @@ __device__ Walk<Line> walk_share(const Schedule &s)
     return Walk<Line>(s, share_begin(line, block, blocks), block < blocks ? share_begin(line, block + 1, blocks) : line);
 }
 
+// The value of lane 0 of a whole warp, which lets the compiler keep what follows
+// from it in registers that the warp shares.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(~0u, x, 0); }
+
+// The next segment, for a whole warp.  (Products issue from such registers: as
+// long as the warps' own numbers and segments looked different from lane to lane,
+// moving each product's operands there made the forward 8% and the backward 10%
+// slower.)
+template <typename Line>
+__device__ __forceinline__ bool next_uniform(Walk<Line> &walk, Segment &g)
+{
+    if (!uniform(walk.next(g))) return false;
+    g.begin = uniform(g.begin);
+    g.end = uniform(g.end);
+    g.total = uniform(g.total);
+    g.length = uniform(g.length);
+    g.tile = uniform(g.tile);
+    return true;
+}
+
 // Partial results of a block: slot 2 c for a tile cut at its start by the block's
 // share, 2 c + 1 for one cut at its end alone.
 __device__ __forceinline__ int partial_slot(const Segment &g, int block) { return 2 * block + (g.begin > 0 ? 0 : 1); }

@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
     const uint32_t tail = at_bars + S::kBarriers * 8;
     uint32_t *s_words = (uint32_t *)(s_raw + (tail - raw));
     float *s_sum = (float *)(s_words + 4);   // [part][row]
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = (int)uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     const WaitGuard guard = {s_words + 1, a.status};
     if (threadIdx.x == 0) {
         s_words[1] = 0;
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
             };
             auto release = [&](uint32_t x) { product_commit(leader, bar.ring_free + 8 * (x % S::kStages)); };
             uint32_t n = 0, seg = 0, step = 0;
-            while (walk.next(g)) {
+            while (next_uniform(walk, g)) {
                 if (g.length == 0) continue;
                 barrier_wait_warp(bar.own, seg & 1, guard);
                 const uint32_t s_q = s_own, s_do = s_own + S::kTileBytes;
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
         const float2 c2 = make_float2(c, c), f2 = make_float2(f_dp, f_dp);
         uint32_t n = 0, seg = 0, step = 0;
         // The next segment's place and statistics are fetched while one is finished.
-        bool there = walk.next(g);
+        bool there = next_uniform(walk, g);
         float lse = 0.0f, delta = 0.0f;
         auto statistics = [&](const Segment &t) {
             const int head = t.tile / a.q_tiles;
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                     if (lane == 0) barrier_arrive(bar.ready);
                 }
             }
-            there = walk.next(g);
+            there = next_uniform(walk, g);
             fetch();
             if (t.length > 0) {
                 barrier_wait_warp(bar.done, seg++ & 1, guard);
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
     const Bars<HD> bar(at_bars);
     const uint32_t tail = at_bars + S::kBarriers * 8;
     uint32_t *s_words = (uint32_t *)(s_raw + (tail - raw));
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = (int)uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     const WaitGuard guard = {s_words + 1, a.status};
     if (threadIdx.x == 0) {
         s_words[1] = 0;
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
             };
             auto release = [&](uint32_t x) { product_commit(leader, bar.ring_free + 8 * (x % S::kStages)); };
             uint32_t n = 0, seg = 0, step = 0;
-            while (walk.next(g)) {
+            while (next_uniform(walk, g)) {
                 if (g.tile * kKeyTile >= g.length) continue;
                 barrier_wait_warp(bar.own, seg & 1, guard);
                 auto scores = [&](uint32_t x) {
@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
         const float f_dp = shift.ds / shift.p, f_k = a.scale / shift.ds, f_v = 1.0f / shift.p;
         const float2 c2 = make_float2(c, c), f2 = make_float2(f_dp, f_dp);
         uint32_t n = 0, seg = 0, step = 0;
-        while (walk.next(g)) {
+        while (next_uniform(walk, g)) {
             const int row = g.tile * kKeyTile + row_in_tile;        // key (packed)
             const bool any = g.tile * kKeyTile < g.length, live = row < g.length;
             if (any) {
@@ -639,7 +639,6 @@ done:
 // ---- sums of cut tiles' parts -----------------------------------------------------------
 
 constexpr int kSumBlock = 256;
-constexpr int kSumItems = 4;    // items of 8 elements a thread takes, whose loads are in flight together
 
 // Adds up the parts of 8 elements at `at` of every slot; parts first - 1 .. last.
 template <typename T>
@@ -665,14 +664,11 @@ __global__ void __launch_bounds__(kSumBlock) k_attention_sum_q(const __grid_cons
     int last;
     if (!cut_tile<QueryLine>(a.work, grid, first, g, last)) return;
     const int head = g.tile / a.q_tiles, row0 = (g.tile - head * a.q_tiles) * kRowTile;
-#pragma unroll
-    for (int k = 0; k < kSumItems; ++k) {
-        const int i = (blockIdx.y * kSumItems + k) * kSumBlock + threadIdx.x, r = i / chunks, c = (i - r * chunks) * 8;
-        const int64_t row = row0 + r;
-        if (r >= kRowTile || row >= a.q_len) continue;
-        sum_parts(a.partial + (int64_t)r * a.dim + c, (int64_t)kRowTile * a.dim, first, last,
-                  (T *)a.dq + g.item * a.dq_item + row * a.dq_token + head * a.dq_head + c);
-    }
+    const int i = blockIdx.y * kSumBlock + threadIdx.x, r = i / chunks, c = (i - r * chunks) * 8;
+    const int64_t row = row0 + r;
+    if (r >= kRowTile || row >= a.q_len) return;
+    sum_parts(a.partial + (int64_t)r * a.dim + c, (int64_t)kRowTile * a.dim, first, last,
+              (T *)a.dq + g.item * a.dq_item + row * a.dq_token + head * a.dq_head + c);
 }
 
 template <typename T>
@@ -683,17 +679,14 @@ __global__ void __launch_bounds__(kSumBlock) k_attention_sum_kv(const __grid_con
     const int first = blockIdx.x + 1, chunks = a.dim / 8;
     int last;
     if (!cut_tile<KeyLine>(a.work, grid, first, g, last)) return;
-#pragma unroll
-    for (int k = 0; k < kSumItems; ++k) {
-        const int i = (blockIdx.y * kSumItems + k) * kSumBlock + threadIdx.x;
-        const int r2 = i / chunks, c = (i - r2 * chunks) * 8, r = r2 >> 1, which = r2 & 1;   // dk, dv
-        const int row = g.tile * kKeyTile + r;
-        if (r >= kKeyTile || row >= (a.index ? g.length : a.kv_len)) continue;
-        const int64_t key = a.index ? a.index[(int64_t)g.item * a.kv_len + row] : row;
-        T *out = which ? (T *)a.dv + g.item * a.dv_item + key * a.dv_token + g.head * a.dv_head
-                       : (T *)a.dk + g.item * a.dk_item + key * a.dk_token + g.head * a.dk_head;
-        sum_parts(a.partial + ((int64_t)r * 2 + which) * a.dim + c, (int64_t)kRowTile * 2 * a.dim, first, last, out + c);
-    }
+    const int i = blockIdx.y * kSumBlock + threadIdx.x;
+    const int r2 = i / chunks, c = (i - r2 * chunks) * 8, r = r2 >> 1, which = r2 & 1;   // dk, dv
+    const int row = g.tile * kKeyTile + r;
+    if (r >= kKeyTile || row >= (a.index ? g.length : a.kv_len)) return;
+    const int64_t key = a.index ? a.index[(int64_t)g.item * a.kv_len + row] : row;
+    T *out = which ? (T *)a.dv + g.item * a.dv_item + key * a.dv_token + g.head * a.dv_head
+                   : (T *)a.dk + g.item * a.dk_item + key * a.dk_token + g.head * a.dk_head;
+    sum_parts(a.partial + ((int64_t)r * 2 + which) * a.dim + c, (int64_t)kRowTile * 2 * a.dim, first, last, out + c);
 }
 
 // ---- statistics of the rows ----------------------------------------------------------------
@@ -836,8 +829,8 @@ template <typename T, int HD>
 int launch_backward(gsr_ctx *ctx, BackwardArgs &a, const Schedule &by_query, const Schedule &by_key, int blocks_q,
                     int blocks_k, cudaStream_t stream)
 {
-    // Blocks of a cut tile's sum: its rows' vectors over a block's items.
-    const int vectors = kRowTile * a.dim / 8, each = kSumBlock * kSumItems;
+    // Blocks of a cut tile's sum: its rows' vectors.
+    const int vectors = kRowTile * a.dim / 8, each = kSumBlock;
     // Queries first: they leave delta as the keys' kernel takes it.
     a.work = by_query;
     if (int rc = launch_big(ctx, k_attention_grad_q<T, HD>, "k_attention_grad_q", blocks_q, BackwardShape<HD>::kSmemQ, a,

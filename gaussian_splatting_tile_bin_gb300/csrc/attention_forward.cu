@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
     const uint32_t b_q = bars, b_q_free = bars + 8, b_kv = bars + 16, b_kv_free = b_kv + 8 * S::kStages;
     const uint32_t b_s = b_kv_free + 8 * S::kStages, b_p = b_s + 16, b_o = b_p + 16, tail = b_o + 16;
     uint32_t *s_words = (uint32_t *)(s_raw + (tail - raw));   // tensor memory base, abort flag
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = (int)uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     const WaitGuard guard = {s_words + 1, a.status};
 
     if (threadIdx.x == 0) {
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
                 product_rows<HD>(leader, tmem + t * kKeyTile, s_q + t * S::kTileBytes, stage_at(n), form, steps);
                 product_commit(leader, b_s + 8 * t);
             };
-            while (walk.next(g)) {
+            while (next_uniform(walk, g)) {
                 if (g.length == 0) continue;
                 const int head = g.tile / row_tiles, row0 = (g.tile - head * row_tiles) * 2 * kRowTile;
                 const int tiles = a.q_len - row0 > kRowTile ? 2 : 1;
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
         const float c = a.scale_log2;
         const uint32_t at_s = tmem + lanes + t * kKeyTile;
         uint32_t kv = 0, n = 0;   // ring position; key tiles this row tile has seen
-        while (walk.next(g)) {
+        while (next_uniform(walk, g)) {
             const int head = g.tile / row_tiles, row0 = (g.tile - head * row_tiles) * 2 * kRowTile + t * kRowTile;
             const int row = row0 + row_in_tile;
             const bool whole = g.whole();
@@ -350,9 +350,9 @@ done:
 
 // Joins the parts of a cut tile: weights exp(lse_part - lse).  Block x handles the
 // tile that the start of share x + 1 cuts, if that is the first share to start
-// inside it; a thread takes 8 elements of kJoinItems rows.
+// inside it; a thread takes 8 elements of a row (of four rows: 4 us
+// longer, each a chain of loads).
 constexpr int kJoinBlock = 256;
-constexpr int kJoinItems = 4;
 
 template <typename T>
 __global__ void __launch_bounds__(kJoinBlock) k_attention_join(const __grid_constant__ ForwardArgs a, int grid)
@@ -365,40 +365,37 @@ __global__ void __launch_bounds__(kJoinBlock) k_attention_join(const __grid_cons
     const int head = g.tile / a.row_tiles, row0 = (g.tile - head * a.row_tiles) * 2 * kRowTile;
     constexpr int kRows = 2 * kRowTile;
     const int slot0 = 2 * first - 1;   // then 2 b of the blocks b = first .. last
-#pragma unroll
-    for (int k = 0; k < kJoinItems; ++k) {
-        const int i = (blockIdx.y * kJoinItems + k) * kJoinBlock + threadIdx.x, r = i / chunks, c = (i - r * chunks) * 8;
-        const int row = row0 + r;
-        if (r >= kRows || row >= a.q_len) continue;
-        const float lse0 = a.partial_lse[(int64_t)slot0 * kRows + r];
-        float top = lse0;
-        for (int b = first; b <= last; ++b) top = fmaxf(top, a.partial_lse[(int64_t)2 * b * kRows + r]);
-        const float shift = top == -INFINITY ? 0.0f : top;
-        float total = 0.0f, o[8] = {};
-        auto add = [&](int64_t slot, float lse) {
-            const float w = expf(lse - shift);
-            total += w;
-            const float4 *p = (const float4 *)(a.partial + (slot * kRows + r) * a.dim + c);
-            const float4 f = p[0], h = p[1];
-            if (w != 0.0f) {
-                o[0] = fmaf(w, f.x, o[0]);
-                o[1] = fmaf(w, f.y, o[1]);
-                o[2] = fmaf(w, f.z, o[2]);
-                o[3] = fmaf(w, f.w, o[3]);
-                o[4] = fmaf(w, h.x, o[4]);
-                o[5] = fmaf(w, h.y, o[5]);
-                o[6] = fmaf(w, h.z, o[6]);
-                o[7] = fmaf(w, h.w, o[7]);
-            }
-        };
-        add(slot0, lse0);
-        for (int b = first; b <= last; ++b) add(2 * b, a.partial_lse[(int64_t)2 * b * kRows + r]);
-        const float inv = total > 0.0f ? 1.0f / total : (total == 0.0f ? 0.0f : total);
-        T *out = (T *)a.out + g.item * a.out_item + (int64_t)row * a.out_token + head * a.out_head + c;
-        *(uint4 *)out = make_uint4(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv),
-                                   pack2<T>(o[4] * inv, o[5] * inv), pack2<T>(o[6] * inv, o[7] * inv));
-        if (c == 0) a.lse[((int64_t)g.item * a.q_heads + head) * a.q_len + row] = top + logf(total);
-    }
+    const int i = blockIdx.y * kJoinBlock + threadIdx.x, r = i / chunks, c = (i - r * chunks) * 8;
+    const int row = row0 + r;
+    if (r >= kRows || row >= a.q_len) return;
+    const float lse0 = a.partial_lse[(int64_t)slot0 * kRows + r];
+    float top = lse0;
+    for (int b = first; b <= last; ++b) top = fmaxf(top, a.partial_lse[(int64_t)2 * b * kRows + r]);
+    const float shift = top == -INFINITY ? 0.0f : top;
+    float total = 0.0f, o[8] = {};
+    auto add = [&](int64_t slot, float lse) {
+        const float w = expf(lse - shift);
+        total += w;
+        const float4 *p = (const float4 *)(a.partial + (slot * kRows + r) * a.dim + c);
+        const float4 f = p[0], h = p[1];
+        if (w != 0.0f) {
+            o[0] = fmaf(w, f.x, o[0]);
+            o[1] = fmaf(w, f.y, o[1]);
+            o[2] = fmaf(w, f.z, o[2]);
+            o[3] = fmaf(w, f.w, o[3]);
+            o[4] = fmaf(w, h.x, o[4]);
+            o[5] = fmaf(w, h.y, o[5]);
+            o[6] = fmaf(w, h.z, o[6]);
+            o[7] = fmaf(w, h.w, o[7]);
+        }
+    };
+    add(slot0, lse0);
+    for (int b = first; b <= last; ++b) add(2 * b, a.partial_lse[(int64_t)2 * b * kRows + r]);
+    const float inv = total > 0.0f ? 1.0f / total : (total == 0.0f ? 0.0f : total);
+    T *out = (T *)a.out + g.item * a.out_item + (int64_t)row * a.out_token + head * a.out_head + c;
+    *(uint4 *)out = make_uint4(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv),
+                               pack2<T>(o[4] * inv, o[5] * inv), pack2<T>(o[6] * inv, o[7] * inv));
+    if (c == 0) a.lse[((int64_t)g.item * a.q_heads + head) * a.q_len + row] = top + logf(total);
 }
 
 // Rows of an item without keys.
@@ -429,7 +426,7 @@ int launch_forward(gsr_ctx *ctx, ForwardArgs &a, int blocks, cudaStream_t stream
                             "k_attention_forward"))
         return rc;
     if (blocks == 1 || a.work.length <= kKeyTile) return GSR_OK;   // tiles of one step are never cut
-    const int vectors = 2 * kRowTile * a.dim / 8, each = kJoinBlock * kJoinItems;
+    const int vectors = 2 * kRowTile * a.dim / 8, each = kJoinBlock;
     return cuda_check(ctx, launch_kernel(ctx, k_attention_join<T>,
                                          dim3((unsigned)blocks - 1, (unsigned)((vectors + each - 1) / each)), kJoinBlock,
                                          stream, a, blocks),

@@ -259,6 +259,14 @@ template <int HD>
 __device__ __forceinline__ void product_rows(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t form, int steps)
 {
     const uint32_t a0 = operand_rows(a), b0 = operand_rows(b);
+    if (steps == HD / 16) {
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k) {
+            const uint32_t at = ((k >> 2) * kBlockBytes + (k & 3) * 32) >> 4;
+            product_ss(leader, d, a0 + at, b0 + at, form, k != 0);
+        }
+        return;
+    }
 #pragma unroll
     for (int k = 0; k < HD / 16; ++k) {
         const uint32_t at = ((k >> 2) * kBlockBytes + (k & 3) * 32) >> 4;
