@@ -287,16 +287,18 @@ done:
     }
 }
 
-// Joins the splits of a row, one warp a row, four dimensions a lane.
-constexpr int kFewJoinBlock = 128;
+// Joins the splits of a row, one block a row: a warp takes every fourth split, four
+// dimensions a lane, and the warps' sums meet in shared memory in their order.
+constexpr int kFewJoinWarps = 4;
 
 template <typename T>
-__global__ void __launch_bounds__(kFewJoinBlock) k_attention_few_join(const __grid_constant__ FewArgs a, int64_t rows)
+__global__ void __launch_bounds__(kFewJoinWarps * 32) k_attention_few_join(const __grid_constant__ FewArgs a)
 {
     grid_dependency_begin();
-    const int lane = threadIdx.x % 32;
-    const int64_t r = (int64_t)blockIdx.x * (kFewJoinBlock / 32) + threadIdx.x / 32;
-    if (r >= rows) return;
+    __shared__ float4 s_o[kFewJoinWarps][32];
+    __shared__ float s_total[kFewJoinWarps];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int64_t r = blockIdx.x;
     const int per_unit = a.q_len * a.group, row = (int)(r % per_unit);
     const int64_t unit = r / per_unit, item = unit / a.kv_heads;
     const int token = row / a.group, head = (int)(unit % a.kv_heads) * a.group + row % a.group;
@@ -308,8 +310,8 @@ __global__ void __launch_bounds__(kFewJoinBlock) k_attention_few_join(const __gr
     float total = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const bool mine = lane * 4 < a.dim;
-#pragma unroll 8
-    for (int s = 0; s < a.splits; ++s) {
+#pragma unroll 4
+    for (int s = warp; s < a.splits; s += kFewJoinWarps) {
         const float w = expf(a.partial_lse[part0 + s * 16] - shift);
         total += w;
         if (mine) {
@@ -319,6 +321,15 @@ __global__ void __launch_bounds__(kFewJoinBlock) k_attention_few_join(const __gr
             o.z = fmaf(w, f.z, o.z);
             o.w = fmaf(w, f.w, o.w);
         }
+    }
+    s_o[warp][lane] = o;
+    if (lane == 0) s_total[warp] = total;
+    __syncthreads();
+    if (warp > 0) return;
+    for (int w = 1; w < kFewJoinWarps; ++w) {
+        const float4 f = s_o[w][lane];
+        o = make_float4(o.x + f.x, o.y + f.y, o.z + f.z, o.w + f.w);
+        total += s_total[w];
     }
     const float inv = total > 0.0f ? 1.0f / total : (total == 0.0f ? 0.0f : total);
     if (mine)
@@ -341,8 +352,7 @@ int launch_few(gsr_ctx *ctx, const FewArgs &a, int64_t units, cudaStream_t strea
         return rc;
     if (a.splits == 1) return GSR_OK;
     const int64_t rows = units * a.q_len * a.group;
-    return cuda_check(ctx, launch_kernel(ctx, k_attention_few_join<T>, dim3((unsigned)((rows + 3) / 4)), kFewJoinBlock,
-                                         stream, a, rows),
+    return cuda_check(ctx, launch_kernel(ctx, k_attention_few_join<T>, dim3((unsigned)rows), kFewJoinWarps * 32, stream, a),
                       "k_attention_few_join");
 }
 

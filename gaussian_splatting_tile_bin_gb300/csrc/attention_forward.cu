@@ -7,27 +7,29 @@
 // block holds two tiles of 128 query rows, each with its own 128 threads (one
 // row a thread) and its own score and output accumulators in tensor memory.  One
 // thread issues the products: scores S = Q K^T (operands in shared memory) and
-// outputs O += P V with P in tensor memory, where it replaces the scores it came
-// from.  While one tile's threads take the exponentials, the tensor cores work
-// for the other tile, so both pipes stay busy.  K and V tiles arrive by bulk
-// tensor copies through a ring of stages.
+// outputs O += P V with P in tensor memory.  While one tile's threads take the
+// exponentials, the tensor cores work for the other tile, so both pipes stay busy.
+// K and V tiles arrive by bulk tensor copies through a ring of stages.
 //
-// m is the maximum of the row's first keys.  It moves only when some keys' sum of
-// exp(s - m) exceeds 2^12, which tells that without a maximum of every tile (the
-// comparisons took a third of the softmax' time): the row then takes its true
-// maximum and the sum and the output so far are rescaled.  Until then P exceeds 1 by at
+// P has columns of its own at head_dim 64, so the next scores are computed as soon
+// as these are read; at 128, where the accumulators fill tensor memory, it
+// replaces the scores and the next ones come behind its product.
+//
+// m starts as the maximum of the row's first keys, in whole powers of 2.  It moves
+// only when 64 keys' sum of exp(s - m) exceeds 2^12, which tells that without a
+// maximum of every tile (the comparisons took a third of the softmax' time): the
+// row then takes its true maximum, and the sum, the output and the first half's P
+// are scaled by a power of 2, which rounds nothing.  Until then P exceeds 1 by at
 // most that factor, which 16-bit P and float sums hold without loss.  P is
 // rounded to the storage type (the tensor cores take 16-bit operands at the full
 // rate); l sums the unrounded values in float.
 //
-// Bound by the tensor cores at head_dim 128: 4,864 queries x 8,192 keys x 16 heads
-// in bf16 take 193 us, 1,690 TFLOP/s, 89% of a large library product's rate (the
-// pipe is active 64% of a quarter of that size, 4 heads in 57 us, where starts and
-// ends weigh more; issue slots 33%, exponentials 32%).  At head_dim 64, 168 us
-// (970 TFLOP/s): a product with 64 columns of output takes the time of one with
-// 128, and each tile's chain of scores, exponentials and output is no shorter.
-// There, four tiles with units of 64 keys took 192 us, two tiles with such units
-// 165 to 197, and turns that keep the two groups' exponentials apart 183.
+// Bound by the tensor cores: 4,864 queries x 8,192 keys x 16 heads in bf16 take
+// 182 us at head_dim 128, 1,790 TFLOP/s, 94% of a large library product's rate, and
+// 133 us at 64 (1,225 TFLOP/s; a product with 64 columns of output takes the time
+// of one with 128).  At 64, scores that waited for P's product took 154 us, four
+// tiles with units of 64 keys 192, two tiles with such units 165 to 197, and turns
+// that keep the two groups' exponentials apart 183.
 #include <math.h>
 
 #include "attention.cuh"
@@ -39,6 +41,13 @@ constexpr int kRowTile = 128;
 constexpr int kForwardThreads = 384;   // two row groups of 128; four warps of which one copies and one issues
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLargestSum = 4096.0f;
+
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t pair)
+{
+    const Vec<T, 2> v = *(const Vec<T, 2> *)&pair;
+    return make_float2(to_float(v.e[0]), to_float(v.e[1]));
+}
 
 struct ForwardArgs {
     CUtensorMap q, k, v;
@@ -60,9 +69,13 @@ struct ForwardShape {
     static constexpr int kBlocks = HD / 64;
     static constexpr int kTileBytes = kBlocks * kBlockBytes;
     static constexpr int kStages = HD == 128 ? 5 : 8;
-    static constexpr int kBarriers = 2 + 2 * kStages + 6;
+    static constexpr int kBarriers = 2 + 2 * kStages + 8;
     static constexpr int kSmem = 1024 + (2 + kStages) * kTileBytes + kBarriers * 8 + 16;
-    static constexpr int kOut = 256;   // tensor memory column of the outputs
+    // Tensor memory columns: two tiles' scores, outputs and P.  Where there is room
+    // for P beside the scores, the next scores are computed while P is.
+    static constexpr bool kApart = HD <= 64;
+    static constexpr int kOut = 256;
+    static constexpr int kP = kApart ? kOut + 2 * HD : 0, kPEach = kApart ? 64 : kKeyTile;
     static constexpr int kColumns = 512;
 };
 
@@ -76,7 +89,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
     const uint32_t base = (raw + 1023) & ~1023u;
     const uint32_t s_q = base, s_kv = base + 2 * S::kTileBytes, bars = s_kv + S::kStages * S::kTileBytes;
     const uint32_t b_q = bars, b_q_free = bars + 8, b_kv = bars + 16, b_kv_free = b_kv + 8 * S::kStages;
-    const uint32_t b_s = b_kv_free + 8 * S::kStages, b_p = b_s + 16, b_o = b_p + 16, tail = b_o + 16;
+    const uint32_t b_s = b_kv_free + 8 * S::kStages, b_p = b_s + 16, b_o = b_p + 16, b_read = b_o + 16, tail = b_read + 16;
     uint32_t *s_words = (uint32_t *)(s_raw + (tail - raw));   // tensor memory base, abort flag
     const int warp = (int)uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     const WaitGuard guard = {s_words + 1, a.status};
@@ -93,6 +106,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
             barrier_init(b_s + 8 * i, 1);
             barrier_init(b_p + 8 * i, 4);
             barrier_init(b_o + 8 * i, 1);
+            barrier_init(b_read + 8 * i, 4);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async();
@@ -147,11 +161,16 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
             const uint32_t form_s = product_form<T>(kKeyTile, false);
             const uint32_t form_o = product_form<T>((a.dim + 15) & ~15, true);
             const int steps = (a.dim + 15) / 16;
-            uint32_t kv = 0, seg = 0, p[2] = {0, 0};
+            uint32_t kv = 0, seg = 0, p[2] = {0, 0}, read[2] = {0, 0};
             auto stage_at = [&](uint32_t n) { return s_kv + n % S::kStages * S::kTileBytes; };
             auto await = [&](uint32_t n) { barrier_wait_warp(b_kv + 8 * (n % S::kStages), n / S::kStages & 1, guard); };
             auto release = [&](uint32_t n) { product_commit(leader, b_kv_free + 8 * (n % S::kStages)); };
             auto scores = [&](int t, uint32_t n, uint32_t form) {
+                if (S::kApart) {
+                    if (read[t] > 0) barrier_wait_warp(b_read + 8 * t, (read[t] - 1) & 1, guard);
+                    ++read[t];
+                    tmem_fence_after();
+                }
                 product_rows<HD>(leader, tmem + t * kKeyTile, s_q + t * S::kTileBytes, stage_at(n), form, steps);
                 product_commit(leader, b_s + 8 * t);
             };
@@ -164,21 +183,32 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
                 tmem_fence_after();
                 // The tile's last step takes the scores of its keys alone.
                 const uint32_t form_last = product_form<T>(round_keys(g.length - (g.total - 1) * kKeyTile), false);
-                for (int t = 0; t < tiles; ++t) scores(t, kv, g.begin + 1 < g.total ? form_s : form_last);
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    if (t < tiles) scores(t, kv, g.begin + 1 < g.total ? form_s : form_last);
                 release(kv);
                 // The next segment's Q arrives while this one's last keys are worked on.
                 if (g.begin + 1 == g.end) product_commit(leader, b_q_free);
                 for (int i = g.begin; i < g.end; ++i, kv += 2) {
                     const bool more = i + 1 < g.end;
                     const uint32_t form_next = i + 2 < g.total ? form_s : form_last;
-                    await(kv + 1);
-                    for (int t = 0; t < tiles; ++t) {
+                    if (!S::kApart) await(kv + 1);
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (t >= tiles) continue;
+                        if (S::kApart) {
+                            if (more) {
+                                if (t == 0) await(kv + 2);
+                                scores(t, kv + 2, form_next);
+                            }
+                            if (t == 0) await(kv + 1);
+                        }
                         barrier_wait_warp(b_p + 8 * t, p[t]++ & 1, guard);
                         tmem_fence_after();
-                        product_across(leader, tmem + S::kOut + t * HD, tmem + t * kKeyTile, stage_at(kv + 1), form_o,
-                                       i > g.begin);
+                        product_across(leader, tmem + S::kOut + t * HD, tmem + S::kP + t * S::kPEach, stage_at(kv + 1),
+                                       form_o, i > g.begin);
                         product_commit(leader, b_o + 8 * t);
-                        if (more) {
+                        if (!S::kApart && more) {
                             if (t == 0) await(kv + 2);
                             scores(t, kv + 2, form_next);
                         }
@@ -198,27 +228,24 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
         const uint32_t at_o = tmem + lanes + S::kOut + t * HD;
         const int row_in_tile = warp % 4 * 32 + lane;
         const float c = a.scale_log2;
-        const uint32_t at_s = tmem + lanes + t * kKeyTile;
+        const uint32_t at_s = tmem + lanes + t * kKeyTile, at_p = tmem + lanes + S::kP + t * S::kPEach;
         uint32_t kv = 0, n = 0;   // ring position; key tiles this row tile has seen
         while (next_uniform(walk, g)) {
             const int head = g.tile / row_tiles, row0 = (g.tile - head * row_tiles) * 2 * kRowTile + t * kRowTile;
             const int row = row0 + row_in_tile;
             const bool whole = g.whole();
-            float m = -INFINITY, l = 0.0f;
+            float m = -INFINITY, l = 0.0f;   // the reference, a whole number of powers of 2; the sum
             const bool active = row0 < a.q_len;
             if (g.length > 0 && active) {
                 for (int i = g.begin; i < g.end; ++i, ++n) {
                     barrier_wait_warp(b_s + 8 * t, n & 1, guard);
                     tmem_fence_after();
-                    // The second half of the scores arrives while the first is worked on.
                     uint32_t r[4][32];
                     tmem_load32(r[0], at_s);
                     tmem_load32(r[1], at_s + 32);
                     tmem_wait_load();
                     pin(r[0]);
                     pin(r[1]);
-                    tmem_load32(r[2], at_s + 64);
-                    tmem_load32(r[3], at_s + 96);
                     const int valid = g.length - i * kKeyTile;
                     const bool ragged = valid < kKeyTile;
                     if (ragged && t == 0) {
@@ -244,43 +271,45 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
                                 part[y % 4] = fmaxf(part[y % 4], __uint_as_float(r[2 * h + x][y]));
                         return fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
                     };
-                    // exp(s - m) of 64 keys into tensor memory, and their sum.
-                    auto exponentials = [&](int h) {
-                        const float shift = m == -INFINITY ? 0.0f : -m * c;
+                    // 2^(c s - m) of 64 keys, and their sum.
+                    uint32_t packed[2][32];
+                    auto exponentials = [&](int h, float shift) {
                         const float2 c2 = make_float2(c, c), shift2 = make_float2(shift, shift);
                         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            uint32_t packed[16];
-#pragma unroll
-                            for (int y = 0; y < 32; y += 2) {
-                                float2 e = fma2(make_float2(__uint_as_float(r[2 * h + x][y]),
-                                                            __uint_as_float(r[2 * h + x][y + 1])),
-                                                c2, shift2);
-                                e.x = exp2_fast(e.x);
-                                e.y = exp2_fast(e.y);
-                                sum[y / 2 & 1] = add2(sum[y / 2 & 1], e);
-                                packed[y / 2] = pack2<T>(e.x, e.y);
-                            }
-                            tmem_store16(at_s + h * 32 + x * 16, packed);
+                        for (int y = 0; y < 64; y += 2) {
+                            float2 e = fma2(make_float2(__uint_as_float(r[2 * h + y / 32][y % 32]),
+                                                        __uint_as_float(r[2 * h + y / 32][y % 32 + 1])),
+                                            c2, shift2);
+                            e.x = exp2_fast(e.x);
+                            e.y = exp2_fast(e.y);
+                            sum[y / 2 & 1] = add2(sum[y / 2 & 1], e);
+                            packed[h][y / 2] = pack2<T>(e.x, e.y);
                         }
                         return (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
                     };
-                    if (ragged) clear_ragged(0);
-                    if (i == g.begin) m = largest(0);
-                    float sum = exponentials(0);
-                    tmem_wait_load();
-                    pin(r[2]);
-                    pin(r[3]);
-                    if (ragged) clear_ragged(1);
-                    sum += exponentials(1);
-                    if (__any_sync(~0u, sum > kLargestSum)) {
-                        const float next = fmaxf(m, fmaxf(largest(0), largest(1)));
-                        const float keep = exp2_fast((m - (next == -INFINITY ? 0.0f : next)) * c);
+                    // The products of the keys before are complete.
+                    auto await_output = [&] {
+                        if (S::kApart && n > 0) {
+                            barrier_wait_warp(b_o + 8 * t, (n - 1) & 1, guard);
+                            tmem_fence_after();
+                        }
+                    };
+                    // The keys' true maximum becomes the reference, and what was summed before is scaled down.
+                    auto raise = [&](int h) {
+                        const float next = fmaxf(m, ceilf(largest(h) * c));
+                        const float down = next - m;   // whole; NaN when both are infinite
+                        const float keep = down > 126.0f ? 0.0f : down > 0.0f ? __int_as_float((127 - (int)down) << 23) : 1.0f;
                         m = next;
                         l *= keep;
-                        // The products of the keys before are complete: these scores came behind them.
-                        if (i > g.begin)
+                        if (h == 1)
+#pragma unroll
+                            for (int y = 0; y < 32; ++y) {
+                                const float2 e = unpack2<T>(packed[0][y]);
+                                packed[0][y] = pack2<T>(e.x * keep, e.y * keep);
+                            }
+                        if (i > g.begin) {
+                            await_output();
                             for (int x = 0; x < HD; x += 32) {
                                 uint32_t o[32];
                                 tmem_load32(o, at_o + x);
@@ -290,10 +319,38 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
                                 for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * keep);
                                 tmem_store32(at_o + x, o);
                             }
-                        sum = exponentials(0);
-                        sum += exponentials(1);
+                        }
+                        return exponentials(h, next == -INFINITY ? 0.0f : -next);
+                    };
+                    auto half = [&](int h) {
+                        float sum = exponentials(h, -m);
+                        if (__any_sync(~0u, !(sum <= kLargestSum))) {
+                            sum = raise(h);
+                            if (h == 1 && !S::kApart) tmem_store32(at_p, packed[0]);
+                        }
+                        l += sum;
+                        if (!S::kApart) tmem_store32(at_p + h * 32, packed[h]);
+                    };
+                    if (ragged) clear_ragged(0);
+                    if (i == g.begin) m = ceilf(largest(0) * c);
+                    half(0);
+                    tmem_load32(r[2], at_s + 64);   // any earlier takes more registers than there are
+                    tmem_load32(r[3], at_s + 96);
+                    tmem_wait_load();
+                    pin(r[2]);
+                    pin(r[3]);
+                    if (S::kApart) {
+                        tmem_fence_before();
+                        __syncwarp();
+                        if (lane == 0) barrier_arrive(b_read + 8 * t);
                     }
-                    l += sum;
+                    if (ragged) clear_ragged(1);
+                    half(1);
+                    if (S::kApart) {
+                        await_output();
+                        tmem_store32(at_p, packed[0]);
+                        tmem_store32(at_p + 32, packed[1]);
+                    }
                     tmem_wait_store();
                     tmem_fence_before();
                     __syncwarp();
@@ -306,7 +363,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
             if (!active) continue;
             const bool store = row < a.q_len;
             const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-            const float lse = m * (c * kLn2) + logf(l);
+            const float lse = m * kLn2 + logf(l);
             const int slot = partial_slot(g, blockIdx.x);
             T *out = (T *)a.out + g.item * a.out_item + (int64_t)row * a.out_token + head * a.out_head;
             float *partial = a.partial + ((int64_t)slot * 2 * kRowTile + t * kRowTile + row_in_tile) * a.dim;
