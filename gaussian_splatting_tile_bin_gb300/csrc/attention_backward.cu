@@ -22,15 +22,15 @@
 // and ds times a power of two that brings the largest |do| to about 1; both
 // powers are divided out of the float sums at the end.
 //
-// Bound by the tensor cores and by the wait for p: 4,864 queries x 8,192 keys x 16
-// heads in bf16 take 690 us for all three gradients at head_dim 128 (1,180 TFLOP/s
-// on the five products a gradient cannot do without, 1,650 on the seven done) and
-// 531 us at 64.  At 4 heads the tensor pipe is active 68% of both kernels, DRAM
-// reads are the inputs' own 27 MB.  A step of dk and dv (128 x 128) takes the
-// exponentials of two warps a scheduler about 990 cycles and ds 610; the products
-// wait 400 of their 2,350 for p.  Four warpgroups instead of two took 697 us, Q and
-// dO of the dq kernel in tensor memory 692, statistics read before the scores' wait
-// 700, dP of the next step ahead of this step's dq 794.
+// Bound by the tensor cores: 4,864 queries x 8,192 keys x 16 heads in bf16 take
+// 640 us for all three gradients at head_dim 128 (1,275 TFLOP/s on the five
+// products a gradient cannot do without, 1,785 on the seven done, 94% of a large
+// library product's rate) and 475 us at 64 (860 and 1,200; a product with 64
+// columns takes the time of one with 128).  At 4 heads the tensor pipe is active
+// 77 and 73% of the two kernels, starts and ends included; DRAM reads are the
+// inputs' own 27 MB.  Four warpgroups instead of two take 651 and 477 us; Q and dO
+// of the dq kernel in tensor memory, statistics read before the scores' wait and
+// dP of the next step ahead of this step's dq were no faster either.
 #include <math.h>
 
 #include "attention.cuh"
