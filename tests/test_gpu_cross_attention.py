@@ -283,3 +283,35 @@ def test_many_items_of_many_lengths(gsr, ctx, d):
     q, k, v, dout = _inputs(b, lq, lk, 2, 1, d, F16, 71)
     lengths = torch.tensor([(37 * i) % 301 if i % 5 else 0 for i in range(b)], dtype=torch.int32)
     _compare(gsr, ctx, q, k, v, dout, lengths=lengths)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_that_jump_inside_a_tile(gsr, ctx, dtype, d):
+    """The largest scores in the second half of a tile, in one key, in a tail, and lower ones behind them."""
+    q, k, v, dout = _inputs(2, 300, 700, 2, 1, d, dtype, 5 + d)
+    q[..., 0] = 4.0
+    level = torch.zeros(700)
+    level[64:128], level[192:256], level[300], level[390:450], level[690:] = 10.0, 20.0, 25.0, -15.0, 33.0
+    level = torch.stack([level, level.flip(0)])
+    k = (0.2 * k).to(dtype)
+    k[:, :, 0, 0] = level.to(dtype)
+    _compare(gsr, ctx, q, k, v, dout, scale=1.0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("lq", [4, 300])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_of_minus_infinity(gsr, ctx, dtype, lq, d):
+    """Valid keys whose scores are -inf weigh nothing, the first ones and whole tiles among them."""
+    q, k, v, dout = _inputs(2, lq, 400, 2, 1, d, dtype, 6 + d)
+    q[..., 0] = 1.0
+    none = torch.zeros(2, 400, dtype=torch.bool)
+    none[0, :64] = none[0, 100:110] = none[0, 256:384] = True
+    none[1, :200] = none[1, 399] = True
+    k[none] = 0.0
+    want = ref.attention(q.double(), k.double(), v.double(), ~none, d ** -0.5, dtype)
+    k[..., 0] = torch.where(none[:, :, None], float("-inf"), k[..., 0])
+    out, lse = gsr.cross_attention_forward(ctx, q.cuda(), k.cuda(), v.cuda())
+    ref.check(lse, want["lse"], "lse")
+    ref.check(out, want["out"], "out")
