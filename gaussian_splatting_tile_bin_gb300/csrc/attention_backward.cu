@@ -18,9 +18,9 @@
 // buffers in turn (queries as rows).
 //
 // Rounding.  p and ds are rounded to the storage type, as the tensor cores take
-// operands of one type.  f16 has few exponents: p is held times 2^14 (p <= 1),
-// and ds times a power of two that brings the largest |do| to about 1; both
-// powers are divided out of the float sums at the end.
+// operands of one type.  f16 has few exponents: p is held times 2^14 (p <= 1), and
+// ds times a power of two that brings its bound, 2 |do| |v| of the longest rows,
+// to f16's largest values; both powers are divided out of the float sums at the end.
 //
 // Bound by the tensor cores: 4,864 queries x 8,192 keys x 16 heads in bf16 take
 // 640 us for all three gradients at head_dim 128 (1,275 TFLOP/s on the five
@@ -54,14 +54,15 @@ struct RangeShift {
 template <typename T>
 constexpr float kShiftP = std::is_same<T, __half>::value ? 16384.0f : 1.0f;
 
-// amax: bits of the largest |do|.
+// norms: bits of the largest squared length of do's rows and of v's.
 template <typename T>
-__device__ __forceinline__ RangeShift range_shift(const uint32_t *amax)
+__device__ __forceinline__ RangeShift range_shift(const uint32_t *norms)
 {
     RangeShift shift = {kShiftP<T>, 1.0f};
     if constexpr (std::is_same<T, __half>::value) {
-        const float top = __uint_as_float(*amax);
-        if (top > 0.0f && top < INFINITY) shift.ds = exp2f((float)-ilogbf(top));
+        // |dp| and |delta| are at most this, so |ds| shifted is below 2^15.
+        const float bound = sqrtf(__uint_as_float(norms[0])) * sqrtf(__uint_as_float(norms[1]));
+        if (bound > 0.0f && bound < INFINITY) shift.ds = exp2f((float)max(-60, min(60, 13 - ilogbf(bound))));
     }
     return shift;
 }
@@ -72,7 +73,7 @@ struct BackwardArgs {
     const float *lse2;           // [batch, q_heads, q_pad]: log2(shift.p) - lse log2e
     const float *row_delta;      // the same: -do . o
     float *delta;                // the same: -delta shift.ds / shift.p, left by the dq kernel
-    const uint32_t *amax;
+    const uint32_t *norms;
     void *dq, *dk, *dv;
     int64_t dq_item, dq_token, dq_head, dk_item, dk_token, dk_head, dv_item, dv_token, dv_head;
     const int32_t *index;        // original keys of packed ones, [batch, kv_len], or NULL
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
         const uint32_t at_s = tmem + lanes + S::kS + column0, at_dp = tmem + lanes + S::kDp + column0;
         const int row_in_tile = warp % 4 * 32 + lane;
         const float c = a.scale_log2;
-        const RangeShift shift = range_shift<T>(a.amax);
+        const RangeShift shift = range_shift<T>(a.norms);
         const float f_dp = shift.ds / shift.p, f_out = a.scale / shift.ds;
         const float2 c2 = make_float2(c, c), f2 = make_float2(f_dp, f_dp);
         uint32_t n = 0, seg = 0, step = 0;
@@ -530,7 +531,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
         const uint32_t at_s = tmem + lanes + S::kS + column0, at_dp = tmem + lanes + S::kDp + column0;
         const int row_in_tile = warp % 4 * 32 + lane;
         const float c = a.scale_log2;
-        const RangeShift shift = range_shift<T>(a.amax);
+        const RangeShift shift = range_shift<T>(a.norms);
         const float f_dp = shift.ds / shift.p, f_k = a.scale / shift.ds, f_v = 1.0f / shift.p;
         const float2 c2 = make_float2(c, c), f2 = make_float2(f_dp, f_dp);
         uint32_t n = 0, seg = 0, step = 0;
@@ -692,12 +693,14 @@ __global__ void __launch_bounds__(kSumBlock) k_attention_sum_kv(const __grid_con
 // ---- statistics of the rows ----------------------------------------------------------------
 
 struct RowArgs {
-    gsr_heads out, dout;
+    gsr_heads out, dout, v;
     const float *lse;
     float *lse2, *delta;
-    uint32_t *amax;          // bits of the largest |do| (f16)
-    int64_t rows;            // batch x q_pad x q_heads
-    int q_len, q_pad, q_heads, dim;
+    uint32_t *norms;         // bits of the largest squared length of a row of dout and of v (f16)
+    const int32_t *lengths;
+    int64_t rows, v_rows;    // batch x q_pad x q_heads; batch x kv_len x kv_heads
+    int64_t row_blocks;      // blocks that take the queries' rows; those behind take v's
+    int q_len, q_pad, q_heads, kv_len, kv_heads, dim;
 };
 
 // Lanes of a row, 8 elements each, and a row's place: rows run over heads, then
@@ -707,23 +710,21 @@ struct RowPlace {
     int64_t row;
     uint32_t item, token, head;
     int c;
-    bool live;               // elements of a query (not of the padding)
-    __device__ RowPlace(const RowArgs &a, int64_t block)
+    __device__ RowPlace(int64_t block, int64_t rows, int tokens, int heads)
     {
         row = block * (256 / LANES) + threadIdx.x / LANES;
         c = threadIdx.x % LANES * 8;
-        if (a.rows >> 32) {   // many items of few queries, padded
-            const int64_t t = row / a.q_heads;
-            head = (uint32_t)(row - t * a.q_heads);
-            item = (uint32_t)(t / a.q_pad);
-            token = (uint32_t)(t - (int64_t)item * a.q_pad);
+        if (rows >> 32) {   // many items of few queries, padded
+            const int64_t t = row / heads;
+            head = (uint32_t)(row - t * heads);
+            item = (uint32_t)(t / tokens);
+            token = (uint32_t)(t - (int64_t)item * tokens);
         } else {
-            const uint32_t r = (uint32_t)row, t = r / a.q_heads;
-            head = r - t * a.q_heads;
-            item = t / a.q_pad;
-            token = t - item * a.q_pad;
+            const uint32_t r = (uint32_t)row, t = r / heads;
+            head = r - t * heads;
+            item = t / tokens;
+            token = t - item * tokens;
         }
-        live = row < a.rows && token < (uint32_t)a.q_len && c < a.dim;
     }
     template <typename T>
     __device__ Vec<T, 8> load(const gsr_heads &t) const
@@ -733,53 +734,78 @@ struct RowPlace {
     }
 };
 
-// -lse in base 2 with p's shift folded in, -delta, and the largest |do| for ds'
-// shift; rows behind q_len, and rows without keys, get p = 0.
+// The sum over a row's lanes.
+template <int LANES>
+__device__ __forceinline__ float row_sum(float x)
+{
+    for (int d = LANES / 2; d > 0; d /= 2) x += __shfl_xor_sync(~0u, x, d);
+    return x;
+}
+
+// -lse in base 2 with p's shift folded in, -delta, and the longest rows of dout and
+// of v's valid keys for ds' shift; rows behind q_len, and rows without keys, get p = 0.
 template <typename T, int LANES>
 __global__ void __launch_bounds__(256) k_attention_rows(const RowArgs a)
 {
     grid_dependency_begin();
-    const RowPlace<LANES> at(a, blockIdx.x);
-    float sum = 0.0f;
-    uint32_t top = 0;
-    if (at.live) {
-        const Vec<T, 8> o = at.template load<T>(a.out), d = at.template load<T>(a.dout);
+    constexpr bool kNorms = std::is_same<T, __half>::value;
+    const bool queries = blockIdx.x < a.row_blocks;
+    float length = 0.0f;
+    if (queries) {
+        const RowPlace<LANES> at(blockIdx.x, a.rows, a.q_pad, a.q_heads);
+        float sum = 0.0f;
+        if (at.row < a.rows && at.token < (uint32_t)a.q_len && at.c < a.dim) {
+            const Vec<T, 8> o = at.template load<T>(a.out), d = at.template load<T>(a.dout);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            sum = fmaf(to_float(o.e[e]), to_float(d.e[e]), sum);
-            top = max(top, __float_as_uint(fabsf(to_float(d.e[e]))));
+            for (int e = 0; e < 8; ++e) {
+                sum = fmaf(to_float(o.e[e]), to_float(d.e[e]), sum);
+                if (kNorms) length = fmaf(to_float(d.e[e]), to_float(d.e[e]), length);
+            }
+        }
+        sum = row_sum<LANES>(sum);
+        if (at.row < a.rows && at.c == 0) {
+            const int64_t row = (int64_t)at.item * a.q_heads + at.head, to = row * a.q_pad + at.token;
+            float lse = INFINITY;
+            if (at.token < (uint32_t)a.q_len) {
+                lse = a.lse[row * a.q_len + at.token];
+                lse = lse == -INFINITY ? INFINITY : lse * kLog2e - log2f(kShiftP<T>);
+            }
+            a.lse2[to] = -lse;
+            a.delta[to] = -sum;
+        }
+    } else {
+        const RowPlace<LANES> at(blockIdx.x - a.row_blocks, a.v_rows, a.kv_len, a.kv_heads);
+        if (at.row < a.v_rows && at.c < a.dim && (int)at.token < item_length(a.lengths, a.kv_len, (int)at.item)) {
+            const Vec<T, 8> v = at.template load<T>(a.v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) length = fmaf(to_float(v.e[e]), to_float(v.e[e]), length);
         }
     }
-    for (int d = LANES / 2; d > 0; d /= 2) sum += __shfl_xor_sync(~0u, sum, d);
-    if (at.row < a.rows && at.c == 0) {
-        const int64_t row = (int64_t)at.item * a.q_heads + at.head, to = row * a.q_pad + at.token;
-        float lse = INFINITY;
-        if (at.token < (uint32_t)a.q_len) {
-            lse = a.lse[row * a.q_len + at.token];
-            lse = lse == -INFINITY ? INFINITY : lse * kLog2e - log2f(kShiftP<T>);
-        }
-        a.lse2[to] = -lse;
-        a.delta[to] = -sum;
-    }
-    if constexpr (std::is_same<T, __half>::value) {
+    if constexpr (kNorms) {
         // The largest of all is the same in any order; what is there already needs no atomic.
         __shared__ uint32_t s_top[8];
-        top = __reduce_max_sync(~0u, top);
+        uint32_t top = __reduce_max_sync(~0u, __float_as_uint(row_sum<LANES>(length)));
         if (threadIdx.x % 32 == 0) s_top[threadIdx.x / 32] = top;
         __syncthreads();
         if (threadIdx.x == 0) {
             for (int w = 1; w < 8; ++w) top = max(top, s_top[w]);
-            if (top > *(volatile uint32_t *)a.amax) atomicMax(a.amax, top);
+            uint32_t *to = a.norms + (queries ? 0 : 1);
+            if (top > *(volatile uint32_t *)to) atomicMax(to, top);
         }
     }
 }
 
 template <typename T, int LANES>
-int row_statistics(gsr_ctx *ctx, const RowArgs &r, cudaStream_t stream)
+int row_statistics(gsr_ctx *ctx, RowArgs &r, cudaStream_t stream)
 {
-    const int64_t blocks = (r.rows + 256 / LANES - 1) / (256 / LANES);
-    if (std::is_same<T, __half>::value)
-        if (int rc = cuda_check(ctx, cudaMemsetAsync(r.amax, 0, sizeof(uint32_t), stream), "k_attention_rows")) return rc;
+    constexpr int kRows = 256 / LANES;
+    r.row_blocks = (r.rows + kRows - 1) / kRows;
+    int64_t blocks = r.row_blocks;
+    if (std::is_same<T, __half>::value) {
+        blocks += (r.v_rows + kRows - 1) / kRows;
+        if (int rc = cuda_check(ctx, cudaMemsetAsync(r.norms, 0, 2 * sizeof(uint32_t), stream), "k_attention_rows"))
+            return rc;
+    }
     return cuda_check(ctx, launch_kernel(ctx, k_attention_rows<T, LANES>, dim3((unsigned)blocks), 256, stream, r),
                       "k_attention_rows");
 }
@@ -897,26 +923,12 @@ int backward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr
     unsigned char *p = (unsigned char *)work + packed;
     float *lse2 = (float *)p, *row_delta = (float *)(p + stats);
     a.partial = (float *)(p + 3 * stats);
-    uint32_t *amax = (uint32_t *)(p + 3 * stats + partial);
+    uint32_t *norms = (uint32_t *)(p + 3 * stats + partial);
     a.lse2 = lse2;
     a.row_delta = row_delta;
     a.delta = (float *)(p + 2 * stats);
-    a.amax = amax;
+    a.norms = norms;
     a.status = ctx->status_dev;
-
-    RowArgs r = {};
-    r.out = out;
-    r.dout = dout;
-    r.lse = lse;
-    r.lse2 = lse2;
-    r.delta = row_delta;
-    r.amax = amax;
-    r.rows = rows;
-    r.q_len = d.q_len;
-    r.q_pad = a.q_pad;
-    r.q_heads = d.q_heads;
-    r.dim = d.head_dim;
-    if (int rc = d.head_dim <= 64 ? row_statistics<T, 8>(ctx, r, stream) : row_statistics<T, 16>(ctx, r, stream)) return rc;
 
     gsr_heads keys = k, values = v;
     if (d.key_mask) {
@@ -928,6 +940,25 @@ int backward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr
         a.index = pack.index;
         if (int rc = zero_rows(ctx, dk, dv, d, d.kv_len, d.kv_heads, true, stream)) return rc;
     }
+    RowArgs r = {};
+    r.out = out;
+    r.dout = dout;
+    r.v = values;
+    r.lengths = by_query.lengths;
+    r.lse = lse;
+    r.lse2 = lse2;
+    r.delta = row_delta;
+    r.norms = norms;
+    r.rows = rows;
+    r.q_len = d.q_len;
+    r.q_pad = a.q_pad;
+    r.q_heads = d.q_heads;
+    r.v_rows = (int64_t)d.batch * d.kv_len * d.kv_heads;
+    r.kv_len = d.kv_len;
+    r.kv_heads = d.kv_heads;
+    r.dim = d.head_dim;
+    if (int rc = d.head_dim <= 64 ? row_statistics<T, 8>(ctx, r, stream) : row_statistics<T, 16>(ctx, r, stream)) return rc;
+
     a.wide_q = rows_of_32_bytes(dq, d.head_dim);
     a.wide_kv = rows_of_32_bytes(dk, d.head_dim) && rows_of_32_bytes(dv, d.head_dim);
     a.q_item = q.batch_stride != 0;

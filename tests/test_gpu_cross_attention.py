@@ -315,3 +315,25 @@ def test_scores_of_minus_infinity(gsr, ctx, dtype, lq, d):
     out, lse = gsr.cross_attention_forward(ctx, q.cuda(), k.cuda(), v.cuda())
     ref.check(lse, want["lse"], "lse")
     ref.check(out, want["out"], "out")
+
+
+@pytest.mark.parametrize("lq,lk,d", [(1, 2066, 104), (3, 1321, 8), (5, 2286, 32)])
+def test_small_gradients_of_single_rows(gsr, ctx, lq, lk, d):
+    """f16 key gradients of a few queries, most of whose probabilities are far below 1."""
+    for seed in range(6):
+        q, k, v, dout = _inputs(2, lq, lk, 2, 2, d, F16, seed, size=4.0)
+        _compare(gsr, ctx, q, k, v, 1.9 * dout)
+
+
+def test_gradients_of_large_values(gsr, ctx):
+    """f16 values and output gradients whose products pass f16's range."""
+    q, k, v, dout = _inputs(1, 150, 300, 2, 1, 128, F16, 8)
+    v, dout = (9000.0 * v).clamp(-6e4, 6e4), 0.01 * dout
+    valid = torch.ones(1, 300, dtype=torch.bool)
+    for factor in (1.0, 1e-3):
+        want = ref.attention(q.double(), k.double(), v.double(), valid, 128 ** -0.5, F16, (factor * dout).double())
+        dev = [t.cuda() for t in (q, k, v)]
+        out, lse = gsr.cross_attention_forward(ctx, *dev)
+        grads = gsr.cross_attention_backward(ctx, *dev, out, lse, (factor * dout).cuda())
+        for name, got in zip(("dq", "dk", "dv"), grads):
+            ref.check(got, want[name], name)
