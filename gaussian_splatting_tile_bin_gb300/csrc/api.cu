@@ -125,6 +125,11 @@ void gsr_destroy(gsr_ctx *ctx)
         cudaFree(ctx->bwd_items);
         cudaFree(ctx->fwd_items);
         cudaFree(ctx->work);
+        while (gsr::Outgrown *kept = ctx->outgrown) {
+            ctx->outgrown = kept->next;
+            cudaFree(kept->buffer);
+            delete kept;
+        }
         if (ctx->status_host) cudaFreeHost(ctx->status_host);
         if (ctx->work_event) cudaEventDestroy(ctx->work_event);
         if (ctx->host_total) cudaFreeHost(ctx->host_total);

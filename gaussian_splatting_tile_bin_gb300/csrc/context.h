@@ -2,6 +2,16 @@
 // arena and the state the calls share.  Host code only; no kernel reads it.
 #pragma once
 
+namespace gsr {
+
+// A buffer that was outgrown but has to stay.
+struct Outgrown {
+    void *buffer;
+    Outgrown *next;
+};
+
+}  // namespace gsr
+
 struct gsr_ctx {
     int device = 0;
     std::string err;
@@ -76,6 +86,8 @@ struct gsr_ctx {
     // time, ordered between streams by an event.
     size_t cap_work = 0;
     unsigned char *work = nullptr;
+    bool work_captured = false;                 // a captured call was given it: graphs hold its address
+    gsr::Outgrown *outgrown = nullptr;          // smaller ones that graphs hold, kept until gsr_destroy
     cudaStream_t work_stream = nullptr;         // stream of the last call that used it
     cudaEvent_t work_event = nullptr;           // recorded after that call
     bool work_pending = false;                  // work_event holds a record

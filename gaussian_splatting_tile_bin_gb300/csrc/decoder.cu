@@ -1,5 +1,7 @@
 // decoder.cu -- the workspace of the decoder's operators: scratch memory that
 // one call at a time uses, grown like the rest of the context's arena.
+#include <new>
+
 #include "decoder.cuh"
 
 namespace gsr {
@@ -12,10 +14,18 @@ int workspace(gsr_ctx *ctx, size_t bytes, cudaStream_t stream, void **out)
     if (bytes > ctx->cap_work) {
         if (capture != cudaStreamCaptureStatusNone)
             return fail(ctx, GSR_ERR_CUDA, "the workspace must grow during a capture: make one such call before it");
-        // Queued work of an earlier call may still use the old buffer.
+        // Queued work of an earlier call may still use the old buffer, and the replays
+        // of a graph that captured a call will, as long as the graph lives.
         if (int rc = cuda_check(ctx, cudaDeviceSynchronize(), "workspace growth")) return rc;
-        cudaFree(ctx->work);
+        if (ctx->work_captured) {
+            Outgrown *kept = new (std::nothrow) Outgrown{ctx->work, ctx->outgrown};
+            if (!kept) return fail(ctx, GSR_ERR_OOM, "cannot keep the workspace that captured graphs hold");
+            ctx->outgrown = kept;
+        } else {
+            cudaFree(ctx->work);
+        }
         ctx->work = nullptr;
+        ctx->work_captured = false;
         ctx->cap_work = 0;
         const size_t grown = round_up(bytes, (size_t)1 << 20);
         void *p = nullptr;
@@ -41,6 +51,7 @@ int workspace(gsr_ctx *ctx, size_t bytes, cudaStream_t stream, void **out)
         ctx->status_host = (uint32_t *)host;
         ctx->status_dev = (uint32_t *)dev;
     }
+    if (capture != cudaStreamCaptureStatusNone && bytes > 0) ctx->work_captured = true;
     // A captured call is ordered by its graph; events of the live streams stay out of it.
     if (capture == cudaStreamCaptureStatusNone && ctx->work_pending && ctx->work_stream != stream)
         if (int rc = cuda_check(ctx, cudaStreamWaitEvent(stream, ctx->work_event, 0), "workspace order")) return rc;

@@ -396,8 +396,10 @@ int gsr_peak_kernel(gsr_ctx *ctx, int kind, int32_t iters, float *sink, uint64_t
  * several streams are ordered on that workspace by an event.  A call made while
  * its stream is being captured cannot grow the workspace (GSR_ERR_CUDA): make
  * one such call before the capture, and order a graph's replays with the
- * context's other calls.  Inputs and outputs must not overlap unless a call
- * says so. */
+ * context's other calls.  A graph holds the workspace it was captured with: when
+ * a later call outgrows that, the old one is kept until gsr_destroy, before which
+ * the graph's last replay has to be complete.  Inputs and outputs must not
+ * overlap unless a call says so. */
 
 /* Element types of the decoder's arrays. */
 enum { GSR_F32 = 0, GSR_BF16 = 1, GSR_F16 = 2 };

@@ -1,0 +1,110 @@
+"""The decoder operators' host code on the CPU, against a runtime that runs nothing
+(fake_runtime.cpp): which uses of the workspace streams, events and captures order,
+and what happens to memory that a captured graph holds."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+OK, INVALID_ARG, CUDA, OOM = 0, 1, 2, 3
+ONE, TWO, THREE = (ctypes.c_void_p(0x100 * i) for i in (1, 2, 3))
+AT = 1 << 30    # where the arrays would lie; nothing reads them
+
+
+@pytest.fixture(scope="module")
+def lib(tmp_path_factory):
+    import __graft_entry__
+    build = __graft_entry__._build_module()
+    build.build()
+    objects = [os.path.join(build.BUILD, os.path.basename(s) + ".o") for s in build.sources()]
+    if not all(os.path.exists(o) for o in objects):
+        build.build(force=True)
+    out = str(tmp_path_factory.mktemp("fake") / "libgsr_fake.so")
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    # -Bsymbolic: the fake runtime's functions, whatever else the process has loaded
+    subprocess.check_call(["g++", "-O1", "-shared", "-fPIC", "-Wl,-Bsymbolic", f"-I{cuda}/include", "-o", out,
+                           os.path.join(HERE, "fake_runtime.cpp"), *objects, "-ldl"])
+    fake = ctypes.CDLL(out)
+    for name in ("fake_new_stream", "fake_begin_capture", "fake_end_capture"):
+        getattr(fake, name).argtypes = [ctypes.c_void_p]
+    fake.fake_edge.argtypes = [ctypes.c_void_p] * 2
+    for name, pointers in (("group_norm_forward", 9), ("group_norm_backward", 12), ("rotary_forward", 7),
+                           ("cross_attention_forward", 8), ("cross_attention_backward", 12)):
+        getattr(fake, "gsr_" + name).argtypes = [ctypes.c_void_p] * pointers
+    fake.gsr_destroy.argtypes = [ctypes.c_void_p]
+    fake.gsr_last_error.argtypes = [ctypes.c_void_p]
+    fake.gsr_last_error.restype = ctypes.c_char_p
+    return fake
+
+
+@pytest.fixture
+def ctx(lib):
+    lib.fake_reset()
+    handle = ctypes.c_void_p()
+    assert lib.gsr_create(ctypes.byref(handle), 0) == OK
+    yield handle
+    lib.fake_reset()
+
+
+def _heads(tokens, heads, dim=64):
+    from gaussian_splatting_tile_bin_gb300 import _abi
+    return _abi.HEADS.pack(AT, tokens * heads * dim, heads * dim, dim)
+
+
+def attention(lib, ctx, stream, tokens=200, keys=700, mask=False, backward=False):
+    from gaussian_splatting_tile_bin_gb300 import _abi
+    desc = _abi.ATTENTION.pack(2, 2, tokens, keys, 4, 2, 64, 0.125, 0, AT if mask else 0)
+    q, k = _heads(tokens, 4), _heads(keys, 2)
+    if backward:
+        return lib.gsr_cross_attention_backward(ctx, desc, q, k, k, q, AT, q, q, k, k, stream)
+    return lib.gsr_cross_attention_forward(ctx, desc, q, k, k, q, AT, stream)
+
+
+def norm(lib, ctx, stream, channels=64, backward=False):
+    from gaussian_splatting_tile_bin_gb300 import _abi
+    desc = _abi.GROUP_NORM.pack(1, 2, channels, 8, 200000, 1, 1e-5)
+    if backward:
+        return lib.gsr_group_norm_backward(ctx, desc, AT, AT, AT, AT, AT, AT, AT, AT, AT, stream)
+    return lib.gsr_group_norm_forward(ctx, desc, AT, AT, AT, AT, AT, AT, stream)
+
+
+def test_eager_streams_are_ordered(lib, ctx):
+    for call in (attention, norm):
+        for stream in (ONE, TWO, ONE, THREE):
+            assert call(lib, ctx, stream) == OK
+            assert call(lib, ctx, stream, backward=True) == OK
+    assert lib.fake_conflicts() == 0 and lib.fake_launches() > 20
+
+
+@pytest.mark.parametrize("call", [attention, norm])
+def test_growth_keeps_what_a_graph_holds(lib, ctx, call):
+    assert call(lib, ctx, ONE) == OK
+    lib.fake_begin_capture(ONE)
+    assert call(lib, ctx, ONE) == OK
+    lib.fake_end_capture(ONE)
+    size = {attention: dict(tokens=3000, keys=9000, mask=True), norm: dict(channels=2048)}[call]
+    assert call(lib, ctx, ONE, **size) == OK
+    assert lib.fake_freed_while_held() == 0
+    # A second graph takes the grown workspace, and the next growth keeps both.
+    lib.fake_begin_capture(TWO)
+    assert call(lib, ctx, TWO, **size) == OK
+    lib.fake_end_capture(TWO)
+    assert attention(lib, ctx, ONE, tokens=6000, keys=40000, mask=True, backward=True) == OK
+    assert lib.fake_freed_while_held() == 0 and lib.fake_allocations() == 3
+    lib.gsr_destroy(ctx)
+    assert lib.fake_live() == 0
+
+
+def test_growth_frees_what_no_graph_holds(lib, ctx):
+    for keys in (500, 5000, 50000):
+        assert attention(lib, ctx, ONE, keys=keys, mask=True) == OK
+        assert lib.fake_allocations() == 1
+
+
+def test_growth_during_a_capture_is_refused(lib, ctx):
+    assert attention(lib, ctx, ONE) == OK
+    lib.fake_begin_capture(ONE)
+    assert attention(lib, ctx, ONE, keys=50000, mask=True) == CUDA
+    assert b"capture" in lib.gsr_last_error(ctx)

@@ -1,0 +1,67 @@
+"""The decoder operators' workspace under captured graphs and several streams."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def gsr():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import gaussian_splatting_tile_bin_gb300 as g
+    return g
+
+
+@pytest.fixture
+def ctx(gsr):
+    c = gsr.Context(0)
+    yield c
+    torch.cuda.synchronize()
+    c.close()
+
+
+def _step(gsr, ctx, lq, lk, seed, dtype=torch.float16):
+    """A masked attention step and a norm's, forward and backward, as a function of a stream."""
+    g = torch.Generator().manual_seed(seed)
+    q, dout = (torch.randn(2, lq, 4, 64, generator=g).to(dtype).cuda() for _ in range(2))
+    k, v = (torch.randn(2, lk, 2, 64, generator=g).to(dtype).cuda() for _ in range(2))
+    mask = (torch.rand(2, lk, generator=g) < 0.7).cuda()
+    x, dy = (torch.randn(2, 5 * lk, 96, generator=g).to(dtype).cuda() for _ in range(2))
+
+    def step(stream=None):
+        out, lse = gsr.cross_attention_forward(ctx, q, k, v, key_mask=mask, stream=stream)
+        grads = gsr.cross_attention_backward(ctx, q, k, v, out, lse, dout, key_mask=mask, stream=stream)
+        y, mean, rstd = gsr.group_norm_forward(ctx, x, 6, stream=stream)
+        norm_grads = gsr.group_norm_backward(ctx, dy, x, 6, None, None, mean, rstd, stream=stream)
+        one, lse1 = gsr.cross_attention_forward(ctx, q[:, :1], k, v, key_mask=mask, stream=stream)
+        return (out, lse, *grads, y, mean, rstd, *norm_grads, one, lse1)
+
+    return step
+
+
+def _same(got, want):
+    return all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_replay_after_the_workspace_has_grown(gsr, ctx):
+    step = _step(gsr, ctx, 200, 700, 1)
+    want = step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert _same(got, want)
+    larger = _step(gsr, ctx, 1500, 6000, 2)
+    first = larger()
+    # Memory that other tensors take meanwhile keeps what they hold.
+    others = [torch.full((1 << 20,), 7, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    for t in got:
+        t.zero_()
+    graph.replay()
+    second = larger()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert _same(got, want) and _same(second, first)
+    assert all((t == 7).all() for t in others)
