@@ -132,6 +132,11 @@ void gsr_destroy(gsr_ctx *ctx)
         }
         if (ctx->status_host) cudaFreeHost(ctx->status_host);
         if (ctx->work_event) cudaEventDestroy(ctx->work_event);
+        while (gsr::CaptureMark *mark = ctx->captures) {
+            ctx->captures = mark->next;
+            if (mark->event) cudaEventDestroy(mark->event);
+            delete mark;
+        }
         if (ctx->host_total) cudaFreeHost(ctx->host_total);
     }
     delete ctx;

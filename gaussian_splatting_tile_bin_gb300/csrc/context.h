@@ -10,6 +10,15 @@ struct Outgrown {
     Outgrown *next;
 };
 
+// The last call of a capture.  (Nothing tells when a capture has ended, and
+// captures may overlap, so each keeps its own.)
+struct CaptureMark {
+    unsigned long long id;
+    cudaStream_t stream;
+    cudaEvent_t event;      // recorded after the call, in the capture
+    CaptureMark *next;
+};
+
 }  // namespace gsr
 
 struct gsr_ctx {
@@ -83,7 +92,8 @@ struct gsr_ctx {
     uint64_t bin_calls = 0;                     // gsr_bin_splats calls made
 
     // Workspace of the decoder's operators (decoder.cu): scratch of one call at a
-    // time, ordered between streams by an event.
+    // time, ordered between streams by an event, and between the streams of one
+    // capture by another, which becomes an edge of the graph.
     size_t cap_work = 0;
     unsigned char *work = nullptr;
     bool work_captured = false;                 // a captured call was given it: graphs hold its address
@@ -91,6 +101,7 @@ struct gsr_ctx {
     cudaStream_t work_stream = nullptr;         // stream of the last call that used it
     cudaEvent_t work_event = nullptr;           // recorded after that call
     bool work_pending = false;                  // work_event holds a record
+    gsr::CaptureMark *captures = nullptr;       // captures that have used it, kept until gsr_destroy
     uint32_t *status_host = nullptr;            // pinned: set by a kernel whose bounded wait ran out
     uint32_t *status_dev = nullptr;             // its device address
 

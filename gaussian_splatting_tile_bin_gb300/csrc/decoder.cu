@@ -5,12 +5,23 @@
 #include "decoder.cuh"
 
 namespace gsr {
+namespace {
+
+CaptureMark *find_capture(const gsr_ctx *ctx, unsigned long long id)
+{
+    CaptureMark *mark = ctx->captures;
+    while (mark && mark->id != id) mark = mark->next;
+    return mark;
+}
+
+}  // namespace
 
 int workspace(gsr_ctx *ctx, size_t bytes, cudaStream_t stream, void **out)
 {
     *out = nullptr;
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-    if (int rc = cuda_check(ctx, cudaStreamIsCapturing(stream, &capture), "workspace stream")) return rc;
+    unsigned long long id = 0;
+    if (int rc = cuda_check(ctx, cudaStreamGetCaptureInfo(stream, &capture, &id), "workspace stream")) return rc;
     if (bytes > ctx->cap_work) {
         if (capture != cudaStreamCaptureStatusNone)
             return fail(ctx, GSR_ERR_CUDA, "the workspace must grow during a capture: make one such call before it");
@@ -51,10 +62,16 @@ int workspace(gsr_ctx *ctx, size_t bytes, cudaStream_t stream, void **out)
         ctx->status_host = (uint32_t *)host;
         ctx->status_dev = (uint32_t *)dev;
     }
-    if (capture != cudaStreamCaptureStatusNone && bytes > 0) ctx->work_captured = true;
-    // A captured call is ordered by its graph; events of the live streams stay out of it.
-    if (capture == cudaStreamCaptureStatusNone && ctx->work_pending && ctx->work_stream != stream)
+    // A captured call is ordered with the others of its capture; the events of live
+    // streams and of other captures stay out of it.
+    if (capture != cudaStreamCaptureStatusNone) {
+        if (bytes > 0) ctx->work_captured = true;
+        const CaptureMark *mark = find_capture(ctx, id);
+        if (mark && mark->stream != stream)
+            if (int rc = cuda_check(ctx, cudaStreamWaitEvent(stream, mark->event, 0), "workspace order")) return rc;
+    } else if (ctx->work_pending && ctx->work_stream != stream) {
         if (int rc = cuda_check(ctx, cudaStreamWaitEvent(stream, ctx->work_event, 0), "workspace order")) return rc;
+    }
     *out = ctx->work;
     return GSR_OK;
 }
@@ -62,15 +79,26 @@ int workspace(gsr_ctx *ctx, size_t bytes, cudaStream_t stream, void **out)
 int workspace_done(gsr_ctx *ctx, cudaStream_t stream)
 {
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-    if (int rc = cuda_check(ctx, cudaStreamIsCapturing(stream, &capture), "workspace stream")) return rc;
-    if (capture != cudaStreamCaptureStatusNone) return GSR_OK;
-    if (!ctx->work_event)
-        if (int rc = cuda_check(ctx, cudaEventCreateWithFlags(&ctx->work_event, cudaEventDisableTiming),
-                                "workspace event"))
+    unsigned long long id = 0;
+    if (int rc = cuda_check(ctx, cudaStreamGetCaptureInfo(stream, &capture, &id), "workspace stream")) return rc;
+    cudaStream_t *last = &ctx->work_stream;
+    cudaEvent_t *event = &ctx->work_event;
+    if (capture != cudaStreamCaptureStatusNone) {
+        CaptureMark *mark = find_capture(ctx, id);
+        if (!mark) {
+            mark = new (std::nothrow) CaptureMark{id, nullptr, nullptr, ctx->captures};
+            if (!mark) return fail(ctx, GSR_ERR_OOM, "cannot note the capture's use of the workspace");
+            ctx->captures = mark;
+        }
+        last = &mark->stream;
+        event = &mark->event;
+    }
+    if (!*event)
+        if (int rc = cuda_check(ctx, cudaEventCreateWithFlags(event, cudaEventDisableTiming), "workspace event"))
             return rc;
-    if (int rc = cuda_check(ctx, cudaEventRecord(ctx->work_event, stream), "workspace event")) return rc;
-    ctx->work_stream = stream;
-    ctx->work_pending = true;
+    if (int rc = cuda_check(ctx, cudaEventRecord(*event, stream), "workspace event")) return rc;
+    *last = stream;
+    if (capture == cudaStreamCaptureStatusNone) ctx->work_pending = true;
     return GSR_OK;
 }
 

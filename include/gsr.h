@@ -393,7 +393,8 @@ int gsr_peak_kernel(gsr_ctx *ctx, int kind, int32_t iters, float *sink, uint64_t
  * below follow the conventions at the top of this file; a call that needs
  * scratch memory takes it from a workspace of the context's arena, which grows
  * (synchronising the device) and never shrinks.  Calls on one context from
- * several streams are ordered on that workspace by an event.  A call made while
+ * several streams are ordered on that workspace by an event, and so are those
+ * on several streams of one capture, as an edge of its graph.  A call made while
  * its stream is being captured cannot grow the workspace (GSR_ERR_CUDA): make
  * one such call before the capture, and order a graph's replays with the
  * context's other calls.  A graph holds the workspace it was captured with: when

@@ -9,7 +9,7 @@ import pytest
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 OK, INVALID_ARG, CUDA, OOM = 0, 1, 2, 3
-ONE, TWO, THREE = (ctypes.c_void_p(0x100 * i) for i in (1, 2, 3))
+ONE, TWO, THREE, FOUR = (ctypes.c_void_p(0x100 * i) for i in (1, 2, 3, 4))
 AT = 1 << 30    # where the arrays would lie; nothing reads them
 
 
@@ -108,3 +108,38 @@ def test_growth_during_a_capture_is_refused(lib, ctx):
     lib.fake_begin_capture(ONE)
     assert attention(lib, ctx, ONE, keys=50000, mask=True) == CUDA
     assert b"capture" in lib.gsr_last_error(ctx)
+
+
+@pytest.mark.parametrize("call", [attention, norm])
+def test_streams_of_one_capture_are_ordered(lib, ctx, call):
+    """Branches that the caller forks and joins share the workspace one after the other."""
+    for stream in (ONE, TWO):
+        assert call(lib, ctx, stream) == OK
+        assert call(lib, ctx, stream, backward=True) == OK
+    for _ in range(2):
+        lib.fake_begin_capture(ONE)
+        assert lib.fake_edge(ONE, TWO) == OK and lib.fake_edge(ONE, THREE) == OK
+        for stream in (ONE, TWO, THREE, ONE, TWO):
+            assert call(lib, ctx, stream) == OK
+        assert call(lib, ctx, THREE, backward=True) == OK
+        assert lib.fake_edge(TWO, ONE) == OK and lib.fake_edge(THREE, ONE) == OK
+        lib.fake_end_capture(ONE)
+        # Outside the capture the live streams go on as before it.
+        assert call(lib, ctx, TWO) == OK and call(lib, ctx, ONE) == OK
+    assert lib.fake_conflicts() == 0 and lib.fake_pulled_in() == 0
+
+
+def test_captures_side_by_side(lib, ctx):
+    """Captures that know nothing of each other, with live calls between theirs."""
+    for stream in (ONE, TWO, THREE, FOUR):
+        assert attention(lib, ctx, stream) == OK
+    lib.fake_begin_capture(ONE)
+    lib.fake_begin_capture(TWO)
+    assert lib.fake_edge(ONE, THREE) == OK
+    for stream in (ONE, FOUR, TWO, THREE, FOUR, TWO, ONE):
+        assert attention(lib, ctx, stream) == OK
+    assert lib.fake_edge(THREE, ONE) == OK
+    lib.fake_end_capture(ONE)
+    lib.fake_end_capture(TWO)
+    assert attention(lib, ctx, ONE) == OK
+    assert lib.fake_conflicts() == 0 and lib.fake_pulled_in() == 0

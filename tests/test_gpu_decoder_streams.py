@@ -65,3 +65,29 @@ def test_replay_after_the_workspace_has_grown(gsr, ctx):
     torch.cuda.synchronize()
     assert _same(got, want) and _same(second, first)
     assert all((t == 7).all() for t in others)
+
+
+def test_streams_of_one_capture(gsr, ctx):
+    """Steps on forked streams of one capture share the context's workspace."""
+    steps = [_step(gsr, ctx, 300 + 40 * i, 900 + 100 * i, 10 + i) for i in range(3)]
+    want = [step() for step in steps]
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in steps[1:]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        for side in sides:
+            side.wait_stream(main)
+        got = [steps[0]()]
+        for step, side in zip(steps[1:], sides):
+            with torch.cuda.stream(side):
+                got.append(step())
+        again = steps[0]()
+        for side in sides:
+            main.wait_stream(side)
+    for _ in range(3):
+        for t in [t for one in got for t in one] + list(again):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(_same(a, b) for a, b in zip(got, want)) and _same(again, want[0])
