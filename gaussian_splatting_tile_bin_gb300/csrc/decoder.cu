@@ -20,8 +20,9 @@ int workspace(gsr_ctx *ctx, size_t bytes, cudaStream_t stream, void **out)
 {
     *out = nullptr;
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-    unsigned long long id = 0;
+    unsigned long long id = 0, number = 0;
     if (int rc = cuda_check(ctx, cudaStreamGetCaptureInfo(stream, &capture, &id), "workspace stream")) return rc;
+    if (int rc = cuda_check(ctx, cudaStreamGetId(stream, &number), "workspace stream")) return rc;
     if (bytes > ctx->cap_work) {
         if (capture != cudaStreamCaptureStatusNone)
             return fail(ctx, GSR_ERR_CUDA, "the workspace must grow during a capture: make one such call before it");
@@ -67,9 +68,9 @@ int workspace(gsr_ctx *ctx, size_t bytes, cudaStream_t stream, void **out)
     if (capture != cudaStreamCaptureStatusNone) {
         if (bytes > 0) ctx->work_captured = true;
         const CaptureMark *mark = find_capture(ctx, id);
-        if (mark && mark->stream != stream)
+        if (mark && mark->stream != number)
             if (int rc = cuda_check(ctx, cudaStreamWaitEvent(stream, mark->event, 0), "workspace order")) return rc;
-    } else if (ctx->work_pending && ctx->work_stream != stream) {
+    } else if (ctx->work_pending && ctx->work_stream != number) {
         if (int rc = cuda_check(ctx, cudaStreamWaitEvent(stream, ctx->work_event, 0), "workspace order")) return rc;
     }
     *out = ctx->work;
@@ -79,14 +80,15 @@ int workspace(gsr_ctx *ctx, size_t bytes, cudaStream_t stream, void **out)
 int workspace_done(gsr_ctx *ctx, cudaStream_t stream)
 {
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-    unsigned long long id = 0;
+    unsigned long long id = 0, number = 0;
     if (int rc = cuda_check(ctx, cudaStreamGetCaptureInfo(stream, &capture, &id), "workspace stream")) return rc;
-    cudaStream_t *last = &ctx->work_stream;
+    if (int rc = cuda_check(ctx, cudaStreamGetId(stream, &number), "workspace stream")) return rc;
+    unsigned long long *last = &ctx->work_stream;
     cudaEvent_t *event = &ctx->work_event;
     if (capture != cudaStreamCaptureStatusNone) {
         CaptureMark *mark = find_capture(ctx, id);
         if (!mark) {
-            mark = new (std::nothrow) CaptureMark{id, nullptr, nullptr, ctx->captures};
+            mark = new (std::nothrow) CaptureMark{id, 0, nullptr, ctx->captures};
             if (!mark) return fail(ctx, GSR_ERR_OOM, "cannot note the capture's use of the workspace");
             ctx->captures = mark;
         }
@@ -97,7 +99,7 @@ int workspace_done(gsr_ctx *ctx, cudaStream_t stream)
         if (int rc = cuda_check(ctx, cudaEventCreateWithFlags(event, cudaEventDisableTiming), "workspace event"))
             return rc;
     if (int rc = cuda_check(ctx, cudaEventRecord(*event, stream), "workspace event")) return rc;
-    *last = stream;
+    *last = number;
     if (capture == cudaStreamCaptureStatusNone) ctx->work_pending = true;
     return GSR_OK;
 }

@@ -143,3 +143,13 @@ def test_captures_side_by_side(lib, ctx):
     lib.fake_end_capture(TWO)
     assert attention(lib, ctx, ONE) == OK
     assert lib.fake_conflicts() == 0 and lib.fake_pulled_in() == 0
+
+
+@pytest.mark.parametrize("call", [attention, norm])
+def test_a_handle_that_another_stream_has_taken(lib, ctx, call):
+    """A stream destroyed with work queued, whose handle the next stream gets."""
+    for _ in range(2):
+        assert call(lib, ctx, ONE) == OK
+        lib.fake_new_stream(ONE)
+    assert call(lib, ctx, ONE) == OK
+    assert lib.fake_conflicts() == 0
