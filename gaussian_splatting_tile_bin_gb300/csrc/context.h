@@ -14,8 +14,7 @@ struct Outgrown {
 // captures may overlap, so each keeps its own.)
 struct CaptureMark {
     unsigned long long id;
-    unsigned long long stream;   // its number: a handle may be another stream's by the next call
-    cudaEvent_t event;           // recorded after the call, in the capture
+    cudaEvent_t event;      // recorded after the call, in the capture
     CaptureMark *next;
 };
 
@@ -98,7 +97,8 @@ struct gsr_ctx {
     unsigned char *work = nullptr;
     bool work_captured = false;                 // a captured call was given it: graphs hold its address
     gsr::Outgrown *outgrown = nullptr;          // smaller ones that graphs hold, kept until gsr_destroy
-    unsigned long long work_stream = 0;         // number of the stream of the last call that used it
+    unsigned long long work_stream = 0;         // number of the last live call's stream: its handle
+                                                // may be another stream's by the next call
     cudaEvent_t work_event = nullptr;           // recorded after that call
     bool work_pending = false;                  // work_event holds a record
     gsr::CaptureMark *captures = nullptr;       // captures that have used it, kept until gsr_destroy

@@ -20,9 +20,8 @@ int workspace(gsr_ctx *ctx, size_t bytes, cudaStream_t stream, void **out)
 {
     *out = nullptr;
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-    unsigned long long id = 0, number = 0;
+    unsigned long long id = 0;
     if (int rc = cuda_check(ctx, cudaStreamGetCaptureInfo(stream, &capture, &id), "workspace stream")) return rc;
-    if (int rc = cuda_check(ctx, cudaStreamGetId(stream, &number), "workspace stream")) return rc;
     if (bytes > ctx->cap_work) {
         if (capture != cudaStreamCaptureStatusNone)
             return fail(ctx, GSR_ERR_CUDA, "the workspace must grow during a capture: make one such call before it");
@@ -63,15 +62,19 @@ int workspace(gsr_ctx *ctx, size_t bytes, cudaStream_t stream, void **out)
         ctx->status_host = (uint32_t *)host;
         ctx->status_dev = (uint32_t *)dev;
     }
-    // A captured call is ordered with the others of its capture; the events of live
-    // streams and of other captures stay out of it.
+    // A captured call is ordered with the others of its capture (on the same stream
+    // too: a stream that is being captured cannot be asked for its number); the events
+    // of live streams and of other captures stay out of it.
     if (capture != cudaStreamCaptureStatusNone) {
         if (bytes > 0) ctx->work_captured = true;
         const CaptureMark *mark = find_capture(ctx, id);
-        if (mark && mark->stream != number)
+        if (mark && mark->event)
             if (int rc = cuda_check(ctx, cudaStreamWaitEvent(stream, mark->event, 0), "workspace order")) return rc;
-    } else if (ctx->work_pending && ctx->work_stream != number) {
-        if (int rc = cuda_check(ctx, cudaStreamWaitEvent(stream, ctx->work_event, 0), "workspace order")) return rc;
+    } else if (ctx->work_pending) {
+        unsigned long long number = 0;
+        if (int rc = cuda_check(ctx, cudaStreamGetId(stream, &number), "workspace stream")) return rc;
+        if (ctx->work_stream != number)
+            if (int rc = cuda_check(ctx, cudaStreamWaitEvent(stream, ctx->work_event, 0), "workspace order")) return rc;
     }
     *out = ctx->work;
     return GSR_OK;
@@ -80,27 +83,26 @@ int workspace(gsr_ctx *ctx, size_t bytes, cudaStream_t stream, void **out)
 int workspace_done(gsr_ctx *ctx, cudaStream_t stream)
 {
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-    unsigned long long id = 0, number = 0;
+    unsigned long long id = 0;
     if (int rc = cuda_check(ctx, cudaStreamGetCaptureInfo(stream, &capture, &id), "workspace stream")) return rc;
-    if (int rc = cuda_check(ctx, cudaStreamGetId(stream, &number), "workspace stream")) return rc;
-    unsigned long long *last = &ctx->work_stream;
     cudaEvent_t *event = &ctx->work_event;
     if (capture != cudaStreamCaptureStatusNone) {
         CaptureMark *mark = find_capture(ctx, id);
         if (!mark) {
-            mark = new (std::nothrow) CaptureMark{id, 0, nullptr, ctx->captures};
+            mark = new (std::nothrow) CaptureMark{id, nullptr, ctx->captures};
             if (!mark) return fail(ctx, GSR_ERR_OOM, "cannot note the capture's use of the workspace");
             ctx->captures = mark;
         }
-        last = &mark->stream;
         event = &mark->event;
     }
     if (!*event)
         if (int rc = cuda_check(ctx, cudaEventCreateWithFlags(event, cudaEventDisableTiming), "workspace event"))
             return rc;
     if (int rc = cuda_check(ctx, cudaEventRecord(*event, stream), "workspace event")) return rc;
-    *last = number;
-    if (capture == cudaStreamCaptureStatusNone) ctx->work_pending = true;
+    if (capture == cudaStreamCaptureStatusNone) {
+        ctx->work_pending = true;
+        return cuda_check(ctx, cudaStreamGetId(stream, &ctx->work_stream), "workspace stream");
+    }
     return GSR_OK;
 }
 

@@ -203,7 +203,11 @@ cudaError_t cudaStreamGetCaptureInfo(cudaStream_t s, cudaStreamCaptureStatus *to
     *id = at(s).capture;
     return cudaStreamIsCapturing(s, to);
 }
-cudaError_t cudaStreamGetId(cudaStream_t s, unsigned long long *id) { return *id = at(s).uid, cudaSuccess; }
+cudaError_t cudaStreamGetId(cudaStream_t s, unsigned long long *id)
+{
+    *id = at(s).uid;
+    return at(s).capture ? cudaErrorStreamCaptureUnsupported : cudaSuccess;
+}
 
 cudaError_t cudaEventCreateWithFlags(cudaEvent_t *e, unsigned)
 {
