@@ -918,8 +918,9 @@ int backward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr
     const size_t packed = d.key_mask ? round_up(packed_bytes(d), 256) : 0;
     const size_t stats = round_up((size_t)rows * sizeof(float), 512);
     const size_t partial = round_up((size_t)2 * blocks * kRowTile * 2 * d.head_dim * sizeof(float), 256);
+    Workspace workspace(ctx, stream);
     void *work;
-    if (int rc = workspace(ctx, packed + 3 * stats + partial + 256, stream, &work)) return rc;
+    if (int rc = workspace.take(packed + 3 * stats + partial + 256, &work)) return rc;
     unsigned char *p = (unsigned char *)work + packed;
     float *lse2 = (float *)p, *row_delta = (float *)(p + stats);
     a.partial = (float *)(p + 3 * stats);
@@ -976,7 +977,7 @@ int backward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr
     const int rc = d.head_dim <= 64 ? launch_backward<T, 64>(ctx, a, by_query, by_key, blocks, blocks, stream)
                                     : launch_backward<T, 128>(ctx, a, by_query, by_key, blocks, blocks, stream);
     if (rc) return rc;
-    return workspace_done(ctx, stream);
+    return workspace.done();
 }
 
 }  // namespace

@@ -393,8 +393,9 @@ int few_rows_forward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, c
     a.splits = (int)(splits < 1 ? 1 : splits);
     const size_t parts = a.splits > 1 ? (size_t)units * a.splits * 16 : 0;
     const size_t partial = round_up(parts * d.head_dim * sizeof(float), 256);
+    Workspace workspace(ctx, stream);
     void *work;
-    if (int rc = workspace(ctx, partial + parts * sizeof(float), stream, &work)) return rc;
+    if (int rc = workspace.take(partial + parts * sizeof(float), &work)) return rc;
     a.partial = (float *)work;
     a.partial_lse = (float *)((unsigned char *)work + partial);
     a.status = ctx->status_dev;
@@ -408,7 +409,7 @@ int few_rows_forward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, c
         rc = d.head_dim <= 64 ? launch_few<__half, 64>(ctx, a, units, stream)
                               : launch_few<__half, 128>(ctx, a, units, stream);
     if (rc) return rc;
-    return parts > 0 ? workspace_done(ctx, stream) : GSR_OK;
+    return workspace.done();
 }
 
 }  // namespace gsr

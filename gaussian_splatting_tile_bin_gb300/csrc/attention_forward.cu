@@ -519,8 +519,9 @@ int forward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr_
     const size_t rows = (size_t)2 * blocks * 2 * kRowTile;
     const size_t packed = d.key_mask ? round_up(packed_bytes(d), 256) : 0;
     const size_t partial = round_up(rows * d.head_dim * sizeof(float), 256);
+    Workspace workspace(ctx, stream);
     void *work;
-    if (int rc = workspace(ctx, packed + partial + rows * sizeof(float), stream, &work)) return rc;
+    if (int rc = workspace.take(packed + partial + rows * sizeof(float), &work)) return rc;
     a.partial = (float *)((unsigned char *)work + packed);
     a.partial_lse = (float *)((unsigned char *)work + packed + partial);
     a.status = ctx->status_dev;
@@ -545,7 +546,7 @@ int forward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr_
     const int rc = d.head_dim <= 64 ? launch_forward<T, 64>(ctx, a, blocks, stream)
                                     : launch_forward<T, 128>(ctx, a, blocks, stream);
     if (rc) return rc;
-    return workspace_done(ctx, stream);
+    return workspace.done();
 }
 
 }  // namespace

@@ -16,8 +16,10 @@ CaptureMark *find_capture(const gsr_ctx *ctx, unsigned long long id)
 
 }  // namespace
 
-int workspace(gsr_ctx *ctx, size_t bytes, cudaStream_t stream, void **out)
+int Workspace::take(size_t bytes, void **out)
 {
+    gsr_ctx *ctx = ctx_;
+    const cudaStream_t stream = stream_;
     *out = nullptr;
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
     unsigned long long id = 0;
@@ -62,11 +64,13 @@ int workspace(gsr_ctx *ctx, size_t bytes, cudaStream_t stream, void **out)
         ctx->status_host = (uint32_t *)host;
         ctx->status_dev = (uint32_t *)dev;
     }
+    *out = ctx->work;
+    if (bytes == 0) return GSR_OK;
     // A captured call is ordered with the others of its capture (on the same stream
     // too: a stream that is being captured cannot be asked for its number); the events
     // of live streams and of other captures stay out of it.
     if (capture != cudaStreamCaptureStatusNone) {
-        if (bytes > 0) ctx->work_captured = true;
+        ctx->work_captured = true;
         const CaptureMark *mark = find_capture(ctx, id);
         if (mark && mark->event)
             if (int rc = cuda_check(ctx, cudaStreamWaitEvent(stream, mark->event, 0), "workspace order")) return rc;
@@ -76,12 +80,30 @@ int workspace(gsr_ctx *ctx, size_t bytes, cudaStream_t stream, void **out)
         if (ctx->work_stream != number)
             if (int rc = cuda_check(ctx, cudaStreamWaitEvent(stream, ctx->work_event, 0), "workspace order")) return rc;
     }
-    *out = ctx->work;
+    used_ = true;
     return GSR_OK;
 }
 
-int workspace_done(gsr_ctx *ctx, cudaStream_t stream)
+int Workspace::done()
 {
+    if (!used_) return GSR_OK;
+    used_ = false;
+    return mark();
+}
+
+Workspace::~Workspace()
+{
+    if (!used_) return;
+    std::string reason;            // of the failure, which an error of the mark's must not replace
+    reason.swap(ctx_->err);
+    mark();
+    reason.swap(ctx_->err);
+}
+
+int Workspace::mark()
+{
+    gsr_ctx *ctx = ctx_;
+    const cudaStream_t stream = stream_;
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
     unsigned long long id = 0;
     if (int rc = cuda_check(ctx, cudaStreamGetCaptureInfo(stream, &capture, &id), "workspace stream")) return rc;

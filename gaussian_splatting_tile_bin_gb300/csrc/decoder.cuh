@@ -147,11 +147,24 @@ __device__ __forceinline__ void set_pair(Vec<T, V> &v, int i, float2 f)
     }
 }
 
-// Scratch memory of `bytes` for the launches that follow on `stream`, and the
-// mark after them.  workspace() grows the context's arena and makes `stream`
-// wait for the last call that used it on another stream.
-int workspace(gsr_ctx *ctx, size_t bytes, cudaStream_t stream, void **out);
-int workspace_done(gsr_ctx *ctx, cudaStream_t stream);
+// Scratch memory for a call's launches on `stream`.  take() grows the context's
+// arena and makes `stream` wait for the last call that used it; done() marks this
+// call's use.  A call that fails in between has perhaps launched work that uses the
+// memory, so its use is marked on the way out.  take() of 0 bytes orders nothing.
+class Workspace {
+public:
+    Workspace(gsr_ctx *ctx, cudaStream_t stream) : ctx_(ctx), stream_(stream) {}
+    ~Workspace();
+    Workspace(const Workspace &) = delete;
+    int take(size_t bytes, void **out);
+    int done();
+
+private:
+    int mark();
+    gsr_ctx *ctx_;
+    cudaStream_t stream_;
+    bool used_ = false;
+};
 
 // GSR_ERR_CUDA, once, if a kernel's bounded wait ran out in an earlier call.
 int check_status(gsr_ctx *ctx);

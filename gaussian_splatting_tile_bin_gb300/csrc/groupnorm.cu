@@ -1022,9 +1022,10 @@ int run_norm(gsr_ctx *ctx, const gsr_group_norm &d, NormArgs &a, bool backward, 
     const size_t sums = backward ? (size_t)d.samples * d.channels * sizeof(float2) : 0;
     const size_t group_sums = backward ? (size_t)d.samples * d.groups * sizeof(float2) : 0;
     const bool scratch = partial + sums + group_sums > 0;
+    Workspace workspace(ctx, stream);
     void *work = nullptr;
     if (scratch)
-        if (int rc = workspace(ctx, partial + sums + group_sums, stream, &work)) return rc;
+        if (int rc = workspace.take(partial + sums + group_sums, &work)) return rc;
     a.partial = (float2 *)work;
     a.sums = (float2 *)((unsigned char *)work + partial);
     a.group_sums = (float2 *)((unsigned char *)work + partial + sums);
@@ -1036,7 +1037,7 @@ int run_norm(gsr_ctx *ctx, const gsr_group_norm &d, NormArgs &a, bool backward, 
     else
         e = dispatch_act<__half>(ctx, a, p, r, d.activation, width, backward, stream);
     if (int rc = cuda_check(ctx, e, backward ? "group norm backward" : "group norm forward")) return rc;
-    return scratch ? workspace_done(ctx, stream) : GSR_OK;
+    return workspace.done();
 }
 
 }  // namespace

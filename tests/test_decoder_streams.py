@@ -153,3 +153,29 @@ def test_a_handle_that_another_stream_has_taken(lib, ctx, call):
         lib.fake_new_stream(ONE)
     assert call(lib, ctx, ONE) == OK
     assert lib.fake_conflicts() == 0
+
+
+def _uses():
+    yield lambda lib, ctx, stream: attention(lib, ctx, stream, mask=True)
+    yield lambda lib, ctx, stream: attention(lib, ctx, stream, mask=True, backward=True)
+    yield lambda lib, ctx, stream: attention(lib, ctx, stream, tokens=2, keys=20000)
+    yield lambda lib, ctx, stream: norm(lib, ctx, stream)
+    yield lambda lib, ctx, stream: norm(lib, ctx, stream, backward=True)
+
+
+@pytest.mark.parametrize("call", list(_uses()))
+@pytest.mark.parametrize("fail", ["fake_fail_launch", "fake_fail_map"])
+def test_a_failed_call_leaves_its_mark(lib, ctx, call, fail):
+    """A call that fails after some of its launches: what it launched is ordered before the next use."""
+    assert call(lib, ctx, ONE) == OK
+    failed = 0
+    for n in range(1, 12):
+        getattr(lib, fail)(n)
+        rc = call(lib, ctx, ONE if n % 2 else TWO)
+        getattr(lib, fail)(0)
+        failed += rc != OK
+        assert rc in (OK, CUDA) and (rc == OK or lib.gsr_last_error(ctx))
+        assert call(lib, ctx, TWO if n % 2 else ONE) == OK
+    assert lib.fake_conflicts() == 0
+    if fail == "fake_fail_launch":
+        assert failed >= 2
