@@ -19,8 +19,11 @@
 //
 // Rounding.  p and ds are rounded to the storage type, as the tensor cores take
 // operands of one type.  f16 has few exponents: p is held times 2^14 (p <= 1), and
-// ds times a power of two that brings its bound, 2 |do| |v| of the longest rows,
-// to f16's largest values; both powers are divided out of the float sums at the end.
+// ds times a power of two that brings its bound, 2 |do| |v|, to f16's largest
+// values; both powers are divided out of the float sums at the end.  A query's ds in
+// dq takes |do| of its own row, dk's sums over the queries the longest row of the
+// group's heads, and |v| is the longest row's of the same item and key head: rows
+// that never meet in a product do not cost each other bits.
 //
 // Bound by the tensor cores: 4,864 queries x 8,192 keys x 16 heads in bf16 take
 // 640 us for all three gradients at head_dim 128 (1,275 TFLOP/s on the five
@@ -45,41 +48,42 @@ constexpr int kComputeWarps = 4 * kGroups;
 constexpr int kBackwardThreads = 128 * kGroups + 128;   // and four warps of which one copies and one issues
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Powers that keep f16 p and ds in range.
-struct RangeShift {
-    float p;        // p is held times this
-    float ds;       // ds is held times this
-};
-
+// f16 p is held times this.
 template <typename T>
 constexpr float kShiftP = std::is_same<T, __half>::value ? 16384.0f : 1.0f;
 
-// norms: bits of the largest squared length of do's rows and of v's.
+// ds is held times this, a power of 2, where do's and v's rows are at most this long
+// (squared; of 16-bit values, so that their product is in float's range): |dp| and
+// |delta| are at most the lengths' product, so |ds| then stays below 2^15.
 template <typename T>
-__device__ __forceinline__ RangeShift range_shift(const uint32_t *norms)
+__device__ __forceinline__ float shift_ds(float dout_length2, float v_length2)
 {
-    RangeShift shift = {kShiftP<T>, 1.0f};
     if constexpr (std::is_same<T, __half>::value) {
-        // |dp| and |delta| are at most this, so |ds| shifted is below 2^15.
-        const float bound = sqrtf(__uint_as_float(norms[0])) * sqrtf(__uint_as_float(norms[1]));
-        if (bound > 0.0f && bound < INFINITY) shift.ds = exp2f((float)max(-60, min(60, 13 - ilogbf(bound))));
+        const int exponent = __float_as_int(dout_length2 * v_length2) >> 23 & 255;
+        if (exponent != 0 && exponent != 255) return __int_as_float((127 + 13 - ((exponent - 127) >> 1)) << 23);
     }
-    return shift;
+    return 1.0f;
 }
+
+// 1 / x of such a power.
+__device__ __forceinline__ float inverse_power(float x) { return __int_as_float((254 << 23) - __float_as_int(x)); }
 
 struct BackwardArgs {
     CUtensorMap q, k, v, dout;
     Schedule work;
-    const float *lse2;           // [batch, q_heads, q_pad]: log2(shift.p) - lse log2e
+    const float *lse2;           // [batch, q_heads, q_pad]: log2(kShiftP) - lse log2e
     const float *row_delta;      // the same: -do . o
-    float *delta;                // the same: -delta shift.ds / shift.p, left by the dq kernel
-    const uint32_t *norms;
+    float *delta;                // the same: -delta times the keys' kernel's shift_ds / kShiftP, left by the dq kernel
+    // f16: squared lengths of do's rows (as lse2), and the largest of do's and of v's
+    // rows of an item and key head ([batch, kv_heads]).
+    const float *dout_length2;
+    const float2 *top_length2;
     void *dq, *dk, *dv;
     int64_t dq_item, dq_token, dq_head, dk_item, dk_token, dk_head, dv_item, dv_token, dv_head;
     const int32_t *index;        // original keys of packed ones, [batch, kv_len], or NULL
     float *partial;              // [2 blocks][128][dim] (dq) or [2 blocks][128][2 dim] (dk, dv)
     uint32_t *status;
-    int q_len, q_pad, kv_len, q_heads, group, dim;
+    int q_len, q_pad, kv_len, q_heads, kv_heads, group, dim;
     int q_tiles;                 // tiles of 128 queries per head
     int q_item, q_head, dout_item, dout_head, k_item, k_head, v_item, v_head;
     bool wide_q, wide_kv;        // the gradients' rows take 32-byte stores
@@ -286,13 +290,13 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
         const uint32_t at_s = tmem + lanes + S::kS + column0, at_dp = tmem + lanes + S::kDp + column0;
         const int row_in_tile = warp % 4 * 32 + lane;
         const float c = a.scale_log2;
-        const RangeShift shift = range_shift<T>(a.norms);
-        const float f_dp = shift.ds / shift.p, f_out = a.scale / shift.ds;
-        const float2 c2 = make_float2(c, c), f2 = make_float2(f_dp, f_dp);
+        const float2 c2 = make_float2(c, c);
         uint32_t n = 0, seg = 0, step = 0;
         // The next segment's place and statistics are fetched while one is finished.
         bool there = next_uniform(walk, g);
         float lse = 0.0f, delta = 0.0f;
+        float length2 = 0.0f;
+        float2 top2 = make_float2(0.0f, 0.0f);
         auto statistics = [&](const Segment &t) {
             const int head = t.tile / a.q_tiles;
             return ((int64_t)t.item * a.q_heads + head) * a.q_pad + (t.tile - head * a.q_tiles) * kRowTile + row_in_tile;
@@ -301,14 +305,22 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
             if (!there || g.length == 0) return;
             lse = a.lse2[statistics(g)];
             delta = a.row_delta[statistics(g)];
+            if (kShiftP<T> != 1.0f) {
+                length2 = a.dout_length2[statistics(g)];
+                top2 = a.top_length2[(int64_t)g.item * a.kv_heads + g.tile / a.q_tiles / a.group];
+            }
         };
         fetch();
         while (there) {
             const Segment t = g;
+            // This row's power for ds, and the one that the keys' kernel takes.
+            const float shift = shift_ds<T>(length2, top2.y), shift_keys = shift_ds<T>(top2.x, top2.y);
+            const float f_dp = shift / kShiftP<T>;
+            const float2 f2 = make_float2(f_dp, f_dp);
             if (t.length > 0) {
                 const float2 lse2 = make_float2(lse, lse);
                 float2 delta2 = make_float2(delta * f_dp, delta * f_dp);
-                if (part == 0 && t.begin == 0 && t.total > 1) a.delta[statistics(t)] = delta2.x;
+                if (part == 0 && t.begin == 0 && t.total > 1) a.delta[statistics(t)] = delta * shift_keys / kShiftP<T>;
                 for (int i = t.begin; i < t.end; ++i, n += 2, ++step) {
                     Columns r;
                     barrier_wait_warp(bar.s, step & 1, guard);
@@ -344,9 +356,9 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                         sum = 0.0f;
 #pragma unroll
                         for (int x = 0; x < kGroups; ++x) sum += s_sum[x * kRowTile + row_in_tile];
-                        const float exact = -sum * (f_dp / shift.p);
-                        delta2 = make_float2(exact, exact);
-                        if (part == 0) a.delta[statistics(t)] = exact;
+                        const float exact = -sum / kShiftP<T>;
+                        delta2 = make_float2(exact * f_dp, exact * f_dp);
+                        if (part == 0) a.delta[statistics(t)] = exact * shift_keys / kShiftP<T>;
                     }
                     uint32_t packed[kColumnsEach / 2];
 #pragma unroll
@@ -376,6 +388,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                 barrier_wait_warp(bar.done, seg++ & 1, guard);
                 tmem_fence_after();
             }
+            const float f_out = a.scale * inverse_power(shift);
             const int head = t.tile / a.q_tiles, row = (t.tile - head * a.q_tiles) * kRowTile + row_in_tile;
             T *out = (T *)a.dq + t.item * a.dq_item + (int64_t)row * a.dq_token + head * a.dq_head;
             float *partial = a.partial + ((int64_t)partial_slot(t, blockIdx.x) * kRowTile + row_in_tile) * a.dim;
@@ -531,13 +544,19 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
         const uint32_t at_s = tmem + lanes + S::kS + column0, at_dp = tmem + lanes + S::kDp + column0;
         const int row_in_tile = warp % 4 * 32 + lane;
         const float c = a.scale_log2;
-        const RangeShift shift = range_shift<T>(a.norms);
-        const float f_dp = shift.ds / shift.p, f_k = a.scale / shift.ds, f_v = 1.0f / shift.p;
-        const float2 c2 = make_float2(c, c), f2 = make_float2(f_dp, f_dp);
+        const float2 c2 = make_float2(c, c);
         uint32_t n = 0, seg = 0, step = 0;
         while (next_uniform(walk, g)) {
             const int row = g.tile * kKeyTile + row_in_tile;        // key (packed)
             const bool any = g.tile * kKeyTile < g.length, live = row < g.length;
+            float shift = 1.0f;
+            if (kShiftP<T> != 1.0f) {
+                const float2 top2 = a.top_length2[(int64_t)g.item * a.kv_heads + g.head];
+                shift = shift_ds<T>(top2.x, top2.y);
+            }
+            const float f_dp = shift / kShiftP<T>, f_k = a.scale * inverse_power(shift);
+            constexpr float f_v = 1.0f / kShiftP<T>;
+            const float2 f2 = make_float2(f_dp, f_dp);
             if (any) {
                 const bool tail_tile = g.length - g.tile * kKeyTile < kKeyTile;
                 for (int i = g.begin; i < g.end; ++i, n += 2, ++step) {
@@ -696,35 +715,26 @@ struct RowArgs {
     gsr_heads out, dout, v;
     const float *lse;
     float *lse2, *delta;
-    uint32_t *norms;         // bits of the largest squared length of a row of dout and of v (f16)
+    float *dout_length2;     // f16: squared lengths of dout's rows, and the bits of the largest of them and
+    uint2 *top_length2;      // of v's rows by item and key head
     const int32_t *lengths;
-    int64_t rows, v_rows;    // batch x q_pad x q_heads; batch x kv_len x kv_heads
     int64_t row_blocks;      // blocks that take the queries' rows; those behind take v's
-    int q_len, q_pad, q_heads, kv_len, kv_heads, dim;
+    int q_len, q_pad, q_heads, kv_len, kv_heads, group, dim;
 };
 
-// Lanes of a row, 8 elements each, and a row's place: rows run over heads, then
-// tokens, as they lie in memory.
+// A block's rows, of one item and head: lanes of a row, 8 elements each, and its place.
 template <int LANES>
 struct RowPlace {
-    int64_t row;
-    uint32_t item, token, head;
-    int c;
-    __device__ RowPlace(int64_t block, int64_t rows, int tokens, int heads)
+    static constexpr int kRows = 256 / LANES;
+    uint32_t item, head;
+    int token, c;
+    __device__ RowPlace(uint32_t block, int tokens, int heads)
     {
-        row = block * (256 / LANES) + threadIdx.x / LANES;
+        const uint32_t each = (uint32_t)(tokens + kRows - 1) / kRows, unit = block / each;
+        item = unit / heads;
+        head = unit - item * heads;
+        token = (int)(block - unit * each) * kRows + threadIdx.x / LANES;
         c = threadIdx.x % LANES * 8;
-        if (rows >> 32) {   // many items of few queries, padded
-            const int64_t t = row / heads;
-            head = (uint32_t)(row - t * heads);
-            item = (uint32_t)(t / tokens);
-            token = (uint32_t)(t - (int64_t)item * tokens);
-        } else {
-            const uint32_t r = (uint32_t)row, t = r / heads;
-            head = r - t * heads;
-            item = t / tokens;
-            token = t - item * tokens;
-        }
     }
     template <typename T>
     __device__ Vec<T, 8> load(const gsr_heads &t) const
@@ -742,68 +752,74 @@ __device__ __forceinline__ float row_sum(float x)
     return x;
 }
 
-// -lse in base 2 with p's shift folded in, -delta, and the longest rows of dout and
-// of v's valid keys for ds' shift; rows behind q_len, and rows without keys, get p = 0.
+// -lse in base 2 with p's shift folded in, -delta, and the lengths of dout's rows and
+// of v's valid keys' for ds' shifts; rows behind q_len, and rows without keys, get p = 0.
 template <typename T, int LANES>
 __global__ void __launch_bounds__(256) k_attention_rows(const RowArgs a)
 {
     grid_dependency_begin();
-    constexpr bool kNorms = std::is_same<T, __half>::value;
+    constexpr bool kLengths = std::is_same<T, __half>::value;
     const bool queries = blockIdx.x < a.row_blocks;
-    float length = 0.0f;
+    const RowPlace<LANES> at(queries ? blockIdx.x : blockIdx.x - (uint32_t)a.row_blocks, queries ? a.q_pad : a.kv_len,
+                             queries ? a.q_heads : a.kv_heads);
+    float length2 = 0.0f;
     if (queries) {
-        const RowPlace<LANES> at(blockIdx.x, a.rows, a.q_pad, a.q_heads);
         float sum = 0.0f;
-        if (at.row < a.rows && at.token < (uint32_t)a.q_len && at.c < a.dim) {
+        if (at.token < a.q_len && at.c < a.dim) {
             const Vec<T, 8> o = at.template load<T>(a.out), d = at.template load<T>(a.dout);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 sum = fmaf(to_float(o.e[e]), to_float(d.e[e]), sum);
-                if (kNorms) length = fmaf(to_float(d.e[e]), to_float(d.e[e]), length);
+                if (kLengths) length2 = fmaf(to_float(d.e[e]), to_float(d.e[e]), length2);
             }
         }
         sum = row_sum<LANES>(sum);
-        if (at.row < a.rows && at.c == 0) {
+        if (kLengths) length2 = row_sum<LANES>(length2);
+        if (at.c == 0) {   // q_pad is a multiple of a block's rows
             const int64_t row = (int64_t)at.item * a.q_heads + at.head, to = row * a.q_pad + at.token;
             float lse = INFINITY;
-            if (at.token < (uint32_t)a.q_len) {
+            if (at.token < a.q_len) {
                 lse = a.lse[row * a.q_len + at.token];
                 lse = lse == -INFINITY ? INFINITY : lse * kLog2e - log2f(kShiftP<T>);
             }
             a.lse2[to] = -lse;
             a.delta[to] = -sum;
+            if (kLengths) a.dout_length2[to] = length2;
         }
     } else {
-        const RowPlace<LANES> at(blockIdx.x - a.row_blocks, a.v_rows, a.kv_len, a.kv_heads);
-        if (at.row < a.v_rows && at.c < a.dim && (int)at.token < item_length(a.lengths, a.kv_len, (int)at.item)) {
+        if (at.c < a.dim && at.token < item_length(a.lengths, a.kv_len, (int)at.item)) {
             const Vec<T, 8> v = at.template load<T>(a.v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) length = fmaf(to_float(v.e[e]), to_float(v.e[e]), length);
+            for (int e = 0; e < 8; ++e) length2 = fmaf(to_float(v.e[e]), to_float(v.e[e]), length2);
         }
+        length2 = row_sum<LANES>(length2);
     }
-    if constexpr (kNorms) {
+    if constexpr (kLengths) {
         // The largest of all is the same in any order; what is there already needs no atomic.
         __shared__ uint32_t s_top[8];
-        uint32_t top = __reduce_max_sync(~0u, __float_as_uint(row_sum<LANES>(length)));
+        uint32_t top = __reduce_max_sync(~0u, __float_as_uint(length2));
         if (threadIdx.x % 32 == 0) s_top[threadIdx.x / 32] = top;
         __syncthreads();
         if (threadIdx.x == 0) {
             for (int w = 1; w < 8; ++w) top = max(top, s_top[w]);
-            uint32_t *to = a.norms + (queries ? 0 : 1);
+            uint2 *unit = a.top_length2 + (int64_t)at.item * a.kv_heads + (queries ? at.head / a.group : at.head);
+            uint32_t *to = queries ? &unit->x : &unit->y;
             if (top > *(volatile uint32_t *)to) atomicMax(to, top);
         }
     }
 }
 
 template <typename T, int LANES>
-int row_statistics(gsr_ctx *ctx, RowArgs &r, cudaStream_t stream)
+int row_statistics(gsr_ctx *ctx, RowArgs &r, int batch, cudaStream_t stream)
 {
-    constexpr int kRows = 256 / LANES;
-    r.row_blocks = (r.rows + kRows - 1) / kRows;
+    constexpr int kRows = RowPlace<LANES>::kRows;
+    static_assert(kRowTile % kRows == 0, "a tile's rows are whole blocks");
+    r.row_blocks = (int64_t)batch * r.q_heads * (r.q_pad / kRows);
     int64_t blocks = r.row_blocks;
     if (std::is_same<T, __half>::value) {
-        blocks += (r.v_rows + kRows - 1) / kRows;
-        if (int rc = cuda_check(ctx, cudaMemsetAsync(r.norms, 0, 2 * sizeof(uint32_t), stream), "k_attention_rows"))
+        const int64_t units = (int64_t)batch * r.kv_heads;
+        blocks += units * ((r.kv_len + kRows - 1) / kRows);
+        if (int rc = cuda_check(ctx, cudaMemsetAsync(r.top_length2, 0, units * sizeof(uint2), stream), "k_attention_rows"))
             return rc;
     }
     return cuda_check(ctx, launch_kernel(ctx, k_attention_rows<T, LANES>, dim3((unsigned)blocks), 256, stream, r),
@@ -890,6 +906,7 @@ int backward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr
     a.q_len = d.q_len;
     a.kv_len = d.kv_len;
     a.q_heads = d.q_heads;
+    a.kv_heads = d.kv_heads;
     a.group = d.q_heads / d.kv_heads;
     a.dim = d.head_dim;
     a.q_tiles = (d.q_len + kRowTile - 1) / kRowTile;
@@ -920,15 +937,21 @@ int backward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr
     const size_t partial = round_up((size_t)2 * blocks * kRowTile * 2 * d.head_dim * sizeof(float), 256);
     Workspace workspace(ctx, stream);
     void *work;
-    if (int rc = workspace.take(packed + 3 * stats + partial + 256, &work)) return rc;
+    const bool lengths = d.dtype == GSR_F16;
+    const size_t top = lengths ? (size_t)d.batch * d.kv_heads * sizeof(float2) : 0;
+    if (int rc = workspace.take(packed + (lengths ? 4 : 3) * stats + partial + top, &work)) return rc;
     unsigned char *p = (unsigned char *)work + packed;
     float *lse2 = (float *)p, *row_delta = (float *)(p + stats);
     a.partial = (float *)(p + 3 * stats);
-    uint32_t *norms = (uint32_t *)(p + 3 * stats + partial);
     a.lse2 = lse2;
     a.row_delta = row_delta;
     a.delta = (float *)(p + 2 * stats);
-    a.norms = norms;
+    float *dout_length2 = (float *)(p + 3 * stats + partial);
+    unsigned char *top_length2 = p + 4 * stats + partial;
+    if (lengths) {
+        a.dout_length2 = dout_length2;
+        a.top_length2 = (const float2 *)top_length2;
+    }
     a.status = ctx->status_dev;
 
     gsr_heads keys = k, values = v;
@@ -949,16 +972,18 @@ int backward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr
     r.lse = lse;
     r.lse2 = lse2;
     r.delta = row_delta;
-    r.norms = norms;
-    r.rows = rows;
+    r.dout_length2 = dout_length2;
+    r.top_length2 = (uint2 *)top_length2;
+    r.group = a.group;
     r.q_len = d.q_len;
     r.q_pad = a.q_pad;
     r.q_heads = d.q_heads;
-    r.v_rows = (int64_t)d.batch * d.kv_len * d.kv_heads;
     r.kv_len = d.kv_len;
     r.kv_heads = d.kv_heads;
     r.dim = d.head_dim;
-    if (int rc = d.head_dim <= 64 ? row_statistics<T, 8>(ctx, r, stream) : row_statistics<T, 16>(ctx, r, stream)) return rc;
+    if (int rc = d.head_dim <= 64 ? row_statistics<T, 8>(ctx, r, d.batch, stream)
+                                     : row_statistics<T, 16>(ctx, r, d.batch, stream))
+        return rc;
 
     a.wide_q = rows_of_32_bytes(dq, d.head_dim);
     a.wide_kv = rows_of_32_bytes(dk, d.head_dim) && rows_of_32_bytes(dv, d.head_dim);
