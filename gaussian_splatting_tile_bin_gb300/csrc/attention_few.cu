@@ -27,7 +27,7 @@ constexpr int kTileKeys = 64;
 constexpr int kWarps = 4;
 constexpr int kFewThreads = (kWarps + 1) * 32;
 constexpr int kStages = 3;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct FewArgs {
     CUtensorMap k, v;
@@ -42,7 +42,7 @@ struct FewArgs {
     uint32_t *status;
     int q_len, kv_len, q_heads, kv_heads, group, dim, splits;
     int k_item, k_head, v_item, v_head;
-    float scale_log2;
+    float scale, scale_log2;
 };
 
 template <int HD>
@@ -203,12 +203,14 @@ __global__ void __launch_bounds__(kFewThreads) k_attention_few(const __grid_cons
             for (int r = 0; r < 2; ++r) {
                 const float top = quad_max(fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1])));
                 const float next = fmaxf(m[r], top);
-                const float shift = next == -INFINITY ? 0.0f : -next * c;
-                const float keep = exp2_fast(fmaf(m[r], c, shift));
+                // The difference first: where the maximum stays, `keep` is 1, and not what
+                // the rounding of m c leaves, tile after tile.
+                const float from = next == -INFINITY ? 0.0f : next;
+                const float keep = exp2_fast((m[r] - from) * c);
                 m[r] = next;
                 float e[4];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) e[x] = exp2_fast(fmaf(s[x >> 1][2 * r + (x & 1)], c, shift));
+                for (int x = 0; x < 4; ++x) e[x] = exp2_fast((s[x >> 1][2 * r + (x & 1)] - from) * c);
                 l[r] = fmaf(l[r], keep, (e[0] + e[1]) + (e[2] + e[3]));
                 p[r] = pack2<T>(e[0], e[1]);
                 p[r + 2] = pack2<T>(e[2], e[3]);
@@ -263,18 +265,18 @@ done:
         if (d >= a.dim) continue;
         float top = -INFINITY;
         for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w * 16 + row]);
-        const float shift = top == -INFINITY ? 0.0f : -top * a.scale_log2;
+        const float from = top == -INFINITY ? 0.0f : top;
         float sum = 0.0f;
         float2 f = make_float2(0.0f, 0.0f);
         for (int w = 0; w < kWarps; ++w) {
-            const float weight = exp2_fast(fmaf(s_m[w * 16 + row], a.scale_log2, shift));
+            const float weight = exp2_fast((s_m[w * 16 + row] - from) * a.scale_log2);
             const float2 g = *(const float2 *)&s_o[(w * 16 + row) * HD + d];
             sum = fmaf(weight, s_l[w * 16 + row], sum);
             if (weight != 0.0f) f = make_float2(fmaf(weight, g.x, f.x), fmaf(weight, g.y, f.y));
         }
         const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
         f = make_float2(f.x * inv, f.y * inv);
-        const float lse = top * (a.scale_log2 * kLn2) + logf(sum);
+        const float lse = top * a.scale + logf(sum);
         const int token = row / a.group, head = key_head * a.group + row % a.group;
         if (a.splits == 1) {
             *(uint32_t *)((T *)a.out + item * a.out_item + token * a.out_token + head * a.out_head + d) =
@@ -380,6 +382,7 @@ int few_rows_forward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, c
     a.kv_heads = d.kv_heads;
     a.group = d.q_heads / d.kv_heads;
     a.dim = d.head_dim;
+    a.scale = d.scale;
     a.scale_log2 = d.scale * kLog2e;
     a.k_item = k.batch_stride != 0;
     a.k_head = k.head_stride != 0;
