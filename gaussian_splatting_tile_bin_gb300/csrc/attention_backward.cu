@@ -356,7 +356,8 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_q(const 
                         sum = 0.0f;
 #pragma unroll
                         for (int x = 0; x < kGroups; ++x) sum += s_sum[x * kRowTile + row_in_tile];
-                        const float exact = -sum / kShiftP<T>;
+                        // (The zero rows behind the last query meet an infinite key as NaN.)
+                        const float exact = lse == -INFINITY ? 0.0f : -sum / kShiftP<T>;
                         delta2 = make_float2(exact * f_dp, exact * f_dp);
                         if (part == 0) a.delta[statistics(t)] = exact * shift_keys / kShiftP<T>;
                     }
@@ -559,6 +560,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
             const float2 f2 = make_float2(f_dp, f_dp);
             if (any) {
                 const bool tail_tile = g.length - g.tile * kKeyTile < kKeyTile;
+                int left = a.q_len - g.begin % a.q_tiles * kRowTile;   // queries from this step's first on
                 for (int i = g.begin; i < g.end; ++i, n += 2, ++step) {
                     const float4 *lse4 = (const float4 *)(s_raw + (s_stat - raw) + n % S::kStages * S::kStatBytes) +
                                          column0 / 4;
@@ -585,6 +587,16 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
                     if (tail_tile && !live)
 #pragma unroll
                         for (int y = 0; y < kColumnsEach / 2; ++y) p[y] = make_float2(0.0f, 0.0f);
+                    // The zero rows behind the last query meet an infinite key as NaN.
+                    if (left < column0 + kColumnsEach) {
+#pragma unroll
+                        for (int y = 0; y < kColumnsEach / 2; ++y) {
+                            if (column0 + 2 * y >= left) p[y].x = 0.0f;
+                            if (column0 + 2 * y + 1 >= left) p[y].y = 0.0f;
+                        }
+                    }
+                    left -= kRowTile;
+                    if (left <= 0) left = a.q_len;
 #pragma unroll
                     for (int y = 0; y < kColumnsEach / 2; ++y) packed[y] = pack2<T>(p[y].x, p[y].y);
                     __syncwarp();
