@@ -152,6 +152,7 @@ def train(steps=60, views=3, grid=16, side=128, seed=0, log=print):
         losses.append(loss.item())
         if step % 10 == 0 or step == steps - 1:
             log(f"step {step}: loss {losses[-1]:.5f}")
+    ctx.synchronize()                               # raises if a kernel gave up on the way
     ctx.close()
     return losses
 

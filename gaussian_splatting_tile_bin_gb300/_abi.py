@@ -95,6 +95,8 @@ def _load():
     lib.gsr_project_forward.restype = ctypes.c_int
     lib.gsr_project_backward.argtypes = [P, P, i32, ctypes.POINTER(_Camera), P, P, P]
     lib.gsr_project_backward.restype = ctypes.c_int
+    lib.gsr_synchronize.argtypes = [P, P]
+    lib.gsr_synchronize.restype = ctypes.c_int
     lib.gsr_exp_neg.argtypes = [P, P, P, i32, P]
     lib.gsr_exp_neg.restype = ctypes.c_int
     lib.gsr_peak_kernel.argtypes = [P, ctypes.c_int, i32, P, ctypes.POINTER(ctypes.c_uint64), P]
@@ -162,6 +164,13 @@ class Context:
         st = _BinStats()
         self._check(lib.gsr_get_bin_stats(self._h, ctypes.byref(st)))
         return {name: (int(getattr(st, name))) for name, _ in _BinStats._fields_}
+
+    def synchronize(self, stream=None):
+        """Waits for the work on `stream` (default: the current stream); GsrError if a
+        kernel of the decoder's operators gave up waiting, so that what it and later
+        calls wrote is not valid.  Call it where their results leave the GPU, and
+        after a graph's replays."""
+        self._check(lib.gsr_synchronize(self._h, _stream_ptr(stream, self.device)))
 
     def close(self):
         if getattr(self, "_h", None):

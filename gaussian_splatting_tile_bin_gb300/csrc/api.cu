@@ -505,6 +505,17 @@ int check_key(gsr_ctx *ctx, const gsr_attention *d, const gsr_heads *t, const ch
 
 extern "C" {
 
+int gsr_synchronize(gsr_ctx *ctx, void *stream)
+{
+    gsr::Range range("gsr_synchronize");
+    if (!ctx) return GSR_ERR_INVALID_ARG;
+    ctx->err.clear();
+    DeviceGuard g(ctx->device);
+    if (!g.ok) return fail(ctx, GSR_ERR_CUDA, "cannot select the context's device");
+    if (int rc = cuda_check(ctx, cudaStreamSynchronize((cudaStream_t)stream), "gsr_synchronize")) return rc;
+    return gsr::check_status(ctx);
+}
+
 int gsr_group_norm_forward(gsr_ctx *ctx, const gsr_group_norm *desc, const void *x, const float *weight,
                            const float *bias, void *out, float *mean, float *rstd, void *stream)
 {
@@ -514,6 +525,7 @@ int gsr_group_norm_forward(gsr_ctx *ctx, const gsr_group_norm *desc, const void 
     if (int rc = check_group_norm(ctx, desc, x, weight, bias, out, mean, rstd)) return rc;
     DeviceGuard g(ctx->device);
     if (!g.ok) return fail(ctx, GSR_ERR_CUDA, "cannot select the context's device");
+    if (int rc = gsr::check_status(ctx)) return rc;
     if (desc->samples == 0 || desc->positions == 0) return GSR_OK;
     return gsr::group_norm_forward(ctx, *desc, x, weight, bias, out, mean, rstd, (cudaStream_t)stream);
 }
@@ -532,6 +544,7 @@ int gsr_group_norm_backward(gsr_ctx *ctx, const gsr_group_norm *desc, const void
         return fail(ctx, GSR_ERR_INVALID_ARG, "an array is not aligned to its element");
     DeviceGuard g(ctx->device);
     if (!g.ok) return fail(ctx, GSR_ERR_CUDA, "cannot select the context's device");
+    if (int rc = gsr::check_status(ctx)) return rc;
     return gsr::group_norm_backward(ctx, *desc, dl_dout, x, weight, bias, mean, rstd, dl_dx, dl_dweight, dl_dbias,
                                     (cudaStream_t)stream);
 }
@@ -545,6 +558,7 @@ int gsr_rotary_forward(gsr_ctx *ctx, const gsr_rotary *desc, const gsr_heads *x,
     if (int rc = check_rotary(ctx, desc, x, positions, frequencies, out)) return rc;
     DeviceGuard g(ctx->device);
     if (!g.ok) return fail(ctx, GSR_ERR_CUDA, "cannot select the context's device");
+    if (int rc = gsr::check_status(ctx)) return rc;
     if (desc->batch == 0 || desc->tokens == 0) return GSR_OK;
     return gsr::rotary(ctx, *desc, *x, positions, frequencies, *out, 1.0f, (cudaStream_t)stream);
 }
@@ -558,6 +572,7 @@ int gsr_rotary_backward(gsr_ctx *ctx, const gsr_rotary *desc, const gsr_heads *d
     if (int rc = check_rotary(ctx, desc, dl_dout, positions, frequencies, dl_dx)) return rc;
     DeviceGuard g(ctx->device);
     if (!g.ok) return fail(ctx, GSR_ERR_CUDA, "cannot select the context's device");
+    if (int rc = gsr::check_status(ctx)) return rc;
     if (desc->batch == 0 || desc->tokens == 0) return GSR_OK;
     return gsr::rotary(ctx, *desc, *dl_dout, positions, frequencies, *dl_dx, -1.0f, (cudaStream_t)stream);
 }
@@ -577,6 +592,7 @@ int gsr_cross_attention_forward(gsr_ctx *ctx, const gsr_attention *desc, const g
     if (!lse || !aligned(lse, 4)) return fail(ctx, GSR_ERR_INVALID_ARG, "lse is NULL or misaligned");
     DeviceGuard g(ctx->device);
     if (!g.ok) return fail(ctx, GSR_ERR_CUDA, "cannot select the context's device");
+    if (int rc = gsr::check_status(ctx)) return rc;
     return gsr::cross_attention_forward(ctx, *desc, *q, *k, *v, *out, lse, (cudaStream_t)stream);
 }
 
@@ -602,6 +618,7 @@ int gsr_cross_attention_backward(gsr_ctx *ctx, const gsr_attention *desc, const 
         return fail(ctx, GSR_ERR_INVALID_ARG, "lse is NULL or misaligned");
     DeviceGuard g(ctx->device);
     if (!g.ok) return fail(ctx, GSR_ERR_CUDA, "cannot select the context's device");
+    if (int rc = gsr::check_status(ctx)) return rc;
     return gsr::cross_attention_backward(ctx, *desc, *q, *k, *v, *out, lse, *dl_dout, *dl_dq, *dl_dk, *dl_dv,
                                          (cudaStream_t)stream);
 }

@@ -1023,7 +1023,6 @@ int cross_attention_backward(gsr_ctx *ctx, const gsr_attention &d, const gsr_hea
                              const gsr_heads &v, const gsr_heads &out, const float *lse, const gsr_heads &dout,
                              const gsr_heads &dq, const gsr_heads &dk, const gsr_heads &dv, cudaStream_t stream)
 {
-    if (int rc = check_status(ctx)) return rc;
     return d.dtype == GSR_BF16 ? backward<__nv_bfloat16>(ctx, d, q, k, v, out, lse, dout, dq, dk, dv, stream)
                                : backward<__half>(ctx, d, q, k, v, out, lse, dout, dq, dk, dv, stream);
 }

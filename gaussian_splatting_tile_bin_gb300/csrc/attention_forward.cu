@@ -554,7 +554,6 @@ int forward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr_
 int cross_attention_forward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr_heads &k,
                             const gsr_heads &v, const gsr_heads &out, float *lse, cudaStream_t stream)
 {
-    if (int rc = check_status(ctx)) return rc;
     if (d.kv_len > 0 && (int64_t)d.q_len * (d.q_heads / d.kv_heads) <= kFewRows)
         return few_rows_forward(ctx, d, q, k, v, out, lse, stream);
     return d.dtype == GSR_BF16 ? forward<__nv_bfloat16>(ctx, d, q, k, v, out, lse, stream)

@@ -166,7 +166,8 @@ private:
     bool used_ = false;
 };
 
-// GSR_ERR_CUDA, once, if a kernel's bounded wait ran out in an earlier call.
+// GSR_ERR_CUDA, once, if a kernel's bounded wait ran out in an earlier call, as far
+// as that has run.
 int check_status(gsr_ctx *ctx);
 
 inline size_t round_up(size_t n, size_t unit) { return (n + unit - 1) / unit * unit; }

@@ -61,7 +61,8 @@ __device__ __forceinline__ bool barrier_try(uint32_t bar, uint32_t parity)
 // microseconds) marks the block as aborted and reports to the host's status
 // word, and every later wait of the block returns at once: the copying thread
 // then stops (its barriers could not count copies that nothing waits for), the
-// others run through the rest of their loops, and the host refuses the results.
+// others run through the rest of their loops, and the results are not valid.  The
+// context's next call of a decoder operator or gsr_synchronize says so.
 constexpr long long kWaitCycles = 4000000000ll;
 
 struct WaitGuard {

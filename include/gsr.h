@@ -402,6 +402,16 @@ int gsr_peak_kernel(gsr_ctx *ctx, int kind, int32_t iters, float *sink, uint64_t
  * the graph's last replay has to be complete.  Inputs and outputs must not
  * overlap unless a call says so. */
 
+/* Waits for the work on `stream`, and tells whether it is to be trusted.
+ * Every wait inside the attention kernels is bounded (seconds, where a step takes
+ * microseconds).  One that runs out ends its kernel without a fault, but what the
+ * call wrote is not valid, nor is what later calls made of it.  That is reported
+ * once, as GSR_ERR_CUDA: by the context's next call of a decoder operator, before
+ * it launches anything, as far as the work has run by then; or by this call, which
+ * misses nothing on `stream`, graph replays among it.
+ * Errors: GSR_ERR_INVALID_ARG (ctx is NULL), GSR_ERR_CUDA. */
+int gsr_synchronize(gsr_ctx *ctx, void *stream);
+
 /* Element types of the decoder's arrays. */
 enum { GSR_F32 = 0, GSR_BF16 = 1, GSR_F16 = 2 };
 

@@ -179,3 +179,30 @@ def test_a_failed_call_leaves_its_mark(lib, ctx, call, fail):
     assert lib.fake_conflicts() == 0
     if fail == "fake_fail_launch":
         assert failed >= 2
+
+
+def rotary(lib, ctx, stream):
+    from gaussian_splatting_tile_bin_gb300 import _abi
+    desc = _abi.ROTARY.pack(2, 2, 200, 4, 64, 0, 1, 16, 0, 0, 0, 0, 0)
+    return lib.gsr_rotary_forward(ctx, desc, _heads(200, 4), AT, AT, _heads(200, 4), stream)
+
+
+def test_a_wait_that_ran_out_is_reported(lib, ctx):
+    """By the next call of any decoder operator, or by gsr_synchronize; once."""
+    lib.gsr_synchronize.argtypes = [ctypes.c_void_p] * 2
+    assert lib.gsr_synchronize(None, None) == INVALID_ARG
+    assert lib.gsr_synchronize(ctx, None) == OK      # nothing has run yet
+    assert attention(lib, ctx, ONE) == OK
+    for call in (lambda: lib.gsr_synchronize(ctx, ONE), lambda: attention(lib, ctx, ONE),
+                 lambda: attention(lib, ctx, ONE, tokens=1), lambda: attention(lib, ctx, ONE, backward=True),
+                 lambda: norm(lib, ctx, ONE), lambda: norm(lib, ctx, ONE, backward=True),
+                 lambda: rotary(lib, ctx, ONE)):
+        assert call() == OK
+        lib.fake_set_status()
+        launches = lib.fake_launches()
+        assert call() == CUDA and b"gave up waiting" in lib.gsr_last_error(ctx)
+        assert lib.fake_launches() == launches
+        assert call() == OK
+    lib.fake_set_status()                            # by the last call of a program
+    assert lib.gsr_synchronize(ctx, ONE) == CUDA
+    assert lib.gsr_synchronize(ctx, ONE) == OK

@@ -91,3 +91,14 @@ def test_streams_of_one_capture(gsr, ctx):
         graph.replay()
         torch.cuda.synchronize()
         assert all(_same(a, b) for a, b in zip(got, want)) and _same(again, want[0])
+
+
+def test_synchronize(gsr, ctx):
+    ctx.synchronize()
+    step = _step(gsr, ctx, 200, 300, 5)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = step(side)
+    ctx.synchronize(side)
+    assert side.query() and _same(step(), got)
+    ctx.synchronize()
