@@ -401,6 +401,14 @@ def _first(t, name, among):
     return t.get_device()
 
 
+def _on(ctx, t, name, among):
+    """_first of a call on `ctx`, whose device the tensors have to be on: the kernels run there."""
+    index = _first(t, name, among)
+    if index != ctx.device:
+        raise ValueError(f"{name} is on cuda:{index}, the context on cuda:{ctx.device}")
+    return index
+
+
 def _refuse(t, name, dtype, shape, index):
     if not isinstance(t, torch.Tensor) or t.get_device() != index:
         raise ValueError(f"{name} must be a CUDA tensor on cuda:{index}")
@@ -492,7 +500,7 @@ def group_norm_forward(ctx: Context, x: torch.Tensor, groups: int, weight=None, 
     (f32, bf16 or f16; weight and bias [channels] f32 or None).  `activation` is
     "none", "silu" or "gelu".  Returns (out, mean, rstd), the last two
     [samples, groups] f32 for the backward.  out may be x."""
-    index = _first(x, "x", DTYPES)
+    index = _on(ctx, x, "x", DTYPES)
     dtype, shape, dev = x.dtype, x.shape, x.device
     desc = _norm_desc(x, groups, eps, activation)
     channels, stats = shape[-1:], (shape[0], max(int(groups), 0))
@@ -512,7 +520,7 @@ def group_norm_backward(ctx: Context, dl_dout: torch.Tensor, x: torch.Tensor, gr
                         dl_dweight=None, dl_dbias=None, stream=None):
     """Returns (dL/dx as x, dL/dweight [channels] f32, dL/dbias [channels] f32) for
     dL/dout, with the forward's x, weight, bias, mean and rstd.  dl_dx may be dl_dout."""
-    index = _first(x, "x", DTYPES)
+    index = _on(ctx, x, "x", DTYPES)
     dtype, shape, dev = x.dtype, x.shape, x.device
     desc = _norm_desc(x, groups, 1.0, activation)
     channels, stats = shape[-1:], (shape[0], int(groups))
@@ -536,7 +544,7 @@ def rotary_frequencies(sections, base: float = 10000.0, device="cuda") -> torch.
 
 
 def _rotary(call, name, ctx, x, positions, frequencies, sections, interleaved, out, out_name, stream):
-    index = _first(x, name, DTYPES)
+    index = _on(ctx, x, name, DTYPES)
     dtype, shape = x.dtype, x.shape
     if len(shape) != 4:
         raise ValueError(f"{name} must have shape [batch, tokens, heads, head_dim], got {tuple(shape)}")
@@ -577,9 +585,9 @@ def rotary_backward(ctx: Context, dl_dout: torch.Tensor, positions: torch.Tensor
                    dl_dx, "dl_dx", stream)
 
 
-def _attention(q, k, v, kv_lengths, key_mask, scale):
+def _attention(ctx, q, k, v, kv_lengths, key_mask, scale):
     """The packed description and q, k, v; the device's index and k's shape."""
-    index = _first(q, "q", _HALVES)
+    index = _on(ctx, q, "q", _HALVES)
     dtype, shape = q.dtype, q.shape
     if len(shape) != 4 or not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("q, k and v must have shape [batch, tokens, heads, head_dim]")
@@ -606,7 +614,7 @@ def cross_attention_forward(ctx: Context, q: torch.Tensor, k: torch.Tensor, v: t
     (bool or uint8) is 0, take no part; a row without any gives 0 and lse -inf.
     `scale` defaults to head_dim ** -0.5.  Returns (out as q, lse [batch, q_heads,
     q_len] f32)."""
-    index, _, desc, at_q, at_k, at_v = _attention(q, k, v, kv_lengths, key_mask, scale)
+    index, _, desc, at_q, at_k, at_v = _attention(ctx, q, k, v, kv_lengths, key_mask, scale)
     dtype, shape = q.dtype, q.shape
     rows = (shape[0], shape[2], shape[1])
     out, at_out = _heads_out(out, "out", dtype, shape, index, q.device, stream, q)
@@ -621,7 +629,7 @@ def cross_attention_backward(ctx: Context, q: torch.Tensor, k: torch.Tensor, v: 
                              dl_dq=None, dl_dk=None, dl_dv=None, stream=None):
     """Returns (dL/dq, dL/dk, dL/dv) for dL/dout, with the forward's arguments, out
     and lse.  Keys that took no part get zeros."""
-    index, keys, desc, at_q, at_k, at_v = _attention(q, k, v, kv_lengths, key_mask, scale)
+    index, keys, desc, at_q, at_k, at_v = _attention(ctx, q, k, v, kv_lengths, key_mask, scale)
     dtype, shape, dev = q.dtype, q.shape, q.device
     dl_dq, at_dq = _heads_out(dl_dq, "dl_dq", dtype, shape, index, dev, stream, q)
     dl_dk, at_dk = _heads_out(dl_dk, "dl_dk", dtype, keys, index, dev, stream, k)
