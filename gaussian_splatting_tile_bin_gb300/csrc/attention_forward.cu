@@ -15,14 +15,16 @@
 // as these are read; at 128, where the accumulators fill tensor memory, it
 // replaces the scores and the next ones come behind its product.
 //
-// m starts as the maximum of the row's first keys, in whole powers of 2.  It moves
-// only when 64 keys' sum of exp(s - m) exceeds 2^12, which tells that without a
-// maximum of every tile (the comparisons took a third of the softmax' time): the
-// row then takes its true maximum, and the sum, the output and the first half's P
-// are scaled by a power of 2, which rounds nothing.  Until then P exceeds 1 by at
-// most that factor, which 16-bit P and float sums hold without loss.  P is
-// rounded to the storage type (the tensor cores take 16-bit operands at the full
-// rate); l sums the unrounded values in float.
+// m starts as the maximum of the row's first 64 keys, to 2^-12 of a power of 2, so
+// that this key's P rounds to 1 and a row that it takes is its v.  m moves only when
+// 64 keys' sum of exp(s - m) exceeds 2^12, which tells that without a maximum of
+// every tile (the comparisons took a third of the softmax' time): the row then takes
+// a maximum of these keys, a whole number of powers of 2 higher.  The sum and the output are
+// scaled by that power, which rounds nothing, and so is the first half's P, of which
+// f16 rounds what falls below its normal range, 2^-14 of the row's largest.  Until
+// then P exceeds 1 by at most 2^12, which 16-bit P and float sums hold.  P is rounded
+// to the storage type (the tensor cores take 16-bit operands at the full rate); l
+// sums the unrounded values in float.
 //
 // Bound by the tensor cores: 4,864 queries x 8,192 keys x 16 heads in bf16 take
 // 182 us at head_dim 128, 1,790 TFLOP/s, 94% of a large library product's rate, and
@@ -234,7 +236,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
             const int head = g.tile / row_tiles, row0 = (g.tile - head * row_tiles) * 2 * kRowTile + t * kRowTile;
             const int row = row0 + row_in_tile;
             const bool whole = g.whole();
-            float m = -INFINITY, l = 0.0f;   // the reference, a whole number of powers of 2; the sum
+            float m = -INFINITY, l = 0.0f;   // the reference, in powers of 2; the sum
             const bool active = row0 < a.q_len;
             if (g.length > 0 && active) {
                 for (int i = g.begin; i < g.end; ++i, ++n) {
@@ -295,11 +297,14 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
                             tmem_fence_after();
                         }
                     };
-                    // The keys' true maximum becomes the reference, and what was summed before is scaled down.
+                    // The keys' maximum becomes the reference (at most 1 above it once there was
+                    // another), and what was summed before is scaled down.
+                    auto first = [](float top) { return rintf(top * 4096.0f) * (1.0f / 4096.0f); };
                     auto raise = [&](int h) {
-                        const float next = fmaxf(m, ceilf(largest(h) * c));
-                        const float down = next - m;   // whole; NaN when both are infinite
-                        const float keep = down > 126.0f ? 0.0f : down > 0.0f ? __int_as_float((127 - (int)down) << 23) : 1.0f;
+                        const float top = largest(h) * c;
+                        const float down = m == -INFINITY ? INFINITY : fmaxf(ceilf(top - m), 0.0f);   // whole
+                        const float next = m == -INFINITY ? first(top) : m + down;
+                        const float keep = down > 126.0f ? 0.0f : __int_as_float((127 - (int)down) << 23);
                         m = next;
                         l *= keep;
                         if (h == 1)
@@ -332,7 +337,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
                         if (!S::kApart) tmem_store32(at_p + h * 32, packed[h]);
                     };
                     if (ragged) clear_ragged(0);
-                    if (i == g.begin) m = ceilf(largest(0) * c);
+                    if (i == g.begin) m = first(largest(0) * c);
                     half(0);
                     tmem_load32(r[2], at_s + 64);   // any earlier takes more registers than there are
                     tmem_load32(r[3], at_s + 96);
