@@ -231,11 +231,27 @@ __device__ __forceinline__ void store32(void *p, uint32_t a, uint32_t b, uint32_
                  : "memory");
 }
 
-// Up to 32 results of a row, `left` of them there, to their place (whole) or to
-// the partial results.  A thread holds a row, so its neighbours' stores fall into
-// other lines: the wider each is the fewer there are.  `wide`: out's rows and
-// `left` are multiples of 32 bytes.
+// An average of v whose weights P were rounded to 16 bits may come out above the
+// largest v by 2^-11 of it, which beside f16's largest number is infinity.
 template <typename T>
+__device__ __forceinline__ float within_range(float x)
+{
+    if constexpr (std::is_same<T, __half>::value) return fabsf(x) < 65600.0f ? fminf(fmaxf(x, -65504.0f), 65504.0f) : x;
+    return x;
+}
+
+// Two averages as a 16-bit pair.
+template <typename T>
+__device__ __forceinline__ uint32_t pack_average(float lo, float hi)
+{
+    return pack2<T>(within_range<T>(lo), within_range<T>(hi));
+}
+
+// Up to 32 results of a row (AVERAGE: averages of v), `left` of them there, to their
+// place (whole) or to the partial results.  A thread holds a row, so its
+// neighbours' stores fall into other lines: the wider each is the fewer there are.
+// `wide`: out's rows and `left` are multiples of 32 bytes.
+template <typename T, bool AVERAGE = false>
 __device__ __forceinline__ void store_results(T *out, float *partial, bool whole, bool wide, int left, const float (&f)[32])
 {
     if (!whole) {
@@ -249,7 +265,8 @@ __device__ __forceinline__ void store_results(T *out, float *partial, bool whole
     }
     uint32_t w[16];
 #pragma unroll
-    for (int y = 0; y < 16; ++y) w[y] = pack2<T>(f[2 * y], f[2 * y + 1]);
+    for (int y = 0; y < 16; ++y)
+        w[y] = AVERAGE ? pack_average<T>(f[2 * y], f[2 * y + 1]) : pack2<T>(f[2 * y], f[2 * y + 1]);
     if (wide) {
 #pragma unroll
         for (int y = 0; y < 16; y += 8)

@@ -280,7 +280,7 @@ done:
         const int token = row / a.group, head = key_head * a.group + row % a.group;
         if (a.splits == 1) {
             *(uint32_t *)((T *)a.out + item * a.out_item + token * a.out_token + head * a.out_head + d) =
-                pack2<T>(f.x, f.y);
+                pack_average<T>(f.x, f.y);
             if (d == 0) a.lse[((int64_t)item * a.q_heads + head) * a.q_len + token] = lse;
         } else {
             const int64_t part = (int64_t)blockIdx.x * 16 + row;
@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(kFewJoinWarps * 32) k_attention_few_join(const
     const float inv = total > 0.0f ? 1.0f / total : (total == 0.0f ? 0.0f : total);
     if (mine)
         *(uint2 *)((T *)a.out + item * a.out_item + token * a.out_token + head * a.out_head + lane * 4) =
-            make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
+            make_uint2(pack_average<T>(o.x * inv, o.y * inv), pack_average<T>(o.z * inv, o.w * inv));
     if (lane == 0) a.lse[(item * a.q_heads + head) * a.q_len + token] = top + logf(total);
 }
 

@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kForwardThreads, 1) k_attention_forward(const 
                     float f[32];
 #pragma unroll
                     for (int y = 0; y < 32; ++y) f[y] = inv == 0.0f ? 0.0f : __uint_as_float(o[y]) * inv;
-                    store_results(out + x, partial + x, whole, a.wide, a.dim - x, f);
+                    store_results<T, true>(out + x, partial + x, whole, a.wide, a.dim - x, f);
                 }
             }
             if (store) {
@@ -455,8 +455,8 @@ __global__ void __launch_bounds__(kJoinBlock) k_attention_join(const __grid_cons
     for (int b = first; b <= last; ++b) add(2 * b, a.partial_lse[(int64_t)2 * b * kRows + r]);
     const float inv = total > 0.0f ? 1.0f / total : (total == 0.0f ? 0.0f : total);
     T *out = (T *)a.out + g.item * a.out_item + (int64_t)row * a.out_token + head * a.out_head + c;
-    *(uint4 *)out = make_uint4(pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv),
-                               pack2<T>(o[4] * inv, o[5] * inv), pack2<T>(o[6] * inv, o[7] * inv));
+    *(uint4 *)out = make_uint4(pack_average<T>(o[0] * inv, o[1] * inv), pack_average<T>(o[2] * inv, o[3] * inv),
+                               pack_average<T>(o[4] * inv, o[5] * inv), pack_average<T>(o[6] * inv, o[7] * inv));
     if (c == 0) a.lse[((int64_t)g.item * a.q_heads + head) * a.q_len + row] = top + logf(total);
 }
 
