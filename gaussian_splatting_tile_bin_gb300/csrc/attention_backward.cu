@@ -19,7 +19,7 @@
 //
 // Rounding.  p and ds are rounded to the storage type, as the tensor cores take
 // operands of one type.  f16 has few exponents: p is held times 2^14 (p <= 1), and
-// ds times a power of two that brings its bound, 2 |do| |v|, to f16's largest
+// ds times a power of two that brings its bound, |do| |v| / 2, to f16's largest
 // values; both powers are divided out of the float sums at the end.  A query's ds in
 // dq takes |do| of its own row, dk's sums over the queries the longest row of the
 // group's heads, and |v| is the longest row's of the same item and key head: rows
@@ -53,14 +53,16 @@ template <typename T>
 constexpr float kShiftP = std::is_same<T, __half>::value ? 16384.0f : 1.0f;
 
 // ds is held times this, a power of 2, where do's and v's rows are at most this long
-// (squared; of 16-bit values, so that their product is in float's range): |dp| and
-// |delta| are at most the lengths' product, so |ds| then stays below 2^15.
+// (squared; of 16-bit values, so that their product is in float's range).  |dp| is at
+// most the lengths' product B, and a row's ds = p ((1 - p) dp - sum of the others' p dp)
+// at most 2 B p (1 - p) <= B / 2 and some 2^-10 B of rounding: below 2^15.1 then.
+// So only a B of 2^16 or more, whose ds may pass f16's range, costs small ds bits.
 template <typename T>
 __device__ __forceinline__ float shift_ds(float dout_length2, float v_length2)
 {
     if constexpr (std::is_same<T, __half>::value) {
         const int exponent = __float_as_int(dout_length2 * v_length2) >> 23 & 255;
-        if (exponent != 0 && exponent != 255) return __int_as_float((127 + 13 - ((exponent - 127) >> 1)) << 23);
+        if (exponent != 0 && exponent != 255) return __int_as_float((127 + 15 - ((exponent - 127) >> 1)) << 23);
     }
     return 1.0f;
 }

@@ -77,3 +77,32 @@ def test_nan_stays_in_its_item(gsr, ctx, dtype):
     got = _run(gsr, ctx, q, k, v, dout)
     for a, b in zip(got, clean):
         assert torch.equal(a[::2], b[::2])
+
+
+@pytest.mark.parametrize("b,lq,lk,hq,hk,d,size", [(10, 2, 80, 4, 4, 104, 1.0), (6, 3, 282, 8, 4, 72, 3.0),
+                                                  (1, 1, 202, 3, 3, 72, 3.0), (1, 2, 258, 8, 2, 88, 8.0)])
+def test_products_below_the_range_keep_small_gradients(gsr, ctx, b, lq, lk, hq, hk, d, size):
+    """|dL/dout| |v| below 2^16 cannot take ds out of f16's range: ds is not scaled down."""
+    q, k, v, dout = _inputs(b, lq, lk, hq, hk, d, F16, 1)
+    q, v, dout = size * q, 30.0 * v, 10.0 * dout
+    want = ref.attention(q.double(), k.double(), v.double(), torch.ones(b, lk, dtype=torch.bool), 0.3, F16, dout.double())
+    for name, got in zip(("dq", "dk", "dv"), _run(gsr, ctx, q, k, v, dout, scale=0.3)[2:]):
+        ref.check(got, want[name], name)
+
+
+@pytest.mark.parametrize("lk", [2, 200])
+def test_ds_at_its_bound(gsr, ctx, lk):
+    """Two keys with half of the weight each and opposite values: ds is half of |dL/dout| |v|, 320,000."""
+    q = torch.full((1, 150, 1, 64), 1e-3).to(F16)
+    q[..., 0] = 0.125
+    k = torch.zeros(1, lk, 1, 64).to(F16)
+    k[:, 2:, :, 0] = -800.0
+    v = torch.full((1, lk, 1, 64), 100.0).to(F16)
+    v[:, 1] = -100.0
+    dout = torch.zeros(1, 150, 1, 64).to(F16)
+    dout[:, 7] = 100.0
+    valid = torch.ones(1, lk, dtype=torch.bool)
+    want = ref.attention(q.double(), k.double(), v.double(), valid, 1.0, F16, dout.double())
+    assert want["dk"][0].abs().max() == 40000
+    for name, got in zip(("dq", "dk", "dv"), _run(gsr, ctx, q, k, v, dout, scale=1.0)[2:]):
+        ref.check(got, want[name], name)
