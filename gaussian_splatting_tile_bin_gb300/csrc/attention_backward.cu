@@ -562,7 +562,6 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
             const float2 f2 = make_float2(f_dp, f_dp);
             if (any) {
                 const bool tail_tile = g.length - g.tile * kKeyTile < kKeyTile;
-                int left = a.q_len - g.begin % a.q_tiles * kRowTile;   // queries from this step's first on
                 for (int i = g.begin; i < g.end; ++i, n += 2, ++step) {
                     const float4 *lse4 = (const float4 *)(s_raw + (s_stat - raw) + n % S::kStages * S::kStatBytes) +
                                          column0 / 4;
@@ -586,19 +585,19 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) k_attention_grad_kv(const
                         p[y].x = exp2_fast(p[y].x);
                         p[y].y = exp2_fast(p[y].y);
                     }
-                    if (tail_tile && !live)
+                    // Rows behind the item's keys, and columns behind the last query, whose lse2
+                    // is -inf: zero rows that meet an infinite key as NaN.
+                    const bool dead = tail_tile && !live;
+                    if (dead || lse4[kColumnsEach / 4 - 1].w == -INFINITY) {
 #pragma unroll
-                        for (int y = 0; y < kColumnsEach / 2; ++y) p[y] = make_float2(0.0f, 0.0f);
-                    // The zero rows behind the last query meet an infinite key as NaN.
-                    if (left < column0 + kColumnsEach) {
-#pragma unroll
-                        for (int y = 0; y < kColumnsEach / 2; ++y) {
-                            if (column0 + 2 * y >= left) p[y].x = 0.0f;
-                            if (column0 + 2 * y + 1 >= left) p[y].y = 0.0f;
+                        for (int y = 0; y < kColumnsEach / 2; y += 2) {
+                            const float4 l = lse4[y / 2];
+                            if (dead || l.x == -INFINITY) p[y].x = 0.0f;
+                            if (dead || l.y == -INFINITY) p[y].y = 0.0f;
+                            if (dead || l.z == -INFINITY) p[y + 1].x = 0.0f;
+                            if (dead || l.w == -INFINITY) p[y + 1].y = 0.0f;
                         }
                     }
-                    left -= kRowTile;
-                    if (left <= 0) left = a.q_len;
 #pragma unroll
                     for (int y = 0; y < kColumnsEach / 2; ++y) packed[y] = pack2<T>(p[y].x, p[y].y);
                     __syncwarp();
