@@ -433,8 +433,9 @@ enum { GSR_ACT_NONE = 0, GSR_ACT_SILU = 1, GSR_ACT_GELU = 2 };
  * in float as means and centred squares, merged in a fixed order: the same bits
  * on every run.  positions = 0 writes nothing.
  * Errors: GSR_ERR_INVALID_ARG (null or misaligned arrays; a negative size;
- * groups < 1 or not dividing channels; channels > GSR_MAX_CHANNELS; eps not
- * finite or <= 0; unknown dtype or activation), GSR_ERR_OOM, GSR_ERR_CUDA. */
+ * groups < 1 or not dividing channels; channels > GSR_MAX_CHANNELS; samples above
+ * 2^20 or positions x channels above 2^40; eps not finite or <= 0; unknown dtype or
+ * activation), GSR_ERR_OOM, GSR_ERR_CUDA. */
 #define GSR_MAX_CHANNELS 4096
 typedef struct gsr_group_norm {
     int32_t dtype;
