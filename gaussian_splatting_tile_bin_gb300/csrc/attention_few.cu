@@ -44,6 +44,7 @@ struct FewArgs {
     int q_len, kv_len, q_heads, kv_heads, group, dim, splits;
     int k_item, k_head, v_item, v_head;
     float scale, scale_log2;
+    uint32_t zero;           // 0, which the compiler does not know
 };
 
 template <int HD>
@@ -225,16 +226,23 @@ __global__ void __launch_bounds__(kFewThreads) k_attention_few(const __grid_cons
             const uint32_t pair0 = live >> ((lane % 4) * 2), pair1 = pair0 >> 8;
             const uint32_t keep0 = (pair0 & 1 ? 0xffffu : 0u) | (pair0 & 2 ? 0xffff0000u : 0u);
             const uint32_t keep1 = (pair1 & 1 ? 0xffffu : 0u) | (pair1 & 2 ? 0xffff0000u : 0u);
+            uint32_t seen = 0;
 #pragma unroll
             for (int x = 0; x < HD / 16; ++x) {
                 uint32_t b[4];   // dimensions 0-7: keys 0-7 and 8-15, dimensions 8-15: the same
                 const int chunk = (x & 3) * 2 + v_chunk;
                 load_matrix4_across(b, at_v + (x >> 2) * S::kBlockBytes + v_row * 128 + ((chunk ^ (v_row & 7)) << 4));
+                seen |= b[0];
                 product16<T>(o[2 * x], p, b[0] & keep0, b[1] & keep1);
                 product16<T>(o[2 * x + 1], p, b[2] & keep0, b[3] & keep1);
             }
+            // The stage is free once its fragments are in registers.  K's are: the scores
+            // came from them.  V's need not be: their products may well run behind this
+            // point, and a warp that is held up beside another kernel's then reads the
+            // next tile.  So the arrival depends on what every load of V has brought.
+            fence_async();
             __syncwarp();
-            if (lane == 0) barrier_arrive(b_free + 8 * stage);
+            if (lane == 0) barrier_arrive(b_free + 8 * stage + (seen & a.zero));
         }
     }
 

@@ -102,3 +102,39 @@ def test_synchronize(gsr, ctx):
     ctx.synchronize(side)
     assert side.query() and _same(step(), got)
     ctx.synchronize()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_rows_beside_other_kernels(gsr, ctx, d):
+    """Few rows against more tiles than their ring has stages, on branches of a graph beside
+    kernels that fill the SMs: warps that are held up at any point."""
+    g = torch.Generator().manual_seed(d)
+    few = []
+    for lk in (300, 450, 700):
+        q = torch.randn(3, 3, 4, d, generator=g).bfloat16().cuda()
+        k, v = (torch.randn(3, lk, 4, d, generator=g).bfloat16().cuda() for _ in range(2))
+        few.append((q, k, v, gsr.cross_attention_forward(ctx, q, k, v)))
+    big = _step(gsr, ctx, 300, 2000, 3, torch.bfloat16)
+    want = big()
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in few]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        got = [[] for _ in few]
+        for side in sides:
+            side.wait_stream(main)
+        heavy = [big(), big()]
+        for (q, k, v, _), side, outs in zip(few, sides, got):
+            with torch.cuda.stream(side):
+                outs += [gsr.cross_attention_forward(ctx, q, k, v) for _ in range(20)]
+        for side in sides:
+            main.wait_stream(side)
+    for _ in range(40):
+        for outs in got:
+            for out, _ in outs:
+                out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(_same(one, f[3]) for f, outs in zip(few, got) for one in outs)
+        assert all(_same(h, want) for h in heavy)
