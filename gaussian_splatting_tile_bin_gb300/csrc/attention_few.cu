@@ -184,12 +184,14 @@ __global__ void __launch_bounds__(kFewThreads) k_attention_few(const __grid_cons
             valid = takes_part(i + 1);
             barrier_wait_warp(b_full + 8 * stage, n / kStages & 1, guard);
             const uint32_t at_k = ring + stage * S::kStageBytes, at_v = at_k + S::kTileBytes;
+            uint32_t seen = 0;
             float s[2][4] = {};
 #pragma unroll
             for (int k = 0; k < HD / 16; ++k) {
                 uint32_t b[4];   // keys 0-7: two chunks of 8 dimensions, keys 8-15: two
                 const int chunk = (k & 3) * 2 + k_chunk;
                 load_matrix4(b, at_k + (k >> 2) * S::kBlockBytes + k_row * 128 + ((chunk ^ (k_row & 7)) << 4));
+                seen |= b[0];
                 product16<T>(s[0], q[k], b[0], b[1]);
                 product16<T>(s[1], q[k], b[2], b[3]);
             }
@@ -226,7 +228,6 @@ __global__ void __launch_bounds__(kFewThreads) k_attention_few(const __grid_cons
             const uint32_t pair0 = live >> ((lane % 4) * 2), pair1 = pair0 >> 8;
             const uint32_t keep0 = (pair0 & 1 ? 0xffffu : 0u) | (pair0 & 2 ? 0xffff0000u : 0u);
             const uint32_t keep1 = (pair1 & 1 ? 0xffffu : 0u) | (pair1 & 2 ? 0xffff0000u : 0u);
-            uint32_t seen = 0;
 #pragma unroll
             for (int x = 0; x < HD / 16; ++x) {
                 uint32_t b[4];   // dimensions 0-7: keys 0-7 and 8-15, dimensions 8-15: the same
@@ -236,10 +237,10 @@ __global__ void __launch_bounds__(kFewThreads) k_attention_few(const __grid_cons
                 product16<T>(o[2 * x], p, b[0] & keep0, b[1] & keep1);
                 product16<T>(o[2 * x + 1], p, b[2] & keep0, b[3] & keep1);
             }
-            // The stage is free once its fragments are in registers.  K's are: the scores
-            // came from them.  V's need not be: their products may well run behind this
-            // point, and a warp that is held up beside another kernel's then reads the
-            // next tile.  So the arrival depends on what every load of V has brought.
+            // The stage is free once its fragments are in registers, which nothing here
+            // waits for: the products may well run behind this point, and a warp that is
+            // held up beside another kernel's then reads the next tile.  So the arrival
+            // depends on what every load has brought.
             fence_async();
             __syncwarp();
             if (lane == 0) barrier_arrive(b_free + 8 * stage + (seen & a.zero));
