@@ -184,14 +184,12 @@ __global__ void __launch_bounds__(kFewThreads) k_attention_few(const __grid_cons
             valid = takes_part(i + 1);
             barrier_wait_warp(b_full + 8 * stage, n / kStages & 1, guard);
             const uint32_t at_k = ring + stage * S::kStageBytes, at_v = at_k + S::kTileBytes;
-            uint32_t seen = 0;
             float s[2][4] = {};
 #pragma unroll
             for (int k = 0; k < HD / 16; ++k) {
                 uint32_t b[4];   // keys 0-7: two chunks of 8 dimensions, keys 8-15: two
                 const int chunk = (k & 3) * 2 + k_chunk;
                 load_matrix4(b, at_k + (k >> 2) * S::kBlockBytes + k_row * 128 + ((chunk ^ (k_row & 7)) << 4));
-                seen |= b[0];
                 product16<T>(s[0], q[k], b[0], b[1]);
                 product16<T>(s[1], q[k], b[2], b[3]);
             }
@@ -228,6 +226,7 @@ __global__ void __launch_bounds__(kFewThreads) k_attention_few(const __grid_cons
             const uint32_t pair0 = live >> ((lane % 4) * 2), pair1 = pair0 >> 8;
             const uint32_t keep0 = (pair0 & 1 ? 0xffffu : 0u) | (pair0 & 2 ? 0xffff0000u : 0u);
             const uint32_t keep1 = (pair1 & 1 ? 0xffffu : 0u) | (pair1 & 2 ? 0xffff0000u : 0u);
+            uint32_t seen = p[0];   // of all of K
 #pragma unroll
             for (int x = 0; x < HD / 16; ++x) {
                 uint32_t b[4];   // dimensions 0-7: keys 0-7 and 8-15, dimensions 8-15: the same
