@@ -265,8 +265,16 @@ __device__ __forceinline__ void store_results(T *out, float *partial, bool whole
     }
     uint32_t w[16];
 #pragma unroll
-    for (int y = 0; y < 16; ++y)
-        w[y] = AVERAGE ? pack_average<T>(f[2 * y], f[2 * y + 1]) : pack2<T>(f[2 * y], f[2 * y + 1]);
+    for (int y = 0; y < 16; ++y) w[y] = pack2<T>(f[2 * y], f[2 * y + 1]);
+    if constexpr (AVERAGE && std::is_same<T, __half>::value) {
+        __half2 top = __habs2(*(const __half2 *)&w[0]);
+#pragma unroll
+        for (int y = 1; y < 16; ++y) top = __hmax2(top, __habs2(*(const __half2 *)&w[y]));
+        if (__hisinf(__low2half(top)) || __hisinf(__high2half(top))) {
+#pragma unroll
+            for (int y = 0; y < 16; ++y) w[y] = pack_average<T>(f[2 * y], f[2 * y + 1]);
+        }
+    }
     if (wide) {
 #pragma unroll
         for (int y = 0; y < 16; y += 8)
