@@ -26,10 +26,10 @@
 // that never meet in a product do not cost each other bits.
 //
 // Bound by the tensor cores: 4,864 queries x 8,192 keys x 16 heads in bf16 take
-// 643 us for all three gradients at head_dim 128 (1,270 TFLOP/s on the five
+// 634 to 643 us for all three gradients at head_dim 128 (1,270 TFLOP/s on the five
 // products a gradient cannot do without, 1,780 on the seven done, 93% of a large
-// library product's rate) and 470 us at 64 (870 and 1,215; by these times a product
-// with 64 columns takes that of one with 128), in f16 675 and 481.  At 4 heads the tensor pipe is active
+// library product's rate) and 468 us at 64 (870 and 1,220; by these times a product
+// with 64 columns takes that of one with 128), in f16 662 to 675 and 484.  At 4 heads the tensor pipe is active
 // 77 and 73% of the two kernels, starts and ends included; DRAM reads are the
 // inputs' own 27 MB.  Four warpgroups instead of two take 651 and 477 us; Q and dO
 // of the dq kernel in tensor memory, statistics read before the scores' wait and
