@@ -123,6 +123,7 @@ int Workspace::mark()
     if (int rc = cuda_check(ctx, cudaEventRecord(*event, stream), "workspace event")) return rc;
     if (capture == cudaStreamCaptureStatusNone) {
         ctx->work_pending = true;
+        ctx->work_stream = ~0ull;   // no stream's: the next call waits, should the number not be had
         return cuda_check(ctx, cudaStreamGetId(stream, &ctx->work_stream), "workspace stream");
     }
     return GSR_OK;

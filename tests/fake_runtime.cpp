@@ -44,7 +44,7 @@ std::set<uintptr_t> held;                // by captured launches
 void *status = nullptr;
 int next_uid, next_address, host_allocations, events, conflicts, freed_while_held, pulled_in, launches;
 unsigned long long next_capture;
-int launch_to_fail, map_to_fail;
+int launch_to_fail, map_to_fail, number_to_fail;
 
 Stream &at(void *handle)
 {
@@ -106,7 +106,7 @@ void fake_reset()
     uses.clear();
     held.clear();
     host_allocations = events = 0;
-    conflicts = freed_while_held = pulled_in = launches = launch_to_fail = map_to_fail = 0;
+    conflicts = freed_while_held = pulled_in = launches = launch_to_fail = map_to_fail = number_to_fail = 0;
 }
 int fake_conflicts() { return conflicts; }
 int fake_freed_while_held() { return freed_while_held; }
@@ -116,6 +116,7 @@ int fake_live() { return (int)allocations.size() + host_allocations + events; }
 int fake_allocations() { return (int)allocations.size(); }
 void fake_fail_launch(int n) { launch_to_fail = n; }
 void fake_fail_map(int n) { map_to_fail = n; }
+void fake_fail_number(int n) { number_to_fail = n; }
 void fake_set_status() { *(uint32_t *)status = 1; }
 // Another stream under a handle whose stream was destroyed.
 void fake_new_stream(void *handle) { streams.erase(handle); }
@@ -205,8 +206,10 @@ cudaError_t cudaStreamGetCaptureInfo(cudaStream_t s, cudaStreamCaptureStatus *to
 }
 cudaError_t cudaStreamGetId(cudaStream_t s, unsigned long long *id)
 {
+    if (at(s).capture) return cudaErrorStreamCaptureUnsupported;
+    if (number_to_fail > 0 && --number_to_fail == 0) return cudaErrorUnknown;
     *id = at(s).uid;
-    return at(s).capture ? cudaErrorStreamCaptureUnsupported : cudaSuccess;
+    return cudaSuccess;
 }
 
 cudaError_t cudaEventCreateWithFlags(cudaEvent_t *e, unsigned)

@@ -164,7 +164,7 @@ def _uses():
 
 
 @pytest.mark.parametrize("call", list(_uses()))
-@pytest.mark.parametrize("fail", ["fake_fail_launch", "fake_fail_map"])
+@pytest.mark.parametrize("fail", ["fake_fail_launch", "fake_fail_map", "fake_fail_number"])
 def test_a_failed_call_leaves_its_mark(lib, ctx, call, fail):
     """A call that fails after some of its launches: what it launched is ordered before the next use."""
     assert call(lib, ctx, ONE) == OK
@@ -206,3 +206,13 @@ def test_a_wait_that_ran_out_is_reported(lib, ctx):
     lib.fake_set_status()                            # by the last call of a program
     assert lib.gsr_synchronize(ctx, ONE) == CUDA
     assert lib.gsr_synchronize(ctx, ONE) == OK
+
+
+@pytest.mark.parametrize("call", [attention, norm])
+def test_a_stream_whose_number_is_not_had(lib, ctx, call):
+    """The call's own use is marked all the same, and the stream before it is not taken for its."""
+    assert call(lib, ctx, ONE) == OK
+    lib.fake_fail_number(2)              # asked before and after a call's launches
+    assert call(lib, ctx, TWO) == CUDA
+    assert call(lib, ctx, ONE) == OK
+    assert lib.fake_conflicts() == 0
