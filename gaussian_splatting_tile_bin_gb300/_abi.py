@@ -44,7 +44,7 @@ class _Camera(ctypes.Structure):
     _fields_ = [("v", ctypes.c_float * CAMERA_FIELDS)]
 
 
-# gsr_group_norm, gsr_heads, gsr_rotary and gsr_attention, packed per call: an
+# gsr_group_norm, gsr_heads, gsr_rotary, gsr_attention, gsr_layer_norm and gsr_recurrence, packed per call: an
 # order of magnitude quicker than filling ctypes structures, which these calls of
 # a few microseconds would notice.
 MAX_AXES = 4
@@ -54,6 +54,9 @@ ROTARY = struct.Struct("@12iq")        # dtype, batch, tokens, heads, head_dim, 
                                        # positions_int, positions_batch_stride
 ATTENTION = struct.Struct("@7if2P")    # dtype, batch, q_len, kv_len, q_heads, kv_heads, head_dim, scale,
                                        # kv_lengths, key_mask
+LAYER_NORM = struct.Struct("@5if")     # dtype, batch, tokens, heads, channels, eps
+RECURRENCE = struct.Struct("@5iP")     # dtype, batch, tokens, channels, reverse, lengths
+RECURRENCE_BLOCK = 64                  # GSR_RECURRENCE_BLOCK
 
 
 class _BinStats(ctypes.Structure):
@@ -103,7 +106,9 @@ def _load():
     lib.gsr_peak_kernel.restype = ctypes.c_int
     for name, pointers in (("gsr_group_norm_forward", 9), ("gsr_group_norm_backward", 12), ("gsr_rotary_forward", 7),
                            ("gsr_rotary_backward", 7), ("gsr_cross_attention_forward", 8),
-                           ("gsr_cross_attention_backward", 12)):
+                           ("gsr_cross_attention_backward", 12), ("gsr_layer_norm_forward", 11),
+                           ("gsr_layer_norm_backward", 12), ("gsr_gated_recurrence_forward", 10),
+                           ("gsr_gated_recurrence_backward", 13)):
         getattr(lib, name).argtypes = [P] * pointers
         getattr(lib, name).restype = ctypes.c_int
     return lib
@@ -639,3 +644,154 @@ def cross_attention_backward(ctx: Context, q: torch.Tensor, k: torch.Tensor, v: 
         _array(lse, "lse", _F32, (shape[0], shape[2], shape[1]), index),
         _heads(dl_dout, "dl_dout", dtype, shape, index), at_dq, at_dk, at_dv, _raw_stream(stream, index)))
     return dl_dq, dl_dk, dl_dv
+
+
+def _rows(t, name, dtype, shape, index):
+    """A packed gsr_heads of a tensor [..., channels] with one to three leading
+    dimensions, any strides but a contiguous last dimension."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index):
+        _refuse(t, name, dtype, shape, index)
+    strides = t.stride()
+    if strides[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    n = len(strides)
+    return HEADS.pack(t.data_ptr(), strides[0] if n > 2 else 0, strides[1] if n > 2 else strides[0],
+                      strides[2] if n > 3 else 0)
+
+
+def _rows_out(t, name, dtype, shape, index, device, stream, like=None):
+    """An output [..., channels], made if None, and its packed gsr_heads."""
+    if t is None:
+        t = _new(shape, dtype, device, stream, like)
+    return t, _rows(t, name, dtype, shape, index)
+
+
+def _layer_desc(x, eps):
+    shape = x.shape
+    n = len(shape)
+    if not 2 <= n <= 4:
+        raise ValueError("x must have shape [tokens, channels], [batch, tokens, channels] or [batch, tokens, heads, "
+                         f"channels], got {tuple(shape)}")
+    return LAYER_NORM.pack(DTYPES[x.dtype], shape[0] if n > 2 else 1, shape[1] if n > 2 else shape[0],
+                           shape[2] if n > 3 else 1, shape[-1], eps)
+
+
+def layer_norm_forward(ctx: Context, x: torch.Tensor, weight=None, bias=None, residual=None, eps: float = 1e-5,
+                       out=None, total=None, mean=None, rstd=None, stream=None):
+    """Layer norm over the channels of x [tokens, channels], [batch, tokens, channels]
+    or [batch, tokens, heads, channels] (f32, bf16 or f16; any strides with a
+    contiguous last dimension; weight and bias [channels] f32 or None), or of
+    total = x + residual.  Returns (out, total, mean, rstd), total being x without a
+    residual and the last two [...] f32, for the backward.  out and total may be x or
+    residual, but not each other."""
+    index = _on(ctx, x, "x", DTYPES)
+    dtype, shape, dev = x.dtype, x.shape, x.device
+    desc = _layer_desc(x, eps)
+    channels, stats = shape[-1:], shape[:-1]
+    at_x = _rows(x, "x", dtype, shape, index)
+    out, at_out = _rows_out(out, "out", dtype, shape, index, dev, stream, x)
+    at_residual = at_total = None
+    if residual is not None:
+        at_residual = _rows(residual, "residual", dtype, shape, index)
+        total, at_total = _rows_out(total, "total", dtype, shape, index, dev, stream, x)
+    elif total is not None:
+        raise ValueError("total is x itself without a residual")
+    else:
+        total = x
+    mean, at_mean = _array_out(mean, "mean", _F32, stats, index, dev, stream)
+    rstd, at_rstd = _array_out(rstd, "rstd", _F32, stats, index, dev, stream)
+    ctx._check(lib.gsr_layer_norm_forward(
+        ctx._h, desc, at_x, at_residual, None if weight is None else _array(weight, "weight", _F32, channels, index),
+        None if bias is None else _array(bias, "bias", _F32, channels, index), at_out, at_total, at_mean, at_rstd,
+        _raw_stream(stream, index)))
+    return out, total, mean, rstd
+
+
+def layer_norm_backward(ctx: Context, dl_dout: torch.Tensor, total: torch.Tensor, weight, mean: torch.Tensor,
+                        rstd: torch.Tensor, dl_dtotal=None, dl_dx=None, dl_dweight=None, dl_dbias=None, stream=None):
+    """Returns (dL/dx as total, dL/dweight [channels] f32, dL/dbias [channels] f32) for
+    dL/dout and, where total goes on past the norm, dL/dtotal; with the forward's
+    total, weight, mean and rstd.  dL/dx is the residual's gradient too.  dl_dx may be
+    dl_dout or dl_dtotal."""
+    index = _on(ctx, total, "total", DTYPES)
+    dtype, shape, dev = total.dtype, total.shape, total.device
+    desc = _layer_desc(total, 1.0)
+    channels, stats = shape[-1:], shape[:-1]
+    dl_dx, at_dx = _rows_out(dl_dx, "dl_dx", dtype, shape, index, dev, stream, total)
+    dl_dweight, at_dweight = _array_out(dl_dweight, "dl_dweight", _F32, channels, index, dev, stream)
+    dl_dbias, at_dbias = _array_out(dl_dbias, "dl_dbias", _F32, channels, index, dev, stream)
+    ctx._check(lib.gsr_layer_norm_backward(
+        ctx._h, desc, _rows(dl_dout, "dl_dout", dtype, shape, index), _rows(total, "total", dtype, shape, index),
+        None if weight is None else _array(weight, "weight", _F32, channels, index),
+        _array(mean, "mean", _F32, stats, index), _array(rstd, "rstd", _F32, stats, index),
+        None if dl_dtotal is None else _rows(dl_dtotal, "dl_dtotal", dtype, shape, index), at_dx, at_dweight, at_dbias,
+        _raw_stream(stream, index)))
+    return dl_dx, dl_dweight, dl_dbias
+
+
+def _recurrence(ctx, x, forget, gate, lengths, reverse):
+    """The packed description and x, forget and gate; the device's index."""
+    index = _on(ctx, x, "x", DTYPES)
+    dtype, shape = x.dtype, x.shape
+    if len(shape) != 3:
+        raise ValueError(f"x must have shape [batch, tokens, channels], got {tuple(shape)}")
+    batch, tokens, channels = shape
+    at_lengths = 0 if lengths is None else _array(lengths, "lengths", torch.int32, (batch,), index)
+    desc = RECURRENCE.pack(DTYPES[dtype], batch, tokens, channels, bool(reverse), at_lengths)
+    return index, desc, _rows(x, "x", dtype, shape, index), _rows(forget, "forget", dtype, shape, index), \
+        None if gate is None else _rows(gate, "gate", dtype, shape, index)
+
+
+def gated_recurrence_forward(ctx: Context, x: torch.Tensor, forget: torch.Tensor, gate=None, initial=None,
+                             lengths=None, reverse: bool = False, keep: bool = True, out=None, final=None, states=None,
+                             stream=None):
+    """h_t = a_t h_(t-1) + (1 - a_t) x_t with a = sigmoid(forget) over the tokens of
+    x, forget [batch, tokens, channels] (f32, bf16 or f16; views with a contiguous
+    last dimension), and out = h silu(gate), or h without a gate.  `reverse` runs from
+    the last token to the first; item b has lengths[b] tokens (int32, all if None),
+    and out is 0 behind them.  h starts at initial [batch, channels] f32 (0 if None).
+    Returns (out, final [batch, channels] f32, states): the last h, to go on from,
+    and what the backward needs (None with keep=False).  out may be x, final may be
+    initial."""
+    index, desc, at_x, at_forget, at_gate = _recurrence(ctx, x, forget, gate, lengths, reverse)
+    dtype, shape, dev = x.dtype, x.shape, x.device
+    batch, tokens, channels = shape
+    state = (batch, channels)
+    out, at_out = _rows_out(out, "out", dtype, shape, index, dev, stream)
+    final, at_final = _array_out(final, "final", _F32, state, index, dev, stream)
+    at_states = None
+    if keep:
+        blocks = (batch, -(-tokens // RECURRENCE_BLOCK), channels)
+        states, at_states = _array_out(states, "states", _F32, blocks, index, dev, stream)
+    elif states is not None:
+        raise ValueError("states are written with keep=True only")
+    ctx._check(lib.gsr_gated_recurrence_forward(
+        ctx._h, desc, at_x, at_forget, at_gate, None if initial is None else _array(initial, "initial", _F32, state, index),
+        at_out, at_final, at_states, _raw_stream(stream, index)))
+    return out, final, states
+
+
+def gated_recurrence_backward(ctx: Context, dl_dout: torch.Tensor, x: torch.Tensor, forget: torch.Tensor, gate,
+                              states: torch.Tensor, dl_dfinal=None, lengths=None, reverse: bool = False, dl_dx=None,
+                              dl_dforget=None, dl_dgate=None, dl_dinitial=None, stream=None):
+    """Returns (dL/dx, dL/dforget, dL/dgate, dL/dinitial [batch, channels] f32) for
+    dL/dout and, where the last state went on, dL/dfinal; with the forward's arguments
+    and states.  dL/dgate is None without a gate.  dl_dx may be dl_dout."""
+    index, desc, at_x, at_forget, at_gate = _recurrence(ctx, x, forget, gate, lengths, reverse)
+    dtype, shape, dev = x.dtype, x.shape, x.device
+    batch, tokens, channels = shape
+    state = (batch, channels)
+    dl_dx, at_dx = _rows_out(dl_dx, "dl_dx", dtype, shape, index, dev, stream)
+    dl_dforget, at_dforget = _rows_out(dl_dforget, "dl_dforget", dtype, shape, index, dev, stream)
+    at_dgate = None
+    if gate is not None:
+        dl_dgate, at_dgate = _rows_out(dl_dgate, "dl_dgate", dtype, shape, index, dev, stream)
+    elif dl_dgate is not None:
+        raise ValueError("dl_dgate has no gate")
+    dl_dinitial, at_dinitial = _array_out(dl_dinitial, "dl_dinitial", _F32, state, index, dev, stream)
+    ctx._check(lib.gsr_gated_recurrence_backward(
+        ctx._h, desc, _rows(dl_dout, "dl_dout", dtype, shape, index), at_x, at_forget, at_gate,
+        _array(states, "states", _F32, (batch, -(-tokens // RECURRENCE_BLOCK), channels), index),
+        None if dl_dfinal is None else _array(dl_dfinal, "dl_dfinal", _F32, state, index), at_dx, at_dforget, at_dgate,
+        at_dinitial, _raw_stream(stream, index)))
+    return dl_dx, dl_dforget, dl_dgate, dl_dinitial

@@ -501,6 +501,52 @@ int check_key(gsr_ctx *ctx, const gsr_attention *d, const gsr_heads *t, const ch
     return check_heads(ctx, t, name, d->batch, d->kv_len, d->kv_heads, 16, 8, output);
 }
 
+int check_layer_norm(gsr_ctx *ctx, const gsr_layer_norm *d, const float *weight, const float *mean, const float *rstd)
+{
+    if (!d) return fail(ctx, GSR_ERR_INVALID_ARG, "desc is NULL");
+    if (!known_dtype(d->dtype)) return fail(ctx, GSR_ERR_INVALID_ARG, "unknown dtype");
+    if (d->batch < 0 || d->tokens < 0 || d->heads < 0) return fail(ctx, GSR_ERR_INVALID_ARG, "a size is negative");
+    if (d->channels < 1 || d->channels > GSR_MAX_NORM_CHANNELS)
+        return fail(ctx, GSR_ERR_INVALID_ARG, "channels outside [1, GSR_MAX_NORM_CHANNELS]");
+    if (d->heads > GSR_MAX_HEADS) return fail(ctx, GSR_ERR_INVALID_ARG, "heads above GSR_MAX_HEADS");
+    const int64_t tokens = (int64_t)d->batch * d->tokens;
+    if (tokens > GSR_MAX_TOKENS) return fail(ctx, GSR_ERR_INVALID_ARG, "batch * tokens above GSR_MAX_TOKENS");
+    if (tokens * d->heads > 0x7fffffff) return fail(ctx, GSR_ERR_INVALID_ARG, "2^31 rows or more");
+    if (!std::isfinite(d->eps) || !(d->eps > 0.0f))
+        return fail(ctx, GSR_ERR_INVALID_ARG, "eps must be finite and > 0");
+    if (tokens * d->heads > 0 && (!mean || !rstd)) return fail(ctx, GSR_ERR_INVALID_ARG, "mean or rstd is NULL");
+    if (!aligned(weight, 4) || !aligned(mean, 4) || !aligned(rstd, 4))
+        return fail(ctx, GSR_ERR_INVALID_ARG, "an array is not aligned to its element");
+    return GSR_OK;
+}
+
+int check_row(gsr_ctx *ctx, const gsr_layer_norm *d, const gsr_heads *t, const char *name, bool output)
+{
+    return check_heads(ctx, t, name, d->batch, d->tokens, d->heads, element_size(d->dtype), 1, output);
+}
+
+int check_recurrence(gsr_ctx *ctx, const gsr_recurrence *d)
+{
+    if (!d) return fail(ctx, GSR_ERR_INVALID_ARG, "desc is NULL");
+    if (!known_dtype(d->dtype)) return fail(ctx, GSR_ERR_INVALID_ARG, "unknown dtype");
+    if (d->batch < 0 || d->tokens < 0) return fail(ctx, GSR_ERR_INVALID_ARG, "a size is negative");
+    if (d->channels < 1 || d->channels > GSR_MAX_RECURRENCE_CHANNELS)
+        return fail(ctx, GSR_ERR_INVALID_ARG, "channels outside [1, GSR_MAX_RECURRENCE_CHANNELS]");
+    if (d->batch > (1 << 16) || d->tokens > (1 << 24) || (int64_t)d->batch * d->tokens > GSR_MAX_TOKENS)
+        return fail(ctx, GSR_ERR_INVALID_ARG, "batch above 2^16, tokens above 2^24 or their product above GSR_MAX_TOKENS");
+    // The kernels number blocks of a batch item, tokens and channels.
+    const int64_t blocks = ((int64_t)d->tokens + GSR_RECURRENCE_BLOCK - 1) / GSR_RECURRENCE_BLOCK + 1;
+    if ((int64_t)d->batch * blocks > 0x7fffffff / ((d->channels + 31) / 32))
+        return fail(ctx, GSR_ERR_INVALID_ARG, "2^31 blocks of 64 tokens x 32 channels or more");
+    if (!aligned(d->lengths, 4)) return fail(ctx, GSR_ERR_INVALID_ARG, "lengths must be 4-byte aligned");
+    return GSR_OK;
+}
+
+int check_tokens(gsr_ctx *ctx, const gsr_recurrence *d, const gsr_heads *t, const char *name, bool output)
+{
+    return check_heads(ctx, t, name, d->batch, d->tokens, 1, element_size(d->dtype), 1, output);
+}
+
 }  // namespace
 
 extern "C" {
@@ -621,6 +667,111 @@ int gsr_cross_attention_backward(gsr_ctx *ctx, const gsr_attention *desc, const 
     if (int rc = gsr::check_status(ctx)) return rc;
     return gsr::cross_attention_backward(ctx, *desc, *q, *k, *v, *out, lse, *dl_dout, *dl_dq, *dl_dk, *dl_dv,
                                          (cudaStream_t)stream);
+}
+
+int gsr_layer_norm_forward(gsr_ctx *ctx, const gsr_layer_norm *desc, const gsr_heads *x, const gsr_heads *residual,
+                           const float *weight, const float *bias, const gsr_heads *out, const gsr_heads *total,
+                           float *mean, float *rstd, void *stream)
+{
+    gsr::Range range("gsr_layer_norm_forward");
+    if (!ctx) return GSR_ERR_INVALID_ARG;
+    ctx->err.clear();
+    if (int rc = check_layer_norm(ctx, desc, weight, mean, rstd)) return rc;
+    if (!aligned(bias, 4)) return fail(ctx, GSR_ERR_INVALID_ARG, "an array is not aligned to its element");
+    if ((residual == nullptr) != (total == nullptr))
+        return fail(ctx, GSR_ERR_INVALID_ARG, "residual and total go together");
+    if (int rc = check_row(ctx, desc, x, "x", false)) return rc;
+    if (int rc = check_row(ctx, desc, out, "out", true)) return rc;
+    if (residual) {
+        if (int rc = check_row(ctx, desc, residual, "residual", false)) return rc;
+        if (int rc = check_row(ctx, desc, total, "total", true)) return rc;
+    }
+    if (desc->batch == 0 || desc->tokens == 0 || desc->heads == 0) return GSR_OK;
+    if (total && total->data == out->data) return fail(ctx, GSR_ERR_INVALID_ARG, "out and total are the same array");
+    DeviceGuard g(ctx->device);
+    if (!g.ok) return fail(ctx, GSR_ERR_CUDA, "cannot select the context's device");
+    if (int rc = gsr::check_status(ctx)) return rc;
+    return gsr::layer_norm_forward(ctx, *desc, *x, residual, weight, bias, *out, total, mean, rstd,
+                                   (cudaStream_t)stream);
+}
+
+int gsr_layer_norm_backward(gsr_ctx *ctx, const gsr_layer_norm *desc, const gsr_heads *dl_dout,
+                            const gsr_heads *total, const float *weight, const float *mean, const float *rstd,
+                            const gsr_heads *dl_dtotal, const gsr_heads *dl_dx, float *dl_dweight, float *dl_dbias,
+                            void *stream)
+{
+    gsr::Range range("gsr_layer_norm_backward");
+    if (!ctx) return GSR_ERR_INVALID_ARG;
+    ctx->err.clear();
+    if (int rc = check_layer_norm(ctx, desc, weight, mean, rstd)) return rc;
+    if (!aligned(dl_dweight, 4) || !aligned(dl_dbias, 4))
+        return fail(ctx, GSR_ERR_INVALID_ARG, "an array is not aligned to its element");
+    if (int rc = check_row(ctx, desc, dl_dout, "dl_dout", false)) return rc;
+    if (int rc = check_row(ctx, desc, total, "total", false)) return rc;
+    if (dl_dtotal)
+        if (int rc = check_row(ctx, desc, dl_dtotal, "dl_dtotal", false)) return rc;
+    if (int rc = check_row(ctx, desc, dl_dx, "dl_dx", true)) return rc;
+    DeviceGuard g(ctx->device);
+    if (!g.ok) return fail(ctx, GSR_ERR_CUDA, "cannot select the context's device");
+    if (int rc = gsr::check_status(ctx)) return rc;
+    return gsr::layer_norm_backward(ctx, *desc, *dl_dout, *total, weight, mean, rstd, dl_dtotal, *dl_dx, dl_dweight,
+                                    dl_dbias, (cudaStream_t)stream);
+}
+
+int gsr_gated_recurrence_forward(gsr_ctx *ctx, const gsr_recurrence *desc, const gsr_heads *x,
+                                 const gsr_heads *forget, const gsr_heads *gate, const float *initial,
+                                 const gsr_heads *out, float *final, float *states, void *stream)
+{
+    gsr::Range range("gsr_gated_recurrence_forward");
+    if (!ctx) return GSR_ERR_INVALID_ARG;
+    ctx->err.clear();
+    if (int rc = check_recurrence(ctx, desc)) return rc;
+    if (int rc = check_tokens(ctx, desc, x, "x", false)) return rc;
+    if (int rc = check_tokens(ctx, desc, forget, "forget", false)) return rc;
+    if (gate)
+        if (int rc = check_tokens(ctx, desc, gate, "gate", false)) return rc;
+    if (int rc = check_tokens(ctx, desc, out, "out", true)) return rc;
+    if (desc->batch == 0) return GSR_OK;
+    if (!final) return fail(ctx, GSR_ERR_INVALID_ARG, "final is NULL");
+    if (!aligned(initial, 4) || !aligned(final, 4) || !aligned(states, 4))
+        return fail(ctx, GSR_ERR_INVALID_ARG, "an array is not aligned to its element");
+    DeviceGuard g(ctx->device);
+    if (!g.ok) return fail(ctx, GSR_ERR_CUDA, "cannot select the context's device");
+    if (int rc = gsr::check_status(ctx)) return rc;
+    return gsr::gated_recurrence_forward(ctx, *desc, *x, *forget, gate, initial, *out, final, states,
+                                         (cudaStream_t)stream);
+}
+
+int gsr_gated_recurrence_backward(gsr_ctx *ctx, const gsr_recurrence *desc, const gsr_heads *dl_dout,
+                                  const gsr_heads *x, const gsr_heads *forget, const gsr_heads *gate,
+                                  const float *states, const float *dl_dfinal, const gsr_heads *dl_dx,
+                                  const gsr_heads *dl_dforget, const gsr_heads *dl_dgate, float *dl_dinitial,
+                                  void *stream)
+{
+    gsr::Range range("gsr_gated_recurrence_backward");
+    if (!ctx) return GSR_ERR_INVALID_ARG;
+    ctx->err.clear();
+    if (int rc = check_recurrence(ctx, desc)) return rc;
+    if ((gate == nullptr) != (dl_dgate == nullptr))
+        return fail(ctx, GSR_ERR_INVALID_ARG, "gate and dl_dgate go together");
+    if (int rc = check_tokens(ctx, desc, dl_dout, "dl_dout", false)) return rc;
+    if (int rc = check_tokens(ctx, desc, x, "x", false)) return rc;
+    if (int rc = check_tokens(ctx, desc, forget, "forget", false)) return rc;
+    if (int rc = check_tokens(ctx, desc, dl_dx, "dl_dx", true)) return rc;
+    if (int rc = check_tokens(ctx, desc, dl_dforget, "dl_dforget", true)) return rc;
+    if (gate) {
+        if (int rc = check_tokens(ctx, desc, gate, "gate", false)) return rc;
+        if (int rc = check_tokens(ctx, desc, dl_dgate, "dl_dgate", true)) return rc;
+    }
+    if (desc->batch == 0) return GSR_OK;
+    if (desc->tokens > 0 && !states) return fail(ctx, GSR_ERR_INVALID_ARG, "states is NULL");
+    if (!aligned(states, 4) || !aligned(dl_dfinal, 4) || !aligned(dl_dinitial, 4))
+        return fail(ctx, GSR_ERR_INVALID_ARG, "an array is not aligned to its element");
+    DeviceGuard g(ctx->device);
+    if (!g.ok) return fail(ctx, GSR_ERR_CUDA, "cannot select the context's device");
+    if (int rc = gsr::check_status(ctx)) return rc;
+    return gsr::gated_recurrence_backward(ctx, *desc, *dl_dout, *x, *forget, gate, states, dl_dfinal, *dl_dx,
+                                          *dl_dforget, dl_dgate, dl_dinitial, (cudaStream_t)stream);
 }
 
 }  // extern "C"

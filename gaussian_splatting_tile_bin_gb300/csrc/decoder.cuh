@@ -1,5 +1,5 @@
 // decoder.cuh -- the decoder's operators (group norm, rotary positions, cross
-// attention): their host sides, and what they share: element types, vector access,
+// attention, layer norm, gated recurrence): their host sides, and what they share: element types, vector access,
 // launches with dynamic shared memory, the workspace.
 #pragma once
 
@@ -24,6 +24,20 @@ int cross_attention_forward(gsr_ctx *ctx, const gsr_attention &d, const gsr_head
 int cross_attention_backward(gsr_ctx *ctx, const gsr_attention &d, const gsr_heads &q, const gsr_heads &k,
                              const gsr_heads &v, const gsr_heads &out, const float *lse, const gsr_heads &dout,
                              const gsr_heads &dq, const gsr_heads &dk, const gsr_heads &dv, cudaStream_t stream);
+// residual, total, dtotal, gate and dgate may be null.
+int layer_norm_forward(gsr_ctx *ctx, const gsr_layer_norm &d, const gsr_heads &x, const gsr_heads *residual,
+                       const float *weight, const float *bias, const gsr_heads &out, const gsr_heads *total,
+                       float *mean, float *rstd, cudaStream_t stream);
+int layer_norm_backward(gsr_ctx *ctx, const gsr_layer_norm &d, const gsr_heads &dout, const gsr_heads &total,
+                        const float *weight, const float *mean, const float *rstd, const gsr_heads *dtotal,
+                        const gsr_heads &dx, float *dweight, float *dbias, cudaStream_t stream);
+int gated_recurrence_forward(gsr_ctx *ctx, const gsr_recurrence &d, const gsr_heads &x, const gsr_heads &forget,
+                             const gsr_heads *gate, const float *initial, const gsr_heads &out, float *final,
+                             float *states, cudaStream_t stream);
+int gated_recurrence_backward(gsr_ctx *ctx, const gsr_recurrence &d, const gsr_heads &dout, const gsr_heads &x,
+                              const gsr_heads &forget, const gsr_heads *gate, const float *states,
+                              const float *dfinal, const gsr_heads &dx, const gsr_heads &dforget,
+                              const gsr_heads *dgate, float *dinitial, cudaStream_t stream);
 
 // launch_kernel with smem bytes of dynamic shared memory, and in clusters of
 // `cluster` blocks.

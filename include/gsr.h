@@ -389,7 +389,9 @@ int gsr_peak_kernel(gsr_ctx *ctx, int kind, int32_t iters, float *sink, uint64_t
  * in front of it: feature maps of the input views (group norm with an
  * activation, channels last), positions of patch tokens and Gaussian tokens
  * (rotary positions with several axes), and Gaussian tokens that attend to the
- * tokens of all views (cross attention to states of another length).  The calls
+ * tokens of all views (cross attention to states of another length), and layers of
+ * tokens in between (layer norm behind a residual sum, a gated linear recurrence in
+ * either direction).  The calls
  * below follow the conventions at the top of this file; a call that needs
  * scratch memory takes it from a workspace of the context's arena, which grows
  * (synchronising the device) and never shrinks.  Calls on one context from
@@ -403,7 +405,7 @@ int gsr_peak_kernel(gsr_ctx *ctx, int kind, int32_t iters, float *sink, uint64_t
  * overlap unless a call says so. */
 
 /* Waits for the work on `stream`, and tells whether it is to be trusted.
- * Every wait inside the attention kernels is bounded (seconds, where a step takes
+ * Every wait inside the attention's and the recurrence's kernels is bounded (seconds, where a step takes
  * microseconds).  One that runs out ends its kernel without a fault, but what the
  * call wrote is not valid, nor is what later calls made of it.  That is reported
  * once, as GSR_ERR_CUDA: by the context's next call of a decoder operator, before
@@ -554,6 +556,109 @@ int gsr_cross_attention_backward(gsr_ctx *ctx, const gsr_attention *desc, const 
                                  const gsr_heads *v, const gsr_heads *out, const float *lse,
                                  const gsr_heads *dl_dout, const gsr_heads *dl_dq, const gsr_heads *dl_dk,
                                  const gsr_heads *dl_dv, void *stream);
+
+/* Layer norm of the channels of each token (or of each head of a token), behind the
+ * sum of a residual connection:
+ *   total = x + residual, rounded to dtype (x itself without a residual)
+ *   mean, var of total over its channels
+ *   out = (total - mean) / sqrt(var + eps) * weight[c] + bias[c].
+ *
+ *   dtype       type of x, residual, out and total (GSR_F32, GSR_BF16, GSR_F16)
+ *   x, residual, out, total   [batch, tokens, heads, channels]; residual and total
+ *               are both NULL or both not; out and total may be x or residual
+ *               itself (same data and strides), but not each other
+ *   weight, bias   device, [channels] float; each may be NULL (1 and 0)
+ *   mean, rstd  device, [batch, tokens, heads] float, written (for the backward)
+ * All arrays aligned to their element.  Those aligned to 16 bytes, with strides
+ * and channels multiples of 16 bytes, take a vectorised path.  Statistics are taken
+ * in float, the variance from centred values, in a fixed order: the same bits on
+ * every run.
+ * Errors: GSR_ERR_INVALID_ARG (null or misaligned arrays; negative sizes; channels
+ * outside [1, GSR_MAX_NORM_CHANNELS]; heads above GSR_MAX_HEADS, batch * tokens above
+ * GSR_MAX_TOKENS, 2^31 rows or more; out or total with a stride of 0 over more than
+ * one item; eps not finite or <= 0; unknown dtype), GSR_ERR_OOM, GSR_ERR_CUDA. */
+#define GSR_MAX_NORM_CHANNELS 16384
+typedef struct gsr_layer_norm {
+    int32_t dtype;
+    int32_t batch, tokens, heads, channels;
+    float eps;
+} gsr_layer_norm;
+int gsr_layer_norm_forward(gsr_ctx *ctx, const gsr_layer_norm *desc, const gsr_heads *x, const gsr_heads *residual,
+                           const float *weight, const float *bias, const gsr_heads *out, const gsr_heads *total,
+                           float *mean, float *rstd, void *stream);
+
+/* Backward of gsr_layer_norm_forward: with xh = (total - mean) rstd and
+ * g = dL/dout weight,
+ *   dL/dx = rstd (g - mean(g) - xh mean(g xh)) + dl_dtotal
+ *   dL/dweight = sum dL/dout xh,  dL/dbias = sum dL/dout  (over all rows).
+ * dL/dx is the residual's gradient as well.
+ *   total       the forward's (its x, without a residual), with its mean and rstd
+ *   dl_dtotal   NULL, or the gradient that reaches total past this norm
+ *   dl_dx       may be dl_dout or dl_dtotal itself (same data and strides)
+ *   dl_dweight, dl_dbias   device, [channels] float, overwritten; each may be NULL
+ * The same bits on every run.  Errors: as the forward. */
+int gsr_layer_norm_backward(gsr_ctx *ctx, const gsr_layer_norm *desc, const gsr_heads *dl_dout,
+                            const gsr_heads *total, const float *weight, const float *mean, const float *rstd,
+                            const gsr_heads *dl_dtotal, const gsr_heads *dl_dx, float *dl_dweight, float *dl_dbias,
+                            void *stream);
+
+/* A gated linear recurrence over the tokens of each item, channel by channel:
+ *   a_t = sigmoid(forget_t),  h_t = a_t h_(t-1) + (1 - a_t) x_t,
+ *   out_t = h_t gate_t sigmoid(gate_t)   (h_t without a gate).
+ * Tokens run upwards, or downwards with reverse; h starts at initial.  Item b has
+ * min(max(lengths[b], 0), tokens) tokens, its first ones in either direction; what
+ * lies behind them is not read, out is 0 there, and the gradients are.
+ *
+ *   dtype      type of x, forget, gate and out (GSR_F32, GSR_BF16, GSR_F16); h is
+ *              kept in float
+ *   lengths    device, [batch] int32 or NULL (all tokens)
+ *   x, forget, gate, out   [batch, tokens, channels]: gsr_heads of one head; gate
+ *              may be NULL; out may be x, forget or gate itself (same data and strides)
+ *   initial    device, [batch, channels] float or NULL (0)
+ *   final      device, [batch, channels] float, written: h behind the last token
+ *              (initial, for an item without tokens); may be initial itself
+ *   states     device, [batch, blocks, channels] float with a block for every
+ *              GSR_RECURRENCE_BLOCK tokens, or NULL: h in front of each block of the
+ *              recurrence's order, for the backward.  Blocks behind an item's last
+ *              token are left as they were, and not read.
+ * All arrays aligned to their element.  x and forget that are not finite reach their
+ * channel's later tokens only.  The same bits on every run.
+ * Errors: GSR_ERR_INVALID_ARG (null or misaligned arrays; negative sizes; channels
+ * outside [1, GSR_MAX_RECURRENCE_CHANNELS]; batch above 2^16, tokens above 2^24,
+ * batch * tokens above GSR_MAX_TOKENS; 2^31 blocks of 64 tokens x 32 channels or
+ * more; outputs with a stride of 0 over more than one item; unknown dtype),
+ * GSR_ERR_OOM, GSR_ERR_CUDA. */
+#define GSR_RECURRENCE_BLOCK 64
+#define GSR_MAX_RECURRENCE_CHANNELS 65536
+typedef struct gsr_recurrence {
+    int32_t dtype;
+    int32_t batch, tokens, channels;
+    int32_t reverse;
+    const int32_t *lengths;
+} gsr_recurrence;
+int gsr_gated_recurrence_forward(gsr_ctx *ctx, const gsr_recurrence *desc, const gsr_heads *x,
+                                 const gsr_heads *forget, const gsr_heads *gate, const float *initial,
+                                 const gsr_heads *out, float *final, float *states, void *stream);
+
+/* Backward of gsr_gated_recurrence_forward.  With silu(o) = o sigmoid(o) and dh_t
+ * the gradient of everything that h_t reaches,
+ *   dh_t = dL/dout_t silu(gate_t) + a_(t+1) dh_(t+1)   (dl_dfinal behind the last),
+ *   dL/dx = dh (1 - a),  dL/dforget = dh (h_(t-1) - x) a (1 - a),
+ *   dL/dgate = dL/dout h silu'(gate),  dL/dinitial = a_0 dh_0
+ * (the first and last token in the recurrence's order).  h is computed again from
+ * the forward's states.
+ *   gate, dl_dgate   both NULL or both not
+ *   dl_dfinal   device, [batch, channels] float or NULL (0)
+ *   dl_dx, dl_dforget, dl_dgate   [batch, tokens, channels], overwritten; dl_dx may
+ *               be dl_dout itself
+ *   dl_dinitial   device, [batch, channels] float, overwritten, or NULL; may be
+ *               dl_dfinal itself
+ * The same bits on every run.  Errors: as the forward. */
+int gsr_gated_recurrence_backward(gsr_ctx *ctx, const gsr_recurrence *desc, const gsr_heads *dl_dout,
+                                  const gsr_heads *x, const gsr_heads *forget, const gsr_heads *gate,
+                                  const float *states, const float *dl_dfinal, const gsr_heads *dl_dx,
+                                  const gsr_heads *dl_dforget, const gsr_heads *dl_dgate, float *dl_dinitial,
+                                  void *stream);
 
 #ifdef __cplusplus
 }
