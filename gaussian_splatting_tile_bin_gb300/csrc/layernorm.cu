@@ -5,13 +5,22 @@
 // and with g = dout w
 //   dx = rstd (g - mean(g) - xh mean(g xh)) + dtotal,  dw = sum dout xh,  db = sum dout.
 //
-// One warp a row, three passes over it.
+// Bound by HBM.  A row stays in the registers of its team (lanes of a warp, a warp
+// or several) between the statistics and the result, so every array moves once.
+// The backward's blocks walk rows and keep their channels' shares of dw and db in
+// registers; a second kernel adds the blocks' sums in order.
+//
+// Numerics.  The variance is the mean of centred squares, from the registers; sums
+// over a row pass a thread's elements and a tree, in a fixed order.
+#include <algorithm>
+#include <type_traits>
+
 #include "decoder.cuh"
 
 namespace gsr {
 namespace {
 
-constexpr int kRowBlock = 256;
+constexpr int kRowThreads = 512;   // of a block, where a row needs no more
 
 // The rows of one [batch, tokens, heads, channels] array.
 struct Rows {
@@ -24,146 +33,606 @@ struct LayerArgs {
     const float *weight, *bias;
     float *mean, *rstd, *dweight, *dbias;
     float2 *partial;                // [blocks, channels]: (sum dout xh, sum dout)
-    int tokens, heads, channels, rows, blocks;
+    int batch, tokens, heads, channels;
+    uint32_t rows;
+    int team;                       // threads of a row
+    int blocks;
     float eps;
 };
 
+// A row's first element.  Arrays whose rows lie at one stride arrive as one item of
+// one head.
 template <typename T>
-__device__ __forceinline__ T *row_of(const Rows &r, const LayerArgs &a, int row)
+__device__ __forceinline__ T *row_of(const LayerArgs &a, const Rows &r, uint32_t row)
 {
-    const int token = row / a.heads, head = row - token * a.heads;
-    const int b = token / a.tokens, t = token - b * a.tokens;
-    return (T *)r.data + b * r.batch + t * r.token + head * r.head;
+    if (a.batch == 1 && a.heads == 1) return (T *)r.data + row * r.token;
+    const uint32_t token = row / (uint32_t)a.heads, item = token / (uint32_t)a.tokens;
+    return (T *)r.data + item * r.batch + (token - item * (uint32_t)a.tokens) * r.token +
+           (row - token * (uint32_t)a.heads) * r.head;
 }
 
-__device__ __forceinline__ float warp_sum(float v)
+template <typename T>
+__device__ __forceinline__ float2 unpack2(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w)
 {
-    for (int d = 16; d > 0; d /= 2) v += __shfl_xor_sync(~0u, v, d);
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t w)
+{
+    return __half22float2(*(const __half2 *)&w);
+}
+
+// A thread's elements of a row: N accesses of V, `team` threads apart, taken in pairs.
+template <typename T, int V, int N>
+struct Part {
+    Vec<T, V> v[N];
+    static constexpr int kPairs = N * V / 2;
+    static_assert(N * V % 2 == 0, "elements come in pairs");
+
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[i].e[j] = from_float<T>(0.0f);
+    }
+    __device__ __forceinline__ void load(const T *row, const LayerArgs &a, int lane)
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int c = (i * a.team + lane) * V;
+            if (c < a.channels) v[i] = *(const Vec<T, V> *)(row + c);
+        }
+    }
+    __device__ __forceinline__ void store(T *row, const LayerArgs &a, int lane) const
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int c = (i * a.team + lane) * V;
+            if (c < a.channels) *(Vec<T, V> *)(row + c) = v[i];
+        }
+    }
+    __device__ __forceinline__ float2 get(int p) const
+    {
+        if constexpr (V == 1)
+            return make_float2(to_float(v[2 * p].e[0]), to_float(v[(2 * p + 1) % N].e[0]));
+        else if constexpr (sizeof(T) == 2)
+            return unpack2<T>(((const uint32_t *)&v[p / (V / 2)])[p % (V / 2)]);
+        else
+            return pair_of(v[p / (V / 2)], p % (V / 2) * 2);
+    }
+    __device__ __forceinline__ void set(int p, float2 f)
+    {
+        if constexpr (V == 1) {
+            v[2 * p].e[0] = from_float<T>(f.x);
+            v[(2 * p + 1) % N].e[0] = from_float<T>(f.y);
+        } else {
+            set_pair(v[p / (V / 2)], p % (V / 2) * 2, f);
+        }
+    }
+};
+
+// The first channel of a pair, and of its second half.
+template <int V>
+__device__ __forceinline__ int pair_channel(const LayerArgs &a, int lane, int p, int half)
+{
+    if (V == 1) return (2 * p + half) * a.team + lane;
+    return (p / ((V + 1) / 2) * a.team + lane) * V + p % ((V + 1) / 2) * 2 + half;
+}
+
+// A pair of a parameter; `missing` where there is none, 0 behind the channels.
+template <int V>
+__device__ __forceinline__ float2 parameter(const float *from, const LayerArgs &a, int lane, int p, float missing)
+{
+    const int c0 = pair_channel<V>(a, lane, p, 0), c1 = pair_channel<V>(a, lane, p, 1);
+    float2 f = make_float2(0.0f, 0.0f);
+    if constexpr (V > 1) {
+        if (c0 < a.channels) f = from ? *(const float2 *)(from + c0) : make_float2(missing, missing);
+    } else {
+        if (c0 < a.channels) f.x = from ? from[c0] : missing;
+        if (c1 < a.channels) f.y = from ? from[c1] : missing;
+    }
+    return f;
+}
+
+// Sums of a team (of one float or two).  Teams up to a warp: by shuffles.  Wider ones
+// meet at a barrier of their own, over shared memory in two copies, so that one
+// barrier a sum is enough.
+__device__ __forceinline__ void add_lane(float &v, int d) { v += __shfl_xor_sync(~0u, v, d); }
+__device__ __forceinline__ void add_lane(float2 &v, int d)
+{
+    add_lane(v.x, d);
+    add_lane(v.y, d);
+}
+__device__ __forceinline__ float four(const float4 *s) { return s->x + s->y + (s->z + s->w); }
+__device__ __forceinline__ float2 four(const float2 (*s)[4])
+{
+    return make_float2((*s)[0].x + (*s)[1].x + ((*s)[2].x + (*s)[3].x), (*s)[0].y + (*s)[1].y + ((*s)[2].y + (*s)[3].y));
+}
+
+__device__ __forceinline__ void team_barrier(int team, int threads)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(threads) : "memory");
+}
+
+// s_sums: the team's [2][kTeamWarps], 0 behind its warps; turn: which copy.
+constexpr int kTeamWarps = 32;
+
+template <bool WIDE, typename F>
+__device__ __forceinline__ F team_sum(F v, const LayerArgs &a, float2 *s_sums, int team, int &turn)
+{
+    if constexpr (!WIDE) {
+        for (int d = a.team / 2; d > 0; d /= 2) add_lane(v, d);
+    } else {
+        using Four = std::conditional_t<std::is_same_v<F, float>, float4, float2[4]>;
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) add_lane(v, d);
+        F *s = (F *)(s_sums + turn * kTeamWarps);
+        turn ^= 1;
+        const int warps = a.team / 32;
+        if (threadIdx.x % 32 == 0) s[threadIdx.x / 32 - team * warps] = v;
+        team_barrier(team, a.team);
+        v = four((const Four *)s);
+        for (int w = 4; w < warps; w += 4) {
+            const F more = four((const Four *)(s + w));
+            if constexpr (std::is_same_v<F, float>)
+                v += more;
+            else
+                v = add2(v, more);
+        }
+    }
     return v;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kRowBlock) k_layer_norm(const LayerArgs a)
+// Clears the sums of the warps that a block's teams do not have.
+template <bool WIDE>
+__device__ __forceinline__ void clear_sums(float2 *s_all, int teams)
 {
-    grid_dependency_begin();
-    const int row = blockIdx.x * (kRowBlock / 32) + threadIdx.x / 32, lane = threadIdx.x % 32;
-    if (row >= a.rows) return;
-    const T *x = row_of<T>(a.x, a, row);
-    T *out = row_of<T>(a.out, a, row);
-    if (a.residual.data) {
-        const T *residual = row_of<T>(a.residual, a, row);
-        T *total = row_of<T>(a.total, a, row);
-        for (int c = lane; c < a.channels; c += 32) total[c] = from_float<T>(to_float(x[c]) + to_float(residual[c]));
-        x = total;
-    }
-    float sum = 0.0f, square = 0.0f;
-    for (int c = lane; c < a.channels; c += 32) sum += to_float(x[c]);
-    const float mean = warp_sum(sum) / a.channels;
-    for (int c = lane; c < a.channels; c += 32) {
-        const float d = to_float(x[c]) - mean;
-        square = fmaf(d, d, square);
-    }
-    const float rstd = 1.0f / sqrtf(warp_sum(square) / a.channels + a.eps);
-    for (int c = lane; c < a.channels; c += 32)
-        out[c] = from_float<T>(fmaf((to_float(x[c]) - mean) * rstd, a.weight ? a.weight[c] : 1.0f,
-                                    a.bias ? a.bias[c] : 0.0f));
-    if (lane == 0) {
-        a.mean[row] = mean;
-        a.rstd[row] = rstd;
+    if constexpr (WIDE) {
+        for (int i = threadIdx.x; i < teams * 2 * kTeamWarps; i += blockDim.x) s_all[i] = make_float2(0.0f, 0.0f);
+        __syncthreads();
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kRowBlock) k_layer_norm_grad(const LayerArgs a)
+// ---- rows in flight --------------------------------------------------------------------
+
+// A block walks rows, `teams` at a time, and every thread's elements of the next ones
+// come through a ring of its own in shared memory (asynchronous copies; no thread
+// waits for another): S stages of A arrays, as many as 200 KB hold on an SM.  Single elements of
+// 2 bytes have no such copies and are read directly (S = 0).
+template <typename T, int V, int N, int A, int THREADS, int BLOCKS>
+constexpr int kStages = sizeof(T) * V < 4
+                            ? 0
+                            : std::min(8, 200 * 1024 / (BLOCKS * THREADS * A * N * V * (int)sizeof(T)));
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *to, const void *from)
+{
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(BYTES) : "memory");
+}
+
+template <typename T, int V, int N, int A, int S>
+struct Ring {
+    using Access = Vec<T, V>;
+    Access *mine;          // the thread's first slot
+    const Rows &r0, &r1, &r2;
+    int at = 0;            // of the current stage's first slot
+
+    __device__ __forceinline__ const Rows &array(int k) const { return k == 0 ? r0 : k == 1 ? r1 : r2; }
+    __device__ __forceinline__ int step() const { return (int)blockDim.x; }
+    // Starts the copies of a row into the current stage, if there is such a row.
+    __device__ __forceinline__ void fetch(const LayerArgs &a, uint32_t row, int lane) const
+    {
+        if constexpr (S > 0) {
+            if (row < a.rows) {
+#pragma unroll
+                for (int k = 0; k < A; ++k)
+                    if (array(k).data) {
+                        const T *from = row_of<T>(a, array(k), row);
+#pragma unroll
+                        for (int i = 0; i < N; ++i) {
+                            const int c = (i * a.team + lane) * V;
+                            if (c < a.channels) copy_async<sizeof(Access)>(mine + at + (k * N + i) * step(), from + c);
+                        }
+                    }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    }
+    __device__ __forceinline__ void advance()
+    {
+        at += A * N * step();
+        if (at >= S * A * N * step()) at = 0;
+    }
+    // Slots behind the channels are 0 from here on.
+    __device__ __forceinline__ void start(const LayerArgs &a, uint32_t row, uint32_t stride, int lane)
+    {
+        for (int k = 0; k < S; ++k) {
+            for (int i = 0; i < A * N; ++i)
+                if (((i % N) * a.team + lane) * V >= a.channels) mine[at + i * step()] = Access{};
+            fetch(a, row + k * stride, lane);
+            advance();
+        }
+    }
+    // The oldest row's elements.  Its stage is free once they have been used.
+    __device__ __forceinline__ void take(const LayerArgs &a, uint32_t row, int lane, Part<T, V, N> (&to)[A]) const
+    {
+        if constexpr (S > 0) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(S > 0 ? S - 1 : 0) : "memory");
+#pragma unroll
+            for (int k = 0; k < A; ++k)
+                if (array(k).data)
+#pragma unroll
+                    for (int i = 0; i < N; ++i) to[k].v[i] = mine[at + (k * N + i) * step()];
+        } else {
+#pragma unroll
+            for (int k = 0; k < A; ++k)
+                if (array(k).data) {
+                    to[k].clear();
+                    if (row < a.rows) to[k].load(row_of<T>(a, array(k), row), a, lane);
+                }
+        }
+    }
+    // Waits for the copies of rows behind the last.
+    __device__ __forceinline__ void finish() const
+    {
+        if constexpr (S > 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+};
+
+// ---- forward ------------------------------------------------------------------------
+
+template <typename T, int V, int N, bool WIDE, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) k_layer_norm(const LayerArgs a)
 {
     grid_dependency_begin();
-    const int row = blockIdx.x * (kRowBlock / 32) + threadIdx.x / 32, lane = threadIdx.x % 32;
-    if (row >= a.rows) return;
-    const T *total = row_of<T>(a.total, a, row), *dout = row_of<T>(a.x, a, row);
-    const T *dtotal = a.residual.data ? row_of<T>(a.residual, a, row) : nullptr;
-    T *dx = row_of<T>(a.out, a, row);
-    const float mean = a.mean[row], rstd = a.rstd[row], share = 1.0f / a.channels;
-    float s1 = 0.0f, s2 = 0.0f;
-    for (int c = lane; c < a.channels; c += 32) {
-        const float xh = (to_float(total[c]) - mean) * rstd, g = to_float(dout[c]) * (a.weight ? a.weight[c] : 1.0f);
-        s1 += g;
-        s2 = fmaf(g, xh, s2);
+    extern __shared__ __align__(16) unsigned char s_bytes[];   // the teams' sums, then the ring
+    using Elements = Part<T, V, N>;
+    constexpr int kPairs = Elements::kPairs, S = kStages<T, V, N, 2, THREADS, BLOCKS>;
+    const int teams = blockDim.x / a.team, team = threadIdx.x / a.team, lane = threadIdx.x % a.team;
+    const uint32_t stride = gridDim.x * (uint32_t)teams;
+    float2 *s_sums = (float2 *)s_bytes + team * 2 * kTeamWarps;
+    Ring<T, V, N, 2, S> ring = {(Vec<T, V> *)(s_bytes + (WIDE ? teams * 2 * kTeamWarps * sizeof(float2) : 0)) + threadIdx.x, a.x,
+                                a.residual, a.residual};
+
+    // (Below 2^31 rows, steps ahead of them below 2^32.  All teams take the same number of steps.)
+    uint32_t row = blockIdx.x * teams + team, first = blockIdx.x * teams;
+    ring.start(a, row, stride, lane);
+    clear_sums<WIDE>((float2 *)s_bytes, teams);
+    float2 weight[kPairs], bias[kPairs];
+#pragma unroll
+    for (int p = 0; p < kPairs; ++p) {
+        weight[p] = parameter<V>(a.weight, a, lane, p, 1.0f);
+        bias[p] = parameter<V>(a.bias, a, lane, p, 0.0f);
     }
-    s1 = warp_sum(s1) * share;
-    s2 = warp_sum(s2) * share;
-    for (int c = lane; c < a.channels; c += 32) {
-        const float xh = (to_float(total[c]) - mean) * rstd, g = to_float(dout[c]) * (a.weight ? a.weight[c] : 1.0f);
-        float d = rstd * (g - s1 - xh * s2);
-        if (dtotal) d += to_float(dtotal[c]);
-        dx[c] = from_float<T>(d);
+    const float share = 1.0f / (float)a.channels;
+    const bool full = a.channels == a.team * V * N;
+    int turn = 0;
+    for (; first < a.rows; first += stride, row += stride) {
+        const bool valid = row < a.rows;
+        Elements in[2];
+        ring.take(a, row, lane, in);
+        Elements &x = in[0];
+        if (a.residual.data) {
+#pragma unroll
+            for (int p = 0; p < kPairs; ++p) x.set(p, add2(x.get(p), in[1].get(p)));
+            if (valid) x.store(row_of<T>(a, a.total, row), a, lane);
+        }
+        float2 f[kPairs], sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int p = 0; p < kPairs; ++p) sum = add2(sum, f[p] = x.get(p));
+        ring.fetch(a, row + S * stride, lane);
+        ring.advance();
+        const float mean = team_sum<WIDE>(sum.x + sum.y, a, s_sums, team, turn) * share;
+        const float2 minus = make_float2(-mean, -mean);
+        sum = make_float2(0.0f, 0.0f);
+        if (full) {
+#pragma unroll
+            for (int p = 0; p < kPairs; ++p) {
+                f[p] = add2(f[p], minus);
+                sum = fma2(f[p], f[p], sum);
+            }
+        } else {
+#pragma unroll
+            for (int p = 0; p < kPairs; ++p) {
+                f[p] = add2(f[p], minus);
+                if (pair_channel<V>(a, lane, p, 0) >= a.channels) f[p].x = 0.0f;
+                if (pair_channel<V>(a, lane, p, 1) >= a.channels) f[p].y = 0.0f;
+                sum = fma2(f[p], f[p], sum);
+            }
+        }
+        const float var = team_sum<WIDE>(sum.x + sum.y, a, s_sums, team, turn) * share;
+        const float rstd = rsqrtf(var + a.eps);
+        const float2 scale = make_float2(rstd, rstd);
+#pragma unroll
+        for (int p = 0; p < kPairs; ++p) x.set(p, fma2(mul2(f[p], scale), weight[p], bias[p]));
+        if (valid) {
+            x.store(row_of<T>(a, a.out, row), a, lane);
+            if (lane == 0) {
+                a.mean[row] = mean;
+                a.rstd[row] = rstd;
+            }
+        }
+    }
+    ring.finish();
+}
+
+// ---- backward -----------------------------------------------------------------------
+
+template <typename T, int V, int N, bool WIDE, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) k_layer_norm_grad(const LayerArgs a)
+{
+    grid_dependency_begin();
+    // The teams' sums, then the ring; at the end the block's shares of dw and db.
+    extern __shared__ __align__(16) unsigned char s_bytes[];
+    float2 *s_work = (float2 *)s_bytes;
+    using Elements = Part<T, V, N>;
+    constexpr int kPairs = Elements::kPairs, S = kStages<T, V, N, 3, THREADS, BLOCKS>;
+    const int teams = blockDim.x / a.team, team = threadIdx.x / a.team, lane = threadIdx.x % a.team;
+    const uint32_t stride = gridDim.x * (uint32_t)teams;
+    float2 *s_sums = s_work + team * 2 * kTeamWarps;
+    Ring<T, V, N, 3, S> ring = {(Vec<T, V> *)(s_bytes + (WIDE ? teams * 2 * kTeamWarps * sizeof(float2) : 0)) + threadIdx.x,
+                                a.total, a.x, a.residual};
+
+    // (As in the forward.)
+    uint32_t row = blockIdx.x * teams + team, first = blockIdx.x * teams;
+    ring.start(a, row, stride, lane);
+    clear_sums<WIDE>((float2 *)s_bytes, teams);
+    float2 weight[kPairs], dw[kPairs], db[kPairs];
+#pragma unroll
+    for (int p = 0; p < kPairs; ++p) {
+        weight[p] = parameter<V>(a.weight, a, lane, p, 1.0f);
+        dw[p] = db[p] = make_float2(0.0f, 0.0f);
+    }
+    const float share = 1.0f / (float)a.channels;
+    int turn = 0;
+    float mean = row < a.rows ? a.mean[row] : 0.0f, rstd = row < a.rows ? a.rstd[row] : 0.0f;
+    for (; first < a.rows; first += stride, row += stride) {
+        Elements in[3];
+        ring.take(a, row, lane, in);
+        Elements &total = in[0], &dout = in[1], &dtotal = in[2];
+        const float2 minus = make_float2(-mean, -mean), scale = make_float2(rstd, rstd);
+        const uint32_t after = row + stride;
+        if (after < a.rows) {
+            mean = a.mean[after];
+            rstd = a.rstd[after];
+        }
+        if (row >= a.rows) {   // (its stage holds an older row)
+            dout.clear();
+            total.clear();
+        }
+        float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
+#pragma unroll
+        for (int p = 0; p < kPairs; ++p) {
+            const float2 d = dout.get(p), g = mul2(d, weight[p]);
+            const float2 hat = mul2(add2(total.get(p), minus), scale);
+            s1 = add2(s1, g);
+            s2 = fma2(g, hat, s2);
+            dw[p] = fma2(d, hat, dw[p]);
+            db[p] = add2(db[p], d);
+        }
+        ring.fetch(a, row + S * stride, lane);
+        ring.advance();
+        const float2 m = team_sum<WIDE>(make_float2(s1.x + s1.y, s2.x + s2.y), a, s_sums, team, turn);
+        const float2 m1 = make_float2(-m.x * share, -m.x * share), m2 = make_float2(-m.y * share, -m.y * share);
+        if (row >= a.rows) continue;
+#pragma unroll
+        for (int p = 0; p < kPairs; ++p) {
+            const float2 hat = mul2(add2(total.get(p), minus), scale);
+            const float2 d = fma2(hat, m2, fma2(dout.get(p), weight[p], m1));
+            total.set(p, a.residual.data ? fma2(d, scale, dtotal.get(p)) : mul2(d, scale));
+        }
+        total.store(row_of<T>(a, a.out, row), a, lane);
+    }
+    ring.finish();
+    if (!a.partial) return;
+
+    // The block's sums: lanes of a warp that hold the same channels, then teams in order.
+    if (!WIDE)
+        for (int d = a.team; d < 32; d *= 2)
+#pragma unroll
+            for (int p = 0; p < kPairs; ++p) {
+                dw[p].x += __shfl_xor_sync(~0u, dw[p].x, d);
+                dw[p].y += __shfl_xor_sync(~0u, dw[p].y, d);
+                db[p].x += __shfl_xor_sync(~0u, db[p].x, d);
+                db[p].y += __shfl_xor_sync(~0u, db[p].y, d);
+            }
+    const int width = WIDE ? a.team : 32;
+    const int group = threadIdx.x / width, groups = blockDim.x / width;
+    const bool mine = threadIdx.x % width < a.team;
+    float2 *out = a.partial + (int64_t)blockIdx.x * a.channels;
+    for (int k = 0; k < groups; ++k) {
+        __syncthreads();
+        if (k == group && mine)
+#pragma unroll
+            for (int p = 0; p < kPairs; ++p)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int c = pair_channel<V>(a, lane, p, half);
+                    if (c >= a.channels) continue;
+                    float2 v = half ? make_float2(dw[p].y, db[p].y) : make_float2(dw[p].x, db[p].x);
+                    if (k > 0) v = add2(s_work[c], v);
+                    if (k < groups - 1)
+                        s_work[c] = v;
+                    else
+                        out[c] = v;
+                }
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kRowBlock) k_layer_norm_sums(const LayerArgs a)
+// Adds the blocks' sums: 32 channels a block, 32 threads a channel.
+constexpr int kParamSlices = 32;
+
+__global__ void __launch_bounds__(32 * kParamSlices) k_layer_norm_params(const LayerArgs a)
 {
     grid_dependency_begin();
-    const int c = blockIdx.y * kRowBlock + threadIdx.x;
-    if (c >= a.channels) return;
+    __shared__ float2 s_sum[kParamSlices][33];
+    const int c = blockIdx.x * 32 + threadIdx.x % 32, slice = threadIdx.x / 32;
     float2 sum = make_float2(0.0f, 0.0f);
-    for (int row = blockIdx.x; row < a.rows; row += a.blocks) {
-        const float d = to_float(row_of<T>(a.x, a, row)[c]);
-        sum.x = fmaf(d, (to_float(row_of<T>(a.total, a, row)[c]) - a.mean[row]) * a.rstd[row], sum.x);
-        sum.y += d;
-    }
-    a.partial[(int64_t)blockIdx.x * a.channels + c] = sum;
+    if (c < a.channels)
+#pragma unroll 4
+        for (int i = slice; i < a.blocks; i += kParamSlices) sum = add2(sum, a.partial[(int64_t)i * a.channels + c]);
+    s_sum[slice][threadIdx.x % 32] = sum;
+    __syncthreads();
+    // A warp takes a channel: its lanes the slices.
+    sum = s_sum[threadIdx.x % 32][slice];
+    for (int d = 16; d > 0; d /= 2) add_lane(sum, d);
+    const int channel = blockIdx.x * 32 + slice;
+    if (threadIdx.x % 32 != 0 || channel >= a.channels) return;
+    if (a.dweight) a.dweight[channel] = sum.x;
+    if (a.dbias) a.dbias[channel] = sum.y;
 }
 
-__global__ void __launch_bounds__(kRowBlock) k_layer_norm_params(const LayerArgs a)
-{
-    grid_dependency_begin();
-    const int c = blockIdx.x * kRowBlock + threadIdx.x;
-    if (c >= a.channels) return;
-    float2 sum = make_float2(0.0f, 0.0f);
-    for (int i = 0; i < a.blocks; ++i) {
-        const float2 v = a.partial[(int64_t)i * a.channels + c];
-        sum.x += v.x;
-        sum.y += v.y;
-    }
-    if (a.dweight) a.dweight[c] = sum.x;
-    if (a.dbias) a.dbias[c] = sum.y;
-}
+// ---- host ---------------------------------------------------------------------------
 
 Rows rows_of(const gsr_heads *t)
 {
     return t ? Rows{t->data, t->batch_stride, t->token_stride, t->head_stride} : Rows{};
 }
 
+// Takes dimensions together that every array walks at one stride: heads into
+// tokens, then items into tokens.
+void collapse(LayerArgs &a)
+{
+    Rows *arrays[] = {&a.x, &a.residual, &a.out, &a.total};
+    bool flat = true;
+    for (const Rows *r : arrays)
+        if (r->data && a.heads > 1 && a.tokens > 1) flat = flat && r->token == a.heads * r->head;
+    if (flat && a.heads > 1) {
+        a.tokens *= a.heads;
+        a.heads = 1;
+        for (Rows *r : arrays) r->token = r->head;
+    }
+    if (a.heads > 1 || a.batch == 1) return;
+    for (const Rows *r : arrays)
+        if (r->data && a.tokens > 1) flat = flat && r->batch == a.tokens * r->token;
+    if (!flat) return;
+    for (Rows *r : arrays)
+        if (a.tokens == 1) r->token = r->batch;
+    a.tokens *= a.batch;
+    a.batch = 1;
+}
+
 LayerArgs args_of(const gsr_layer_norm &d)
 {
     LayerArgs a = {};
+    a.batch = d.batch;
     a.tokens = d.tokens;
     a.heads = d.heads;
     a.channels = d.channels;
-    a.rows = d.batch * d.tokens * d.heads;
+    a.rows = (uint32_t)d.batch * (uint32_t)d.tokens * (uint32_t)d.heads;
     a.eps = d.eps;
     return a;
 }
 
-unsigned row_blocks(const LayerArgs &a) { return (unsigned)(((int64_t)a.rows + kRowBlock / 32 - 1) / (kRowBlock / 32)); }
-
-template <typename T>
-cudaError_t run_forward(gsr_ctx *ctx, const LayerArgs &a, cudaStream_t stream)
+// Elements of an access: 16 bytes, or 4 where channels, strides or arrays allow no
+// more, or one.
+int access_width(const LayerArgs &a, int size)
 {
-    return launch_kernel(ctx, k_layer_norm<T>, dim3(row_blocks(a)), kRowBlock, stream, a);
+    for (int bytes : {16, 4}) {
+        const int v = bytes / size;
+        if (v <= 1) break;
+        bool ok = a.channels % v == 0;
+        for (const float *p : {a.weight, a.bias}) ok = ok && (uintptr_t)p % 8 == 0;   // read in pairs
+        for (const Rows *r : {&a.x, &a.residual, &a.out, &a.total})
+            if (r->data)
+                ok = ok && (uintptr_t)r->data % bytes == 0 && (a.batch == 1 || r->batch % v == 0) &&
+                     (a.tokens == 1 || r->token % v == 0) && (a.heads == 1 || r->head % v == 0);
+        if (ok) return v;
+    }
+    return 1;
 }
 
-template <typename T>
-cudaError_t run_backward(gsr_ctx *ctx, const LayerArgs &a, cudaStream_t stream)
+int power_of_two(int n)
 {
-    const unsigned columns = (unsigned)((a.channels + kRowBlock - 1) / kRowBlock);
-    cudaError_t e = cudaSuccess;
-    if (a.partial) {   // first: dx may take dout's place
-        e = launch_kernel(ctx, k_layer_norm_sums<T>, dim3((unsigned)a.blocks, columns), kRowBlock, stream, a);
-        if (e == cudaSuccess) e = launch_kernel(ctx, k_layer_norm_params, dim3(columns), kRowBlock, stream, a);
+    int p = 1;
+    while (p < n) p *= 2;
+    return p;
+}
+
+// How a row is divided: elements of a thread, threads, and blocks of how many rows.
+struct Plan {
+    int teams, occupancy;
+};
+
+// One access a thread where that makes a warp or less, 16 elements otherwise.
+template <int V>
+constexpr bool one_access(int channels)
+{
+    return V > 1 && channels <= 32 * V;
+}
+
+// Few rows are spread over the SMs rather than over the teams of one block.
+template <int V>
+Plan plan_rows(const gsr_ctx *ctx, LayerArgs &a)
+{
+    Plan p;
+    const bool one = one_access<V>(a.channels);
+    const int each = one ? V : 16, threads = (a.channels + each - 1) / each;
+    a.team = threads <= 32 ? power_of_two(threads) : (threads + 31) / 32 * 32;
+    p.occupancy = one ? 2 : 1;
+    const uint64_t spread = ((uint64_t)a.rows + ctx->num_sms - 1) / ctx->num_sms;
+    p.teams = a.team > kRowThreads ? 1 : kRowThreads / a.team;
+    while (a.team * p.teams > 128 && (uint64_t)p.teams > spread) p.teams = (p.teams + 1) / 2;
+    if (p.teams * a.team % 32 != 0) p.teams = 32 / a.team;   // whole warps
+    const uint64_t blocks = ((uint64_t)a.rows + p.teams - 1) / p.teams, most = (uint64_t)p.occupancy * ctx->num_sms;
+    a.blocks = (int)(blocks < most ? blocks : most);
+    return p;
+}
+
+template <typename T, int V, int N, bool WIDE, int THREADS, int BLOCKS, bool BACKWARD>
+cudaError_t launch_rows(gsr_ctx *ctx, LayerArgs &a, int teams, cudaStream_t stream)
+{
+    constexpr int kArrays = BACKWARD ? 3 : 2;
+    const int threads = teams * a.team;
+    const size_t ring = (size_t)kStages<T, V, N, kArrays, THREADS, BLOCKS> * kArrays * N * threads * sizeof(T) * V;
+    const size_t sums = WIDE ? (size_t)teams * 2 * kTeamWarps * sizeof(float2) : 0;
+    const size_t shares = BACKWARD && threads > (WIDE ? a.team : 32) ? (size_t)a.channels * sizeof(float2) : 0;
+    const size_t smem = sums + ring > shares ? sums + ring : shares;
+    void (*kernel)(LayerArgs);
+    if constexpr (BACKWARD)
+        kernel = k_layer_norm_grad<T, V, N, WIDE, THREADS, BLOCKS>;
+    else
+        kernel = k_layer_norm<T, V, N, WIDE, THREADS, BLOCKS>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_kernel_smem(ctx, kernel, dim3((unsigned)a.blocks), threads, smem, 1, stream, a);
+}
+
+template <typename T, int V, bool BACKWARD>
+cudaError_t dispatch_rows(gsr_ctx *ctx, LayerArgs &a, const Plan &p, cudaStream_t stream)
+{
+    constexpr int N = 16 / V;
+    if constexpr (V > 1)
+        if (one_access<V>(a.channels)) return launch_rows<T, V, 1, false, kRowThreads, 2, BACKWARD>(ctx, a, p.teams, stream);
+    if (a.team <= 32) return launch_rows<T, V, N, false, kRowThreads, 1, BACKWARD>(ctx, a, p.teams, stream);
+    if (a.team <= kRowThreads) return launch_rows<T, V, N, true, kRowThreads, 1, BACKWARD>(ctx, a, p.teams, stream);
+    return launch_rows<T, V, N, true, 1024, 1, BACKWARD>(ctx, a, p.teams, stream);
+}
+
+// f<T, V>() for the description's type and the arrays' widest access.
+template <typename F>
+auto with_access(int dtype, const LayerArgs &a, F f)
+{
+    if (dtype == GSR_F32) {
+        if (access_width(a, 4) == 4) return f(float(), std::integral_constant<int, 4>());
+        return f(float(), std::integral_constant<int, 1>());
     }
-    if (e == cudaSuccess) e = launch_kernel(ctx, k_layer_norm_grad<T>, dim3(row_blocks(a)), kRowBlock, stream, a);
-    return e;
+    const int v = access_width(a, 2);
+    if (dtype == GSR_BF16) {
+        if (v == 8) return f(__nv_bfloat16(), std::integral_constant<int, 8>());
+        if (v == 2) return f(__nv_bfloat16(), std::integral_constant<int, 2>());
+        return f(__nv_bfloat16(), std::integral_constant<int, 1>());
+    }
+    if (v == 8) return f(__half(), std::integral_constant<int, 8>());
+    if (v == 2) return f(__half(), std::integral_constant<int, 2>());
+    return f(__half(), std::integral_constant<int, 1>());
 }
 
 }  // namespace
@@ -181,13 +650,12 @@ int layer_norm_forward(gsr_ctx *ctx, const gsr_layer_norm &d, const gsr_heads &x
     a.bias = bias;
     a.mean = mean;
     a.rstd = rstd;
-    cudaError_t e;
-    if (d.dtype == GSR_F32)
-        e = run_forward<float>(ctx, a, stream);
-    else if (d.dtype == GSR_BF16)
-        e = run_forward<__nv_bfloat16>(ctx, a, stream);
-    else
-        e = run_forward<__half>(ctx, a, stream);
+    collapse(a);
+    const cudaError_t e = with_access(d.dtype, a, [&](auto t, auto v) {
+        constexpr int V = decltype(v)::value;
+        const Plan p = plan_rows<V>(ctx, a);
+        return dispatch_rows<decltype(t), V, false>(ctx, a, p, stream);
+    });
     return cuda_check(ctx, e, "layer norm forward");
 }
 
@@ -213,21 +681,27 @@ int layer_norm_backward(gsr_ctx *ctx, const gsr_layer_norm &d, const gsr_heads &
     a.rstd = const_cast<float *>(rstd);
     a.dweight = dweight;
     a.dbias = dbias;
-    a.blocks = a.rows < 2 * ctx->num_sms ? a.rows : 2 * ctx->num_sms;
+    collapse(a);
     Workspace workspace(ctx, stream);
-    if (dweight || dbias) {
-        void *work = nullptr;
-        if (int rc = workspace.take((size_t)a.blocks * d.channels * sizeof(float2), &work)) return rc;
-        a.partial = (float2 *)work;
-    }
-    cudaError_t e;
-    if (d.dtype == GSR_F32)
-        e = run_backward<float>(ctx, a, stream);
-    else if (d.dtype == GSR_BF16)
-        e = run_backward<__nv_bfloat16>(ctx, a, stream);
-    else
-        e = run_backward<__half>(ctx, a, stream);
-    if (int rc = cuda_check(ctx, e, "layer norm backward")) return rc;
+    int rc = GSR_OK;
+    const cudaError_t e = with_access(d.dtype, a, [&](auto t, auto v) {
+        using T = decltype(t);
+        constexpr int V = decltype(v)::value;
+        const Plan p = plan_rows<V>(ctx, a);
+        if (dweight || dbias) {
+            void *work = nullptr;
+            rc = workspace.take((size_t)a.blocks * d.channels * sizeof(float2), &work);
+            if (rc != GSR_OK) return cudaSuccess;
+            a.partial = (float2 *)work;
+        }
+        cudaError_t e = dispatch_rows<T, V, true>(ctx, a, p, stream);
+        if (e == cudaSuccess && a.partial)
+            e = launch_kernel(ctx, k_layer_norm_params, dim3((unsigned)((a.channels + 31) / 32)), 32 * kParamSlices,
+                              stream, a);
+        return e;
+    });
+    if (rc != GSR_OK) return rc;
+    if (int bad = cuda_check(ctx, e, "layer norm backward")) return bad;
     return workspace.done();
 }
 
