@@ -20,9 +20,10 @@
 // run.  A published pair is one 64-bit word, which is all ones before that (no pair
 // is: A is never that NaN).
 //
-// Numerics.  Of a and 1 - a the smaller one, w <= 1/2, is e / (1 + e) with e =
-// exp(-|f|), and a step moves h or x by w times their difference: nothing cancels for
-// gates near 0 or 1, and A takes 1 - w as A - w A.
+// Numerics.  With e = exp(-|f|), the larger of a and 1 - a is 1 / (1 + e) and the smaller
+// e / (1 + e): neither is taken as a difference, so gates near 0 and 1 lose nothing.
+#include <type_traits>
+
 #include "decoder.cuh"
 
 namespace gsr {
@@ -49,6 +50,7 @@ struct RecurrenceArgs {
     const int *lengths;
     int batch, tokens, channels, blocks;
     int tiles, slabs;            // of all tokens, of all channels
+    uint32_t work;               // their number over all items
     int reverse;
     unsigned long long *pairs, *ends;   // published: [batch, slabs, tiles] and [batch, slabs, groups] rows of words
     uint32_t *ticket;            // all ones before the first
@@ -56,31 +58,99 @@ struct RecurrenceArgs {
     uint32_t *status;
 };
 
-// ---- the affine maps ------------------------------------------------------------------
+// ---- channels --------------------------------------------------------------------------
 
+// A thread's channels: one or a pair, whose arithmetic is one instruction for both.
+template <int V>
+using Lanes = std::conditional_t<V == 2, float2, float>;
+
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float2 mul(float2 a, float2 b) { return mul2(a, b); }
+__device__ __forceinline__ float add(float a, float b) { return a + b; }
+__device__ __forceinline__ float2 add(float2 a, float2 b) { return add2(a, b); }
+__device__ __forceinline__ float mad(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float2 mad(float2 a, float2 b, float2 c) { return fma2(a, b, c); }
+__device__ __forceinline__ float minus(float a) { return -a; }
+__device__ __forceinline__ float2 minus(float2 a) { return make_float2(-a.x, -a.y); }
+__device__ __forceinline__ void fill(float &v, float x) { v = x; }
+__device__ __forceinline__ void fill(float2 &v, float x) { v = make_float2(x, x); }
+__device__ __forceinline__ float &at(float &v, int) { return v; }
+__device__ __forceinline__ float &at(float2 &v, int j) { return j ? v.y : v.x; }
+__device__ __forceinline__ float at(const float &v, int) { return v; }
+__device__ __forceinline__ float at(const float2 &v, int j) { return j ? v.y : v.x; }
+
+// Bits of a thread's elements of one token.
+template <typename T, int V>
+using Raw = std::conditional_t<sizeof(T) * V == 8, uint2, std::conditional_t<sizeof(T) * V == 4, uint32_t, uint16_t>>;
+
+template <typename T, int V>
+__device__ __forceinline__ Lanes<V> value_of(const Raw<T, V> &r)
+{
+    if constexpr (V == 1) {
+        return to_float(*(const T *)&r);
+    } else if constexpr (sizeof(T) == 4) {
+        return make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
+    } else if constexpr (std::is_same_v<T, __half>) {
+        return __half22float2(*(const __half2 *)&r);
+    } else {
+        return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
+    }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> raw_of(Lanes<V> v)
+{
+    if constexpr (V == 1) {
+        const T t = from_float<T>(v);
+        return *(const Raw<T, V> *)&t;
+    } else if constexpr (sizeof(T) == 4) {
+        return make_uint2(__float_as_uint(v.x), __float_as_uint(v.y));
+    } else {
+        return pack2<T>(v.x, v.y);
+    }
+}
+
+__device__ __forceinline__ void clear(uint2 &r) { r = make_uint2(0, 0); }
+__device__ __forceinline__ void clear(uint32_t &r) { r = 0; }
+__device__ __forceinline__ void clear(uint16_t &r) { r = 0; }
+
+// state -> a state + h
+template <int V>
 struct Map {
-    float a, h;   // state -> a state + h
+    Lanes<V> a, h;
 };
 
-__device__ __forceinline__ Map then(const Map &first, const Map &second)
+template <int V>
+__device__ __forceinline__ Map<V> then(const Map<V> &first, const Map<V> &second)
 {
-    return {second.a * first.a, fmaf(second.a, first.h, second.h)};
-}
-
-__device__ __forceinline__ unsigned long long word_of(const Map &m)
-{
-    return (unsigned long long)__float_as_uint(m.h) << 32 | __float_as_uint(m.a);
-}
-
-__device__ __forceinline__ Map map_of(unsigned long long w)
-{
-    return {__uint_as_float((uint32_t)w), __uint_as_float((uint32_t)(w >> 32))};
+    return {mul(second.a, first.a), mad(second.a, first.h, second.h)};
 }
 
 template <int V>
 struct Words {
     unsigned long long w[V];
+
+    __device__ __forceinline__ static Words of(const Map<V> &m)
+    {
+        Words v;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            v.w[j] = (unsigned long long)__float_as_uint(at(m.h, j)) << 32 | __float_as_uint(at(m.a, j));
+        return v;
+    }
+    __device__ __forceinline__ Map<V> map() const
+    {
+        Map<V> m;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            at(m.a, j) = __uint_as_float((uint32_t)w[j]);
+            at(m.h, j) = __uint_as_float((uint32_t)(w[j] >> 32));
+        }
+        return m;
+    }
 };
+
+// ---- the chain ---------------------------------------------------------------------------
 
 __device__ __forceinline__ void publish(unsigned long long *to, const Words<1> &v)
 {
@@ -134,16 +204,9 @@ struct Tile {
     int length, count;     // the item's tokens and tiles
 };
 
-// A block's tile; the ticket counts in the order of the chains.
-__device__ __forceinline__ Tile take_tile(const RecurrenceArgs &a, int tile_tokens, bool backward)
+// The n-th tile in the order of the chains.
+__device__ __forceinline__ Tile tile_at(const RecurrenceArgs &a, uint32_t n, int tile_tokens, bool backward)
 {
-    uint32_t n = blockIdx.x;
-    if (a.ticket) {
-        __shared__ uint32_t s_ticket;
-        if (threadIdx.x == 0) s_ticket = atomicAdd(a.ticket, 1u) + 1u;
-        __syncthreads();
-        n = s_ticket;
-    }
     Tile t;
     const uint32_t chains = (uint32_t)a.batch * a.slabs, place = n / chains, chain = n - place * chains;
     t.b = chain / a.slabs;
@@ -154,107 +217,126 @@ __device__ __forceinline__ Tile take_tile(const RecurrenceArgs &a, int tile_toke
     return t;
 }
 
-// A warp's tokens of one array: `from` the first one's address for this lane, in steps
-// of `step` elements.  Behind the item's length tokens come in their own order.
-struct Walk {
-    int64_t first, step;
-};
-
-__device__ __forceinline__ Walk walk(const RecurrenceArgs &a, const Tokens &t, const Tile &tile, int k, int c)
-{
-    const int64_t at = a.reverse ? tile.length - 1 - k : k;
-    return {tile.b * t.batch + at * t.token + c, a.reverse ? -t.token : t.token};
-}
-
-template <typename T, int V>
-__device__ __forceinline__ void clear_tokens(const RecurrenceArgs &a, const Tokens &t, int b, int from, int to, int c)
-{
-    Vec<T, V> zero;
-#pragma unroll
-    for (int j = 0; j < V; ++j) zero.e[j] = from_float<T>(0.0f);
-    T *at = (T *)t.data + b * t.batch + from * t.token + c;
-    for (int k = from; k < to; ++k, at += t.token) *(Vec<T, V> *)at = zero;
-}
-
 // The state in front of a chain, read by the warp that publishes the first tile's map
 // and handed to the others: once that map is out, nobody reads the array, in which a
 // block may write the state behind the chain.
 template <int V>
-__device__ __forceinline__ void load_seed(const RecurrenceArgs &a, int warp, bool here, int64_t at, float *seed)
+__device__ __forceinline__ void load_seed(const RecurrenceArgs &a, int warp, bool here, int64_t from, Lanes<V> *seed)
 {
     if (warp != kWarps - 1) return;
 #pragma unroll
-    for (int j = 0; j < V; ++j) seed[j] = here && a.initial ? a.initial[at + j] : 0.0f;
+    for (int j = 0; j < V; ++j) at(*seed, j) = here && a.initial ? a.initial[from + j] : 0.0f;
+}
+
+template <int V>
+__device__ __forceinline__ void store_state(float *to, const Lanes<V> &v)
+{
+#pragma unroll
+    for (int j = 0; j < V; ++j) to[j] = at(v, j);
 }
 
 // The state in front of the block's tile, for this lane's channels.  `tile_map`: the
-// tile's own map (warp kWarps - 1 has it); `seed`: the state in front of the first tile.
+// tile's own map (warp kWarps - 1 has it); `seed`: the state in front of the first tile (0 for others).
 // place: the tile's in its chain of t.count.
 template <int V>
-__device__ __forceinline__ void chain(const RecurrenceArgs &a, const Tile &t, int place, const Map (&tile_map)[V],
-                                      const float *seed, Map (*s_maps)[32 * V], float (&state)[V])
+__device__ __forceinline__ Lanes<V> chain(const RecurrenceArgs &a, const Tile &t, int place, const Map<V> &tile_map,
+                                          const Lanes<V> &seed, Map<V> (*s_maps)[32])
 {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-#pragma unroll
-    for (int j = 0; j < V; ++j) state[j] = seed[j];
-    if (t.count == 1) return;
+    if (t.count == 1) return seed;
     const int64_t row = (int64_t)t.b * a.slabs + t.slab;
     const int groups = (a.tiles + kGroup - 1) / kGroup, group = place / kGroup;
     unsigned long long *pairs = a.pairs + row * a.tiles * (32 * V) + lane * V;
     unsigned long long *ends = a.ends + row * groups * (32 * V) + lane * V;
     if (warp == kWarps - 1 && place + 1 < t.count) {
-        Words<V> w;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {   // the first tile's, as a map of no state
-            const Map m = place == 0 ? Map{0.0f, fmaf(tile_map[j].a, seed[j], tile_map[j].h)} : tile_map[j];
-            w.w[j] = word_of(m);
+        Map<V> m = tile_map;
+        if (place == 0) {   // as a map of no state
+            m.h = mad(m.a, seed, m.h);
+            fill(m.a, 0.0f);
         }
-        publish(pairs + (int64_t)place * (32 * V), w);
+        publish(pairs + (int64_t)place * (32 * V), Words<V>::of(m));
     }
-    if (place == 0) return;
+    if (place == 0) return seed;
     // Each warp folds four tiles of the group; the first one behind the group's start.
-    Map m[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) m[j] = {1.0f, 0.0f};
+    Map<V> m;
+    fill(m.a, 1.0f);
+    fill(m.h, 0.0f);
     const int first = group * kGroup + 4 * warp;
-    Words<V> seen[5];
+    Words<V> seen[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (first + i < place) look(pairs + (int64_t)(first + i) * (32 * V), seen[i]);
     if (warp == 0 && group > 0) {
-        look(ends + (int64_t)group * (32 * V), seen[4]);
-        wait_for(a, ends + (int64_t)group * (32 * V), seen[4]);
-#pragma unroll
-        for (int j = 0; j < V; ++j) m[j] = map_of(seen[4].w[j]);
+        Words<V> end;
+        look(ends + (int64_t)group * (32 * V), end);
+        wait_for(a, ends + (int64_t)group * (32 * V), end);
+        m = end.map();
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (first + i < place) {
             wait_for(a, pairs + (int64_t)(first + i) * (32 * V), seen[i]);
-#pragma unroll
-            for (int j = 0; j < V; ++j) m[j] = then(m[j], map_of(seen[i].w[j]));
+            m = then(m, seen[i].map());
         }
-#pragma unroll
-    for (int j = 0; j < V; ++j) s_maps[warp][lane * V + j] = m[j];
+    s_maps[warp][lane] = m;
     __syncthreads();
+    Lanes<V> state;
+    fill(state, 0.0f);   // (the first map of a chain takes no state)
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        state[j] = 0.0f;   // (the first map of a chain takes no state)
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const Map v = s_maps[w][lane * V + j];
-            state[j] = fmaf(v.a, state[j], v.h);
-        }
+    for (int w = 0; w < kWarps; ++w) {
+        const Map<V> v = s_maps[w][lane];
+        state = mad(v.a, state, v.h);
     }
     if (warp == kWarps - 1 && place % kGroup == kGroup - 1 && place + 1 < t.count) {
-        Words<V> w;
-#pragma unroll
-        for (int j = 0; j < V; ++j) w.w[j] = word_of({0.0f, fmaf(tile_map[j].a, state[j], tile_map[j].h)});
-        publish(ends + (int64_t)(group + 1) * (32 * V), w);
+        fill(m.a, 0.0f);
+        m.h = mad(tile_map.a, state, tile_map.h);
+        publish(ends + (int64_t)(group + 1) * (32 * V), Words<V>::of(m));
     }
+    return state;
 }
 
-// ---- gates -------------------------------------------------------------------------------
+// ---- runs of tokens ------------------------------------------------------------------------
+
+// A warp's run of an array: a lane's elements of token after token, in the recurrence's
+// order.
+template <typename T, int V>
+struct Run {
+    using R = Raw<T, V>;
+    T *at;
+    int64_t step;
+
+    __device__ __forceinline__ Run(const RecurrenceArgs &a, const Tokens &t, const Tile &tile, int k, int c)
+    {
+        at = (T *)t.data + tile.b * t.batch + (int64_t)(a.reverse ? tile.length - 1 - k : k) * t.token + c;
+        step = a.reverse ? -t.token : t.token;
+    }
+    // N tokens of which `count` (the same in a warp) are there; the others as 0.
+    template <int N>
+    __device__ __forceinline__ void load(R (&r)[N], int count) const
+    {
+        const T *p = at;
+        if (count == N) {
+#pragma unroll
+            for (int i = 0; i < N; ++i, p += step) r[i] = *(const R *)p;
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i, p += step) {
+                clear(r[i]);
+                if (i < count) r[i] = *(const R *)p;
+            }
+        }
+    }
+    __device__ __forceinline__ void store(int i, const Lanes<V> &v) const { *(R *)(at + i * step) = raw_of<T, V>(v); }
+};
+
+template <typename T, int V>
+__device__ __forceinline__ void clear_tokens(const Tokens &t, int b, int from, int to, int c)
+{
+    Raw<T, V> zero;
+    clear(zero);
+    T *p = (T *)t.data + b * t.batch + (int64_t)from * t.token + c;
+    for (int k = from; k < to; ++k, p += t.token) *(Raw<T, V> *)p = zero;
+}
 
 // exp(-x) for x >= 0.  For f32 the product x log2(e) is kept to twice float's length.
 template <typename T>
@@ -267,264 +349,271 @@ __device__ __forceinline__ float exp_minus(float x)
     return x < 120.0f ? fmaf(e, lo * kLn2, e) : e;   // (beyond, 0; the products may not be finite)
 }
 
-// The step's weight: the smaller of a and 1 - a, below 0 (or -0) where it is 1 - a.
+// a = sigmoid(f) and s = 1 - a.
 template <typename T>
-__device__ __forceinline__ float gate_weight(float f)
+__device__ __forceinline__ void split(float f, float &a, float &s)
 {
-    const float e = exp_minus<T>(fabsf(f)), w = e * rcp_fast(1.0f + e);
-    return __uint_as_float(__float_as_uint(w) | (~__float_as_uint(f) & 0x80000000u));
+    const float e = exp_minus<T>(fabsf(f)), large = rcp_fast(1.0f + e), small = e * large;
+    a = f < 0.0f ? small : large;
+    s = f < 0.0f ? large : small;
 }
 
-__device__ __forceinline__ bool keeps(float c) { return __float_as_int(c) < 0; }
-
-// h -> a h + (1 - a) x
-__device__ __forceinline__ float step(float c, float h, float x) { return fmaf(c, h - x, keeps(c) ? h : x); }
-// v -> a v
-__device__ __forceinline__ float keep(float c, float v) { return fmaf(c, v, keeps(c) ? v : 0.0f); }
+template <typename T>
+__device__ __forceinline__ void split(float2 f, float2 &a, float2 &s)
+{
+    split<T>(f.x, a.x, s.x);
+    split<T>(f.y, a.y, s.y);
+}
 
 template <typename T>
 __device__ __forceinline__ float sigmoid(float o)
 {
-    const float e = exp_minus<T>(fabsf(o)), r = rcp_fast(1.0f + e);
-    return o < 0.0f ? e * r : r;
+    if constexpr (sizeof(T) == 2) return rcp_fast(1.0f + exp2_fast(o * -1.4426950408889634f));
+    float a, s;
+    split<T>(o, a, s);
+    return a;
+}
+
+template <typename T>
+__device__ __forceinline__ float2 sigmoid(float2 o)
+{
+    return make_float2(sigmoid<T>(o.x), sigmoid<T>(o.y));
+}
+
+// Walks the block's tiles: its own, or tickets as long as there are some.  The next
+// ticket is asked for while a tile is worked on.
+template <typename F>
+__device__ __forceinline__ void for_tiles(const RecurrenceArgs &a, F f)
+{
+    if (!a.ticket) {
+        f(blockIdx.x);
+        return;
+    }
+    __shared__ uint32_t s_ticket[2];
+    uint32_t next = 0;
+    if (threadIdx.x == 0) next = atomicAdd(a.ticket, 1u) + 1u;
+    for (int turn = 0;; turn ^= 1) {
+        if (threadIdx.x == 0) s_ticket[turn] = next;
+        __syncthreads();   // (also: the last tile's shared memory has been read)
+        const uint32_t n = s_ticket[turn];
+        if (n >= a.work) return;
+        if (threadIdx.x == 0) next = atomicAdd(a.ticket, 1u) + 1u;
+        f(n);
+    }
 }
 
 // ---- forward -----------------------------------------------------------------------------
 
 template <typename T, int V, bool GATE>
-__global__ void __launch_bounds__(kThreads, 2) k_recurrence(const RecurrenceArgs a)
+__device__ __forceinline__ void forward_tile(const RecurrenceArgs &a, const Tile &t, Map<V> (*s_maps)[kWarps][32],
+                                             Lanes<V> *s_seed)
 {
-    grid_dependency_begin();
-    __shared__ Map s_maps[2][kWarps][32 * V];
-    __shared__ float s_seed[32 * V];
-    const Tile t = take_tile(a, kTile, false);
+    using F = Lanes<V>;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int c0 = t.slab * (32 * V) + lane * V;
-    const bool mine = c0 < a.channels;
-    const int k0 = t.index * kTile + warp * kRun;
-    const int count = mine ? min(max(t.length - k0, 0), kRun) : 0;
-    if (mine) clear_tokens<T, V>(a, a.out, t.b, max(k0, t.length), min(k0 + kRun, a.tokens), c0);
-    const int64_t at_state = (int64_t)t.b * a.channels + c0;
-    load_seed<V>(a, warp, mine && t.index == 0, at_state, s_seed + lane * V);
+    const int own_c = t.slab * (32 * V) + lane * V, c = min(own_c, a.channels - V);
+    const bool mine = own_c == c;   // (other lanes compute the last one's channels)
+    const int k0 = t.index * kTile + warp * kRun, count = min(max(t.length - k0, 0), kRun);
+    if (mine) clear_tokens<T, V>(a.out, t.b, max(k0, t.length), min(k0 + kRun, a.tokens), c);
+    const int64_t at_state = (int64_t)t.b * a.channels + c;
+    load_seed<V>(a, warp, t.index == 0, at_state, s_seed + lane);
     if (t.index >= t.count) {
-        if (t.length == 0 && t.index == 0 && warp == kWarps - 1 && mine)
-#pragma unroll
-            for (int j = 0; j < V; ++j) a.final[at_state + j] = s_seed[lane * V + j];
+        if (t.length == 0 && t.index == 0 && warp == kWarps - 1 && mine) store_state<V>(a.final + at_state, s_seed[lane]);
         return;
     }
 
-    using Access = Vec<T, V>;
-    Access x[kRun], o[kRun];
-    float c[kRun][V];
+    F keep[kRun], enter[kRun];   // a and (1 - a) x
+    Raw<T, V> o[kRun];
     {
-        const Walk wx = walk(a, a.x, t, k0, c0), wf = walk(a, a.forget, t, k0, c0), wo = walk(a, a.gate, t, k0, c0);
-        Access f[kRun];
-#pragma unroll
-        for (int i = 0; i < kRun; ++i)
-            if (i < count) {
-                f[i] = *(const Access *)((const T *)a.forget.data + wf.first + i * wf.step);
-                x[i] = *(const Access *)((const T *)a.x.data + wx.first + i * wx.step);
-                if (GATE) o[i] = *(const Access *)((const T *)a.gate.data + wo.first + i * wo.step);
-            }
-#pragma unroll
-        for (int i = 0; i < kRun; ++i)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                if (i >= count) x[i].e[j] = from_float<T>(0.0f);
-                c[i][j] = i < count ? gate_weight<T>(to_float(f[i].e[j])) : -0.0f;   // no step
-            }
-    }
-    Map own[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        own[j] = {1.0f, 0.0f};
+        Raw<T, V> x[kRun], f[kRun];
+        Run<T, V>(a, a.forget, t, k0, c).load(f, count);
+        Run<T, V>(a, a.x, t, k0, c).load(x, count);
+        if (GATE) Run<T, V>(a, a.gate, t, k0, c).load(o, count);
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
-            own[j].h = step(c[i][j], own[j].h, to_float(x[i].e[j]));
-            own[j].a = keep(c[i][j], own[j].a);
+            F s;
+            split<T>(value_of<T, V>(f[i]), keep[i], s);
+            enter[i] = mul(s, value_of<T, V>(x[i]));
         }
-        s_maps[0][warp][lane * V + j] = own[j];
+        if (count < kRun)
+#pragma unroll
+            for (int i = 0; i < kRun; ++i)
+                if (i >= count) {   // no step
+                    fill(keep[i], 1.0f);
+                    fill(enter[i], 0.0f);
+                }
     }
-    __syncthreads();
-    // The warps in front of this one, and for the last warp the tile.
-    Map before[V], all[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        before[j] = {1.0f, 0.0f};
-        for (int w = 0; w < warp; ++w) before[j] = then(before[j], s_maps[0][w][lane * V + j]);
-        all[j] = then(before[j], own[j]);
-    }
-    float h[V];
-    chain<V>(a, t, t.index, all, s_seed + lane * V, s_maps[1], h);
-#pragma unroll
-    for (int j = 0; j < V; ++j) h[j] = fmaf(before[j].a, h[j], before[j].h);
-    if (count == 0) return;
-
-    if (a.states && k0 % kStateStep == 0)
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            a.states[((int64_t)t.b * a.blocks + k0 / kStateStep) * a.channels + c0 + j] = h[j];
-    const Walk wy = walk(a, a.out, t, k0, c0);
+    Map<V> own;
+    fill(own.a, 1.0f);
+    fill(own.h, 0.0f);
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
-        float y[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            y[j] = h[j] = step(c[i][j], h[j], to_float(x[i].e[j]));
-            if (GATE) {
-                const float g = to_float(o[i].e[j]);
-                y[j] *= g * sigmoid<T>(g);
-            }
+        own.h = mad(keep[i], own.h, enter[i]);
+        own.a = mul(keep[i], own.a);
+    }
+    s_maps[0][warp][lane] = own;
+    __syncthreads();
+    // The warps in front of this one, and with them the tile's map in the last warp.
+    Map<V> before;
+    fill(before.a, 1.0f);
+    fill(before.h, 0.0f);
+    for (int w = 0; w < warp; ++w) before = then(before, s_maps[0][w][lane]);
+    F h = chain<V>(a, t, t.index, then(before, own), s_seed[lane], s_maps[1]);
+    h = mad(before.a, h, before.h);
+    if (count == 0 || !mine) return;
+
+    if (a.states && k0 % kStateStep == 0)
+        store_state<V>(a.states + ((int64_t)t.b * a.blocks + k0 / kStateStep) * a.channels + c, h);
+    const Run<T, V> out(a, a.out, t, k0, c);
+    auto token = [&](int i) {
+        h = mad(keep[i], h, enter[i]);
+        if constexpr (GATE) {
+            const F g = value_of<T, V>(o[i]);
+            return mul(h, mul(g, sigmoid<T>(g)));
+        } else {
+            return h;
         }
-        if (i < count) {
-            Access out;
-            if constexpr (V == 1)
-                out.e[0] = from_float<T>(y[0]);
-            else
-                set_pair(out, 0, make_float2(y[0], y[V - 1]));
-            *(Access *)((T *)a.out.data + wy.first + i * wy.step) = out;
+    };
+    if (count == kRun) {
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) out.store(i, token(i));
+    } else {
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
+            const F y = token(i);
+            if (i < count) out.store(i, y);
         }
     }
-    if (k0 < t.length && k0 + kRun >= t.length)
-#pragma unroll
-        for (int j = 0; j < V; ++j) a.final[at_state + j] = h[j];
+    if (k0 + kRun >= t.length) store_state<V>(a.final + at_state, h);
+}
+
+template <typename T, int V, bool GATE>
+__global__ void __launch_bounds__(kThreads, 2) k_recurrence(const RecurrenceArgs a)
+{
+    grid_dependency_begin();
+    __shared__ Map<V> s_maps[2][kWarps][32];
+    __shared__ Lanes<V> s_seed[32];
+    for_tiles(a, [&](uint32_t n) { forward_tile<T, V, GATE>(a, tile_at(a, n, kTile, false), s_maps, s_seed); });
 }
 
 // ---- backward ----------------------------------------------------------------------------
 
 template <typename T, int V, bool GATE>
-__global__ void __launch_bounds__(kThreads, 2) k_recurrence_grad(const RecurrenceArgs a)
+__device__ __forceinline__ void backward_tile(const RecurrenceArgs &a, const Tile &t, Map<V> (*s_maps)[kWarps][32],
+                                              Lanes<V> (*s_h)[32], Lanes<V> *s_seed)
 {
-    grid_dependency_begin();
-    __shared__ Map s_maps[2][kWarps][32 * V];
-    __shared__ float s_h[kWarps][32 * V], s_seed[32 * V];
-    const Tile t = take_tile(a, kGradTile, true);
+    using F = Lanes<V>;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int c0 = t.slab * (32 * V) + lane * V;
-    const bool mine = c0 < a.channels;
-    const int k0 = t.index * kGradTile + warp * kGradRun;
-    const int count = mine ? min(max(t.length - k0, 0), kGradRun) : 0;
+    const int own_c = t.slab * (32 * V) + lane * V, c = min(own_c, a.channels - V);
+    const bool mine = own_c == c;
+    const int k0 = t.index * kGradTile + warp * kGradRun, count = min(max(t.length - k0, 0), kGradRun);
     if (mine) {
         const int from = max(k0, t.length), to = min(k0 + kGradRun, a.tokens);
-        clear_tokens<T, V>(a, a.dx, t.b, from, to, c0);
-        clear_tokens<T, V>(a, a.dforget, t.b, from, to, c0);
-        if (GATE) clear_tokens<T, V>(a, a.dgate, t.b, from, to, c0);
+        clear_tokens<T, V>(a.dx, t.b, from, to, c);
+        clear_tokens<T, V>(a.dforget, t.b, from, to, c);
+        if (GATE) clear_tokens<T, V>(a.dgate, t.b, from, to, c);
     }
-    const int64_t at_state = (int64_t)t.b * a.channels + c0;
+    const int64_t at_state = (int64_t)t.b * a.channels + c;
     const int place = t.count - 1 - t.index;   // in the chain, which starts at the last token
-    load_seed<V>(a, warp, mine && (place == 0 || t.length == 0), at_state, s_seed + lane * V);
+    load_seed<V>(a, warp, place == 0 || t.length == 0, at_state, s_seed + lane);
     if (place < 0) {
         if (t.length == 0 && t.index == 0 && warp == kWarps - 1 && mine && a.final)
-#pragma unroll
-            for (int j = 0; j < V; ++j) a.final[at_state + j] = s_seed[lane * V + j];
+            store_state<V>(a.final + at_state, s_seed[lane]);
         return;
     }
 
-    using Access = Vec<T, V>;
-    Access x[kGradRun], o[kGradRun], dy[kGradRun];
-    float c[kGradRun][V], sig[kGradRun][V], before[V];
+    // dout silu(o): dL/dh_t without what comes from behind; dout silu'(o).
+    F keep[kGradRun], rest[kGradRun], into[kGradRun], slope[kGradRun], before;
+    Raw<T, V> x[kGradRun];
     {
-        const Walk wx = walk(a, a.x, t, k0, c0), wf = walk(a, a.forget, t, k0, c0), wo = walk(a, a.gate, t, k0, c0),
-                   wd = walk(a, a.dout, t, k0, c0);
-        Access f[kGradRun];
-#pragma unroll
-        for (int i = 0; i < kGradRun; ++i)
-            if (i < count) {
-                f[i] = *(const Access *)((const T *)a.forget.data + wf.first + i * wf.step);
-                x[i] = *(const Access *)((const T *)a.x.data + wx.first + i * wx.step);
-                dy[i] = *(const Access *)((const T *)a.dout.data + wd.first + i * wd.step);
-                if (GATE) o[i] = *(const Access *)((const T *)a.gate.data + wo.first + i * wo.step);
-            }
+        Raw<T, V> f[kGradRun], dy[kGradRun], o[kGradRun];
+        Run<T, V>(a, a.forget, t, k0, c).load(f, count);
+        Run<T, V>(a, a.x, t, k0, c).load(x, count);
+        Run<T, V>(a, a.dout, t, k0, c).load(dy, count);
+        if (GATE) Run<T, V>(a, a.gate, t, k0, c).load(o, count);
 #pragma unroll
         for (int j = 0; j < V; ++j)
-            before[j] = mine ? a.states[((int64_t)t.b * a.blocks + t.index) * a.channels + c0 + j] : 0.0f;
-#pragma unroll
-        for (int i = 0; i < kGradRun; ++i)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                if (i >= count) {
-                    x[i].e[j] = dy[i].e[j] = from_float<T>(0.0f);
-                    if (GATE) o[i].e[j] = from_float<T>(0.0f);
-                }
-                c[i][j] = i < count ? gate_weight<T>(to_float(f[i].e[j])) : -0.0f;   // no step
-                sig[i][j] = GATE ? sigmoid<T>(to_float(o[i].e[j])) : 1.0f;
-            }
-    }
-    // dL/dh_t without what comes from behind.
-    auto into = [&](int i, int j) {
-        const float d = to_float(dy[i].e[j]);
-        return GATE ? d * (to_float(o[i].e[j]) * sig[i][j]) : d;
-    };
-    Map own[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        float h = 0.0f;
-        own[j] = {1.0f, 0.0f};
+            at(before, j) = a.states[((int64_t)t.b * a.blocks + t.index) * a.channels + c + j];
 #pragma unroll
         for (int i = 0; i < kGradRun; ++i) {
-            h = step(c[i][j], h, to_float(x[i].e[j]));
-            own[j].a = keep(c[i][j], own[j].a);
+            split<T>(value_of<T, V>(f[i]), keep[i], rest[i]);
+            const F d = value_of<T, V>(dy[i]);
+            if constexpr (GATE) {
+                const F g = value_of<T, V>(o[i]), s = sigmoid<T>(g);
+                into[i] = mul(d, mul(g, s));
+                F one;
+                fill(one, 1.0f);
+                slope[i] = mul(d, mul(s, mad(g, mad(minus(s), one, one), one)));
+            } else {
+                into[i] = d;
+            }
         }
+        if (count < kGradRun)
 #pragma unroll
-        for (int i = kGradRun - 1; i >= 0; --i) own[j].h = keep(c[i][j], own[j].h + into(i, j));
-        s_maps[0][warp][lane * V + j] = own[j];
-        s_h[warp][lane * V + j] = h;
+            for (int i = 0; i < kGradRun; ++i)
+                if (i >= count) {   // no step (its x and dout are 0)
+                    fill(keep[i], 1.0f);
+                    fill(rest[i], 0.0f);
+                }
     }
+    Map<V> own;
+    F h;
+    fill(h, 0.0f);
+    fill(own.a, 1.0f);
+    fill(own.h, 0.0f);
+#pragma unroll
+    for (int i = 0; i < kGradRun; ++i) {
+        h = mad(keep[i], h, mul(rest[i], value_of<T, V>(x[i])));
+        own.a = mul(keep[i], own.a);
+    }
+#pragma unroll
+    for (int i = kGradRun - 1; i >= 0; --i) own.h = mul(keep[i], add(own.h, into[i]));
+    s_maps[0][warp][lane] = own;
+    s_h[warp][lane] = h;
     __syncthreads();
-    // h in front of this warp's run; the gradient's map of the warps behind it.  The last
-    // warp to fold, of the chain's, is kWarps - 1: it takes the tile's map.
-    Map behind[V], all[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        for (int w = 0; w < warp; ++w) before[j] = fmaf(s_maps[0][w][lane * V + j].a, before[j], s_h[w][lane * V + j]);
-        behind[j] = {1.0f, 0.0f};
-        for (int w = kWarps - 1; w > warp; --w) behind[j] = then(behind[j], s_maps[0][w][lane * V + j]);
-        all[j] = own[j];
-        if (warp == kWarps - 1)
-            for (int w = kWarps - 2; w >= 0; --w) all[j] = then(all[j], s_maps[0][w][lane * V + j]);
-    }
-    float p[V];
-    chain<V>(a, t, place, all, s_seed + lane * V, s_maps[1], p);
-    if (count == 0) return;
-#pragma unroll
-    for (int j = 0; j < V; ++j) p[j] = fmaf(behind[j].a, p[j], behind[j].h);
+    // h in front of this warp's run, and the gradient's map of the warps behind it; the
+    // tile's map in the warp that publishes.
+    for (int w = 0; w < warp; ++w) before = mad(s_maps[0][w][lane].a, before, s_h[w][lane]);
+    Map<V> behind, all = own;
+    fill(behind.a, 1.0f);
+    fill(behind.h, 0.0f);
+    for (int w = kWarps - 1; w > warp; --w) behind = then(behind, s_maps[0][w][lane]);
+    if (warp == kWarps - 1)
+        for (int w = kWarps - 2; w >= 0; --w) all = then(all, s_maps[0][w][lane]);
+    F p = chain<V>(a, t, place, all, s_seed[lane], s_maps[1]);
+    if (count == 0 || !mine) return;
+    p = mad(behind.a, p, behind.h);
 
-    float h[kGradRun + 1][V];   // in front of each token, and behind the last
+    F hs[kGradRun + 1];   // in front of each token, and behind the last
+    hs[0] = before;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        h[0][j] = before[j];
+    for (int i = 0; i < kGradRun; ++i) hs[i + 1] = mad(keep[i], hs[i], mul(rest[i], value_of<T, V>(x[i])));
+    const Run<T, V> dx(a, a.dx, t, k0, c), df(a, a.dforget, t, k0, c), dg(a, a.dgate, t, k0, c);
+    auto token = [&](int i, bool there) {
+        const F dh = add(p, into[i]);
+        p = mul(keep[i], dh);
+        if (!there) return;
+        const F enter = mul(dh, rest[i]);
+        dx.store(i, enter);
+        df.store(i, mul(mul(enter, keep[i]), add(hs[i], minus(value_of<T, V>(x[i])))));
+        if constexpr (GATE) dg.store(i, mul(slope[i], hs[i + 1]));
+    };
+    if (count == kGradRun) {
 #pragma unroll
-        for (int i = 0; i < kGradRun; ++i) h[i + 1][j] = step(c[i][j], h[i][j], to_float(x[i].e[j]));
+        for (int i = kGradRun - 1; i >= 0; --i) token(i, true);
+    } else {
+#pragma unroll
+        for (int i = kGradRun - 1; i >= 0; --i) token(i, i < count);
     }
-    const Walk wx = walk(a, a.dx, t, k0, c0), wf = walk(a, a.dforget, t, k0, c0), wo = walk(a, a.dgate, t, k0, c0);
-#pragma unroll
-    for (int i = kGradRun - 1; i >= 0; --i) {
-        float gx[V], gf[V], go[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float dh = p[j] + into(i, j), w = fabsf(c[i][j]);
-            p[j] = keep(c[i][j], dh);
-            gx[j] = dh * (keeps(c[i][j]) ? w : 1.0f - w);
-            gf[j] = dh * (h[i][j] - to_float(x[i].e[j])) * fmaf(-w, w, w);
-            const float g = to_float(o[i].e[j]), s = sig[i][j];
-            go[j] = GATE ? to_float(dy[i].e[j]) * h[i + 1][j] * (s * fmaf(g, 1.0f - s, 1.0f)) : 0.0f;
-        }
-        if (i >= count) continue;
-        auto store = [&](const Tokens &to, const Walk &w, const float (&v)[V]) {
-            Access out;
-            if constexpr (V == 1)
-                out.e[0] = from_float<T>(v[0]);
-            else
-                set_pair(out, 0, make_float2(v[0], v[V - 1]));
-            *(Access *)((T *)to.data + w.first + i * w.step) = out;
-        };
-        store(a.dx, wx, gx);
-        store(a.dforget, wf, gf);
-        if (GATE) store(a.dgate, wo, go);
-    }
-    if (t.index == 0 && warp == 0 && a.final)
-#pragma unroll
-        for (int j = 0; j < V; ++j) a.final[at_state + j] = p[j];
+    if (k0 == 0 && a.final) store_state<V>(a.final + at_state, p);
+}
+
+template <typename T, int V, bool GATE>
+__global__ void __launch_bounds__(kThreads, 2) k_recurrence_grad(const RecurrenceArgs a)
+{
+    grid_dependency_begin();
+    __shared__ Map<V> s_maps[2][kWarps][32];
+    __shared__ Lanes<V> s_h[kWarps][32], s_seed[32];
+    for_tiles(a, [&](uint32_t n) { backward_tile<T, V, GATE>(a, tile_at(a, n, kGradTile, true), s_maps, s_h, s_seed); });
 }
 
 // ---- host --------------------------------------------------------------------------------
@@ -584,7 +673,9 @@ int run(gsr_ctx *ctx, RecurrenceArgs &a, cudaStream_t stream)
         kernel = a.gate.data ? k_recurrence_grad<T, V, true> : k_recurrence_grad<T, V, false>;
     else
         kernel = a.gate.data ? k_recurrence<T, V, true> : k_recurrence<T, V, false>;
-    const dim3 grid((unsigned)((int64_t)a.tiles * a.batch * a.slabs));
+    a.work = (uint32_t)a.tiles * a.batch * a.slabs;
+    const uint32_t most = a.tiles > 1 ? 2u * ctx->num_sms : a.work;
+    const dim3 grid(a.work < most ? a.work : most);
     if (int rc = cuda_check(ctx, launch_kernel(ctx, kernel, grid, kThreads, stream, a), what)) return rc;
     return workspace.done();
 }
