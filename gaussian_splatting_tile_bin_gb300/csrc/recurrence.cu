@@ -5,38 +5,51 @@
 // and with dh_t = dout_t silu(o_t) + a_(t+1) dh_(t+1)
 //   dx = dh (1 - a),  df = dh (h_(t-1) - x) a (1 - a),  do = dout h silu'(o).
 //
-// Bound by HBM.  A block takes a tile of tokens by 32 or 64 channels, each warp a run
-// of tokens, whose values stay in registers: a run's effect on the state before it is
-// affine, h -> A h + H, and so is a warp's, a tile's and a chain of tiles'.  The tile
-// reads its inputs once, composes its (A, H), takes the state in front of it from the
-// tiles before, and then runs its tokens from that state.  The backward does the same
-// from the end with p_t = a_t dh_t, for which p -> A p + P, and computes h again from
-// the forward's states.
+// Bound by HBM.  A block takes a tile of tokens by 32 lanes of channels (128 bytes a
+// token), each of its working warps a run of tokens, whose gates stay in registers: a
+// run's effect on the state before it is affine, h -> A h + H, and so is a tile's and a
+// chain of tiles'.  The tile reads its inputs once, composes its (A, H), takes the state
+// in front of it from the tiles before, and runs its tokens from that state.  The
+// backward does the same from the end with p_t = a_t dh_t, for which p -> A p + P, and
+// computes h again from the forward's states.
 //
 // The chain.  Tiles are taken from a ticket in the chain's order, so a tile waits only
-// for blocks that run or have run.  Each publishes its (A, H); every kGroup-th also the
-// state behind it, and a tile folds what its group's tiles before it have published:
-// the composition does not depend on timing, so results are the same bits on every
-// run.  A published pair is one 64-bit word, which is all ones before that (no pair
-// is: A is never that NaN).
+// for tiles that blocks work on or are done with.  Each publishes its (A, H); every
+// kGroup-th also the state behind it, and a tile folds what its group's tiles before it
+// have published: the composition does not depend on timing, so results are the same
+// bits on every run.  A published pair is one 64-bit word, which is all ones before that
+// (no pair is: A is never that NaN).
+//
+// A block's warps.  Eight work on runs.  One takes tickets and starts the tiles' copies
+// into a ring of stages.  One follows the chain, beside the copies and the working warps,
+// so that the state is mostly there when they need it.  One composes the runs' maps,
+// publishes the tile's and hands each run the map of those in front of it.
 //
 // Numerics.  With e = exp(-|f|), the larger of a and 1 - a is 1 / (1 + e) and the smaller
 // e / (1 + e): neither is taken as a difference, so gates near 0 and 1 lose nothing.
+#include <initializer_list>
 #include <type_traits>
 
-#include "decoder.cuh"
+#include "tensor.cuh"
 
 namespace gsr {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kGroup = 4 * kWarps;         // tiles of a group: four for each warp to fold
+constexpr int kWarps = 8;                  // that work on runs
+constexpr int kComposeWarp = kWarps, kChainWarp = kWarps + 1, kFetchWarp = kWarps + 2;
+constexpr int kThreads = 32 * (kWarps + 4);
+constexpr int kBlocks = 2;                 // of an SM
+// Registers of a thread: the start's, and after the warps beside the runs have given
+// theirs to the others.
+constexpr int kStart = 80, kFew = 48, kMany = 96;
+static_assert(kWarps == 8 && 4 * kFew + 8 * kMany <= 12 * kStart, "the shares must fit what a block starts with");
+constexpr int kGroup = 32, kAhead = 4;     // tiles of a group; words in flight of the warp that folds them
 constexpr int kRun = 16, kGradRun = 8;     // tokens of a warp
 constexpr int kTile = kWarps * kRun, kGradTile = kWarps * kGradRun;
+constexpr int kStages = 2, kGradStages = 3;
+constexpr int kRowBytes = 128;             // of a token in a stage
 constexpr int kStateStep = GSR_RECURRENCE_BLOCK;
 static_assert(kStateStep % kRun == 0 && kGradTile == kStateStep, "states lie where runs and tiles start");
-constexpr long long kChainCycles = 4000000000ll;   // of a wait: seconds, where a tile takes microseconds
 
 struct Tokens {
     void *data;
@@ -79,17 +92,15 @@ __device__ __forceinline__ float &at(float2 &v, int j) { return j ? v.y : v.x; }
 __device__ __forceinline__ float at(const float &v, int) { return v; }
 __device__ __forceinline__ float at(const float2 &v, int j) { return j ? v.y : v.x; }
 
-// Bits of a thread's elements of one token.
+// Bits of a thread's elements of one token: a float, a pair of 16 bits, or one.
 template <typename T, int V>
-using Raw = std::conditional_t<sizeof(T) * V == 8, uint2, std::conditional_t<sizeof(T) * V == 4, uint32_t, uint16_t>>;
+using Raw = std::conditional_t<sizeof(T) * V == 4, uint32_t, uint16_t>;
 
 template <typename T, int V>
 __device__ __forceinline__ Lanes<V> value_of(const Raw<T, V> &r)
 {
     if constexpr (V == 1) {
         return to_float(*(const T *)&r);
-    } else if constexpr (sizeof(T) == 4) {
-        return make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
     } else if constexpr (std::is_same_v<T, __half>) {
         return __half22float2(*(const __half2 *)&r);
     } else {
@@ -103,14 +114,11 @@ __device__ __forceinline__ Raw<T, V> raw_of(Lanes<V> v)
     if constexpr (V == 1) {
         const T t = from_float<T>(v);
         return *(const Raw<T, V> *)&t;
-    } else if constexpr (sizeof(T) == 4) {
-        return make_uint2(__float_as_uint(v.x), __float_as_uint(v.y));
     } else {
         return pack2<T>(v.x, v.y);
     }
 }
 
-__device__ __forceinline__ void clear(uint2 &r) { r = make_uint2(0, 0); }
 __device__ __forceinline__ void clear(uint32_t &r) { r = 0; }
 __device__ __forceinline__ void clear(uint16_t &r) { r = 0; }
 
@@ -189,7 +197,7 @@ __device__ __forceinline__ void wait_for(const RecurrenceArgs &a, const unsigned
         if (ready(v)) return;
         if (turn % 64 != 0) continue;
         if (*(volatile uint32_t *)a.aborted == 0) return;
-        if (clock64() - start > kChainCycles) {
+        if (clock64() - start > kWaitCycles) {
             *(volatile uint32_t *)a.aborted = 0;
             *(volatile uint32_t *)a.status = 1;
             return;
@@ -197,35 +205,32 @@ __device__ __forceinline__ void wait_for(const RecurrenceArgs &a, const unsigned
     }
 }
 
-// ---- tiles -------------------------------------------------------------------------------
-
 struct Tile {
     int b, slab, index;    // item, channel slab, place along the tokens
     int length, count;     // the item's tokens and tiles
 };
 
 // The n-th tile in the order of the chains.
-__device__ __forceinline__ Tile tile_at(const RecurrenceArgs &a, uint32_t n, int tile_tokens, bool backward)
+template <bool BACKWARD>
+__device__ __forceinline__ Tile tile_at(const RecurrenceArgs &a, uint32_t n)
 {
+    constexpr int kTokens = BACKWARD ? kGradTile : kTile;
     Tile t;
     const uint32_t chains = (uint32_t)a.batch * a.slabs, place = n / chains, chain = n - place * chains;
     t.b = chain / a.slabs;
     t.slab = chain - t.b * a.slabs;
-    t.index = backward ? a.tiles - 1 - (int)place : (int)place;
+    t.index = BACKWARD ? a.tiles - 1 - (int)place : (int)place;
     t.length = a.lengths ? min(max(a.lengths[t.b], 0), a.tokens) : a.tokens;
-    t.count = (t.length + tile_tokens - 1) / tile_tokens;
+    t.count = (t.length + kTokens - 1) / kTokens;
     return t;
 }
 
-// The state in front of a chain, read by the warp that publishes the first tile's map
-// and handed to the others: once that map is out, nobody reads the array, in which a
-// block may write the state behind the chain.
-template <int V>
-__device__ __forceinline__ void load_seed(const RecurrenceArgs &a, int warp, bool here, int64_t from, Lanes<V> *seed)
+// A tile's place in its chain, which the backward starts at the last token; below 0, or
+// no less than t.count, for tiles behind an item's tokens.
+template <bool BACKWARD>
+__device__ __forceinline__ int place_of(const Tile &t)
 {
-    if (warp != kWarps - 1) return;
-#pragma unroll
-    for (int j = 0; j < V; ++j) at(*seed, j) = here && a.initial ? a.initial[from + j] : 0.0f;
+    return BACKWARD ? t.count - 1 - t.index : t.index;
 }
 
 template <int V>
@@ -235,64 +240,204 @@ __device__ __forceinline__ void store_state(float *to, const Lanes<V> &v)
     for (int j = 0; j < V; ++j) to[j] = at(v, j);
 }
 
-// The state in front of the block's tile, for this lane's channels.  `tile_map`: the
-// tile's own map (warp kWarps - 1 has it); `seed`: the state in front of the first tile (0 for others).
-// place: the tile's in its chain of t.count.
-template <int V>
-__device__ __forceinline__ Lanes<V> chain(const RecurrenceArgs &a, const Tile &t, int place, const Map<V> &tile_map,
-                                          const Lanes<V> &seed, Map<V> (*s_maps)[32])
+// What a block's warps share.
+template <int V, int S>
+struct Shared {
+    Map<V> runs[kWarps][32];         // the runs' maps
+    Map<V> before[kWarps][32];       // of the runs in front of each
+    Map<V> tile[2][32];              // the tile's, in turn
+    Lanes<V> carry[2][32];           // the state in front of the tile, in turn
+    Lanes<V> h[kWarps][32];          // backward: H of the runs' forward maps, and h in front of each
+    Lanes<V> h_before[kWarps][32];
+    Tile tiles[S];
+    uint32_t last[S];                // no tile: the tickets are at an end
+    uint64_t known[S], full[S], empty[S];
+    uint64_t runs_ready, state_ready;
+    uint32_t aborted;
+};
+
+// A warp's arrival: what its lanes have written is there for who waits.
+__device__ __forceinline__ void warp_arrive(uint64_t &bar)
 {
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    if (t.count == 1) return seed;
-    const int64_t row = (int64_t)t.b * a.slabs + t.slab;
-    const int groups = (a.tiles + kGroup - 1) / kGroup, group = place / kGroup;
-    unsigned long long *pairs = a.pairs + row * a.tiles * (32 * V) + lane * V;
-    unsigned long long *ends = a.ends + row * groups * (32 * V) + lane * V;
-    if (warp == kWarps - 1 && place + 1 < t.count) {
-        Map<V> m = tile_map;
-        if (place == 0) {   // as a map of no state
-            m.h = mad(m.a, seed, m.h);
-            fill(m.a, 0.0f);
+    __syncwarp();
+    if (threadIdx.x % 32 == 0) barrier_arrive(smem_address(&bar));
+}
+
+__device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFew)); }
+__device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMany)); }
+
+// ---- the warps beside the runs ---------------------------------------------------------
+
+struct Maps {
+    CUtensorMap x, forget, gate, dout;
+};
+
+__device__ __forceinline__ void copy_tokens(uint32_t to, const CUtensorMap *map, uint32_t bar, int channel, int token, int item)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(to),
+        "l"(map), "r"(bar), "r"(channel), "r"(token), "r"(item)
+        : "memory");
+}
+
+// One lane: tickets in turn, and the copies of their tiles.
+template <int V, int S, bool GATE, bool COPY, bool BACKWARD>
+__device__ __forceinline__ void fetch_tiles(const RecurrenceArgs &a, const Maps &maps, Shared<V, S> &s, uint32_t stages,
+                                            const WaitGuard &guard)
+{
+    constexpr int kTokens = BACKWARD ? kGradTile : kTile, kBytes = kTokens * kRowBytes;
+    constexpr int kArrays = 2 + (GATE ? 1 : 0) + (BACKWARD ? 1 : 0);
+    for (uint32_t i = 0;; ++i) {
+        const uint32_t n = a.ticket ? atomicAdd(a.ticket, 1u) + 1u : blockIdx.x + i * gridDim.x;
+        const uint32_t stage = i % S;
+        barrier_wait(smem_address(&s.empty[stage]), i / S & 1 ^ 1, guard);
+        const bool last = n >= a.work || guard.stop();
+        Tile t = {};
+        if (!last) t = tile_at<BACKWARD>(a, n);
+        s.tiles[stage] = t;
+        s.last[stage] = last;
+        barrier_arrive(smem_address(&s.known[stage]));
+        if (last) return;
+        if constexpr (COPY) {
+            const uint32_t full = smem_address(&s.full[stage]);
+            if (t.index >= t.count) {
+                barrier_arrive(full);
+                continue;
+            }
+            barrier_expect(full, kArrays * kBytes);
+            const int token = a.reverse ? t.length - (t.index + 1) * kTokens : t.index * kTokens;
+            uint32_t to = stages + stage * kArrays * kBytes;
+            const CUtensorMap *order[4] = {&maps.forget, &maps.x, GATE ? &maps.gate : &maps.dout, &maps.dout};
+            const Tokens *arrays[4] = {&a.forget, &a.x, GATE ? &a.gate : &a.dout, &a.dout};
+#pragma unroll
+            for (int k = 0; k < kArrays; ++k, to += kBytes)
+                copy_tokens(to, order[k], full, t.slab * 32 * V, token, arrays[k]->batch ? t.b : 0);
         }
-        publish(pairs + (int64_t)place * (32 * V), Words<V>::of(m));
     }
-    if (place == 0) return seed;
-    // Each warp folds four tiles of the group; the first one behind the group's start.
+}
+
+// Calls f(tile, stage, parity, j) for the block's tiles in turn, and leaves the stage:
+// the parity of the stage's turn, and how many tiles with tokens came before.  (Once a
+// wait has run out there may be no tile where one is looked for.)
+template <int V, int S, typename F>
+__device__ __forceinline__ void each_tile(Shared<V, S> &s, const WaitGuard &guard, F f)
+{
+    uint32_t j = 0;
+    for (uint32_t i = 0;; ++i) {
+        const uint32_t stage = i % S;
+        barrier_wait_warp(smem_address(&s.known[stage]), i / S & 1, guard);
+        if (guard.stop() || s.last[stage]) return;
+        const Tile t = s.tiles[stage];
+        f(t, stage, i / S & 1, j);
+        if (t.index < t.count) ++j;
+        warp_arrive(s.empty[stage]);
+    }
+}
+
+// Composes the runs' maps in order, publishes the tile's, and gives each run the map of
+// those in front of it.  It alone reads the state in front of a chain: once the first
+// tile's map is out nobody reads that array, in which a block may write the state behind
+// the chain.
+template <int V, int S, bool BACKWARD>
+__device__ __forceinline__ void compose_runs(const RecurrenceArgs &a, Shared<V, S> &s, const Tile &t, uint32_t j,
+                                             const WaitGuard &guard)
+{
+    const int lane = threadIdx.x % 32, c = min(t.slab * (32 * V) + lane * V, a.channels - V);
+    const int place = place_of<BACKWARD>(t);
+    if (t.index >= t.count) {
+        if (t.length == 0 && t.index == 0 && a.final)
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const int64_t state = (int64_t)t.b * a.channels + c + k;
+                a.final[state] = a.initial ? a.initial[state] : 0.0f;
+            }
+        return;
+    }
+    Lanes<V> seed, h;
+    fill(seed, 0.0f);
+    if (place == 0 && a.initial)
+#pragma unroll
+        for (int k = 0; k < V; ++k) at(seed, k) = a.initial[(int64_t)t.b * a.channels + c + k];
+    if (BACKWARD)
+#pragma unroll
+        for (int k = 0; k < V; ++k) at(h, k) = a.states[((int64_t)t.b * a.blocks + t.index) * a.channels + c + k];
+    barrier_wait_warp(smem_address(&s.runs_ready), j & 1, guard);
     Map<V> m;
     fill(m.a, 1.0f);
     fill(m.h, 0.0f);
-    const int first = group * kGroup + 4 * warp;
-    Words<V> seen[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (first + i < place) look(pairs + (int64_t)(first + i) * (32 * V), seen[i]);
-    if (warp == 0 && group > 0) {
-        Words<V> end;
-        look(ends + (int64_t)group * (32 * V), end);
-        wait_for(a, ends + (int64_t)group * (32 * V), end);
-        m = end.map();
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (first + i < place) {
-            wait_for(a, pairs + (int64_t)(first + i) * (32 * V), seen[i]);
-            m = then(m, seen[i].map());
-        }
-    s_maps[warp][lane] = m;
-    __syncthreads();
-    Lanes<V> state;
-    fill(state, 0.0f);   // (the first map of a chain takes no state)
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-        const Map<V> v = s_maps[w][lane];
-        state = mad(v.a, state, v.h);
+        const int run = BACKWARD ? kWarps - 1 - w : w;
+        s.before[run][lane] = m;
+        m = then(m, s.runs[run][lane]);
     }
-    if (warp == kWarps - 1 && place % kGroup == kGroup - 1 && place + 1 < t.count) {
+    if (place + 1 < t.count) {
+        Map<V> out = m;
+        if (place == 0) {   // as a map of no state
+            out.h = mad(out.a, seed, out.h);
+            fill(out.a, 0.0f);
+        }
+        publish(a.pairs + (((int64_t)t.b * a.slabs + t.slab) * a.tiles + place) * (32 * V) + lane * V, Words<V>::of(out));
+    }
+    if (BACKWARD)
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            s.h_before[w][lane] = h;
+            h = mad(s.runs[w][lane].a, h, s.h[w][lane]);
+        }
+    s.tile[j & 1][lane] = m;
+    if (place == 0) s.carry[j & 1][lane] = seed;
+    warp_arrive(s.state_ready);
+}
+
+// Folds the maps that the group's tiles before this one have published into the state
+// in front of it, and publishes the state behind a group.
+template <int V, int S, bool BACKWARD>
+__device__ __forceinline__ void follow_chain(const RecurrenceArgs &a, Shared<V, S> &s, const Tile &t, uint32_t j,
+                                             const WaitGuard &guard)
+{
+    if (t.index >= t.count) return;
+    const int lane = threadIdx.x % 32, place = place_of<BACKWARD>(t);
+    const int64_t row = (int64_t)t.b * a.slabs + t.slab;
+    const int groups = (a.tiles + kGroup - 1) / kGroup, group = place / kGroup;
+    const unsigned long long *pairs = a.pairs + row * a.tiles * (32 * V) + lane * V;
+    unsigned long long *ends = a.ends + row * groups * (32 * V) + lane * V;
+    Lanes<V> state;
+    if (place > 0) {
+        fill(state, 0.0f);   // (the first map of a chain takes no state)
+        Words<V> end;
+        if (group > 0) look(ends + (int64_t)group * (32 * V), end);
+        for (int first = group * kGroup; first < place; first += kAhead) {
+            Words<V> seen[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (first + k < place) look(pairs + (int64_t)(first + k) * (32 * V), seen[k]);
+            if (group > 0 && first == group * kGroup) {
+                wait_for(a, ends + (int64_t)group * (32 * V), end);
+                state = end.map().h;
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (first + k < place) {
+                    wait_for(a, pairs + (int64_t)(first + k) * (32 * V), seen[k]);
+                    const Map<V> m = seen[k].map();
+                    state = mad(m.a, state, m.h);
+                }
+        }
+        if (group > 0 && place == group * kGroup) {
+            wait_for(a, ends + (int64_t)group * (32 * V), end);
+            state = end.map().h;
+        }
+        s.carry[j & 1][lane] = state;
+    }
+    warp_arrive(s.state_ready);
+    barrier_wait_warp(smem_address(&s.state_ready), j & 1, guard);
+    if (place % kGroup == kGroup - 1 && place + 1 < t.count) {
+        Map<V> m = s.tile[j & 1][lane];
+        m.h = mad(m.a, state, m.h);
         fill(m.a, 0.0f);
-        m.h = mad(tile_map.a, state, tile_map.h);
         publish(ends + (int64_t)(group + 1) * (32 * V), Words<V>::of(m));
     }
-    return state;
 }
 
 // ---- runs of tokens ------------------------------------------------------------------------
@@ -329,6 +474,24 @@ struct Run {
     __device__ __forceinline__ void store(int i, const Lanes<V> &v) const { *(R *)(at + i * step) = raw_of<T, V>(v); }
 };
 
+// The same of a tile in a stage, a lane's 4 bytes of row after row.
+struct StagedRun {
+    uint32_t at;
+    int step;
+
+    __device__ __forceinline__ StagedRun(const RecurrenceArgs &a, uint32_t stage, int tile_tokens, int first)
+    {
+        at = stage + (a.reverse ? tile_tokens - 1 - first : first) * kRowBytes + threadIdx.x % 32 * 4;
+        step = a.reverse ? -kRowBytes : kRowBytes;
+    }
+    __device__ __forceinline__ uint32_t word(int i, int array_bytes) const
+    {
+        uint32_t w;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at + i * step + array_bytes) : "memory");
+        return w;
+    }
+};
+
 template <typename T, int V>
 __device__ __forceinline__ void clear_tokens(const Tokens &t, int b, int from, int to, int c)
 {
@@ -336,6 +499,13 @@ __device__ __forceinline__ void clear_tokens(const Tokens &t, int b, int from, i
     clear(zero);
     T *p = (T *)t.data + b * t.batch + (int64_t)from * t.token + c;
     for (int k = from; k < to; ++k, p += t.token) *(Raw<T, V> *)p = zero;
+}
+
+// A staged word's elements.
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> raw_bits(uint32_t w)
+{
+    return (Raw<T, V>)w;
 }
 
 // exp(-x) for x >= 0.  For f32 the product x log2(e) is kept to twice float's length.
@@ -380,68 +550,52 @@ __device__ __forceinline__ float2 sigmoid(float2 o)
     return make_float2(sigmoid<T>(o.x), sigmoid<T>(o.y));
 }
 
-// Walks the block's tiles: its own, or tickets as long as there are some.  The next
-// ticket is asked for while a tile is worked on.
-template <typename F>
-__device__ __forceinline__ void for_tiles(const RecurrenceArgs &a, F f)
-{
-    if (!a.ticket) {
-        f(blockIdx.x);
-        return;
-    }
-    __shared__ uint32_t s_ticket[2];
-    uint32_t next = 0;
-    if (threadIdx.x == 0) next = atomicAdd(a.ticket, 1u) + 1u;
-    for (int turn = 0;; turn ^= 1) {
-        if (threadIdx.x == 0) s_ticket[turn] = next;
-        __syncthreads();   // (also: the last tile's shared memory has been read)
-        const uint32_t n = s_ticket[turn];
-        if (n >= a.work) return;
-        if (threadIdx.x == 0) next = atomicAdd(a.ticket, 1u) + 1u;
-        f(n);
-    }
-}
-
 // ---- forward -----------------------------------------------------------------------------
 
-template <typename T, int V, bool GATE>
-__device__ __forceinline__ void forward_tile(const RecurrenceArgs &a, const Tile &t, Map<V> (*s_maps)[kWarps][32],
-                                             Lanes<V> *s_seed)
+template <typename T, int V, bool GATE, bool COPY, int S>
+__device__ __forceinline__ void forward_run(const RecurrenceArgs &a, Shared<V, S> &s, const Tile &t, uint32_t j,
+                                            uint32_t stage_at, uint32_t full, uint32_t parity, const WaitGuard &guard)
 {
     using F = Lanes<V>;
+    constexpr int kBytes = kTile * kRowBytes;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int own_c = t.slab * (32 * V) + lane * V, c = min(own_c, a.channels - V);
-    const bool mine = own_c == c;   // (other lanes compute the last one's channels)
+    const bool mine = own_c == c;   // (other lanes compute the last one's channels, or none)
     const int k0 = t.index * kTile + warp * kRun, count = min(max(t.length - k0, 0), kRun);
     if (mine) clear_tokens<T, V>(a.out, t.b, max(k0, t.length), min(k0 + kRun, a.tokens), c);
-    const int64_t at_state = (int64_t)t.b * a.channels + c;
-    load_seed<V>(a, warp, t.index == 0, at_state, s_seed + lane);
-    if (t.index >= t.count) {
-        if (t.length == 0 && t.index == 0 && warp == kWarps - 1 && mine) store_state<V>(a.final + at_state, s_seed[lane]);
-        return;
-    }
+    if (t.index >= t.count) return;
 
     F keep[kRun], enter[kRun];   // a and (1 - a) x
-    Raw<T, V> o[kRun];
-    {
+    Raw<T, V> o[GATE ? kRun : 1];
+    const StagedRun staged(a, stage_at, kTile, warp * kRun);
+    if constexpr (COPY) {
+        barrier_wait_warp(full, parity, guard);
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
+            const Raw<T, V> f = raw_bits<T, V>(staged.word(i, 0)), x = raw_bits<T, V>(staged.word(i, kBytes));
+            F r;
+            split<T>(value_of<T, V>(f), keep[i], r);
+            enter[i] = mul(r, value_of<T, V>(x));
+        }
+    } else {
         Raw<T, V> x[kRun], f[kRun];
         Run<T, V>(a, a.forget, t, k0, c).load(f, count);
         Run<T, V>(a, a.x, t, k0, c).load(x, count);
         if (GATE) Run<T, V>(a, a.gate, t, k0, c).load(o, count);
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
-            F s;
-            split<T>(value_of<T, V>(f[i]), keep[i], s);
-            enter[i] = mul(s, value_of<T, V>(x[i]));
+            F r;
+            split<T>(value_of<T, V>(f[i]), keep[i], r);
+            enter[i] = mul(r, value_of<T, V>(x[i]));
         }
-        if (count < kRun)
-#pragma unroll
-            for (int i = 0; i < kRun; ++i)
-                if (i >= count) {   // no step
-                    fill(keep[i], 1.0f);
-                    fill(enter[i], 0.0f);
-                }
     }
+    if (count < kRun)
+#pragma unroll
+        for (int i = 0; i < kRun; ++i)
+            if (i >= count) {   // no step
+                fill(keep[i], 1.0f);
+                fill(enter[i], 0.0f);
+            }
     Map<V> own;
     fill(own.a, 1.0f);
     fill(own.h, 0.0f);
@@ -450,15 +604,11 @@ __device__ __forceinline__ void forward_tile(const RecurrenceArgs &a, const Tile
         own.h = mad(keep[i], own.h, enter[i]);
         own.a = mul(keep[i], own.a);
     }
-    s_maps[0][warp][lane] = own;
-    __syncthreads();
-    // The warps in front of this one, and with them the tile's map in the last warp.
-    Map<V> before;
-    fill(before.a, 1.0f);
-    fill(before.h, 0.0f);
-    for (int w = 0; w < warp; ++w) before = then(before, s_maps[0][w][lane]);
-    F h = chain<V>(a, t, t.index, then(before, own), s_seed[lane], s_maps[1]);
-    h = mad(before.a, h, before.h);
+    s.runs[warp][lane] = own;
+    warp_arrive(s.runs_ready);
+    barrier_wait_warp(smem_address(&s.state_ready), j & 1, guard);
+    const Map<V> before = s.before[warp][lane];
+    F h = mad(before.a, s.carry[j & 1][lane], before.h);
     if (count == 0 || !mine) return;
 
     if (a.states && k0 % kStateStep == 0)
@@ -467,7 +617,7 @@ __device__ __forceinline__ void forward_tile(const RecurrenceArgs &a, const Tile
     auto token = [&](int i) {
         h = mad(keep[i], h, enter[i]);
         if constexpr (GATE) {
-            const F g = value_of<T, V>(o[i]);
+            const F g = value_of<T, V>(COPY ? raw_bits<T, V>(staged.word(i, 2 * kBytes)) : o[i]);
             return mul(h, mul(g, sigmoid<T>(g)));
         } else {
             return h;
@@ -483,25 +633,17 @@ __device__ __forceinline__ void forward_tile(const RecurrenceArgs &a, const Tile
             if (i < count) out.store(i, y);
         }
     }
-    if (k0 + kRun >= t.length) store_state<V>(a.final + at_state, h);
-}
-
-template <typename T, int V, bool GATE>
-__global__ void __launch_bounds__(kThreads, 2) k_recurrence(const RecurrenceArgs a)
-{
-    grid_dependency_begin();
-    __shared__ Map<V> s_maps[2][kWarps][32];
-    __shared__ Lanes<V> s_seed[32];
-    for_tiles(a, [&](uint32_t n) { forward_tile<T, V, GATE>(a, tile_at(a, n, kTile, false), s_maps, s_seed); });
+    if (k0 + kRun >= t.length) store_state<V>(a.final + (int64_t)t.b * a.channels + c, h);
 }
 
 // ---- backward ----------------------------------------------------------------------------
 
-template <typename T, int V, bool GATE>
-__device__ __forceinline__ void backward_tile(const RecurrenceArgs &a, const Tile &t, Map<V> (*s_maps)[kWarps][32],
-                                              Lanes<V> (*s_h)[32], Lanes<V> *s_seed)
+template <typename T, int V, bool GATE, bool COPY, int S>
+__device__ __forceinline__ void backward_run(const RecurrenceArgs &a, Shared<V, S> &s, const Tile &t, uint32_t j,
+                                             uint32_t stage_at, uint32_t full, uint32_t parity, const WaitGuard &guard)
 {
     using F = Lanes<V>;
+    constexpr int kBytes = kGradTile * kRowBytes;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int own_c = t.slab * (32 * V) + lane * V, c = min(own_c, a.channels - V);
     const bool mine = own_c == c;
@@ -512,37 +654,47 @@ __device__ __forceinline__ void backward_tile(const RecurrenceArgs &a, const Til
         clear_tokens<T, V>(a.dforget, t.b, from, to, c);
         if (GATE) clear_tokens<T, V>(a.dgate, t.b, from, to, c);
     }
-    const int64_t at_state = (int64_t)t.b * a.channels + c;
-    const int place = t.count - 1 - t.index;   // in the chain, which starts at the last token
-    load_seed<V>(a, warp, place == 0 || t.length == 0, at_state, s_seed + lane);
-    if (place < 0) {
-        if (t.length == 0 && t.index == 0 && warp == kWarps - 1 && mine && a.final)
-            store_state<V>(a.final + at_state, s_seed[lane]);
-        return;
-    }
+    if (t.index >= t.count) return;
 
     // dout silu(o): dL/dh_t without what comes from behind; dout silu'(o).
-    F keep[kGradRun], rest[kGradRun], into[kGradRun], slope[kGradRun], before;
+    F keep[kGradRun], rest[kGradRun], into[kGradRun], slope[kGradRun];
     Raw<T, V> x[kGradRun];
     {
-        Raw<T, V> f[kGradRun], dy[kGradRun], o[kGradRun];
-        Run<T, V>(a, a.forget, t, k0, c).load(f, count);
-        Run<T, V>(a, a.x, t, k0, c).load(x, count);
-        Run<T, V>(a, a.dout, t, k0, c).load(dy, count);
-        if (GATE) Run<T, V>(a, a.gate, t, k0, c).load(o, count);
+        Raw<T, V> f[kGradRun], dy[kGradRun], o[GATE ? kGradRun : 1];
+        if constexpr (COPY) {
+            const StagedRun staged(a, stage_at, kGradTile, warp * kGradRun);
+            barrier_wait_warp(full, parity, guard);
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            at(before, j) = a.states[((int64_t)t.b * a.blocks + t.index) * a.channels + c + j];
+            for (int i = 0; i < kGradRun; ++i) {
+                f[i] = raw_bits<T, V>(staged.word(i, 0));
+                x[i] = raw_bits<T, V>(staged.word(i, kBytes));
+                if (GATE) o[i] = raw_bits<T, V>(staged.word(i, 2 * kBytes));
+                dy[i] = raw_bits<T, V>(staged.word(i, (GATE ? 3 : 2) * kBytes));
+            }
+            if (count < kGradRun)
+#pragma unroll
+                for (int i = 0; i < kGradRun; ++i)
+                    if (i >= count) {
+                        clear(x[i]);
+                        clear(dy[i]);
+                        if constexpr (GATE) clear(o[i]);
+                    }
+        } else {
+            Run<T, V>(a, a.forget, t, k0, c).load(f, count);
+            Run<T, V>(a, a.x, t, k0, c).load(x, count);
+            Run<T, V>(a, a.dout, t, k0, c).load(dy, count);
+            if (GATE) Run<T, V>(a, a.gate, t, k0, c).load(o, count);
+        }
 #pragma unroll
         for (int i = 0; i < kGradRun; ++i) {
             split<T>(value_of<T, V>(f[i]), keep[i], rest[i]);
             const F d = value_of<T, V>(dy[i]);
             if constexpr (GATE) {
-                const F g = value_of<T, V>(o[i]), s = sigmoid<T>(g);
-                into[i] = mul(d, mul(g, s));
+                const F g = value_of<T, V>(o[i]), r = sigmoid<T>(g);
+                into[i] = mul(d, mul(g, r));
                 F one;
                 fill(one, 1.0f);
-                slope[i] = mul(d, mul(s, mad(g, mad(minus(s), one, one), one)));
+                slope[i] = mul(d, mul(r, mad(g, add(one, minus(r)), one)));
             } else {
                 into[i] = d;
             }
@@ -567,24 +719,16 @@ __device__ __forceinline__ void backward_tile(const RecurrenceArgs &a, const Til
     }
 #pragma unroll
     for (int i = kGradRun - 1; i >= 0; --i) own.h = mul(keep[i], add(own.h, into[i]));
-    s_maps[0][warp][lane] = own;
-    s_h[warp][lane] = h;
-    __syncthreads();
-    // h in front of this warp's run, and the gradient's map of the warps behind it; the
-    // tile's map in the warp that publishes.
-    for (int w = 0; w < warp; ++w) before = mad(s_maps[0][w][lane].a, before, s_h[w][lane]);
-    Map<V> behind, all = own;
-    fill(behind.a, 1.0f);
-    fill(behind.h, 0.0f);
-    for (int w = kWarps - 1; w > warp; --w) behind = then(behind, s_maps[0][w][lane]);
-    if (warp == kWarps - 1)
-        for (int w = kWarps - 2; w >= 0; --w) all = then(all, s_maps[0][w][lane]);
-    F p = chain<V>(a, t, place, all, s_seed[lane], s_maps[1]);
+    s.runs[warp][lane] = own;
+    s.h[warp][lane] = h;
+    warp_arrive(s.runs_ready);
+    barrier_wait_warp(smem_address(&s.state_ready), j & 1, guard);
+    const Map<V> behind = s.before[warp][lane];
+    F p = mad(behind.a, s.carry[j & 1][lane], behind.h);
     if (count == 0 || !mine) return;
-    p = mad(behind.a, p, behind.h);
 
     F hs[kGradRun + 1];   // in front of each token, and behind the last
-    hs[0] = before;
+    hs[0] = s.h_before[warp][lane];
 #pragma unroll
     for (int i = 0; i < kGradRun; ++i) hs[i + 1] = mad(keep[i], hs[i], mul(rest[i], value_of<T, V>(x[i])));
     const Run<T, V> dx(a, a.dx, t, k0, c), df(a, a.dforget, t, k0, c), dg(a, a.dgate, t, k0, c);
@@ -604,16 +748,59 @@ __device__ __forceinline__ void backward_tile(const RecurrenceArgs &a, const Til
 #pragma unroll
         for (int i = kGradRun - 1; i >= 0; --i) token(i, i < count);
     }
-    if (k0 == 0 && a.final) store_state<V>(a.final + at_state, p);
+    if (k0 == 0 && a.final) store_state<V>(a.final + (int64_t)t.b * a.channels + c, p);
 }
 
-template <typename T, int V, bool GATE>
-__global__ void __launch_bounds__(kThreads, 2) k_recurrence_grad(const RecurrenceArgs a)
+// COPY: tiles come through the ring of stages; otherwise the runs' warps read them.
+template <typename T, int V, bool GATE, bool COPY, bool BACKWARD>
+__global__ void __launch_bounds__(kThreads, kBlocks)
+    k_recurrence(const RecurrenceArgs a, const __grid_constant__ Maps maps)
 {
     grid_dependency_begin();
-    __shared__ Map<V> s_maps[2][kWarps][32];
-    __shared__ Lanes<V> s_h[kWarps][32], s_seed[32];
-    for_tiles(a, [&](uint32_t n) { backward_tile<T, V, GATE>(a, tile_at(a, n, kGradTile, true), s_maps, s_h, s_seed); });
+    constexpr int S = BACKWARD ? kGradStages : kStages;
+    constexpr int kStageBytes = (2 + (GATE ? 1 : 0) + (BACKWARD ? 1 : 0)) * (BACKWARD ? kGradTile : kTile) * kRowBytes;
+    extern __shared__ unsigned char s_bytes[];
+    __shared__ Shared<V, S> s;
+    const uint32_t stages = (smem_address(s_bytes) + 127u) / 128u * 128u;
+    const WaitGuard guard = {&s.aborted, a.status};
+    if (threadIdx.x == 0) {
+        s.aborted = 0;
+        for (int k = 0; k < S; ++k) {
+            barrier_init(smem_address(&s.known[k]), 1);
+            barrier_init(smem_address(&s.full[k]), 1);
+            barrier_init(smem_address(&s.empty[k]), kWarps + 2);
+        }
+        barrier_init(smem_address(&s.runs_ready), kWarps);
+        barrier_init(smem_address(&s.state_ready), 2);
+        fence_async();
+    }
+    __syncthreads();
+    const int warp = threadIdx.x / 32;
+    if (warp >= kWarps) {
+        give_registers();
+        if (warp == kFetchWarp) {
+            if (threadIdx.x % 32 == 0) fetch_tiles<V, S, GATE, COPY, BACKWARD>(a, maps, s, stages, guard);
+        } else if (warp == kChainWarp) {
+            each_tile(s, guard, [&](const Tile &t, uint32_t, uint32_t, uint32_t j) {
+                follow_chain<V, S, BACKWARD>(a, s, t, j, guard);
+            });
+        } else if (warp == kComposeWarp) {
+            each_tile(s, guard, [&](const Tile &t, uint32_t, uint32_t, uint32_t j) {
+                compose_runs<V, S, BACKWARD>(a, s, t, j, guard);
+            });
+        }
+    } else {
+        take_registers();
+        each_tile(s, guard, [&](const Tile &t, uint32_t stage, uint32_t parity, uint32_t j) {
+            const uint32_t from = stages + stage * kStageBytes, full = smem_address(&s.full[stage]);
+            if constexpr (BACKWARD)
+                backward_run<T, V, GATE, COPY, S>(a, s, t, j, from, full, parity, guard);
+            else
+                forward_run<T, V, GATE, COPY, S>(a, s, t, j, from, full, parity, guard);
+        });
+    }
+    if (s.aborted && a.aborted && threadIdx.x % 32 == 0) *(volatile uint32_t *)a.aborted = 0;
+    drain_if_aborted(guard);
 }
 
 // ---- host --------------------------------------------------------------------------------
@@ -635,60 +822,96 @@ RecurrenceArgs args_of(const gsr_recurrence &d)
     return a;
 }
 
-// Whether every array can be accessed in pairs of elements.
-bool in_pairs(const RecurrenceArgs &a, int size)
+bool all_arrays(const RecurrenceArgs &a, std::initializer_list<const Tokens *> arrays, int size, int64_t unit)
 {
-    bool ok = a.channels % 2 == 0;
-    for (const Tokens *t : {&a.x, &a.forget, &a.gate, &a.out, &a.dout, &a.dx, &a.dforget, &a.dgate})
+    bool ok = true;
+    for (const Tokens *t : arrays)
         if (t->data)
-            ok = ok && (uintptr_t)t->data % (2 * size) == 0 && (a.batch == 1 || t->batch % 2 == 0) &&
-                 (a.tokens == 1 || t->token % 2 == 0);
+            ok = ok && (uintptr_t)t->data % (unit * size) == 0 && (a.batch == 1 || t->batch % unit == 0) &&
+                 (a.tokens == 1 || t->token % unit == 0);
     return ok;
 }
 
+template <typename T, int V, bool GATE, bool COPY, bool BACKWARD>
+int launch(gsr_ctx *ctx, RecurrenceArgs &a, int dtype, const char *what, cudaStream_t stream)
+{
+    constexpr int kTokens = BACKWARD ? kGradTile : kTile, kArrays = 2 + (GATE ? 1 : 0) + (BACKWARD ? 1 : 0);
+    constexpr int kBytes = COPY ? (BACKWARD ? kGradStages : kStages) * kArrays * kTokens * kRowBytes + 128 : 0;
+    Maps maps = {};
+    if (COPY) {
+        const struct { CUtensorMap *map; const Tokens *t; } inputs[4] = {
+            {&maps.x, &a.x}, {&maps.forget, &a.forget}, {&maps.gate, &a.gate}, {&maps.dout, &a.dout}};
+        for (const auto &in : inputs)
+            if (in.t->data)
+                if (int rc = tokens_map(ctx, in.map, in.t->data, dtype, a.channels, a.tokens, a.batch, in.t->token,
+                                        in.t->batch, kRowBytes / (int)sizeof(T), kTokens))
+                    return rc;
+    }
+    auto *kernel = k_recurrence<T, V, GATE, COPY, BACKWARD>;
+    // (One that starts with fewer registers than the shares add up to would wait for them.)
+    cudaFuncAttributes attributes;
+    if (int rc = cuda_check(ctx, cudaFuncGetAttributes(&attributes, kernel), what)) return rc;
+    if (attributes.numRegs < kStart) return fail(ctx, GSR_ERR_CUDA, std::string(what) + ": compiled with too few registers");
+    if (kBytes > 0)
+        if (int rc = cuda_check(ctx, cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes), what))
+            return rc;
+    const uint32_t most = (uint32_t)(kBlocks * ctx->num_sms);
+    return cuda_check(ctx, launch_kernel_smem(ctx, kernel, dim3(a.work < most ? a.work : most), kThreads, kBytes, 1, stream,
+                                              a, maps), what);
+}
+
 template <typename T, int V, bool BACKWARD>
-int run(gsr_ctx *ctx, RecurrenceArgs &a, cudaStream_t stream)
+int run(gsr_ctx *ctx, RecurrenceArgs &a, int dtype, cudaStream_t stream)
 {
     const char *what = BACKWARD ? "gated recurrence backward" : "gated recurrence forward";
-    constexpr int kTokens = BACKWARD ? kGradTile : kTile, kSlab = 32 * V;
+    constexpr int kTokens = BACKWARD ? kGradTile : kTile, kSlab = 32 * V, kUnit = 16 / (int)sizeof(T);
     a.tiles = (a.tokens + kTokens - 1) / kTokens;
     if (a.tiles == 0) a.tiles = 1;   // for the states of items without tokens
     a.slabs = (a.channels + kSlab - 1) / kSlab;
+    a.work = (uint32_t)a.tiles * a.batch * a.slabs;
     Workspace workspace(ctx, stream);
-    if (a.tiles > 1) {
-        const size_t chains = (size_t)a.batch * a.slabs, groups = (a.tiles + kGroup - 1) / kGroup;
-        const size_t pairs = chains * a.tiles * kSlab * sizeof(unsigned long long);
-        const size_t ends = chains * groups * kSlab * sizeof(unsigned long long), bytes = pairs + ends + 16;
-        void *work = nullptr;
-        if (int rc = workspace.take(bytes, &work)) return rc;
+    const bool chained = a.tiles > 1;
+    const size_t chains = (size_t)a.batch * a.slabs, groups = (a.tiles + kGroup - 1) / kGroup;
+    const size_t pairs = chained ? chains * a.tiles * kSlab * sizeof(unsigned long long) : 0;
+    const size_t ends = chained ? chains * groups * kSlab * sizeof(unsigned long long) : 0;
+    const size_t bytes = chained ? pairs + ends + 16 : 0;
+    void *work = nullptr;
+    if (int rc = workspace.take(bytes, &work)) return rc;
+    a.status = ctx->status_dev;
+    if (chained) {
         if (int rc = cuda_check(ctx, cudaMemsetAsync(work, 0xff, bytes, stream), what)) return rc;
         a.pairs = (unsigned long long *)work;
         a.ends = a.pairs + pairs / sizeof(unsigned long long);
         a.ticket = (uint32_t *)((unsigned char *)work + pairs + ends);
         a.aborted = a.ticket + 1;
-        a.status = ctx->status_dev;
     }
-    void (*kernel)(RecurrenceArgs);
-    if constexpr (BACKWARD)
-        kernel = a.gate.data ? k_recurrence_grad<T, V, true> : k_recurrence_grad<T, V, false>;
-    else
-        kernel = a.gate.data ? k_recurrence<T, V, true> : k_recurrence<T, V, false>;
-    a.work = (uint32_t)a.tiles * a.batch * a.slabs;
-    const uint32_t most = a.tiles > 1 ? 2u * ctx->num_sms : a.work;
-    const dim3 grid(a.work < most ? a.work : most);
-    if (int rc = cuda_check(ctx, launch_kernel(ctx, kernel, grid, kThreads, stream, a), what)) return rc;
+    // Copies of whole tiles where the arrays allow them and a block has more than one to come.
+    const bool copy = chained && kSlab * (int)sizeof(T) == kRowBytes &&
+                      all_arrays(a, {&a.x, &a.forget, &a.gate, &a.dout}, (int)sizeof(T), kUnit);
+    int rc;
+    if constexpr (kSlab * (int)sizeof(T) == kRowBytes) {
+        if (copy)
+            rc = a.gate.data ? launch<T, V, true, true, BACKWARD>(ctx, a, dtype, what, stream)
+                             : launch<T, V, false, true, BACKWARD>(ctx, a, dtype, what, stream);
+    }
+    if (!copy)
+        rc = a.gate.data ? launch<T, V, true, false, BACKWARD>(ctx, a, dtype, what, stream)
+                         : launch<T, V, false, false, BACKWARD>(ctx, a, dtype, what, stream);
+    if (rc != GSR_OK) return rc;
     return workspace.done();
 }
 
+// 16-bit elements in pairs where channels and arrays allow it.
 template <bool BACKWARD>
 int dispatch(gsr_ctx *ctx, RecurrenceArgs &a, int dtype, cudaStream_t stream)
 {
-    const bool pairs = in_pairs(a, dtype == GSR_F32 ? 4 : 2);
-    if (dtype == GSR_F32)
-        return pairs ? run<float, 2, BACKWARD>(ctx, a, stream) : run<float, 1, BACKWARD>(ctx, a, stream);
+    if (dtype == GSR_F32) return run<float, 1, BACKWARD>(ctx, a, dtype, stream);
+    const bool pairs = a.channels % 2 == 0 && all_arrays(a, {&a.x, &a.forget, &a.gate, &a.out, &a.dout, &a.dx, &a.dforget,
+                                                             &a.dgate}, 2, 2);
     if (dtype == GSR_BF16)
-        return pairs ? run<__nv_bfloat16, 2, BACKWARD>(ctx, a, stream) : run<__nv_bfloat16, 1, BACKWARD>(ctx, a, stream);
-    return pairs ? run<__half, 2, BACKWARD>(ctx, a, stream) : run<__half, 1, BACKWARD>(ctx, a, stream);
+        return pairs ? run<__nv_bfloat16, 2, BACKWARD>(ctx, a, dtype, stream)
+                     : run<__nv_bfloat16, 1, BACKWARD>(ctx, a, dtype, stream);
+    return pairs ? run<__half, 2, BACKWARD>(ctx, a, dtype, stream) : run<__half, 1, BACKWARD>(ctx, a, dtype, stream);
 }
 
 }  // namespace

@@ -117,6 +117,27 @@ int heads_map(gsr_ctx *ctx, CUtensorMap *map, const gsr_heads &t, int dtype, int
     return GSR_OK;
 }
 
+int tokens_map(gsr_ctx *ctx, CUtensorMap *map, void *data, int dtype, int64_t channels, int64_t tokens, int64_t batch,
+               int64_t token_stride, int64_t batch_stride, int box_channels, int box_tokens)
+{
+    const EncodeTiled encode = encoder();
+    if (!encode) return fail(ctx, GSR_ERR_CUDA, "the driver offers no cuTensorMapEncodeTiled");
+    const int64_t size = dtype == GSR_F32 ? 4 : 2, items = batch_stride != 0 ? batch : 1;
+    const cuuint64_t extents[3] = {(cuuint64_t)channels, (cuuint64_t)tokens, (cuuint64_t)items};
+    // (An extent of 1 may carry any stride; give it one the encoder takes.)
+    const cuuint64_t strides[2] = {(cuuint64_t)(token_stride * size),
+                                   (cuuint64_t)(items > 1 ? batch_stride * size : token_stride * size)};
+    const cuuint32_t box[3] = {(cuuint32_t)box_channels, (cuuint32_t)box_tokens, 1}, one[3] = {1, 1, 1};
+    const CUtensorMapDataType type = dtype == GSR_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : dtype == GSR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const CUresult r = encode(map, type, 3, data, extents, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(ctx, GSR_ERR_CUDA, "cuTensorMapEncodeTiled: error " + std::to_string((int)r));
+    return GSR_OK;
+}
+
 size_t packed_bytes(const gsr_attention &d)
 {
     const size_t rows = (size_t)d.batch * d.kv_heads * d.kv_len * d.head_dim * 2;

@@ -17,6 +17,12 @@
 
 namespace gsr {
 
+// The tensor map of an array [batch, tokens, channels] (strides in elements, multiples of
+// 16 bytes; an array that all items share has a batch stride of 0 and one item), for boxes
+// of box_tokens rows of box_channels.
+int tokens_map(gsr_ctx *ctx, CUtensorMap *map, void *data, int dtype, int64_t channels, int64_t tokens, int64_t batch,
+               int64_t token_stride, int64_t batch_stride, int box_channels, int box_tokens);
+
 constexpr int kBlockBytes = 128 * 128;   // 128 rows of 64 16-bit elements
 
 __device__ __forceinline__ uint32_t smem_address(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
