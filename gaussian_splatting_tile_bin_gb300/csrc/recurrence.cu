@@ -14,19 +14,22 @@
 // computes h again from the forward's states.
 //
 // The chain.  Tiles are taken from a ticket in the chain's order, so a tile waits only
-// for tiles that blocks work on or are done with.  Each publishes its (A, H); every
-// kGroup-th also the state behind it, and a tile folds what its group's tiles before it
-// have published: the composition does not depend on timing, so results are the same
+// for tiles that blocks work on or are done with.  Each publishes its (A, H), the
+// last of a group also the state behind it, and a tile folds what its group's tiles before
+// it have published: the composition does not depend on timing, so results are the same
 // bits on every run.  A published pair is one 64-bit word, which is all ones before that
 // (no pair is: A is never that NaN).
 //
 // A block's warps.  Eight work on runs.  One takes tickets and starts the tiles' copies
-// into a ring of stages.  One follows the chain, beside the copies and the working warps,
-// so that the state is mostly there when they need it.  One composes the runs' maps,
-// publishes the tile's and hands each run the map of those in front of it.
+// into a ring of stages.  One follows the chain.  One composes the runs' maps, publishes
+// the tile's and hands each run the map of those in front of it.  A working warp composes
+// its run of the next tile before it finishes the one of the last: its gates and inputs
+// wait in tensor memory (256 columns a block) meanwhile, so that the time that a map takes
+// along the chain is spent on work.
 //
 // Numerics.  With e = exp(-|f|), the larger of a and 1 - a is 1 / (1 + e) and the smaller
-// e / (1 + e): neither is taken as a difference, so gates near 0 and 1 lose nothing.
+// e / (1 + e): neither is taken as a difference, so gates near 0 and 1 lose nothing.  What
+// waits is 1 - a, which may be small and a sequence's memory, and a is 1 minus it.
 #include <initializer_list>
 #include <type_traits>
 
@@ -43,7 +46,9 @@ constexpr int kBlocks = 2;                 // of an SM
 // theirs to the others.
 constexpr int kStart = 80, kFew = 48, kMany = 96;
 static_assert(kWarps == 8 && 4 * kFew + 8 * kMany <= 12 * kStart, "the shares must fit what a block starts with");
-constexpr int kGroup = 32, kAhead = 4;     // tiles of a group; words in flight of the warp that folds them
+constexpr int kMinGroup = 16, kMaxGroup = 32;   // tiles of a group
+constexpr int kAhead = 4;                  // words in flight of the warp that folds them
+constexpr int kColumns = 256, kSlotColumns = kColumns / 2;   // of tensor memory: two tiles' runs
 constexpr int kRun = 16, kGradRun = 8;     // tokens of a warp
 constexpr int kTile = kWarps * kRun, kGradTile = kWarps * kGradRun;
 constexpr int kStages = 2, kGradStages = 3;
@@ -63,6 +68,7 @@ struct RecurrenceArgs {
     const int *lengths;
     int batch, tokens, channels, blocks;
     int tiles, slabs;            // of all tokens, of all channels
+    int group, groups;           // tiles of a group, groups of all tokens
     uint32_t work;               // their number over all items
     int reverse;
     unsigned long long *pairs, *ends;   // published: [batch, slabs, tiles] and [batch, slabs, groups] rows of words
@@ -240,20 +246,20 @@ __device__ __forceinline__ void store_state(float *to, const Lanes<V> &v)
     for (int j = 0; j < V; ++j) to[j] = at(v, j);
 }
 
-// What a block's warps share.
+// What a block's warps share.  A tile's part is its number's, modulo 2 or 4: what one
+// warp writes for a tile, others have read of the one that used the same place before
+// they let the writer go on.
 template <int V, int S>
 struct Shared {
-    Map<V> runs[kWarps][32];         // the runs' maps
-    Map<V> before[kWarps][32];       // of the runs in front of each
-    Map<V> tile[2][32];              // the tile's, in turn
-    Lanes<V> carry[2][32];           // the state in front of the tile, in turn
-    Lanes<V> h[kWarps][32];          // backward: H of the runs' forward maps, and h in front of each
-    Lanes<V> h_before[kWarps][32];
+    Map<V> runs[2][kWarps][32];         // the runs' maps, then in their place those of the runs in front of each
+    Map<V> tile[4][32];                 // the tile's
+    Lanes<V> carry[4][32];              // the state in front of the tile
+    Lanes<V> h[2][kWarps][32];          // backward: H of the runs' forward maps, then h in front of each
     Tile tiles[S];
-    uint32_t last[S];                // no tile: the tickets are at an end
+    uint32_t last[S];                   // no tile: the tickets are at an end
     uint64_t known[S], full[S], empty[S];
-    uint64_t runs_ready, state_ready;
-    uint32_t aborted;
+    uint64_t runs_ready[2], state_ready[2];
+    uint32_t aborted, columns;
 };
 
 // A warp's arrival: what its lanes have written is there for who waits.
@@ -316,9 +322,9 @@ __device__ __forceinline__ void fetch_tiles(const RecurrenceArgs &a, const Maps 
     }
 }
 
-// Calls f(tile, stage, parity, j) for the block's tiles in turn, and leaves the stage:
-// the parity of the stage's turn, and how many tiles with tokens came before.  (Once a
-// wait has run out there may be no tile where one is looked for.)
+// Calls f(tile, j) for the block's tiles in turn, j of which with tokens came before, and
+// leaves their stages.  (Once a wait has run out there may be no tile where one is looked
+// for.)
 template <int V, int S, typename F>
 __device__ __forceinline__ void each_tile(Shared<V, S> &s, const WaitGuard &guard, F f)
 {
@@ -328,9 +334,9 @@ __device__ __forceinline__ void each_tile(Shared<V, S> &s, const WaitGuard &guar
         barrier_wait_warp(smem_address(&s.known[stage]), i / S & 1, guard);
         if (guard.stop() || s.last[stage]) return;
         const Tile t = s.tiles[stage];
-        f(t, stage, i / S & 1, j);
-        if (t.index < t.count) ++j;
         warp_arrive(s.empty[stage]);
+        f(t, j);
+        if (t.index < t.count) ++j;
     }
 }
 
@@ -361,15 +367,23 @@ __device__ __forceinline__ void compose_runs(const RecurrenceArgs &a, Shared<V, 
     if (BACKWARD)
 #pragma unroll
         for (int k = 0; k < V; ++k) at(h, k) = a.states[((int64_t)t.b * a.blocks + t.index) * a.channels + c + k];
-    barrier_wait_warp(smem_address(&s.runs_ready), j & 1, guard);
+    barrier_wait_warp(smem_address(&s.runs_ready[j & 1]), j >> 1 & 1, guard);
+    if (BACKWARD)
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const Lanes<V> own = s.h[j & 1][w][lane];
+            s.h[j & 1][w][lane] = h;
+            h = mad(s.runs[j & 1][w][lane].a, h, own);
+        }
     Map<V> m;
     fill(m.a, 1.0f);
     fill(m.h, 0.0f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-        const int run = BACKWARD ? kWarps - 1 - w : w;
-        s.before[run][lane] = m;
-        m = then(m, s.runs[run][lane]);
+        Map<V> &place_of_run = s.runs[j & 1][BACKWARD ? kWarps - 1 - w : w][lane];
+        const Map<V> own = place_of_run;
+        place_of_run = m;
+        m = then(m, own);
     }
     if (place + 1 < t.count) {
         Map<V> out = m;
@@ -379,19 +393,14 @@ __device__ __forceinline__ void compose_runs(const RecurrenceArgs &a, Shared<V, 
         }
         publish(a.pairs + (((int64_t)t.b * a.slabs + t.slab) * a.tiles + place) * (32 * V) + lane * V, Words<V>::of(out));
     }
-    if (BACKWARD)
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            s.h_before[w][lane] = h;
-            h = mad(s.runs[w][lane].a, h, s.h[w][lane]);
-        }
-    s.tile[j & 1][lane] = m;
-    if (place == 0) s.carry[j & 1][lane] = seed;
-    warp_arrive(s.state_ready);
+    s.tile[j & 3][lane] = m;
+    if (place == 0) s.carry[j & 3][lane] = seed;
+    warp_arrive(s.state_ready[j & 1]);
 }
 
-// Folds the maps that the group's tiles before this one have published into the state
-// in front of it, and publishes the state behind a group.
+// Folds the maps that the group's tiles before this one have published, takes them
+// behind the group's first state to the state in front of the tile, and publishes the
+// state behind a group.
 template <int V, int S, bool BACKWARD>
 __device__ __forceinline__ void follow_chain(const RecurrenceArgs &a, Shared<V, S> &s, const Tile &t, uint32_t j,
                                              const WaitGuard &guard)
@@ -399,45 +408,45 @@ __device__ __forceinline__ void follow_chain(const RecurrenceArgs &a, Shared<V, 
     if (t.index >= t.count) return;
     const int lane = threadIdx.x % 32, place = place_of<BACKWARD>(t);
     const int64_t row = (int64_t)t.b * a.slabs + t.slab;
-    const int groups = (a.tiles + kGroup - 1) / kGroup, group = place / kGroup;
+    const int group = place / a.group, first = group * a.group;
     const unsigned long long *pairs = a.pairs + row * a.tiles * (32 * V) + lane * V;
-    unsigned long long *ends = a.ends + row * groups * (32 * V) + lane * V;
+    unsigned long long *ends = a.ends + (row * a.groups + group) * (32 * V) + lane * V;
     Lanes<V> state;
+    fill(state, 0.0f);   // (the first map of a chain takes no state)
     if (place > 0) {
-        fill(state, 0.0f);   // (the first map of a chain takes no state)
-        Words<V> end;
-        if (group > 0) look(ends + (int64_t)group * (32 * V), end);
-        for (int first = group * kGroup; first < place; first += kAhead) {
+        Map<V> m;
+        fill(m.a, 1.0f);
+        fill(m.h, 0.0f);
+        for (int from = first; from < place; from += kAhead) {
             Words<V> seen[kAhead];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
-                if (first + k < place) look(pairs + (int64_t)(first + k) * (32 * V), seen[k]);
-            if (group > 0 && first == group * kGroup) {
-                wait_for(a, ends + (int64_t)group * (32 * V), end);
-                state = end.map().h;
-            }
+                if (from + k < place) look(pairs + (int64_t)(from + k) * (32 * V), seen[k]);
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
-                if (first + k < place) {
-                    wait_for(a, pairs + (int64_t)(first + k) * (32 * V), seen[k]);
-                    const Map<V> m = seen[k].map();
-                    state = mad(m.a, state, m.h);
+                if (from + k < place) {
+                    wait_for(a, pairs + (int64_t)(from + k) * (32 * V), seen[k]);
+                    m = then(m, seen[k].map());
                 }
         }
-        if (group > 0 && place == group * kGroup) {
-            wait_for(a, ends + (int64_t)group * (32 * V), end);
+        if (group > 0) {
+            Words<V> end;
+            look(ends, end);
+            wait_for(a, ends, end);
             state = end.map().h;
         }
-        s.carry[j & 1][lane] = state;
+        state = mad(m.a, state, m.h);
+        s.carry[j & 3][lane] = state;
     }
-    warp_arrive(s.state_ready);
-    barrier_wait_warp(smem_address(&s.state_ready), j & 1, guard);
-    if (place % kGroup == kGroup - 1 && place + 1 < t.count) {
-        Map<V> m = s.tile[j & 1][lane];
-        m.h = mad(m.a, state, m.h);
-        fill(m.a, 0.0f);
-        publish(ends + (int64_t)(group + 1) * (32 * V), Words<V>::of(m));
-    }
+    // (A barrier for even tiles and one for odd: the working warps look at a tile's when
+    // the next one's may be through already.)
+    warp_arrive(s.state_ready[j & 1]);
+    barrier_wait_warp(smem_address(&s.state_ready[j & 1]), j >> 1 & 1, guard);
+    if (place % a.group != a.group - 1 || place + 1 >= t.count) return;
+    Map<V> end = s.tile[j & 3][lane];
+    end.h = mad(end.a, state, end.h);
+    fill(end.a, 0.0f);
+    publish(ends + 32 * V, Words<V>::of(end));
 }
 
 // ---- runs of tokens ------------------------------------------------------------------------
@@ -508,6 +517,26 @@ __device__ __forceinline__ Raw<T, V> raw_bits(uint32_t w)
     return (Raw<T, V>)w;
 }
 
+// a and 1 - a as one number: the smaller of them, below 0 (or -0) where it is 1 - a.
+__device__ __forceinline__ float fold_gate(float a, float s) { return a < s ? a : -s; }
+__device__ __forceinline__ float2 fold_gate(float2 a, float2 s)
+{
+    return make_float2(fold_gate(a.x, s.x), fold_gate(a.y, s.y));
+}
+__device__ __forceinline__ void unfold_gate(float c, float &a, float &s, float &product)
+{
+    const float small = fabsf(c), large = 1.0f - small;
+    const bool kept = __float_as_int(c) < 0;
+    a = kept ? large : small;
+    s = kept ? small : large;
+    product = small * large;
+}
+__device__ __forceinline__ void unfold_gate(float2 c, float2 &a, float2 &s, float2 &product)
+{
+    unfold_gate(c.x, a.x, s.x, product.x);
+    unfold_gate(c.y, a.y, s.y, product.y);
+}
+
 // exp(-x) for x >= 0.  For f32 the product x log2(e) is kept to twice float's length.
 template <typename T>
 __device__ __forceinline__ float exp_minus(float x)
@@ -528,11 +557,16 @@ __device__ __forceinline__ void split(float f, float &a, float &s)
     s = f < 0.0f ? large : small;
 }
 
+// (One reciprocal for both: 1 / x = y (1 / (x y)).)
 template <typename T>
 __device__ __forceinline__ void split(float2 f, float2 &a, float2 &s)
 {
-    split<T>(f.x, a.x, s.x);
-    split<T>(f.y, a.y, s.y);
+    const float2 e = make_float2(exp_minus<T>(fabsf(f.x)), exp_minus<T>(fabsf(f.y)));
+    const float2 one = add2(e, make_float2(1.0f, 1.0f));
+    const float r = rcp_fast(one.x * one.y);
+    const float2 large = mul2(make_float2(one.y, one.x), make_float2(r, r)), small = mul2(e, large);
+    a = make_float2(f.x < 0.0f ? small.x : large.x, f.y < 0.0f ? small.y : large.y);
+    s = make_float2(f.x < 0.0f ? large.x : small.x, f.y < 0.0f ? large.y : small.y);
 }
 
 template <typename T>
@@ -550,205 +584,366 @@ __device__ __forceinline__ float2 sigmoid(float2 o)
     return make_float2(sigmoid<T>(o.x), sigmoid<T>(o.y));
 }
 
+// Values of N lanes' words, packed for tensor memory and back.
+template <int N>
+__device__ __forceinline__ void put(uint32_t *to, const float (&v)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) to[i] = __float_as_uint(v[i]);
+}
+template <int N>
+__device__ __forceinline__ void put(uint32_t *to, const float2 (&v)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        to[2 * i] = __float_as_uint(v[i].x);
+        to[2 * i + 1] = __float_as_uint(v[i].y);
+    }
+}
+__device__ __forceinline__ void get(const uint32_t *from, int i, float &v) { v = __uint_as_float(from[i]); }
+__device__ __forceinline__ void get(const uint32_t *from, int i, float2 &v)
+{
+    v = make_float2(__uint_as_float(from[2 * i]), __uint_as_float(from[2 * i + 1]));
+}
+
+// What a working warp knows of its run.
+template <typename T, int V>
+struct RunPlace {
+    int c, k0, count;      // first channel, first token in the recurrence's order, tokens
+    bool mine;             // (other lanes compute the last one's channels, or none)
+
+    __device__ __forceinline__ RunPlace(const RecurrenceArgs &a, const Tile &t, int tile_tokens, int run)
+    {
+        const int own = t.slab * (32 * V) + threadIdx.x % 32 * V;
+        c = min(own, a.channels - V);
+        mine = own == c;
+        k0 = t.index * tile_tokens + threadIdx.x / 32 * run;
+        count = min(max(t.length - k0, 0), run);
+    }
+};
+
 // ---- forward -----------------------------------------------------------------------------
 
+// Words of a run in tensor memory: 1 - a, x and the gate, 64 at most.
 template <typename T, int V, bool GATE, bool COPY, int S>
-__device__ __forceinline__ void forward_run(const RecurrenceArgs &a, Shared<V, S> &s, const Tile &t, uint32_t j,
-                                            uint32_t stage_at, uint32_t full, uint32_t parity, const WaitGuard &guard)
-{
+struct Forward {
     using F = Lanes<V>;
-    constexpr int kBytes = kTile * kRowBytes;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int own_c = t.slab * (32 * V) + lane * V, c = min(own_c, a.channels - V);
-    const bool mine = own_c == c;   // (other lanes compute the last one's channels, or none)
-    const int k0 = t.index * kTile + warp * kRun, count = min(max(t.length - k0, 0), kRun);
-    if (mine) clear_tokens<T, V>(a.out, t.b, max(k0, t.length), min(k0 + kRun, a.tokens), c);
-    if (t.index >= t.count) return;
+    using R = Raw<T, V>;
+    [[maybe_unused]] static constexpr int kTokens = kTile, kLength = kRun, kBytes = kTile * kRowBytes;
 
-    F keep[kRun], enter[kRun];   // a and (1 - a) x
-    Raw<T, V> o[GATE ? kRun : 1];
-    const StagedRun staged(a, stage_at, kTile, warp * kRun);
-    if constexpr (COPY) {
-        barrier_wait_warp(full, parity, guard);
-#pragma unroll
-        for (int i = 0; i < kRun; ++i) {
-            const Raw<T, V> f = raw_bits<T, V>(staged.word(i, 0)), x = raw_bits<T, V>(staged.word(i, kBytes));
-            F r;
-            split<T>(value_of<T, V>(f), keep[i], r);
-            enter[i] = mul(r, value_of<T, V>(x));
-        }
-    } else {
-        Raw<T, V> x[kRun], f[kRun];
-        Run<T, V>(a, a.forget, t, k0, c).load(f, count);
-        Run<T, V>(a, a.x, t, k0, c).load(x, count);
-        if (GATE) Run<T, V>(a, a.gate, t, k0, c).load(o, count);
-#pragma unroll
-        for (int i = 0; i < kRun; ++i) {
-            F r;
-            split<T>(value_of<T, V>(f[i]), keep[i], r);
-            enter[i] = mul(r, value_of<T, V>(x[i]));
-        }
+    static __device__ __forceinline__ void clear_rest(const RecurrenceArgs &a, const Tile &t)
+    {
+        const RunPlace<T, V> at(a, t, kTokens, kLength);
+        if (at.mine) clear_tokens<T, V>(a.out, t.b, max(at.k0, t.length), min(at.k0 + kLength, a.tokens), at.c);
     }
-    if (count < kRun)
+
+    // Reads a run, composes its map and leaves it in tensor memory.
+    static __device__ __forceinline__ void compose(const RecurrenceArgs &a, Shared<V, S> &s, const Tile &t, uint32_t j,
+                                                   uint32_t stage, uint32_t columns)
+    {
+        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+        const RunPlace<T, V> at(a, t, kTokens, kLength);
+        uint32_t w0[32], w1[32];
+        F rest[kLength];
+        R x[kLength];
+        Map<V> own;
+        fill(own.a, 1.0f);
+        fill(own.h, 0.0f);
+        {
+            R f[kLength], o[GATE ? kLength : 1];
+            if constexpr (COPY) {
+                const StagedRun staged(a, stage, kTokens, warp * kLength);
 #pragma unroll
-        for (int i = 0; i < kRun; ++i)
-            if (i >= count) {   // no step
-                fill(keep[i], 1.0f);
-                fill(enter[i], 0.0f);
+                for (int i = 0; i < kLength; ++i) {
+                    f[i] = raw_bits<T, V>(staged.word(i, 0));
+                    x[i] = raw_bits<T, V>(staged.word(i, kBytes));
+                    if constexpr (GATE) o[i] = raw_bits<T, V>(staged.word(i, 2 * kBytes));
+                }
+            } else {
+                Run<T, V>(a, a.forget, t, at.k0, at.c).load(f, at.count);
+                Run<T, V>(a, a.x, t, at.k0, at.c).load(x, at.count);
+                if constexpr (GATE) Run<T, V>(a, a.gate, t, at.k0, at.c).load(o, at.count);
             }
-    Map<V> own;
-    fill(own.a, 1.0f);
-    fill(own.h, 0.0f);
+            if (at.count == kLength) {
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-        own.h = mad(keep[i], own.h, enter[i]);
-        own.a = mul(keep[i], own.a);
+                for (int i = 0; i < kLength; ++i) step(f[i], x[i], true, rest[i], own);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kLength; ++i) {
+                    if (i >= at.count) clear(x[i]);
+                    step(f[i], x[i], i < at.count, rest[i], own);
+                }
+            }
+            if constexpr (GATE)
+#pragma unroll
+                for (int i = 0; i < kLength; ++i) w1[(V == 2 ? 16 : 0) + i] = o[i];
+        }
+        s.runs[j & 1][warp][lane] = own;
+        put(w0, rest);
+#pragma unroll
+        for (int i = 0; i < kLength; ++i) (V == 2 ? w1 : w0 + 16)[i] = x[i];
+        if (!GATE || V == 1)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w1[16 + i] = 0;
+        tmem_store32(columns, w0);
+        if (V == 2 || GATE) tmem_store32(columns + 32, w1);
+        tmem_wait_store();
     }
-    s.runs[warp][lane] = own;
-    warp_arrive(s.runs_ready);
-    barrier_wait_warp(smem_address(&s.state_ready), j & 1, guard);
-    const Map<V> before = s.before[warp][lane];
-    F h = mad(before.a, s.carry[j & 1][lane], before.h);
-    if (count == 0 || !mine) return;
 
-    if (a.states && k0 % kStateStep == 0)
-        store_state<V>(a.states + ((int64_t)t.b * a.blocks + k0 / kStateStep) * a.channels + c, h);
-    const Run<T, V> out(a, a.out, t, k0, c);
-    auto token = [&](int i) {
-        h = mad(keep[i], h, enter[i]);
-        if constexpr (GATE) {
-            const F g = value_of<T, V>(COPY ? raw_bits<T, V>(staged.word(i, 2 * kBytes)) : o[i]);
-            return mul(h, mul(g, sigmoid<T>(g)));
-        } else {
-            return h;
+    static __device__ __forceinline__ void step(R f, R x, bool there, F &rest, Map<V> &own)
+    {
+        F keep;
+        split<T>(value_of<T, V>(f), keep, rest);
+        if (!there) {
+            fill(keep, 1.0f);
+            fill(rest, 0.0f);
         }
-    };
-    if (count == kRun) {
-#pragma unroll
-        for (int i = 0; i < kRun; ++i) out.store(i, token(i));
-    } else {
-#pragma unroll
-        for (int i = 0; i < kRun; ++i) {
-            const F y = token(i);
-            if (i < count) out.store(i, y);
-        }
+        own.h = mad(keep, own.h, mul(rest, value_of<T, V>(x)));
+        own.a = mul(keep, own.a);
     }
-    if (k0 + kRun >= t.length) store_state<V>(a.final + (int64_t)t.b * a.channels + c, h);
-}
+
+    // Runs the tokens from the state in front of them.
+    static __device__ __forceinline__ void finish(const RecurrenceArgs &a, Shared<V, S> &s, const Tile &t, uint32_t j,
+                                                  uint32_t columns)
+    {
+        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+        const RunPlace<T, V> at(a, t, kTokens, kLength);
+        uint32_t w0[32], w1[32];
+        tmem_load32(w0, columns);
+        if (V == 2 || GATE) tmem_load32(w1, columns + 32);
+        const Map<V> before = s.runs[j & 1][warp][lane];
+        F h = mad(before.a, s.carry[j & 3][lane], before.h), one;
+        fill(one, 1.0f);
+        tmem_wait_load();
+        pin(w0);
+        if (V == 2 || GATE) pin(w1);
+        if (at.count == 0 || !at.mine) return;
+        if (a.states && at.k0 % kStateStep == 0)
+            store_state<V>(a.states + ((int64_t)t.b * a.blocks + at.k0 / kStateStep) * a.channels + at.c, h);
+        const Run<T, V> out(a, a.out, t, at.k0, at.c);
+        auto token = [&](int i) {
+            F rest;
+            get(w0, i, rest);
+            const F x = value_of<T, V>((R)(V == 2 ? w1 : w0 + 16)[i]);
+            h = mad(add(one, minus(rest)), h, mul(rest, x));
+            if constexpr (GATE) {
+                const F g = value_of<T, V>((R)w1[(V == 2 ? 16 : 0) + i]);
+                return mul(h, mul(g, sigmoid<T>(g)));
+            } else {
+                return h;
+            }
+        };
+        if (at.count == kLength) {
+#pragma unroll
+            for (int i = 0; i < kLength; ++i) out.store(i, token(i));
+        } else {
+#pragma unroll
+            for (int i = 0; i < kLength; ++i) {
+                const F y = token(i);
+                if (i < at.count) out.store(i, y);
+            }
+        }
+        if (at.k0 + kLength >= t.length) store_state<V>(a.final + (int64_t)t.b * a.channels + at.c, h);
+    }
+};
 
 // ---- backward ----------------------------------------------------------------------------
 
+// Words of a run in tensor memory: the folded gate, dout silu(o) (dL/dh_t without what
+// comes from behind), dout silu'(o) and x, 56 at most.
 template <typename T, int V, bool GATE, bool COPY, int S>
-__device__ __forceinline__ void backward_run(const RecurrenceArgs &a, Shared<V, S> &s, const Tile &t, uint32_t j,
-                                             uint32_t stage_at, uint32_t full, uint32_t parity, const WaitGuard &guard)
-{
+struct Backward {
     using F = Lanes<V>;
-    constexpr int kBytes = kGradTile * kRowBytes;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int own_c = t.slab * (32 * V) + lane * V, c = min(own_c, a.channels - V);
-    const bool mine = own_c == c;
-    const int k0 = t.index * kGradTile + warp * kGradRun, count = min(max(t.length - k0, 0), kGradRun);
-    if (mine) {
-        const int from = max(k0, t.length), to = min(k0 + kGradRun, a.tokens);
-        clear_tokens<T, V>(a.dx, t.b, from, to, c);
-        clear_tokens<T, V>(a.dforget, t.b, from, to, c);
-        if (GATE) clear_tokens<T, V>(a.dgate, t.b, from, to, c);
-    }
-    if (t.index >= t.count) return;
+    using R = Raw<T, V>;
+    [[maybe_unused]] static constexpr int kTokens = kGradTile, kLength = kGradRun, kBytes = kGradTile * kRowBytes;
 
-    // dout silu(o): dL/dh_t without what comes from behind; dout silu'(o).
-    F keep[kGradRun], rest[kGradRun], into[kGradRun], slope[kGradRun];
-    Raw<T, V> x[kGradRun];
+    static __device__ __forceinline__ void clear_rest(const RecurrenceArgs &a, const Tile &t)
     {
-        Raw<T, V> f[kGradRun], dy[kGradRun], o[GATE ? kGradRun : 1];
-        if constexpr (COPY) {
-            const StagedRun staged(a, stage_at, kGradTile, warp * kGradRun);
-            barrier_wait_warp(full, parity, guard);
+        const RunPlace<T, V> at(a, t, kTokens, kLength);
+        if (!at.mine) return;
+        const int from = max(at.k0, t.length), to = min(at.k0 + kLength, a.tokens);
+        clear_tokens<T, V>(a.dx, t.b, from, to, at.c);
+        clear_tokens<T, V>(a.dforget, t.b, from, to, at.c);
+        if (GATE) clear_tokens<T, V>(a.dgate, t.b, from, to, at.c);
+    }
+
+    static __device__ __forceinline__ void compose(const RecurrenceArgs &a, Shared<V, S> &s, const Tile &t, uint32_t j,
+                                                   uint32_t stage, uint32_t columns)
+    {
+        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+        const RunPlace<T, V> at(a, t, kTokens, kLength);
+        F keep[kLength], rest[kLength], into[kLength], slope[kLength], h, one;
+        R x[kLength];
+        fill(one, 1.0f);
+        {
+            R f[kLength], dy[kLength], o[GATE ? kLength : 1];
+            if constexpr (COPY) {
+                const StagedRun staged(a, stage, kTokens, warp * kLength);
 #pragma unroll
-            for (int i = 0; i < kGradRun; ++i) {
-                f[i] = raw_bits<T, V>(staged.word(i, 0));
-                x[i] = raw_bits<T, V>(staged.word(i, kBytes));
-                if (GATE) o[i] = raw_bits<T, V>(staged.word(i, 2 * kBytes));
-                dy[i] = raw_bits<T, V>(staged.word(i, (GATE ? 3 : 2) * kBytes));
+                for (int i = 0; i < kLength; ++i) {
+                    f[i] = raw_bits<T, V>(staged.word(i, 0));
+                    x[i] = raw_bits<T, V>(staged.word(i, kBytes));
+                    if constexpr (GATE) o[i] = raw_bits<T, V>(staged.word(i, 2 * kBytes));
+                    dy[i] = raw_bits<T, V>(staged.word(i, (GATE ? 3 : 2) * kBytes));
+                }
+            } else {
+                Run<T, V>(a, a.forget, t, at.k0, at.c).load(f, at.count);
+                Run<T, V>(a, a.x, t, at.k0, at.c).load(x, at.count);
+                Run<T, V>(a, a.dout, t, at.k0, at.c).load(dy, at.count);
+                if constexpr (GATE) Run<T, V>(a, a.gate, t, at.k0, at.c).load(o, at.count);
             }
-            if (count < kGradRun)
+            if (at.count < kLength)
 #pragma unroll
-                for (int i = 0; i < kGradRun; ++i)
-                    if (i >= count) {
+                for (int i = 0; i < kLength; ++i)
+                    if (i >= at.count) {
                         clear(x[i]);
                         clear(dy[i]);
                         if constexpr (GATE) clear(o[i]);
                     }
-        } else {
-            Run<T, V>(a, a.forget, t, k0, c).load(f, count);
-            Run<T, V>(a, a.x, t, k0, c).load(x, count);
-            Run<T, V>(a, a.dout, t, k0, c).load(dy, count);
-            if (GATE) Run<T, V>(a, a.gate, t, k0, c).load(o, count);
-        }
 #pragma unroll
-        for (int i = 0; i < kGradRun; ++i) {
-            split<T>(value_of<T, V>(f[i]), keep[i], rest[i]);
-            const F d = value_of<T, V>(dy[i]);
-            if constexpr (GATE) {
-                const F g = value_of<T, V>(o[i]), r = sigmoid<T>(g);
-                into[i] = mul(d, mul(g, r));
-                F one;
-                fill(one, 1.0f);
-                slope[i] = mul(d, mul(r, mad(g, add(one, minus(r)), one)));
-            } else {
-                into[i] = d;
-            }
-        }
-        if (count < kGradRun)
-#pragma unroll
-            for (int i = 0; i < kGradRun; ++i)
-                if (i >= count) {   // no step (its x and dout are 0)
-                    fill(keep[i], 1.0f);
-                    fill(rest[i], 0.0f);
+            for (int i = 0; i < kLength; ++i) {
+                split<T>(value_of<T, V>(f[i]), keep[i], rest[i]);
+                const F d = value_of<T, V>(dy[i]);
+                if constexpr (GATE) {
+                    const F g = value_of<T, V>(o[i]), r = sigmoid<T>(g);
+                    into[i] = mul(d, mul(g, r));
+                    slope[i] = mul(d, mul(r, mad(g, add(one, minus(r)), one)));
+                } else {
+                    into[i] = d;
+                    fill(slope[i], 0.0f);
                 }
-    }
-    Map<V> own;
-    F h;
-    fill(h, 0.0f);
-    fill(own.a, 1.0f);
-    fill(own.h, 0.0f);
+            }
+            if (at.count < kLength)
 #pragma unroll
-    for (int i = 0; i < kGradRun; ++i) {
-        h = mad(keep[i], h, mul(rest[i], value_of<T, V>(x[i])));
-        own.a = mul(keep[i], own.a);
-    }
+                for (int i = 0; i < kLength; ++i)
+                    if (i >= at.count) {   // no step (its x and dout are 0)
+                        fill(keep[i], 1.0f);
+                        fill(rest[i], 0.0f);
+                    }
+        }
+        Map<V> own;
+        fill(h, 0.0f);
+        fill(own.a, 1.0f);
+        fill(own.h, 0.0f);
 #pragma unroll
-    for (int i = kGradRun - 1; i >= 0; --i) own.h = mul(keep[i], add(own.h, into[i]));
-    s.runs[warp][lane] = own;
-    s.h[warp][lane] = h;
-    warp_arrive(s.runs_ready);
-    barrier_wait_warp(smem_address(&s.state_ready), j & 1, guard);
-    const Map<V> behind = s.before[warp][lane];
-    F p = mad(behind.a, s.carry[j & 1][lane], behind.h);
-    if (count == 0 || !mine) return;
+        for (int i = 0; i < kLength; ++i) {
+            h = mad(keep[i], h, mul(rest[i], value_of<T, V>(x[i])));
+            own.a = mul(keep[i], own.a);
+        }
+#pragma unroll
+        for (int i = kLength - 1; i >= 0; --i) own.h = mul(keep[i], add(own.h, into[i]));
+        s.runs[j & 1][warp][lane] = own;
+        s.h[j & 1][warp][lane] = h;
+        uint32_t w0[32], w1[32];
+#pragma unroll
+        for (int i = 0; i < kLength; ++i) rest[i] = fold_gate(keep[i], rest[i]);
+        put(w0, rest);
+        put(w0 + 8 * V, into);
+        if (V == 2) {
+            put(w1, slope);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                w1[16 + i] = x[i];
+                w1[24 + i] = 0;
+            }
+            tmem_store32(columns + 32, w1);
+        } else {
+            put(w0 + 16, slope);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w0[24 + i] = x[i];
+        }
+        tmem_store32(columns, w0);
+        tmem_wait_store();
+    }
 
-    F hs[kGradRun + 1];   // in front of each token, and behind the last
-    hs[0] = s.h_before[warp][lane];
+    static __device__ __forceinline__ void finish(const RecurrenceArgs &a, Shared<V, S> &s, const Tile &t, uint32_t j,
+                                                  uint32_t columns)
+    {
+        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+        const RunPlace<T, V> at(a, t, kTokens, kLength);
+        uint32_t w0[32], w1[32];
+        tmem_load32(w0, columns);
+        if (V == 2) tmem_load32(w1, columns + 32);
+        const Map<V> behind = s.runs[j & 1][warp][lane];
+        F p = mad(behind.a, s.carry[j & 3][lane], behind.h);
+        F hs[kLength + 1];   // in front of each token, and behind the last
+        hs[0] = s.h[j & 1][warp][lane];
+        tmem_wait_load();
+        pin(w0);
+        if (V == 2) pin(w1);
+        if (at.count == 0 || !at.mine) return;
+        auto word = [&](int part, int i) {   // 1 - a, into, slope
+            F v;
+            if (V == 2 && part == 2)
+                get(w1, i, v);
+            else
+                get(w0, part * 8 + i, v);
+            return v;
+        };
+        auto x = [&](int i) { return value_of<T, V>((R)(V == 2 ? w1[16 + i] : w0[24 + i])); };
 #pragma unroll
-    for (int i = 0; i < kGradRun; ++i) hs[i + 1] = mad(keep[i], hs[i], mul(rest[i], value_of<T, V>(x[i])));
-    const Run<T, V> dx(a, a.dx, t, k0, c), df(a, a.dforget, t, k0, c), dg(a, a.dgate, t, k0, c);
-    auto token = [&](int i, bool there) {
-        const F dh = add(p, into[i]);
-        p = mul(keep[i], dh);
-        if (!there) return;
-        const F enter = mul(dh, rest[i]);
-        dx.store(i, enter);
-        df.store(i, mul(mul(enter, keep[i]), add(hs[i], minus(value_of<T, V>(x[i])))));
-        if constexpr (GATE) dg.store(i, mul(slope[i], hs[i + 1]));
-    };
-    if (count == kGradRun) {
+        for (int i = 0; i < kLength; ++i) {
+            F keep, rest, product;
+            unfold_gate(word(0, i), keep, rest, product);
+            hs[i + 1] = mad(keep, hs[i], mul(rest, x(i)));
+        }
+        const Run<T, V> dx(a, a.dx, t, at.k0, at.c), df(a, a.dforget, t, at.k0, at.c), dg(a, a.dgate, t, at.k0, at.c);
+        auto token = [&](int i, bool there) {
+            F keep, rest, product;
+            unfold_gate(word(0, i), keep, rest, product);
+            const F dh = add(p, word(1, i));
+            p = mul(keep, dh);
+            if (!there) return;
+            dx.store(i, mul(dh, rest));
+            df.store(i, mul(mul(dh, product), add(hs[i], minus(x(i)))));
+            if constexpr (GATE) dg.store(i, mul(word(2, i), hs[i + 1]));
+        };
+        if (at.count == kLength) {
 #pragma unroll
-        for (int i = kGradRun - 1; i >= 0; --i) token(i, true);
-    } else {
+            for (int i = kLength - 1; i >= 0; --i) token(i, true);
+        } else {
 #pragma unroll
-        for (int i = kGradRun - 1; i >= 0; --i) token(i, i < count);
+            for (int i = kLength - 1; i >= 0; --i) token(i, i < at.count);
+        }
+        if (at.k0 == 0 && a.final) store_state<V>(a.final + (int64_t)t.b * a.channels + at.c, p);
     }
-    if (k0 == 0 && a.final) store_state<V>(a.final + (int64_t)t.b * a.channels + c, p);
+};
+
+// A working warp's tiles: the next one's run is composed before the last one's ends.
+template <typename Work, int V, int S, bool COPY>
+__device__ __forceinline__ void work_tiles(const RecurrenceArgs &a, Shared<V, S> &s, uint32_t stages, int stage_bytes,
+                                           const WaitGuard &guard)
+{
+    const int warp = threadIdx.x / 32;
+    const uint32_t columns = s.columns + ((uint32_t)(warp % 4) << 21) + warp / 4 * (kSlotColumns / 2);   // lane << 16
+    Tile before = {};
+    bool open = false;
+    uint32_t j = 0;
+    auto finish = [&] {
+        const uint32_t k = j - 1;
+        barrier_wait_warp(smem_address(&s.state_ready[k & 1]), k >> 1 & 1, guard);
+        Work::finish(a, s, before, k, columns + (k & 1) * kSlotColumns);
+        __syncwarp();
+    };
+    for (uint32_t i = 0;; ++i) {
+        const uint32_t stage = i % S;
+        barrier_wait_warp(smem_address(&s.known[stage]), i / S & 1, guard);
+        if (guard.stop() || s.last[stage]) break;
+        const Tile t = s.tiles[stage];
+        if (t.length < a.tokens) Work::clear_rest(a, t);
+        const bool some = t.index < t.count;
+        if (some) {
+            if (COPY) barrier_wait_warp(smem_address(&s.full[stage]), i / S & 1, guard);
+            Work::compose(a, s, t, j, stages + stage * stage_bytes, columns + (j & 1) * kSlotColumns);
+            warp_arrive(s.runs_ready[j & 1]);
+        }
+        warp_arrive(s.empty[stage]);
+        if (open) finish();
+        open = some;
+        before = t;
+        if (some) ++j;
+    }
+    if (open && !guard.stop()) finish();
 }
 
 // COPY: tiles come through the ring of stages; otherwise the runs' warps read them.
@@ -763,6 +958,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     __shared__ Shared<V, S> s;
     const uint32_t stages = (smem_address(s_bytes) + 127u) / 128u * 128u;
     const WaitGuard guard = {&s.aborted, a.status};
+    const int warp = threadIdx.x / 32;
     if (threadIdx.x == 0) {
         s.aborted = 0;
         for (int k = 0; k < S; ++k) {
@@ -770,37 +966,36 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
             barrier_init(smem_address(&s.full[k]), 1);
             barrier_init(smem_address(&s.empty[k]), kWarps + 2);
         }
-        barrier_init(smem_address(&s.runs_ready), kWarps);
-        barrier_init(smem_address(&s.state_ready), 2);
+        for (int k = 0; k < 2; ++k) {
+            barrier_init(smem_address(&s.runs_ready[k]), kWarps);
+            barrier_init(smem_address(&s.state_ready[k]), 2);
+        }
         fence_async();
     }
+    if (warp == kComposeWarp) tmem_alloc(smem_address(&s.columns), kColumns);
+    tmem_fence_before();
     __syncthreads();
-    const int warp = threadIdx.x / 32;
+    tmem_fence_after();
     if (warp >= kWarps) {
         give_registers();
         if (warp == kFetchWarp) {
             if (threadIdx.x % 32 == 0) fetch_tiles<V, S, GATE, COPY, BACKWARD>(a, maps, s, stages, guard);
+            __syncwarp();
         } else if (warp == kChainWarp) {
-            each_tile(s, guard, [&](const Tile &t, uint32_t, uint32_t, uint32_t j) {
-                follow_chain<V, S, BACKWARD>(a, s, t, j, guard);
-            });
+            each_tile(s, guard, [&](const Tile &t, uint32_t j) { follow_chain<V, S, BACKWARD>(a, s, t, j, guard); });
         } else if (warp == kComposeWarp) {
-            each_tile(s, guard, [&](const Tile &t, uint32_t, uint32_t, uint32_t j) {
-                compose_runs<V, S, BACKWARD>(a, s, t, j, guard);
-            });
+            each_tile(s, guard, [&](const Tile &t, uint32_t j) { compose_runs<V, S, BACKWARD>(a, s, t, j, guard); });
         }
     } else {
         take_registers();
-        each_tile(s, guard, [&](const Tile &t, uint32_t stage, uint32_t parity, uint32_t j) {
-            const uint32_t from = stages + stage * kStageBytes, full = smem_address(&s.full[stage]);
-            if constexpr (BACKWARD)
-                backward_run<T, V, GATE, COPY, S>(a, s, t, j, from, full, parity, guard);
-            else
-                forward_run<T, V, GATE, COPY, S>(a, s, t, j, from, full, parity, guard);
-        });
+        using Work = std::conditional_t<BACKWARD, Backward<T, V, GATE, COPY, S>, Forward<T, V, GATE, COPY, S>>;
+        work_tiles<Work, V, S, COPY>(a, s, stages, kStageBytes, guard);
     }
     if (s.aborted && a.aborted && threadIdx.x % 32 == 0) *(volatile uint32_t *)a.aborted = 0;
     drain_if_aborted(guard);
+    tmem_fence_before();
+    __syncthreads();
+    if (warp == kComposeWarp) tmem_free(s.columns, kColumns);
 }
 
 // ---- host --------------------------------------------------------------------------------
@@ -871,9 +1066,14 @@ int run(gsr_ctx *ctx, RecurrenceArgs &a, int dtype, cudaStream_t stream)
     a.work = (uint32_t)a.tiles * a.batch * a.slabs;
     Workspace workspace(ctx, stream);
     const bool chained = a.tiles > 1;
-    const size_t chains = (size_t)a.batch * a.slabs, groups = (a.tiles + kGroup - 1) / kGroup;
+    const size_t chains = (size_t)a.batch * a.slabs;
+    // A group's state follows the last one's a good microsecond later.  Where many chains share the SMs, a few of a
+    // chain's tiles take longer than that; where there are few, more tiles of a chain are under way at a time.
+    a.group = kMinGroup;
+    while (a.group < kMaxGroup && a.group * chains < 256) a.group *= 2;
+    a.groups = (a.tiles + a.group - 1) / a.group;
     const size_t pairs = chained ? chains * a.tiles * kSlab * sizeof(unsigned long long) : 0;
-    const size_t ends = chained ? chains * groups * kSlab * sizeof(unsigned long long) : 0;
+    const size_t ends = chained ? chains * a.groups * kSlab * sizeof(unsigned long long) : 0;
     const size_t bytes = chained ? pairs + ends + 16 : 0;
     void *work = nullptr;
     if (int rc = workspace.take(bytes, &work)) return rc;
