@@ -544,7 +544,10 @@ int check_recurrence(gsr_ctx *ctx, const gsr_recurrence *d)
 
 int check_tokens(gsr_ctx *ctx, const gsr_recurrence *d, const gsr_heads *t, const char *name, bool output)
 {
-    return check_heads(ctx, t, name, d->batch, d->tokens, 1, element_size(d->dtype), 1, output);
+    if (int rc = check_heads(ctx, t, name, d->batch, d->tokens, 1, element_size(d->dtype), 1, output)) return rc;
+    if (d->batch > 0 && d->tokens > 1 && t->token_stride > 0x7fffffff)
+        return fail(ctx, GSR_ERR_INVALID_ARG, std::string(name) + ": the token stride must be below 2^31");
+    return GSR_OK;
 }
 
 }  // namespace

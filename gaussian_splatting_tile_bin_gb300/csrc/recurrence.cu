@@ -51,7 +51,7 @@ constexpr int kAhead = 4;                  // words in flight of the warp that f
 constexpr int kColumns = 256, kSlotColumns = kColumns / 2;   // of tensor memory: two tiles' runs
 constexpr int kRun = 16, kGradRun = 8;     // tokens of a warp
 constexpr int kTile = kWarps * kRun, kGradTile = kWarps * kGradRun;
-constexpr int kStages = 2, kGradStages = 3;
+constexpr int kStages = 2;
 constexpr int kRowBytes = 128;             // of a token in a stage
 constexpr int kStateStep = GSR_RECURRENCE_BLOCK;
 static_assert(kStateStep % kRun == 0 && kGradTile == kStateStep, "states lie where runs and tiles start");
@@ -249,12 +249,14 @@ __device__ __forceinline__ void store_state(float *to, const Lanes<V> &v)
 // What a block's warps share.  A tile's part is its number's, modulo 2 or 4: what one
 // warp writes for a tile, others have read of the one that used the same place before
 // they let the writer go on.
-template <int V, int S>
+template <int V, int S, bool BACKWARD>
 struct Shared {
     Map<V> runs[2][kWarps][32];         // the runs' maps, then in their place those of the runs in front of each
     Map<V> tile[4][32];                 // the tile's
     Lanes<V> carry[4][32];              // the state in front of the tile
-    Lanes<V> h[2][kWarps][32];          // backward: H of the runs' forward maps, then h in front of each
+    // Backward: H of the runs' forward maps, then h in front of each; x (its elements' bits).
+    Lanes<V> h[BACKWARD ? 2 : 1][BACKWARD ? kWarps : 1][32];
+    uint32_t x[BACKWARD ? 2 : 1][BACKWARD ? kWarps : 1][BACKWARD ? kGradRun : 1][32];
     Tile tiles[S];
     uint32_t last[S];                   // no tile: the tickets are at an end
     uint64_t known[S], full[S], empty[S];
@@ -288,7 +290,7 @@ __device__ __forceinline__ void copy_tokens(uint32_t to, const CUtensorMap *map,
 
 // One lane: tickets in turn, and the copies of their tiles.
 template <int V, int S, bool GATE, bool COPY, bool BACKWARD>
-__device__ __forceinline__ void fetch_tiles(const RecurrenceArgs &a, const Maps &maps, Shared<V, S> &s, uint32_t stages,
+__device__ __forceinline__ void fetch_tiles(const RecurrenceArgs &a, const Maps &maps, Shared<V, S, BACKWARD> &s, uint32_t stages,
                                             const WaitGuard &guard)
 {
     constexpr int kTokens = BACKWARD ? kGradTile : kTile, kBytes = kTokens * kRowBytes;
@@ -325,8 +327,8 @@ __device__ __forceinline__ void fetch_tiles(const RecurrenceArgs &a, const Maps 
 // Calls f(tile, j) for the block's tiles in turn, j of which with tokens came before, and
 // leaves their stages.  (Once a wait has run out there may be no tile where one is looked
 // for.)
-template <int V, int S, typename F>
-__device__ __forceinline__ void each_tile(Shared<V, S> &s, const WaitGuard &guard, F f)
+template <int V, int S, bool BACKWARD, typename F>
+__device__ __forceinline__ void each_tile(Shared<V, S, BACKWARD> &s, const WaitGuard &guard, F f)
 {
     uint32_t j = 0;
     for (uint32_t i = 0;; ++i) {
@@ -345,7 +347,7 @@ __device__ __forceinline__ void each_tile(Shared<V, S> &s, const WaitGuard &guar
 // tile's map is out nobody reads that array, in which a block may write the state behind
 // the chain.
 template <int V, int S, bool BACKWARD>
-__device__ __forceinline__ void compose_runs(const RecurrenceArgs &a, Shared<V, S> &s, const Tile &t, uint32_t j,
+__device__ __forceinline__ void compose_runs(const RecurrenceArgs &a, Shared<V, S, BACKWARD> &s, const Tile &t, uint32_t j,
                                              const WaitGuard &guard)
 {
     const int lane = threadIdx.x % 32, c = min(t.slab * (32 * V) + lane * V, a.channels - V);
@@ -402,7 +404,7 @@ __device__ __forceinline__ void compose_runs(const RecurrenceArgs &a, Shared<V, 
 // behind the group's first state to the state in front of the tile, and publishes the
 // state behind a group.
 template <int V, int S, bool BACKWARD>
-__device__ __forceinline__ void follow_chain(const RecurrenceArgs &a, Shared<V, S> &s, const Tile &t, uint32_t j,
+__device__ __forceinline__ void follow_chain(const RecurrenceArgs &a, Shared<V, S, BACKWARD> &s, const Tile &t, uint32_t j,
                                              const WaitGuard &guard)
 {
     if (t.index >= t.count) return;
@@ -452,35 +454,35 @@ __device__ __forceinline__ void follow_chain(const RecurrenceArgs &a, Shared<V, 
 // ---- runs of tokens ------------------------------------------------------------------------
 
 // A warp's run of an array: a lane's elements of token after token, in the recurrence's
-// order.
+// order.  (Steps are below 2^31 elements, so that an address is one multiply-add.)
 template <typename T, int V>
 struct Run {
     using R = Raw<T, V>;
     T *at;
-    int64_t step;
+    int step;
 
     __device__ __forceinline__ Run(const RecurrenceArgs &a, const Tokens &t, const Tile &tile, int k, int c)
     {
         at = (T *)t.data + tile.b * t.batch + (int64_t)(a.reverse ? tile.length - 1 - k : k) * t.token + c;
-        step = a.reverse ? -t.token : t.token;
+        step = a.reverse ? -(int)t.token : (int)t.token;
     }
+    __device__ __forceinline__ R *token(int i) const { return (R *)(at + (int64_t)step * i); }
     // N tokens of which `count` (the same in a warp) are there; the others as 0.
     template <int N>
     __device__ __forceinline__ void load(R (&r)[N], int count) const
     {
-        const T *p = at;
         if (count == N) {
 #pragma unroll
-            for (int i = 0; i < N; ++i, p += step) r[i] = *(const R *)p;
+            for (int i = 0; i < N; ++i) r[i] = *token(i);
         } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i, p += step) {
+            for (int i = 0; i < N; ++i) {
                 clear(r[i]);
-                if (i < count) r[i] = *(const R *)p;
+                if (i < count) r[i] = *token(i);
             }
         }
     }
-    __device__ __forceinline__ void store(int i, const Lanes<V> &v) const { *(R *)(at + i * step) = raw_of<T, V>(v); }
+    __device__ __forceinline__ void store(int i, const Lanes<V> &v) const { *token(i) = raw_of<T, V>(v); }
 };
 
 // The same of a tile in a stage, a lane's 4 bytes of row after row.
@@ -515,26 +517,6 @@ template <typename T, int V>
 __device__ __forceinline__ Raw<T, V> raw_bits(uint32_t w)
 {
     return (Raw<T, V>)w;
-}
-
-// a and 1 - a as one number: the smaller of them, below 0 (or -0) where it is 1 - a.
-__device__ __forceinline__ float fold_gate(float a, float s) { return a < s ? a : -s; }
-__device__ __forceinline__ float2 fold_gate(float2 a, float2 s)
-{
-    return make_float2(fold_gate(a.x, s.x), fold_gate(a.y, s.y));
-}
-__device__ __forceinline__ void unfold_gate(float c, float &a, float &s, float &product)
-{
-    const float small = fabsf(c), large = 1.0f - small;
-    const bool kept = __float_as_int(c) < 0;
-    a = kept ? large : small;
-    s = kept ? small : large;
-    product = small * large;
-}
-__device__ __forceinline__ void unfold_gate(float2 c, float2 &a, float2 &s, float2 &product)
-{
-    unfold_gate(c.x, a.x, s.x, product.x);
-    unfold_gate(c.y, a.y, s.y, product.y);
 }
 
 // exp(-x) for x >= 0.  For f32 the product x log2(e) is kept to twice float's length.
@@ -606,6 +588,35 @@ __device__ __forceinline__ void get(const uint32_t *from, int i, float2 &v)
     v = make_float2(__uint_as_float(from[2 * i]), __uint_as_float(from[2 * i + 1]));
 }
 
+// 16 columns of the calling thread's lane.
+__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_load16(uint32_t (&r)[16], uint32_t at)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at)
+        : "memory");
+}
+// (As tensor.cuh's: values of a load are used behind its wait.)
+__device__ __forceinline__ void pin16(uint32_t (&r)[16])
+{
+#pragma unroll
+    for (int i = 0; i < 16; i += 8)
+        asm volatile(""
+                     : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                       "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+
 // What a working warp knows of its run.
 template <typename T, int V>
 struct RunPlace {
@@ -638,7 +649,7 @@ struct Forward {
     }
 
     // Reads a run, composes its map and leaves it in tensor memory.
-    static __device__ __forceinline__ void compose(const RecurrenceArgs &a, Shared<V, S> &s, const Tile &t, uint32_t j,
+    static __device__ __forceinline__ void compose(const RecurrenceArgs &a, Shared<V, S, false> &s, const Tile &t, uint32_t j,
                                                    uint32_t stage, uint32_t columns)
     {
         const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -703,7 +714,7 @@ struct Forward {
     }
 
     // Runs the tokens from the state in front of them.
-    static __device__ __forceinline__ void finish(const RecurrenceArgs &a, Shared<V, S> &s, const Tile &t, uint32_t j,
+    static __device__ __forceinline__ void finish(const RecurrenceArgs &a, Shared<V, S, false> &s, const Tile &t, uint32_t j,
                                                   uint32_t columns)
     {
         const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -749,13 +760,15 @@ struct Forward {
 
 // ---- backward ----------------------------------------------------------------------------
 
-// Words of a run in tensor memory: the folded gate, dout silu(o) (dL/dh_t without what
-// comes from behind), dout silu'(o) and x, 56 at most.
+// Words of a run in tensor memory: a, 1 - a, dout silu(o) (dL/dh_t without what comes from
+// behind) and dout silu'(o), 16 each; x waits in shared memory.  With u_t = a_t (h_(t-1) -
+// x_t), h_t = x_t + u_t and dL/df_t = dL/dx_t u_t.
 template <typename T, int V, bool GATE, bool COPY, int S>
 struct Backward {
     using F = Lanes<V>;
     using R = Raw<T, V>;
     [[maybe_unused]] static constexpr int kTokens = kGradTile, kLength = kGradRun, kBytes = kGradTile * kRowBytes;
+    static constexpr int kWords = kLength * V;
 
     static __device__ __forceinline__ void clear_rest(const RecurrenceArgs &a, const Tile &t)
     {
@@ -767,66 +780,85 @@ struct Backward {
         if (GATE) clear_tokens<T, V>(a.dgate, t.b, from, to, at.c);
     }
 
-    static __device__ __forceinline__ void compose(const RecurrenceArgs &a, Shared<V, S> &s, const Tile &t, uint32_t j,
+    static __device__ __forceinline__ void park(uint32_t columns, int part, const F (&v)[kLength])
+    {
+        uint32_t w[16];
+        put(w, v);
+        if (V == 1)
+#pragma unroll
+            for (int i = 8; i < 16; ++i) w[i] = 0;
+        tmem_store16(columns + 16 * part, w);
+    }
+    static __device__ __forceinline__ F value(const uint32_t (&w)[16], int i)
+    {
+        F v;
+        get(w, i, v);
+        return v;
+    }
+
+    static __device__ __forceinline__ void compose(const RecurrenceArgs &a, Shared<V, S, true> &s, const Tile &t, uint32_t j,
                                                    uint32_t stage, uint32_t columns)
     {
         const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
         const RunPlace<T, V> at(a, t, kTokens, kLength);
-        F keep[kLength], rest[kLength], into[kLength], slope[kLength], h, one;
-        R x[kLength];
-        fill(one, 1.0f);
-        {
-            R f[kLength], dy[kLength], o[GATE ? kLength : 1];
-            if constexpr (COPY) {
-                const StagedRun staged(a, stage, kTokens, warp * kLength);
-#pragma unroll
-                for (int i = 0; i < kLength; ++i) {
-                    f[i] = raw_bits<T, V>(staged.word(i, 0));
-                    x[i] = raw_bits<T, V>(staged.word(i, kBytes));
-                    if constexpr (GATE) o[i] = raw_bits<T, V>(staged.word(i, 2 * kBytes));
-                    dy[i] = raw_bits<T, V>(staged.word(i, (GATE ? 3 : 2) * kBytes));
-                }
-            } else {
-                Run<T, V>(a, a.forget, t, at.k0, at.c).load(f, at.count);
-                Run<T, V>(a, a.x, t, at.k0, at.c).load(x, at.count);
-                Run<T, V>(a, a.dout, t, at.k0, at.c).load(dy, at.count);
-                if constexpr (GATE) Run<T, V>(a, a.gate, t, at.k0, at.c).load(o, at.count);
-            }
-            if (at.count < kLength)
-#pragma unroll
-                for (int i = 0; i < kLength; ++i)
-                    if (i >= at.count) {
-                        clear(x[i]);
-                        clear(dy[i]);
-                        if constexpr (GATE) clear(o[i]);
-                    }
+        F keep[kLength], rest[kLength], into[kLength], h;
+        R x[kLength], f[kLength], dy[kLength], o[GATE ? kLength : 1];
+        if constexpr (COPY) {
+            const StagedRun staged(a, stage, kTokens, warp * kLength);
 #pragma unroll
             for (int i = 0; i < kLength; ++i) {
-                split<T>(value_of<T, V>(f[i]), keep[i], rest[i]);
-                const F d = value_of<T, V>(dy[i]);
-                if constexpr (GATE) {
-                    const F g = value_of<T, V>(o[i]), r = sigmoid<T>(g);
-                    into[i] = mul(d, mul(g, r));
-                    slope[i] = mul(d, mul(r, mad(g, add(one, minus(r)), one)));
-                } else {
-                    into[i] = d;
-                    fill(slope[i], 0.0f);
-                }
+                f[i] = raw_bits<T, V>(staged.word(i, 0));
+                x[i] = raw_bits<T, V>(staged.word(i, kBytes));
+                if constexpr (GATE) o[i] = raw_bits<T, V>(staged.word(i, 2 * kBytes));
+                dy[i] = raw_bits<T, V>(staged.word(i, (GATE ? 3 : 2) * kBytes));
             }
-            if (at.count < kLength)
-#pragma unroll
-                for (int i = 0; i < kLength; ++i)
-                    if (i >= at.count) {   // no step (its x and dout are 0)
-                        fill(keep[i], 1.0f);
-                        fill(rest[i], 0.0f);
-                    }
+        } else {
+            Run<T, V>(a, a.forget, t, at.k0, at.c).load(f, at.count);
+            Run<T, V>(a, a.x, t, at.k0, at.c).load(x, at.count);
+            Run<T, V>(a, a.dout, t, at.k0, at.c).load(dy, at.count);
+            if constexpr (GATE) Run<T, V>(a, a.gate, t, at.k0, at.c).load(o, at.count);
         }
+        if (at.count < kLength)
+#pragma unroll
+            for (int i = 0; i < kLength; ++i)
+                if (i >= at.count) {
+                    clear(x[i]);
+                    clear(dy[i]);
+                    if constexpr (GATE) clear(o[i]);
+                }
+        if constexpr (GATE) {
+            F slope[kLength], one;
+            fill(one, 1.0f);
+#pragma unroll
+            for (int i = 0; i < kLength; ++i) {
+                const F d = value_of<T, V>(dy[i]), g = value_of<T, V>(o[i]), r = sigmoid<T>(g), dr = mul(d, r);
+                into[i] = mul(dr, g);
+                slope[i] = mul(dr, mad(g, add(one, minus(r)), one));
+            }
+            park(columns, 3, slope);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kLength; ++i) into[i] = value_of<T, V>(dy[i]);
+        }
+        park(columns, 2, into);
+#pragma unroll
+        for (int i = 0; i < kLength; ++i) split<T>(value_of<T, V>(f[i]), keep[i], rest[i]);
+        if (at.count < kLength)
+#pragma unroll
+            for (int i = 0; i < kLength; ++i)
+                if (i >= at.count) {   // no step (its x and dout are 0)
+                    fill(keep[i], 1.0f);
+                    fill(rest[i], 0.0f);
+                }
+        park(columns, 0, keep);
+        park(columns, 1, rest);
         Map<V> own;
         fill(h, 0.0f);
         fill(own.a, 1.0f);
         fill(own.h, 0.0f);
 #pragma unroll
         for (int i = 0; i < kLength; ++i) {
+            s.x[j & 1][warp][i][lane] = x[i];
             h = mad(keep[i], h, mul(rest[i], value_of<T, V>(x[i])));
             own.a = mul(keep[i], own.a);
         }
@@ -834,69 +866,49 @@ struct Backward {
         for (int i = kLength - 1; i >= 0; --i) own.h = mul(keep[i], add(own.h, into[i]));
         s.runs[j & 1][warp][lane] = own;
         s.h[j & 1][warp][lane] = h;
-        uint32_t w0[32], w1[32];
-#pragma unroll
-        for (int i = 0; i < kLength; ++i) rest[i] = fold_gate(keep[i], rest[i]);
-        put(w0, rest);
-        put(w0 + 8 * V, into);
-        if (V == 2) {
-            put(w1, slope);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                w1[16 + i] = x[i];
-                w1[24 + i] = 0;
-            }
-            tmem_store32(columns + 32, w1);
-        } else {
-            put(w0 + 16, slope);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w0[24 + i] = x[i];
-        }
-        tmem_store32(columns, w0);
         tmem_wait_store();
     }
 
-    static __device__ __forceinline__ void finish(const RecurrenceArgs &a, Shared<V, S> &s, const Tile &t, uint32_t j,
+    static __device__ __forceinline__ void finish(const RecurrenceArgs &a, Shared<V, S, true> &s, const Tile &t, uint32_t j,
                                                   uint32_t columns)
     {
         const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
         const RunPlace<T, V> at(a, t, kTokens, kLength);
-        uint32_t w0[32], w1[32];
-        tmem_load32(w0, columns);
-        if (V == 2) tmem_load32(w1, columns + 32);
+        uint32_t keep[16], rest[16], into[16];
+        F u[kLength], h = s.h[j & 1][warp][lane];
         const Map<V> behind = s.runs[j & 1][warp][lane];
         F p = mad(behind.a, s.carry[j & 3][lane], behind.h);
-        F hs[kLength + 1];   // in front of each token, and behind the last
-        hs[0] = s.h[j & 1][warp][lane];
-        tmem_wait_load();
-        pin(w0);
-        if (V == 2) pin(w1);
-        if (at.count == 0 || !at.mine) return;
-        auto word = [&](int part, int i) {   // 1 - a, into, slope
-            F v;
-            if (V == 2 && part == 2)
-                get(w1, i, v);
-            else
-                get(w0, part * 8 + i, v);
-            return v;
-        };
-        auto x = [&](int i) { return value_of<T, V>((R)(V == 2 ? w1[16 + i] : w0[24 + i])); };
+        {
+            uint32_t slope[16];
+            tmem_load16(keep, columns);
+            if (GATE) tmem_load16(slope, columns + 48);
+            tmem_wait_load();
+            pin16(keep);
+            if (GATE) pin16(slope);
+            tmem_load16(rest, columns + 16);
+            tmem_load16(into, columns + 32);
+            const bool some = at.count > 0 && at.mine;
+            const Run<T, V> dg(a, a.dgate, t, at.k0, at.c);
 #pragma unroll
-        for (int i = 0; i < kLength; ++i) {
-            F keep, rest, product;
-            unfold_gate(word(0, i), keep, rest, product);
-            hs[i + 1] = mad(keep, hs[i], mul(rest, x(i)));
+            for (int i = 0; i < kLength; ++i) {
+                const F x = value_of<T, V>((R)s.x[j & 1][warp][i][lane]);
+                u[i] = mul(value(keep, i), add(h, minus(x)));
+                h = add(x, u[i]);
+                if constexpr (GATE)
+                    if (some && i < at.count) dg.store(i, mul(value(slope, i), h));
+            }
+            tmem_wait_load();
+            pin16(rest);
+            pin16(into);
+            if (!some) return;
         }
-        const Run<T, V> dx(a, a.dx, t, at.k0, at.c), df(a, a.dforget, t, at.k0, at.c), dg(a, a.dgate, t, at.k0, at.c);
+        const Run<T, V> dx(a, a.dx, t, at.k0, at.c), df(a, a.dforget, t, at.k0, at.c);
         auto token = [&](int i, bool there) {
-            F keep, rest, product;
-            unfold_gate(word(0, i), keep, rest, product);
-            const F dh = add(p, word(1, i));
-            p = mul(keep, dh);
+            const F dh = add(p, value(into, i)), enter = mul(dh, value(rest, i));
+            p = mul(value(keep, i), dh);
             if (!there) return;
-            dx.store(i, mul(dh, rest));
-            df.store(i, mul(mul(dh, product), add(hs[i], minus(x(i)))));
-            if constexpr (GATE) dg.store(i, mul(word(2, i), hs[i + 1]));
+            dx.store(i, enter);
+            df.store(i, mul(enter, u[i]));
         };
         if (at.count == kLength) {
 #pragma unroll
@@ -910,8 +922,8 @@ struct Backward {
 };
 
 // A working warp's tiles: the next one's run is composed before the last one's ends.
-template <typename Work, int V, int S, bool COPY>
-__device__ __forceinline__ void work_tiles(const RecurrenceArgs &a, Shared<V, S> &s, uint32_t stages, int stage_bytes,
+template <typename Work, int V, int S, bool COPY, bool BACKWARD>
+__device__ __forceinline__ void work_tiles(const RecurrenceArgs &a, Shared<V, S, BACKWARD> &s, uint32_t stages, int stage_bytes,
                                            const WaitGuard &guard)
 {
     const int warp = threadIdx.x / 32;
@@ -952,10 +964,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     k_recurrence(const RecurrenceArgs a, const __grid_constant__ Maps maps)
 {
     grid_dependency_begin();
-    constexpr int S = BACKWARD ? kGradStages : kStages;
+    constexpr int S = kStages;
     constexpr int kStageBytes = (2 + (GATE ? 1 : 0) + (BACKWARD ? 1 : 0)) * (BACKWARD ? kGradTile : kTile) * kRowBytes;
     extern __shared__ unsigned char s_bytes[];
-    __shared__ Shared<V, S> s;
+    __shared__ Shared<V, S, BACKWARD> s;
     const uint32_t stages = (smem_address(s_bytes) + 127u) / 128u * 128u;
     const WaitGuard guard = {&s.aborted, a.status};
     const int warp = threadIdx.x / 32;
@@ -989,7 +1001,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     } else {
         take_registers();
         using Work = std::conditional_t<BACKWARD, Backward<T, V, GATE, COPY, S>, Forward<T, V, GATE, COPY, S>>;
-        work_tiles<Work, V, S, COPY>(a, s, stages, kStageBytes, guard);
+        work_tiles<Work, V, S, COPY, BACKWARD>(a, s, stages, kStageBytes, guard);
     }
     if (s.aborted && a.aborted && threadIdx.x % 32 == 0) *(volatile uint32_t *)a.aborted = 0;
     drain_if_aborted(guard);
@@ -1031,7 +1043,7 @@ template <typename T, int V, bool GATE, bool COPY, bool BACKWARD>
 int launch(gsr_ctx *ctx, RecurrenceArgs &a, int dtype, const char *what, cudaStream_t stream)
 {
     constexpr int kTokens = BACKWARD ? kGradTile : kTile, kArrays = 2 + (GATE ? 1 : 0) + (BACKWARD ? 1 : 0);
-    constexpr int kBytes = COPY ? (BACKWARD ? kGradStages : kStages) * kArrays * kTokens * kRowBytes + 128 : 0;
+    constexpr int kBytes = COPY ? kStages * kArrays * kTokens * kRowBytes + 128 : 0;
     Maps maps = {};
     if (COPY) {
         const struct { CUtensorMap *map; const Tokens *t; } inputs[4] = {

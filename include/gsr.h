@@ -626,7 +626,7 @@ int gsr_layer_norm_backward(gsr_ctx *ctx, const gsr_layer_norm *desc, const gsr_
  * Errors: GSR_ERR_INVALID_ARG (null or misaligned arrays; negative sizes; channels
  * outside [1, GSR_MAX_RECURRENCE_CHANNELS]; batch above 2^16, tokens above 2^24,
  * batch * tokens above GSR_MAX_TOKENS; 2^31 blocks of 64 tokens x 32 channels or
- * more; outputs with a stride of 0 over more than one item; unknown dtype),
+ * more; a token stride of 2^31 elements or more; outputs with a stride of 0 over more than one item; unknown dtype),
  * GSR_ERR_OOM, GSR_ERR_CUDA. */
 #define GSR_RECURRENCE_BLOCK 64
 #define GSR_MAX_RECURRENCE_CHANNELS 65536
