@@ -21,7 +21,7 @@
 // (no pair is: A is never that NaN).
 //
 // A block's warps.  Eight work on runs.  One takes tickets and starts the tiles' copies
-// into a ring of stages.  One follows the chain.  One composes the runs' maps, publishes
+// into a ring of stages.  Two follow the chain.  One composes the runs' maps, publishes
 // the tile's and hands each run the map of those in front of it.  A working warp composes
 // its run of the next tile before it finishes the one of the last: its gates and inputs
 // wait in tensor memory (256 columns a block) meanwhile, so that the time that a map takes
@@ -39,7 +39,7 @@ namespace gsr {
 namespace {
 
 constexpr int kWarps = 8;                  // that work on runs
-constexpr int kComposeWarp = kWarps, kChainWarp = kWarps + 1, kFetchWarp = kWarps + 2;
+constexpr int kComposeWarp = kWarps, kFetchWarp = kWarps + 1, kChainWarp = kWarps + 2;   // two of the last
 constexpr int kThreads = 32 * (kWarps + 4);
 constexpr int kBlocks = 2;                 // of an SM
 // Registers of a thread: the start's, and after the warps beside the runs have given
@@ -47,7 +47,7 @@ constexpr int kBlocks = 2;                 // of an SM
 constexpr int kStart = 80, kFew = 48, kMany = 96;
 static_assert(kWarps == 8 && 4 * kFew + 8 * kMany <= 12 * kStart, "the shares must fit what a block starts with");
 constexpr int kMinGroup = 16, kMaxGroup = 32;   // tiles of a group
-constexpr int kAhead = 4;                  // words in flight of the warp that folds them
+constexpr int kAhead = 8;                  // words in flight of a warp that folds them
 constexpr int kColumns = 256, kSlotColumns = kColumns / 2;   // of tensor memory: two tiles' runs
 constexpr int kRun = 16, kGradRun = 8;     // tokens of a warp
 constexpr int kTile = kWarps * kRun, kGradTile = kWarps * kGradRun;
@@ -174,40 +174,38 @@ __device__ __forceinline__ void publish(unsigned long long *to, const Words<2> &
 {
     asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};" ::"l"(to), "l"(v.w[0]), "l"(v.w[1]) : "memory");
 }
-__device__ __forceinline__ void look(const unsigned long long *at, Words<1> &v)
+__device__ __forceinline__ void look(const unsigned long long *at, unsigned long long &w)
 {
-    asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(v.w[0]) : "l"(at) : "memory");
+    asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(w) : "l"(at) : "memory");
 }
-__device__ __forceinline__ void look(const unsigned long long *at, Words<2> &v)
+// Looks at `count` rows of words, a lane at its own of each, until all are there or the
+// wait has run out (here or elsewhere).  Rows that are missing are looked at together.
+template <int N>
+__device__ __forceinline__ void wait_for(const RecurrenceArgs &a, const unsigned long long *at, int stride, int count,
+                                         unsigned long long (&v)[N])
 {
-    asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];" : "=l"(v.w[0]), "=l"(v.w[1]) : "l"(at) : "memory");
-}
-
-template <int V>
-__device__ __forceinline__ bool ready(const Words<V> &v)
-{
-    bool all = true;
 #pragma unroll
-    for (int j = 0; j < V; ++j) all = all && v.w[j] != ~0ull;
-    return all;
-}
-
-// Looks until the words are there, or the wait has run out (here or elsewhere).
-template <int V>
-__device__ __forceinline__ void wait_for(const RecurrenceArgs &a, const unsigned long long *at, Words<V> &v)
-{
-    if (ready(v)) return;
+    for (int k = 0; k < N; ++k) {
+        v[k] = ~0ull;
+        if (k < count) look(at + k * stride, v[k]);
+    }
     const long long start = clock64();
     for (int turn = 1;; ++turn) {
-        look(at, v);
-        if (ready(v)) return;
+        bool all = true;
+#pragma unroll
+        for (int k = 0; k < N; ++k) all = all && (k >= count || v[k] != ~0ull);
+        if (__all_sync(~0u, all)) return;
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (k < count && v[k] == ~0ull) look(at + k * stride, v[k]);
         if (turn % 64 != 0) continue;
-        if (*(volatile uint32_t *)a.aborted == 0) return;
+        bool stop = *(volatile uint32_t *)a.aborted == 0;
         if (clock64() - start > kWaitCycles) {
             *(volatile uint32_t *)a.aborted = 0;
             *(volatile uint32_t *)a.status = 1;
-            return;
+            stop = true;
         }
+        if (__any_sync(~0u, stop)) return;
     }
 }
 
@@ -402,53 +400,48 @@ __device__ __forceinline__ void compose_runs(const RecurrenceArgs &a, Shared<V, 
 
 // Folds the maps that the group's tiles before this one have published, takes them
 // behind the group's first state to the state in front of the tile, and publishes the
-// state behind a group.
+// state behind a group.  A warp for each of a lane's channels.
 template <int V, int S, bool BACKWARD>
 __device__ __forceinline__ void follow_chain(const RecurrenceArgs &a, Shared<V, S, BACKWARD> &s, const Tile &t, uint32_t j,
                                              const WaitGuard &guard)
 {
-    if (t.index >= t.count) return;
-    const int lane = threadIdx.x % 32, place = place_of<BACKWARD>(t);
+    const int lane = threadIdx.x % 32, channel = threadIdx.x / 32 - kChainWarp, place = place_of<BACKWARD>(t);
+    if (t.index >= t.count || channel >= V) return;
     const int64_t row = (int64_t)t.b * a.slabs + t.slab;
-    const int group = place / a.group, first = group * a.group;
-    const unsigned long long *pairs = a.pairs + row * a.tiles * (32 * V) + lane * V;
-    unsigned long long *ends = a.ends + (row * a.groups + group) * (32 * V) + lane * V;
-    Lanes<V> state;
-    fill(state, 0.0f);   // (the first map of a chain takes no state)
+    const int group = place / a.group, first = group * a.group, count = place - first;
+    const unsigned long long *pairs = a.pairs + (row * a.tiles + first) * (32 * V) + lane * V + channel;
+    unsigned long long *ends = a.ends + (row * a.groups + group) * (32 * V) + lane * V + channel;
+    float state = 0.0f;   // (the first map of a chain takes no state)
     if (place > 0) {
-        Map<V> m;
-        fill(m.a, 1.0f);
-        fill(m.h, 0.0f);
-        for (int from = first; from < place; from += kAhead) {
-            Words<V> seen[kAhead];
+        // The tile right before this one is the last to come; once it is there, so are
+        // most of the others.
+        unsigned long long last[1], seen[kAhead], end[1];
+        Map<1> m = {1.0f, 0.0f};
+        if (count > 0) {
+            wait_for(a, pairs + (count - 1) * (32 * V), 0, 1, last);
+            for (int from = 0; from < count - 1; from += kAhead) {
+                wait_for(a, pairs + from * (32 * V), 32 * V, count - 1 - from, seen);
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (from + k < place) look(pairs + (int64_t)(from + k) * (32 * V), seen[k]);
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (from + k < place) {
-                    wait_for(a, pairs + (int64_t)(from + k) * (32 * V), seen[k]);
-                    m = then(m, seen[k].map());
-                }
+                for (int k = 0; k < kAhead; ++k)
+                    if (from + k < count - 1) m = then(m, Words<1>{{seen[k]}}.map());
+            }
+            m = then(m, Words<1>{{last[0]}}.map());
         }
         if (group > 0) {
-            Words<V> end;
-            look(ends, end);
-            wait_for(a, ends, end);
-            state = end.map().h;
+            wait_for(a, ends, 0, 1, end);
+            state = Words<1>{{end[0]}}.map().h;
         }
         state = mad(m.a, state, m.h);
-        s.carry[j & 3][lane] = state;
+        at(s.carry[j & 3][lane], channel) = state;
     }
     // (A barrier for even tiles and one for odd: the working warps look at a tile's when
     // the next one's may be through already.)
     warp_arrive(s.state_ready[j & 1]);
     barrier_wait_warp(smem_address(&s.state_ready[j & 1]), j >> 1 & 1, guard);
     if (place % a.group != a.group - 1 || place + 1 >= t.count) return;
-    Map<V> end = s.tile[j & 3][lane];
-    end.h = mad(end.a, state, end.h);
-    fill(end.a, 0.0f);
-    publish(ends + 32 * V, Words<V>::of(end));
+    const Map<V> tile = s.tile[j & 3][lane];
+    const Map<1> end = {0.0f, mad(at(tile.a, channel), state, at(tile.h, channel))};
+    publish(ends + 32 * V, Words<1>::of(end));
 }
 
 // ---- runs of tokens ------------------------------------------------------------------------
@@ -768,7 +761,6 @@ struct Backward {
     using F = Lanes<V>;
     using R = Raw<T, V>;
     [[maybe_unused]] static constexpr int kTokens = kGradTile, kLength = kGradRun, kBytes = kGradTile * kRowBytes;
-    static constexpr int kWords = kLength * V;
 
     static __device__ __forceinline__ void clear_rest(const RecurrenceArgs &a, const Tile &t)
     {
@@ -976,11 +968,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
         for (int k = 0; k < S; ++k) {
             barrier_init(smem_address(&s.known[k]), 1);
             barrier_init(smem_address(&s.full[k]), 1);
-            barrier_init(smem_address(&s.empty[k]), kWarps + 2);
+            barrier_init(smem_address(&s.empty[k]), kWarps + 3);
         }
         for (int k = 0; k < 2; ++k) {
             barrier_init(smem_address(&s.runs_ready[k]), kWarps);
-            barrier_init(smem_address(&s.state_ready[k]), 2);
+            barrier_init(smem_address(&s.state_ready[k]), 1 + V);
         }
         fence_async();
     }
@@ -993,7 +985,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
         if (warp == kFetchWarp) {
             if (threadIdx.x % 32 == 0) fetch_tiles<V, S, GATE, COPY, BACKWARD>(a, maps, s, stages, guard);
             __syncwarp();
-        } else if (warp == kChainWarp) {
+        } else if (warp >= kChainWarp) {
             each_tile(s, guard, [&](const Tile &t, uint32_t j) { follow_chain<V, S, BACKWARD>(a, s, t, j, guard); });
         } else if (warp == kComposeWarp) {
             each_tile(s, guard, [&](const Tile &t, uint32_t j) { compose_runs<V, S, BACKWARD>(a, s, t, j, guard); });
