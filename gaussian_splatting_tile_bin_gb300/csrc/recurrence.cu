@@ -178,17 +178,22 @@ __device__ __forceinline__ void look(const unsigned long long *at, unsigned long
 {
     asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(w) : "l"(at) : "memory");
 }
-// Looks at `count` rows of words, a lane at its own of each, until all are there or the
-// wait has run out (here or elsewhere).  Rows that are missing are looked at together.
+// A lane's words of `count` rows, and a wait for those that are missing: looked at together
+// until all are there or the wait has run out (here or elsewhere).
 template <int N>
-__device__ __forceinline__ void wait_for(const RecurrenceArgs &a, const unsigned long long *at, int stride, int count,
-                                         unsigned long long (&v)[N])
+__device__ __forceinline__ void look(const unsigned long long *at, int stride, int count, unsigned long long (&v)[N])
 {
 #pragma unroll
     for (int k = 0; k < N; ++k) {
         v[k] = ~0ull;
         if (k < count) look(at + k * stride, v[k]);
     }
+}
+
+template <int N>
+__device__ __forceinline__ void wait_for(const RecurrenceArgs &a, const unsigned long long *at, int stride, int count,
+                                         unsigned long long (&v)[N])
+{
     const long long start = clock64();
     for (int turn = 1;; ++turn) {
         bool all = true;
@@ -413,19 +418,19 @@ __device__ __forceinline__ void follow_chain(const RecurrenceArgs &a, Shared<V, 
     unsigned long long *ends = a.ends + (row * a.groups + group) * (32 * V) + lane * V + channel;
     float state = 0.0f;   // (the first map of a chain takes no state)
     if (place > 0) {
-        // The tile right before this one is the last to come; once it is there, so are
-        // most of the others.
-        unsigned long long last[1], seen[kAhead], end[1];
+        // The latest tiles' maps are waited for together, behind the older ones, which are
+        // mostly there.
+        unsigned long long seen[kAhead], end[1];
         Map<1> m = {1.0f, 0.0f};
-        if (count > 0) {
-            wait_for(a, pairs + (count - 1) * (32 * V), 0, 1, last);
-            for (int from = 0; from < count - 1; from += kAhead) {
-                wait_for(a, pairs + from * (32 * V), 32 * V, count - 1 - from, seen);
+        look(ends, 0, group > 0, end);
+        for (int from = 0; from < count;) {
+            const int take = count - from > kAhead ? min(kAhead, count - from - kAhead) : count - from;
+            look(pairs + from * (32 * V), 32 * V, take, seen);
+            wait_for(a, pairs + from * (32 * V), 32 * V, take, seen);
 #pragma unroll
-                for (int k = 0; k < kAhead; ++k)
-                    if (from + k < count - 1) m = then(m, Words<1>{{seen[k]}}.map());
-            }
-            m = then(m, Words<1>{{last[0]}}.map());
+            for (int k = 0; k < kAhead; ++k)
+                if (k < take) m = then(m, Words<1>{{seen[k]}}.map());
+            from += take;
         }
         if (group > 0) {
             wait_for(a, ends, 0, 1, end);
