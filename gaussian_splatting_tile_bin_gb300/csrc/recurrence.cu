@@ -14,11 +14,13 @@
 // computes h again from the forward's states.
 //
 // The chain.  Tiles are taken from a ticket in the chain's order, so a tile waits only
-// for tiles that blocks work on or are done with.  Each publishes its (A, H), the
-// last of a group also the state behind it, and a tile folds what its group's tiles before
-// it have published: the composition does not depend on timing, so results are the same
-// bits on every run.  A published pair is one 64-bit word, which is all ones before that
-// (no pair is: A is never that NaN).
+// for tiles that blocks work on or are done with.  Each publishes its (A, H), the last of
+// a group the group's, and again, as a map of no state, once it knows the state behind it.
+// A tile folds its group's maps, and takes the state in front of the group from the latest
+// group whose state is known and the maps of those behind that: always map by map, so
+// that the bits are the same wherever it starts, and results are on every run.  A map is
+// one 64-bit word, which is all ones before it is published (no map is: A is never that
+// NaN).
 //
 // A block's warps.  Eight work on runs.  One takes tickets and starts the tiles' copies
 // into a ring of stages.  Two follow the chain.  One composes the runs' maps, publishes
@@ -46,8 +48,7 @@ constexpr int kBlocks = 2;                 // of an SM
 // theirs to the others.
 constexpr int kStart = 80, kFew = 48, kMany = 96;
 static_assert(kWarps == 8 && 4 * kFew + 8 * kMany <= 12 * kStart, "the shares must fit what a block starts with");
-constexpr int kMinGroup = 16, kMaxGroup = 32;   // tiles of a group
-constexpr int kAhead = 8;                  // words in flight of a warp that folds them
+constexpr int kGroup = 8, kWindow = 2;     // tiles of a group; groups that a tile looks back on
 constexpr int kColumns = 256, kSlotColumns = kColumns / 2;   // of tensor memory: two tiles' runs
 constexpr int kRun = 16, kGradRun = 8;     // tokens of a warp
 constexpr int kTile = kWarps * kRun, kGradTile = kWarps * kGradRun;
@@ -68,7 +69,7 @@ struct RecurrenceArgs {
     const int *lengths;
     int batch, tokens, channels, blocks;
     int tiles, slabs;            // of all tokens, of all channels
-    int group, groups;           // tiles of a group, groups of all tokens
+    int groups;                  // of all tokens
     uint32_t work;               // their number over all items
     int reverse;
     unsigned long long *pairs, *ends;   // published: [batch, slabs, tiles] and [batch, slabs, groups] rows of words
@@ -140,69 +141,52 @@ __device__ __forceinline__ Map<V> then(const Map<V> &first, const Map<V> &second
     return {mul(second.a, first.a), mad(second.a, first.h, second.h)};
 }
 
-template <int V>
-struct Words {
-    unsigned long long w[V];
-
-    __device__ __forceinline__ static Words of(const Map<V> &m)
-    {
-        Words v;
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            v.w[j] = (unsigned long long)__float_as_uint(at(m.h, j)) << 32 | __float_as_uint(at(m.a, j));
-        return v;
-    }
-    __device__ __forceinline__ Map<V> map() const
-    {
-        Map<V> m;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            at(m.a, j) = __uint_as_float((uint32_t)w[j]);
-            at(m.h, j) = __uint_as_float((uint32_t)(w[j] >> 32));
-        }
-        return m;
-    }
-};
+// A map of one channel as a word.
+__device__ __forceinline__ unsigned long long word_of(const Map<1> &m)
+{
+    return (unsigned long long)__float_as_uint(m.h) << 32 | __float_as_uint(m.a);
+}
+__device__ __forceinline__ Map<1> map_of(unsigned long long w)
+{
+    return {__uint_as_float((uint32_t)w), __uint_as_float((uint32_t)(w >> 32))};
+}
+constexpr unsigned long long kNoMap = ~0ull;
+// (A word whose map takes no state, A = 0: one of a known state.)
+__device__ __forceinline__ bool is_state(unsigned long long w) { return (uint32_t)w == 0; }
 
 // ---- the chain ---------------------------------------------------------------------------
 
-__device__ __forceinline__ void publish(unsigned long long *to, const Words<1> &v)
+__device__ __forceinline__ void publish(unsigned long long *to, unsigned long long w)
 {
-    asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(to), "l"(v.w[0]) : "memory");
-}
-__device__ __forceinline__ void publish(unsigned long long *to, const Words<2> &v)
-{
-    asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};" ::"l"(to), "l"(v.w[0]), "l"(v.w[1]) : "memory");
+    asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(to), "l"(w) : "memory");
 }
 __device__ __forceinline__ void look(const unsigned long long *at, unsigned long long &w)
 {
     asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(w) : "l"(at) : "memory");
 }
-// A lane's words of `count` rows, and a wait for those that are missing: looked at together
-// until all are there or the wait has run out (here or elsewhere).
+// A lane's words of `count` rows, and a wait until they are enough for every lane: looked
+// at together until then, those that are missing or (known_only) no map of a known state,
+// or until the wait has run out (here or elsewhere).
 template <int N>
 __device__ __forceinline__ void look(const unsigned long long *at, int stride, int count, unsigned long long (&v)[N])
 {
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        v[k] = ~0ull;
+        v[k] = kNoMap;
         if (k < count) look(at + k * stride, v[k]);
     }
 }
 
-template <int N>
+template <int N, typename F>
 __device__ __forceinline__ void wait_for(const RecurrenceArgs &a, const unsigned long long *at, int stride, int count,
-                                         unsigned long long (&v)[N])
+                                         unsigned long long (&v)[N], bool known_only, F enough)
 {
     const long long start = clock64();
     for (int turn = 1;; ++turn) {
-        bool all = true;
-#pragma unroll
-        for (int k = 0; k < N; ++k) all = all && (k >= count || v[k] != ~0ull);
-        if (__all_sync(~0u, all)) return;
+        if (__all_sync(~0u, enough())) return;
 #pragma unroll
         for (int k = 0; k < N; ++k)
-            if (k < count && v[k] == ~0ull) look(at + k * stride, v[k]);
+            if (k < count && (known_only ? !is_state(v[k]) : v[k] == kNoMap)) look(at + k * stride, v[k]);
         if (turn % 64 != 0) continue;
         bool stop = *(volatile uint32_t *)a.aborted == 0;
         if (clock64() - start > kWaitCycles) {
@@ -263,7 +247,7 @@ struct Shared {
     Tile tiles[S];
     uint32_t last[S];                   // no tile: the tickets are at an end
     uint64_t known[S], full[S], empty[S];
-    uint64_t runs_ready[2], state_ready[2];
+    uint64_t runs_ready[2], tile_ready[2], state_ready[2];
     uint32_t aborted, columns;
 };
 
@@ -396,16 +380,23 @@ __device__ __forceinline__ void compose_runs(const RecurrenceArgs &a, Shared<V, 
             out.h = mad(out.a, seed, out.h);
             fill(out.a, 0.0f);
         }
-        publish(a.pairs + (((int64_t)t.b * a.slabs + t.slab) * a.tiles + place) * (32 * V) + lane * V, Words<V>::of(out));
+        unsigned long long *to = a.pairs + (((int64_t)t.b * a.slabs + t.slab) * a.tiles + place) * (32 * V) + lane;
+#pragma unroll
+        for (int k = 0; k < V; ++k) publish(to + 32 * k, word_of({at(out.a, k), at(out.h, k)}));
+    }
+    if (place == 0) {
+        m.h = mad(m.a, seed, m.h);   // (as published)
+        fill(m.a, 0.0f);
+        s.carry[j & 3][lane] = seed;
     }
     s.tile[j & 3][lane] = m;
-    if (place == 0) s.carry[j & 3][lane] = seed;
+    warp_arrive(s.tile_ready[j & 1]);
     warp_arrive(s.state_ready[j & 1]);
 }
 
-// Folds the maps that the group's tiles before this one have published, takes them
-// behind the group's first state to the state in front of the tile, and publishes the
-// state behind a group.  A warp for each of a lane's channels.
+// Folds the maps that the group's tiles before this one have published, finds the state
+// in front of the group, and with both the one in front of the tile; publishes the group's
+// map and the state behind it.  A warp for each of a lane's channels.
 template <int V, int S, bool BACKWARD>
 __device__ __forceinline__ void follow_chain(const RecurrenceArgs &a, Shared<V, S, BACKWARD> &s, const Tile &t, uint32_t j,
                                              const WaitGuard &guard)
@@ -413,28 +404,51 @@ __device__ __forceinline__ void follow_chain(const RecurrenceArgs &a, Shared<V, 
     const int lane = threadIdx.x % 32, channel = threadIdx.x / 32 - kChainWarp, place = place_of<BACKWARD>(t);
     if (t.index >= t.count || channel >= V) return;
     const int64_t row = (int64_t)t.b * a.slabs + t.slab;
-    const int group = place / a.group, first = group * a.group, count = place - first;
-    const unsigned long long *pairs = a.pairs + (row * a.tiles + first) * (32 * V) + lane * V + channel;
-    unsigned long long *ends = a.ends + (row * a.groups + group) * (32 * V) + lane * V + channel;
+    const int group = place / kGroup, count = place - group * kGroup, groups = min(group, kWindow);
+    const unsigned long long *pairs = a.pairs + (row * a.tiles + group * kGroup) * (32 * V) + channel * 32 + lane;
+    unsigned long long *ends = a.ends + (row * a.groups + group) * (32 * V) + channel * 32 + lane;
+    const unsigned long long *window = ends - groups * (32 * V);
     float state = 0.0f;   // (the first map of a chain takes no state)
     if (place > 0) {
-        // The latest tiles' maps are waited for together, behind the older ones, which are
-        // mostly there.
-        unsigned long long seen[kAhead], end[1];
-        Map<1> m = {1.0f, 0.0f};
-        look(ends, 0, group > 0, end);
-        for (int from = 0; from < count;) {
-            const int take = count - from > kAhead ? min(kAhead, count - from - kAhead) : count - from;
-            look(pairs + from * (32 * V), 32 * V, take, seen);
-            wait_for(a, pairs + from * (32 * V), 32 * V, take, seen);
+        unsigned long long seen[kGroup - 1], behind[kWindow];
+        look(pairs, 32 * V, count, seen);
+        look(window, 32 * V, groups, behind);
+        wait_for(a, pairs, 32 * V, count, seen, false, [&] {
+            bool all = true;
 #pragma unroll
-            for (int k = 0; k < kAhead; ++k)
-                if (k < take) m = then(m, Words<1>{{seen[k]}}.map());
-            from += take;
+            for (int k = 0; k < kGroup - 1; ++k) all = all && (k >= count || seen[k] != kNoMap);
+            return all;
+        });
+        Map<1> m = {1.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < kGroup - 1; ++k)
+            if (k < count) m = then(m, map_of(seen[k]));
+        const bool closes = count == kGroup - 1 && place + 1 < t.count;
+        Map<1> whole = m;
+        if (closes) {
+            barrier_wait_warp(smem_address(&s.tile_ready[j & 1]), j >> 1 & 1, guard);
+            const Map<V> tile = s.tile[j & 3][lane];
+            whole = then(m, Map<1>{at(tile.a, channel), at(tile.h, channel)});
+            // (The first group's takes no state, whatever its A has become.)
+            publish(ends, word_of({group > 0 ? whole.a : 0.0f, whole.h}));
         }
         if (group > 0) {
-            wait_for(a, ends, 0, 1, end);
-            state = Words<1>{{end[0]}}.map().h;
+            // The latest word of a known state, and maps from there on.
+            wait_for(a, window, 32 * V, groups, behind, true, [&] {
+                bool known = false;
+#pragma unroll
+                for (int k = 0; k < kWindow; ++k)
+                    if (k < groups) known = is_state(behind[k]) || (known && behind[k] != kNoMap);
+                return known;
+            });
+#pragma unroll
+            for (int k = 0; k < kWindow; ++k)
+                if (k < groups) {
+                    const Map<1> g = map_of(behind[k]);
+                    state = is_state(behind[k]) ? g.h : fmaf(g.a, state, g.h);
+                }
+            // (A map that took no state before says the same again.)
+            if (closes) publish(ends, word_of({0.0f, whole.a == 0.0f ? whole.h : mad(whole.a, state, whole.h)}));
         }
         state = mad(m.a, state, m.h);
         at(s.carry[j & 3][lane], channel) = state;
@@ -443,10 +457,6 @@ __device__ __forceinline__ void follow_chain(const RecurrenceArgs &a, Shared<V, 
     // the next one's may be through already.)
     warp_arrive(s.state_ready[j & 1]);
     barrier_wait_warp(smem_address(&s.state_ready[j & 1]), j >> 1 & 1, guard);
-    if (place % a.group != a.group - 1 || place + 1 >= t.count) return;
-    const Map<V> tile = s.tile[j & 3][lane];
-    const Map<1> end = {0.0f, mad(at(tile.a, channel), state, at(tile.h, channel))};
-    publish(ends + 32 * V, Words<1>::of(end));
 }
 
 // ---- runs of tokens ------------------------------------------------------------------------
@@ -977,6 +987,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
         }
         for (int k = 0; k < 2; ++k) {
             barrier_init(smem_address(&s.runs_ready[k]), kWarps);
+            barrier_init(smem_address(&s.tile_ready[k]), 1);
             barrier_init(smem_address(&s.state_ready[k]), 1 + V);
         }
         fence_async();
@@ -1076,11 +1087,7 @@ int run(gsr_ctx *ctx, RecurrenceArgs &a, int dtype, cudaStream_t stream)
     Workspace workspace(ctx, stream);
     const bool chained = a.tiles > 1;
     const size_t chains = (size_t)a.batch * a.slabs;
-    // A group's state follows the last one's a good microsecond later.  Where many chains share the SMs, a few of a
-    // chain's tiles take longer than that; where there are few, more tiles of a chain are under way at a time.
-    a.group = kMinGroup;
-    while (a.group < kMaxGroup && a.group * chains < 256) a.group *= 2;
-    a.groups = (a.tiles + a.group - 1) / a.group;
+    a.groups = (a.tiles + kGroup - 1) / kGroup;
     const size_t pairs = chained ? chains * a.tiles * kSlab * sizeof(unsigned long long) : 0;
     const size_t ends = chained ? chains * a.groups * kSlab * sizeof(unsigned long long) : 0;
     const size_t bytes = chained ? pairs + ends + 16 : 0;
