@@ -20,7 +20,11 @@
 namespace gsr {
 namespace {
 
-constexpr int kRowThreads = 512;   // of a block, where a row needs no more
+constexpr int kRowThreads = 512;   // of a block, one to an SM, where a row needs no more
+// Elements of a thread: parameters, their gradients' sums and a row's inputs stay in
+// registers (8 in two blocks an SM: 80,000 x 128 in f16 in 10.2 and 24 us, 6.7 and 12.3 with
+// 16; 100,000 x 256 in bf16 in 23 us forward, 15).
+constexpr int kElements = 16;
 
 // The rows of one [batch, tokens, heads, channels] array.
 struct Rows {
@@ -40,12 +44,11 @@ struct LayerArgs {
     float eps;
 };
 
-// A row's first element.  Arrays whose rows lie at one stride arrive as one item of
-// one head.
+// A row's first element.  `flat`: the rows lie at one stride (one item of one head).
 template <typename T>
-__device__ __forceinline__ T *row_of(const LayerArgs &a, const Rows &r, uint32_t row)
+__device__ __forceinline__ T *row_of(const LayerArgs &a, const Rows &r, uint32_t row, bool flat)
 {
-    if (a.batch == 1 && a.heads == 1) return (T *)r.data + row * r.token;
+    if (flat) return (T *)r.data + row * r.token;
     const uint32_t token = row / (uint32_t)a.heads, item = token / (uint32_t)a.tokens;
     return (T *)r.data + item * r.batch + (token - item * (uint32_t)a.tokens) * r.token +
            (row - token * (uint32_t)a.heads) * r.head;
@@ -164,7 +167,9 @@ template <bool WIDE, typename F>
 __device__ __forceinline__ F team_sum(F v, const LayerArgs &a, float2 *s_sums, int team, int &turn)
 {
     if constexpr (!WIDE) {
-        for (int d = a.team / 2; d > 0; d /= 2) add_lane(v, d);
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2)
+            if (d < a.team) add_lane(v, d);
     } else {
         using Four = std::conditional_t<std::is_same_v<F, float>, float4, float2[4]>;
 #pragma unroll
@@ -200,12 +205,13 @@ __device__ __forceinline__ void clear_sums(float2 *s_all, int teams)
 
 // A block walks rows, `teams` at a time, and every thread's elements of the next ones
 // come through a ring of its own in shared memory (asynchronous copies; no thread
-// waits for another): S stages of A arrays, as many as 200 KB hold on an SM.  Single elements of
+// waits for another): S stages of A arrays, three (two are slower without a residual, 45.8
+// to 43.5 us for 32,640 x 2,048 in bf16, four and eight no faster) or what 200 KB hold.  Single elements of
 // 2 bytes have no such copies and are read directly (S = 0).
-template <typename T, int V, int N, int A, int THREADS, int BLOCKS>
+template <typename T, int V, int N, int A, int THREADS>
 constexpr int kStages = sizeof(T) * V < 4
                             ? 0
-                            : std::min(8, 200 * 1024 / (BLOCKS * THREADS * A * N * V * (int)sizeof(T)));
+                            : std::min(3, 200 * 1024 / (THREADS * A * N * V * (int)sizeof(T)));
 
 template <int BYTES>
 __device__ __forceinline__ void copy_async(void *to, const void *from)
@@ -217,45 +223,42 @@ __device__ __forceinline__ void copy_async(void *to, const void *from)
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(BYTES) : "memory");
 }
 
-template <typename T, int V, int N, int A, int S>
+template <typename T, int V, int N, int A, int S, int THREADS>
 struct Ring {
     using Access = Vec<T, V>;
+    static constexpr int kStage = A * N * THREADS;
     Access *mine;          // the thread's first slot
     const Rows &r0, &r1, &r2;
+    bool flat;
     int at = 0;            // of the current stage's first slot
 
     __device__ __forceinline__ const Rows &array(int k) const { return k == 0 ? r0 : k == 1 ? r1 : r2; }
-    __device__ __forceinline__ int step() const { return (int)blockDim.x; }
+    __device__ __forceinline__ Access *slot(int k, int i) const { return mine + at + (k * N + i) * THREADS; }
     // Starts the copies of a row into the current stage, if there is such a row.
     __device__ __forceinline__ void fetch(const LayerArgs &a, uint32_t row, int lane) const
     {
         if constexpr (S > 0) {
             if (row < a.rows) {
 #pragma unroll
-                for (int k = 0; k < A; ++k)
-                    if (array(k).data) {
-                        const T *from = row_of<T>(a, array(k), row);
+                for (int k = 0; k < A; ++k) {
+                    const T *from = row_of<T>(a, array(k), row, flat);
 #pragma unroll
-                        for (int i = 0; i < N; ++i) {
-                            const int c = (i * a.team + lane) * V;
-                            if (c < a.channels) copy_async<sizeof(Access)>(mine + at + (k * N + i) * step(), from + c);
-                        }
+                    for (int i = 0; i < N; ++i) {
+                        const int c = (i * a.team + lane) * V;
+                        if (c < a.channels) copy_async<sizeof(Access)>(slot(k, i), from + c);
                     }
+                }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
     }
-    __device__ __forceinline__ void advance()
-    {
-        at += A * N * step();
-        if (at >= S * A * N * step()) at = 0;
-    }
+    __device__ __forceinline__ void advance() { at = at + kStage >= S * kStage ? 0 : at + kStage; }
     // Slots behind the channels are 0 from here on.
     __device__ __forceinline__ void start(const LayerArgs &a, uint32_t row, uint32_t stride, int lane)
     {
         for (int k = 0; k < S; ++k) {
             for (int i = 0; i < A * N; ++i)
-                if (((i % N) * a.team + lane) * V >= a.channels) mine[at + i * step()] = Access{};
+                if (((i % N) * a.team + lane) * V >= a.channels) *slot(0, i) = Access{};
             fetch(a, row + k * stride, lane);
             advance();
         }
@@ -267,16 +270,14 @@ struct Ring {
             asm volatile("cp.async.wait_group %0;" ::"n"(S > 0 ? S - 1 : 0) : "memory");
 #pragma unroll
             for (int k = 0; k < A; ++k)
-                if (array(k).data)
 #pragma unroll
-                    for (int i = 0; i < N; ++i) to[k].v[i] = mine[at + (k * N + i) * step()];
+                for (int i = 0; i < N; ++i) to[k].v[i] = *slot(k, i);
         } else {
 #pragma unroll
-            for (int k = 0; k < A; ++k)
-                if (array(k).data) {
-                    to[k].clear();
-                    if (row < a.rows) to[k].load(row_of<T>(a, array(k), row), a, lane);
-                }
+            for (int k = 0; k < A; ++k) {
+                to[k].clear();
+                if (row < a.rows) to[k].load(row_of<T>(a, array(k), row, flat), a, lane);
+            }
         }
     }
     // Waits for the copies of rows behind the last.
@@ -288,18 +289,19 @@ struct Ring {
 
 // ---- forward ------------------------------------------------------------------------
 
-template <typename T, int V, int N, bool WIDE, int THREADS, int BLOCKS>
-__global__ void __launch_bounds__(THREADS, BLOCKS) k_layer_norm(const LayerArgs a)
+template <typename T, int V, int N, bool WIDE, int THREADS, bool SUM>
+__global__ void __launch_bounds__(THREADS, 1) k_layer_norm(const LayerArgs a)
 {
     grid_dependency_begin();
     extern __shared__ __align__(16) unsigned char s_bytes[];   // the teams' sums, then the ring
     using Elements = Part<T, V, N>;
-    constexpr int kPairs = Elements::kPairs, S = kStages<T, V, N, 2, THREADS, BLOCKS>;
+    constexpr int kPairs = Elements::kPairs, A = SUM ? 2 : 1, S = kStages<T, V, N, A, THREADS>;
+    const bool flat = a.batch == 1 && a.heads == 1;
     const int teams = blockDim.x / a.team, team = threadIdx.x / a.team, lane = threadIdx.x % a.team;
     const uint32_t stride = gridDim.x * (uint32_t)teams;
     float2 *s_sums = (float2 *)s_bytes + team * 2 * kTeamWarps;
-    Ring<T, V, N, 2, S> ring = {(Vec<T, V> *)(s_bytes + (WIDE ? teams * 2 * kTeamWarps * sizeof(float2) : 0)) + threadIdx.x, a.x,
-                                a.residual, a.residual};
+    Ring<T, V, N, A, S, THREADS> ring = {(Vec<T, V> *)(s_bytes + (WIDE ? teams * 2 * kTeamWarps * sizeof(float2) : 0)) + threadIdx.x,
+                                         a.x, a.residual, a.residual, flat};
 
     // (Below 2^31 rows, steps ahead of them below 2^32.  All teams take the same number of steps.)
     uint32_t row = blockIdx.x * teams + team, first = blockIdx.x * teams;
@@ -316,13 +318,13 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) k_layer_norm(const LayerArgs 
     int turn = 0;
     for (; first < a.rows; first += stride, row += stride) {
         const bool valid = row < a.rows;
-        Elements in[2];
+        Elements in[A];
         ring.take(a, row, lane, in);
         Elements &x = in[0];
-        if (a.residual.data) {
+        if constexpr (SUM) {
 #pragma unroll
-            for (int p = 0; p < kPairs; ++p) x.set(p, add2(x.get(p), in[1].get(p)));
-            if (valid) x.store(row_of<T>(a, a.total, row), a, lane);
+            for (int p = 0; p < kPairs; ++p) x.set(p, add2(x.get(p), in[A - 1].get(p)));
+            if (valid) x.store(row_of<T>(a, a.total, row, flat), a, lane);
         }
         float2 f[kPairs], sum = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -353,7 +355,7 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) k_layer_norm(const LayerArgs 
 #pragma unroll
         for (int p = 0; p < kPairs; ++p) x.set(p, fma2(mul2(f[p], scale), weight[p], bias[p]));
         if (valid) {
-            x.store(row_of<T>(a, a.out, row), a, lane);
+            x.store(row_of<T>(a, a.out, row, flat), a, lane);
             if (lane == 0) {
                 a.mean[row] = mean;
                 a.rstd[row] = rstd;
@@ -365,20 +367,21 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) k_layer_norm(const LayerArgs 
 
 // ---- backward -----------------------------------------------------------------------
 
-template <typename T, int V, int N, bool WIDE, int THREADS, int BLOCKS>
-__global__ void __launch_bounds__(THREADS, BLOCKS) k_layer_norm_grad(const LayerArgs a)
+template <typename T, int V, int N, bool WIDE, int THREADS, bool SUM>
+__global__ void __launch_bounds__(THREADS, 1) k_layer_norm_grad(const LayerArgs a)
 {
     grid_dependency_begin();
     // The teams' sums, then the ring; at the end the block's shares of dw and db.
     extern __shared__ __align__(16) unsigned char s_bytes[];
     float2 *s_work = (float2 *)s_bytes;
     using Elements = Part<T, V, N>;
-    constexpr int kPairs = Elements::kPairs, S = kStages<T, V, N, 3, THREADS, BLOCKS>;
+    constexpr int kPairs = Elements::kPairs, A = SUM ? 3 : 2, S = kStages<T, V, N, A, THREADS>;
+    const bool flat = a.batch == 1 && a.heads == 1;
     const int teams = blockDim.x / a.team, team = threadIdx.x / a.team, lane = threadIdx.x % a.team;
     const uint32_t stride = gridDim.x * (uint32_t)teams;
     float2 *s_sums = s_work + team * 2 * kTeamWarps;
-    Ring<T, V, N, 3, S> ring = {(Vec<T, V> *)(s_bytes + (WIDE ? teams * 2 * kTeamWarps * sizeof(float2) : 0)) + threadIdx.x,
-                                a.total, a.x, a.residual};
+    Ring<T, V, N, A, S, THREADS> ring = {(Vec<T, V> *)(s_bytes + (WIDE ? teams * 2 * kTeamWarps * sizeof(float2) : 0)) + threadIdx.x,
+                                         a.total, a.x, a.residual, flat};
 
     // (As in the forward.)
     uint32_t row = blockIdx.x * teams + team, first = blockIdx.x * teams;
@@ -394,9 +397,9 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) k_layer_norm_grad(const Layer
     int turn = 0;
     float mean = row < a.rows ? a.mean[row] : 0.0f, rstd = row < a.rows ? a.rstd[row] : 0.0f;
     for (; first < a.rows; first += stride, row += stride) {
-        Elements in[3];
+        Elements in[A];
         ring.take(a, row, lane, in);
-        Elements &total = in[0], &dout = in[1], &dtotal = in[2];
+        Elements &total = in[0], &dout = in[1];
         const float2 minus = make_float2(-mean, -mean), scale = make_float2(rstd, rstd);
         const uint32_t after = row + stride;
         if (after < a.rows) {
@@ -426,14 +429,16 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) k_layer_norm_grad(const Layer
         for (int p = 0; p < kPairs; ++p) {
             const float2 hat = mul2(add2(total.get(p), minus), scale);
             const float2 d = fma2(hat, m2, fma2(dout.get(p), weight[p], m1));
-            total.set(p, a.residual.data ? fma2(d, scale, dtotal.get(p)) : mul2(d, scale));
+            total.set(p, SUM ? fma2(d, scale, in[A - 1].get(p)) : mul2(d, scale));
         }
-        total.store(row_of<T>(a, a.out, row), a, lane);
+        total.store(row_of<T>(a, a.out, row, flat), a, lane);
     }
     ring.finish();
     if (!a.partial) return;
 
-    // The block's sums: lanes of a warp that hold the same channels, then teams in order.
+    // The block's sums: lanes of a warp that hold the same channels, then teams in order,
+    // all of them in shared memory side by side (64 KB, where a team after the other took
+    // 8 us of 65,000 x 512's 58).
     if (!WIDE)
         for (int d = a.team; d < 32; d *= 2)
 #pragma unroll
@@ -443,26 +448,22 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) k_layer_norm_grad(const Layer
                 db[p].x += __shfl_xor_sync(~0u, db[p].x, d);
                 db[p].y += __shfl_xor_sync(~0u, db[p].y, d);
             }
-    const int width = WIDE ? a.team : 32;
-    const int group = threadIdx.x / width, groups = blockDim.x / width;
-    const bool mine = threadIdx.x % width < a.team;
+    const int width = WIDE ? a.team : 32, each = 2 * kPairs * width;
+    const int group = threadIdx.x / width, groups = blockDim.x / width, own = threadIdx.x % width;
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < kPairs; ++p) {
+        s_work[group * each + 2 * p * width + own] = make_float2(dw[p].x, db[p].x);
+        s_work[group * each + (2 * p + 1) * width + own] = make_float2(dw[p].y, db[p].y);
+    }
+    __syncthreads();
     float2 *out = a.partial + (int64_t)blockIdx.x * a.channels;
-    for (int k = 0; k < groups; ++k) {
-        __syncthreads();
-        if (k == group && mine)
-#pragma unroll
-            for (int p = 0; p < kPairs; ++p)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int c = pair_channel<V>(a, lane, p, half);
-                    if (c >= a.channels) continue;
-                    float2 v = half ? make_float2(dw[p].y, db[p].y) : make_float2(dw[p].x, db[p].x);
-                    if (k > 0) v = add2(s_work[c], v);
-                    if (k < groups - 1)
-                        s_work[c] = v;
-                    else
-                        out[c] = v;
-                }
+    for (int i = threadIdx.x; i < each; i += blockDim.x) {
+        const int element = i / width, l = i - element * width, c = pair_channel<V>(a, l, element / 2, element % 2);
+        if (l >= a.team || c >= a.channels) continue;
+        float2 sum = s_work[i];
+        for (int k = 1; k < groups; ++k) sum = add2(sum, s_work[k * each + i]);
+        out[c] = sum;
     }
 }
 
@@ -556,64 +557,55 @@ int power_of_two(int n)
     return p;
 }
 
-// How a row is divided: elements of a thread, threads, and blocks of how many rows.
-struct Plan {
-    int teams, occupancy;
-};
-
-// One access a thread where that makes a warp or less, 16 elements otherwise.
-template <int V>
-constexpr bool one_access(int channels)
+// Divides a row over a team, kElements of it to a thread, and the rows over blocks of
+// teams; returns a block's teams.  Few rows are spread over the SMs rather than over the
+// teams of one block.
+int plan_rows(const gsr_ctx *ctx, LayerArgs &a)
 {
-    return V > 1 && channels <= 32 * V;
-}
-
-// Few rows are spread over the SMs rather than over the teams of one block.
-template <int V>
-Plan plan_rows(const gsr_ctx *ctx, LayerArgs &a)
-{
-    Plan p;
-    const bool one = one_access<V>(a.channels);
-    const int each = one ? V : 16, threads = (a.channels + each - 1) / each;
+    const int threads = (a.channels + kElements - 1) / kElements;
     a.team = threads <= 32 ? power_of_two(threads) : (threads + 31) / 32 * 32;
-    p.occupancy = one ? 2 : 1;
     const uint64_t spread = ((uint64_t)a.rows + ctx->num_sms - 1) / ctx->num_sms;
-    p.teams = a.team > kRowThreads ? 1 : kRowThreads / a.team;
-    while (a.team * p.teams > 128 && (uint64_t)p.teams > spread) p.teams = (p.teams + 1) / 2;
-    if (p.teams * a.team % 32 != 0) p.teams = 32 / a.team;   // whole warps
-    const uint64_t blocks = ((uint64_t)a.rows + p.teams - 1) / p.teams, most = (uint64_t)p.occupancy * ctx->num_sms;
-    a.blocks = (int)(blocks < most ? blocks : most);
-    return p;
+    int teams = a.team > kRowThreads ? 1 : kRowThreads / a.team;
+    while (a.team * teams > 128 && (uint64_t)teams > spread) teams = (teams + 1) / 2;
+    if (teams * a.team % 32 != 0) teams = 32 / a.team;   // whole warps
+    const uint64_t blocks = ((uint64_t)a.rows + teams - 1) / teams;
+    a.blocks = (int)(blocks < (uint64_t)ctx->num_sms ? blocks : ctx->num_sms);
+    return teams;
 }
 
-template <typename T, int V, int N, bool WIDE, int THREADS, int BLOCKS, bool BACKWARD>
+template <typename T, int V, int N, bool WIDE, int THREADS, bool BACKWARD, bool SUM>
 cudaError_t launch_rows(gsr_ctx *ctx, LayerArgs &a, int teams, cudaStream_t stream)
 {
-    constexpr int kArrays = BACKWARD ? 3 : 2;
+    constexpr int kArrays = (BACKWARD ? 2 : 1) + SUM;
     const int threads = teams * a.team;
-    const size_t ring = (size_t)kStages<T, V, N, kArrays, THREADS, BLOCKS> * kArrays * N * threads * sizeof(T) * V;
+    const size_t ring = (size_t)kStages<T, V, N, kArrays, THREADS> * kArrays * N * THREADS * sizeof(T) * V;
     const size_t sums = WIDE ? (size_t)teams * 2 * kTeamWarps * sizeof(float2) : 0;
-    const size_t shares = BACKWARD && threads > (WIDE ? a.team : 32) ? (size_t)a.channels * sizeof(float2) : 0;
-    const size_t smem = sums + ring > shares ? sums + ring : shares;
+    const size_t shares = BACKWARD ? (size_t)threads * N * V * sizeof(float2) : 0;
+    const size_t smem = std::max(sums + ring, shares);
     void (*kernel)(LayerArgs);
     if constexpr (BACKWARD)
-        kernel = k_layer_norm_grad<T, V, N, WIDE, THREADS, BLOCKS>;
+        kernel = k_layer_norm_grad<T, V, N, WIDE, THREADS, SUM>;
     else
-        kernel = k_layer_norm<T, V, N, WIDE, THREADS, BLOCKS>;
+        kernel = k_layer_norm<T, V, N, WIDE, THREADS, SUM>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return launch_kernel_smem(ctx, kernel, dim3((unsigned)a.blocks), threads, smem, 1, stream, a);
 }
 
-template <typename T, int V, bool BACKWARD>
-cudaError_t dispatch_rows(gsr_ctx *ctx, LayerArgs &a, const Plan &p, cudaStream_t stream)
+template <typename T, int V, bool BACKWARD, bool SUM>
+cudaError_t dispatch_rows(gsr_ctx *ctx, LayerArgs &a, int teams, cudaStream_t stream)
 {
-    constexpr int N = 16 / V;
-    if constexpr (V > 1)
-        if (one_access<V>(a.channels)) return launch_rows<T, V, 1, false, kRowThreads, 2, BACKWARD>(ctx, a, p.teams, stream);
-    if (a.team <= 32) return launch_rows<T, V, N, false, kRowThreads, 1, BACKWARD>(ctx, a, p.teams, stream);
-    if (a.team <= kRowThreads) return launch_rows<T, V, N, true, kRowThreads, 1, BACKWARD>(ctx, a, p.teams, stream);
-    return launch_rows<T, V, N, true, 1024, 1, BACKWARD>(ctx, a, p.teams, stream);
+    constexpr int N = kElements / V;
+    if (a.team <= 32) return launch_rows<T, V, N, false, kRowThreads, BACKWARD, SUM>(ctx, a, teams, stream);
+    if (a.team <= kRowThreads) return launch_rows<T, V, N, true, kRowThreads, BACKWARD, SUM>(ctx, a, teams, stream);
+    return launch_rows<T, V, N, true, 1024, BACKWARD, SUM>(ctx, a, teams, stream);
+}
+
+template <typename T, int V, bool BACKWARD>
+cudaError_t dispatch_sum(gsr_ctx *ctx, LayerArgs &a, int teams, cudaStream_t stream)
+{
+    return a.residual.data ? dispatch_rows<T, V, BACKWARD, true>(ctx, a, teams, stream)
+                           : dispatch_rows<T, V, BACKWARD, false>(ctx, a, teams, stream);
 }
 
 // f<T, V>() for the description's type and the arrays' widest access.
@@ -653,8 +645,7 @@ int layer_norm_forward(gsr_ctx *ctx, const gsr_layer_norm &d, const gsr_heads &x
     collapse(a);
     const cudaError_t e = with_access(d.dtype, a, [&](auto t, auto v) {
         constexpr int V = decltype(v)::value;
-        const Plan p = plan_rows<V>(ctx, a);
-        return dispatch_rows<decltype(t), V, false>(ctx, a, p, stream);
+        return dispatch_sum<decltype(t), V, false>(ctx, a, plan_rows(ctx, a), stream);
     });
     return cuda_check(ctx, e, "layer norm forward");
 }
@@ -687,14 +678,14 @@ int layer_norm_backward(gsr_ctx *ctx, const gsr_layer_norm &d, const gsr_heads &
     const cudaError_t e = with_access(d.dtype, a, [&](auto t, auto v) {
         using T = decltype(t);
         constexpr int V = decltype(v)::value;
-        const Plan p = plan_rows<V>(ctx, a);
+        const int teams = plan_rows(ctx, a);
         if (dweight || dbias) {
             void *work = nullptr;
             rc = workspace.take((size_t)a.blocks * d.channels * sizeof(float2), &work);
             if (rc != GSR_OK) return cudaSuccess;
             a.partial = (float2 *)work;
         }
-        cudaError_t e = dispatch_rows<T, V, true>(ctx, a, p, stream);
+        cudaError_t e = dispatch_sum<T, V, true>(ctx, a, teams, stream);
         if (e == cudaSuccess && a.partial)
             e = launch_kernel(ctx, k_layer_norm_params, dim3((unsigned)((a.channels + 31) / 32)), 32 * kParamSlices,
                               stream, a);
