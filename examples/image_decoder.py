@@ -1,12 +1,14 @@
 """Fits a small image-to-Gaussians decoder through the rasterizer.
 
-Feature maps of a few views go through a group norm with SiLU; their patches
+Feature maps of a few views go through a group norm with SiLU and, with --layers,
+through layers that mix the patches of all views (a layer norm behind the residual
+sum, gated recurrences over the tokens in both directions); their patches
 become keys and values with rotary positions (view, row, column); Gaussian tokens
 attend to all of them, a linear head turns each token into a 3-D Gaussian, and
 the Gaussians are projected, binned and composited.  The image's gradient goes
 back the same way into every parameter.
 
-    python examples/image_decoder.py --steps 60
+    python examples/image_decoder.py --steps 60 --layers 1
 """
 import argparse
 import os
@@ -63,6 +65,65 @@ class CrossAttention(torch.autograd.Function):
         return (None, *grads, None)
 
 
+class SumNorm(torch.autograd.Function):
+    """(layer norm of x + residual, x + residual)."""
+
+    @staticmethod
+    def forward(fn, ctx, x, residual, weight, bias):
+        out, total, mean, rstd = gsr.layer_norm_forward(ctx, x, weight, bias, residual=residual)
+        fn.save_for_backward(total, weight, mean, rstd)
+        fn.ctx = ctx
+        return out, total
+
+    @staticmethod
+    def backward(fn, dout, dtotal):
+        total, weight, mean, rstd = fn.saved_tensors
+        dx, dw, db = gsr.layer_norm_backward(fn.ctx, dout.contiguous(), total, weight, mean, rstd,
+                                             dl_dtotal=dtotal.contiguous())
+        return None, dx, dx, dw, db
+
+
+class Recurrence(torch.autograd.Function):
+    """The gated recurrence of a projection's three parts [batch, tokens, 3 channels]."""
+
+    @staticmethod
+    def forward(fn, ctx, parts, reverse):
+        x, forget, gate = parts.chunk(3, dim=2)
+        out, _, states = gsr.gated_recurrence_forward(ctx, x, forget, gate, reverse=reverse)
+        fn.save_for_backward(parts, states)
+        fn.ctx, fn.reverse = ctx, reverse
+        return out
+
+    @staticmethod
+    def backward(fn, dout):
+        parts, states = fn.saved_tensors
+        x, forget, gate = parts.chunk(3, dim=2)
+        dparts = torch.empty(parts.shape, dtype=parts.dtype, device=parts.device)
+        dx, dforget, dgate = dparts.chunk(3, dim=2)
+        gsr.gated_recurrence_backward(fn.ctx, dout.contiguous(), x, forget, gate, states, reverse=fn.reverse, dl_dx=dx,
+                                      dl_dforget=dforget, dl_dgate=dgate)
+        return None, dparts, None
+
+
+class TokenLayer(torch.nn.Module):
+    """Mixes tokens along their sequence, forwards and backwards."""
+
+    def __init__(self, ctx, channels, generator):
+        super().__init__()
+        self.ctx = ctx
+        self.norm_weight = torch.nn.Parameter(torch.ones(channels, device="cuda"))
+        self.norm_bias = torch.nn.Parameter(torch.zeros(channels, device="cuda"))
+        draw = lambda rows, cols: torch.nn.Parameter((torch.randn((rows, cols), generator=generator) * rows ** -0.5).cuda())  # noqa: E731
+        self.to_parts, self.back = draw(channels, 6 * channels), draw(2 * channels, channels)
+
+    def forward(self, x, residual):
+        """Returns the layer's output and the sum that it is to be added to."""
+        y, total = SumNorm.apply(self.ctx, x, residual, self.norm_weight, self.norm_bias)
+        ahead, back = (y @ self.to_parts.to(y.dtype)).chunk(2, dim=2)
+        mixed = torch.cat([Recurrence.apply(self.ctx, ahead, False), Recurrence.apply(self.ctx, back, True)], dim=2)
+        return mixed @ self.back.to(y.dtype), total
+
+
 class Render(torch.autograd.Function):
     """Gaussians [n, 14] to an image [side * side, 3]."""
 
@@ -85,7 +146,7 @@ class Render(torch.autograd.Function):
 
 
 class Decoder(torch.nn.Module):
-    def __init__(self, ctx, views, grid, channels=64, tokens=1024, q_heads=4, kv_heads=2, dim=64, seed=0):
+    def __init__(self, ctx, views, grid, channels=64, tokens=1024, q_heads=4, kv_heads=2, dim=64, seed=0, layers=0):
         super().__init__()
         self.ctx, self.shape = ctx, (tokens, q_heads, kv_heads, dim)
         gen_ = torch.Generator().manual_seed(seed)
@@ -99,6 +160,8 @@ class Decoder(torch.nn.Module):
         self.to_v = parameter(channels, kv_heads * dim, scale=channels ** -0.5)
         self.queries = parameter(1, tokens, q_heads * dim, scale=1.0)
         self.head = parameter(q_heads * dim, 14, scale=0.02)
+        self.layers = torch.nn.ModuleList(TokenLayer(ctx, channels, torch.Generator().manual_seed(seed + 1 + i))
+                                          for i in range(layers))
         # The Gaussians the head's output is added to: a cloud in the middle of the scene.
         base = torch.zeros(tokens, 14)
         base[:, :3] = torch.rand((tokens, 3), generator=gen_) * 2 - 1
@@ -119,6 +182,10 @@ class Decoder(torch.nn.Module):
         tokens, q_heads, kv_heads, dim = self.shape
         x = NormAct.apply(self.ctx, features, 8, self.norm_weight, self.norm_bias)
         x = x.reshape(1, -1, features.shape[-1])
+        residual = torch.zeros_like(x)
+        for layer in self.layers:
+            x, residual = layer(x, residual)
+        x = x + residual
         k = (x @ self.to_k.to(x.dtype)).view(1, -1, kv_heads, dim)
         v = (x @ self.to_v.to(x.dtype)).view(1, -1, kv_heads, dim)
         q = self.queries.to(x.dtype).view(1, tokens, q_heads, dim)
@@ -128,7 +195,7 @@ class Decoder(torch.nn.Module):
         return self.base + out.reshape(tokens, -1).float() @ self.head
 
 
-def train(steps=60, views=3, grid=16, side=128, seed=0, log=print):
+def train(steps=60, views=3, grid=16, side=128, seed=0, log=print, layers=0):
     """Returns the losses of `steps` Adam steps towards one view of a synthetic scene."""
     ctx = gsr.Context(0)
     scene = gen.lego_scene(n=4000, seed=seed)
@@ -140,7 +207,7 @@ def train(steps=60, views=3, grid=16, side=128, seed=0, log=print):
     features = torch.randn((views, grid, grid, 64), generator=generator).to(torch.bfloat16).cuda()
     key_mask = torch.ones((1, views * grid * grid), dtype=torch.bool, device="cuda")
     key_mask[:, ::grid] = False                     # the first column of every view lies off the object
-    model = Decoder(ctx, views, grid, seed=seed)
+    model = Decoder(ctx, views, grid, seed=seed, layers=layers)
     optimizer = torch.optim.Adam(model.parameters(), lr=1e-2)
     losses = []
     for step in range(steps):
@@ -160,4 +227,6 @@ def train(steps=60, views=3, grid=16, side=128, seed=0, log=print):
 if __name__ == "__main__":
     parser = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     parser.add_argument("--steps", type=int, default=60)
-    train(parser.parse_args().steps)
+    parser.add_argument("--layers", type=int, default=0)
+    args = parser.parse_args()
+    train(args.steps, layers=args.layers)

@@ -54,6 +54,8 @@ constexpr int kRun = 16, kGradRun = 8;     // tokens of a warp
 constexpr int kTile = kWarps * kRun, kGradTile = kWarps * kGradRun;
 constexpr int kStages = 2;
 constexpr int kRowBytes = 128;             // of a token in a stage
+// Up to so many tokens a thread runs them alone.
+constexpr int kFewTokens = 16, kFewAhead = 4, kFewThreads = 64;
 constexpr int kStateStep = GSR_RECURRENCE_BLOCK;
 static_assert(kStateStep % kRun == 0 && kGradTile == kStateStep, "states lie where runs and tiles start");
 
@@ -357,6 +359,7 @@ __device__ __forceinline__ void compose_runs(const RecurrenceArgs &a, Shared<V, 
 #pragma unroll
         for (int k = 0; k < V; ++k) at(h, k) = a.states[((int64_t)t.b * a.blocks + t.index) * a.channels + c + k];
     barrier_wait_warp(smem_address(&s.runs_ready[j & 1]), j >> 1 & 1, guard);
+    GSR_CANARY(26 + j % 4);
     if (BACKWARD)
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
@@ -403,6 +406,7 @@ __device__ __forceinline__ void follow_chain(const RecurrenceArgs &a, Shared<V, 
 {
     const int lane = threadIdx.x % 32, channel = threadIdx.x / 32 - kChainWarp, place = place_of<BACKWARD>(t);
     if (t.index >= t.count || channel >= V) return;
+    GSR_CANARY(21);
     const int64_t row = (int64_t)t.b * a.slabs + t.slab;
     const int group = place / kGroup, count = place - group * kGroup, groups = min(group, kWindow);
     const unsigned long long *pairs = a.pairs + (row * a.tiles + group * kGroup) * (32 * V) + channel * 32 + lane;
@@ -451,6 +455,7 @@ __device__ __forceinline__ void follow_chain(const RecurrenceArgs &a, Shared<V, 
             if (closes) publish(ends, word_of({0.0f, whole.a == 0.0f ? whole.h : mad(whole.a, state, whole.h)}));
         }
         state = mad(m.a, state, m.h);
+        GSR_CANARY(22 + j % 4);
         at(s.carry[j & 3][lane], channel) = state;
     }
     // (A barrier for even tiles and one for odd: the working warps look at a tile's when
@@ -940,6 +945,7 @@ __device__ __forceinline__ void work_tiles(const RecurrenceArgs &a, Shared<V, S,
     uint32_t j = 0;
     auto finish = [&] {
         const uint32_t k = j - 1;
+        GSR_CANARY(34 + k % 4);
         barrier_wait_warp(smem_address(&s.state_ready[k & 1]), k >> 1 & 1, guard);
         Work::finish(a, s, before, k, columns + (k & 1) * kSlotColumns);
         __syncwarp();
@@ -953,6 +959,7 @@ __device__ __forceinline__ void work_tiles(const RecurrenceArgs &a, Shared<V, S,
         const bool some = t.index < t.count;
         if (some) {
             if (COPY) barrier_wait_warp(smem_address(&s.full[stage]), i / S & 1, guard);
+            GSR_CANARY(30 + j % 4);
             Work::compose(a, s, t, j, stages + stage * stage_bytes, columns + (j & 1) * kSlotColumns);
             warp_arrive(s.runs_ready[j & 1]);
         }
@@ -1016,6 +1023,55 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     tmem_fence_before();
     __syncthreads();
     if (warp == kComposeWarp) tmem_free(s.columns, kColumns);
+}
+
+// ---- few tokens --------------------------------------------------------------------------
+
+// A few tokens of each item, as they come one after the other while a model answers: a
+// thread takes a lane's channels of an item, with no chain and nothing shared.
+template <typename T, int V, bool GATE>
+__global__ void __launch_bounds__(kFewThreads) k_recurrence_few(const RecurrenceArgs a)
+{
+    grid_dependency_begin();
+    using F = Lanes<V>;
+    using R = Raw<T, V>;
+    const uint32_t lanes = (uint32_t)(a.channels + V - 1) / V, n = blockIdx.x * kFewThreads + threadIdx.x;   // up to 2^32
+    if (n >= (uint64_t)lanes * a.batch) return;
+    Tile t = {};
+    t.b = n / lanes;
+    t.length = a.lengths ? min(max(a.lengths[t.b], 0), a.tokens) : a.tokens;
+    const int c = (n - t.b * lanes) * V;
+    const int64_t at_state = (int64_t)t.b * a.channels + c;
+    const Run<T, V> x(a, a.x, t, 0, c), f(a, a.forget, t, 0, c), o(a, a.gate, t, 0, c), out(a, a.out, t, 0, c);
+    F h;
+#pragma unroll
+    for (int j = 0; j < V; ++j) at(h, j) = a.initial ? a.initial[at_state + j] : 0.0f;
+    if (a.states && t.length > 0) store_state<V>(a.states + (int64_t)t.b * a.blocks * a.channels + c, h);
+    for (int first = 0; first < t.length; first += kFewAhead) {
+        R xs[kFewAhead], fs[kFewAhead], os[GATE ? kFewAhead : 1];
+#pragma unroll
+        for (int i = 0; i < kFewAhead; ++i)
+            if (first + i < t.length) {
+                xs[i] = *x.token(first + i);
+                fs[i] = *f.token(first + i);
+                if constexpr (GATE) os[i] = *o.token(first + i);
+            }
+#pragma unroll
+        for (int i = 0; i < kFewAhead; ++i) {
+            if (first + i >= t.length) continue;
+            F keep, rest;
+            split<T>(value_of<T, V>(fs[i]), keep, rest);
+            h = mad(keep, h, mul(rest, value_of<T, V>(xs[i])));
+            if constexpr (GATE) {
+                const F g = value_of<T, V>(os[i]);
+                out.store(first + i, mul(h, mul(g, sigmoid<T>(g))));
+            } else {
+                out.store(first + i, h);
+            }
+        }
+    }
+    clear_tokens<T, V>(a.out, t.b, t.length, a.tokens, c);
+    store_state<V>(a.final + at_state, h);
 }
 
 // ---- host --------------------------------------------------------------------------------
@@ -1084,6 +1140,13 @@ int run(gsr_ctx *ctx, RecurrenceArgs &a, int dtype, cudaStream_t stream)
     if (a.tiles == 0) a.tiles = 1;   // for the states of items without tokens
     a.slabs = (a.channels + kSlab - 1) / kSlab;
     a.work = (uint32_t)a.tiles * a.batch * a.slabs;
+    if (!BACKWARD && a.tokens <= kFewTokens) {
+        const int64_t lanes = (int64_t)a.batch * ((a.channels + V - 1) / V);
+        const dim3 grid((unsigned)((lanes + kFewThreads - 1) / kFewThreads));
+        return cuda_check(ctx, a.gate.data ? launch_kernel(ctx, k_recurrence_few<T, V, true>, grid, kFewThreads, stream, a)
+                                           : launch_kernel(ctx, k_recurrence_few<T, V, false>, grid, kFewThreads, stream, a),
+                          what);
+    }
     Workspace workspace(ctx, stream);
     const bool chained = a.tiles > 1;
     const size_t chains = (size_t)a.batch * a.slabs;
