@@ -153,8 +153,10 @@ __device__ __forceinline__ Map<1> map_of(unsigned long long w)
     return {__uint_as_float((uint32_t)w), __uint_as_float((uint32_t)(w >> 32))};
 }
 constexpr unsigned long long kNoMap = ~0ull;
-// (A word whose map takes no state, A = 0: one of a known state.)
-__device__ __forceinline__ bool is_state(unsigned long long w) { return (uint32_t)w == 0; }
+// The A of a known state, which takes none before it: -0, which no product of gates is.  (A
+// product that comes out as 0 still takes its state: one that is not a number stays so.)
+constexpr float kNoState = -0.0f;
+__device__ __forceinline__ bool is_state(unsigned long long w) { return (uint32_t)w == 0x80000000u; }
 
 // ---- the chain ---------------------------------------------------------------------------
 
@@ -381,7 +383,7 @@ __device__ __forceinline__ void compose_runs(const RecurrenceArgs &a, Shared<V, 
         Map<V> out = m;
         if (place == 0) {   // as a map of no state
             out.h = mad(out.a, seed, out.h);
-            fill(out.a, 0.0f);
+            fill(out.a, kNoState);
         }
         unsigned long long *to = a.pairs + (((int64_t)t.b * a.slabs + t.slab) * a.tiles + place) * (32 * V) + lane;
 #pragma unroll
@@ -389,7 +391,7 @@ __device__ __forceinline__ void compose_runs(const RecurrenceArgs &a, Shared<V, 
     }
     if (place == 0) {
         m.h = mad(m.a, seed, m.h);   // (as published)
-        fill(m.a, 0.0f);
+        fill(m.a, kNoState);
         s.carry[j & 3][lane] = seed;
     }
     s.tile[j & 3][lane] = m;
@@ -434,7 +436,7 @@ __device__ __forceinline__ void follow_chain(const RecurrenceArgs &a, Shared<V, 
             const Map<V> tile = s.tile[j & 3][lane];
             whole = then(m, Map<1>{at(tile.a, channel), at(tile.h, channel)});
             // (The first group's takes no state, whatever its A has become.)
-            publish(ends, word_of({group > 0 ? whole.a : 0.0f, whole.h}));
+            publish(ends, word_of({group > 0 ? whole.a : kNoState, whole.h}));
         }
         if (group > 0) {
             // The latest word of a known state, and maps from there on.
@@ -451,8 +453,7 @@ __device__ __forceinline__ void follow_chain(const RecurrenceArgs &a, Shared<V, 
                     const Map<1> g = map_of(behind[k]);
                     state = is_state(behind[k]) ? g.h : fmaf(g.a, state, g.h);
                 }
-            // (A map that took no state before says the same again.)
-            if (closes) publish(ends, word_of({0.0f, whole.a == 0.0f ? whole.h : mad(whole.a, state, whole.h)}));
+            if (closes) publish(ends, word_of({kNoState, mad(whole.a, state, whole.h)}));
         }
         state = mad(m.a, state, m.h);
         GSR_CANARY(22 + j % 4);
