@@ -48,7 +48,13 @@ constexpr int kBlocks = 2;                 // of an SM
 // theirs to the others.
 constexpr int kStart = 80, kFew = 48, kMany = 96;
 static_assert(kWarps == 8 && 4 * kFew + 8 * kMany <= 12 * kStart, "the shares must fit what a block starts with");
-constexpr int kGroup = 8, kWindow = 2;     // tiles of a group; groups that a tile looks back on
+constexpr int kGroup = 8;                  // tiles of a group
+// Groups that a tile looks back on.  Where many chains share the SMs a few of a chain's
+// tiles are under way, and words that are looked at cost time (32,640 x 2,048 in bf16,
+// backward: 168 us with 2, 174 to 223 with 3 to 8); where there are few chains most of
+// their tiles are, and a state travels by as many groups at a time (32,640 x 64: 20.6 us
+// with 2, 14.9 with 8).
+constexpr int kNear = 2, kFar = 8, kManyChains = 4;
 constexpr int kColumns = 256, kSlotColumns = kColumns / 2;   // of tensor memory: two tiles' runs
 constexpr int kRun = 16, kGradRun = 8;     // tokens of a warp
 constexpr int kTile = kWarps * kRun, kGradTile = kWarps * kGradRun;
@@ -71,7 +77,7 @@ struct RecurrenceArgs {
     const int *lengths;
     int batch, tokens, channels, blocks;
     int tiles, slabs;            // of all tokens, of all channels
-    int groups;                  // of all tokens
+    int groups, far;             // of all tokens; whether a tile looks back on kFar of them
     uint32_t work;               // their number over all items
     int reverse;
     unsigned long long *pairs, *ends;   // published: [batch, slabs, tiles] and [batch, slabs, groups] rows of words
@@ -399,6 +405,29 @@ __device__ __forceinline__ void compose_runs(const RecurrenceArgs &a, Shared<V, 
     warp_arrive(s.state_ready[j & 1]);
 }
 
+// The state in front of a group: the latest of the last `count` groups' words that is a
+// known state, and the maps from there on.
+template <int N>
+__device__ __forceinline__ float state_behind(const RecurrenceArgs &a, const unsigned long long *words, int stride, int count,
+                                              unsigned long long (&seen)[N])
+{
+    wait_for(a, words, stride, count, seen, true, [&] {
+        bool known = false;
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (k < count) known = is_state(seen[k]) || (known && seen[k] != kNoMap);
+        return known;
+    });
+    float state = 0.0f;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        if (k < count) {
+            const Map<1> m = map_of(seen[k]);
+            state = is_state(seen[k]) ? m.h : fmaf(m.a, state, m.h);
+        }
+    return state;
+}
+
 // Folds the maps that the group's tiles before this one have published, finds the state
 // in front of the group, and with both the one in front of the tile; publishes the group's
 // map and the state behind it.  A warp for each of a lane's channels.
@@ -406,20 +435,20 @@ template <int V, int S, bool BACKWARD>
 __device__ __forceinline__ void follow_chain(const RecurrenceArgs &a, Shared<V, S, BACKWARD> &s, const Tile &t, uint32_t j,
                                              const WaitGuard &guard)
 {
+    constexpr int kRow = 32 * V;
     const int lane = threadIdx.x % 32, channel = threadIdx.x / 32 - kChainWarp, place = place_of<BACKWARD>(t);
     if (t.index >= t.count || channel >= V) return;
     GSR_CANARY(21);
     const int64_t row = (int64_t)t.b * a.slabs + t.slab;
-    const int group = place / kGroup, count = place - group * kGroup, groups = min(group, kWindow);
-    const unsigned long long *pairs = a.pairs + (row * a.tiles + group * kGroup) * (32 * V) + channel * 32 + lane;
-    unsigned long long *ends = a.ends + (row * a.groups + group) * (32 * V) + channel * 32 + lane;
-    const unsigned long long *window = ends - groups * (32 * V);
-    float state = 0.0f;   // (the first map of a chain takes no state)
+    const int group = place / kGroup, count = place - group * kGroup;
+    const unsigned long long *pairs = a.pairs + (row * a.tiles + group * kGroup) * kRow + channel * 32 + lane;
+    unsigned long long *ends = a.ends + (row * a.groups + group) * kRow + channel * 32 + lane;
     if (place > 0) {
-        unsigned long long seen[kGroup - 1], behind[kWindow];
-        look(pairs, 32 * V, count, seen);
-        look(window, 32 * V, groups, behind);
-        wait_for(a, pairs, 32 * V, count, seen, false, [&] {
+        unsigned long long seen[kGroup - 1], near[kNear];
+        const int nearby = min(group, kNear);
+        look(pairs, kRow, count, seen);
+        if (!a.far) look(ends - nearby * kRow, kRow, nearby, near);
+        wait_for(a, pairs, kRow, count, seen, false, [&] {
             bool all = true;
 #pragma unroll
             for (int k = 0; k < kGroup - 1; ++k) all = all && (k >= count || seen[k] != kNoMap);
@@ -438,21 +467,16 @@ __device__ __forceinline__ void follow_chain(const RecurrenceArgs &a, Shared<V, 
             // (The first group's takes no state, whatever its A has become.)
             publish(ends, word_of({group > 0 ? whole.a : kNoState, whole.h}));
         }
+        float state = 0.0f;   // (the first group's maps take none)
         if (group > 0) {
-            // The latest word of a known state, and maps from there on.
-            wait_for(a, window, 32 * V, groups, behind, true, [&] {
-                bool known = false;
-#pragma unroll
-                for (int k = 0; k < kWindow; ++k)
-                    if (k < groups) known = is_state(behind[k]) || (known && behind[k] != kNoMap);
-                return known;
-            });
-#pragma unroll
-            for (int k = 0; k < kWindow; ++k)
-                if (k < groups) {
-                    const Map<1> g = map_of(behind[k]);
-                    state = is_state(behind[k]) ? g.h : fmaf(g.a, state, g.h);
-                }
+            if (a.far) {
+                const int back = min(group, kFar);
+                unsigned long long far[kFar];
+                look(ends - back * kRow, kRow, back, far);
+                state = state_behind(a, ends - back * kRow, kRow, back, far);
+            } else {
+                state = state_behind(a, ends - nearby * kRow, kRow, nearby, near);
+            }
             if (closes) publish(ends, word_of({kNoState, mad(whole.a, state, whole.h)}));
         }
         state = mad(m.a, state, m.h);
@@ -1152,6 +1176,7 @@ int run(gsr_ctx *ctx, RecurrenceArgs &a, int dtype, cudaStream_t stream)
     const bool chained = a.tiles > 1;
     const size_t chains = (size_t)a.batch * a.slabs;
     a.groups = (a.tiles + kGroup - 1) / kGroup;
+    a.far = chains < kManyChains;
     const size_t pairs = chained ? chains * a.tiles * kSlab * sizeof(unsigned long long) : 0;
     const size_t ends = chained ? chains * a.groups * kSlab * sizeof(unsigned long long) : 0;
     const size_t bytes = chained ? pairs + ends + 16 : 0;
