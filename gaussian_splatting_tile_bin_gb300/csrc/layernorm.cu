@@ -6,12 +6,20 @@
 //   dx = rstd (g - mean(g) - xh mean(g xh)) + dtotal,  dw = sum dout xh,  db = sum dout.
 //
 // Bound by HBM.  A row stays in the registers of its team (lanes of a warp, a warp
-// or several) between the statistics and the result, so every array moves once.
-// The backward's blocks walk rows and keep their channels' shares of dw and db in
-// registers; a second kernel adds the blocks' sums in order.
+// or several) between the statistics and the result, so every array moves once; a block
+// walks rows, and its threads' copies run three rows ahead, so that the parameters and,
+// backward, the channels' shares of dw and db stay in registers too.  A second kernel adds
+// the blocks' shares in order.  32,640 x 2,048 in bf16 behind a residual (four arrays of 134
+// MB each way, 79 us at the copy rate): forward 93 us, backward 83 us; without one 43 us of
+// 39 and 67 us of 59.  Rows of 128 in f16 (80,000): 6.6 us of 6.0 and 12.3 us of 9.0, of
+// which the second kernel's launch is about 3.  Channels that are no multiple of 16 bytes
+// take accesses of 4 bytes or one element: 129 and 140 us at 2,050, 197 and 177 at 2,049,
+// bound by the number of accesses.  Above 8,192 channels a block of 1,024 threads has 64
+// registers a thread, and the backward spills (4,000 x 16,384 in bf16: 215 us of 58).
 //
-// Numerics.  The variance is the mean of centred squares, from the registers; sums
-// over a row pass a thread's elements and a tree, in a fixed order.
+// Numerics.  The variance is the mean of centred squares, from the registers; sums over
+// a row pass a thread's elements and a tree, in a fixed order, all in float.  The norm of a
+// sum is that of the rounded sum, which the backward reads.
 #include <algorithm>
 #include <type_traits>
 
