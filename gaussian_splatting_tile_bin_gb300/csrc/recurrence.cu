@@ -35,8 +35,7 @@
 // 145 us, bound by HBM; the rest is what a map and a state take through L2.  Tiles without a
 // ring and a chain of their own took 170 and 323 us, with them 136 and 299, with runs that
 // wait in tensor memory 115 and 213; a chain whose missing words are looked at together 102
-// and 188, and groups that publish their map before their state 95 and 168.  One reciprocal
-// serves a pair of gates, as reciprocals have half the rate of exponentials.
+// and 188, and groups that publish their map before their state 95 and 168.
 //
 // Numerics.  With e = exp(-|f|), the larger of a and 1 - a is 1 / (1 + e) and the smaller
 // e / (1 + e): neither is taken as a difference, so gates near 0 and 1 lose nothing.  (The
@@ -588,16 +587,11 @@ __device__ __forceinline__ void split(float f, float &a, float &s)
     s = f < 0.0f ? large : small;
 }
 
-// (One reciprocal for both: 1 / x = y (1 / (x y)).)
 template <typename T>
 __device__ __forceinline__ void split(float2 f, float2 &a, float2 &s)
 {
-    const float2 e = make_float2(exp_minus<T>(fabsf(f.x)), exp_minus<T>(fabsf(f.y)));
-    const float2 one = add2(e, make_float2(1.0f, 1.0f));
-    const float r = rcp_fast(one.x * one.y);
-    const float2 large = mul2(make_float2(one.y, one.x), make_float2(r, r)), small = mul2(e, large);
-    a = make_float2(f.x < 0.0f ? small.x : large.x, f.y < 0.0f ? small.y : large.y);
-    s = make_float2(f.x < 0.0f ? large.x : small.x, f.y < 0.0f ? large.y : small.y);
+    split<T>(f.x, a.x, s.x);
+    split<T>(f.y, a.y, s.y);
 }
 
 template <typename T>

@@ -109,6 +109,31 @@ def test_not_finite_over_groups(gsr, ctx):  # noqa: F811
         assert all(torch.equal(a.view(torch.int32), b.view(torch.int32)) for a, b in zip(run, runs[0]))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("n,c", [(9, 64), (9, 33), (300, 64), (300, 66), (300, 33), (3000, 64)])
+def test_not_finite_stays_in_its_channel(gsr, ctx, dtype, n, c):  # noqa: F811
+    """Beside its neighbour in a pair too: in the values, both gates, the gradients and the states."""
+    t = {k: _dev(v) for k, v in _inputs(2, n, c, dtype, 47).items()}
+    clean = _run(gsr, ctx, t)
+    places = {"x": (0, n // 2, 5), "forget": (1, n // 3, 6), "gate": (0, n // 2, 9), "dout": (1, n - 1, 12)}
+    for value in (float("nan"), float("inf"), -float("inf")):
+        for key, place in places.items():
+            bad = {k: v.clone() for k, v in t.items()}
+            bad[key][place] = value
+            got = _run(gsr, ctx, bad)
+            others = torch.ones(c, dtype=torch.bool, device="cuda")
+            others[place[2]] = False
+            for name, want in clean.items():
+                assert torch.equal(got[name][..., others], want[..., others]), (key, name)
+                assert torch.equal(got[name][1 - place[0]], want[1 - place[0]]), (key, name)
+            if key in ("x", "forget") and value != value:
+                assert torch.isnan(got["out"][place[0], place[1]:, place[2]]).all()
+                assert torch.isnan(got["final"][place[0], place[2]])
+            if key == "forget" and value != value:   # what the state meets reaches every gradient before it
+                assert torch.isnan(got["dx"][place[0], :place[1] + 1, place[2]]).all()
+                assert torch.isnan(got["dinitial"][place[0], place[2]])
+
+
 def test_random_shapes(gsr, ctx):  # noqa: F811
     g = torch.Generator().manual_seed(46)
     pick = lambda *values: values[int(torch.randint(len(values), (1,), generator=g))]  # noqa: E731
