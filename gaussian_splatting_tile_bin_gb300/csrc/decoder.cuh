@@ -6,6 +6,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
+
 #include "internal.cuh"
 
 namespace gsr {
@@ -62,6 +64,21 @@ cudaError_t launch_kernel_smem(gsr_ctx *ctx, void (*kernel)(Params...), dim3 gri
     ++ctx->launches;
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
+
+// Whether something that holds for a kernel on a device has still to be done there; for a
+// static of each kernel's launch.  (Raising a kernel's limit of dynamic shared memory takes
+// 2.4 us of a call on the host.)
+class OncePerDevice {
+public:
+    bool due(const gsr_ctx *ctx) const { return ctx->device >= 64 || !(done_.load() >> ctx->device & 1); }
+    void done(const gsr_ctx *ctx)
+    {
+        if (ctx->device < 64) done_.fetch_or(1ull << ctx->device);
+    }
+
+private:
+    std::atomic<unsigned long long> done_{0};
+};
 
 __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }

@@ -585,18 +585,22 @@ template <typename T, int V, int N, bool WIDE, int THREADS, bool BACKWARD, bool 
 cudaError_t launch_rows(gsr_ctx *ctx, LayerArgs &a, int teams, cudaStream_t stream)
 {
     constexpr int kArrays = (BACKWARD ? 2 : 1) + SUM;
+    constexpr size_t kRing = (size_t)kStages<T, V, N, kArrays, THREADS> * kArrays * N * THREADS * sizeof(T) * V;
+    constexpr size_t kTeamSums = 2 * kTeamWarps * sizeof(float2), kShares = N * V * sizeof(float2);   // of a team, a thread
     const int threads = teams * a.team;
-    const size_t ring = (size_t)kStages<T, V, N, kArrays, THREADS> * kArrays * N * THREADS * sizeof(T) * V;
-    const size_t sums = WIDE ? (size_t)teams * 2 * kTeamWarps * sizeof(float2) : 0;
-    const size_t shares = BACKWARD ? (size_t)threads * N * V * sizeof(float2) : 0;
-    const size_t smem = std::max(sums + ring, shares);
+    const size_t smem = std::max(kRing + (WIDE ? teams * kTeamSums : 0), BACKWARD ? threads * kShares : 0);
     void (*kernel)(LayerArgs);
     if constexpr (BACKWARD)
         kernel = k_layer_norm_grad<T, V, N, WIDE, THREADS, SUM>;
     else
         kernel = k_layer_norm<T, V, N, WIDE, THREADS, SUM>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
+    static OncePerDevice once;
+    if (once.due(ctx)) {
+        constexpr size_t kMost = std::max(kRing + (WIDE ? THREADS / 64 * kTeamSums : 0), BACKWARD ? THREADS * kShares : 0);
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
+        if (e != cudaSuccess) return e;
+        once.done(ctx);
+    }
     return launch_kernel_smem(ctx, kernel, dim3((unsigned)a.blocks), threads, smem, 1, stream, a);
 }
 

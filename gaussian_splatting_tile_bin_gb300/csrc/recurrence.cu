@@ -1149,13 +1149,19 @@ int launch(gsr_ctx *ctx, RecurrenceArgs &a, int dtype, const char *what, cudaStr
                     return rc;
     }
     auto *kernel = k_recurrence<T, V, GATE, COPY, BACKWARD>;
-    // (One that starts with fewer registers than the shares add up to would wait for them.)
-    cudaFuncAttributes attributes;
-    if (int rc = cuda_check(ctx, cudaFuncGetAttributes(&attributes, kernel), what)) return rc;
-    if (attributes.numRegs < kStart) return fail(ctx, GSR_ERR_CUDA, std::string(what) + ": compiled with too few registers");
-    if (kBytes > 0)
-        if (int rc = cuda_check(ctx, cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes), what))
-            return rc;
+    static OncePerDevice once;
+    if (once.due(ctx)) {
+        // (A kernel that starts with fewer registers than the shares add up to would wait for them.)
+        cudaFuncAttributes attributes;
+        if (int rc = cuda_check(ctx, cudaFuncGetAttributes(&attributes, kernel), what)) return rc;
+        if (attributes.numRegs < kStart)
+            return fail(ctx, GSR_ERR_CUDA, std::string(what) + ": compiled with too few registers");
+        if (kBytes > 0)
+            if (int rc = cuda_check(ctx, cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes),
+                                    what))
+                return rc;
+        once.done(ctx);
+    }
     const uint32_t most = (uint32_t)(kBlocks * ctx->num_sms);
     return cuda_check(ctx, launch_kernel_smem(ctx, kernel, dim3(a.work < most ? a.work : most), kThreads, kBytes, 1, stream,
                                               a, maps), what);

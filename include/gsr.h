@@ -594,7 +594,8 @@ int gsr_layer_norm_forward(gsr_ctx *ctx, const gsr_layer_norm *desc, const gsr_h
  * dL/dx is the residual's gradient as well.
  *   total       the forward's (its x, without a residual), with its mean and rstd
  *   dl_dtotal   NULL, or the gradient that reaches total past this norm
- *   dl_dx       may be dl_dout or dl_dtotal itself (same data and strides)
+ *   dl_dx       may be dl_dout or dl_dtotal itself (same data and strides); an input
+ *               that items share by a stride of 0 has a gradient for each of them
  *   dl_dweight, dl_dbias   device, [channels] float, overwritten; each may be NULL
  * The same bits on every run.  Errors: as the forward. */
 int gsr_layer_norm_backward(gsr_ctx *ctx, const gsr_layer_norm *desc, const gsr_heads *dl_dout,
@@ -615,8 +616,9 @@ int gsr_layer_norm_backward(gsr_ctx *ctx, const gsr_layer_norm *desc, const gsr_
  *   x, forget, gate, out   [batch, tokens, channels]: gsr_heads of one head; gate
  *              may be NULL; out may be x, forget or gate itself (same data and strides)
  *   initial    device, [batch, channels] float or NULL (0)
- *   final      device, [batch, channels] float, written: h behind the last token
- *              (initial, for an item without tokens); may be initial itself
+ *   final      device, [batch, channels] float, written: h behind the last token of
+ *              the recurrence's order (initial, for an item without tokens); may be
+ *              initial itself
  *   states     device, [batch, blocks, channels] float with a block for every
  *              GSR_RECURRENCE_BLOCK tokens, or NULL: h in front of each block of the
  *              recurrence's order, for the backward.  Blocks behind an item's last
@@ -650,7 +652,8 @@ int gsr_gated_recurrence_forward(gsr_ctx *ctx, const gsr_recurrence *desc, const
  *   gate, dl_dgate   both NULL or both not
  *   dl_dfinal   device, [batch, channels] float or NULL (0)
  *   dl_dx, dl_dforget, dl_dgate   [batch, tokens, channels], overwritten; dl_dx may
- *               be dl_dout itself
+ *               be dl_dout itself.  An input that items share by a stride of 0 has a
+ *               gradient for each of them.
  *   dl_dinitial   device, [batch, channels] float, overwritten, or NULL; may be
  *               dl_dfinal itself
  * The same bits on every run.  Errors: as the forward. */
