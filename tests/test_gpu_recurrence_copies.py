@@ -77,6 +77,31 @@ def test_shared_and_strided_items(gsr, ctx):  # noqa: F811
     assert (grad[:, 1::2] == 5).all() and (grad[:, :, :32] == 5).all() and (grad[:, :, 64:] == 5).all()
 
 
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_token_major_arrays(gsr, ctx, dtype, reverse):  # noqa: F811
+    """Views of [tokens, batch, channels]: the items' stride is less than the tokens'."""
+    t = _inputs(3, 400, 72, dtype, 47)
+    _compare(gsr, ctx, t, lengths=[400, 0, 277], reverse=reverse,
+             place=lambda v: None if v is None else v.transpose(0, 1).contiguous().cuda().transpose(0, 1))
+
+
+def test_windows_that_overlap(gsr, ctx):  # noqa: F811
+    """Inputs whose tokens share channels, and whose items share tokens, with the next."""
+    t = _inputs(3, 300, 64, BF16, 48)
+    g = torch.Generator().manual_seed(49)
+    at = {}
+    for name in ("x", "forget", "gate"):
+        base = (2 * torch.randn(300 * 32 + 2 * 800 + 64, generator=g)).bfloat16()
+        t[name], at[name] = (v.as_strided((3, 300, 64), (800, 32, 1)) for v in (base, base.cuda()))
+    out, final, states = gsr.gated_recurrence_forward(ctx, at["x"], at["forget"], at["gate"], initial=_dev(t["initial"]))
+    grads = gsr.gated_recurrence_backward(ctx, _dev(t["dout"]), at["x"], at["forget"], at["gate"], states,
+                                          dl_dfinal=_dev(t["dfinal"]))
+    want = _want(t)
+    for name, got in zip(("out", "final") + NAMES, (out, final) + grads):
+        ref.check(got, want[name], name)
+
+
 def test_extremes_over_groups(gsr, ctx):  # noqa: F811
     """Tiles and groups whose gates are shut or open throughout: maps of no state, and of nothing
     but the state."""
