@@ -14,8 +14,9 @@
 // 39 and 67 us of 59.  Rows of 128 in f16 (80,000): 6.6 us of 6.0 and 12.3 us of 9.0, of
 // which the second kernel's launch is about 3.  Channels that are no multiple of 16 bytes
 // take accesses of 4 bytes or one element: 129 and 140 us at 2,050, 197 and 177 at 2,049,
-// bound by the number of accesses.  Above 8,192 channels a block of 1,024 threads has 64
-// registers a thread, and the backward spills (4,000 x 16,384 in bf16: 215 us of 58).
+// bound by the number of accesses.  Above 8,192 channels a row takes 1,024 threads:
+// of a block forward, of two backward (4,000 x 16,384 in bf16: 67 us of 39 and 87 of 58, for
+// what a sum costs between warps with one row at a time).
 //
 // Numerics.  The variance is the mean of centred squares, from the registers; sums over
 // a row pass a thread's elements and a tree, in a fixed order, all in float.  The norm of a
@@ -23,12 +24,12 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "decoder.cuh"
+#include "tensor.cuh"
 
 namespace gsr {
 namespace {
 
-constexpr int kRowThreads = 512;   // of a block, one to an SM, where a row needs no more
+constexpr int kRowThreads = 512, kLongThreads = 1024;   // of a block, one to an SM; of a long row's, forward
 // Elements of a thread: parameters, their gradients' sums and a row's inputs stay in
 // registers (8 in two blocks an SM: 80,000 x 128 in f16 in 10.2 and 24 us, 6.7 and 12.3 with
 // 16; 100,000 x 256 in bf16 in 23 us forward, 15).
@@ -48,8 +49,9 @@ struct LayerArgs {
     int batch, tokens, heads, channels;
     uint32_t rows;
     int team;                       // threads of a row
-    int blocks;
+    int blocks;                     // (or pairs of them)
     float eps;
+    uint32_t *status;
 };
 
 // A row's first element.  `flat`: the rows lie at one stride (one item of one head).
@@ -148,9 +150,51 @@ __device__ __forceinline__ float2 parameter(const float *from, const LayerArgs &
     return f;
 }
 
+// Teams: lanes of a warp, a block's warps, or those of two blocks of a cluster: backward,
+// rows of more than 8,192 channels (4,000 x 16,384 in bf16 behind a residual in 100 us; a
+// block of 1,024 threads has 64 registers a thread, spills and took 231).  Forward a block
+// holds them: the two sums a row cost two blocks more than they gain (without a residual 82
+// us, 67 in one block; with one 105 and 121; 4,000 x 12,345 180 and 143).
+constexpr int kInWarp = 0, kInBlock = 1, kInTwo = 2;
+template <int KIND>
+constexpr int kBlocksOf = KIND == kInTwo ? 2 : 1;   // a team's
+
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Of a block whose rows another one of its cluster shares.
+struct Beside {
+    uint64_t full[2];   // the other's sums are there, for either copy
+    uint32_t aborted;
+};
+
+// Writes to the cluster's other block, where this one's `at` is, and counts the bytes at
+// its `bar`.  (No fence: one would wait for the row's stores too, 0.6 us.)
+__device__ __forceinline__ uint32_t beside(const void *at)
+{
+    uint32_t to;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_address(at)), "r"(blockIdx.x % 2 ^ 1));
+    return to;
+}
+__device__ __forceinline__ void store_beside(const float *at, float v, const uint64_t *bar)
+{
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(beside(at)), "f"(v),
+                 "r"(beside(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void store_beside(const float2 *at, float2 v, const uint64_t *bar)
+{
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(beside(at)),
+                 "f"(v.x), "f"(v.y), "r"(beside(bar))
+                 : "memory");
+}
+
 // Sums of a team (of one float or two).  Teams up to a warp: by shuffles.  Wider ones
 // meet at a barrier of their own, over shared memory in two copies, so that one
-// barrier a sum is enough.
+// barrier a sum is enough.  Two blocks write their warps' sums to each other: a copy is
+// written again once the other block has all of the sum in between, so behind its reads.
 __device__ __forceinline__ void add_lane(float &v, int d) { v += __shfl_xor_sync(~0u, v, d); }
 __device__ __forceinline__ void add_lane(float2 &v, int d)
 {
@@ -171,10 +215,10 @@ __device__ __forceinline__ void team_barrier(int team, int threads)
 // s_sums: the team's [2][kTeamWarps], 0 behind its warps; turn: which copy.
 constexpr int kTeamWarps = 32;
 
-template <bool WIDE, typename F>
-__device__ __forceinline__ F team_sum(F v, const LayerArgs &a, float2 *s_sums, int team, int &turn)
+template <int KIND, typename F>
+__device__ __forceinline__ F team_sum(F v, const LayerArgs &a, float2 *s_sums, int team, uint32_t &turn, Beside *s_beside = nullptr)
 {
-    if constexpr (!WIDE) {
+    if constexpr (KIND == kInWarp) {
 #pragma unroll
         for (int d = 16; d > 0; d /= 2)
             if (d < a.team) add_lane(v, d);
@@ -182,11 +226,29 @@ __device__ __forceinline__ F team_sum(F v, const LayerArgs &a, float2 *s_sums, i
         using Four = std::conditional_t<std::is_same_v<F, float>, float4, float2[4]>;
 #pragma unroll
         for (int d = 16; d > 0; d /= 2) add_lane(v, d);
-        F *s = (F *)(s_sums + turn * kTeamWarps);
-        turn ^= 1;
+        const uint32_t copy = turn & 1, parity = turn >> 1 & 1;
+        F *s = (F *)(s_sums + copy * kTeamWarps);
+        ++turn;
         const int warps = a.team / 32;
-        if (threadIdx.x % 32 == 0) s[threadIdx.x / 32 - team * warps] = v;
-        team_barrier(team, a.team);
+        if constexpr (KIND == kInTwo) {
+            // (Once a wait has run out the barriers are left as they are, here and, for want
+            // of this block's sums, in the other block.)
+            const WaitGuard guard = {&s_beside->aborted, a.status};
+            uint64_t *full = &s_beside->full[copy];
+            GSR_CANARY(38 + copy);
+            if (threadIdx.x % 32 == 0 && !guard.stop()) {
+                if (threadIdx.x == 0) barrier_expect(smem_address(full), blockDim.x / 32 * sizeof(F));
+                F *at = s + (blockIdx.x % 2 * blockDim.x + threadIdx.x) / 32;
+                *at = v;
+                store_beside(at, v, full);
+            }
+            __syncthreads();
+            barrier_wait_warp(smem_address(full), parity, guard);
+            GSR_CANARY(40 + copy);
+        } else {
+            if (threadIdx.x % 32 == 0) s[threadIdx.x / 32 - team * warps] = v;
+            team_barrier(team, a.team);
+        }
         v = four((const Four *)s);
         for (int w = 4; w < warps; w += 4) {
             const F more = four((const Four *)(s + w));
@@ -200,12 +262,30 @@ __device__ __forceinline__ F team_sum(F v, const LayerArgs &a, float2 *s_sums, i
 }
 
 // Clears the sums of the warps that a block's teams do not have.
-template <bool WIDE>
-__device__ __forceinline__ void clear_sums(float2 *s_all, int teams)
+template <int KIND>
+__device__ __forceinline__ void start_sums(float2 *s_all, int teams, Beside *s_beside = nullptr)
 {
-    if constexpr (WIDE) {
+    if constexpr (KIND != kInWarp)
         for (int i = threadIdx.x; i < teams * 2 * kTeamWarps; i += blockDim.x) s_all[i] = make_float2(0.0f, 0.0f);
+    if constexpr (KIND == kInTwo) {
+        if (threadIdx.x == 0) {
+            s_beside->aborted = 0;
+            for (uint64_t &full : s_beside->full) barrier_init(smem_address(&full), 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        cluster_barrier();
+    } else if constexpr (KIND == kInBlock) {
         __syncthreads();
+    }
+}
+
+// A block leaves once the other one writes to it no more.
+template <int KIND>
+__device__ __forceinline__ void end_sums(const LayerArgs &a, Beside &s_beside)
+{
+    if constexpr (KIND == kInTwo) {
+        drain_if_aborted({&s_beside.aborted, a.status});
+        cluster_barrier();
     }
 }
 
@@ -297,7 +377,7 @@ struct Ring {
 
 // ---- forward ------------------------------------------------------------------------
 
-template <typename T, int V, int N, bool WIDE, int THREADS, bool SUM>
+template <typename T, int V, int N, int KIND, int THREADS, bool SUM>
 __global__ void __launch_bounds__(THREADS, 1) k_layer_norm(const LayerArgs a)
 {
     grid_dependency_begin();
@@ -308,13 +388,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_layer_norm(const LayerArgs a)
     const int teams = blockDim.x / a.team, team = threadIdx.x / a.team, lane = threadIdx.x % a.team;
     const uint32_t stride = gridDim.x * (uint32_t)teams;
     float2 *s_sums = (float2 *)s_bytes + team * 2 * kTeamWarps;
-    Ring<T, V, N, A, S, THREADS> ring = {(Vec<T, V> *)(s_bytes + (WIDE ? teams * 2 * kTeamWarps * sizeof(float2) : 0)) + threadIdx.x,
+    Ring<T, V, N, A, S, THREADS> ring = {(Vec<T, V> *)(s_bytes + (KIND != kInWarp ? teams * 2 * kTeamWarps * sizeof(float2) : 0)) + threadIdx.x,
                                          a.x, a.residual, a.residual, flat};
 
     // (Below 2^31 rows, steps ahead of them below 2^32.  All teams take the same number of steps.)
     uint32_t row = blockIdx.x * teams + team, first = blockIdx.x * teams;
     ring.start(a, row, stride, lane);
-    clear_sums<WIDE>((float2 *)s_bytes, teams);
+    start_sums<KIND>((float2 *)s_bytes, teams);
     float2 weight[kPairs], bias[kPairs];
 #pragma unroll
     for (int p = 0; p < kPairs; ++p) {
@@ -323,7 +403,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_layer_norm(const LayerArgs a)
     }
     const float share = 1.0f / (float)a.channels;
     const bool full = a.channels == a.team * V * N;
-    int turn = 0;
+    uint32_t turn = 0;
     for (; first < a.rows; first += stride, row += stride) {
         const bool valid = row < a.rows;
         Elements in[A];
@@ -339,7 +419,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_layer_norm(const LayerArgs a)
         for (int p = 0; p < kPairs; ++p) sum = add2(sum, f[p] = x.get(p));
         ring.fetch(a, row + S * stride, lane);
         ring.advance();
-        const float mean = team_sum<WIDE>(sum.x + sum.y, a, s_sums, team, turn) * share;
+        const float mean = team_sum<KIND>(sum.x + sum.y, a, s_sums, team, turn) * share;
         const float2 minus = make_float2(-mean, -mean);
         sum = make_float2(0.0f, 0.0f);
         if (full) {
@@ -357,7 +437,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_layer_norm(const LayerArgs a)
                 sum = fma2(f[p], f[p], sum);
             }
         }
-        const float var = team_sum<WIDE>(sum.x + sum.y, a, s_sums, team, turn) * share;
+        const float var = team_sum<KIND>(sum.x + sum.y, a, s_sums, team, turn) * share;
         const float rstd = rsqrtf(var + a.eps);
         const float2 scale = make_float2(rstd, rstd);
 #pragma unroll
@@ -375,26 +455,28 @@ __global__ void __launch_bounds__(THREADS, 1) k_layer_norm(const LayerArgs a)
 
 // ---- backward -----------------------------------------------------------------------
 
-template <typename T, int V, int N, bool WIDE, int THREADS, bool SUM>
+template <typename T, int V, int N, int KIND, int THREADS, bool SUM>
 __global__ void __launch_bounds__(THREADS, 1) k_layer_norm_grad(const LayerArgs a)
 {
     grid_dependency_begin();
     // The teams' sums, then the ring; at the end the block's shares of dw and db.
     extern __shared__ __align__(16) unsigned char s_bytes[];
+    __shared__ Beside s_beside;
     float2 *s_work = (float2 *)s_bytes;
     using Elements = Part<T, V, N>;
-    constexpr int kPairs = Elements::kPairs, A = SUM ? 3 : 2, S = kStages<T, V, N, A, THREADS>;
+    constexpr int kPairs = Elements::kPairs, A = SUM ? 3 : 2, S = kStages<T, V, N, A, THREADS>, X = kBlocksOf<KIND>;
     const bool flat = a.batch == 1 && a.heads == 1;
-    const int teams = blockDim.x / a.team, team = threadIdx.x / a.team, lane = threadIdx.x % a.team;
-    const uint32_t stride = gridDim.x * (uint32_t)teams;
+    const int teams = X * blockDim.x / a.team, team = threadIdx.x / a.team;
+    const int lane = KIND == kInTwo ? blockIdx.x % 2 * blockDim.x + threadIdx.x : threadIdx.x % a.team;
+    const uint32_t block = blockIdx.x / X, stride = gridDim.x / X * (uint32_t)teams;
     float2 *s_sums = s_work + team * 2 * kTeamWarps;
-    Ring<T, V, N, A, S, THREADS> ring = {(Vec<T, V> *)(s_bytes + (WIDE ? teams * 2 * kTeamWarps * sizeof(float2) : 0)) + threadIdx.x,
+    Ring<T, V, N, A, S, THREADS> ring = {(Vec<T, V> *)(s_bytes + (KIND != kInWarp ? teams * 2 * kTeamWarps * sizeof(float2) : 0)) + threadIdx.x,
                                          a.total, a.x, a.residual, flat};
 
     // (As in the forward.)
-    uint32_t row = blockIdx.x * teams + team, first = blockIdx.x * teams;
+    uint32_t row = block * teams + team, first = block * teams;
     ring.start(a, row, stride, lane);
-    clear_sums<WIDE>((float2 *)s_bytes, teams);
+    start_sums<KIND>((float2 *)s_bytes, teams, &s_beside);
     float2 weight[kPairs], dw[kPairs], db[kPairs];
 #pragma unroll
     for (int p = 0; p < kPairs; ++p) {
@@ -402,7 +484,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_layer_norm_grad(const LayerArgs 
         dw[p] = db[p] = make_float2(0.0f, 0.0f);
     }
     const float share = 1.0f / (float)a.channels;
-    int turn = 0;
+    uint32_t turn = 0;
     float mean = row < a.rows ? a.mean[row] : 0.0f, rstd = row < a.rows ? a.rstd[row] : 0.0f;
     for (; first < a.rows; first += stride, row += stride) {
         Elements in[A];
@@ -430,7 +512,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_layer_norm_grad(const LayerArgs 
         }
         ring.fetch(a, row + S * stride, lane);
         ring.advance();
-        const float2 m = team_sum<WIDE>(make_float2(s1.x + s1.y, s2.x + s2.y), a, s_sums, team, turn);
+        const float2 m = team_sum<KIND>(make_float2(s1.x + s1.y, s2.x + s2.y), a, s_sums, team, turn, &s_beside);
         const float2 m1 = make_float2(-m.x * share, -m.x * share), m2 = make_float2(-m.y * share, -m.y * share);
         if (row >= a.rows) continue;
 #pragma unroll
@@ -442,12 +524,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_layer_norm_grad(const LayerArgs 
         total.store(row_of<T>(a, a.out, row, flat), a, lane);
     }
     ring.finish();
+    end_sums<KIND>(a, s_beside);
     if (!a.partial) return;
 
     // The block's sums: lanes of a warp that hold the same channels, then teams in order,
     // all of them in shared memory side by side (64 KB, where a team after the other took
     // 8 us of 65,000 x 512's 58).
-    if (!WIDE)
+    if (KIND == kInWarp)
         for (int d = a.team; d < 32; d *= 2)
 #pragma unroll
             for (int p = 0; p < kPairs; ++p) {
@@ -456,7 +539,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_layer_norm_grad(const LayerArgs 
                 db[p].x += __shfl_xor_sync(~0u, db[p].x, d);
                 db[p].y += __shfl_xor_sync(~0u, db[p].y, d);
             }
-    const int width = WIDE ? a.team : 32, each = 2 * kPairs * width;
+    const int width = KIND == kInWarp ? 32 : a.team / X, each = 2 * kPairs * width, before = X > 1 ? lane - threadIdx.x : 0;
     const int group = threadIdx.x / width, groups = blockDim.x / width, own = threadIdx.x % width;
     __syncthreads();
 #pragma unroll
@@ -465,9 +548,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_layer_norm_grad(const LayerArgs 
         s_work[group * each + (2 * p + 1) * width + own] = make_float2(dw[p].y, db[p].y);
     }
     __syncthreads();
-    float2 *out = a.partial + (int64_t)blockIdx.x * a.channels;
+    float2 *out = a.partial + (int64_t)block * a.channels;
     for (int i = threadIdx.x; i < each; i += blockDim.x) {
-        const int element = i / width, l = i - element * width, c = pair_channel<V>(a, l, element / 2, element % 2);
+        const int element = i / width, l = before + i - element * width;
+        const int c = pair_channel<V>(a, l, element / 2, element % 2);
         if (l >= a.team || c >= a.channels) continue;
         float2 sum = s_work[i];
         for (int k = 1; k < groups; ++k) sum = add2(sum, s_work[k * each + i]);
@@ -568,49 +652,55 @@ int power_of_two(int n)
 // Divides a row over a team, kElements of it to a thread, and the rows over blocks of
 // teams; returns a block's teams.  Few rows are spread over the SMs rather than over the
 // teams of one block.
-int plan_rows(const gsr_ctx *ctx, LayerArgs &a)
+int plan_rows(const gsr_ctx *ctx, LayerArgs &a, bool backward)
 {
     const int threads = (a.channels + kElements - 1) / kElements;
-    a.team = threads <= 32 ? power_of_two(threads) : (threads + 31) / 32 * 32;
+    const bool two = backward && threads > kRowThreads;
+    const int whole = two ? 64 : 32;
+    a.team = threads <= 32 ? power_of_two(threads) : (threads + whole - 1) / whole * whole;
     const uint64_t spread = ((uint64_t)a.rows + ctx->num_sms - 1) / ctx->num_sms;
     int teams = a.team > kRowThreads ? 1 : kRowThreads / a.team;
     while (a.team * teams > 128 && (uint64_t)teams > spread) teams = (teams + 1) / 2;
     if (teams * a.team % 32 != 0) teams = 32 / a.team;   // whole warps
     const uint64_t blocks = ((uint64_t)a.rows + teams - 1) / teams;
-    a.blocks = (int)(blocks < (uint64_t)ctx->num_sms ? blocks : ctx->num_sms);
+    a.blocks = (int)std::min(blocks, (uint64_t)ctx->num_sms / (two ? 2 : 1));
     return teams;
 }
 
-template <typename T, int V, int N, bool WIDE, int THREADS, bool BACKWARD, bool SUM>
+template <typename T, int V, int N, int KIND, int THREADS, bool BACKWARD, bool SUM>
 cudaError_t launch_rows(gsr_ctx *ctx, LayerArgs &a, int teams, cudaStream_t stream)
 {
     constexpr int kArrays = (BACKWARD ? 2 : 1) + SUM;
     constexpr size_t kRing = (size_t)kStages<T, V, N, kArrays, THREADS> * kArrays * N * THREADS * sizeof(T) * V;
     constexpr size_t kTeamSums = 2 * kTeamWarps * sizeof(float2), kShares = N * V * sizeof(float2);   // of a team, a thread
-    const int threads = teams * a.team;
-    const size_t smem = std::max(kRing + (WIDE ? teams * kTeamSums : 0), BACKWARD ? threads * kShares : 0);
+    const int threads = teams * a.team / kBlocksOf<KIND>;
+    const size_t smem = std::max(kRing + (KIND != kInWarp ? teams * kTeamSums : 0), BACKWARD ? threads * kShares : 0);
     void (*kernel)(LayerArgs);
     if constexpr (BACKWARD)
-        kernel = k_layer_norm_grad<T, V, N, WIDE, THREADS, SUM>;
+        kernel = k_layer_norm_grad<T, V, N, KIND, THREADS, SUM>;
     else
-        kernel = k_layer_norm<T, V, N, WIDE, THREADS, SUM>;
+        kernel = k_layer_norm<T, V, N, KIND, THREADS, SUM>;
     static OncePerDevice once;
     if (once.due(ctx)) {
-        constexpr size_t kMost = std::max(kRing + (WIDE ? THREADS / 64 * kTeamSums : 0), BACKWARD ? THREADS * kShares : 0);
+        constexpr size_t kMost = std::max(kRing + (KIND != kInWarp ? THREADS / 64 * kTeamSums : 0), BACKWARD ? THREADS * kShares : 0);
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
         if (e != cudaSuccess) return e;
         once.done(ctx);
     }
-    return launch_kernel_smem(ctx, kernel, dim3((unsigned)a.blocks), threads, smem, 1, stream, a);
+    constexpr unsigned kBlocks = kBlocksOf<KIND>;
+    return launch_kernel_smem(ctx, kernel, dim3(a.blocks * kBlocks), threads, smem, kBlocks, stream, a);
 }
 
 template <typename T, int V, bool BACKWARD, bool SUM>
 cudaError_t dispatch_rows(gsr_ctx *ctx, LayerArgs &a, int teams, cudaStream_t stream)
 {
     constexpr int N = kElements / V;
-    if (a.team <= 32) return launch_rows<T, V, N, false, kRowThreads, BACKWARD, SUM>(ctx, a, teams, stream);
-    if (a.team <= kRowThreads) return launch_rows<T, V, N, true, kRowThreads, BACKWARD, SUM>(ctx, a, teams, stream);
-    return launch_rows<T, V, N, true, 1024, BACKWARD, SUM>(ctx, a, teams, stream);
+    if (a.team <= 32) return launch_rows<T, V, N, kInWarp, kRowThreads, BACKWARD, SUM>(ctx, a, teams, stream);
+    if (a.team <= kRowThreads) return launch_rows<T, V, N, kInBlock, kRowThreads, BACKWARD, SUM>(ctx, a, teams, stream);
+    if constexpr (BACKWARD)
+        return launch_rows<T, V, N, kInTwo, kRowThreads, true, SUM>(ctx, a, teams, stream);
+    else
+        return launch_rows<T, V, N, kInBlock, kLongThreads, false, SUM>(ctx, a, teams, stream);
 }
 
 template <typename T, int V, bool BACKWARD>
@@ -657,7 +747,7 @@ int layer_norm_forward(gsr_ctx *ctx, const gsr_layer_norm &d, const gsr_heads &x
     collapse(a);
     const cudaError_t e = with_access(d.dtype, a, [&](auto t, auto v) {
         constexpr int V = decltype(v)::value;
-        return dispatch_sum<decltype(t), V, false>(ctx, a, plan_rows(ctx, a), stream);
+        return dispatch_sum<decltype(t), V, false>(ctx, a, plan_rows(ctx, a, false), stream);
     });
     return cuda_check(ctx, e, "layer norm forward");
 }
@@ -690,12 +780,13 @@ int layer_norm_backward(gsr_ctx *ctx, const gsr_layer_norm &d, const gsr_heads &
     const cudaError_t e = with_access(d.dtype, a, [&](auto t, auto v) {
         using T = decltype(t);
         constexpr int V = decltype(v)::value;
-        const int teams = plan_rows(ctx, a);
-        if (dweight || dbias) {
+        const int teams = plan_rows(ctx, a, true);
+        if (dweight || dbias || a.team > kRowThreads) {   // (without shares: for the status word of waits)
             void *work = nullptr;
-            rc = workspace.take((size_t)a.blocks * d.channels * sizeof(float2), &work);
+            rc = workspace.take(dweight || dbias ? (size_t)a.blocks * d.channels * sizeof(float2) : 0, &work);
             if (rc != GSR_OK) return cudaSuccess;
-            a.partial = (float2 *)work;
+            if (dweight || dbias) a.partial = (float2 *)work;
+            a.status = ctx->status_dev;
         }
         cudaError_t e = dispatch_sum<T, V, true>(ctx, a, teams, stream);
         if (e == cudaSuccess && a.partial)

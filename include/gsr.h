@@ -405,8 +405,8 @@ int gsr_peak_kernel(gsr_ctx *ctx, int kind, int32_t iters, float *sink, uint64_t
  * overlap unless a call says so. */
 
 /* Waits for the work on `stream`, and tells whether it is to be trusted.
- * Every wait inside the attention's and the recurrence's kernels is bounded (seconds, where a step takes
- * microseconds).  One that runs out ends its kernel without a fault, but what the
+ * Every wait inside the attention's, the recurrence's and the layer norm's kernels
+ * is bounded (seconds, where a step takes microseconds).  One that runs out ends its kernel without a fault, but what the
  * call wrote is not valid, nor is what later calls made of it.  That is reported
  * once, as GSR_ERR_CUDA: by the context's next call of a decoder operator, before
  * it launches anything, as far as the work has run by then; or by this call, which

@@ -70,6 +70,32 @@ def test_many_rows(gsr, ctx, dtype, rows, c):
     _compare(gsr, ctx, *_inputs((rows, c), dtype, rows))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("rows,c", [(2, 8193), (75, 8704), (76, 8720), (77, 9000), (153, 12352), (230, 16376), (310, 16383)])
+def test_rows_over_two_blocks(gsr, ctx, dtype, rows, c):
+    """Rows of more than 8,192 channels, around the number that are under way at a time."""
+    _compare(gsr, ctx, *_inputs((rows, c), dtype, c, rows % 2 == 0))
+
+
+def test_rows_over_two_blocks_in_place_and_captured(gsr, ctx):
+    x, r, dout, dt, w, b = (t.cuda() for t in _inputs((2, 90, 10000), BF16, 12))
+    out, total, mean, rstd = gsr.layer_norm_forward(ctx, x, w, b, residual=r)
+    dx, dw, db = gsr.layer_norm_backward(ctx, dout, total, w, mean, rstd, dl_dtotal=dt)
+    y, s, d = x.clone(), r.clone(), dout.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _, _, m, q = gsr.layer_norm_forward(ctx, y, w, b, residual=s, out=y, total=s)
+        _, ew, eb = gsr.layer_norm_backward(ctx, d, s, w, m, q, dl_dtotal=dt, dl_dx=d)
+    for _ in range(2):
+        y.copy_(x)
+        s.copy_(r)
+        d.copy_(dout)
+        graph.replay()
+        for got, want in ((y, out), (s, total), (m, mean), (q, rstd), (d, dx), (ew, dw), (eb, db)):
+            assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("weight,bias", [(False, False), (True, False), (False, True)])
 def test_missing_parameters(gsr, ctx, weight, bias):
     x, r, dout, dt, w, b = _inputs((50, 96), F32, 5)

@@ -1,6 +1,7 @@
 """Token layers as a decoder uses them: norms, recurrences in both directions and attention
 in a row, captured, on branches beside each other, and beyond a grid's and 32 bits' limits."""
 import glob
+import importlib
 import os
 import subprocess
 import sys
@@ -240,26 +241,34 @@ def test_recurrences_beside_attention(gsr, ctx):
         c.close()
 
 
-def test_warps_that_are_held_up_change_no_bit(gsr, tmp_path):
-    """A build of the recurrence in which warps sleep pseudo-random times where they wait for and
-    hand over maps and states."""
+def _held_up(tmp_path, name, helper):
+    """The outputs of a helper over a build in which the warps of one source sleep pseudo-random
+    times, and those of this one."""
     from gaussian_splatting_tile_bin_gb300 import build as b
-    source, obj, lib = os.path.join(b.CSRC, "recurrence.cu"), str(tmp_path / "recurrence.o"), str(tmp_path / "libgsr.so")
-    objects = [o for o in glob.glob(os.path.join(b.BUILD, "*.o")) if os.path.basename(o) != "recurrence.cu.o"]
+    source, obj, lib = os.path.join(b.CSRC, name), str(tmp_path / "held_up.o"), str(tmp_path / "libgsr.so")
+    objects = [o for o in glob.glob(os.path.join(b.BUILD, "*.o")) if os.path.basename(o) != name + ".o"]
     assert len(objects) == len(b.sources()) - 1
     subprocess.check_call([b._nvcc(), *b.NVCC_FLAGS, "-DGSR_RACE_CANARY", "-c", source, "-o", obj])
     subprocess.check_call([b._nvcc(), *b.ARCH, "-shared", "-o", lib, obj, *objects])
     out = tmp_path / "canary.npz"
-    r = subprocess.run([sys.executable, os.path.join(HERE, "recurrence_canary_run.py"), str(out)],
+    r = subprocess.run([sys.executable, os.path.join(HERE, helper + ".py"), str(out)],
                        env=dict(os.environ, GSR_LIBRARY=lib), capture_output=True, text=True, timeout=900)
     assert r.returncode == 0, r.stderr[-2000:]
     sys.path.insert(0, HERE)
-    import recurrence_canary_run
-    want = recurrence_canary_run.outputs()
-    got = np.load(out)
+    want, got = importlib.import_module(helper).outputs(), np.load(out)
     assert set(got.files) == set(want)
     for name, value in want.items():
         assert np.array_equal(got[name].view(np.uint8), value.view(np.uint8)), name
+
+
+def test_warps_that_are_held_up_change_no_bit(gsr, tmp_path):
+    """Where the recurrence's wait for and hand over maps and states."""
+    _held_up(tmp_path, "recurrence.cu", "recurrence_canary_run")
+
+
+def test_blocks_that_share_rows_are_held_up(gsr, tmp_path):
+    """Where the layer norm's warps hand their sums to the other block of a row."""
+    _held_up(tmp_path, "layernorm.cu", "layer_norm_canary_run")
 
 
 # -- sizes -----------------------------------------------------------------------------------
