@@ -10,13 +10,13 @@
 // walks rows, and its threads' copies run three rows ahead, so that the parameters and,
 // backward, the channels' shares of dw and db stay in registers too.  A second kernel adds
 // the blocks' shares in order.  32,640 x 2,048 in bf16 behind a residual (four arrays of 134
-// MB each way, 79 us at the copy rate): forward 93 us, backward 83 us; without one 43 us of
-// 39 and 67 us of 59.  Rows of 128 in f16 (80,000): 6.6 us of 6.0 and 12.3 us of 9.0, of
+// MB each way, 79 us at the copy rate): forward 88 us, backward 83 us; without one 42 us of
+// 39 and 67 us of 59.  Rows of 128 in f16 (80,000): 6.7 us of 6.0 and 12.3 us of 9.0, of
 // which the second kernel's launch is about 3.  Channels that are no multiple of 16 bytes
-// take accesses of 4 bytes or one element: 129 and 140 us at 2,050, 197 and 177 at 2,049,
+// take accesses of 4 bytes or one element: 115 and 140 us at 2,050, 183 and 174 at 2,049,
 // bound by the number of accesses.  Above 8,192 channels a row takes 1,024 threads:
 // of a block forward, of two backward (4,000 x 16,384 in bf16: 67 us of 39 and 87 of 58, for
-// what a sum costs between warps with one row at a time).
+// what sums cost between warps with one row at a time).
 //
 // Numerics.  The variance is the mean of centred squares, from the registers; sums over
 // a row pass a thread's elements and a tree, in a fixed order, all in float.  The norm of a
@@ -293,8 +293,8 @@ __device__ __forceinline__ void end_sums(const LayerArgs &a, Beside &s_beside)
 
 // A block walks rows, `teams` at a time, and every thread's elements of the next ones
 // come through a ring of its own in shared memory (asynchronous copies; no thread
-// waits for another): S stages of A arrays, three (two are slower without a residual, 45.8
-// to 43.5 us for 32,640 x 2,048 in bf16, four and eight no faster) or what 200 KB hold.  Single elements of
+// waits for another): S stages of A arrays, three (two are slower without a residual, 44.1
+// to 41.8 us for 32,640 x 2,048 in bf16, four and eight no faster) or what 200 KB hold.  Single elements of
 // 2 bytes have no such copies and are read directly (S = 0).
 template <typename T, int V, int N, int A, int THREADS>
 constexpr int kStages = sizeof(T) * V < 4
@@ -377,13 +377,18 @@ struct Ring {
 
 // ---- forward ------------------------------------------------------------------------
 
-template <typename T, int V, int N, int KIND, int THREADS, bool SUM>
+// AHEAD: a row's centred squares meet with the next one's sum, so that a team meets once a
+// row, and behind a residual, where the next row is in registers, two stages of the ring do.
+template <typename T, int V, int N, int A, int THREADS, bool AHEAD>
+constexpr int kForwardStages = std::min(kStages<T, V, N, A, THREADS>, AHEAD && A > 1 ? 2 : 3);
+
+template <typename T, int V, int N, int KIND, int THREADS, bool SUM, bool AHEAD>
 __global__ void __launch_bounds__(THREADS, 1) k_layer_norm(const LayerArgs a)
 {
     grid_dependency_begin();
     extern __shared__ __align__(16) unsigned char s_bytes[];   // the teams' sums, then the ring
     using Elements = Part<T, V, N>;
-    constexpr int kPairs = Elements::kPairs, A = SUM ? 2 : 1, S = kStages<T, V, N, A, THREADS>;
+    constexpr int kPairs = Elements::kPairs, A = SUM ? 2 : 1, S = kForwardStages<T, V, N, A, THREADS, AHEAD>;
     const bool flat = a.batch == 1 && a.heads == 1;
     const int teams = blockDim.x / a.team, team = threadIdx.x / a.team, lane = threadIdx.x % a.team;
     const uint32_t stride = gridDim.x * (uint32_t)teams;
@@ -404,51 +409,66 @@ __global__ void __launch_bounds__(THREADS, 1) k_layer_norm(const LayerArgs a)
     const float share = 1.0f / (float)a.channels;
     const bool full = a.channels == a.team * V * N;
     uint32_t turn = 0;
-    for (; first < a.rows; first += stride, row += stride) {
-        const bool valid = row < a.rows;
+    // A row's total (ahead, stored where its squares are taken) and a thread's share of its sum.
+    auto take = [&](uint32_t from, Elements &x) {
         Elements in[A];
-        ring.take(a, row, lane, in);
-        Elements &x = in[0];
+        ring.take(a, from, lane, in);
+        x = in[0];
         if constexpr (SUM) {
 #pragma unroll
             for (int p = 0; p < kPairs; ++p) x.set(p, add2(x.get(p), in[A - 1].get(p)));
-            if (valid) x.store(row_of<T>(a, a.total, row, flat), a, lane);
+            if (!AHEAD && from < a.rows) x.store(row_of<T>(a, a.total, from, flat), a, lane);
         }
-        float2 f[kPairs], sum = make_float2(0.0f, 0.0f);
+        float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int p = 0; p < kPairs; ++p) sum = add2(sum, f[p] = x.get(p));
-        ring.fetch(a, row + S * stride, lane);
+        for (int p = 0; p < kPairs; ++p) sum = add2(sum, x.get(p));
+        ring.fetch(a, from + S * stride, lane);
         ring.advance();
-        const float mean = team_sum<KIND>(sum.x + sum.y, a, s_sums, team, turn) * share;
+        return sum.x + sum.y;
+    };
+    Elements x;
+    float mean;
+    if constexpr (AHEAD) mean = team_sum<KIND>(take(row, x), a, s_sums, team, turn) * share;
+    for (; first < a.rows; first += stride, row += stride) {
+        if constexpr (!AHEAD) mean = team_sum<KIND>(take(row, x), a, s_sums, team, turn) * share;
         const float2 minus = make_float2(-mean, -mean);
-        sum = make_float2(0.0f, 0.0f);
+        float2 f[kPairs], sum = make_float2(0.0f, 0.0f);
         if (full) {
 #pragma unroll
             for (int p = 0; p < kPairs; ++p) {
-                f[p] = add2(f[p], minus);
+                f[p] = add2(x.get(p), minus);
                 sum = fma2(f[p], f[p], sum);
             }
         } else {
 #pragma unroll
             for (int p = 0; p < kPairs; ++p) {
-                f[p] = add2(f[p], minus);
+                f[p] = add2(x.get(p), minus);
                 if (pair_channel<V>(a, lane, p, 0) >= a.channels) f[p].x = 0.0f;
                 if (pair_channel<V>(a, lane, p, 1) >= a.channels) f[p].y = 0.0f;
                 sum = fma2(f[p], f[p], sum);
             }
         }
-        const float var = team_sum<KIND>(sum.x + sum.y, a, s_sums, team, turn) * share;
-        const float rstd = rsqrtf(var + a.eps);
-        const float2 scale = make_float2(rstd, rstd);
+        float2 sums = make_float2(sum.x + sum.y, 0.0f);
+        if constexpr (AHEAD) {
+            if (SUM && row < a.rows) x.store(row_of<T>(a, a.total, row, flat), a, lane);
+            if (first + stride < a.rows) sums.y = take(row + stride, x);
+            sums = team_sum<KIND>(sums, a, s_sums, team, turn);
+        } else {
+            sums.x = team_sum<KIND>(sums.x, a, s_sums, team, turn);
+        }
+        const float rstd = rsqrtf(sums.x * share + a.eps);
+        if (row < a.rows) {
+            const float2 scale = make_float2(rstd, rstd);
+            Elements y;
 #pragma unroll
-        for (int p = 0; p < kPairs; ++p) x.set(p, fma2(mul2(f[p], scale), weight[p], bias[p]));
-        if (valid) {
-            x.store(row_of<T>(a, a.out, row, flat), a, lane);
+            for (int p = 0; p < kPairs; ++p) y.set(p, fma2(mul2(f[p], scale), weight[p], bias[p]));
+            y.store(row_of<T>(a, a.out, row, flat), a, lane);
             if (lane == 0) {
                 a.mean[row] = mean;
                 a.rstd[row] = rstd;
             }
         }
+        if constexpr (AHEAD) mean = sums.y * share;
     }
     ring.finish();
 }
@@ -667,11 +687,12 @@ int plan_rows(const gsr_ctx *ctx, LayerArgs &a, bool backward)
     return teams;
 }
 
-template <typename T, int V, int N, int KIND, int THREADS, bool BACKWARD, bool SUM>
+template <typename T, int V, int N, int KIND, int THREADS, bool BACKWARD, bool SUM, bool AHEAD = false>
 cudaError_t launch_rows(gsr_ctx *ctx, LayerArgs &a, int teams, cudaStream_t stream)
 {
     constexpr int kArrays = (BACKWARD ? 2 : 1) + SUM;
-    constexpr size_t kRing = (size_t)kStages<T, V, N, kArrays, THREADS> * kArrays * N * THREADS * sizeof(T) * V;
+    constexpr int kInFlight = BACKWARD ? kStages<T, V, N, kArrays, THREADS> : kForwardStages<T, V, N, kArrays, THREADS, AHEAD>;
+    constexpr size_t kRing = (size_t)kInFlight * kArrays * N * THREADS * sizeof(T) * V;
     constexpr size_t kTeamSums = 2 * kTeamWarps * sizeof(float2), kShares = N * V * sizeof(float2);   // of a team, a thread
     const int threads = teams * a.team / kBlocksOf<KIND>;
     const size_t smem = std::max(kRing + (KIND != kInWarp ? teams * kTeamSums : 0), BACKWARD ? threads * kShares : 0);
@@ -679,7 +700,7 @@ cudaError_t launch_rows(gsr_ctx *ctx, LayerArgs &a, int teams, cudaStream_t stre
     if constexpr (BACKWARD)
         kernel = k_layer_norm_grad<T, V, N, KIND, THREADS, SUM>;
     else
-        kernel = k_layer_norm<T, V, N, KIND, THREADS, SUM>;
+        kernel = k_layer_norm<T, V, N, KIND, THREADS, SUM, AHEAD>;
     static OncePerDevice once;
     if (once.due(ctx)) {
         constexpr size_t kMost = std::max(kRing + (KIND != kInWarp ? THREADS / 64 * kTeamSums : 0), BACKWARD ? THREADS * kShares : 0);
@@ -695,12 +716,22 @@ template <typename T, int V, bool BACKWARD, bool SUM>
 cudaError_t dispatch_rows(gsr_ctx *ctx, LayerArgs &a, int teams, cudaStream_t stream)
 {
     constexpr int N = kElements / V;
-    if (a.team <= 32) return launch_rows<T, V, N, kInWarp, kRowThreads, BACKWARD, SUM>(ctx, a, teams, stream);
-    if (a.team <= kRowThreads) return launch_rows<T, V, N, kInBlock, kRowThreads, BACKWARD, SUM>(ctx, a, teams, stream);
-    if constexpr (BACKWARD)
+    if constexpr (BACKWARD) {
+        if (a.team <= 32) return launch_rows<T, V, N, kInWarp, kRowThreads, true, SUM>(ctx, a, teams, stream);
+        if (a.team <= kRowThreads) return launch_rows<T, V, N, kInBlock, kRowThreads, true, SUM>(ctx, a, teams, stream);
         return launch_rows<T, V, N, kInTwo, kRowThreads, true, SUM>(ctx, a, teams, stream);
-    else
+    } else {
+        // A team meets once a row (AHEAD) but where one or two to a block write totals (16,000 x 4,096 in
+        // bf16 behind a residual: 89 us with it, 79 to 85 without; three and more, 32,640 x 2,050 115 and
+        // 130, x 2,048 88 and 93; without a residual 47 and 60) or a thread has 64 registers (4,000 x
+        // 16,384: 79 and 67).
+        if (a.team <= 32) return launch_rows<T, V, N, kInWarp, kRowThreads, false, SUM, true>(ctx, a, teams, stream);
+        if (a.team <= kRowThreads / 3 || (!SUM && a.team <= kRowThreads))
+            return launch_rows<T, V, N, kInBlock, kRowThreads, false, SUM, true>(ctx, a, teams, stream);
+        if constexpr (SUM)
+            if (a.team <= kRowThreads) return launch_rows<T, V, N, kInBlock, kRowThreads, false, SUM>(ctx, a, teams, stream);
         return launch_rows<T, V, N, kInBlock, kLongThreads, false, SUM>(ctx, a, teams, stream);
+    }
 }
 
 template <typename T, int V, bool BACKWARD>
