@@ -377,18 +377,24 @@ struct Ring {
 
 // ---- forward ------------------------------------------------------------------------
 
-// AHEAD: a row's centred squares meet with the next one's sum, so that a team meets once a
-// row, and behind a residual, where the next row is in registers, two stages of the ring do.
-template <typename T, int V, int N, int A, int THREADS, bool AHEAD>
-constexpr int kForwardStages = std::min(kStages<T, V, N, A, THREADS>, AHEAD && A > 1 ? 2 : 3);
+// Ahead: a row's centred squares meet with the next one's sum, so that a team meets once a
+// row (in bf16, behind a residual: 21,845 x 3,000 in 83 us, with two meetings 106; 13,107 x
+// 5,000 in 96 and 123; x 4,096, x 8,192 and x 2,048 within 10% either way, as DRAM takes four
+// streams; without one 8,000 x 8,192 in 51 and 64).  Behind a residual, where the next row
+// is in registers, two stages of the ring do.  Not with 64 registers a thread (4,000 x
+// 16,384 without a residual: 79 us with it, 67 without).
+template <int THREADS>
+constexpr bool kAhead = THREADS == kRowThreads;
+template <typename T, int V, int N, int A, int THREADS>
+constexpr int kForwardStages = std::min(kStages<T, V, N, A, THREADS>, kAhead<THREADS> && A > 1 ? 2 : 3);
 
-template <typename T, int V, int N, int KIND, int THREADS, bool SUM, bool AHEAD>
+template <typename T, int V, int N, int KIND, int THREADS, bool SUM>
 __global__ void __launch_bounds__(THREADS, 1) k_layer_norm(const LayerArgs a)
 {
     grid_dependency_begin();
     extern __shared__ __align__(16) unsigned char s_bytes[];   // the teams' sums, then the ring
     using Elements = Part<T, V, N>;
-    constexpr int kPairs = Elements::kPairs, A = SUM ? 2 : 1, S = kForwardStages<T, V, N, A, THREADS, AHEAD>;
+    constexpr int kPairs = Elements::kPairs, A = SUM ? 2 : 1, S = kForwardStages<T, V, N, A, THREADS>;
     const bool flat = a.batch == 1 && a.heads == 1;
     const int teams = blockDim.x / a.team, team = threadIdx.x / a.team, lane = threadIdx.x % a.team;
     const uint32_t stride = gridDim.x * (uint32_t)teams;
@@ -417,7 +423,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_layer_norm(const LayerArgs a)
         if constexpr (SUM) {
 #pragma unroll
             for (int p = 0; p < kPairs; ++p) x.set(p, add2(x.get(p), in[A - 1].get(p)));
-            if (!AHEAD && from < a.rows) x.store(row_of<T>(a, a.total, from, flat), a, lane);
+            if (!kAhead<THREADS> && from < a.rows) x.store(row_of<T>(a, a.total, from, flat), a, lane);
         }
         float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -428,9 +434,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_layer_norm(const LayerArgs a)
     };
     Elements x;
     float mean;
-    if constexpr (AHEAD) mean = team_sum<KIND>(take(row, x), a, s_sums, team, turn) * share;
+    if constexpr (kAhead<THREADS>) mean = team_sum<KIND>(take(row, x), a, s_sums, team, turn) * share;
     for (; first < a.rows; first += stride, row += stride) {
-        if constexpr (!AHEAD) mean = team_sum<KIND>(take(row, x), a, s_sums, team, turn) * share;
+        if constexpr (!kAhead<THREADS>) mean = team_sum<KIND>(take(row, x), a, s_sums, team, turn) * share;
         const float2 minus = make_float2(-mean, -mean);
         float2 f[kPairs], sum = make_float2(0.0f, 0.0f);
         if (full) {
@@ -449,7 +455,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_layer_norm(const LayerArgs a)
             }
         }
         float2 sums = make_float2(sum.x + sum.y, 0.0f);
-        if constexpr (AHEAD) {
+        if constexpr (kAhead<THREADS>) {
             if (SUM && row < a.rows) x.store(row_of<T>(a, a.total, row, flat), a, lane);
             if (first + stride < a.rows) sums.y = take(row + stride, x);
             sums = team_sum<KIND>(sums, a, s_sums, team, turn);
@@ -468,7 +474,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_layer_norm(const LayerArgs a)
                 a.rstd[row] = rstd;
             }
         }
-        if constexpr (AHEAD) mean = sums.y * share;
+        if constexpr (kAhead<THREADS>) mean = sums.y * share;
     }
     ring.finish();
 }
@@ -687,11 +693,11 @@ int plan_rows(const gsr_ctx *ctx, LayerArgs &a, bool backward)
     return teams;
 }
 
-template <typename T, int V, int N, int KIND, int THREADS, bool BACKWARD, bool SUM, bool AHEAD = false>
+template <typename T, int V, int N, int KIND, int THREADS, bool BACKWARD, bool SUM>
 cudaError_t launch_rows(gsr_ctx *ctx, LayerArgs &a, int teams, cudaStream_t stream)
 {
     constexpr int kArrays = (BACKWARD ? 2 : 1) + SUM;
-    constexpr int kInFlight = BACKWARD ? kStages<T, V, N, kArrays, THREADS> : kForwardStages<T, V, N, kArrays, THREADS, AHEAD>;
+    constexpr int kInFlight = BACKWARD ? kStages<T, V, N, kArrays, THREADS> : kForwardStages<T, V, N, kArrays, THREADS>;
     constexpr size_t kRing = (size_t)kInFlight * kArrays * N * THREADS * sizeof(T) * V;
     constexpr size_t kTeamSums = 2 * kTeamWarps * sizeof(float2), kShares = N * V * sizeof(float2);   // of a team, a thread
     const int threads = teams * a.team / kBlocksOf<KIND>;
@@ -700,7 +706,7 @@ cudaError_t launch_rows(gsr_ctx *ctx, LayerArgs &a, int teams, cudaStream_t stre
     if constexpr (BACKWARD)
         kernel = k_layer_norm_grad<T, V, N, KIND, THREADS, SUM>;
     else
-        kernel = k_layer_norm<T, V, N, KIND, THREADS, SUM, AHEAD>;
+        kernel = k_layer_norm<T, V, N, KIND, THREADS, SUM>;
     static OncePerDevice once;
     if (once.due(ctx)) {
         constexpr size_t kMost = std::max(kRing + (KIND != kInWarp ? THREADS / 64 * kTeamSums : 0), BACKWARD ? THREADS * kShares : 0);
@@ -716,22 +722,12 @@ template <typename T, int V, bool BACKWARD, bool SUM>
 cudaError_t dispatch_rows(gsr_ctx *ctx, LayerArgs &a, int teams, cudaStream_t stream)
 {
     constexpr int N = kElements / V;
-    if constexpr (BACKWARD) {
-        if (a.team <= 32) return launch_rows<T, V, N, kInWarp, kRowThreads, true, SUM>(ctx, a, teams, stream);
-        if (a.team <= kRowThreads) return launch_rows<T, V, N, kInBlock, kRowThreads, true, SUM>(ctx, a, teams, stream);
+    if (a.team <= 32) return launch_rows<T, V, N, kInWarp, kRowThreads, BACKWARD, SUM>(ctx, a, teams, stream);
+    if (a.team <= kRowThreads) return launch_rows<T, V, N, kInBlock, kRowThreads, BACKWARD, SUM>(ctx, a, teams, stream);
+    if constexpr (BACKWARD)
         return launch_rows<T, V, N, kInTwo, kRowThreads, true, SUM>(ctx, a, teams, stream);
-    } else {
-        // A team meets once a row (AHEAD) but where one or two to a block write totals (16,000 x 4,096 in
-        // bf16 behind a residual: 89 us with it, 79 to 85 without; three and more, 32,640 x 2,050 115 and
-        // 130, x 2,048 88 and 93; without a residual 47 and 60) or a thread has 64 registers (4,000 x
-        // 16,384: 79 and 67).
-        if (a.team <= 32) return launch_rows<T, V, N, kInWarp, kRowThreads, false, SUM, true>(ctx, a, teams, stream);
-        if (a.team <= kRowThreads / 3 || (!SUM && a.team <= kRowThreads))
-            return launch_rows<T, V, N, kInBlock, kRowThreads, false, SUM, true>(ctx, a, teams, stream);
-        if constexpr (SUM)
-            if (a.team <= kRowThreads) return launch_rows<T, V, N, kInBlock, kRowThreads, false, SUM>(ctx, a, teams, stream);
+    else
         return launch_rows<T, V, N, kInBlock, kLongThreads, false, SUM>(ctx, a, teams, stream);
-    }
 }
 
 template <typename T, int V, bool BACKWARD>
