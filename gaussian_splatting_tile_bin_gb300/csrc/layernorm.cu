@@ -14,9 +14,9 @@
 // 39 and 67 us of 59.  Rows of 128 in f16 (80,000): 6.7 us of 6.0 and 12.3 us of 9.0, of
 // which the second kernel's launch is about 3.  Channels that are no multiple of 16 bytes
 // take accesses of 4 bytes or one element: 115 and 140 us at 2,050, 183 and 174 at 2,049,
-// bound by the number of accesses.  Above 8,192 channels a row takes 1,024 threads:
-// of a block forward, of two backward (4,000 x 16,384 in bf16: 67 us of 39 and 87 of 58, for
-// what sums cost between warps with one row at a time).
+// bound by the number of accesses.  Rows of
+// more than 8,192 channels are shared by two blocks (4,000 x 16,384 in bf16: 65 us of 39 and
+// 90 of 58, for what sums cost between warps with one row at a time).
 //
 // Numerics.  The variance is the mean of centred squares, from the registers; sums over
 // a row pass a thread's elements and a tree, in a fixed order, all in float.  The norm of a
@@ -29,7 +29,7 @@
 namespace gsr {
 namespace {
 
-constexpr int kRowThreads = 512, kLongThreads = 1024;   // of a block, one to an SM; of a long row's, forward
+constexpr int kRowThreads = 512;   // of a block, one to an SM
 // Elements of a thread: parameters, their gradients' sums and a row's inputs stay in
 // registers (8 in two blocks an SM: 80,000 x 128 in f16 in 10.2 and 24 us, 6.7 and 12.3 with
 // 16; 100,000 x 256 in bf16 in 23 us forward, 15).
@@ -150,11 +150,11 @@ __device__ __forceinline__ float2 parameter(const float *from, const LayerArgs &
     return f;
 }
 
-// Teams: lanes of a warp, a block's warps, or those of two blocks of a cluster: backward,
-// rows of more than 8,192 channels (4,000 x 16,384 in bf16 behind a residual in 100 us; a
-// block of 1,024 threads has 64 registers a thread, spills and took 231).  Forward a block
-// holds them: the two sums a row cost two blocks more than they gain (without a residual 82
-// us, 67 in one block; with one 105 and 121; 4,000 x 12,345 180 and 143).
+// Teams: lanes of a warp, a block's warps, or, for rows of more than 8,192 channels, those of
+// two blocks of a cluster (4,000 x 16,384 in bf16 behind a residual in 84 us forward and 99
+// backward, without one 65 and 90; a block of 1,024 threads, which has 64 registers a thread
+// and spills, took 118 and 231, 66 and 212.  It was faster forward for 5,000 x 9,000 without a
+// residual, 63 and 69, and for the single elements of 4,000 x 12,345, 141 and 166).
 constexpr int kInWarp = 0, kInBlock = 1, kInTwo = 2;
 template <int KIND>
 constexpr int kBlocksOf = KIND == kInTwo ? 2 : 1;   // a team's
@@ -216,7 +216,7 @@ __device__ __forceinline__ void team_barrier(int team, int threads)
 constexpr int kTeamWarps = 32;
 
 template <int KIND, typename F>
-__device__ __forceinline__ F team_sum(F v, const LayerArgs &a, float2 *s_sums, int team, uint32_t &turn, Beside *s_beside = nullptr)
+__device__ __forceinline__ F team_sum(F v, const LayerArgs &a, float2 *s_sums, int team, uint32_t &turn, Beside &s_beside)
 {
     if constexpr (KIND == kInWarp) {
 #pragma unroll
@@ -233,8 +233,8 @@ __device__ __forceinline__ F team_sum(F v, const LayerArgs &a, float2 *s_sums, i
         if constexpr (KIND == kInTwo) {
             // (Once a wait has run out the barriers are left as they are, here and, for want
             // of this block's sums, in the other block.)
-            const WaitGuard guard = {&s_beside->aborted, a.status};
-            uint64_t *full = &s_beside->full[copy];
+            const WaitGuard guard = {&s_beside.aborted, a.status};
+            uint64_t *full = &s_beside.full[copy];
             GSR_CANARY(38 + copy);
             if (threadIdx.x % 32 == 0 && !guard.stop()) {
                 if (threadIdx.x == 0) barrier_expect(smem_address(full), blockDim.x / 32 * sizeof(F));
@@ -263,14 +263,14 @@ __device__ __forceinline__ F team_sum(F v, const LayerArgs &a, float2 *s_sums, i
 
 // Clears the sums of the warps that a block's teams do not have.
 template <int KIND>
-__device__ __forceinline__ void start_sums(float2 *s_all, int teams, Beside *s_beside = nullptr)
+__device__ __forceinline__ void start_sums(float2 *s_all, int teams, Beside &s_beside)
 {
     if constexpr (KIND != kInWarp)
         for (int i = threadIdx.x; i < teams * 2 * kTeamWarps; i += blockDim.x) s_all[i] = make_float2(0.0f, 0.0f);
     if constexpr (KIND == kInTwo) {
         if (threadIdx.x == 0) {
-            s_beside->aborted = 0;
-            for (uint64_t &full : s_beside->full) barrier_init(smem_address(&full), 1);
+            s_beside.aborted = 0;
+            for (uint64_t &full : s_beside.full) barrier_init(smem_address(&full), 1);
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
         cluster_barrier();
@@ -281,7 +281,7 @@ __device__ __forceinline__ void start_sums(float2 *s_all, int teams, Beside *s_b
 
 // A block leaves once the other one writes to it no more.
 template <int KIND>
-__device__ __forceinline__ void end_sums(const LayerArgs &a, Beside &s_beside)
+__device__ __forceinline__ void end_sums(const LayerArgs &a, Beside s_beside)
 {
     if constexpr (KIND == kInTwo) {
         drain_if_aborted({&s_beside.aborted, a.status});
@@ -296,10 +296,10 @@ __device__ __forceinline__ void end_sums(const LayerArgs &a, Beside &s_beside)
 // waits for another): S stages of A arrays, three (two are slower without a residual, 44.1
 // to 41.8 us for 32,640 x 2,048 in bf16, four and eight no faster) or what 200 KB hold.  Single elements of
 // 2 bytes have no such copies and are read directly (S = 0).
-template <typename T, int V, int N, int A, int THREADS>
+template <typename T, int V, int N, int A>
 constexpr int kStages = sizeof(T) * V < 4
                             ? 0
-                            : std::min(3, 200 * 1024 / (THREADS * A * N * V * (int)sizeof(T)));
+                            : std::min(3, 200 * 1024 / (kRowThreads * A * N * V * (int)sizeof(T)));
 
 template <int BYTES>
 __device__ __forceinline__ void copy_async(void *to, const void *from)
@@ -311,17 +311,17 @@ __device__ __forceinline__ void copy_async(void *to, const void *from)
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(BYTES) : "memory");
 }
 
-template <typename T, int V, int N, int A, int S, int THREADS>
+template <typename T, int V, int N, int A, int S>
 struct Ring {
     using Access = Vec<T, V>;
-    static constexpr int kStage = A * N * THREADS;
+    static constexpr int kStage = A * N * kRowThreads;
     Access *mine;          // the thread's first slot
     const Rows &r0, &r1, &r2;
     bool flat;
     int at = 0;            // of the current stage's first slot
 
     __device__ __forceinline__ const Rows &array(int k) const { return k == 0 ? r0 : k == 1 ? r1 : r2; }
-    __device__ __forceinline__ Access *slot(int k, int i) const { return mine + at + (k * N + i) * THREADS; }
+    __device__ __forceinline__ Access *slot(int k, int i) const { return mine + at + (k * N + i) * kRowThreads; }
     // Starts the copies of a row into the current stage, if there is such a row.
     __device__ __forceinline__ void fetch(const LayerArgs &a, uint32_t row, int lane) const
     {
@@ -377,35 +377,34 @@ struct Ring {
 
 // ---- forward ------------------------------------------------------------------------
 
-// Ahead: a row's centred squares meet with the next one's sum, so that a team meets once a
-// row (in bf16, behind a residual: 21,845 x 3,000 in 83 us, with two meetings 106; 13,107 x
-// 5,000 in 96 and 123; x 4,096, x 8,192 and x 2,048 within 10% either way, as DRAM takes four
-// streams; without one 8,000 x 8,192 in 51 and 64).  Behind a residual, where the next row
-// is in registers, two stages of the ring do.  Not with 64 registers a thread (4,000 x
-// 16,384 without a residual: 79 us with it, 67 without).
-template <int THREADS>
-constexpr bool kAhead = THREADS == kRowThreads;
-template <typename T, int V, int N, int A, int THREADS>
-constexpr int kForwardStages = std::min(kStages<T, V, N, A, THREADS>, kAhead<THREADS> && A > 1 ? 2 : 3);
+// A row's centred squares meet with the next one's sum, so that a team meets once a row (in
+// bf16, behind a residual: 21,845 x 3,000 in 83 us, with two meetings 106; 13,107 x 5,000 in
+// 96 and 123; x 4,096, x 8,192 and x 2,048 within 10% either way, as DRAM takes four streams;
+// without one 8,000 x 8,192 in 51 and 64).  Behind a residual, where the next row is in
+// registers, two stages of the ring do.
+template <typename T, int V, int N, int A>
+constexpr int kForwardStages = std::min(kStages<T, V, N, A>, A > 1 ? 2 : 3);
 
-template <typename T, int V, int N, int KIND, int THREADS, bool SUM>
-__global__ void __launch_bounds__(THREADS, 1) k_layer_norm(const LayerArgs a)
+template <typename T, int V, int N, int KIND, bool SUM>
+__global__ void __launch_bounds__(kRowThreads, 1) k_layer_norm(const LayerArgs a)
 {
     grid_dependency_begin();
     extern __shared__ __align__(16) unsigned char s_bytes[];   // the teams' sums, then the ring
+    __shared__ Beside s_beside;
     using Elements = Part<T, V, N>;
-    constexpr int kPairs = Elements::kPairs, A = SUM ? 2 : 1, S = kForwardStages<T, V, N, A, THREADS>;
+    constexpr int kPairs = Elements::kPairs, A = SUM ? 2 : 1, S = kForwardStages<T, V, N, A>, X = kBlocksOf<KIND>;
     const bool flat = a.batch == 1 && a.heads == 1;
-    const int teams = blockDim.x / a.team, team = threadIdx.x / a.team, lane = threadIdx.x % a.team;
-    const uint32_t stride = gridDim.x * (uint32_t)teams;
+    const int teams = X * blockDim.x / a.team, team = threadIdx.x / a.team;
+    const int lane = KIND == kInTwo ? blockIdx.x % 2 * blockDim.x + threadIdx.x : threadIdx.x % a.team;
+    const uint32_t block = blockIdx.x / X, stride = gridDim.x / X * (uint32_t)teams;
     float2 *s_sums = (float2 *)s_bytes + team * 2 * kTeamWarps;
-    Ring<T, V, N, A, S, THREADS> ring = {(Vec<T, V> *)(s_bytes + (KIND != kInWarp ? teams * 2 * kTeamWarps * sizeof(float2) : 0)) + threadIdx.x,
+    Ring<T, V, N, A, S> ring = {(Vec<T, V> *)(s_bytes + (KIND != kInWarp ? teams * 2 * kTeamWarps * sizeof(float2) : 0)) + threadIdx.x,
                                          a.x, a.residual, a.residual, flat};
 
     // (Below 2^31 rows, steps ahead of them below 2^32.  All teams take the same number of steps.)
-    uint32_t row = blockIdx.x * teams + team, first = blockIdx.x * teams;
+    uint32_t row = block * teams + team, first = block * teams;
     ring.start(a, row, stride, lane);
-    start_sums<KIND>((float2 *)s_bytes, teams);
+    start_sums<KIND>((float2 *)s_bytes, teams, s_beside);
     float2 weight[kPairs], bias[kPairs];
 #pragma unroll
     for (int p = 0; p < kPairs; ++p) {
@@ -415,7 +414,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_layer_norm(const LayerArgs a)
     const float share = 1.0f / (float)a.channels;
     const bool full = a.channels == a.team * V * N;
     uint32_t turn = 0;
-    // A row's total (ahead, stored where its squares are taken) and a thread's share of its sum.
+    // A row's total (stored where its squares are taken) and a thread's share of its sum.
     auto take = [&](uint32_t from, Elements &x) {
         Elements in[A];
         ring.take(a, from, lane, in);
@@ -423,7 +422,6 @@ __global__ void __launch_bounds__(THREADS, 1) k_layer_norm(const LayerArgs a)
         if constexpr (SUM) {
 #pragma unroll
             for (int p = 0; p < kPairs; ++p) x.set(p, add2(x.get(p), in[A - 1].get(p)));
-            if (!kAhead<THREADS> && from < a.rows) x.store(row_of<T>(a, a.total, from, flat), a, lane);
         }
         float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -433,10 +431,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_layer_norm(const LayerArgs a)
         return sum.x + sum.y;
     };
     Elements x;
-    float mean;
-    if constexpr (kAhead<THREADS>) mean = team_sum<KIND>(take(row, x), a, s_sums, team, turn) * share;
+    float mean = team_sum<KIND>(take(row, x), a, s_sums, team, turn, s_beside) * share;
     for (; first < a.rows; first += stride, row += stride) {
-        if constexpr (!kAhead<THREADS>) mean = team_sum<KIND>(take(row, x), a, s_sums, team, turn) * share;
         const float2 minus = make_float2(-mean, -mean);
         float2 f[kPairs], sum = make_float2(0.0f, 0.0f);
         if (full) {
@@ -455,13 +451,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_layer_norm(const LayerArgs a)
             }
         }
         float2 sums = make_float2(sum.x + sum.y, 0.0f);
-        if constexpr (kAhead<THREADS>) {
-            if (SUM && row < a.rows) x.store(row_of<T>(a, a.total, row, flat), a, lane);
-            if (first + stride < a.rows) sums.y = take(row + stride, x);
-            sums = team_sum<KIND>(sums, a, s_sums, team, turn);
-        } else {
-            sums.x = team_sum<KIND>(sums.x, a, s_sums, team, turn);
-        }
+        if (SUM && row < a.rows) x.store(row_of<T>(a, a.total, row, flat), a, lane);
+        if (first + stride < a.rows) sums.y = take(row + stride, x);
+        sums = team_sum<KIND>(sums, a, s_sums, team, turn, s_beside);
         const float rstd = rsqrtf(sums.x * share + a.eps);
         if (row < a.rows) {
             const float2 scale = make_float2(rstd, rstd);
@@ -474,15 +466,16 @@ __global__ void __launch_bounds__(THREADS, 1) k_layer_norm(const LayerArgs a)
                 a.rstd[row] = rstd;
             }
         }
-        if constexpr (kAhead<THREADS>) mean = sums.y * share;
+        mean = sums.y * share;
     }
     ring.finish();
+    end_sums<KIND>(a, s_beside);
 }
 
 // ---- backward -----------------------------------------------------------------------
 
-template <typename T, int V, int N, int KIND, int THREADS, bool SUM>
-__global__ void __launch_bounds__(THREADS, 1) k_layer_norm_grad(const LayerArgs a)
+template <typename T, int V, int N, int KIND, bool SUM>
+__global__ void __launch_bounds__(kRowThreads, 1) k_layer_norm_grad(const LayerArgs a)
 {
     grid_dependency_begin();
     // The teams' sums, then the ring; at the end the block's shares of dw and db.
@@ -490,19 +483,19 @@ __global__ void __launch_bounds__(THREADS, 1) k_layer_norm_grad(const LayerArgs 
     __shared__ Beside s_beside;
     float2 *s_work = (float2 *)s_bytes;
     using Elements = Part<T, V, N>;
-    constexpr int kPairs = Elements::kPairs, A = SUM ? 3 : 2, S = kStages<T, V, N, A, THREADS>, X = kBlocksOf<KIND>;
+    constexpr int kPairs = Elements::kPairs, A = SUM ? 3 : 2, S = kStages<T, V, N, A>, X = kBlocksOf<KIND>;
     const bool flat = a.batch == 1 && a.heads == 1;
     const int teams = X * blockDim.x / a.team, team = threadIdx.x / a.team;
     const int lane = KIND == kInTwo ? blockIdx.x % 2 * blockDim.x + threadIdx.x : threadIdx.x % a.team;
     const uint32_t block = blockIdx.x / X, stride = gridDim.x / X * (uint32_t)teams;
     float2 *s_sums = s_work + team * 2 * kTeamWarps;
-    Ring<T, V, N, A, S, THREADS> ring = {(Vec<T, V> *)(s_bytes + (KIND != kInWarp ? teams * 2 * kTeamWarps * sizeof(float2) : 0)) + threadIdx.x,
+    Ring<T, V, N, A, S> ring = {(Vec<T, V> *)(s_bytes + (KIND != kInWarp ? teams * 2 * kTeamWarps * sizeof(float2) : 0)) + threadIdx.x,
                                          a.total, a.x, a.residual, flat};
 
     // (As in the forward.)
     uint32_t row = block * teams + team, first = block * teams;
     ring.start(a, row, stride, lane);
-    start_sums<KIND>((float2 *)s_bytes, teams, &s_beside);
+    start_sums<KIND>((float2 *)s_bytes, teams, s_beside);
     float2 weight[kPairs], dw[kPairs], db[kPairs];
 #pragma unroll
     for (int p = 0; p < kPairs; ++p) {
@@ -538,7 +531,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_layer_norm_grad(const LayerArgs 
         }
         ring.fetch(a, row + S * stride, lane);
         ring.advance();
-        const float2 m = team_sum<KIND>(make_float2(s1.x + s1.y, s2.x + s2.y), a, s_sums, team, turn, &s_beside);
+        const float2 m = team_sum<KIND>(make_float2(s1.x + s1.y, s2.x + s2.y), a, s_sums, team, turn, s_beside);
         const float2 m1 = make_float2(-m.x * share, -m.x * share), m2 = make_float2(-m.y * share, -m.y * share);
         if (row >= a.rows) continue;
 #pragma unroll
@@ -678,10 +671,10 @@ int power_of_two(int n)
 // Divides a row over a team, kElements of it to a thread, and the rows over blocks of
 // teams; returns a block's teams.  Few rows are spread over the SMs rather than over the
 // teams of one block.
-int plan_rows(const gsr_ctx *ctx, LayerArgs &a, bool backward)
+int plan_rows(const gsr_ctx *ctx, LayerArgs &a)
 {
     const int threads = (a.channels + kElements - 1) / kElements;
-    const bool two = backward && threads > kRowThreads;
+    const bool two = threads > kRowThreads;
     const int whole = two ? 64 : 32;
     a.team = threads <= 32 ? power_of_two(threads) : (threads + whole - 1) / whole * whole;
     const uint64_t spread = ((uint64_t)a.rows + ctx->num_sms - 1) / ctx->num_sms;
@@ -693,23 +686,33 @@ int plan_rows(const gsr_ctx *ctx, LayerArgs &a, bool backward)
     return teams;
 }
 
-template <typename T, int V, int N, int KIND, int THREADS, bool BACKWARD, bool SUM>
+// The word that tells of waits between two blocks of a row, where there are any.
+int status_of(gsr_ctx *ctx, LayerArgs &a, cudaStream_t stream)
+{
+    if (a.team <= kRowThreads) return GSR_OK;
+    void *none = nullptr;
+    const int rc = Workspace(ctx, stream).take(0, &none);
+    a.status = ctx->status_dev;
+    return rc;
+}
+
+template <typename T, int V, int N, int KIND, bool BACKWARD, bool SUM>
 cudaError_t launch_rows(gsr_ctx *ctx, LayerArgs &a, int teams, cudaStream_t stream)
 {
     constexpr int kArrays = (BACKWARD ? 2 : 1) + SUM;
-    constexpr int kInFlight = BACKWARD ? kStages<T, V, N, kArrays, THREADS> : kForwardStages<T, V, N, kArrays, THREADS>;
-    constexpr size_t kRing = (size_t)kInFlight * kArrays * N * THREADS * sizeof(T) * V;
+    constexpr int kInFlight = BACKWARD ? kStages<T, V, N, kArrays> : kForwardStages<T, V, N, kArrays>;
+    constexpr size_t kRing = (size_t)kInFlight * kArrays * N * kRowThreads * sizeof(T) * V;
     constexpr size_t kTeamSums = 2 * kTeamWarps * sizeof(float2), kShares = N * V * sizeof(float2);   // of a team, a thread
     const int threads = teams * a.team / kBlocksOf<KIND>;
     const size_t smem = std::max(kRing + (KIND != kInWarp ? teams * kTeamSums : 0), BACKWARD ? threads * kShares : 0);
     void (*kernel)(LayerArgs);
     if constexpr (BACKWARD)
-        kernel = k_layer_norm_grad<T, V, N, KIND, THREADS, SUM>;
+        kernel = k_layer_norm_grad<T, V, N, KIND, SUM>;
     else
-        kernel = k_layer_norm<T, V, N, KIND, THREADS, SUM>;
+        kernel = k_layer_norm<T, V, N, KIND, SUM>;
     static OncePerDevice once;
     if (once.due(ctx)) {
-        constexpr size_t kMost = std::max(kRing + (KIND != kInWarp ? THREADS / 64 * kTeamSums : 0), BACKWARD ? THREADS * kShares : 0);
+        constexpr size_t kMost = std::max(kRing + (KIND != kInWarp ? kRowThreads / 64 * kTeamSums : 0), BACKWARD ? kRowThreads * kShares : 0);
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
         if (e != cudaSuccess) return e;
         once.done(ctx);
@@ -722,12 +725,9 @@ template <typename T, int V, bool BACKWARD, bool SUM>
 cudaError_t dispatch_rows(gsr_ctx *ctx, LayerArgs &a, int teams, cudaStream_t stream)
 {
     constexpr int N = kElements / V;
-    if (a.team <= 32) return launch_rows<T, V, N, kInWarp, kRowThreads, BACKWARD, SUM>(ctx, a, teams, stream);
-    if (a.team <= kRowThreads) return launch_rows<T, V, N, kInBlock, kRowThreads, BACKWARD, SUM>(ctx, a, teams, stream);
-    if constexpr (BACKWARD)
-        return launch_rows<T, V, N, kInTwo, kRowThreads, true, SUM>(ctx, a, teams, stream);
-    else
-        return launch_rows<T, V, N, kInBlock, kLongThreads, false, SUM>(ctx, a, teams, stream);
+    if (a.team <= 32) return launch_rows<T, V, N, kInWarp, BACKWARD, SUM>(ctx, a, teams, stream);
+    if (a.team <= kRowThreads) return launch_rows<T, V, N, kInBlock, BACKWARD, SUM>(ctx, a, teams, stream);
+    return launch_rows<T, V, N, kInTwo, BACKWARD, SUM>(ctx, a, teams, stream);
 }
 
 template <typename T, int V, bool BACKWARD>
@@ -772,9 +772,11 @@ int layer_norm_forward(gsr_ctx *ctx, const gsr_layer_norm &d, const gsr_heads &x
     a.mean = mean;
     a.rstd = rstd;
     collapse(a);
+    const int teams = plan_rows(ctx, a);
+    if (int rc = status_of(ctx, a, stream)) return rc;
     const cudaError_t e = with_access(d.dtype, a, [&](auto t, auto v) {
         constexpr int V = decltype(v)::value;
-        return dispatch_sum<decltype(t), V, false>(ctx, a, plan_rows(ctx, a, false), stream);
+        return dispatch_sum<decltype(t), V, false>(ctx, a, teams, stream);
     });
     return cuda_check(ctx, e, "layer norm forward");
 }
@@ -802,26 +804,23 @@ int layer_norm_backward(gsr_ctx *ctx, const gsr_layer_norm &d, const gsr_heads &
     a.dweight = dweight;
     a.dbias = dbias;
     collapse(a);
+    const int teams = plan_rows(ctx, a);
+    if (int rc = status_of(ctx, a, stream)) return rc;
     Workspace workspace(ctx, stream);
-    int rc = GSR_OK;
+    if (dweight || dbias) {
+        void *work = nullptr;
+        if (int rc = workspace.take((size_t)a.blocks * d.channels * sizeof(float2), &work)) return rc;
+        a.partial = (float2 *)work;
+    }
     const cudaError_t e = with_access(d.dtype, a, [&](auto t, auto v) {
         using T = decltype(t);
         constexpr int V = decltype(v)::value;
-        const int teams = plan_rows(ctx, a, true);
-        if (dweight || dbias || a.team > kRowThreads) {   // (without shares: for the status word of waits)
-            void *work = nullptr;
-            rc = workspace.take(dweight || dbias ? (size_t)a.blocks * d.channels * sizeof(float2) : 0, &work);
-            if (rc != GSR_OK) return cudaSuccess;
-            if (dweight || dbias) a.partial = (float2 *)work;
-            a.status = ctx->status_dev;
-        }
         cudaError_t e = dispatch_sum<T, V, true>(ctx, a, teams, stream);
         if (e == cudaSuccess && a.partial)
             e = launch_kernel(ctx, k_layer_norm_params, dim3((unsigned)((a.channels + 31) / 32)), 32 * kParamSlices,
                               stream, a);
         return e;
     });
-    if (rc != GSR_OK) return rc;
     if (int bad = cuda_check(ctx, e, "layer norm backward")) return bad;
     return workspace.done();
 }

@@ -103,20 +103,24 @@ def test_few_tokens_and_forward_norms_take_no_workspace(lib, ctx):  # noqa: F811
 
 
 def test_rows_of_two_blocks_have_a_status_word(lib, ctx):  # noqa: F811
-    """Backward, rows that two blocks share wait for each other: without gradients of parameters
+    """Rows that two blocks share wait for each other: forward, and without gradients of parameters,
     too the word that reports a wait is made, before a capture."""
     from gaussian_splatting_tile_bin_gb300 import _abi
     x = _rows(40, 9000)
     call = lambda: lib.gsr_layer_norm_backward(ctx, _abi.LAYER_NORM.pack(1, 2, 40, 1, 9000, 1e-5), x, x, AT, AT, AT, x, x,  # noqa: E731
                                                None, None, ONE)
-    assert norm(lib, ctx, ONE, 9000) == OK
+    assert norm(lib, ctx, ONE, 256) == OK
     launches = lib.fake_launches()
     lib.fake_begin_capture(ONE)
-    assert call() == CUDA and b"capture" in lib.gsr_last_error(ctx) and lib.fake_launches() == launches
+    for use in (call, lambda: norm(lib, ctx, ONE, 9000)):
+        assert use() == CUDA and b"capture" in lib.gsr_last_error(ctx) and lib.fake_launches() == launches
     lib.fake_end_capture(ONE)
-    assert call() == OK and lib.fake_launches() == launches + 1
+    assert call() == OK and norm(lib, ctx, ONE, 9000) == OK and lib.fake_launches() == launches + 2
+    lib.fake_begin_capture(ONE)
+    assert call() == OK and norm(lib, ctx, ONE, 9000) == OK
+    lib.fake_end_capture(ONE)
     lib.fake_set_status()
-    assert call() == CUDA and b"gave up waiting" in lib.gsr_last_error(ctx)
+    assert norm(lib, ctx, ONE, 9000) == CUDA and b"gave up waiting" in lib.gsr_last_error(ctx)
     for stream in (ONE, TWO, THREE, ONE):
         assert norm(lib, ctx, stream, 9000, backward=True) == OK
     assert lib.fake_conflicts() == 0
