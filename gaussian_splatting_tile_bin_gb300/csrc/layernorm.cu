@@ -5,8 +5,8 @@
 // and with g = dout w
 //   dx = rstd (g - mean(g) - xh mean(g xh)) + dtotal,  dw = sum dout xh,  db = sum dout.
 //
-// Bound by HBM.  A row stays in the registers of its team (lanes of a warp, a warp
-// or several) between the statistics and the result, so every array moves once; a block
+// Bound by HBM.  A row stays in the registers of its team (lanes of a warp, a warp,
+// several or two blocks) between the statistics and the result, so every array moves once; a block
 // walks rows, and its threads' copies run three rows ahead, so that the parameters and,
 // backward, the channels' shares of dw and db stay in registers too.  A second kernel adds
 // the blocks' shares in order.  32,640 x 2,048 in bf16 behind a residual (four arrays of 134
@@ -14,9 +14,9 @@
 // 39 and 67 us of 59.  Rows of 128 in f16 (80,000): 6.7 us of 6.0 and 12.3 us of 9.0, of
 // which the second kernel's launch is about 3.  Channels that are no multiple of 16 bytes
 // take accesses of 4 bytes or one element: 115 and 140 us at 2,050, 183 and 174 at 2,049,
-// bound by the number of accesses.  Rows of
-// more than 8,192 channels are shared by two blocks (4,000 x 16,384 in bf16: 65 us of 39 and
-// 90 of 58, for what sums cost between warps with one row at a time).
+// bound by the number of accesses.  Rows of more than 8,192 channels are shared by two blocks
+// (4,000 x 16,384 in bf16: 65 us of 39 and 90 of 58, for what sums cost between warps with one
+// row at a time).
 //
 // Numerics.  The variance is the mean of centred squares, from the registers; sums over
 // a row pass a thread's elements and a tree, in a fixed order, all in float.  The norm of a
@@ -398,8 +398,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) k_layer_norm(const LayerArgs a
     const int lane = KIND == kInTwo ? blockIdx.x % 2 * blockDim.x + threadIdx.x : threadIdx.x % a.team;
     const uint32_t block = blockIdx.x / X, stride = gridDim.x / X * (uint32_t)teams;
     float2 *s_sums = (float2 *)s_bytes + team * 2 * kTeamWarps;
-    Ring<T, V, N, A, S> ring = {(Vec<T, V> *)(s_bytes + (KIND != kInWarp ? teams * 2 * kTeamWarps * sizeof(float2) : 0)) + threadIdx.x,
-                                         a.x, a.residual, a.residual, flat};
+    const size_t sum_bytes = KIND != kInWarp ? teams * 2 * kTeamWarps * sizeof(float2) : 0;
+    Ring<T, V, N, A, S> ring = {(Vec<T, V> *)(s_bytes + sum_bytes) + threadIdx.x, a.x, a.residual, a.residual, flat};
 
     // (Below 2^31 rows, steps ahead of them below 2^32.  All teams take the same number of steps.)
     uint32_t row = block * teams + team, first = block * teams;
@@ -489,8 +489,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) k_layer_norm_grad(const LayerA
     const int lane = KIND == kInTwo ? blockIdx.x % 2 * blockDim.x + threadIdx.x : threadIdx.x % a.team;
     const uint32_t block = blockIdx.x / X, stride = gridDim.x / X * (uint32_t)teams;
     float2 *s_sums = s_work + team * 2 * kTeamWarps;
-    Ring<T, V, N, A, S> ring = {(Vec<T, V> *)(s_bytes + (KIND != kInWarp ? teams * 2 * kTeamWarps * sizeof(float2) : 0)) + threadIdx.x,
-                                         a.total, a.x, a.residual, flat};
+    const size_t sum_bytes = KIND != kInWarp ? teams * 2 * kTeamWarps * sizeof(float2) : 0;
+    Ring<T, V, N, A, S> ring = {(Vec<T, V> *)(s_bytes + sum_bytes) + threadIdx.x, a.total, a.x, a.residual, flat};
 
     // (As in the forward.)
     uint32_t row = block * teams + team, first = block * teams;
@@ -712,7 +712,8 @@ cudaError_t launch_rows(gsr_ctx *ctx, LayerArgs &a, int teams, cudaStream_t stre
         kernel = k_layer_norm<T, V, N, KIND, SUM>;
     static OncePerDevice once;
     if (once.due(ctx)) {
-        constexpr size_t kMost = std::max(kRing + (KIND != kInWarp ? kRowThreads / 64 * kTeamSums : 0), BACKWARD ? kRowThreads * kShares : 0);
+        constexpr size_t kMost = std::max(kRing + (KIND != kInWarp ? kRowThreads / 64 * kTeamSums : 0),
+                                          BACKWARD ? kRowThreads * kShares : 0);
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
         if (e != cudaSuccess) return e;
         once.done(ctx);

@@ -572,7 +572,8 @@ int gsr_cross_attention_backward(gsr_ctx *ctx, const gsr_attention *desc, const 
  * All arrays aligned to their element.  Those aligned to 16 bytes, with strides
  * and channels multiples of 16 bytes, take a vectorised path.  Statistics are taken
  * in float, the variance from centred values, in a fixed order: the same bits on
- * every run.
+ * every run.  Above 8,192 channels a context's first call is made before a capture,
+ * as one that takes a workspace.
  * Errors: GSR_ERR_INVALID_ARG (null or misaligned arrays; negative sizes; channels
  * outside [1, GSR_MAX_NORM_CHANNELS]; heads above GSR_MAX_HEADS, batch * tokens above
  * GSR_MAX_TOKENS, 2^31 rows or more; out or total with a stride of 0 over more than
