@@ -331,6 +331,10 @@ __device__ __forceinline__ void fetch_tiles(const RecurrenceArgs &a, const Maps 
     }
 }
 
+// Whether a wait of the block has run out, as one answer for the whole warp: lanes that
+// each looked for themselves might go different ways, and warp-wide instructions follow.
+__device__ __forceinline__ bool warp_stop(const WaitGuard &guard) { return __any_sync(~0u, guard.stop()); }
+
 // Calls f(tile, j) for the block's tiles in turn, j of which with tokens came before, and
 // leaves their stages.  (Once a wait has run out there may be no tile where one is looked
 // for.)
@@ -341,7 +345,7 @@ __device__ __forceinline__ void each_tile(Shared<V, S, BACKWARD> &s, const WaitG
     for (uint32_t i = 0;; ++i) {
         const uint32_t stage = i % S;
         barrier_wait_warp(smem_address(&s.known[stage]), i / S & 1, guard);
-        if (guard.stop() || s.last[stage]) return;
+        if (warp_stop(guard) || s.last[stage]) return;
         const Tile t = s.tiles[stage];
         warp_arrive(s.empty[stage]);
         f(t, j);
@@ -557,7 +561,10 @@ __device__ __forceinline__ void clear_tokens(const Tokens &t, int b, int from, i
     Raw<T, V> zero;
     clear(zero);
     T *p = (T *)t.data + b * t.batch + (int64_t)from * t.token + c;
-    for (int k = from; k < to; ++k, p += t.token) *(Raw<T, V> *)p = zero;
+    for (int k = from; k < to; ++k, p += t.token) {
+        GSR_CANARY_LANES(50);
+        *(Raw<T, V> *)p = zero;
+    }
 }
 
 // A staged word's elements.
@@ -937,8 +944,12 @@ struct Backward {
                 u[i] = mul(value(keep, i), add(h, minus(x)));
                 h = add(x, u[i]);
                 if constexpr (GATE)
-                    if (some && i < at.count) dg.store(i, mul(value(slope, i), h));
+                    if (some && i < at.count) {
+                        GSR_CANARY_LANES(42 + i);
+                        dg.store(i, mul(value(slope, i), h));
+                    }
             }
+            __syncwarp();   // (lanes behind the channels have not stored)
             tmem_wait_load();
             pin16(rest);
             pin16(into);
@@ -983,9 +994,12 @@ __device__ __forceinline__ void work_tiles(const RecurrenceArgs &a, Shared<V, S,
     for (uint32_t i = 0;; ++i) {
         const uint32_t stage = i % S;
         barrier_wait_warp(smem_address(&s.known[stage]), i / S & 1, guard);
-        if (guard.stop() || s.last[stage]) break;
+        if (warp_stop(guard) || s.last[stage]) break;
         const Tile t = s.tiles[stage];
-        if (t.length < a.tokens) Work::clear_rest(a, t);
+        if (t.length < a.tokens) {
+            Work::clear_rest(a, t);
+            __syncwarp();   // (lanes behind the channels have nothing to clear)
+        }
         const bool some = t.index < t.count;
         if (some) {
             if (COPY) barrier_wait_warp(smem_address(&s.full[stage]), i / S & 1, guard);
@@ -999,7 +1013,7 @@ __device__ __forceinline__ void work_tiles(const RecurrenceArgs &a, Shared<V, S,
         before = t;
         if (some) ++j;
     }
-    if (open && !guard.stop()) finish();
+    if (open && !warp_stop(guard)) finish();
 }
 
 // COPY: tiles come through the ring of stages; otherwise the runs' warps read them.
@@ -1052,7 +1066,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     drain_if_aborted(guard);
     tmem_fence_before();
     __syncthreads();
-    if (warp == kComposeWarp) tmem_free(s.columns, kColumns);
+    if (warp == kComposeWarp) {
+        __syncwarp();
+        tmem_free(s.columns, kColumns);
+    }
 }
 
 // ---- few tokens --------------------------------------------------------------------------
