@@ -27,21 +27,23 @@
 // the tile's and hands each run the map of those in front of it.  A working warp composes
 // its run of the next tile before it finishes the one of the last: its gates and inputs
 // wait in tensor memory (256 columns a block) meanwhile, so that the time that a map takes
-// along the chain is spent on work.
+// along the chain is spent on work.  The forward's output gates, which only a run's end uses,
+// wait in shared memory, where a second ring of copies puts them.
 //
 // What bounds it, and what the parts are worth (32,640 x 2,048 in bf16 with a gate: four
-// arrays of 134 MB forward, 79 us at the copy rate, and seven backward, 138 us): 95 and 168
+// arrays of 134 MB forward, 79 us at the copy rate, and seven backward, 138 us): 90 and 167
 // us, each byte moved once.  Without any wait along the chain the kernels would take 86 and
 // 145 us, bound by HBM; the rest is what a map and a state take through L2.  Tiles without a
 // ring and a chain of their own took 170 and 323 us, with them 136 and 299, with runs that
 // wait in tensor memory 115 and 213; a chain whose missing words are looked at together 102
-// and 188, and groups that publish their map before their state 95 and 168.
+// and 188, and groups that publish their map before their state 95 and 168; the forward's runs
+// that keep a and (1 - a) x, and read their gates from shared memory, 90.
 //
-// Numerics.  With e = exp(-|f|), the larger of a and 1 - a is 1 / (1 + e) and the smaller
-// e / (1 + e): neither is taken as a difference, so gates near 0 and 1 lose nothing.  (The
-// forward's run takes a as 1 minus the 1 - a that it has kept, half an ulp of 1 off; the
-// backward keeps both, as dL/df is their product.)  States, maps and gradients along the
-// chain are floats; results are rounded once.  exp and reciprocal are the hardware's (2 ulp).
+// Numerics.  With e = exp(-|f|), the smaller of a and 1 - a is e / (1 + e), and the larger 1
+// minus it, at least 1/2: both are good to a few ulp of themselves, however far apart they are.
+// The forward's steps are a h + (1 - a) x with both, wherever they are taken, so that what a
+// gate shuts out leaves the rest its bits.  States, maps and gradients along the chain are
+// floats; results are rounded once.  exp and reciprocal are the hardware's (2 ulp).
 #include <initializer_list>
 #include <type_traits>
 
@@ -267,6 +269,7 @@ struct Shared {
     Tile tiles[S];
     uint32_t last[S];                   // no tile: the tickets are at an end
     uint64_t known[S], full[S], empty[S];
+    uint64_t gate_full[2], gate_empty[2];   // the forward's output gates
     uint64_t runs_ready[2], tile_ready[2], state_ready[2];
     uint32_t aborted, columns;
 };
@@ -287,6 +290,16 @@ struct Maps {
     CUtensorMap x, forget, gate, dout;
 };
 
+// Arrays of a tile that come through the stages.
+template <bool GATE, bool BACKWARD>
+constexpr int kStaged = BACKWARD ? 3 + (GATE ? 1 : 0) : 2;
+
+// The first token in memory of a tile (below 0 for the last one of a reversed item, perhaps).
+__device__ __forceinline__ int first_token(const RecurrenceArgs &a, const Tile &t, int tile_tokens)
+{
+    return a.reverse ? t.length - (t.index + 1) * tile_tokens : t.index * tile_tokens;
+}
+
 __device__ __forceinline__ void copy_tokens(uint32_t to, const CUtensorMap *map, uint32_t bar, int channel, int token, int item)
 {
     asm volatile(
@@ -295,13 +308,27 @@ __device__ __forceinline__ void copy_tokens(uint32_t to, const CUtensorMap *map,
         : "memory");
 }
 
-// One lane: tickets in turn, and the copies of their tiles.
+// One lane: tickets in turn, and the copies of their tiles.  The forward's output gates, which
+// are used when a run ends, have places of their own, and follow the next tile's inputs.
 template <int V, int S, bool GATE, bool COPY, bool BACKWARD>
 __device__ __forceinline__ void fetch_tiles(const RecurrenceArgs &a, const Maps &maps, Shared<V, S, BACKWARD> &s, uint32_t stages,
                                             const WaitGuard &guard)
 {
     constexpr int kTokens = BACKWARD ? kGradTile : kTile, kBytes = kTokens * kRowBytes;
-    constexpr int kArrays = 2 + (GATE ? 1 : 0) + (BACKWARD ? 1 : 0);
+    constexpr int kArrays = kStaged<GATE, BACKWARD>;
+    Tile gated = {};             // whose gates are to come
+    uint32_t gates = 0;
+    auto copy_gates = [&] {
+        if (gated.index >= gated.count) return;
+        const uint32_t full = smem_address(&s.gate_full[gates & 1]);
+        barrier_wait(smem_address(&s.gate_empty[gates & 1]), gates >> 1 & 1 ^ 1, guard);
+        GSR_CANARY(23);
+        if (guard.stop()) return;
+        barrier_expect(full, kBytes);
+        copy_tokens(stages + (S * kArrays + (gates & 1)) * kBytes, &maps.gate, full, gated.slab * 32 * V,
+                    first_token(a, gated, kTokens), a.gate.batch ? gated.b : 0);
+        ++gates;
+    };
     for (uint32_t i = 0;; ++i) {
         const uint32_t n = a.ticket ? atomicAdd(a.ticket, 1u) + 1u : blockIdx.x + i * gridDim.x;
         const uint32_t stage = i % S;
@@ -312,22 +339,25 @@ __device__ __forceinline__ void fetch_tiles(const RecurrenceArgs &a, const Maps 
         s.tiles[stage] = t;
         s.last[stage] = last;
         barrier_arrive(smem_address(&s.known[stage]));
-        if (last) return;
         if constexpr (COPY) {
             const uint32_t full = smem_address(&s.full[stage]);
-            if (t.index >= t.count) {
-                barrier_arrive(full);
-                continue;
-            }
-            barrier_expect(full, kArrays * kBytes);
-            const int token = a.reverse ? t.length - (t.index + 1) * kTokens : t.index * kTokens;
-            uint32_t to = stages + stage * kArrays * kBytes;
-            const CUtensorMap *order[4] = {&maps.forget, &maps.x, GATE ? &maps.gate : &maps.dout, &maps.dout};
-            const Tokens *arrays[4] = {&a.forget, &a.x, GATE ? &a.gate : &a.dout, &a.dout};
+            if (t.index < t.count) {
+                barrier_expect(full, kArrays * kBytes);
+                uint32_t to = stages + stage * kArrays * kBytes;
+                const CUtensorMap *order[4] = {&maps.forget, &maps.x, GATE ? &maps.gate : &maps.dout, &maps.dout};
+                const Tokens *arrays[4] = {&a.forget, &a.x, GATE ? &a.gate : &a.dout, &a.dout};
 #pragma unroll
-            for (int k = 0; k < kArrays; ++k, to += kBytes)
-                copy_tokens(to, order[k], full, t.slab * 32 * V, token, arrays[k]->batch ? t.b : 0);
+                for (int k = 0; k < kArrays; ++k, to += kBytes)
+                    copy_tokens(to, order[k], full, t.slab * 32 * V, first_token(a, t, kTokens), arrays[k]->batch ? t.b : 0);
+            } else if (!last) {
+                barrier_arrive(full);
+            }
+            if constexpr (GATE && !BACKWARD) {
+                copy_gates();
+                gated = t;
+            }
         }
+        if (last) return;
     }
 }
 
@@ -537,6 +567,17 @@ struct Run {
     __device__ __forceinline__ void store(int i, const Lanes<V> &v) const { *token(i) = raw_of<T, V>(v); }
 };
 
+__device__ __forceinline__ uint32_t shared_load(uint32_t at)
+{
+    uint32_t w;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
+    return w;
+}
+__device__ __forceinline__ void shared_store(uint32_t at, uint32_t w)
+{
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(w) : "memory");
+}
+
 // The same of a tile in a stage, a lane's 4 bytes of row after row.
 struct StagedRun {
     uint32_t at;
@@ -547,12 +588,7 @@ struct StagedRun {
         at = stage + (a.reverse ? tile_tokens - 1 - first : first) * kRowBytes + threadIdx.x % 32 * 4;
         step = a.reverse ? -kRowBytes : kRowBytes;
     }
-    __device__ __forceinline__ uint32_t word(int i, int array_bytes) const
-    {
-        uint32_t w;
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(at + i * step + array_bytes) : "memory");
-        return w;
-    }
+    __device__ __forceinline__ uint32_t word(int i, int array_bytes) const { return shared_load(at + i * step + array_bytes); }
 };
 
 template <typename T, int V>
@@ -589,7 +625,7 @@ __device__ __forceinline__ float exp_minus(float x)
 template <typename T>
 __device__ __forceinline__ void split(float f, float &a, float &s)
 {
-    const float e = exp_minus<T>(fabsf(f)), large = rcp_fast(1.0f + e), small = e * large;
+    const float e = exp_minus<T>(fabsf(f)), small = e * rcp_fast(1.0f + e), large = 1.0f - small;
     a = f < 0.0f ? small : large;
     s = f < 0.0f ? large : small;
 }
@@ -685,12 +721,16 @@ struct RunPlace {
 
 // ---- forward -----------------------------------------------------------------------------
 
-// Words of a run in tensor memory: 1 - a, x and the gate, 64 at most.
+// Words of a run in tensor memory: a and (1 - a) x, 32 of each at most.  The output gates wait in
+// shared memory, in places for two tiles, where their copy has put them, or the warp; those of
+// single elements that the warp has read go to tensor memory too, which has room for them
+// (32,640 x 2,049 in bf16: 159 us, in shared memory 165).
 template <typename T, int V, bool GATE, bool COPY, int S>
 struct Forward {
     using F = Lanes<V>;
     using R = Raw<T, V>;
     [[maybe_unused]] static constexpr int kTokens = kTile, kLength = kRun, kBytes = kTile * kRowBytes;
+    static constexpr bool kParked = GATE && !COPY && V == 1;   // the gates are in tensor memory
 
     static __device__ __forceinline__ void clear_rest(const RecurrenceArgs &a, const Tile &t)
     {
@@ -700,95 +740,106 @@ struct Forward {
 
     // Reads a run, composes its map and leaves it in tensor memory.
     static __device__ __forceinline__ void compose(const RecurrenceArgs &a, Shared<V, S, false> &s, const Tile &t, uint32_t j,
-                                                   uint32_t stage, uint32_t columns)
+                                                   uint32_t stage, uint32_t gates, uint32_t columns)
     {
         const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
         const RunPlace<T, V> at(a, t, kTokens, kLength);
+        F keep[kLength], enter[kLength];
         uint32_t w0[32], w1[32];
-        F rest[kLength];
-        R x[kLength];
         Map<V> own;
         fill(own.a, 1.0f);
         fill(own.h, 0.0f);
         {
-            R f[kLength], o[GATE ? kLength : 1];
+            R f[kLength], x[kLength];
             if constexpr (COPY) {
                 const StagedRun staged(a, stage, kTokens, warp * kLength);
 #pragma unroll
                 for (int i = 0; i < kLength; ++i) {
                     f[i] = raw_bits<T, V>(staged.word(i, 0));
                     x[i] = raw_bits<T, V>(staged.word(i, kBytes));
-                    if constexpr (GATE) o[i] = raw_bits<T, V>(staged.word(i, 2 * kBytes));
                 }
             } else {
+                R o[GATE ? kLength : 1];
                 Run<T, V>(a, a.forget, t, at.k0, at.c).load(f, at.count);
                 Run<T, V>(a, a.x, t, at.k0, at.c).load(x, at.count);
-                if constexpr (GATE) Run<T, V>(a, a.gate, t, at.k0, at.c).load(o, at.count);
+                // (The gates' loads behind the others': a store to shared memory in front of those
+                // would have them wait.)
+                if constexpr (GATE) {
+                    Run<T, V>(a, a.gate, t, at.k0, at.c).load(o, at.count);
+#pragma unroll
+                    for (int i = 0; i < kLength; ++i) {
+                        if constexpr (kParked)
+                            w1[i] = o[i], w1[16 + i] = 0;
+                        else
+                            shared_store(gates + i * kRowBytes, o[i]);
+                    }
+                }
             }
             if (at.count == kLength) {
 #pragma unroll
-                for (int i = 0; i < kLength; ++i) step(f[i], x[i], true, rest[i], own);
+                for (int i = 0; i < kLength; ++i) step(f[i], x[i], true, keep[i], enter[i], own);
             } else {
 #pragma unroll
-                for (int i = 0; i < kLength; ++i) {
-                    if (i >= at.count) clear(x[i]);
-                    step(f[i], x[i], i < at.count, rest[i], own);
-                }
+                for (int i = 0; i < kLength; ++i) step(f[i], x[i], i < at.count, keep[i], enter[i], own);
             }
-            if constexpr (GATE)
-#pragma unroll
-                for (int i = 0; i < kLength; ++i) w1[(V == 2 ? 16 : 0) + i] = o[i];
         }
         s.runs[j & 1][warp][lane] = own;
-        put(w0, rest);
-#pragma unroll
-        for (int i = 0; i < kLength; ++i) (V == 2 ? w1 : w0 + 16)[i] = x[i];
-        if (!GATE || V == 1)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w1[16 + i] = 0;
+        put(w0, keep);
+        put(V == 2 ? w1 : w0 + 16, enter);
         tmem_store32(columns, w0);
-        if (V == 2 || GATE) tmem_store32(columns + 32, w1);
+        if (V == 2 || kParked) tmem_store32(columns + 32, w1);
         tmem_wait_store();
     }
 
-    static __device__ __forceinline__ void step(R f, R x, bool there, F &rest, Map<V> &own)
+    static __device__ __forceinline__ void step(R f, R x, bool there, F &keep, F &enter, Map<V> &own)
     {
-        F keep;
+        F rest;
         split<T>(value_of<T, V>(f), keep, rest);
+        enter = mul(rest, value_of<T, V>(x));
         if (!there) {
             fill(keep, 1.0f);
-            fill(rest, 0.0f);
+            fill(enter, 0.0f);
         }
-        own.h = mad(keep, own.h, mul(rest, value_of<T, V>(x)));
+        own.h = mad(keep, own.h, enter);
         own.a = mul(keep, own.a);
     }
 
     // Runs the tokens from the state in front of them.
     static __device__ __forceinline__ void finish(const RecurrenceArgs &a, Shared<V, S, false> &s, const Tile &t, uint32_t j,
-                                                  uint32_t columns)
+                                                  uint32_t gates, uint32_t columns)
     {
         const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
         const RunPlace<T, V> at(a, t, kTokens, kLength);
         uint32_t w0[32], w1[32];
         tmem_load32(w0, columns);
-        if (V == 2 || GATE) tmem_load32(w1, columns + 32);
+        if (V == 2 || kParked) tmem_load32(w1, columns + 32);
         const Map<V> before = s.runs[j & 1][warp][lane];
-        F h = mad(before.a, s.carry[j & 3][lane], before.h), one;
-        fill(one, 1.0f);
+        F h = mad(before.a, s.carry[j & 3][lane], before.h);
         tmem_wait_load();
         pin(w0);
-        if (V == 2 || GATE) pin(w1);
+        if (V == 2 || kParked) pin(w1);
         if (at.count == 0 || !at.mine) return;
         if (a.states && at.k0 % kStateStep == 0)
             store_state<V>(a.states + ((int64_t)t.b * a.blocks + at.k0 / kStateStep) * a.channels + at.c, h);
         const Run<T, V> out(a, a.out, t, at.k0, at.c);
+        // (A few tokens' gates are read ahead of the stores, which none of the reads passes.)
+        constexpr int kAhead = 6;
+        R o[GATE ? kLength : 1];
+        const int gate_step = COPY && a.reverse ? -kRowBytes : kRowBytes;
+        auto read = [&](int i) {
+            if constexpr (GATE) o[i] = raw_bits<T, V>(kParked ? w1[i] : shared_load(gates + i * gate_step));
+        };
+        if constexpr (GATE)
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) read(i);
         auto token = [&](int i) {
-            F rest;
-            get(w0, i, rest);
-            const F x = value_of<T, V>((R)(V == 2 ? w1 : w0 + 16)[i]);
-            h = mad(add(one, minus(rest)), h, mul(rest, x));
+            if (GATE && i + kAhead < kLength) read(i + kAhead);
+            F keep, enter;
+            get(w0, i, keep);
+            get(V == 2 ? w1 : w0 + 16, i, enter);
+            h = mad(keep, h, enter);
             if constexpr (GATE) {
-                const F g = value_of<T, V>((R)w1[(V == 2 ? 16 : 0) + i]);
+                const F g = value_of<T, V>(o[i]);
                 return mul(h, mul(g, sigmoid<T>(g)));
             } else {
                 return h;
@@ -846,7 +897,7 @@ struct Backward {
     }
 
     static __device__ __forceinline__ void compose(const RecurrenceArgs &a, Shared<V, S, true> &s, const Tile &t, uint32_t j,
-                                                   uint32_t stage, uint32_t columns)
+                                                   uint32_t stage, uint32_t, uint32_t columns)
     {
         const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
         const RunPlace<T, V> at(a, t, kTokens, kLength);
@@ -919,7 +970,7 @@ struct Backward {
     }
 
     static __device__ __forceinline__ void finish(const RecurrenceArgs &a, Shared<V, S, true> &s, const Tile &t, uint32_t j,
-                                                  uint32_t columns)
+                                                  uint32_t, uint32_t columns)
     {
         const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
         const RunPlace<T, V> at(a, t, kTokens, kLength);
@@ -975,11 +1026,17 @@ struct Backward {
 };
 
 // A working warp's tiles: the next one's run is composed before the last one's ends.
-template <typename Work, int V, int S, bool COPY, bool BACKWARD>
+// gates: the lane's word of its run's first token, of the first of two tiles (in the order of a
+// stage's rows where a copy puts them there, in the recurrence's where the warp does).
+template <typename Work, int V, int S, bool GATE, bool COPY, bool BACKWARD>
 __device__ __forceinline__ void work_tiles(const RecurrenceArgs &a, Shared<V, S, BACKWARD> &s, uint32_t stages, int stage_bytes,
                                            const WaitGuard &guard)
 {
-    const int warp = threadIdx.x / 32;
+    constexpr bool kGates = GATE && COPY && !BACKWARD;
+    constexpr int kGateBytes = kTile * kRowBytes;
+    const int warp = threadIdx.x / 32, first = warp * kRun;
+    const uint32_t gates = stages + (COPY ? S * stage_bytes : 0) + threadIdx.x % 32 * 4 +
+                           (COPY && a.reverse ? kTile - 1 - first : first) * kRowBytes;
     const uint32_t columns = s.columns + ((uint32_t)(warp % 4) << 21) + warp / 4 * (kSlotColumns / 2);   // lane << 16
     Tile before = {};
     bool open = false;
@@ -988,8 +1045,12 @@ __device__ __forceinline__ void work_tiles(const RecurrenceArgs &a, Shared<V, S,
         const uint32_t k = j - 1;
         GSR_CANARY(34 + k % 4);
         barrier_wait_warp(smem_address(&s.state_ready[k & 1]), k >> 1 & 1, guard);
-        Work::finish(a, s, before, k, columns + (k & 1) * kSlotColumns);
-        __syncwarp();
+        if (kGates) barrier_wait_warp(smem_address(&s.gate_full[k & 1]), k >> 1 & 1, guard);
+        Work::finish(a, s, before, k, gates + (k & 1) * kGateBytes, columns + (k & 1) * kSlotColumns);
+        if (kGates)
+            warp_arrive(s.gate_empty[k & 1]);
+        else
+            __syncwarp();
     };
     for (uint32_t i = 0;; ++i) {
         const uint32_t stage = i % S;
@@ -1004,7 +1065,8 @@ __device__ __forceinline__ void work_tiles(const RecurrenceArgs &a, Shared<V, S,
         if (some) {
             if (COPY) barrier_wait_warp(smem_address(&s.full[stage]), i / S & 1, guard);
             GSR_CANARY(30 + j % 4);
-            Work::compose(a, s, t, j, stages + stage * stage_bytes, columns + (j & 1) * kSlotColumns);
+            Work::compose(a, s, t, j, stages + stage * stage_bytes, gates + (j & 1) * kGateBytes,
+                          columns + (j & 1) * kSlotColumns);
             warp_arrive(s.runs_ready[j & 1]);
         }
         warp_arrive(s.empty[stage]);
@@ -1023,7 +1085,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
 {
     grid_dependency_begin();
     constexpr int S = kStages;
-    constexpr int kStageBytes = (2 + (GATE ? 1 : 0) + (BACKWARD ? 1 : 0)) * (BACKWARD ? kGradTile : kTile) * kRowBytes;
+    constexpr int kStageBytes = kStaged<GATE, BACKWARD> * (BACKWARD ? kGradTile : kTile) * kRowBytes;
     extern __shared__ unsigned char s_bytes[];
     __shared__ Shared<V, S, BACKWARD> s;
     const uint32_t stages = (smem_address(s_bytes) + 127u) / 128u * 128u;
@@ -1040,6 +1102,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
             barrier_init(smem_address(&s.runs_ready[k]), kWarps);
             barrier_init(smem_address(&s.tile_ready[k]), 1);
             barrier_init(smem_address(&s.state_ready[k]), 1 + V);
+            barrier_init(smem_address(&s.gate_full[k]), 1);
+            barrier_init(smem_address(&s.gate_empty[k]), kWarps);
         }
         fence_async();
     }
@@ -1060,7 +1124,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     } else {
         take_registers();
         using Work = std::conditional_t<BACKWARD, Backward<T, V, GATE, COPY, S>, Forward<T, V, GATE, COPY, S>>;
-        work_tiles<Work, V, S, COPY, BACKWARD>(a, s, stages, kStageBytes, guard);
+        work_tiles<Work, V, S, GATE, COPY, BACKWARD>(a, s, stages, kStageBytes, guard);
     }
     if (s.aborted && a.aborted && threadIdx.x % 32 == 0) *(volatile uint32_t *)a.aborted = 0;
     drain_if_aborted(guard);
@@ -1153,8 +1217,9 @@ bool all_arrays(const RecurrenceArgs &a, std::initializer_list<const Tokens *> a
 template <typename T, int V, bool GATE, bool COPY, bool BACKWARD>
 int launch(gsr_ctx *ctx, RecurrenceArgs &a, int dtype, const char *what, cudaStream_t stream)
 {
-    constexpr int kTokens = BACKWARD ? kGradTile : kTile, kArrays = 2 + (GATE ? 1 : 0) + (BACKWARD ? 1 : 0);
-    constexpr int kBytes = COPY ? kStages * kArrays * kTokens * kRowBytes + 128 : 0;
+    constexpr int kTokens = BACKWARD ? kGradTile : kTile;
+    constexpr int kTiles = (COPY ? kStages * kStaged<GATE, BACKWARD> : 0) + (GATE && !BACKWARD && (COPY || V == 2) ? 2 : 0);   // of one array
+    constexpr int kBytes = kTiles > 0 ? kTiles * kTokens * kRowBytes + 128 : 0;
     Maps maps = {};
     if (COPY) {
         const struct { CUtensorMap *map; const Tokens *t; } inputs[4] = {
