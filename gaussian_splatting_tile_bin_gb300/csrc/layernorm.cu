@@ -514,25 +514,31 @@ __global__ void __launch_bounds__(kRowThreads, 1) k_layer_norm_grad(const LayerA
         if (after < a.rows) {
             mean = a.mean[after];
             rstd = a.rstd[after];
+        } else {
+            mean = rstd = 0.0f;
         }
         if (row >= a.rows) {   // (its stage holds an older row)
             dout.clear();
             total.clear();
         }
+        // The second sum is of g (total - mean), and rstd comes behind it: an element of 0 behind
+        // the channels then adds g = 0 times -mean.  (Its xh, -mean rstd, may be beyond float's
+        // range, and 0 times that is not a number.)
         float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
 #pragma unroll
         for (int p = 0; p < kPairs; ++p) {
             const float2 d = dout.get(p), g = mul2(d, weight[p]);
-            const float2 hat = mul2(add2(total.get(p), minus), scale);
+            const float2 centred = add2(total.get(p), minus), hat = mul2(centred, scale);
             s1 = add2(s1, g);
-            s2 = fma2(g, hat, s2);
+            s2 = fma2(g, centred, s2);
             dw[p] = fma2(d, hat, dw[p]);
             db[p] = add2(db[p], d);
         }
         ring.fetch(a, row + S * stride, lane);
         ring.advance();
         const float2 m = team_sum<KIND>(make_float2(s1.x + s1.y, s2.x + s2.y), a, s_sums, team, turn, s_beside);
-        const float2 m1 = make_float2(-m.x * share, -m.x * share), m2 = make_float2(-m.y * share, -m.y * share);
+        const float hats = -m.y * share * scale.x;
+        const float2 m1 = make_float2(-m.x * share, -m.x * share), m2 = make_float2(hats, hats);
         if (row >= a.rows) continue;
 #pragma unroll
         for (int p = 0; p < kPairs; ++p) {
