@@ -41,9 +41,9 @@
 //
 // Numerics.  With e = exp(-|f|), the smaller of a and 1 - a is e / (1 + e), and the larger 1
 // minus it, at least 1/2: both are good to a few ulp of themselves, however far apart they are.
-// The forward's steps are a h + (1 - a) x with both, wherever they are taken, so that what a
-// gate shuts out leaves the rest its bits.  States, maps and gradients along the chain are
-// floats; results are rounded once.  exp and reciprocal are the hardware's (2 ulp).
+// A step is a h + (1 - a) x with both, wherever it is taken, so that what a gate shuts out
+// leaves the rest its bits.  States, maps and gradients along the chain are floats; results
+// are rounded once.  exp and reciprocal are the hardware's (2 ulp).
 #include <initializer_list>
 #include <type_traits>
 
@@ -863,7 +863,8 @@ struct Forward {
 
 // Words of a run in tensor memory: a, 1 - a, dout silu(o) (dL/dh_t without what comes from
 // behind) and dout silu'(o), 16 each; x waits in shared memory.  With u_t = a_t (h_(t-1) -
-// x_t), h_t = x_t + u_t and dL/df_t = dL/dx_t u_t.
+// x_t), dL/df_t = dL/dx_t u_t.  (h_t is x_t + u_t too, but loses a small state beside a large
+// x that an open gate keeps out; it is taken as in the forward.)
 template <typename T, int V, bool GATE, bool COPY, int S>
 struct Backward {
     using F = Lanes<V>;
@@ -981,11 +982,12 @@ struct Backward {
         {
             uint32_t slope[16];
             tmem_load16(keep, columns);
+            tmem_load16(rest, columns + 16);
             if (GATE) tmem_load16(slope, columns + 48);
             tmem_wait_load();
             pin16(keep);
+            pin16(rest);
             if (GATE) pin16(slope);
-            tmem_load16(rest, columns + 16);
             tmem_load16(into, columns + 32);
             const bool some = at.count > 0 && at.mine;
             const Run<T, V> dg(a, a.dgate, t, at.k0, at.c);
@@ -993,7 +995,7 @@ struct Backward {
             for (int i = 0; i < kLength; ++i) {
                 const F x = value_of<T, V>((R)s.x[j & 1][warp][i][lane]);
                 u[i] = mul(value(keep, i), add(h, minus(x)));
-                h = add(x, u[i]);
+                h = mad(value(keep, i), h, mul(value(rest, i), x));
                 if constexpr (GATE)
                     if (some && i < at.count) {
                         GSR_CANARY_LANES(42 + i);
@@ -1002,7 +1004,6 @@ struct Backward {
             }
             __syncwarp();   // (lanes behind the channels have not stored)
             tmem_wait_load();
-            pin16(rest);
             pin16(into);
             if (!some) return;
         }
