@@ -281,7 +281,7 @@ __device__ __forceinline__ void start_sums(float2 *s_all, int teams, Beside &s_b
 
 // A block leaves once the other one writes to it no more.
 template <int KIND>
-__device__ __forceinline__ void end_sums(const LayerArgs &a, Beside s_beside)
+__device__ __forceinline__ void end_sums(const LayerArgs &a, Beside &s_beside)
 {
     if constexpr (KIND == kInTwo) {
         drain_if_aborted({&s_beside.aborted, a.status});
