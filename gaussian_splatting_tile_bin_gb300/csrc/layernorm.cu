@@ -246,8 +246,10 @@ __device__ __forceinline__ F team_sum(F v, const LayerArgs &a, float2 *s_sums, i
             barrier_wait_warp(smem_address(full), parity, guard);
             GSR_CANARY(40 + copy);
         } else {
+            GSR_CANARY(52 + copy);
             if (threadIdx.x % 32 == 0) s[threadIdx.x / 32 - team * warps] = v;
             team_barrier(team, a.team);
+            GSR_CANARY(54 + copy);
         }
         v = four((const Four *)s);
         for (int w = 4; w < warps; w += 4) {
