@@ -7,16 +7,16 @@
 //
 // Bound by HBM.  A row stays in the registers of its team (lanes of a warp, a warp,
 // several or two blocks) between the statistics and the result, so every array moves once; a block
-// walks rows, and its threads' copies run three rows ahead, so that the parameters and,
+// walks rows, and its threads' copies run two or three rows ahead, so that the parameters and,
 // backward, the channels' shares of dw and db stay in registers too.  A second kernel adds
 // the blocks' shares in order.  32,640 x 2,048 in bf16 behind a residual (four arrays of 134
 // MB each way, 79 us at the copy rate): forward 88 us, backward 83 us; without one 42 us of
 // 39 and 67 us of 59.  Rows of 128 in f16 (80,000): 6.7 us of 6.0 and 12.3 us of 9.0, of
 // which the second kernel's launch is about 3.  Channels that are no multiple of 16 bytes
-// take accesses of 4 bytes or one element: 115 and 140 us at 2,050, 183 and 174 at 2,049,
-// bound by the number of accesses.  Rows of more than 8,192 channels are shared by two blocks
-// (4,000 x 16,384 in bf16: 65 us of 39 and 90 of 58, for what sums cost between warps with one
-// row at a time).
+// take accesses of 4 bytes or one element: 32,640 rows behind a residual in 114 and 141 us at
+// 2,050, 183 and 177 at 2,049, bound by the number of accesses.  Rows of more than 8,192
+// channels are shared by two blocks (4,000 x 16,384 in bf16: 65 us of 39 and 88 of 58, for what
+// sums cost between warps with one row at a time).
 //
 // Numerics.  The variance is the mean of centred squares, from the registers; sums over
 // a row pass a thread's elements and a tree, in a fixed order, all in float.  The norm of a
@@ -151,8 +151,8 @@ __device__ __forceinline__ float2 parameter(const float *from, const LayerArgs &
 }
 
 // Teams: lanes of a warp, a block's warps, or, for rows of more than 8,192 channels, those of
-// two blocks of a cluster (4,000 x 16,384 in bf16 behind a residual in 84 us forward and 99
-// backward, without one 65 and 90; a block of 1,024 threads, which has 64 registers a thread
+// two blocks of a cluster (4,000 x 16,384 in bf16 behind a residual in 84 us forward and 102
+// backward, without one 65 and 88; a block of 1,024 threads, which has 64 registers a thread
 // and spills, took 118 and 231, 66 and 212.  It was faster forward for 5,000 x 9,000 without a
 // residual, 63 and 69, and for the single elements of 4,000 x 12,345, 141 and 166).
 constexpr int kInWarp = 0, kInBlock = 1, kInTwo = 2;

@@ -31,9 +31,9 @@
 // wait in shared memory, where a second ring of copies puts them.
 //
 // What bounds it, and what the parts are worth (32,640 x 2,048 in bf16 with a gate: four
-// arrays of 134 MB forward, 79 us at the copy rate, and seven backward, 138 us): 90 and 167
-// us, each byte moved once.  Without any wait along the chain the kernels would take 86 and
-// 145 us, bound by HBM; the rest is what a map and a state take through L2.  Tiles without a
+// arrays of 134 MB forward, 79 us at the copy rate, and seven backward, 138 us): 90 and 168
+// us, each byte moved once.  Without any wait along the chain kernels that took 95 and 168 us
+// would have taken 86 and 145, bound by HBM; the rest is what a map and a state take through L2.  Tiles without a
 // ring and a chain of their own took 170 and 323 us, with them 136 and 299, with runs that
 // wait in tensor memory 115 and 213; a chain whose missing words are looked at together 102
 // and 188, and groups that publish their map before their state 95 and 168; the forward's runs
@@ -64,8 +64,10 @@ constexpr int kGroup = 8;                  // tiles of a group
 // Groups that a tile looks back on.  Where many chains share the SMs a few of a chain's
 // tiles are under way, and words that are looked at cost time (32,640 x 2,048 in bf16,
 // backward: 168 us with 2, 174 to 223 with 3 to 8); where there are few chains most of
-// their tiles are, and a state travels by as many groups at a time (32,640 x 64: 20.6 us
-// with 2, 14.9 with 8).
+// their tiles are, and a state travels by as many groups at a time (32,640 x 64: 20.8 us
+// with 2, 14.9 with 8).  The two meet at 4 chains: 25.1 and 23.4 us at 3, 32.1 and 32.5 at
+// 4, 36.5 and 37.8 at 5, 53.2 and 55.7 at 8, 92 and 99 at 16; in f32 21.1 and 16.2 at 2,
+// 28.9 and 28.4 at 4, 47.9 and 48.7 at 8.
 constexpr int kNear = 2, kFar = 8, kManyChains = 4;
 constexpr int kColumns = 256, kSlotColumns = kColumns / 2;   // of tensor memory: two tiles' runs
 constexpr int kRun = 16, kGradRun = 8;     // tokens of a warp
@@ -1300,7 +1302,8 @@ int run(gsr_ctx *ctx, RecurrenceArgs &a, int dtype, cudaStream_t stream)
     return workspace.done();
 }
 
-// 16-bit elements in pairs where channels and arrays allow it.
+// 16-bit elements in pairs where channels and arrays allow it (32,640 x 2,050 in bf16 with a gate,
+// which no copies bring: 120 and 214 us; in single elements, x 2,049, 156 and 306).
 template <bool BACKWARD>
 int dispatch(gsr_ctx *ctx, RecurrenceArgs &a, int dtype, cudaStream_t stream)
 {
