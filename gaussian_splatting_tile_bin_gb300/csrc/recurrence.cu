@@ -33,11 +33,11 @@
 // What bounds it, and what the parts are worth (32,640 x 2,048 in bf16 with a gate: four
 // arrays of 134 MB forward, 79 us at the copy rate, and seven backward, 138 us): 90 and 168
 // us, each byte moved once.  Without any wait along the chain kernels that took 95 and 168 us
-// would have taken 86 and 145, bound by HBM; the rest is what a map and a state take through L2.  Tiles without a
-// ring and a chain of their own took 170 and 323 us, with them 136 and 299, with runs that
-// wait in tensor memory 115 and 213; a chain whose missing words are looked at together 102
-// and 188, and groups that publish their map before their state 95 and 168; the forward's runs
-// that keep a and (1 - a) x, and read their gates from shared memory, 90.
+// would have taken 86 and 145, bound by HBM; the rest is what a map and a state take through
+// L2.  Tiles without a ring and a chain of their own took 170 and 323 us, with them 136 and 299,
+// with runs that wait in tensor memory 115 and 213; a chain whose missing words are looked at
+// together 102 and 188, and groups that publish their map before their state 95 and 168; the
+// forward's runs that keep a and (1 - a) x, and read their gates from shared memory, 90.
 //
 // Numerics.  With e = exp(-|f|), the smaller of a and 1 - a is e / (1 + e), and the larger 1
 // minus it, at least 1/2: both are good to a few ulp of themselves, however far apart they are.
@@ -724,15 +724,12 @@ struct RunPlace {
 // ---- forward -----------------------------------------------------------------------------
 
 // Words of a run in tensor memory: a and (1 - a) x, 32 of each at most.  The output gates wait in
-// shared memory, in places for two tiles, where their copy has put them, or the warp; those of
-// single elements that the warp has read go to tensor memory too, which has room for them
-// (32,640 x 2,049 in bf16: 159 us, in shared memory 165).
+// shared memory, in places for two tiles, where their copy has put them, or the warp.
 template <typename T, int V, bool GATE, bool COPY, int S>
 struct Forward {
     using F = Lanes<V>;
     using R = Raw<T, V>;
     [[maybe_unused]] static constexpr int kTokens = kTile, kLength = kRun, kBytes = kTile * kRowBytes;
-    static constexpr bool kParked = GATE && !COPY && V == 1;   // the gates are in tensor memory
 
     static __device__ __forceinline__ void clear_rest(const RecurrenceArgs &a, const Tile &t)
     {
@@ -764,17 +761,12 @@ struct Forward {
                 R o[GATE ? kLength : 1];
                 Run<T, V>(a, a.forget, t, at.k0, at.c).load(f, at.count);
                 Run<T, V>(a, a.x, t, at.k0, at.c).load(x, at.count);
-                // (The gates' loads behind the others': a store to shared memory in front of those
-                // would have them wait.)
+                // (The gates behind the others: loads would wait for a store to shared memory in
+                // front of them, 126 us for 120 of 32,640 x 2,050 in bf16.)
                 if constexpr (GATE) {
                     Run<T, V>(a, a.gate, t, at.k0, at.c).load(o, at.count);
 #pragma unroll
-                    for (int i = 0; i < kLength; ++i) {
-                        if constexpr (kParked)
-                            w1[i] = o[i], w1[16 + i] = 0;
-                        else
-                            shared_store(gates + i * kRowBytes, o[i]);
-                    }
+                    for (int i = 0; i < kLength; ++i) shared_store(gates + i * kRowBytes, o[i]);
                 }
             }
             if (at.count == kLength) {
@@ -789,7 +781,7 @@ struct Forward {
         put(w0, keep);
         put(V == 2 ? w1 : w0 + 16, enter);
         tmem_store32(columns, w0);
-        if (V == 2 || kParked) tmem_store32(columns + 32, w1);
+        if (V == 2) tmem_store32(columns + 32, w1);
         tmem_wait_store();
     }
 
@@ -814,12 +806,12 @@ struct Forward {
         const RunPlace<T, V> at(a, t, kTokens, kLength);
         uint32_t w0[32], w1[32];
         tmem_load32(w0, columns);
-        if (V == 2 || kParked) tmem_load32(w1, columns + 32);
+        if (V == 2) tmem_load32(w1, columns + 32);
         const Map<V> before = s.runs[j & 1][warp][lane];
         F h = mad(before.a, s.carry[j & 3][lane], before.h);
         tmem_wait_load();
         pin(w0);
-        if (V == 2 || kParked) pin(w1);
+        if (V == 2) pin(w1);
         if (at.count == 0 || !at.mine) return;
         if (a.states && at.k0 % kStateStep == 0)
             store_state<V>(a.states + ((int64_t)t.b * a.blocks + at.k0 / kStateStep) * a.channels + at.c, h);
@@ -829,7 +821,7 @@ struct Forward {
         R o[GATE ? kLength : 1];
         const int gate_step = COPY && a.reverse ? -kRowBytes : kRowBytes;
         auto read = [&](int i) {
-            if constexpr (GATE) o[i] = raw_bits<T, V>(kParked ? w1[i] : shared_load(gates + i * gate_step));
+            if constexpr (GATE) o[i] = raw_bits<T, V>(shared_load(gates + i * gate_step));
         };
         if constexpr (GATE)
 #pragma unroll
@@ -1221,7 +1213,7 @@ template <typename T, int V, bool GATE, bool COPY, bool BACKWARD>
 int launch(gsr_ctx *ctx, RecurrenceArgs &a, int dtype, const char *what, cudaStream_t stream)
 {
     constexpr int kTokens = BACKWARD ? kGradTile : kTile;
-    constexpr int kTiles = (COPY ? kStages * kStaged<GATE, BACKWARD> : 0) + (GATE && !BACKWARD && (COPY || V == 2) ? 2 : 0);   // of one array
+    constexpr int kTiles = (COPY ? kStages * kStaged<GATE, BACKWARD> : 0) + (GATE && !BACKWARD ? 2 : 0);   // of one array
     constexpr int kBytes = kTiles > 0 ? kTiles * kTokens * kRowBytes + 128 : 0;
     Maps maps = {};
     if (COPY) {
